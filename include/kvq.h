@@ -52,7 +52,9 @@ typedef enum {
   KVQ_ERR_ALIGNMENT = 6,    /* a pointer is not 16-byte aligned             */
   KVQ_ERR_TOO_LARGE = 7,    /* needs more than the built-in scratch holds   */
   KVQ_ERR_RANGE = 8,        /* an operand left the FP16 range (see below)   */
-  KVQ_ERR_BOUNDS = 9        /* checked build only: an index left its buffer */
+  KVQ_ERR_BOUNDS = 9,       /* checked build only: an index left its buffer */
+  KVQ_ERR_PAGE = 10         /* paged cache: a table entry, length or offset
+                               points outside the cache (see kvq_pages)     */
 } kvq_status;
 
 /* Correction applied to cached-key scores before the softmax. */
@@ -386,6 +388,149 @@ kvq_status kvq_attention_corrected_noalloc(const kvq_cache *cache, const uint16_
                                            int32_t n_q, int32_t n_r, float scale,
                                            int32_t corr, int32_t flags, uint16_t *out,
                                            float *p_s, float *p_r, void *stream);
+
+/* ---- Paged 8-bit cache ------------------------------------------------------
+ *
+ * A second cache beside the chunk window above, for sequences that have
+ * lengths of their own, grow by single tokens and share pages; no counterpart
+ * in the paper (its rotation and correction are not applied here: at 8 bits
+ * the score noise they act on is small).
+ *
+ * A pool of pages per layer.  A page holds page_tokens consecutive tokens of
+ * one sequence, all kv_heads heads:
+ *   k_codes, v_codes  E4M3 [layers][n_pages][kv_heads][page_tokens][head_dim]
+ *   k_scale, v_scale  BF16 [layers][n_pages][kv_heads]
+ * and stands for the values code * scale.  A scale is a power of two 2^e, one
+ * for the block of a page's tokens of one head, e the smallest integer with
+ * max |x| <= 448 * 2^e over the block, held within [-60, 60].  A power of two
+ * costs a floating-point code no bits, keeps code * scale exact in BF16, and
+ * lets a page whose scale grows (tokens appended to it later) keep the value
+ * of every code that does not become an E4M3 subnormal.
+ * Geometry: head_dim in {64, 128}; page_tokens in {16, 32, 64, 128};
+ * n_pages * kv_heads < 2^31.  Code buffers 16-byte aligned (the caller owns
+ * them; sizes from kvq_pages_bytes).  Calls on one pool that overlap on the
+ * GPU must not write a page that another reads or writes.
+ */
+typedef struct kvq_pages {
+  int32_t layers, n_pages, kv_heads, head_dim, page_tokens;
+  uint8_t *k_codes, *v_codes;
+  uint16_t *k_scale, *v_scale;
+} kvq_pages;
+
+/*
+ * The sequences of a call, all in DEVICE memory, so that a captured graph
+ * follows lengths and tables that change between replays.
+ *   table    int32 [batch][width], rows table_stride elements apart: entry p
+ *            is the page of tokens [p * page_tokens, + page_tokens).  Entries
+ *            past a sequence's length are not read.
+ *   kv_lens  int32 [batch]: tokens per sequence (0 is allowed).
+ *   offsets  int32 [batch + 1], ascending from 0: rows [offsets[b],
+ *            offsets[b + 1]) of the call's packed row tensor belong to
+ *            sequence b (none is allowed).  NULL: one row per sequence
+ *            (rows == batch).
+ *   rows     rows of the packed tensor; rows at or behind offsets[batch] are
+ *            neither read nor written.
+ * A table entry outside [0, n_pages), a length outside [0, width *
+ * page_tokens] or an offset outside [0, rows] makes the call skip what it
+ * points at and record KVQ_ERR_PAGE in the device status word (see
+ * kvq_last_device_status): nothing outside the buffers is touched, and the
+ * call's results for that sequence are not valid.
+ */
+typedef struct kvq_sequences {
+  int32_t batch, width;
+  int64_t table_stride;
+  const int32_t *table;
+  const int32_t *kv_lens;
+  const int32_t *offsets;
+  int32_t rows;
+} kvq_sequences;
+
+/*
+ * Bytes of ONE codes buffer and of ONE scale buffer of this pool.  Host only;
+ * no CUDA call.
+ */
+kvq_status kvq_pages_bytes(const kvq_pages *pages, size_t *codes_bytes, size_t *scale_bytes);
+
+/*
+ * Append: row offsets[b] + i of k_new and v_new becomes token kv_lens[b] -
+ * n_b + i of sequence b (n_b its rows; kv_lens counts them already) in
+ * `layer`.  k_new, v_new: BF16 device, row r of head h at r * row_stride +
+ * h * head_stride elements (both multiples of 8; head_dim contiguous).
+ * Per page, head and K / V, with m = max |x| over the page's new rows and
+ * e(m) the scale exponent above: a page without earlier tokens gets e(m); one
+ * with earlier tokens max(e_old, e(m)), and if that grows, its earlier codes c
+ * become e4m3(c * 2^(e_old - e)).  New codes are e4m3(x * 2^-e), to nearest,
+ * ties to even, saturating.  Tokens of the page behind the last new one keep
+ * their bytes.  No page may be written for two sequences in one call.  A
+ * value that is not finite or beyond 448 * 2^60 records KVQ_ERR_RANGE.
+ */
+kvq_status kvq_pages_append(const kvq_pages *pages, int32_t layer, const uint16_t *k_new,
+                            int64_t k_row_stride, int64_t k_head_stride, const uint16_t *v_new,
+                            int64_t v_row_stride, int64_t v_head_stride,
+                            const kvq_sequences *seqs, void *stream);
+
+/*
+ * Workspace bytes of kvq_paged_attention for this pool, q_heads, rows query
+ * rows in batch sequences of at most max_q rows each.  Depends on the current
+ * device's SM count.  0 on a bad argument.
+ */
+size_t kvq_paged_workspace_bytes(const kvq_pages *pages, int32_t q_heads, int32_t batch,
+                                 int32_t rows, int32_t max_q);
+
+/*
+ * Attention over the pages of `layer`.  q: BF16 device, row r of head h at
+ * r * q_row_stride + h * q_head_stride elements (multiples of 8; head_dim
+ * contiguous); q_heads a multiple of kv_heads, query head h reads cache head
+ * h / (q_heads / kv_heads).  Row i of sequence b's n_b rows stands at
+ * position t = kv_lens[b] - n_b + i and attends to the cached tokens j with
+ *   0 <= j < kv_lens[b],  j <= t when causal != 0,  j > t - window when
+ *   window > 0
+ * (window counts back from t, with or without causal):
+ *   s_j = scale * q . k_j,  out = sum_j softmax(s)_j v_j,
+ *   lse = log sum_j exp(s_j).
+ * A row that attends to nothing gets out = 0, lse = -infinity.  What masked
+ * places hold (NaN codes among it) does not matter when no row of the
+ * sequence's query heads attends there.
+ * out: BF16 [rows][q_heads][head_dim] device, contiguous; lse: fp32
+ * [rows][q_heads] device or NULL.  max_q: at least the largest n_b (rows
+ * beyond it are not computed and record KVQ_ERR_PAGE).  workspace: device,
+ * 16-byte aligned, >= kvq_paged_workspace_bytes; its contents need not be
+ * kept, and calls that overlap on the GPU need workspaces of their own.
+ * rows == 0 is a no-op.
+ */
+kvq_status kvq_paged_attention(const kvq_pages *pages, int32_t layer, const uint16_t *q,
+                               int64_t q_row_stride, int64_t q_head_stride, int32_t q_heads,
+                               const kvq_sequences *seqs, int32_t max_q, float scale,
+                               int32_t causal, int32_t window, void *workspace,
+                               size_t workspace_bytes, uint16_t *out, float *lse, void *stream);
+
+/*
+ * Copy pages src[i] -> dst[i], i < n, of every layer: K, V and scales (the
+ * last, partly filled page of a sequence that forks; full pages are shared
+ * through the tables).  src, dst: HOST arrays, read before the call returns.
+ * Every id within [0, n_pages), the dst distinct and none of them a src;
+ * otherwise KVQ_ERR_INVALID_ARG and nothing is copied.
+ */
+kvq_status kvq_pages_copy(const kvq_pages *pages, const int32_t *src, const int32_t *dst, int32_t n,
+                          void *stream);
+
+/*
+ * Compact: the pages that some table entry names are live, all others free
+ * (a page is freed by writing -1 over its entries; an entry < 0 is empty).
+ * With n live pages, those with ids >= n move, in ascending order, into the
+ * free ids below n, in ascending order, in every layer.  table_out (int32
+ * [batch][width], rows table_out_stride apart; may be the input table with
+ * its stride) gets the new ids, empty entries as they were; n_live (int32
+ * device, one element) gets n: pages [n, n_pages) are free afterwards.
+ * Entries >= n_pages record KVQ_ERR_PAGE and stay as they are.  n_pages <=
+ * 2^20 (else KVQ_ERR_TOO_LARGE).  workspace: device, 16-byte aligned, >=
+ * kvq_pages_compact_workspace_bytes; contents need not be kept.
+ */
+size_t kvq_pages_compact_workspace_bytes(const kvq_pages *pages);
+kvq_status kvq_pages_compact(const kvq_pages *pages, const int32_t *table, int32_t batch,
+                             int32_t width, int64_t table_stride, int32_t *table_out,
+                             int64_t table_out_stride, int32_t *n_live, void *workspace,
+                             size_t workspace_bytes, void *stream);
 
 /*
  * Instrumentation (no counterpart in the paper).  Between kvq_profile_begin

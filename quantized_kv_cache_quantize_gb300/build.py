@@ -20,7 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkvq.so")
 SOURCES = ["kvq_api.cu", "kvq_quant.cu", "kvq_quant_mma.cu", "kvq_attn.cu", "kvq_attn_exact.cu", "kvq_attn_kch.cu",
-           "kvq_attn_pair.cu"]
+           "kvq_attn_pair.cu", "kvq_pages_api.cu", "kvq_pages.cu", "kvq_paged_attn.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

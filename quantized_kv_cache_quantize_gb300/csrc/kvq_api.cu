@@ -306,7 +306,7 @@ const char* kvq_status_string(kvq_status s) {
   switch (s) {
     case KVQ_OK: return "ok";
     case KVQ_ERR_INVALID_ARG: return "invalid argument";
-    case KVQ_ERR_UNSUPPORTED: return "unsupported head_dim/bits/group";
+    case KVQ_ERR_UNSUPPORTED: return "unsupported head_dim/bits/group/page_tokens";
     case KVQ_ERR_CAPACITY: return "append refused by the cache window rules";
     case KVQ_ERR_CUDA: return "CUDA call failed";
     case KVQ_ERR_TIMEOUT: return "bounded wait in a kernel ran out";
@@ -317,6 +317,8 @@ const char* kvq_status_string(kvq_status s) {
       return "an operand left the FP16 range of the tensor-core operands (results invalid)";
     case KVQ_ERR_BOUNDS:
       return "checked build: an index left its buffer (see kvq_debug_bounds_site)";
+    case KVQ_ERR_PAGE:
+      return "paged cache: a table entry, length or offset points outside the cache";
   }
   return "unknown status";
 }
@@ -580,6 +582,8 @@ bool current_context_id(unsigned long long* id) {
 }  // namespace
 
 namespace kvq {
+
+unsigned long long wait_limit_ns() { return g_wait_limit_ns.load(); }
 
 void note_launch() {
   if (g_prof.on) g_kernel_launches.fetch_add(1, std::memory_order_relaxed);

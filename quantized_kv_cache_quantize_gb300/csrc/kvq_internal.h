@@ -295,6 +295,8 @@ kvq_status launch_attention(const AttnLaunch& a, int d, int bits, int group,
 // device address of the attention status word (first in-kernel error since
 // it was last read) in the current device's current context, or null
 int* status_ptr();
+// the limit kvq_set_wait_limit_ns set
+unsigned long long wait_limit_ns();
 // counts a kernel launch of this library while kvq_profile_begin/end records
 void note_launch();
 int* bounds_site_ptr();

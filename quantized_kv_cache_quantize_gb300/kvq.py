@@ -28,6 +28,7 @@ KVQ_ERR_ALIGNMENT = 6
 KVQ_ERR_TOO_LARGE = 7
 KVQ_ERR_RANGE = 8
 KVQ_ERR_BOUNDS = 9
+KVQ_ERR_PAGE = 10
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 KEYS_PER_TOKEN = 0
@@ -63,6 +64,25 @@ class CacheStruct(ctypes.Structure):
     ]
 
 
+class PagesStruct(ctypes.Structure):
+    """Mirror of ``kvq_pages`` in include/kvq.h."""
+    _fields_ = [
+        ("layers", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
+        ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+    ]
+
+
+class SequencesStruct(ctypes.Structure):
+    """Mirror of ``kvq_sequences`` in include/kvq.h."""
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("width", ctypes.c_int32), ("table_stride", ctypes.c_int64),
+        ("table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
+        ("rows", ctypes.c_int32),
+    ]
+
+
 _P = ctypes.c_void_p
 _SIGNATURES = {
     "kvq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -90,6 +110,20 @@ _SIGNATURES = {
                                                        ctypes.c_int32, ctypes.c_float,
                                                        ctypes.c_int32, ctypes.c_int32, _P, _P, _P,
                                                        _P]),
+    "kvq_pages_bytes": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_size_t),
+                                       ctypes.POINTER(ctypes.c_size_t)]),
+    "kvq_pages_append": (ctypes.c_int, [_P, ctypes.c_int32, _P, ctypes.c_int64, ctypes.c_int64,
+                                        _P, ctypes.c_int64, ctypes.c_int64, _P, _P]),
+    "kvq_paged_workspace_bytes": (ctypes.c_size_t, [_P, ctypes.c_int32, ctypes.c_int32,
+                                                    ctypes.c_int32, ctypes.c_int32]),
+    "kvq_paged_attention": (ctypes.c_int, [_P, ctypes.c_int32, _P, ctypes.c_int64, ctypes.c_int64,
+                                           ctypes.c_int32, _P, ctypes.c_int32, ctypes.c_float,
+                                           ctypes.c_int32, ctypes.c_int32, _P, ctypes.c_size_t, _P,
+                                           _P, _P]),
+    "kvq_pages_copy": (ctypes.c_int, [_P, _P, _P, ctypes.c_int32, _P]),
+    "kvq_pages_compact_workspace_bytes": (ctypes.c_size_t, [_P]),
+    "kvq_pages_compact": (ctypes.c_int, [_P, _P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int64,
+                                         _P, ctypes.c_int64, _P, _P, ctypes.c_size_t, _P]),
     "kvq_profile_begin": (ctypes.c_int, []),
     "kvq_profile_end": (ctypes.c_int, [_P, _P]),
 }
@@ -147,6 +181,17 @@ def _stream(stream, device=None) -> ctypes.c_void_p:
     elif device is not None and getattr(stream, "device", device) != device:
         raise ValueError(f"stream belongs to {stream.device}, the call's tensors to {device}")
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+def _alloc_on(stream, device):
+    """Where a call's own tensors (outputs, workspace) are allocated: on the
+    stream its kernels run on, so that the allocator hands out memory whose
+    earlier users are done by then, and takes it back after the call's."""
+    if stream is None or device.type != "cuda":
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
 
 
 def _on_device(device):
@@ -395,6 +440,223 @@ def rotate(x: torch.Tensor, signs, out_dtype=torch.float32, stream=None) -> torc
         _check(lib().kvq_rotate(_ptr(x), rows, d, sb, _ptr(f32), _ptr(f16),
                                 _stream(stream, x.device)), "kvq_rotate")
     return out
+
+
+class PagedCache:
+    """A pool of 8-bit pages (``kvq_pages``): E4M3 codes [layers, n_pages,
+    kv_heads, page_tokens, head_dim] and one power-of-two BF16 scale per page
+    and head [layers, n_pages, kv_heads], for K and for V.  The four tensors
+    are the caller's and are written in place; ``PagedCache.zeros`` makes
+    them.  Which page belongs to which sequence is the caller's block table."""
+
+    def __init__(self, k_codes: torch.Tensor, v_codes: torch.Tensor, k_scale: torch.Tensor,
+                 v_scale: torch.Tensor):
+        if k_codes.dim() != 5:
+            raise ValueError("k_codes must have shape [layers, n_pages, kv_heads, page_tokens, "
+                             f"head_dim], got {list(k_codes.shape)}")
+        for name, t, shape, dtype in (("k_codes", k_codes, k_codes.shape, torch.float8_e4m3fn),
+                                      ("v_codes", v_codes, k_codes.shape, torch.float8_e4m3fn),
+                                      ("k_scale", k_scale, k_codes.shape[:3], torch.bfloat16),
+                                      ("v_scale", v_scale, k_codes.shape[:3], torch.bfloat16)):
+            if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape "
+                                 f"{list(shape)}, got {t.dtype} {list(t.shape)}")
+            if t.device != k_codes.device:
+                raise ValueError(f"{name} is on {t.device}, k_codes on {k_codes.device}")
+        self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
+        c = PagesStruct()
+        c.layers, c.n_pages, c.kv_heads, c.page_tokens, c.head_dim = k_codes.shape
+        c.k_codes, c.v_codes = k_codes.data_ptr(), v_codes.data_ptr()
+        c.k_scale, c.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
+        _check(lib().kvq_pages_bytes(ctypes.byref(c), None, None), "kvq_pages_bytes")
+        self.struct = c
+
+    @classmethod
+    def zeros(cls, layers: int, n_pages: int, kv_heads: int, page_tokens: int, head_dim: int,
+              device="cuda") -> "PagedCache":
+        shape = (layers, n_pages, kv_heads, page_tokens, head_dim)
+        codes = [torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+                 for _ in range(2)]
+        scales = [torch.ones(shape[:3], dtype=torch.bfloat16, device=device) for _ in range(2)]
+        return cls(*codes, *scales)
+
+    layers = property(lambda self: self.struct.layers)
+    n_pages = property(lambda self: self.struct.n_pages)
+    kv_heads = property(lambda self: self.struct.kv_heads)
+    page_tokens = property(lambda self: self.struct.page_tokens)
+    head_dim = property(lambda self: self.struct.head_dim)
+    device = property(lambda self: self.k_codes.device)
+
+    def workspace_bytes(self, q_heads: int, batch: int, rows: int, max_q: int) -> int:
+        """kvq_paged_workspace_bytes."""
+        with _on_device(self.device):
+            return int(lib().kvq_paged_workspace_bytes(ctypes.byref(self.struct), q_heads, batch,
+                                                       rows, max_q))
+
+
+def _int32_dev(cache: PagedCache, t: torch.Tensor, name: str, dim: int) -> torch.Tensor:
+    if t.dtype != torch.int32 or t.dim() != dim or not t.is_cuda:
+        raise ValueError(f"{name} must be a {dim}-dimensional CUDA int32 tensor, got {t.dtype} "
+                         f"{list(t.shape)} on {t.device}")
+    if t.device != cache.device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel() > 0:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return t
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """Elements between rows (one row, or empty ones: its own length)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _paged_rows(cache: PagedCache, t: torch.Tensor, name: str) -> torch.Tensor:
+    """[rows, heads, head_dim] BF16, the channels contiguous, the rows and heads
+    at strides of their own (multiples of 8 elements)."""
+    if t.dim() != 3 or t.shape[2] != cache.head_dim:
+        raise ValueError(f"{name} must have shape [rows, heads, {cache.head_dim}], got {list(t.shape)}")
+    if t.dtype != torch.bfloat16 or not t.is_cuda or (t.stride(2) != 1 and t.numel() > 0):
+        raise ValueError(f"{name} must be a CUDA bfloat16 tensor with contiguous channels")
+    if t.device != cache.device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
+    return t
+
+
+def _sequences(cache: PagedCache, rows: int, block_table, kv_lens, offsets) -> SequencesStruct:
+    _int32_dev(cache, block_table, "block_table", 2)
+    _int32_dev(cache, kv_lens, "kv_lens", 1)
+    batch = int(block_table.shape[0])
+    if kv_lens.shape[0] != batch:
+        raise ValueError(f"kv_lens must have one entry per row of block_table ({batch}), got "
+                         f"{kv_lens.shape[0]}")
+    if offsets is None:
+        if rows != batch:
+            raise ValueError(f"without offsets there is one row per sequence: {rows} rows for "
+                             f"{batch} sequences")
+    else:
+        _int32_dev(cache, offsets, "offsets", 1)
+        if offsets.shape[0] != batch + 1:
+            raise ValueError(f"offsets must have {batch + 1} entries, got {offsets.shape[0]}")
+    s = SequencesStruct()
+    s.batch, s.width, s.table_stride = batch, int(block_table.shape[1]), _row_stride(block_table)
+    s.table, s.kv_lens = block_table.data_ptr(), kv_lens.data_ptr()
+    s.offsets = None if offsets is None else offsets.data_ptr()
+    s.rows = rows
+    return s
+
+
+@_nvtx("kvq_pages_append")
+def pages_append(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor,
+                 block_table: torch.Tensor, kv_lens: torch.Tensor, offsets=None, layer: int = 0,
+                 stream=None):
+    """kvq_pages_append: k_new/v_new [rows, kv_heads, head_dim] bf16, the rows
+    of all sequences packed (rows offsets[b] .. offsets[b + 1] are sequence
+    b's; None: one row each), appended so that sequence b then holds
+    kv_lens[b] tokens."""
+    _paged_rows(cache, k_new, "k_new")
+    _paged_rows(cache, v_new, "v_new")
+    if k_new.shape != v_new.shape or k_new.shape[1] != cache.kv_heads:
+        raise ValueError(f"k_new and v_new must have shape [rows, {cache.kv_heads}, "
+                         f"{cache.head_dim}], got {list(k_new.shape)} and {list(v_new.shape)}")
+    s = _sequences(cache, int(k_new.shape[0]), block_table, kv_lens, offsets)
+    with _on_device(cache.device):
+        _check(lib().kvq_pages_append(
+            ctypes.byref(cache.struct), layer, _ptr(k_new), k_new.stride(0), k_new.stride(1),
+            _ptr(v_new), v_new.stride(0), v_new.stride(1), ctypes.byref(s),
+            _stream(stream, cache.device)), "kvq_pages_append")
+
+
+@_nvtx("kvq_paged_attention")
+def paged_attention(cache: PagedCache, q: torch.Tensor, block_table: torch.Tensor,
+                    kv_lens: torch.Tensor, offsets=None, max_q: int | None = None,
+                    scale: float | None = None, causal: bool = True, window: int = 0,
+                    layer: int = 0, out=None, with_lse: bool = False, workspace=None, stream=None):
+    """kvq_paged_attention: q [rows, q_heads, head_dim] bf16, packed like
+    pages_append's rows (which come first: kv_lens counts the queries' own
+    tokens).  max_q: the most rows a sequence has (default: all of them).
+    Returns out [rows, q_heads, head_dim] (and lse [rows, q_heads] fp32 with
+    with_lse)."""
+    _paged_rows(cache, q, "q")
+    rows, q_heads = int(q.shape[0]), int(q.shape[1])
+    if q_heads < 1 or q_heads % cache.kv_heads:
+        raise ValueError(f"q has {q_heads} heads, not a multiple of the cache's {cache.kv_heads}")
+    s = _sequences(cache, rows, block_table, kv_lens, offsets)
+    max_q = (1 if offsets is None else rows) if max_q is None else max_q
+    scale = 1.0 / math.sqrt(cache.head_dim) if scale is None else scale
+    st = _stream(stream, q.device)
+    if out is not None:
+        if out.device != q.device:
+            raise ValueError(f"out is on {out.device}, q on {q.device}")
+        _check_out(q, out)
+    with _on_device(q.device):
+        with _alloc_on(stream, q.device):
+            if out is None:
+                out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if with_lse else None
+            if workspace is None:
+                workspace = torch.empty(max(cache.workspace_bytes(q_heads, s.batch, rows, max_q), 16),
+                                        dtype=torch.uint8, device=q.device)
+        ws_ptr, ws_size = _workspace_arg(workspace, q.device)
+        _check(lib().kvq_paged_attention(
+            ctypes.byref(cache.struct), layer, _ptr(q), q.stride(0), q.stride(1), q_heads,
+            ctypes.byref(s), max_q, ctypes.c_float(scale), int(bool(causal)), window, ws_ptr,
+            ws_size, _ptr(out), _ptr(lse), st), "kvq_paged_attention")
+    return (out, lse) if with_lse else out
+
+
+def _host_ids(ids, name: str) -> torch.Tensor:
+    t = torch.as_tensor(ids)
+    if t.numel() == 0 and t.dim() == 1:
+        t = t.to(torch.int32)   # an empty list has no type of its own
+    if t.is_cuda or t.dim() != 1 or t.is_floating_point() or t.dtype == torch.bool:
+        raise ValueError(f"{name} must be a list or a 1-dimensional CPU integer tensor")
+    if t.numel() and (int(t.min()) < 0 or int(t.max()) > 0x7FFFFFFF):
+        raise ValueError(f"{name} holds an id outside the pool")
+    return t.to(torch.int32).contiguous()
+
+
+@_nvtx("kvq_pages_copy")
+def pages_copy(cache: PagedCache, src, dst, stream=None):
+    """kvq_pages_copy: pages src[i] -> dst[i] of every layer (lists or CPU
+    integer tensors; the dst distinct, none of them a src)."""
+    src, dst = _host_ids(src, "src"), _host_ids(dst, "dst")
+    if src.shape != dst.shape:
+        raise ValueError(f"src has {src.numel()} pages, dst {dst.numel()}")
+    if cache.device.type != "cuda":
+        raise ValueError(f"the cache is on {cache.device}, not a CUDA device")
+    with _on_device(cache.device):
+        _check(lib().kvq_pages_copy(ctypes.byref(cache.struct), _ptr(src), _ptr(dst), src.numel(),
+                                    _stream(stream, cache.device)), "kvq_pages_copy")
+
+
+@_nvtx("kvq_pages_compact")
+def pages_compact(cache: PagedCache, block_table: torch.Tensor, out=None, workspace=None,
+                  stream=None):
+    """kvq_pages_compact: moves the live pages (entries >= 0 of block_table)
+    of every layer to the front of the pool.  Returns (the rewritten table, a
+    one-element int32 tensor with the number of live pages); out: where to
+    write the table (block_table itself for in place)."""
+    _int32_dev(cache, block_table, "block_table", 2)
+    st = _stream(stream, cache.device)
+    if out is not None:
+        _int32_dev(cache, out, "out", 2)
+        if out.shape != block_table.shape:
+            raise ValueError(f"out must have the shape of block_table {list(block_table.shape)}, "
+                             f"got {list(out.shape)}")
+    with _on_device(cache.device):
+        need = int(lib().kvq_pages_compact_workspace_bytes(ctypes.byref(cache.struct)))
+        with _alloc_on(stream, cache.device):
+            if out is None:
+                out = torch.empty(block_table.shape, dtype=torch.int32, device=cache.device)
+            n_live = torch.empty(1, dtype=torch.int32, device=cache.device)
+            if workspace is None:
+                workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=cache.device)
+        ws_ptr, ws_size = _workspace_arg(workspace, cache.device)
+        _check(lib().kvq_pages_compact(
+            ctypes.byref(cache.struct), _ptr(block_table), block_table.shape[0],
+            block_table.shape[1], _row_stride(block_table), _ptr(out), _row_stride(out),
+            _ptr(n_live), ws_ptr, ws_size, st), "kvq_pages_compact")
+    return out, n_live
 
 
 def last_device_status(stream=None, device=None) -> int:
