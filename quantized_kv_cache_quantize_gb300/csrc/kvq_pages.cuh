@@ -8,9 +8,39 @@
 #include <stdint.h>
 
 #include "kvq_pages.h"
+#include "kvq_sm100.cuh"
 
 namespace kvq {
 namespace {
+
+// Bounded wait on an mbarrier phase: false when the limit ran out (recorded)
+// or `abort` (may be null) was raised by another role.
+__device__ __noinline__ bool page_wait_slow(uint32_t bar, uint32_t parity, unsigned long long limit_ns,
+                                            volatile int* abort, int* status) {
+  const uint64_t t0 = ptx::globaltimer();
+  while (!ptx::mbar_try_wait_sleep(bar, parity, 20000u)) {
+    if (abort != nullptr && *abort) return false;
+    if (ptx::globaltimer() - t0 > limit_ns) {
+      if (abort != nullptr) *abort = 1;
+      atomicCAS(status, 0, (int)KVQ_ERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool page_wait(uint32_t bar, uint32_t parity, unsigned long long limit_ns,
+                                          volatile int* abort, int* status) {
+  return ptx::mbar_try_wait(bar, parity) || page_wait_slow(bar, parity, limit_ns, abort, status);
+}
+// A wait for copies or MMAs this thread has in flight, before it exits:
+// bounded, and at least 100 ms long whatever the limit.
+__device__ __noinline__ void page_drain(uint32_t bar, uint32_t parity, unsigned long long limit_ns) {
+  if (limit_ns < 100000000ull) limit_ns = 100000000ull;
+  const uint64_t t0 = ptx::globaltimer();
+  while (!ptx::mbar_try_wait(bar, parity)) {
+    if (ptx::globaltimer() - t0 > limit_ns) return;
+  }
+}
 
 // 2^e as fp32, -126 <= e <= 127
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }

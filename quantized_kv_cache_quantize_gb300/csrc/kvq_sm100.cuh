@@ -65,6 +65,11 @@ __device__ __forceinline__ void grid_dependency_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// Let the grid that depends on this one start launching (it waits by itself).
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ---- async proxy ----------------------------------------------------------
 // Orders this thread's generic-proxy shared-memory writes before later
 // async-proxy accesses (tensor-core operand reads, TMA).

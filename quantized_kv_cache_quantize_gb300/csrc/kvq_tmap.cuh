@@ -61,5 +61,22 @@ bool make_rows_map(CUtensorMap* m, const void* base, int d, long long rows, int 
   return r == CUDA_SUCCESS;
 }
 
+// 3-D map over a pool's codes [blocks][page][d] bytes, box [1][box_rows][d]:
+// a row is one swizzle span (128 or 64 bytes).
+bool make_pages_map(CUtensorMap* m, const void* base, int d, int page, long long blocks,
+                    int box_rows) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)page, (cuuint64_t)blocks};
+  cuuint64_t strides[2] = {(cuuint64_t)d, (cuuint64_t)d * page};
+  cuuint32_t box[3] = {(cuuint32_t)d, (cuuint32_t)box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
+                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 }  // namespace
 }  // namespace kvq
