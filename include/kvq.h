@@ -422,7 +422,8 @@ typedef struct kvq_pages {
  * follows lengths and tables that change between replays.
  *   table    int32 [batch][width], rows table_stride elements apart: entry p
  *            is the page of tokens [p * page_tokens, + page_tokens).  Entries
- *            past a sequence's length are not read.
+ *            past a sequence's length are not read, nor by the attention
+ *            those of pages wholly before every row's window.
  *   kv_lens  int32 [batch]: tokens per sequence (0 is allowed).
  *   offsets  int32 [batch + 1], ascending from 0: rows [offsets[b],
  *            offsets[b + 1]) of the call's packed row tensor belong to

@@ -94,13 +94,14 @@ def append(pool: Pool, k_new, v_new, table, lens, counts):
 
 def attention(pool: Pool, q, table, lens, counts, scale: float, causal: bool, window: int):
     """(out [rows, q_heads, d], lse [rows, q_heads], bound [rows, q_heads, d],
-    score_err [rows, q_heads]).  ``bound`` is sum_j p_j |v_j| per channel and
-    score_err scale * max_j sum_c |q_c k_jc| over the attended keys: what the
-    error of a lower-precision evaluation is measured by."""
+    score_err [rows, q_heads], query_err [rows, q_heads]).  What the error of
+    a lower-precision evaluation is measured by, over the attended keys:
+    ``bound`` is sum_j p_j |v_j| per channel, score_err scale * max_j sum_c
+    |q_c k_jc|, query_err scale * max_c |q_c| * max_j sum_c |k_jc|."""
     q = np.asarray(q, np.float64)
     rows, hq, d = q.shape
     out, lse = np.zeros((rows, hq, d)), np.full((rows, hq), -math.inf)
-    bound, serr = np.zeros((rows, hq, d)), np.zeros((rows, hq))
+    bound, serr, qerr = np.zeros((rows, hq, d)), np.zeros((rows, hq)), np.zeros((rows, hq))
     at = 0
     for b, (length, n) in enumerate(zip(lens, counts)):
         k, v = pool.rows(0, table[b], length), pool.rows(1, table[b], length)
@@ -124,8 +125,9 @@ def attention(pool: Pool, q, table, lens, counts, scale: float, causal: bool, wi
                 out[at + i, h] = p @ v[g][see]
                 bound[at + i, h] = p @ np.abs(v[g][see])
                 serr[at + i, h] = scale * (np.abs(k[g][see]) @ np.abs(q[at + i, h])).max()
+                qerr[at + i, h] = scale * np.abs(q[at + i, h]).max() * np.abs(k[g][see]).sum(1).max()
         at += n
-    return out, lse, bound, serr
+    return out, lse, bound, serr, qerr
 
 
 def compact(table, n_pages: int):

@@ -6,78 +6,13 @@
 #include <algorithm>
 
 #include "kvq_checks.cuh"
+#include "kvq_paged_chunk.cuh"
 #include "kvq_paged_decode.cuh"
 #include "kvq_pages.cuh"
 #include "kvq_tmap.cuh"
 
 namespace kvq {
 namespace {
-
-// One warp per query row and head; every lane holds D / 32 channels.
-template <int D>
-__global__ void __launch_bounds__(128) paged_attn_kernel(const PagedAttnArgs a) {
-  constexpr int C = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int qh = (int)(w % a.q_heads);
-  const long long rb = w / a.q_heads;
-  const int i = (int)(rb % a.max_q), b = (int)(rb / a.max_q);
-  if (b >= a.s.batch) return;
-  int r0, n;
-  seq_rows(a.s, b, r0, n, a.status);
-  if (n > a.max_q) page_error(a.status);
-  if (i >= n) return;
-  const int len = seq_len(a.s, b, a.p.shift, a.status);
-  const int t = len - n + i, head = qh / a.group;
-  const int hi = a.causal ? min(len, t + 1) : len;
-  const int lo = a.window > 0 ? max(0, t - a.window + 1) : 0;
-  const long long row = r0 + i;
-  float q[C], o[C];
-  for (int c = 0; c < C; ++c) {
-    q[c] = a.scale * __uint_as_float((uint32_t)a.q[row * a.q_row_stride + qh * a.q_head_stride + C * lane + c] << 16);
-    o[c] = 0.f;
-  }
-  float top = -CUDART_INF_F, sum = 0.f;
-  int id = -1;
-  float ks = 0.f, vs = 0.f;
-  for (int j = lo; j < hi; ++j) {
-    const int in = j & (a.p.page - 1);
-    if (in == 0 || j == lo) {
-      id = seq_page(a.s, b, j >> a.p.shift, a.p.n_pages, a.status);
-      if (id >= 0) {
-        ks = pow2f(scale_exp(a.p.scale[0][(long long)id * a.p.heads + head]));
-        vs = pow2f(scale_exp(a.p.scale[1][(long long)id * a.p.heads + head]));
-      }
-    }
-    if (id < 0) continue;
-    const long long at = (((long long)id * a.p.heads + head) * a.p.page + in) * D + C * lane;
-    float s = 0.f;
-    float v[C];
-    for (int c = 0; c < C; c += 2) {
-      const uint32_t kh = f16x2_of_e4m3x2(*reinterpret_cast<const uint16_t*>(a.p.codes[0] + at + c));
-      const uint32_t vh = f16x2_of_e4m3x2(*reinterpret_cast<const uint16_t*>(a.p.codes[1] + at + c));
-      const float2 k2 = __half22float2(*reinterpret_cast<const __half2*>(&kh));
-      const float2 v2 = __half22float2(*reinterpret_cast<const __half2*>(&vh));
-      s += q[c] * k2.x + q[c + 1] * k2.y;
-      v[c] = v2.x * vs;
-      v[c + 1] = v2.y * vs;
-    }
-    for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-    s *= ks;
-    const float next = fmaxf(top, s);
-    const float f = expf(top - next), e = expf(s - next);
-    sum = sum * f + e;
-    for (int c = 0; c < C; ++c) o[c] = o[c] * f + e * v[c];
-    top = next;
-  }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  for (int c = 0; c < C; ++c) {
-    const __nv_bfloat16 v = __float2bfloat16_rn(o[c] * inv);
-    a.out[(row * a.q_heads + qh) * D + C * lane + c] = *reinterpret_cast<const uint16_t*>(&v);
-  }
-  if (lane == 0 && a.lse != nullptr)
-    a.lse[row * a.q_heads + qh] = sum > 0.f ? top + logf(sum) : -CUDART_INF_F;
-}
 
 // ---- few rows: the decoding form ----
 constexpr int kDecRows = 16;
@@ -154,29 +89,82 @@ kvq_status launch_decode(const PagedAttnArgs& a, cudaStream_t stream) {
   return KVQ_OK;
 }
 
+// ---- many rows: the tensor-core form ----
+std::atomic<uint64_t> g_chunk_smem[2][2];
+constexpr int kMaxSplits = 32;
+
+// Key ranges per row tile at most: what fills the SMs twice over.
+int split_limit(int sms, long long ctas) {
+  const long long s = ctas > 0 ? (2LL * sms + ctas - 1) / ctas : 1;
+  return (int)(s > kMaxSplits ? kMaxSplits : s);
+}
+long long chunk_tiles(int batch, int heads, long long cap, int* q_tiles) {
+  const int per = cap <= 128 ? 128 : 256;
+  *q_tiles = (int)((cap + per - 1) / per);
+  return (long long)batch * heads * *q_tiles;
+}
+size_t chunk_ws(int splits, int rows, int q_heads, int d) {
+  return splits > 1 ? (size_t)splits * rows * q_heads * (d + 2) * 4 + 16 : 16;
+}
+
+template <int D, int NQ>
+kvq_status launch_chunk(const PagedAttnArgs& a, cudaStream_t stream) {
+  const int sms = sm_count_current();
+  if (sms <= 0) return KVQ_ERR_CUDA;
+  ChunkArgs c{};
+  c.a = a;
+  const long long cap = (long long)a.max_q * a.group;
+  const long long ctas = chunk_tiles(a.s.batch, a.p.heads, cap, &c.q_tiles);
+  // ranges: the cost model of the window attention's key-range split
+  int max_splits = split_limit(sms, ctas), per = 0;
+  while (max_splits > 1 && chunk_ws(max_splits, a.s.rows, a.q_heads, D) > a.ws_bytes) --max_splits;
+  const long long keys = (long long)a.s.width * a.p.page;
+  attention_split((long long)a.s.batch * a.p.heads, (int)cap, (int)((keys + 127) / 128), 0, D, 128 * NQ, sms,
+                  max_splits, &c.splits, &per);
+  if (a.ws_bytes < chunk_ws(c.splits, a.s.rows, a.q_heads, D)) return KVQ_ERR_INVALID_ARG;
+  c.part_o = static_cast<float*>(a.ws);
+  c.part_ml = c.part_o + (size_t)c.splits * a.s.rows * a.q_heads * D;
+  if (ctas * c.splits > 0x7fffffffLL) return KVQ_ERR_TOO_LARGE;
+  CUtensorMap mk, mv;
+  const long long blocks = (long long)a.p.n_pages * a.p.heads;
+  if (!make_pages_map(&mk, a.p.codes[0], D, a.p.page, blocks, a.p.page) ||
+      !make_pages_map(&mv, a.p.codes[1], D, a.p.page, blocks, a.p.page))
+    return KVQ_ERR_CUDA;
+  using Cfg = ChunkCfg<D, NQ>;
+  if (ensure_smem_limit(chunk_kernel<D, NQ>, Cfg::kAlloc, g_chunk_smem[D == 128][NQ - 1]) != cudaSuccess)
+    return KVQ_ERR_CUDA;
+  if (launch_dependent(chunk_kernel<D, NQ>, (unsigned)(ctas * c.splits), Cfg::kThreads, Cfg::kAlloc, stream, c, mk,
+                       mv) != cudaSuccess)
+    return KVQ_ERR_CUDA;
+  if (c.splits > 1) {
+    const long long warps = (long long)a.s.batch * a.max_q * a.q_heads;
+    if ((warps + 7) / 8 > 0x7fffffffLL) return KVQ_ERR_TOO_LARGE;
+    if (launch_dependent(chunk_join_kernel<D>, (unsigned)((warps + 7) / 8), 256, 0, stream, c) != cudaSuccess)
+      return KVQ_ERR_CUDA;
+  }
+  return KVQ_OK;
+}
+
 }  // namespace
 
 size_t paged_attention_workspace(int kv_heads, int q_heads, int d, int batch, int rows, int max_q) {
   if (max_q > rows) max_q = rows;
   const long long cap = (long long)max_q * (q_heads / kv_heads);
-  if (cap > kDecRows) return 16;
-  return decode_ws(std::max(sm_count_current(), 1), batch, (int)cap, d).bytes;
+  const int sms = std::max(sm_count_current(), 1);
+  if (cap <= kDecRows) return decode_ws(sms, batch, (int)cap, d).bytes;
+  int q_tiles = 0;
+  return chunk_ws(split_limit(sms, chunk_tiles(batch, kv_heads, cap, &q_tiles)), rows, q_heads, d);
 }
 
 kvq_status launch_paged_attention(const PagedAttnArgs& a, cudaStream_t stream) {
-  const long long items = (long long)a.s.batch * a.p.heads;
-  if ((long long)a.max_q * a.group <= kDecRows && items <= 0x7fffffffLL) {
-    const bool wide = a.max_q * a.group > 8;
-    if (a.p.d == 64) return wide ? launch_decode<64, 2>(a, stream) : launch_decode<64, 1>(a, stream);
-    return wide ? launch_decode<128, 2>(a, stream) : launch_decode<128, 1>(a, stream);
+  const long long cap = (long long)a.max_q * a.group;
+  if (cap > 0x3fffffffLL || (long long)a.s.batch * a.p.heads > 0x7fffffffLL) return KVQ_ERR_TOO_LARGE;
+  if (cap <= kDecRows) {
+    if (a.p.d == 64) return cap > 8 ? launch_decode<64, 2>(a, stream) : launch_decode<64, 1>(a, stream);
+    return cap > 8 ? launch_decode<128, 2>(a, stream) : launch_decode<128, 1>(a, stream);
   }
-  const long long warps = (long long)a.s.batch * a.max_q * a.q_heads;
-  const long long grid = (warps + 3) / 4;
-  if (grid > 0x7fffffffLL) return KVQ_ERR_TOO_LARGE;
-  if (a.p.d == 64) paged_attn_kernel<64><<<(unsigned)grid, 128, 0, stream>>>(a);
-  else paged_attn_kernel<128><<<(unsigned)grid, 128, 0, stream>>>(a);
-  note_launch();
-  return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+  if (a.p.d == 64) return cap > 128 ? launch_chunk<64, 2>(a, stream) : launch_chunk<64, 1>(a, stream);
+  return cap > 128 ? launch_chunk<128, 2>(a, stream) : launch_chunk<128, 1>(a, stream);
 }
 
 }  // namespace kvq

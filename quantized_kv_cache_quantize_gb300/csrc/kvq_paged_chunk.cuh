@@ -1,0 +1,660 @@
+// Attention over the paged cache for many query rows per sequence: prompts,
+// chunks, batches of proposed tokens.
+//
+// Per (sequence, cache head) the rows of its query heads are packed, row r =
+// token r / group, head r % group, and a CTA takes 128 NQ of them over all
+// their keys, 128 at a time: S = c Q K^T, O += P V with the running base and
+// sum of the softmax.  4 d flops per row and key against 2 d bytes per key and
+// CTA: bound by the tensor cores, then by the exponentials and what feeds them.
+//
+// Products on tcgen05, accumulators in tensor memory.
+// - Q K^T: the E4M3 key tile goes from the page by TMA straight to the tensor
+//   core (kind::f8f6f4): no conversion, no copy.  The BF16 query row, scaled
+//   by a power of two to a largest magnitude in [128, 256), is split into E4M3
+//   high and low parts, two contractions at twice the 16-bit rate: 4 + 4 bits
+//   hold BF16's 8 exactly for elements down to 2^-9 of the row's largest, and
+//   smaller ones to 2^-17 of it.
+// - P V: P in FP16 from tensor memory (kind::f16); V codes to FP16 (exact) by
+//   four warps, as the transposed operand.  P in two E4M3 parts would spare
+//   that, but its range (2^-9 to 448) is too short for softmax weights.
+// Page scales are powers of two outside the products: K's on the scores, V's
+// on the weight before it is rounded, relative to the largest so far (eref);
+// the sum of weights is taken without them.
+// The base m is raised only when a weight would leave FP16 (a chunk's sum
+// past 2^15), to 2^9 headroom, so weights down to 2^-33 of the largest remain.
+//
+// Roles: 4 NQ warps softmax (one row per thread), 4 warps V conversion, one
+// MMA thread, one TMA warp.  With NQ = 2 the two query tiles alternate on the
+// tensor core (PV0 QK0' PV1 QK1'), each key tile is read and converted once
+// for 256 rows; NQ = 1 (at most 128 rows a head) holds two score buffers and
+// runs the next Q K^T ahead of the softmax instead.
+#pragma once
+
+#include <math_constants.h>
+
+#include "kvq_checks.cuh"
+#include "kvq_pages.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int kTileKeys = 128;
+constexpr int kKStages = 3, kVStages = 2, kMetaSlots = 8;
+
+template <int D, int NQ>
+struct ChunkCfg {
+  static constexpr int kQT = 128 * D;              // one E4M3 query tile
+  static constexpr int kQ = 0;                     // [NQ][high, low]
+  static constexpr int kK = NQ * 2 * kQT;          // key codes
+  static constexpr int kKT = kTileKeys * D;
+  static constexpr int kVr = kK + kKStages * kKT;  // value codes as they arrive
+  static constexpr int kV = kVr + kVStages * kKT;  // values in FP16, D / 64 sub-tiles [128][64]
+  static constexpr int kVT = 2 * kKT;
+  static constexpr int kMeta = kV + kVStages * kVT;
+  static constexpr int kBar = kMeta + kMetaSlots * 32;
+  static constexpr int kBytes = kBar + 256;
+  static constexpr int kAlloc = kBytes + 1024;
+  static constexpr int kSoftmaxWarps = 4 * NQ;
+  static constexpr int kMmaWarp = kSoftmaxWarps + 4;
+  static constexpr int kThreads = (kSoftmaxWarps + 6) * 32;
+  static constexpr int kTO = 256;                  // O tiles behind two score buffers
+  static constexpr int kTCols = 512;
+  static_assert(kTO + NQ * D <= kTCols, "tensor memory");
+  static_assert(kAlloc <= 232448, "shared memory");
+};
+
+enum : int {
+  kCbQ = 0,         // query tiles written (128 NQ arrivals)
+  kCbFullK = 1,     // [3] key codes landed, page exponents written
+  kCbEmptyK = 4,    // [3] the tile's QK MMAs done
+  kCbFullVr = 7,    // [2] value codes landed
+  kCbEmptyVr = 9,   // [2] value codes read (128 arrivals)
+  kCbFullV = 11,    // [2] FP16 values written (128 arrivals)
+  kCbEmptyV = 13,   // [2] the tile's PV MMAs done
+  kCbS = 15,        // [2] scores ready
+  kCbP = 17,        // [2] weights written, O rescaled (128 arrivals)
+  kCbOStep = 19,    // NQ = 1: a tile's PV done
+  kCbODone = 20,    // every MMA done
+  kCbMeta = 21,     // [8] a tile's page exponents written.  Not the key
+                    // barrier: its stage can be refilled, and its phase
+                    // passed twice, before a slow softmax warp looks at it
+  kCbCount = 29
+};
+
+struct ChunkArgs {
+  PagedAttnArgs a;
+  int q_tiles;        // row tiles of 128 NQ per (sequence, cache head), at most
+  int splits;         // key ranges per row tile
+  float* part_o;      // [splits][rows * q_heads][D] (splits > 1)
+  float* part_ml;     // [splits][rows * q_heads][2]
+};
+
+// the 16 keys' page of block `blk` of the line of 16-key blocks
+struct BlockMeta {
+  int id, word;       // word: K exponent + 64, V exponent + 64, valid bit
+};
+
+template <bool MASKED>
+__device__ __forceinline__ void exp_block(const uint32_t* s, float scale, float shift, int lo, int hi,
+                                          uint32_t* pk, float& sum) {
+  const uint64_t s2 = ptx::f2_pack(scale, scale), b2 = ptx::f2_pack(shift, shift);
+  uint64_t acc = ptx::f2_pack(0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    float x0, x1;
+    ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), s2, b2),
+                   x0, x1);
+    float e0 = ptx::ex2_approx(x0), e1 = ptx::ex2_approx(x1);
+    if (MASKED) {
+      e0 = (2 * k >= lo && 2 * k < hi) ? e0 : 0.f;
+      e1 = (2 * k + 1 >= lo && 2 * k + 1 < hi) ? e1 : 0.f;
+    }
+    acc = ptx::f2_add(acc, ptx::f2_pack(e0, e1));
+    pk[k] = ptx::f16x2_rn(e0, e1);
+  }
+  float a, b;
+  ptx::f2_unpack(acc, a, b);
+  sum = a + b;
+}
+
+__device__ __forceinline__ int meta_ek(int w) { return (w & 255) - 64; }
+__device__ __forceinline__ int meta_ev(int w) { return ((w >> 8) & 255) - 64; }
+__device__ __forceinline__ bool meta_ok(int w) { return (w >> 16) != 0; }
+
+template <int D, int NQ>
+__global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
+    chunk_kernel(const __grid_constant__ ChunkArgs p, const __grid_constant__ CUtensorMap map_k,
+                 const __grid_constant__ CUtensorMap map_v) {
+  using C = ChunkCfg<D, NQ>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const PagedAttnArgs& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  ptx::grid_dependency_wait();
+
+  // the longest row tiles (the last ones, under a causal mask) go first
+  const int heads = a.p.heads;
+  unsigned at = blockIdx.x;
+  const int h = (int)(at % (unsigned)heads);
+  at /= (unsigned)heads;
+  const int b = (int)(at % (unsigned)a.s.batch);
+  at /= (unsigned)a.s.batch;
+  const int split = (int)(at % (unsigned)p.splits);
+  const int qt = p.q_tiles - 1 - (int)(at / (unsigned)p.splits);
+  int r0, n;
+  seq_rows(a.s, b, r0, n, a.status);
+  if (n > a.max_q) {
+    page_error(a.status);
+    n = a.max_q;
+  }
+  const int rows = n * a.group;                 // of this head
+  const int row0 = qt * (128 * NQ);
+  if (row0 >= rows) return;
+  const int len = seq_len(a.s, b, a.p.shift, a.status);
+  const int t0 = len - n;                       // position of row 0
+  // keys that some row of the tile attends to, and their 128-key tiles
+  const int i_first = row0 / a.group, i_last = (min(rows, row0 + 128 * NQ) - 1) / a.group;
+  const int key_hi = a.causal ? max(min(len, t0 + i_last + 1), 0) : len;
+  const int key_lo = a.window > 0 ? max(0, t0 + i_first - a.window + 1) : 0;
+  const int tile_lo = key_lo / kTileKeys;
+  const int tiles = key_hi > key_lo ? (key_hi + kTileKeys - 1) / kTileKeys - tile_lo : 0;
+  const int j0 = (int)((long long)tiles * split / p.splits), j1 = (int)((long long)tiles * (split + 1) / p.splits);
+  const int n_t = j1 - j0;
+  const int base = (tile_lo + j0) * kTileKeys;  // first key of local tile 0
+
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + C::kBar + kCbCount * 8);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBar + kCbCount * 8 + 4);
+  const uint32_t bar0 = ptx::smem_u32(smem + C::kBar);
+  auto BAR = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+  if (tid == 0) {
+    ptx::mbar_init(BAR(kCbQ), 128 * NQ);
+    for (int i = 0; i < kKStages; ++i) {
+      ptx::mbar_init(BAR(kCbFullK + i), 1);
+      ptx::mbar_init(BAR(kCbEmptyK + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(BAR(kCbFullVr + i), 1);
+      ptx::mbar_init(BAR(kCbEmptyVr + i), 128);
+      ptx::mbar_init(BAR(kCbFullV + i), 128);
+      ptx::mbar_init(BAR(kCbEmptyV + i), 1);
+      ptx::mbar_init(BAR(kCbS + i), 1);
+      ptx::mbar_init(BAR(kCbP + i), 128);
+    }
+    for (int i = 0; i < kMetaSlots; ++i) ptx::mbar_init(BAR(kCbMeta + i), 1);
+    ptx::mbar_init(BAR(kCbOStep), 1);
+    ptx::mbar_init(BAR(kCbODone), 1);
+    *abort = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 0) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), C::kTCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const unsigned long long lim = a.wait_limit_ns;
+  const int* meta = reinterpret_cast<const int*>(smem + C::kMeta);
+
+  if (warp < C::kSoftmaxWarps) {
+    // =========================== softmax ===========================
+    const int q = warp >> 2;
+    const int r = tid - q * 128;                 // TMEM lane, row of the query tile
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const int row = row0 + q * 128 + r;          // of the head's rows
+    const bool live = row < rows;
+    const int tok = live ? row / a.group : 0;
+    const int hq = h * a.group + (live ? row % a.group : 0);
+    // ---- the query row: scale, split, store (K-major, swizzled) ----
+    float cq;
+    {
+      uint4 raw[D / 8];
+      const uint16_t* qp = a.q + (long long)(r0 + tok) * a.q_row_stride + (long long)hq * a.q_head_stride;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) raw[c] = live ? __ldg(reinterpret_cast<const uint4*>(qp) + c) : make_uint4(0u, 0u, 0u, 0u);
+      uint32_t mx = 0;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx = max(mx, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+      }
+      const int e = max((int)(mx >> 7), 1) - 127 - 7;      // largest magnitude to [2^7, 2^8)
+      const float f0 = pow2f(-(e / 2)), f1 = pow2f(-(e - e / 2));
+      cq = a.scale * 1.4426950408889634f * pow2f(e / 2) * pow2f(e - e / 2);
+      uint8_t* hi_t = smem + C::kQ + q * 2 * C::kQT;
+      uint8_t* lo_t = hi_t + C::kQT;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t wh[4], wl[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint4& v = raw[2 * c + (k >> 1)];
+          const uint32_t w0 = (k & 1) ? v.z : v.x, w1 = (k & 1) ? v.w : v.y;
+          const float x0 = __uint_as_float(w0 << 16) * f0 * f1, x1 = __uint_as_float(w0 & 0xffff0000u) * f0 * f1;
+          const float x2 = __uint_as_float(w1 << 16) * f0 * f1, x3 = __uint_as_float(w1 & 0xffff0000u) * f0 * f1;
+          wh[k] = e4m3x4(x0, x1, x2, x3);
+          const uint32_t h01 = f16x2_of_e4m3x2((uint16_t)wh[k]), h23 = f16x2_of_e4m3x2((uint16_t)(wh[k] >> 16));
+          const float2 a01 = __half22float2(*reinterpret_cast<const __half2*>(&h01));
+          const float2 a23 = __half22float2(*reinterpret_cast<const __half2*>(&h23));
+          wl[k] = e4m3x4(x0 - a01.x, x1 - a01.y, x2 - a23.x, x3 - a23.y);
+        }
+        const int off = D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+        *reinterpret_cast<uint4*>(hi_t + off) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
+        *reinterpret_cast<uint4*>(lo_t + off) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
+      }
+    }
+    ptx::fence_proxy_async_smem();
+    ptx::mbar_arrive(BAR(kCbQ));
+
+    // keys this row attends to (rows past the last: none)
+    const int tq = t0 + tok;
+    const int hi_r = live ? (a.causal ? min(len, tq + 1) : len) : 0;
+    const int lo_r = a.window > 0 ? max(0, tq - a.window + 1) : 0;
+    float m = -CUDART_INF_F, l = 0.f;
+    int eref = -1000;
+    const uint32_t t_o = tmem + C::kTO + q * D + lane_off;
+    bool ok = true;
+    for (int j = 0; j < n_t; ++j) {
+      const int sb = NQ == 2 ? q : (j & 1);
+      const uint32_t t_s = tmem + sb * 128 + lane_off;
+      const uint32_t par = NQ == 2 ? (j & 1) : ((j >> 1) & 1);
+      // a slot of exponents is written again 8 tiles later, the TMA warp at
+      // most 5 ahead of the softmax (3 key stages, 2 score buffers)
+      ok = page_wait(BAR(kCbMeta + (j & (kMetaSlots - 1))), (j / kMetaSlots) & 1, lim, abort, a.status) &&
+           page_wait(BAR(kCbS + sb), par, lim, abort, a.status);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      ptx::tc_fence_after();
+      const int* mt = meta + (j & (kMetaSlots - 1)) * 8;
+      const int e_in = eref;
+      bool blocks = true;
+#pragma unroll
+      for (int k = 0; k < 8; k += 4) {
+        const int4 x = *reinterpret_cast<const int4*>(mt + k);
+        const int w4[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          blocks &= meta_ok(w4[i]);
+          eref = meta_ok(w4[i]) ? max(eref, meta_ev(w4[i])) : eref;
+        }
+      }
+      const int key0 = base + j * kTileKeys;
+      const int lo_t = lo_r - key0, hi_t = hi_r - key0;
+      const bool whole = __all_sync(0xffffffffu, blocks && lo_t <= 0 && hi_t >= kTileKeys);
+      const float m_in = m;
+      float sum_l = 0.f;
+      auto pass = [&](auto tag) {
+        constexpr bool MASKED = decltype(tag)::value;
+#pragma unroll 2
+        for (int c = 0; c < 4; ++c) {
+          uint32_t cur[32], pk[16];
+          ptx::tmem_ld32(t_s + 32 * c, cur);
+          const int2 w2 = *reinterpret_cast<const int2*>(mt + 2 * c);
+          const int wa = w2.x, wb = w2.y;
+          const float ca = cq * pow2f(meta_ek(wa)), cb = cq * pow2f(meta_ek(wb));
+          const int sa = min(max(meta_ev(wa) - eref, -60), 0), sb2 = min(max(meta_ev(wb) - eref, -60), 0);
+          // the row's columns of each block of 16
+          const int loa = meta_ok(wa) ? lo_t - 32 * c : 16, hia = hi_t - 32 * c;
+          const int lob = meta_ok(wb) ? lo_t - 32 * c - 16 : 16, hib = hi_t - 32 * c - 16;
+          float ha, hb;
+          exp_block<MASKED>(cur, ca, (float)sa - m, loa, hia, pk, ha);
+          exp_block<MASKED>(cur + 16, cb, (float)sb2 - m, lob, hib, pk + 8, hb);
+          // past FP16 (or the first weights of all, against the base -inf):
+          // a new base, and what the tile has so far follows it
+          if (__any_sync(0xffffffffu, !(ha + hb <= 32768.0f))) {
+            float top = -CUDART_INF_F;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const bool in_a = !MASKED || (k >= loa && k < hia), in_b = !MASKED || (k >= lob && k < hib);
+              top = in_a ? fmaxf(top, fmaf(__uint_as_float(cur[k]), ca, (float)sa)) : top;
+              top = in_b ? fmaxf(top, fmaf(__uint_as_float(cur[16 + k]), cb, (float)sb2)) : top;
+            }
+            const float m_new = fmaxf(m, top - 9.f);
+            const float f = m > -CUDART_INF_F ? exp2f(m - m_new) : 0.f;
+            sum_l *= f;
+            if (c > 0) {
+              ptx::tmem_st_wait();
+              for (int cc = 0; cc < c; ++cc) {
+                uint32_t v[16];
+                ptx::tmem_ld16(t_s + 16 * cc, v);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                  const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&v[k]));
+                  v[k] = ptx::f16x2_rn(z.x * f, z.y * f);
+                }
+                ptx::tmem_st16(t_s + 16 * cc, v);
+              }
+            }
+            m = m_new;
+            exp_block<MASKED>(cur, ca, (float)sa - m, loa, hia, pk, ha);
+            exp_block<MASKED>(cur + 16, cb, (float)sb2 - m, lob, hib, pk + 8, hb);
+          }
+          sum_l = fmaf(ha, pow2f(-sa), sum_l);
+          sum_l = fmaf(hb, pow2f(-sb2), sum_l);
+          ptx::tmem_st16(t_s + 16 * c, pk);
+        }
+      };
+      if (whole) pass(std::false_type{}); else pass(std::true_type{});
+      if (NQ == 1 && j > 0) {
+        // this tile's QK ran before the previous tile's PV: O waits for it
+        ok = page_wait(BAR(kCbOStep), (j - 1) & 1, lim, abort, a.status);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+      }
+      if (__any_sync(0xffffffffu, m != m_in || eref != e_in)) {
+        const float f = m_in > -CUDART_INF_F ? exp2f(m_in - m) : (m > -CUDART_INF_F ? 0.f : 1.f);
+        l *= f;
+        if (j > 0) {
+          const float fo = e_in > -1000 ? f * pow2f(max(e_in - eref, -126)) : 0.f;
+          const uint64_t f2 = ptx::f2_pack(fo, fo);
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t v[32];
+            ptx::tmem_ld32(t_o + 32 * c, v);
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              float x, y;
+              ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), f2), x, y);
+              v[k] = __float_as_uint(x);
+              v[k + 1] = __float_as_uint(y);
+            }
+            ptx::tmem_st32(t_o + 32 * c, v);
+          }
+        }
+      }
+      l += sum_l;
+      ptx::tmem_st_wait();
+      ptx::tc_fence_before();
+      ptx::mbar_arrive(BAR(kCbP + q));
+    }
+
+    // ---- result ----
+    if (ok) ok = page_wait(BAR(kCbODone), 0, lim, abort, a.status);
+    ok = __all_sync(0xffffffffu, ok && !*abort);
+    if (ok) {
+      ptx::tc_fence_after();
+      const long long orow = (long long)(r0 + tok) * a.q_heads + hq;
+      const bool store = live && KVQ_IN_BOUNDS(orow, (long long)a.s.rows * a.q_heads, a.status, a.bounds_site);
+      const float fe = eref > -1000 ? pow2f(eref) : 0.f;
+      const bool part = p.splits > 1;
+      const float f = part ? fe : (l > 0.f ? fe / l : 0.f);
+      const long long prow = (long long)split * a.s.rows * a.q_heads + orow;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t v[32];
+        if (n_t > 0) {
+          ptx::tmem_ld32(t_o + 32 * c, v);   // warp-collective: every lane
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = 0u;
+        }
+        if (!store) continue;
+        if (part) {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + 32 * c);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            dst[k] = make_float4(__uint_as_float(v[4 * k]) * f, __uint_as_float(v[4 * k + 1]) * f,
+                                 __uint_as_float(v[4 * k + 2]) * f, __uint_as_float(v[4 * k + 3]) * f);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + 32 * c);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t z[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(v[8 * k + 2 * i]) * f,
+                                                             __uint_as_float(v[8 * k + 2 * i + 1]) * f);
+              z[i] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+            dst[k] = make_uint4(z[0], z[1], z[2], z[3]);
+          }
+        }
+      }
+      if (store) {
+        if (part) *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(m, l);
+        else if (a.lse != nullptr) a.lse[orow] = l > 0.f ? 0.6931471805599453f * (m + log2f(l)) : -CUDART_INF_F;
+      }
+    }
+  } else if (warp < C::kMmaWarp) {
+    // ====================== values to FP16 ======================
+    const int r = tid - C::kSoftmaxWarps * 32;   // key of the tile
+    // what no row attends to must not reach the product (zero times NaN)
+    const int first = a.window > 0 ? max(0, t0 - a.window + 1) : 0;
+    for (int j = 0; j < n_t; ++j) {
+      const int s = j & 1;
+      const uint32_t par = (j >> 1) & 1;
+      if (!page_wait(BAR(kCbFullVr + s), par, lim, abort, a.status)) break;
+      const int key = base + j * kTileKeys + r;
+      const bool use = key >= first && key < len && meta_ok(meta[(j & (kMetaSlots - 1)) * 8 + (r >> 4)]);
+      uint4 raw[D / 16];
+      const uint8_t* src = smem + C::kVr + s * C::kKT;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        const int off = D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+        raw[c] = *reinterpret_cast<const uint4*>(src + off);
+        if (!use) raw[c] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      ptx::mbar_arrive(BAR(kCbEmptyVr + s));
+      if (j >= 2 && !page_wait(BAR(kCbEmptyV + s), par ^ 1u, lim, abort, a.status)) break;
+      uint8_t* dst = smem + C::kV + s * C::kVT;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int ch = 2 * c + i;               // 16-byte chunk: channels 8 ch ..
+          uint4 o;
+          o.x = f16x2_of_e4m3x2((uint16_t)w[2 * i]);
+          o.y = f16x2_of_e4m3x2((uint16_t)(w[2 * i] >> 16));
+          o.z = f16x2_of_e4m3x2((uint16_t)w[2 * i + 1]);
+          o.w = f16x2_of_e4m3x2((uint16_t)(w[2 * i + 1] >> 16));
+          *reinterpret_cast<uint4*>(dst + (ch >> 3) * 16384 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = o;
+        }
+      }
+      ptx::fence_proxy_async_smem();
+      ptx::mbar_arrive(BAR(kCbFullV + s));
+    }
+  } else if (warp == C::kMmaWarp) {
+    // ============================= MMA =============================
+    if (lane == 0) {
+      constexpr uint32_t kIdS = ptx::idesc_f8kind(128, kTileKeys);
+      constexpr uint32_t kIdO = ptx::idesc_f16kind(128, D, true, false);
+      constexpr uint32_t kLay = D == 128 ? ptx::kLayoutSw128 : ptx::kLayoutSw64;
+      const uint32_t s_base = ptx::smem_u32(smem);
+      const uint64_t d8 = ptx::smem_desc(s_base, 16, 8 * D, kLay);       // E4M3 rows of D bytes
+      const uint64_t dv = ptx::smem_desc(s_base, 16384, 1024, ptx::kLayoutSw128);
+      auto plus = [](uint64_t d, uint32_t off) { return d + (uint64_t)(off >> 4); };
+      bool ok = n_t == 0 || page_wait(BAR(kCbQ), 0, lim, abort, a.status);
+      auto qk = [&](int ks, int q, uint32_t dst) {
+        const uint64_t db = plus(d8, C::kK + ks * C::kKT);
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          const uint64_t da = plus(d8, C::kQ + (2 * q + part) * C::kQT);
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k)
+            ptx::mma_f8(dst, da + (uint64_t)(2 * k), db + (uint64_t)(2 * k), kIdS, (part > 0 || k > 0) ? 1u : 0u);
+        }
+      };
+      auto pv = [&](int j, int q, uint32_t p_tmem) {
+        const uint64_t db = plus(dv, C::kV + (j & 1) * C::kVT);
+#pragma unroll
+        for (int k = 0; k < kTileKeys / 16; ++k)
+          ptx::mma_f16_ts(tmem + C::kTO + q * D, p_tmem + 8 * k, db + (uint64_t)((k * 2048) >> 4), kIdO,
+                          (j > 0 || k > 0) ? 1u : 0u);
+      };
+      int ks = 0;
+      uint32_t kph = 0;
+      auto next_k = [&]() {
+        const bool good = page_wait(BAR(kCbFullK + ks), kph, lim, abort, a.status);
+        ptx::tc_fence_after();
+        return good;
+      };
+      auto step_k = [&]() {
+        ptx::mma_commit(BAR(kCbEmptyK + ks));
+        if (++ks == kKStages) {
+          ks = 0;
+          kph ^= 1u;
+        }
+      };
+      if (ok && n_t > 0) {
+        ptx::tc_fence_after();
+        ok = next_k();
+        if (ok) {
+          for (int q = 0; q < NQ; ++q) {
+            qk(ks, q, tmem + q * 128);
+            ptx::mma_commit(BAR(kCbS + q));
+          }
+          step_k();
+        }
+        for (int j = 0; j < n_t && ok; ++j) {
+          const bool more = j + 1 < n_t;
+          if (NQ == 1 && more) {
+            if (!(ok = next_k())) break;
+            qk(ks, 0, tmem + ((j + 1) & 1) * 128);
+            ptx::mma_commit(BAR(kCbS + ((j + 1) & 1)));
+            step_k();
+          }
+          for (int q = 0; q < NQ && ok; ++q) {
+            if (!(ok = page_wait(BAR(kCbP + q), j & 1, lim, abort, a.status))) break;
+            if (q == 0 && !(ok = page_wait(BAR(kCbFullV + (j & 1)), (j >> 1) & 1, lim, abort, a.status))) break;
+            ptx::tc_fence_after();
+            pv(j, q, tmem + (NQ == 2 ? q : (j & 1)) * 128);
+            if (q == NQ - 1) ptx::mma_commit(BAR(kCbEmptyV + (j & 1)));
+            if (NQ == 1) ptx::mma_commit(BAR(kCbOStep));
+            if (NQ == 2 && more) {
+              if (q == 0 && !(ok = next_k())) break;
+              qk(ks, q, tmem + q * 128);
+              ptx::mma_commit(BAR(kCbS + q));
+              if (q == 1) step_k();
+            }
+          }
+        }
+      }
+      // every MMA issued is done before the tensor memory goes back
+      ptx::mma_commit(BAR(kCbODone));
+      page_drain(BAR(kCbODone), 0, lim);
+    }
+    __syncwarp();
+  } else {
+    // ============================== TMA ==============================
+    const uint32_t s_base = ptx::smem_u32(smem);
+    // lane k < 8: the page of keys [16 k, 16 k + 16) of a tile
+    auto look = [&](int j) -> BlockMeta {
+      BlockMeta o{-1, 0};
+      const int key = base + j * kTileKeys + 16 * lane;
+      // (a page wholly before every row's window may be gone already)
+      if (j < n_t && lane < 8 && key < key_hi && (((key >> a.p.shift) + 1) << a.p.shift) > key_lo) {
+        o.id = seq_page(a.s, b, key >> a.p.shift, a.p.n_pages, a.status);
+        if (o.id >= 0) {
+          const long long blk = (long long)o.id * heads + h;
+          o.word = (scale_exp(__ldg(a.p.scale[0] + blk)) + 64) | ((scale_exp(__ldg(a.p.scale[1] + blk)) + 64) << 8) |
+                   (1 << 16);
+        }
+      }
+      return o;
+    };
+    BlockMeta cur = look(0);
+    int ks = 0, last_k = -1, last_v = -1;
+    uint32_t kph = 0;
+    bool ok = true;
+    for (int j = 0; j < n_t; ++j) {
+      const BlockMeta nxt = look(j + 1);
+      const bool box = cur.id >= 0 && ((16 * lane) & (a.p.page - 1)) == 0;
+      const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, box));
+      const uint32_t bytes = boxes * (uint32_t)(a.p.page * D);
+      if (j >= kKStages) ok = page_wait(BAR(kCbEmptyK + ks), kph ^ 1u, lim, abort, a.status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (lane < 8) const_cast<int*>(meta)[(j & (kMetaSlots - 1)) * 8 + lane] = cur.word;
+      __syncwarp();
+      if (lane == 0) {
+        ptx::mbar_arrive(BAR(kCbMeta + (j & (kMetaSlots - 1))));
+        if (bytes > 0) ptx::mbar_expect_tx(BAR(kCbFullK + ks), bytes); else ptx::mbar_arrive(BAR(kCbFullK + ks));
+      }
+      __syncwarp();
+      if (box)
+        ptx::tma_load_3d(s_base + C::kK + ks * C::kKT + 16 * lane * D, &map_k, 0, 0, cur.id * heads + h, BAR(kCbFullK + ks));
+      last_k = j;
+      if (j >= kVStages) ok = page_wait(BAR(kCbEmptyVr + (j & 1)), ((j >> 1) - 1) & 1, lim, abort, a.status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (lane == 0) {
+        if (bytes > 0) ptx::mbar_expect_tx(BAR(kCbFullVr + (j & 1)), bytes); else ptx::mbar_arrive(BAR(kCbFullVr + (j & 1)));
+      }
+      __syncwarp();
+      if (box)
+        ptx::tma_load_3d(s_base + C::kVr + (j & 1) * C::kKT + 16 * lane * D, &map_v, 0, 0, cur.id * heads + h,
+                         BAR(kCbFullVr + (j & 1)));
+      last_v = j;
+      if (++ks == kKStages) {
+        ks = 0;
+        kph ^= 1u;
+      }
+      cur = nxt;
+    }
+    // no copy is in flight when the CTA exits, however the others ended
+    for (int j = max(0, last_k - kKStages + 1); j <= last_k; ++j)
+      page_drain(BAR(kCbFullK + j % kKStages), (j / kKStages) & 1, lim);
+    for (int j = max(0, last_v - kVStages + 1); j <= last_v; ++j)
+      page_drain(BAR(kCbFullVr + (j & 1)), (j >> 1) & 1, lim);
+    __syncwarp();
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, C::kTCols);
+  }
+}
+
+// Joins the key ranges of split row tiles: one warp per query row and head,
+// the ranges in order.
+template <int D>
+__global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkArgs p) {
+  constexpr int C = D / 32;
+  ptx::grid_dependency_wait();
+  const PagedAttnArgs& a = p.a;
+  const int lane = threadIdx.x & 31;
+  const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int hq = (int)(w % a.q_heads);
+  const long long rb = w / a.q_heads;
+  const int i = (int)(rb % a.max_q);
+  const long long b = rb / a.max_q;
+  if (b >= a.s.batch) return;
+  int r0, n;
+  seq_rows(a.s, (int)b, r0, n, a.status);
+  if (i >= min(n, a.max_q)) return;
+  const long long row = (long long)(r0 + i) * a.q_heads + hq, step = (long long)a.s.rows * a.q_heads;
+  if (!KVQ_IN_BOUNDS(row, step, a.status, a.bounds_site)) return;
+  float top = -CUDART_INF_F;
+  for (int s = lane; s < p.splits; s += 32) top = fmaxf(top, p.part_ml[(s * step + row) * 2]);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+  const float base = top > -CUDART_INF_F ? top : 0.f;
+  float o[C], l = 0.f;
+#pragma unroll
+  for (int c = 0; c < C; ++c) o[c] = 0.f;
+  for (int s = 0; s < p.splits; ++s) {
+    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (s * step + row) * 2);
+    const float f = ptx::ex2_approx(ml.x - base);
+    l = fmaf(ml.y, f, l);
+#pragma unroll
+    for (int c = 0; c < C; ++c) o[c] = fmaf(p.part_o[(s * step + row) * D + C * lane + c], f, o[c]);
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int c = 0; c < C; c += 2) {
+    const __nv_bfloat162 y = __floats2bfloat162_rn(o[c] * inv, o[c + 1] * inv);
+    *reinterpret_cast<uint32_t*>(a.out + row * D + C * lane + c) = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  if (lane == 0 && a.lse != nullptr) a.lse[row] = l > 0.f ? 0.6931471805599453f * (top + log2f(l)) : -CUDART_INF_F;
+}
+
+}  // namespace
+}  // namespace kvq

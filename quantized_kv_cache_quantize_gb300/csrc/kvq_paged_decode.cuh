@@ -71,6 +71,7 @@ struct DecodeArgs {
 // (lo rounded down to a unit), units of one head.
 struct SeqWork {
   int r0, n, len, lo, units;
+  int seen;   // first key some row attends to; lo is this rounded down
 };
 __device__ __forceinline__ SeqWork seq_work(const PagedAttnArgs& a, int b) {
   SeqWork w;
@@ -81,7 +82,8 @@ __device__ __forceinline__ SeqWork seq_work(const PagedAttnArgs& a, int b) {
   }
   w.len = seq_len(a.s, b, a.p.shift, a.status);
   const int t0 = w.len - w.n;
-  w.lo = (a.window > 0 ? max(0, t0 - a.window + 1) : 0) & ~(kUnit - 1);
+  w.seen = a.window > 0 ? max(0, t0 - a.window + 1) : 0;
+  w.lo = w.seen & ~(kUnit - 1);
   // a sequence with rows has one unit at least: it writes their empty result
   w.units = w.n > 0 ? max(1, (w.len - w.lo + kUnit - 1) / kUnit) : 0;
   return w;
@@ -225,7 +227,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
     auto page_info = [&](int base, int& id, int& ek, int& ev) {
       id = -1;
       ek = ev = 0;
-      if (base + lane < page_end) {
+      // (a page wholly before every row's window may be gone already)
+      if (base + lane < page_end && (base + lane + 1) << shift > w.seen) {
         id = seq_page(a.s, b, base + lane, a.p.n_pages, a.status);
         if (id >= 0) {
           const long long blk = (long long)id * heads + h;
@@ -480,8 +483,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
             // what no row of the sequence may see must not reach the product
             // (a zero weight times a NaN)
             const int key = key0 + r;
-            const bool use = key >= key_first && key < w.len && idt[mt] >= 0 &&
-                             (a.window == 0 || key > t0 - a.window);
+            const bool use = key >= w.seen && key < w.len && idt[mt] >= 0;
 #pragma unroll
             for (int v = 0; v < D / 32; ++v) x[j][v] = use ? x[j][v] : 0u;
           }

@@ -66,32 +66,37 @@ def dev(t, dtype=torch.int32):
     return torch.as_tensor(np.asarray(t)).to(dtype).cuda()
 
 
-def tolerances(out, lse, bound, serr, d, n_keys):
+def tolerances(out, lse, bound, serr, qerr, d, n_keys):
     """How far out and lse may be from the 64-bit answer, element by element.
-    The codes, scales and queries are exact operands; what rounds is
+    The codes and scales are exact operands; what rounds is
+    - a query element far below its row's largest: as two E4M3 parts with the
+      largest magnitude at 2^7 or above, an element is off by half a step of
+      the subnormals at most, 2^-10, so by 2^-17 of the largest (as FP16 with
+      the largest at 2^14 or above: 2^-39);
     - a score: d products summed in fp32 (d + 1 roundings, at 2^-23 each
       because the tensor core may truncate) and the multiplications by the
       scales and log2 e (3 more), all relative to sum |q k|, plus its 2^x
       (2^-21 relative, the special-function unit's bound doubled);
       a shift ds of a score moves p by a factor e^ds, and its sum likewise:
       2 ds relative;
-    - p as a 16-bit operand: 2^-11 (FP16, half a step); weights below 2^-39
-      of the largest are dropped there, n_keys of them at most;
+    - p as a 16-bit operand: 2^-11 (FP16, half a step); FP16 subnormals add
+      2^-25 a key, n_keys of them at most, where the largest weight stands at
+      2^9 or above: 2^-34 of it;
     - sums of n_keys terms in fp32: n_keys 2^-23, relative to sum p |v|;
     - the BF16 output: 2^-8 (half a step) of the value.
     lse: the score's shift, the fp32 sum, and its own representation."""
-    ds = (d + 4) * 2.0 ** -23 * serr + 2.0 ** -21
-    rel = 2 * ds + 2.0 ** -11 + n_keys * 2.0 ** -23 + n_keys * 2.0 ** -39
+    ds = (d + 4) * 2.0 ** -23 * serr + 2.0 ** -17 * qerr + 2.0 ** -21
+    rel = 2 * ds + 2.0 ** -11 + n_keys * 2.0 ** -23 + n_keys * 2.0 ** -34
     tol_o = (2.0 ** -8) * (np.abs(out) + rel[..., None] * bound) + rel[..., None] * bound
     tol_l = ds + n_keys * 2.0 ** -23 + 2.0 ** -21 + np.where(np.isfinite(lse), np.abs(lse), 0) * 2.0 ** -22
     return tol_o, tol_l
 
 
 def check_attention(got, ref, d, n_keys, what=""):
-    out, lse, bound, serr = ref
+    out, lse, bound, serr, qerr = ref
     o = got[0].float().cpu().numpy().astype(np.float64)
     z = got[1].cpu().numpy().astype(np.float64)
-    tol_o, tol_l = tolerances(out, lse, bound, serr, d, n_keys)
+    tol_o, tol_l = tolerances(out, lse, bound, serr, qerr, d, n_keys)
     assert np.isfinite(o).all(), what
     empty = ~np.isfinite(lse)
     assert np.array_equal(z == -np.inf, empty), what

@@ -138,6 +138,9 @@ ATTENTION = [  # d, page, q heads, cache heads, lengths, query rows, causal, win
     (128, 16, 2, 1, [40], [150], True, 0),                      # more rows than keys
     (64, 128, 24, 8, [150, 300], [1, 65], False, 90),
     (128, 64, 3, 1, [640], [1], True, 1),
+    (64, 32, 8, 1, [3000, 2000], [5, 5], True, 0),              # one row tile, many key tiles
+    (128, 64, 2, 1, [2500], [50], False, 2100),
+    (128, 128, 2, 1, [1900], [140], True, 0),
 ]
 
 
@@ -194,6 +197,25 @@ def test_attention_strides_layer_and_stale_pages(d, hq, hkv, rows):
                               scale=0.2, layer=1, with_lse=True, max_q=rows)
     clean()
     check_attention(got, ref, d, 100)
+
+
+@pytest.mark.parametrize("d,page,hq,rows", [(128, 16, 4, 1), (64, 16, 2, 5), (64, 64, 4, 1), (128, 32, 8, 20),
+                                            (64, 16, 6, 30), (128, 128, 2, 300)])
+def test_attention_pages_before_the_window_may_be_gone(d, page, hq, rows):
+    """Table entries of pages wholly before every row's window are not read."""
+    lens, window = [520, 600, 40], 45
+    rng, codes, exps, table = pool_case(31, lens, page, 2, d, e_lo=-8, e_hi=-6)
+    counts = [rows, rows, min(rows, 3)]
+    q = rows_of(rng, sum(counts), hq, d, 0.2)
+    pool = P.Pool([c[0].numpy() for c in codes], [e[0] for e in exps])
+    ref = P.attention(pool, q.double().numpy(), table, lens, counts, 0.1, True, window)
+    t = table.copy()
+    for b, (n, r) in enumerate(zip(lens, counts)):
+        t[b, :max(0, n - r - window + 1) // page] = -1 if b else 1 << 30
+    got = kvq.paged_attention(cache_of(codes, exps), q.cuda(), dev(t), dev(lens), offsets_of(counts), scale=0.1,
+                              window=window, with_lse=True, max_q=max(counts))
+    clean()
+    check_attention(got, ref, d, window)
 
 
 @pytest.mark.parametrize("rows,hq", [(1, 2), (2, 2), (80, 2)])
