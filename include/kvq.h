@@ -423,7 +423,8 @@ typedef struct kvq_pages {
  *   table    int32 [batch][width], rows table_stride elements apart: entry p
  *            is the page of tokens [p * page_tokens, + page_tokens).  Entries
  *            past a sequence's length are not read, nor by the attention
- *            those of pages wholly before every row's window.
+ *            those of pages wholly before every row's window.  width *
+ *            page_tokens <= 2^30 (else KVQ_ERR_TOO_LARGE).
  *   kv_lens  int32 [batch]: tokens per sequence (0 is allowed).
  *   offsets  int32 [batch + 1], ascending from 0: rows [offsets[b],
  *            offsets[b + 1]) of the call's packed row tensor belong to
@@ -472,11 +473,12 @@ kvq_status kvq_pages_append(const kvq_pages *pages, int32_t layer, const uint16_
 
 /*
  * Workspace bytes of kvq_paged_attention for this pool, q_heads, rows query
- * rows in batch sequences of at most max_q rows each.  Depends on the current
- * device's SM count.  0 on a bad argument.
+ * rows in batch sequences of at most max_q rows each, and a table of `width`
+ * entries per sequence.  Depends on the current device's SM count.  0 on a
+ * bad argument; 16 when the call needs none (workspace may be NULL then).
  */
 size_t kvq_paged_workspace_bytes(const kvq_pages *pages, int32_t q_heads, int32_t batch,
-                                 int32_t rows, int32_t max_q);
+                                 int32_t width, int32_t rows, int32_t max_q);
 
 /*
  * Attention over the pages of `layer`.  q: BF16 device, row r of head h at

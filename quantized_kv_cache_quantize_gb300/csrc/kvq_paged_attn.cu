@@ -17,7 +17,7 @@ namespace {
 // ---- few rows: the decoding form ----
 constexpr int kDecRows = 16;
 
-std::atomic<uint64_t> g_decode_smem[2][2];
+std::atomic<uint64_t> g_decode_smem[2][2], g_item_smem[2][2];
 
 template <typename... Args>
 cudaError_t launch_dependent(void (*kern)(Args...), unsigned grid, int threads, int smem,
@@ -49,11 +49,35 @@ DecodeWs decode_ws(int sms, int batch, int rows_cap, int d) {
   return w;
 }
 
+// A CTA per (sequence, cache head): the most units an item can have are few,
+// and the items no more than two waves of CTAs.
+bool decode_by_item(int sms, long long items, long long keys) {
+  return keys <= (long long)kItemUnits * kUnit && items <= 2LL * sms;
+}
+
 template <int D, int NT>
 kvq_status launch_decode(const PagedAttnArgs& a, cudaStream_t stream) {
   const int sms = sm_count_current();
   if (sms <= 0) return KVQ_ERR_CUDA;
   const int rows_cap = a.max_q * a.group;
+  const long long items = (long long)a.s.batch * a.p.heads;
+  CUtensorMap mk, mv;
+  const long long blocks = (long long)a.p.n_pages * a.p.heads;
+  const int box = a.p.page < kUnit ? a.p.page : kUnit;
+  if (!make_pages_map(&mk, a.p.codes[0], D, a.p.page, blocks, box) ||
+      !make_pages_map(&mv, a.p.codes[1], D, a.p.page, blocks, box))
+    return KVQ_ERR_CUDA;
+  const int smem = DecCfg<D>::kAlloc;
+  DecodeArgs d{};
+  d.a = a;
+  d.rows_cap = rows_cap;
+  if (decode_by_item(sms, items, (long long)a.s.width * a.p.page)) {
+    if (ensure_smem_limit(decode_item_kernel<D, NT>, smem, g_item_smem[D == 128][NT - 1]) != cudaSuccess ||
+        launch_dependent(decode_item_kernel<D, NT>, (unsigned)items, kDecWarps * 32, smem, stream, d, mk, mv) !=
+            cudaSuccess)
+      return KVQ_ERR_CUDA;
+    return KVQ_OK;
+  }
   const DecodeWs ws = decode_ws(sms, a.s.batch, rows_cap, D);
   if (a.ws_bytes < ws.bytes) return KVQ_ERR_INVALID_ARG;
   // the units there can be, from the table's width, bound the grid
@@ -63,27 +87,16 @@ kvq_status launch_decode(const PagedAttnArgs& a, cudaStream_t stream) {
     grid = (int)(most / kMinUnits) + 1;
     if (grid > sms) grid = sms;
   }
-  DecodeArgs d{};
-  d.a = a;
   uint8_t* base = static_cast<uint8_t*>(a.ws);
   d.pre = reinterpret_cast<long long*>(base + ws.pre);
   d.part_ml = reinterpret_cast<float*>(base + ws.ml);
   d.part_o = reinterpret_cast<float*>(base + ws.o);
-  d.rows_cap = rows_cap;
   d.warps = grid * kDecWarps;
-  CUtensorMap mk, mv;
-  const long long blocks = (long long)a.p.n_pages * a.p.heads;
-  const int box = a.p.page < kUnit ? a.p.page : kUnit;
-  if (!make_pages_map(&mk, a.p.codes[0], D, a.p.page, blocks, box) ||
-      !make_pages_map(&mv, a.p.codes[1], D, a.p.page, blocks, box))
-    return KVQ_ERR_CUDA;
-  const int smem = DecCfg<D>::kAlloc;
   if (ensure_smem_limit(decode_kernel<D, NT>, smem, g_decode_smem[D == 128][NT - 1]) != cudaSuccess)
     return KVQ_ERR_CUDA;
   if (launch_dependent(decode_kernel<D, NT>, (unsigned)grid, kDecWarps * 32, smem, stream, d, mk, mv) !=
       cudaSuccess)
     return KVQ_ERR_CUDA;
-  const long long items = (long long)a.s.batch * a.p.heads;
   if (launch_dependent(join_kernel<D>, (unsigned)items, kJoinWarps * 32, 0, stream, d) != cudaSuccess)
     return KVQ_ERR_CUDA;
   return KVQ_OK;
@@ -147,11 +160,12 @@ kvq_status launch_chunk(const PagedAttnArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-size_t paged_attention_workspace(int kv_heads, int q_heads, int d, int batch, int rows, int max_q) {
+size_t paged_attention_workspace(int kv_heads, int q_heads, int d, int batch, long long keys, int rows, int max_q) {
   if (max_q > rows) max_q = rows;
   const long long cap = (long long)max_q * (q_heads / kv_heads);
   const int sms = std::max(sm_count_current(), 1);
-  if (cap <= kDecRows) return decode_ws(sms, batch, (int)cap, d).bytes;
+  if (cap <= kDecRows)
+    return decode_by_item(sms, (long long)batch * kv_heads, keys) ? 16 : decode_ws(sms, batch, (int)cap, d).bytes;
   int q_tiles = 0;
   return chunk_ws(split_limit(sms, chunk_tiles(batch, kv_heads, cap, &q_tiles)), rows, q_heads, d);
 }

@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
       BlockMeta o{-1, 0};
       const int key = base + j * kTileKeys + 16 * lane;
       // (a page wholly before every row's window may be gone already)
-      if (j < n_t && lane < 8 && key < key_hi && (((key >> a.p.shift) + 1) << a.p.shift) > key_lo) {
+      if (j < n_t && lane < 8 && key < key_hi && ((long long)((key >> a.p.shift) + 1) << a.p.shift) > key_lo) {
         o.id = seq_page(a.s, b, key >> a.p.shift, a.p.n_pages, a.status);
         if (o.id >= 0) {
           const long long blk = (long long)o.id * heads + h;

@@ -46,6 +46,7 @@ namespace {
 constexpr int kDecWarps = 8;       // per CTA, one CTA per SM
 constexpr int kUnit = 32;          // keys per unit
 constexpr int kMinUnits = 2;       // per warp, when the work is small
+constexpr int kItemUnits = 32;     // of an item at most, for a CTA of its own
 constexpr int kScan = kDecWarps * 32;
 
 template <int D>
@@ -118,13 +119,380 @@ __device__ __forceinline__ void lds64(uint32_t (&w)[2], uint32_t addr) {
 // even, then all odd j)
 __device__ __forceinline__ int key_row(int j) { return (j & 6) ^ ((j & 1) * 5); }
 
+// A warp's ring of stages and where it stands.
+struct Ring {
+  uint32_t data, bars;
+  int stage;
+  uint32_t phase;
+};
+
+// One segment: units [i0, i0 + seg) of (b, h), by one warp.  o, m, l: for the
+// rows nt * 8 + 2 t + c (c = 0, 1) the channels CH g .. of sum p v (channel
+// 2 k + i in o[nt][k][c + 2 i]), the base in units of log 2 and sum p.  False
+// when a wait ran out.
+template <int D, int NT>
+__device__ __forceinline__ bool decode_segment(const PagedAttnArgs& a, const CUtensorMap& map_k,
+                                               const CUtensorMap& map_v, Ring& rg, int b, int h,
+                                               const SeqWork& w, int i0, int seg,
+                                               float (&o)[NT][D / 16][4], float (&m)[NT][2],
+                                               float (&l)[NT][2]) {
+  using C = DecCfg<D>;
+  constexpr int KC = D / 64;       // 16-byte chunks of a key row per lane
+  constexpr int MT = D / 16;       // channel tiles of the output
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, heads = a.p.heads;
+  const float scale_log2 = a.scale * 1.4426950408889634f;
+  const uint32_t ring = rg.data, bars = rg.bars;
+  int& stage = rg.stage;
+  uint32_t& phase = rg.phase;
+  const int rows = w.n * a.group;
+  const int key_first = w.lo + i0 * kUnit;
+  const int key_end = min(w.len, w.lo + (i0 + seg) * kUnit);
+  const int t0 = w.len - w.n;
+  // pages, 32 at a time, one per lane: id (-1: none), exponents of K and V
+  const int shift = a.p.shift;
+  const int page_end = (max(key_end, key_first) + a.p.page - 1) >> shift;
+  int pbase = key_first >> shift;
+  auto page_info = [&](int base, int& id, int& ek, int& ev) {
+    id = -1;
+    ek = ev = 0;
+    // (a page wholly before every row's window may be gone already)
+    if (base + lane < page_end && ((long long)(base + lane + 1) << shift) > w.seen) {
+      id = seq_page(a.s, b, base + lane, a.p.n_pages, a.status);
+      if (id >= 0) {
+        const long long blk = (long long)id * heads + h;
+        ek = scale_exp(__ldg(a.p.scale[0] + blk));
+        ev = scale_exp(__ldg(a.p.scale[1] + blk));
+      }
+    }
+  };
+  int id0, ek0, ev0, id1, ek1, ev1;
+  page_info(pbase, id0, ek0, ev0);
+  page_info(pbase + 32, id1, ek1, ev1);
+  auto pick = [&](int v0, int v1, int pg) {
+    const int r = pg - pbase;
+    const int x = __shfl_sync(0xffffffffu, v0, r & 31), y = __shfl_sync(0xffffffffu, v1, r & 31);
+    return r < 32 ? x : y;
+  };
+  // copy unit i of the segment into stage st (all lanes; lane 0 issues)
+  auto fetch = [&](int i, int st) {
+    const int key0 = key_first + i * kUnit;
+    const uint32_t dst = ring + (uint32_t)(st * C::kStage), bar = bars + 8u * st;
+    const int pg = key0 >> shift;
+    const int ida = pick(id0, id1, pg);
+    const bool two = shift == 4;
+    const int idb = two ? pick(id0, id1, pg + 1) : -1;
+    if (lane == 0) {
+      const int box = two ? 16 : 32;
+      const bool la = ida >= 0 && key0 < key_end, lb = idb >= 0 && key0 + 16 < key_end;
+      const uint32_t bytes = (uint32_t)(2 * box * D) * ((la ? 1u : 0u) + (lb ? 1u : 0u));
+      if (bytes == 0) {
+        ptx::mbar_arrive(bar);
+      } else {
+        ptx::mbar_expect_tx(bar, bytes);
+        const int in = key0 & (a.p.page - 1);
+        if (la) {
+          ptx::tma_load_3d(dst, &map_k, 0, in, ida * heads + h, bar);
+          ptx::tma_load_3d(dst + C::kHalf, &map_v, 0, in, ida * heads + h, bar);
+        }
+        if (lb) {
+          ptx::tma_load_3d(dst + 16 * D, &map_k, 0, 0, idb * heads + h, bar);
+          ptx::tma_load_3d(dst + C::kHalf + 16 * D, &map_v, 0, 0, idb * heads + h, bar);
+        }
+      }
+    }
+  };
+  const int ahead = min(seg, C::kStages);
+  for (int i = 0; i < ahead; ++i) fetch(i, (stage + i) % C::kStages);
+
+  // ---- query rows as B fragments, scaled to FP16 ----
+  uint32_t qf[NT][KC * 4][2];
+  float cq[NT][2];
+  int lo_r[NT][2], hi_r[NT][2];   // keys each column's row attends to
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = nt * 8 + g;
+    uint2 raw[KC * 4];
+#pragma unroll
+    for (int k = 0; k < KC * 4; ++k) raw[k] = make_uint2(0u, 0u);
+    if (r < rows) {
+      const int i = r / a.group, hq = h * a.group + r % a.group;
+      const uint16_t* qp = a.q + (long long)(w.r0 + i) * a.q_row_stride + (long long)hq * a.q_head_stride;
+#pragma unroll
+      for (int k = 0; k < KC; ++k) {
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const uint4 x = __ldg(reinterpret_cast<const uint4*>(qp + 16 * (t + 4 * k)) + v);
+          raw[4 * k + 2 * v] = make_uint2(x.x, x.y);
+          raw[4 * k + 2 * v + 1] = make_uint2(x.z, x.w);
+        }
+      }
+    }
+    uint32_t mx = 0;   // largest magnitude, as its bits
+#pragma unroll
+    for (int k = 0; k < KC * 4; ++k) {
+      mx = max(mx, max(max((raw[k].x & 0x7fffu), (raw[k].x >> 16) & 0x7fffu),
+                       max((raw[k].y & 0x7fffu), (raw[k].y >> 16) & 0x7fffu)));
+    }
+    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    // the maximum's exponent becomes 14 (a subnormal maximum's at most)
+    const int e = max((int)(mx >> 7), 1) - 127 - 14;
+    // x * 2^-e in two steps, each factor a normal number
+    const float f0 = pow2f(-(e / 2)), f1 = pow2f(-(e - e / 2));
+#pragma unroll
+    for (int k = 0; k < KC * 4; ++k) {
+      qf[nt][k][0] = ptx::f16x2_rn(__uint_as_float(raw[k].x << 16) * f0 * f1,
+                                   __uint_as_float(raw[k].x & 0xffff0000u) * f0 * f1);
+      qf[nt][k][1] = ptx::f16x2_rn(__uint_as_float(raw[k].y << 16) * f0 * f1,
+                                   __uint_as_float(raw[k].y & 0xffff0000u) * f0 * f1);
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      // column 2t + c is the row whose lanes have g = 2t + c
+      const int ec = __shfl_sync(0xffffffffu, e, (2 * t + c) * 4);
+      cq[nt][c] = scale_log2 * pow2f(ec / 2) * pow2f(ec - ec / 2);
+      const int rc = nt * 8 + 2 * t + c;
+      const int tq = t0 + rc / a.group;
+      hi_r[nt][c] = rc < rows ? (a.causal ? min(w.len, tq + 1) : w.len) : 0;
+      lo_r[nt][c] = a.window > 0 ? max(0, tq - a.window + 1) : 0;
+    }
+  }
+  // keys every row attends to
+  const int all_lo = a.window > 0 ? max(0, w.len - a.window) : 0;
+  const int all_hi = a.causal ? min(w.len, t0 + 1) : w.len;
+
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o[nt][i][c] = 0.f;
+    m[nt][0] = m[nt][1] = -CUDART_INF_F;
+    l[nt][0] = l[nt][1] = 0.f;
+  }
+  int eref = -1000;   // exponent O is held against (the largest V scale so far)
+  bool ok = true;
+
+  for (int i = 0; i < seg; ++i) {
+    const int key0 = key_first + i * kUnit;
+    ok = page_wait(bars + 8u * stage, phase, a.wait_limit_ns, nullptr, a.status);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    if ((key0 >> shift) - pbase >= 32) {
+      pbase += 32;
+      id0 = id1, ek0 = ek1, ev0 = ev1;
+      page_info(pbase + 32, id1, ek1, ev1);
+    }
+    const uint32_t kb = ring + (uint32_t)(stage * C::kStage), vb = kb + C::kHalf;
+    // one key per 16-row tile decides its page: tiles never straddle pages
+    int idt[2], ekt[2], evt[2];
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+      const int pg = (key0 + 16 * mt) >> shift;
+      idt[mt] = pick(id0, id1, pg);
+      ekt[mt] = pick(ek0, ek1, pg);
+      evt[mt] = pick(ev0, ev1, pg);
+    }
+    const bool whole = key0 >= all_lo && key0 + kUnit <= all_hi && idt[0] >= 0 && idt[1] >= 0;
+
+    // ---- S^T = K Q^T ----
+    float s[2][NT][4];
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[mt][nt][c] = 0.f;
+      const int ra = 16 * mt + key_row(g);
+#pragma unroll
+      for (int k = 0; k < KC; ++k) {
+        uint32_t x[4], y[4];
+        uint32_t off;
+        if (D == 128) off = (uint32_t)(ra * 128 + (((t + 4 * k) ^ (ra & 7)) << 4));
+        else off = (uint32_t)(ra * 64 + ((t ^ ((ra >> 1) & 3)) << 4));
+        lds128(x, kb + off);
+        lds128(y, kb + off + 8 * D);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const uint32_t a0 = lo_f16(x[v]), a1 = lo_f16(y[v]), a2 = hi_f16(x[v]), a3 = hi_f16(y[v]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816(s[mt][nt], a0, a1, a2, a3, qf[nt][4 * k + v][0], qf[nt][4 * k + v][1]);
+        }
+      }
+    }
+    // ---- softmax ----
+    float mx[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) mx[nt][0] = mx[nt][1] = -CUDART_INF_F;
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+      const float fk = pow2f(ekt[mt]);
+      const int ka = key0 + 16 * mt + key_row(g);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float v = s[mt][nt][c] * (cq[nt][c & 1] * fk);
+          if (!whole) {
+            const int key = ka + 8 * (c >> 1);
+            const bool see = key >= lo_r[nt][c & 1] && key < hi_r[nt][c & 1] && idt[mt] >= 0;
+            v = see ? v : -CUDART_INF_F;
+          }
+          s[mt][nt][c] = v;
+          mx[nt][c & 1] = fmaxf(mx[nt][c & 1], v);
+        }
+    }
+    bool grows = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) mx[nt][c] = fmaxf(mx[nt][c], __shfl_xor_sync(0xffffffffu, mx[nt][c], x));
+        grows |= mx[nt][c] > m[nt][c];
+      }
+    const int etop = max(idt[0] >= 0 ? evt[0] : -1000, idt[1] >= 0 ? evt[1] : -1000);
+    if (__any_sync(0xffffffffu, grows || etop > eref)) {
+      const int enew = max(eref, etop);
+      const float fe = eref > -1000 ? pow2f(max(eref - enew, -126)) : 0.f;
+      eref = enew;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float f[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float mn = fmaxf(m[nt][c], mx[nt][c]);
+          f[c] = mn > -CUDART_INF_F ? ptx::ex2_approx(m[nt][c] - mn) : 1.f;
+          m[nt][c] = mn;
+          l[nt][c] *= f[c];
+          f[c] *= fe;
+        }
+#pragma unroll
+        for (int k = 0; k < MT; ++k)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[nt][k][c] *= f[c & 1];
+      }
+    }
+    // ---- weights: P^T as B fragments ----
+    uint32_t pf[2][NT][2];
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+      // 2^15 times the V scale relative to the reference; far smaller
+      // scales stop at 2^-45, where FP16 has dropped the weight already
+      const int sh = 15 + min(max(evt[mt] - eref, -60), 0);
+      const float fs = (float)sh, inv = pow2f(-sh);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float e[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float mc = m[nt][c & 1];
+          e[c] = ptx::ex2_approx(s[mt][nt][c] - (mc > -CUDART_INF_F ? mc : 0.f) + fs);
+        }
+        l[nt][0] = fmaf(e[0] + e[2], inv, l[nt][0]);
+        l[nt][1] = fmaf(e[1] + e[3], inv, l[nt][1]);
+        pf[mt][nt][0] = transpose8x8(ptx::f16x2_rn(e[0], e[1]));
+        pf[mt][nt][1] = transpose8x8(ptx::f16x2_rn(e[2], e[3]));
+      }
+    }
+    // ---- O^T += V^T P^T ----
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+      // rows of fragment columns 2t, 2t + 1, 2t + 8, 2t + 9
+      const int rv[2] = {key_row(2 * t), key_row(2 * t + 1)};
+      uint32_t x[4][D / 32];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = 16 * mt + rv[j & 1] + 8 * (j >> 1);
+        if constexpr (D == 128) lds128(x[j], vb + (uint32_t)(r * 128 + ((g ^ (r & 7)) << 4)));
+        else lds64(x[j], vb + (uint32_t)(r * 64 + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8));
+        if (!whole) {
+          // what no row of the sequence may see must not reach the product
+          // (a zero weight times a NaN)
+          const int key = key0 + r;
+          const bool use = key >= w.seen && key < w.len && idt[mt] >= 0;
+#pragma unroll
+          for (int v = 0; v < D / 32; ++v) x[j][v] = use ? x[j][v] : 0u;
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < D / 32; ++v) {
+        const uint32_t ab0 = __byte_perm(x[0][v], x[1][v], 0x5140), ab1 = __byte_perm(x[0][v], x[1][v], 0x7362);
+        const uint32_t cd0 = __byte_perm(x[2][v], x[3][v], 0x5140), cd1 = __byte_perm(x[2][v], x[3][v], 0x7362);
+        const uint32_t f0 = lo_f16(ab0), f1 = hi_f16(ab0), f2 = lo_f16(cd0), f3 = hi_f16(cd0);
+        const uint32_t e0 = lo_f16(ab1), e1 = hi_f16(ab1), e2 = lo_f16(cd1), e3 = hi_f16(cd1);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma16816(o[nt][2 * v], f0, f1, f2, f3, pf[mt][nt][0], pf[mt][nt][1]);
+          mma16816(o[nt][2 * v + 1], e0, e1, e2, e3, pf[mt][nt][0], pf[mt][nt][1]);
+        }
+      }
+    }
+    __syncwarp();
+    if (i + ahead < seg) fetch(i + ahead, stage);
+    if (++stage == C::kStages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+  if (!ok) {
+    // copies in flight still write this warp's stages: wait for them
+    // (bounded) before it exits
+    for (int i = 0; i < C::kStages; ++i) {
+      page_drain(bars + 8u * stage, phase, a.wait_limit_ns);
+      if (++stage == C::kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+      if (i + 1 >= ahead) break;
+    }
+    return false;
+  }
+  // O in original units, the sums over the keys' lanes
+  const float fo = eref > -1000 ? pow2f(eref) * pow2f(-15) : 0.f;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);
+#pragma unroll
+      for (int k = 0; k < MT; ++k) {
+        o[nt][k][c] *= fo;
+        o[nt][k][c + 2] *= fo;
+      }
+    }
+  return true;
+}
+
+// Row r of the head's rows, from the lane's share (lanes g hold channels
+// CH g .., n = nt, c the row's place): BF16 out and lse.
+template <int D, int NT>
+__device__ __forceinline__ void store_row(const PagedAttnArgs& a, const SeqWork& w, int h, int r,
+                                          const float (&o)[NT][D / 16][4], int nt, int c, float m, float l) {
+  constexpr int CH = D / 8;
+  const int g = (threadIdx.x & 31) >> 2;
+  const long long row = (long long)(w.r0 + r / a.group) * a.q_heads + h * a.group + r % a.group;
+  if (!KVQ_IN_BOUNDS(row, (long long)a.s.rows * a.q_heads, a.status, a.bounds_site)) return;
+  const float f = l > 0.f ? 1.f / l : 0.f;
+  uint32_t v[CH / 2];
+#pragma unroll
+  for (int k = 0; k < CH / 2; ++k) {
+    const __nv_bfloat162 z = __floats2bfloat162_rn(o[nt][k][c] * f, o[nt][k][c + 2] * f);
+    v[k] = *reinterpret_cast<const uint32_t*>(&z);
+  }
+  uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + CH * g);
+#pragma unroll
+  for (int k = 0; k < CH / 8; ++k) dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+  if (g == 0 && a.lse != nullptr) a.lse[row] = l > 0.f ? 0.6931471805599453f * (m + log2f(l)) : -CUDART_INF_F;
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kDecWarps * 32, 1)
     decode_kernel(const __grid_constant__ DecodeArgs p, const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v) {
   using C = DecCfg<D>;
-  constexpr int KC = D / 64;       // 16-byte chunks of a key row per lane
-  constexpr int MT = D / 16;       // channel tiles of the output
   constexpr int CH = D / 8;        // output channels per lane
   extern __shared__ uint8_t smem_raw[];
   __shared__ long long scan_warp[kDecWarps];
@@ -202,10 +570,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
     }
   }
 
-  const float scale_log2 = a.scale * 1.4426950408889634f;
-  int stage = 0;
-  uint32_t phase = 0;
-  bool ok = true;
+  Ring rg{ring, bars, 0, 0u};
   SeqWork w{};
   if (u0 < u1) w = seq_work(a, b);
   int h = 0, i0 = 0;
@@ -213,351 +578,29 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
     h = (int)((u0 - at) / w.units);
     i0 = (int)((u0 - at) % w.units);
   }
-  for (long long u = u0; u < u1 && ok;) {
+  for (long long u = u0; u < u1;) {
     const int seg = (int)min((long long)(w.units - i0), u1 - u);
-    // ---- one segment: units [i0, i0 + seg) of (b, h) ----
+    float o[NT][D / 16][4], m[NT][2], l[NT][2];
+    if (!decode_segment<D, NT>(a, map_k, map_v, rg, b, h, w, i0, seg, o, m, l)) break;
+    // ---- its result: the item's, or a part of it ----
     const int rows = w.n * a.group;
-    const int key_first = w.lo + i0 * kUnit;
-    const int key_end = min(w.len, w.lo + (i0 + seg) * kUnit);
-    const int t0 = w.len - w.n;
-    // pages, 32 at a time, one per lane: id (-1: none), exponents of K and V
-    const int shift = a.p.shift;
-    const int page_end = (max(key_end, key_first) + a.p.page - 1) >> shift;
-    int pbase = key_first >> shift;
-    auto page_info = [&](int base, int& id, int& ek, int& ev) {
-      id = -1;
-      ek = ev = 0;
-      // (a page wholly before every row's window may be gone already)
-      if (base + lane < page_end && (base + lane + 1) << shift > w.seen) {
-        id = seq_page(a.s, b, base + lane, a.p.n_pages, a.status);
-        if (id >= 0) {
-          const long long blk = (long long)id * heads + h;
-          ek = scale_exp(__ldg(a.p.scale[0] + blk));
-          ev = scale_exp(__ldg(a.p.scale[1] + blk));
-        }
-      }
-    };
-    int id0, ek0, ev0, id1, ek1, ev1;
-    page_info(pbase, id0, ek0, ev0);
-    page_info(pbase + 32, id1, ek1, ev1);
-    auto pick = [&](int v0, int v1, int pg) {
-      const int r = pg - pbase;
-      const int x = __shfl_sync(0xffffffffu, v0, r & 31), y = __shfl_sync(0xffffffffu, v1, r & 31);
-      return r < 32 ? x : y;
-    };
-    // copy unit i of the segment into stage st (all lanes; lane 0 issues)
-    auto fetch = [&](int i, int st) {
-      const int key0 = key_first + i * kUnit;
-      const uint32_t dst = ring + (uint32_t)(st * C::kStage), bar = bars + 8u * st;
-      const int pg = key0 >> shift;
-      const int ida = pick(id0, id1, pg);
-      const bool two = shift == 4;
-      const int idb = two ? pick(id0, id1, pg + 1) : -1;
-      if (lane == 0) {
-        const int box = two ? 16 : 32;
-        const bool la = ida >= 0 && key0 < key_end, lb = idb >= 0 && key0 + 16 < key_end;
-        const uint32_t bytes = (uint32_t)(2 * box * D) * ((la ? 1u : 0u) + (lb ? 1u : 0u));
-        if (bytes == 0) {
-          ptx::mbar_arrive(bar);
-        } else {
-          ptx::mbar_expect_tx(bar, bytes);
-          const int in = key0 & (a.p.page - 1);
-          if (la) {
-            ptx::tma_load_3d(dst, &map_k, 0, in, ida * heads + h, bar);
-            ptx::tma_load_3d(dst + C::kHalf, &map_v, 0, in, ida * heads + h, bar);
-          }
-          if (lb) {
-            ptx::tma_load_3d(dst + 16 * D, &map_k, 0, 0, idb * heads + h, bar);
-            ptx::tma_load_3d(dst + C::kHalf + 16 * D, &map_v, 0, 0, idb * heads + h, bar);
-          }
-        }
-      }
-    };
-    const int ahead = min(seg, C::kStages);
-    for (int i = 0; i < ahead; ++i) fetch(i, (stage + i) % C::kStages);
-
-    // ---- query rows as B fragments, scaled to FP16 ----
-    uint32_t qf[NT][KC * 4][2];
-    float cq[NT][2];
-    int lo_r[NT][2], hi_r[NT][2];   // keys each column's row attends to
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = nt * 8 + g;
-      uint2 raw[KC * 4];
-#pragma unroll
-      for (int k = 0; k < KC * 4; ++k) raw[k] = make_uint2(0u, 0u);
-      if (r < rows) {
-        const int i = r / a.group, hq = h * a.group + r % a.group;
-        const uint16_t* qp = a.q + (long long)(w.r0 + i) * a.q_row_stride + (long long)hq * a.q_head_stride;
-#pragma unroll
-        for (int k = 0; k < KC; ++k) {
-#pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            const uint4 x = __ldg(reinterpret_cast<const uint4*>(qp + 16 * (t + 4 * k)) + v);
-            raw[4 * k + 2 * v] = make_uint2(x.x, x.y);
-            raw[4 * k + 2 * v + 1] = make_uint2(x.z, x.w);
-          }
-        }
-      }
-      uint32_t mx = 0;   // largest magnitude, as its bits
-#pragma unroll
-      for (int k = 0; k < KC * 4; ++k) {
-        mx = max(mx, max(max((raw[k].x & 0x7fffu), (raw[k].x >> 16) & 0x7fffu),
-                         max((raw[k].y & 0x7fffu), (raw[k].y >> 16) & 0x7fffu)));
-      }
-      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      // the maximum's exponent becomes 14 (a subnormal maximum's at most)
-      const int e = max((int)(mx >> 7), 1) - 127 - 14;
-      // x * 2^-e in two steps, each factor a normal number
-      const float f0 = pow2f(-(e / 2)), f1 = pow2f(-(e - e / 2));
-#pragma unroll
-      for (int k = 0; k < KC * 4; ++k) {
-        qf[nt][k][0] = ptx::f16x2_rn(__uint_as_float(raw[k].x << 16) * f0 * f1,
-                                     __uint_as_float(raw[k].x & 0xffff0000u) * f0 * f1);
-        qf[nt][k][1] = ptx::f16x2_rn(__uint_as_float(raw[k].y << 16) * f0 * f1,
-                                     __uint_as_float(raw[k].y & 0xffff0000u) * f0 * f1);
-      }
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        // column 2t + c is the row whose lanes have g = 2t + c
-        const int ec = __shfl_sync(0xffffffffu, e, (2 * t + c) * 4);
-        cq[nt][c] = scale_log2 * pow2f(ec / 2) * pow2f(ec - ec / 2);
-        const int rc = nt * 8 + 2 * t + c;
-        const int tq = t0 + rc / a.group;
-        hi_r[nt][c] = rc < rows ? (a.causal ? min(w.len, tq + 1) : w.len) : 0;
-        lo_r[nt][c] = a.window > 0 ? max(0, tq - a.window + 1) : 0;
-      }
-    }
-    // keys every row attends to
-    const int all_lo = a.window > 0 ? max(0, w.len - a.window) : 0;
-    const int all_hi = a.causal ? min(w.len, t0 + 1) : w.len;
-
-    float o[NT][MT][4], m[NT][2], l[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) o[nt][i][c] = 0.f;
-      m[nt][0] = m[nt][1] = -CUDART_INF_F;
-      l[nt][0] = l[nt][1] = 0.f;
-    }
-    int eref = -1000;   // exponent O is held against (the largest V scale so far)
-
-    for (int i = 0; i < seg; ++i) {
-      const int key0 = key_first + i * kUnit;
-      ok = page_wait(bars + 8u * stage, phase, a.wait_limit_ns, nullptr, a.status);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      if ((key0 >> shift) - pbase >= 32) {
-        pbase += 32;
-        id0 = id1, ek0 = ek1, ev0 = ev1;
-        page_info(pbase + 32, id1, ek1, ev1);
-      }
-      const uint32_t kb = ring + (uint32_t)(stage * C::kStage), vb = kb + C::kHalf;
-      // one key per 16-row tile decides its page: tiles never straddle pages
-      int idt[2], ekt[2], evt[2];
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        const int pg = (key0 + 16 * mt) >> shift;
-        idt[mt] = pick(id0, id1, pg);
-        ekt[mt] = pick(ek0, ek1, pg);
-        evt[mt] = pick(ev0, ev1, pg);
-      }
-      const bool whole = key0 >= all_lo && key0 + kUnit <= all_hi && idt[0] >= 0 && idt[1] >= 0;
-
-      // ---- S^T = K Q^T ----
-      float s[2][NT][4];
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) s[mt][nt][c] = 0.f;
-        const int ra = 16 * mt + key_row(g);
-#pragma unroll
-        for (int k = 0; k < KC; ++k) {
-          uint32_t x[4], y[4];
-          uint32_t off;
-          if (D == 128) off = (uint32_t)(ra * 128 + (((t + 4 * k) ^ (ra & 7)) << 4));
-          else off = (uint32_t)(ra * 64 + ((t ^ ((ra >> 1) & 3)) << 4));
-          lds128(x, kb + off);
-          lds128(y, kb + off + 8 * D);
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const uint32_t a0 = lo_f16(x[v]), a1 = lo_f16(y[v]), a2 = hi_f16(x[v]), a3 = hi_f16(y[v]);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma16816(s[mt][nt], a0, a1, a2, a3, qf[nt][4 * k + v][0], qf[nt][4 * k + v][1]);
-          }
-        }
-      }
-      // ---- softmax ----
-      float mx[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) mx[nt][0] = mx[nt][1] = -CUDART_INF_F;
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        const float fk = pow2f(ekt[mt]);
-        const int ka = key0 + 16 * mt + key_row(g);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float v = s[mt][nt][c] * (cq[nt][c & 1] * fk);
-            if (!whole) {
-              const int key = ka + 8 * (c >> 1);
-              const bool see = key >= lo_r[nt][c & 1] && key < hi_r[nt][c & 1] && idt[mt] >= 0;
-              v = see ? v : -CUDART_INF_F;
-            }
-            s[mt][nt][c] = v;
-            mx[nt][c & 1] = fmaxf(mx[nt][c & 1], v);
-          }
-      }
-      bool grows = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-#pragma unroll
-          for (int x = 4; x < 32; x <<= 1) mx[nt][c] = fmaxf(mx[nt][c], __shfl_xor_sync(0xffffffffu, mx[nt][c], x));
-          grows |= mx[nt][c] > m[nt][c];
-        }
-      const int etop = max(idt[0] >= 0 ? evt[0] : -1000, idt[1] >= 0 ? evt[1] : -1000);
-      if (__any_sync(0xffffffffu, grows || etop > eref)) {
-        const int enew = max(eref, etop);
-        const float fe = eref > -1000 ? pow2f(max(eref - enew, -126)) : 0.f;
-        eref = enew;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float f[2];
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const float mn = fmaxf(m[nt][c], mx[nt][c]);
-            f[c] = mn > -CUDART_INF_F ? ptx::ex2_approx(m[nt][c] - mn) : 1.f;
-            m[nt][c] = mn;
-            l[nt][c] *= f[c];
-            f[c] *= fe;
-          }
-#pragma unroll
-          for (int k = 0; k < MT; ++k)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) o[nt][k][c] *= f[c & 1];
-        }
-      }
-      // ---- weights: P^T as B fragments ----
-      uint32_t pf[2][NT][2];
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        // 2^15 times the V scale relative to the reference; far smaller
-        // scales stop at 2^-45, where FP16 has dropped the weight already
-        const int sh = 15 + min(max(evt[mt] - eref, -60), 0);
-        const float fs = (float)sh, inv = pow2f(-sh);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float e[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float mc = m[nt][c & 1];
-            e[c] = ptx::ex2_approx(s[mt][nt][c] - (mc > -CUDART_INF_F ? mc : 0.f) + fs);
-          }
-          l[nt][0] = fmaf(e[0] + e[2], inv, l[nt][0]);
-          l[nt][1] = fmaf(e[1] + e[3], inv, l[nt][1]);
-          pf[mt][nt][0] = transpose8x8(ptx::f16x2_rn(e[0], e[1]));
-          pf[mt][nt][1] = transpose8x8(ptx::f16x2_rn(e[2], e[3]));
-        }
-      }
-      // ---- O^T += V^T P^T ----
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        // rows of fragment columns 2t, 2t + 1, 2t + 8, 2t + 9
-        const int rv[2] = {key_row(2 * t), key_row(2 * t + 1)};
-        uint32_t x[4][D / 32];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = 16 * mt + rv[j & 1] + 8 * (j >> 1);
-          if constexpr (D == 128) lds128(x[j], vb + (uint32_t)(r * 128 + ((g ^ (r & 7)) << 4)));
-          else lds64(x[j], vb + (uint32_t)(r * 64 + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8));
-          if (!whole) {
-            // what no row of the sequence may see must not reach the product
-            // (a zero weight times a NaN)
-            const int key = key0 + r;
-            const bool use = key >= w.seen && key < w.len && idt[mt] >= 0;
-#pragma unroll
-            for (int v = 0; v < D / 32; ++v) x[j][v] = use ? x[j][v] : 0u;
-          }
-        }
-#pragma unroll
-        for (int v = 0; v < D / 32; ++v) {
-          const uint32_t ab0 = __byte_perm(x[0][v], x[1][v], 0x5140), ab1 = __byte_perm(x[0][v], x[1][v], 0x7362);
-          const uint32_t cd0 = __byte_perm(x[2][v], x[3][v], 0x5140), cd1 = __byte_perm(x[2][v], x[3][v], 0x7362);
-          const uint32_t f0 = lo_f16(ab0), f1 = hi_f16(ab0), f2 = lo_f16(cd0), f3 = hi_f16(cd0);
-          const uint32_t e0 = lo_f16(ab1), e1 = hi_f16(ab1), e2 = lo_f16(cd1), e3 = hi_f16(cd1);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma16816(o[nt][2 * v], f0, f1, f2, f3, pf[mt][nt][0], pf[mt][nt][1]);
-            mma16816(o[nt][2 * v + 1], e0, e1, e2, e3, pf[mt][nt][0], pf[mt][nt][1]);
-          }
-        }
-      }
-      __syncwarp();
-      if (i + ahead < seg) fetch(i + ahead, stage);
-      if (++stage == C::kStages) {
-        stage = 0;
-        phase ^= 1u;
-      }
-    }
-    if (!ok) {
-      // copies in flight still write this warp's stages: wait for them
-      // (bounded) before it exits
-      for (int i = 0; i < C::kStages; ++i) {
-        page_drain(bars + 8u * stage, phase, a.wait_limit_ns);
-        if (++stage == C::kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
-        if (i + 1 >= ahead) break;
-      }
-      break;
-    }
-    // ---- this segment's result ----
     const bool complete = seg == w.units;
     const long long slot = 2LL * gw + (u == u0 ? 0 : 1);
-    const float fo = eref > -1000 ? pow2f(eref) * pow2f(-15) : 0.f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float ls = l[nt][c];
-#pragma unroll
-        for (int x = 4; x < 32; x <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, x);
         const int r = nt * 8 + 2 * t + c;
         if (r >= rows) continue;
         if (complete) {
-          const long long row = (long long)(w.r0 + r / a.group) * a.q_heads + h * a.group + r % a.group;
-          const float f = ls > 0.f ? fo / ls : 0.f;
-          if (KVQ_IN_BOUNDS(row, (long long)a.s.rows * a.q_heads, a.status, a.bounds_site)) {
-            uint32_t v[CH / 2];
-#pragma unroll
-            for (int k = 0; k < CH / 2; ++k) {
-              const __nv_bfloat162 z = __floats2bfloat162_rn(o[nt][k][c] * f, o[nt][k][c + 2] * f);
-              v[k] = *reinterpret_cast<const uint32_t*>(&z);
-            }
-            uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + CH * g);
-#pragma unroll
-            for (int k = 0; k < CH / 8; ++k) dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-            if (g == 0 && a.lse != nullptr)
-              a.lse[row] = ls > 0.f ? 0.6931471805599453f * (m[nt][c] + log2f(ls)) : -CUDART_INF_F;
-          }
+          store_row<D, NT>(a, w, h, r, o, nt, c, m[nt][c], l[nt][c]);
         } else {
           float4* dst = reinterpret_cast<float4*>(p.part_o + (slot * p.rows_cap + r) * D + CH * g);
 #pragma unroll
           for (int k = 0; k < CH / 4; ++k)
-            dst[k] = make_float4(o[nt][2 * k][c] * fo, o[nt][2 * k][c + 2] * fo,
-                                 o[nt][2 * k + 1][c] * fo, o[nt][2 * k + 1][c + 2] * fo);
+            dst[k] = make_float4(o[nt][2 * k][c], o[nt][2 * k][c + 2], o[nt][2 * k + 1][c], o[nt][2 * k + 1][c + 2]);
           if (g == 0)
-            *reinterpret_cast<float2*>(p.part_ml + (slot * p.rows_cap + r) * 2) = make_float2(m[nt][c], ls);
+            *reinterpret_cast<float2*>(p.part_ml + (slot * p.rows_cap + r) * 2) = make_float2(m[nt][c], l[nt][c]);
         }
       }
     // ---- the next segment ----
@@ -571,6 +614,100 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
       } while (w.units == 0 && b + 1 < a.s.batch);
       if (w.units == 0) break;   // not with lengths that hold still during the call
     }
+  }
+}
+
+// Short sequences: a CTA per item, the item's units divided among its warps and
+// joined in shared memory.  No scan of the batch, no workspace, one launch:
+// what counts there is the latency of one pass.
+template <int D, int NT>
+__global__ void __launch_bounds__(kDecWarps * 32, 1)
+    decode_item_kernel(const __grid_constant__ DecodeArgs p, const __grid_constant__ CUtensorMap map_k,
+                       const __grid_constant__ CUtensorMap map_v) {
+  using C = DecCfg<D>;
+  constexpr int CH = D / 8;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ float2 ml_s[kDecWarps][NT * 8];
+  const PagedAttnArgs& a = p.a;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  Ring rg{ptx::smem_u32(smem) + (uint32_t)(wid * C::kStages * C::kStage),
+          ptx::smem_u32(smem) + (uint32_t)(C::kBar + wid * C::kStages * 8), 0, 0u};
+  if (lane == 0) {
+    for (int i = 0; i < C::kStages; ++i) ptx::mbar_init(rg.bars + 8 * i, 1);
+    ptx::fence_mbar_init();
+  }
+  __syncwarp();
+  ptx::grid_dependency_wait();
+  const int b = (int)(blockIdx.x / (unsigned)a.p.heads), h = (int)(blockIdx.x % (unsigned)a.p.heads);
+  const SeqWork w = seq_work(a, b);
+  if (w.units == 0) return;
+  const int i0 = w.units * wid / kDecWarps, i1 = w.units * (wid + 1) / kDecWarps;
+  float o[NT][D / 16][4], m[NT][2], l[NT][2];
+  bool ok = true;
+  if (i1 > i0) {
+    ok = decode_segment<D, NT>(a, map_k, map_v, rg, b, h, w, i0, i1 - i0, o, m, l);
+  } else {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        m[nt][c] = -CUDART_INF_F;
+        l[nt][c] = 0.f;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) o[nt][k][c] = o[nt][k][c + 2] = 0.f;
+      }
+  }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      if (g == 0) ml_s[wid][nt * 8 + 2 * t + c] = make_float2(m[nt][c], l[nt][c]);
+  // no copy of any warp is in flight once all are here: the rings are free
+  if (__syncthreads_or(!ok)) return;
+  const int rows = w.n * a.group;
+  float* part = reinterpret_cast<float*>(smem);   // [warp][row][D]
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int r = nt * 8 + 2 * t + c;
+      if (r >= rows || i1 <= i0) continue;
+      float4* dst = reinterpret_cast<float4*>(part + (wid * NT * 8 + r) * D + CH * g);
+#pragma unroll
+      for (int k = 0; k < CH / 4; ++k)
+        dst[k] = make_float4(o[nt][2 * k][c], o[nt][2 * k][c + 2], o[nt][2 * k + 1][c], o[nt][2 * k + 1][c + 2]);
+    }
+  __syncthreads();
+  // a warp per row, the parts in order
+  for (int r = wid; r < rows; r += kDecWarps) {
+    float top = -CUDART_INF_F;
+#pragma unroll
+    for (int k = 0; k < kDecWarps; ++k) top = fmaxf(top, ml_s[k][r].x);
+    const float base = top > -CUDART_INF_F ? top : 0.f;
+    float ls = 0.f, v[D / 32];
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) v[c] = 0.f;
+#pragma unroll
+    for (int k = 0; k < kDecWarps; ++k) {
+      if (w.units * (k + 1) / kDecWarps <= w.units * k / kDecWarps) continue;   // a warp without units
+      const float2 ml = ml_s[k][r];
+      const float f = ptx::ex2_approx(ml.x - base);
+      ls = fmaf(ml.y, f, ls);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) v[c] = fmaf(part[(k * NT * 8 + r) * D + (D / 32) * lane + c], f, v[c]);
+    }
+    const long long row = (long long)(w.r0 + r / a.group) * a.q_heads + h * a.group + r % a.group;
+    if (!KVQ_IN_BOUNDS(row, (long long)a.s.rows * a.q_heads, a.status, a.bounds_site)) continue;
+    const float f = ls > 0.f ? 1.f / ls : 0.f;
+#pragma unroll
+    for (int c = 0; c < D / 32; c += 2) {
+      const __nv_bfloat162 z = __floats2bfloat162_rn(v[c] * f, v[c + 1] * f);
+      *reinterpret_cast<uint32_t*>(a.out + row * D + (D / 32) * lane + c) = *reinterpret_cast<const uint32_t*>(&z);
+    }
+    if (lane == 0 && a.lse != nullptr)
+      a.lse[row] = ls > 0.f ? 0.6931471805599453f * (top + log2f(ls)) : -CUDART_INF_F;
   }
 }
 

@@ -72,7 +72,8 @@ struct CompactArgs {
 
 cudaError_t launch_pages_append(const AppendArgs& a, cudaStream_t stream);
 kvq_status launch_paged_attention(const PagedAttnArgs& a, cudaStream_t stream);
-size_t paged_attention_workspace(int kv_heads, int q_heads, int d, int batch, int rows, int max_q);
+// bytes, 16 where none are needed
+size_t paged_attention_workspace(int kv_heads, int q_heads, int d, int batch, long long keys, int rows, int max_q);
 cudaError_t launch_pages_copy(const PagePool& p, const int32_t* src, const int32_t* dst, int n,
                               cudaStream_t stream);
 cudaError_t launch_pages_compact(const CompactArgs& a, cudaStream_t stream);

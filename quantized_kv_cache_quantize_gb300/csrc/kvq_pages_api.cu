@@ -33,10 +33,11 @@ kvq_status check_pool(const kvq_pages* p) {
   return KVQ_OK;
 }
 
-kvq_status check_sequences(const kvq_sequences* s) {
+kvq_status check_sequences(const kvq_sequences* s, int page_tokens) {
   if (s == nullptr || s->batch < 0 || s->width < 0 || s->rows < 0) return KVQ_ERR_INVALID_ARG;
   if (s->offsets == nullptr && s->rows != s->batch) return KVQ_ERR_INVALID_ARG;
   if (s->batch > (1 << 24)) return KVQ_ERR_INVALID_ARG;
+  if ((long long)s->width * page_tokens > (1LL << 30)) return KVQ_ERR_TOO_LARGE;
   if (s->rows == 0) return KVQ_OK;
   if (s->batch < 1 || s->kv_lens == nullptr) return KVQ_ERR_INVALID_ARG;
   if (s->width > 0 && s->table == nullptr) return KVQ_ERR_INVALID_ARG;
@@ -103,7 +104,7 @@ kvq_status kvq_pages_append(const kvq_pages* pages, int32_t layer, const uint16_
   kvq_status st = check_pool(pages);
   if (st != KVQ_OK) return st;
   if (layer < 0 || layer >= pages->layers) return KVQ_ERR_INVALID_ARG;
-  st = check_sequences(seqs);
+  st = check_sequences(seqs, pages->page_tokens);
   if (st != KVQ_OK) return st;
   if (seqs->rows == 0) return KVQ_OK;
   if (k_new == nullptr || v_new == nullptr) return KVQ_ERR_INVALID_ARG;
@@ -129,10 +130,11 @@ kvq_status kvq_pages_append(const kvq_pages* pages, int32_t layer, const uint16_
 }
 
 size_t kvq_paged_workspace_bytes(const kvq_pages* pages, int32_t q_heads, int32_t batch,
-                                 int32_t rows, int32_t max_q) {
+                                 int32_t width, int32_t rows, int32_t max_q) {
   if (check_geometry(pages) != KVQ_OK) return 0;
-  if (q_heads < 1 || q_heads % pages->kv_heads != 0 || batch < 0 || rows < 0 || max_q < 0) return 0;
-  return kvq::paged_attention_workspace(pages->kv_heads, q_heads, pages->head_dim, batch, rows, max_q);
+  if (q_heads < 1 || q_heads % pages->kv_heads != 0 || batch < 0 || width < 0 || rows < 0 || max_q < 0) return 0;
+  return kvq::paged_attention_workspace(pages->kv_heads, q_heads, pages->head_dim, batch,
+                                        (long long)width * pages->page_tokens, rows, max_q);
 }
 
 kvq_status kvq_paged_attention(const kvq_pages* pages, int32_t layer, const uint16_t* q,
@@ -144,19 +146,20 @@ kvq_status kvq_paged_attention(const kvq_pages* pages, int32_t layer, const uint
   if (st != KVQ_OK) return st;
   if (layer < 0 || layer >= pages->layers) return KVQ_ERR_INVALID_ARG;
   if (q_heads < 1 || q_heads % pages->kv_heads != 0) return KVQ_ERR_INVALID_ARG;
-  st = check_sequences(seqs);
+  st = check_sequences(seqs, pages->page_tokens);
   if (st != KVQ_OK) return st;
   if (!std::isfinite(scale) || scale <= 0.f || window < 0 || max_q < 0) return KVQ_ERR_INVALID_ARG;
   if (seqs->rows == 0) return KVQ_OK;
-  if (max_q < 1 || q == nullptr || out == nullptr || workspace == nullptr) return KVQ_ERR_INVALID_ARG;
+  if (max_q < 1 || q == nullptr || out == nullptr) return KVQ_ERR_INVALID_ARG;
   if (bad_stride(q_row_stride) || bad_stride(q_head_stride) || !aligned(q, 16) || !aligned(out, 16) ||
       !aligned(lse, 4) || !aligned(workspace, 16))
     return KVQ_ERR_ALIGNMENT;
   if (max_q > seqs->rows) max_q = seqs->rows;
   if (seqs->offsets == nullptr) max_q = 1;
-  if (workspace_bytes < kvq::paged_attention_workspace(pages->kv_heads, q_heads, pages->head_dim,
-                                                       seqs->batch, seqs->rows, max_q))
-    return KVQ_ERR_INVALID_ARG;
+  const size_t need = kvq::paged_attention_workspace(
+      pages->kv_heads, q_heads, pages->head_dim, seqs->batch,
+      (long long)seqs->width * pages->page_tokens, seqs->rows, max_q);
+  if (need > 16 && (workspace == nullptr || workspace_bytes < need)) return KVQ_ERR_INVALID_ARG;
   kvq::PagedAttnArgs a{};
   a.p = layer_of(pages, layer);
   a.s = seqs_of(seqs);
@@ -187,20 +190,24 @@ kvq_status kvq_pages_copy(const kvq_pages* pages, const int32_t* src, const int3
   if (n < 0) return KVQ_ERR_INVALID_ARG;
   if (n == 0) return KVQ_OK;
   if (src == nullptr || dst == nullptr) return KVQ_ERR_INVALID_ARG;
-  // ids in the pool; dst distinct, none of them a src: sorted, neighbours
-  // that are equal and not both sources are refused
+  // ids in the pool, dst distinct, none of them a src: the call's number is
+  // noted beside every dst (scratch of this thread, never cleared)
   try {
-    std::vector<int64_t> ids;
-    ids.reserve(2 * (size_t)n);
-    for (int32_t i = 0; i < n; ++i) {
-      if (src[i] < 0 || src[i] >= pages->n_pages || dst[i] < 0 || dst[i] >= pages->n_pages)
-        return KVQ_ERR_INVALID_ARG;
-      ids.push_back(2 * (int64_t)src[i]);
-      ids.push_back(2 * (int64_t)dst[i] + 1);
+    static thread_local std::vector<uint32_t> seen;
+    static thread_local uint32_t call = 0;
+    if (seen.size() < (size_t)pages->n_pages) seen.resize(pages->n_pages, 0u);
+    if (++call == 0) {
+      std::fill(seen.begin(), seen.end(), 0u);
+      call = 1;
     }
-    std::sort(ids.begin(), ids.end());
-    for (size_t i = 1; i < ids.size(); ++i)
-      if (ids[i] / 2 == ids[i - 1] / 2 && (ids[i] & 1)) return KVQ_ERR_INVALID_ARG;
+    const uint32_t most = (uint32_t)pages->n_pages;
+    for (int32_t i = 0; i < n; ++i) {
+      if ((uint32_t)src[i] >= most || (uint32_t)dst[i] >= most || seen[dst[i]] == call)
+        return KVQ_ERR_INVALID_ARG;
+      seen[dst[i]] = call;
+    }
+    for (int32_t i = 0; i < n; ++i)
+      if (seen[src[i]] == call) return KVQ_ERR_INVALID_ARG;
   } catch (...) {
     return KVQ_ERR_TOO_LARGE;   // no host memory for the check
   }

@@ -4,6 +4,7 @@ device memory and streams.  There is no CPU fallback: if libkvq.so is missing
 the first call raises."""
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import functools
@@ -114,8 +115,7 @@ _SIGNATURES = {
                                        ctypes.POINTER(ctypes.c_size_t)]),
     "kvq_pages_append": (ctypes.c_int, [_P, ctypes.c_int32, _P, ctypes.c_int64, ctypes.c_int64,
                                         _P, ctypes.c_int64, ctypes.c_int64, _P, _P]),
-    "kvq_paged_workspace_bytes": (ctypes.c_size_t, [_P, ctypes.c_int32, ctypes.c_int32,
-                                                    ctypes.c_int32, ctypes.c_int32]),
+    "kvq_paged_workspace_bytes": (ctypes.c_size_t, [_P] + [ctypes.c_int32] * 5),
     "kvq_paged_attention": (ctypes.c_int, [_P, ctypes.c_int32, _P, ctypes.c_int64, ctypes.c_int64,
                                            ctypes.c_int32, _P, ctypes.c_int32, ctypes.c_float,
                                            ctypes.c_int32, ctypes.c_int32, _P, ctypes.c_size_t, _P,
@@ -146,13 +146,18 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+@functools.lru_cache(maxsize=None)
+def _cuda_present() -> bool:
+    return torch.cuda.is_available()
+
+
 def _nvtx(name: str):
     """Mark each call of the decorated entry point as an NVTX range (for
     Nsight timelines and ncu --nvtx filters); host-side only."""
     def deco(fn):
         @functools.wraps(fn)
         def wrapped(*args, **kwargs):
-            if not torch.cuda.is_available():
+            if not _cuda_present():
                 return fn(*args, **kwargs)
             torch.cuda.nvtx.range_push(name)
             try:
@@ -183,12 +188,15 @@ def _stream(stream, device=None) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+_NO_SWITCH = contextlib.nullcontext()
+
+
 def _alloc_on(stream, device):
     """Where a call's own tensors (outputs, workspace) are allocated: on the
     stream its kernels run on, so that the allocator hands out memory whose
     earlier users are done by then, and takes it back after the call's."""
     if stream is None or device.type != "cuda":
-        return contextlib.nullcontext()
+        return _NO_SWITCH
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     return torch.cuda.stream(stream)
@@ -470,6 +478,9 @@ class PagedCache:
         c.k_scale, c.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
         _check(lib().kvq_pages_bytes(ctypes.byref(c), None, None), "kvq_pages_bytes")
         self.struct = c
+        self.device = k_codes.device
+        self.layers, self.n_pages, self.kv_heads, self.page_tokens, self.head_dim = k_codes.shape
+        self._at = ctypes.addressof(c)
 
     @classmethod
     def zeros(cls, layers: int, n_pages: int, kv_heads: int, page_tokens: int, head_dim: int,
@@ -480,29 +491,35 @@ class PagedCache:
         scales = [torch.ones(shape[:3], dtype=torch.bfloat16, device=device) for _ in range(2)]
         return cls(*codes, *scales)
 
-    layers = property(lambda self: self.struct.layers)
-    n_pages = property(lambda self: self.struct.n_pages)
-    kv_heads = property(lambda self: self.struct.kv_heads)
-    page_tokens = property(lambda self: self.struct.page_tokens)
-    head_dim = property(lambda self: self.struct.head_dim)
-    device = property(lambda self: self.k_codes.device)
-
-    def workspace_bytes(self, q_heads: int, batch: int, rows: int, max_q: int) -> int:
-        """kvq_paged_workspace_bytes."""
-        with _on_device(self.device):
-            return int(lib().kvq_paged_workspace_bytes(ctypes.byref(self.struct), q_heads, batch,
-                                                       rows, max_q))
+    def workspace_bytes(self, q_heads: int, batch: int, width: int, rows: int, max_q: int) -> int:
+        """kvq_paged_workspace_bytes (width: entries per row of the block table)."""
+        with _switch(self.device):
+            return int(lib().kvq_paged_workspace_bytes(self._at, q_heads, batch, width, rows, max_q))
 
 
-def _int32_dev(cache: PagedCache, t: torch.Tensor, name: str, dim: int) -> torch.Tensor:
-    if t.dtype != torch.int32 or t.dim() != dim or not t.is_cuda:
+def _switch(device):
+    """_on_device, without the cost of a switch where none is needed: the
+    paged calls are short."""
+    if device.type != "cuda" or device.index == torch.cuda.current_device():
+        return _NO_SWITCH
+    return torch.cuda.device(device)
+
+
+def _handle(stream, device) -> int:
+    """_stream's handle, as the number ctypes passes on."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return _stream(stream, device).value or 0
+
+
+def _int32_dev(cache: PagedCache, t: torch.Tensor, name: str, dim: int):
+    if t.dtype is not torch.int32 or t.dim() != dim or not t.is_cuda:
         raise ValueError(f"{name} must be a {dim}-dimensional CUDA int32 tensor, got {t.dtype} "
                          f"{list(t.shape)} on {t.device}")
     if t.device != cache.device:
         raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
     if t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel() > 0:
         raise ValueError(f"{name} must be contiguous in its last dimension")
-    return t
 
 
 def _row_stride(t: torch.Tensor) -> int:
@@ -510,22 +527,25 @@ def _row_stride(t: torch.Tensor) -> int:
     return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
-def _paged_rows(cache: PagedCache, t: torch.Tensor, name: str) -> torch.Tensor:
-    """[rows, heads, head_dim] BF16, the channels contiguous, the rows and heads
-    at strides of their own (multiples of 8 elements)."""
-    if t.dim() != 3 or t.shape[2] != cache.head_dim:
-        raise ValueError(f"{name} must have shape [rows, heads, {cache.head_dim}], got {list(t.shape)}")
-    if t.dtype != torch.bfloat16 or not t.is_cuda or (t.stride(2) != 1 and t.numel() > 0):
+def _paged_rows(cache: PagedCache, t: torch.Tensor, name: str) -> tuple:
+    """Checks [rows, heads, head_dim] BF16, the channels contiguous, the rows
+    and heads at strides of their own (multiples of 8 elements, which the
+    library checks); returns (shape, strides)."""
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != cache.head_dim:
+        raise ValueError(f"{name} must have shape [rows, heads, {cache.head_dim}], got {list(shape)}")
+    strides = t.stride()
+    if t.dtype is not torch.bfloat16 or not t.is_cuda or (strides[2] != 1 and t.numel() > 0):
         raise ValueError(f"{name} must be a CUDA bfloat16 tensor with contiguous channels")
     if t.device != cache.device:
         raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
-    return t
+    return shape, strides
 
 
 def _sequences(cache: PagedCache, rows: int, block_table, kv_lens, offsets) -> SequencesStruct:
     _int32_dev(cache, block_table, "block_table", 2)
     _int32_dev(cache, kv_lens, "kv_lens", 1)
-    batch = int(block_table.shape[0])
+    batch, width = block_table.shape
     if kv_lens.shape[0] != batch:
         raise ValueError(f"kv_lens must have one entry per row of block_table ({batch}), got "
                          f"{kv_lens.shape[0]}")
@@ -537,12 +557,8 @@ def _sequences(cache: PagedCache, rows: int, block_table, kv_lens, offsets) -> S
         _int32_dev(cache, offsets, "offsets", 1)
         if offsets.shape[0] != batch + 1:
             raise ValueError(f"offsets must have {batch + 1} entries, got {offsets.shape[0]}")
-    s = SequencesStruct()
-    s.batch, s.width, s.table_stride = batch, int(block_table.shape[1]), _row_stride(block_table)
-    s.table, s.kv_lens = block_table.data_ptr(), kv_lens.data_ptr()
-    s.offsets = None if offsets is None else offsets.data_ptr()
-    s.rows = rows
-    return s
+    return SequencesStruct(batch, width, _row_stride(block_table), block_table.data_ptr(),
+                           kv_lens.data_ptr(), None if offsets is None else offsets.data_ptr(), rows)
 
 
 @_nvtx("kvq_pages_append")
@@ -553,17 +569,16 @@ def pages_append(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor,
     of all sequences packed (rows offsets[b] .. offsets[b + 1] are sequence
     b's; None: one row each), appended so that sequence b then holds
     kv_lens[b] tokens."""
-    _paged_rows(cache, k_new, "k_new")
-    _paged_rows(cache, v_new, "v_new")
-    if k_new.shape != v_new.shape or k_new.shape[1] != cache.kv_heads:
+    shape, ks = _paged_rows(cache, k_new, "k_new")
+    shape_v, vs = _paged_rows(cache, v_new, "v_new")
+    if shape != shape_v or shape[1] != cache.kv_heads:
         raise ValueError(f"k_new and v_new must have shape [rows, {cache.kv_heads}, "
-                         f"{cache.head_dim}], got {list(k_new.shape)} and {list(v_new.shape)}")
-    s = _sequences(cache, int(k_new.shape[0]), block_table, kv_lens, offsets)
-    with _on_device(cache.device):
+                         f"{cache.head_dim}], got {list(shape)} and {list(shape_v)}")
+    s = _sequences(cache, shape[0], block_table, kv_lens, offsets)
+    with _switch(cache.device):
         _check(lib().kvq_pages_append(
-            ctypes.byref(cache.struct), layer, _ptr(k_new), k_new.stride(0), k_new.stride(1),
-            _ptr(v_new), v_new.stride(0), v_new.stride(1), ctypes.byref(s),
-            _stream(stream, cache.device)), "kvq_pages_append")
+            cache._at, layer, k_new.data_ptr(), ks[0], ks[1], v_new.data_ptr(), vs[0], vs[1],
+            ctypes.addressof(s), _handle(stream, cache.device)), "kvq_pages_append")
 
 
 @_nvtx("kvq_paged_attention")
@@ -576,57 +591,73 @@ def paged_attention(cache: PagedCache, q: torch.Tensor, block_table: torch.Tenso
     tokens).  max_q: the most rows a sequence has (default: all of them).
     Returns out [rows, q_heads, head_dim] (and lse [rows, q_heads] fp32 with
     with_lse)."""
-    _paged_rows(cache, q, "q")
-    rows, q_heads = int(q.shape[0]), int(q.shape[1])
+    shape, qs = _paged_rows(cache, q, "q")
+    rows, q_heads, d = shape
     if q_heads < 1 or q_heads % cache.kv_heads:
         raise ValueError(f"q has {q_heads} heads, not a multiple of the cache's {cache.kv_heads}")
     s = _sequences(cache, rows, block_table, kv_lens, offsets)
-    max_q = (1 if offsets is None else rows) if max_q is None else max_q
-    scale = 1.0 / math.sqrt(cache.head_dim) if scale is None else scale
-    st = _stream(stream, q.device)
+    if max_q is None:
+        max_q = 1 if offsets is None else rows
+    dev = cache.device
+    handle = _handle(stream, dev)
     if out is not None:
-        if out.device != q.device:
-            raise ValueError(f"out is on {out.device}, q on {q.device}")
+        if out.device != dev:
+            raise ValueError(f"out is on {out.device}, q on {dev}")
         _check_out(q, out)
-    with _on_device(q.device):
-        with _alloc_on(stream, q.device):
-            if out is None:
-                out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if with_lse else None
-            if workspace is None:
-                workspace = torch.empty(max(cache.workspace_bytes(q_heads, s.batch, rows, max_q), 16),
-                                        dtype=torch.uint8, device=q.device)
-        ws_ptr, ws_size = _workspace_arg(workspace, q.device)
+    lse = None
+    with _switch(dev), _alloc_on(stream, dev):
+        if out is None:
+            out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        if with_lse:
+            lse = torch.empty((rows, q_heads), dtype=torch.float32, device=dev)
+        if workspace is None:
+            ws, ws_bytes = None, lib().kvq_paged_workspace_bytes(cache._at, q_heads, s.batch, s.width,
+                                                                 rows, max_q)
+            if ws_bytes > 16:
+                workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+                ws = workspace.data_ptr()
+        else:
+            ws_ptr, ws_bytes = _workspace_arg(workspace, dev)
+            ws = ws_ptr.value
         _check(lib().kvq_paged_attention(
-            ctypes.byref(cache.struct), layer, _ptr(q), q.stride(0), q.stride(1), q_heads,
-            ctypes.byref(s), max_q, ctypes.c_float(scale), int(bool(causal)), window, ws_ptr,
-            ws_size, _ptr(out), _ptr(lse), st), "kvq_paged_attention")
+            cache._at, layer, q.data_ptr(), qs[0], qs[1], q_heads, ctypes.addressof(s), max_q,
+            1.0 / math.sqrt(d) if scale is None else scale, 1 if causal else 0, window, ws, ws_bytes,
+            out.data_ptr(), None if lse is None else lse.data_ptr(), handle), "kvq_paged_attention")
     return (out, lse) if with_lse else out
 
 
-def _host_ids(ids, name: str) -> torch.Tensor:
-    t = torch.as_tensor(ids)
-    if t.numel() == 0 and t.dim() == 1:
-        t = t.to(torch.int32)   # an empty list has no type of its own
-    if t.is_cuda or t.dim() != 1 or t.is_floating_point() or t.dtype == torch.bool:
-        raise ValueError(f"{name} must be a list or a 1-dimensional CPU integer tensor")
-    if t.numel() and (int(t.min()) < 0 or int(t.max()) > 0x7FFFFFFF):
-        raise ValueError(f"{name} holds an id outside the pool")
-    return t.to(torch.int32).contiguous()
+def _host_ids(ids, name: str) -> tuple:
+    """(address, number, owner) of page ids in host memory."""
+    if isinstance(ids, torch.Tensor):
+        if ids.is_cuda or ids.dim() != 1 or ids.dtype not in (torch.int32, torch.int64):
+            raise ValueError(f"{name} must be a list or a 1-dimensional CPU int32 or int64 tensor")
+        if ids.dtype is torch.int64:
+            if ids.numel() and (int(ids.min()) < 0 or int(ids.max()) > 0x7FFFFFFF):
+                raise ValueError(f"{name} holds an id outside the pool")
+            ids = ids.to(torch.int32)
+        ids = ids.contiguous()
+        return ids.data_ptr(), ids.numel(), ids
+    try:
+        own = array.array("i", ids)
+    except (TypeError, OverflowError) as e:
+        raise ValueError(f"{name} must be a list of page ids: {e}") from None
+    return own.buffer_info()[0], len(own), own
 
 
 @_nvtx("kvq_pages_copy")
 def pages_copy(cache: PagedCache, src, dst, stream=None):
     """kvq_pages_copy: pages src[i] -> dst[i] of every layer (lists or CPU
     integer tensors; the dst distinct, none of them a src)."""
-    src, dst = _host_ids(src, "src"), _host_ids(dst, "dst")
-    if src.shape != dst.shape:
-        raise ValueError(f"src has {src.numel()} pages, dst {dst.numel()}")
-    if cache.device.type != "cuda":
-        raise ValueError(f"the cache is on {cache.device}, not a CUDA device")
-    with _on_device(cache.device):
-        _check(lib().kvq_pages_copy(ctypes.byref(cache.struct), _ptr(src), _ptr(dst), src.numel(),
-                                    _stream(stream, cache.device)), "kvq_pages_copy")
+    src_at, n, src_own = _host_ids(src, "src")
+    dst_at, n_dst, dst_own = _host_ids(dst, "dst")
+    if n != n_dst:
+        raise ValueError(f"src has {n} pages, dst {n_dst}")
+    dev = cache.device
+    if dev.type != "cuda":
+        raise ValueError(f"the cache is on {dev}, not a CUDA device")
+    with _switch(dev):
+        _check(lib().kvq_pages_copy(cache._at, src_at, dst_at, n, _handle(stream, dev)),
+               "kvq_pages_copy")
 
 
 @_nvtx("kvq_pages_compact")
@@ -637,25 +668,29 @@ def pages_compact(cache: PagedCache, block_table: torch.Tensor, out=None, worksp
     one-element int32 tensor with the number of live pages); out: where to
     write the table (block_table itself for in place)."""
     _int32_dev(cache, block_table, "block_table", 2)
-    st = _stream(stream, cache.device)
+    dev = cache.device
+    handle = _handle(stream, dev)
+    shape = block_table.shape
     if out is not None:
         _int32_dev(cache, out, "out", 2)
-        if out.shape != block_table.shape:
-            raise ValueError(f"out must have the shape of block_table {list(block_table.shape)}, "
-                             f"got {list(out.shape)}")
-    with _on_device(cache.device):
-        need = int(lib().kvq_pages_compact_workspace_bytes(ctypes.byref(cache.struct)))
-        with _alloc_on(stream, cache.device):
-            if out is None:
-                out = torch.empty(block_table.shape, dtype=torch.int32, device=cache.device)
-            n_live = torch.empty(1, dtype=torch.int32, device=cache.device)
-            if workspace is None:
-                workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=cache.device)
-        ws_ptr, ws_size = _workspace_arg(workspace, cache.device)
+        if out.shape != shape:
+            raise ValueError(f"out must have the shape of block_table {list(shape)}, got "
+                             f"{list(out.shape)}")
+    with _switch(dev), _alloc_on(stream, dev):
+        if out is None:
+            out = torch.empty(shape, dtype=torch.int32, device=dev)
+        n_live = torch.empty(1, dtype=torch.int32, device=dev)
+        if workspace is None:
+            need = lib().kvq_pages_compact_workspace_bytes(cache._at)
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+            ws, ws_bytes = workspace.data_ptr(), need
+        else:
+            ws_ptr, ws_bytes = _workspace_arg(workspace, dev)
+            ws = ws_ptr.value
         _check(lib().kvq_pages_compact(
-            ctypes.byref(cache.struct), _ptr(block_table), block_table.shape[0],
-            block_table.shape[1], _row_stride(block_table), _ptr(out), _row_stride(out),
-            _ptr(n_live), ws_ptr, ws_size, st), "kvq_pages_compact")
+            cache._at, block_table.data_ptr(), shape[0], shape[1], _row_stride(block_table),
+            out.data_ptr(), _row_stride(out), n_live.data_ptr(), ws, ws_bytes, handle),
+            "kvq_pages_compact")
     return out, n_live
 
 

@@ -440,7 +440,7 @@ def test_step_in_a_graph_follows_lengths_and_tables():
     table, lens = torch.zeros(2, 9, dtype=torch.int32, device="cuda"), torch.ones(2, dtype=torch.int32, device="cuda")
     k, v, q = (torch.zeros(2, h, d, dtype=torch.bfloat16, device="cuda") for h in (heads, heads, hq))
     table.copy_(dev([[0] * 9, [1] * 9]))
-    ws = torch.empty(cache.workspace_bytes(hq, 2, 2, 1), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(cache.workspace_bytes(hq, 2, 9, 2, 1), dtype=torch.uint8, device="cuda")
 
     def run():
         kvq.pages_append(cache, k, v, table, lens)

@@ -139,7 +139,7 @@ def test_bad_pool(lib, field, value, status):
     c = _pages(**{field: value})
     if (field, value, status) in GEOMETRY:
         assert lib.kvq_pages_bytes(ctypes.byref(c), None, None) == status
-        assert lib.kvq_paged_workspace_bytes(ctypes.byref(c), 8, 1, 1, 1) == 0
+        assert lib.kvq_paged_workspace_bytes(ctypes.byref(c), 8, 1, 1, 1, 1) == 0
         assert lib.kvq_pages_compact_workspace_bytes(ctypes.byref(c)) == 0
     assert _append(lib, c) == status
     assert _attend(lib, c) == status
@@ -174,13 +174,18 @@ def test_attention_refusals(lib):
     assert _attend(lib, heads=6) == 1 and _attend(lib, heads=0) == 1
     assert _attend(lib, scale=float("nan")) == 1 and _attend(lib, scale=0.0) == 1
     assert _attend(lib, window=-1) == 1 and _attend(lib, max_q=0) == 1
-    assert _attend(lib, q=None) == 1 and _attend(lib, out=None) == 1 and _attend(lib, ws=None) == 1
+    assert _attend(lib, q=None) == 1 and _attend(lib, out=None) == 1
+    wide = _seqs(width=1 << 16, table_stride=1 << 16)          # long sequences: parts go through the workspace
+    need = lib.kvq_paged_workspace_bytes(ctypes.byref(_pages()), 8, 3, 1 << 16, 3, 1)
+    assert need > 16
+    assert _attend(lib, s=wide, ws=None) == 1 and _attend(lib, s=wide, ws_bytes=need - 1) == 1
+    assert _attend(lib, s=_seqs(width=1 << 27, table_stride=1 << 27)) == kvq.KVQ_ERR_TOO_LARGE
+    assert _append(lib, s=_seqs(width=1 << 27, table_stride=1 << 27)) == kvq.KVQ_ERR_TOO_LARGE
     assert _attend(lib, q=PTR + 2) == 6 and _attend(lib, out=PTR + 2) == 6 and _attend(lib, lse=PTR + 2) == 6
     assert _attend(lib, ws=PTR + 8) == 6 and _attend(lib, qs=(1024, 12)) == 6
-    assert _attend(lib, ws_bytes=0) == 1
     assert _attend(lib, s=_seqs(rows=0, batch=0)) == 0
     c = _pages()
-    assert lib.kvq_paged_workspace_bytes(ctypes.byref(c), 6, 1, 1, 1) == 0
+    assert lib.kvq_paged_workspace_bytes(ctypes.byref(c), 6, 1, 1, 1, 1) == 0
 
 
 def test_copy_refusals(lib):
@@ -249,9 +254,9 @@ def test_binding_refusals(lib):
             kvq.paged_attention(cache, bad, table, lens)
     with pytest.raises(ValueError, match="CUDA int32"):
         kvq.pages_compact(cache, table)
-    for src, dst in (([1], [2, 3]), ([0.5], [1]), ([-1], [1]), ([1 << 40], [1]),
+    for src, dst in (([1], [2, 3]), ([0.5], [1]), ([1 << 40], [1]), (torch.tensor([-1]), [1]),
                      (torch.ones(1, 1, dtype=torch.int32), [1])):
-        with pytest.raises(ValueError, match="src|outside|list"):
+        with pytest.raises(ValueError, match="src|outside|list|dst"):
             kvq.pages_copy(cache, src, dst)
     with pytest.raises(ValueError, match="not a CUDA device"):
         kvq.pages_copy(cache, [1], [2])
