@@ -20,8 +20,8 @@
 // Page scales are powers of two outside the products: K's on the scores, V's
 // on the weight before it is rounded, relative to the largest so far (eref);
 // the sum of weights is taken without them.
-// The base m is raised only when a weight would leave FP16 (a chunk's sum
-// past 2^15), to 2^9 headroom, so weights down to 2^-33 of the largest remain.
+// The base m is raised only when a weight would leave FP16 (64 keys' sum past
+// 2^15), to leave the largest at 2^9, so weights down to 2^-33 of it remain.
 //
 // Roles: 4 NQ warps softmax (one row per thread), 4 warps V conversion, one
 // MMA thread, one TMA warp.  With NQ = 2 the two query tiles alternate on the
@@ -40,6 +40,10 @@ namespace {
 
 constexpr int kTileKeys = 128;
 constexpr int kKStages = 3, kVStages = 2, kMetaSlots = 8;
+// a slot of a tile's page scales, per block of 16 keys: 2^e of K [8], the V
+// exponent relative to eref [8] (as float) and 2^-that [8]; then eref and the
+// mask of blocks whose page is there
+constexpr int kMetaBytes = 128, kMetaShift = 32, kMetaInv = 64, kMetaRef = 96;
 
 template <int D, int NQ>
 struct ChunkCfg {
@@ -51,8 +55,8 @@ struct ChunkCfg {
   static constexpr int kV = kVr + kVStages * kKT;  // values in FP16, D / 64 sub-tiles [128][64]
   static constexpr int kVT = 2 * kKT;
   static constexpr int kMeta = kV + kVStages * kVT;
-  static constexpr int kBar = kMeta + kMetaSlots * 32;
-  static constexpr int kBytes = kBar + 256;
+  static constexpr int kBar = kMeta + kMetaSlots * kMetaBytes;
+  static constexpr int kBytes = kBar + 512;
   static constexpr int kAlloc = kBytes + 1024;
   static constexpr int kSoftmaxWarps = 4 * NQ;
   static constexpr int kMmaWarp = kSoftmaxWarps + 4;
@@ -64,21 +68,23 @@ struct ChunkCfg {
 };
 
 enum : int {
-  kCbQ = 0,         // query tiles written (128 NQ arrivals)
+  kCbQ = 0,         // query tiles written (4 NQ arrivals, one per warp)
   kCbFullK = 1,     // [3] key codes landed, page exponents written
   kCbEmptyK = 4,    // [3] the tile's QK MMAs done
   kCbFullVr = 7,    // [2] value codes landed
-  kCbEmptyVr = 9,   // [2] value codes read (128 arrivals)
-  kCbFullV = 11,    // [2] FP16 values written (128 arrivals)
+  kCbEmptyVr = 9,   // [2] value codes read (4 arrivals)
+  kCbFullV = 11,    // [2] FP16 values written (4 arrivals)
   kCbEmptyV = 13,   // [2] the tile's PV MMAs done
   kCbS = 15,        // [2] scores ready
-  kCbP = 17,        // [2] weights written, O rescaled (128 arrivals)
+  kCbP = 17,        // [2] weights of keys 0-63 written, O rescaled (4 arrivals)
   kCbOStep = 19,    // NQ = 1: a tile's PV done
   kCbODone = 20,    // every MMA done
   kCbMeta = 21,     // [8] a tile's page exponents written.  Not the key
                     // barrier: its stage can be refilled, and its phase
                     // passed twice, before a slow softmax warp looks at it
-  kCbCount = 29
+  kCbPb = 29,       // [2] weights of keys 64-127 written (4 arrivals)
+  kCbHalf = 31,     // [2] PV of keys 0-63 done
+  kCbCount = 33
 };
 
 struct ChunkArgs {
@@ -89,14 +95,43 @@ struct ChunkArgs {
   float* part_ml;     // [splits][rows * q_heads][2]
 };
 
-// the 16 keys' page of block `blk` of the line of 16-key blocks
-struct BlockMeta {
-  int id, word;       // word: K exponent + 64, V exponent + 64, valid bit
+// the page of a block of 16 keys: id (-1: none), scale exponents
+struct BlockPage {
+  int id, ek, ev;
 };
 
-template <bool MASKED>
-__device__ __forceinline__ void exp_block(const uint32_t* s, float scale, float shift, int lo, int hi,
-                                          uint32_t* pk, float& sum) {
+// shared memory by its 32-bit address (a generic pointer would make each
+// access a generic one)
+__device__ __forceinline__ uint4 lds_u4(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds_u2(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ float lds_f(uint32_t at) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts_f(uint32_t at, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+}
+__device__ __forceinline__ void sts_u4(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void sts_u2(uint32_t at, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(x), "r"(y) : "memory");
+}
+
+// where the base of a row starts: every weight against it is infinite
+constexpr float kLowest = -1e30f;
+
+// weights of 16 scores, 2^(score scale + shift), as FP16 pairs, and their sum
+__device__ __forceinline__ void exp_block(const uint32_t* s, float scale, float shift, uint32_t* pk, float& sum) {
   const uint64_t s2 = ptx::f2_pack(scale, scale), b2 = ptx::f2_pack(shift, shift);
   uint64_t acc = ptx::f2_pack(0.f, 0.f);
 #pragma unroll
@@ -104,22 +139,26 @@ __device__ __forceinline__ void exp_block(const uint32_t* s, float scale, float 
     float x0, x1;
     ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), s2, b2),
                    x0, x1);
-    float e0 = ptx::ex2_approx(x0), e1 = ptx::ex2_approx(x1);
-    if (MASKED) {
-      e0 = (2 * k >= lo && 2 * k < hi) ? e0 : 0.f;
-      e1 = (2 * k + 1 >= lo && 2 * k + 1 < hi) ? e1 : 0.f;
-    }
+    const float e0 = ptx::ex2_approx(x0), e1 = ptx::ex2_approx(x1);
     acc = ptx::f2_add(acc, ptx::f2_pack(e0, e1));
     pk[k] = ptx::f16x2_rn(e0, e1);
   }
-  float a, b;
-  ptx::f2_unpack(acc, a, b);
-  sum = a + b;
+  float x, y;
+  ptx::f2_unpack(acc, x, y);
+  sum = x + y;
+}
+// scores of columns outside [lo, hi) become -inf
+__device__ __forceinline__ void mask_block(uint32_t* s, int lo, int hi) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k) s[k] = k >= lo && k < hi ? s[k] : 0xff800000u;
 }
 
-__device__ __forceinline__ int meta_ek(int w) { return (w & 255) - 64; }
-__device__ __forceinline__ int meta_ev(int w) { return ((w >> 8) & 255) - 64; }
-__device__ __forceinline__ bool meta_ok(int w) { return (w >> 16) != 0; }
+// one arrival for a warp whose lanes are all done (a barrier takes its
+// arrivals one after another: 128 of them cost some hundred cycles)
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(bar);
+}
 
 template <int D, int NQ>
 __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
@@ -167,18 +206,20 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
   const uint32_t bar0 = ptx::smem_u32(smem + C::kBar);
   auto BAR = [&](int i) { return bar0 + 8u * (uint32_t)i; };
   if (tid == 0) {
-    ptx::mbar_init(BAR(kCbQ), 128 * NQ);
+    ptx::mbar_init(BAR(kCbQ), 4 * NQ);
     for (int i = 0; i < kKStages; ++i) {
       ptx::mbar_init(BAR(kCbFullK + i), 1);
       ptx::mbar_init(BAR(kCbEmptyK + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(BAR(kCbFullVr + i), 1);
-      ptx::mbar_init(BAR(kCbEmptyVr + i), 128);
-      ptx::mbar_init(BAR(kCbFullV + i), 128);
+      ptx::mbar_init(BAR(kCbEmptyVr + i), 4);
+      ptx::mbar_init(BAR(kCbFullV + i), 4);
       ptx::mbar_init(BAR(kCbEmptyV + i), 1);
       ptx::mbar_init(BAR(kCbS + i), 1);
-      ptx::mbar_init(BAR(kCbP + i), 128);
+      ptx::mbar_init(BAR(kCbP + i), 4);
+      ptx::mbar_init(BAR(kCbPb + i), 4);
+      ptx::mbar_init(BAR(kCbHalf + i), 1);
     }
     for (int i = 0; i < kMetaSlots; ++i) ptx::mbar_init(BAR(kCbMeta + i), 1);
     ptx::mbar_init(BAR(kCbOStep), 1);
@@ -195,12 +236,12 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const unsigned long long lim = a.wait_limit_ns;
-  const int* meta = reinterpret_cast<const int*>(smem + C::kMeta);
+  const uint32_t sm = ptx::smem_u32(smem);
 
   if (warp < C::kSoftmaxWarps) {
     // =========================== softmax ===========================
     const int q = warp >> 2;
-    const int r = tid - q * 128;                 // TMEM lane, row of the query tile
+    const int r = (warp & 3) * 32 + lane;        // TMEM lane, row of the query tile
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const int row = row0 + q * 128 + r;          // of the head's rows
     const bool live = row < rows;
@@ -210,9 +251,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
     float cq;
     {
       uint4 raw[D / 8];
-      const uint16_t* qp = a.q + (long long)(r0 + tok) * a.q_row_stride + (long long)hq * a.q_head_stride;
+      const uint4* qp = reinterpret_cast<const uint4*>(a.q + (long long)(r0 + tok) * a.q_row_stride +
+                                                       (long long)hq * a.q_head_stride);
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) raw[c] = live ? __ldg(reinterpret_cast<const uint4*>(qp) + c) : make_uint4(0u, 0u, 0u, 0u);
+      for (int c = 0; c < D / 8; ++c) raw[c] = live ? __ldg(qp + c) : make_uint4(0u, 0u, 0u, 0u);
       uint32_t mx = 0;
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) {
@@ -223,8 +265,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
       const int e = max((int)(mx >> 7), 1) - 127 - 7;      // largest magnitude to [2^7, 2^8)
       const float f0 = pow2f(-(e / 2)), f1 = pow2f(-(e - e / 2));
       cq = a.scale * 1.4426950408889634f * pow2f(e / 2) * pow2f(e - e / 2);
-      uint8_t* hi_t = smem + C::kQ + q * 2 * C::kQT;
-      uint8_t* lo_t = hi_t + C::kQT;
+      const uint32_t hi_t = sm + C::kQ + q * 2 * C::kQT;
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
         uint32_t wh[4], wl[4];
@@ -241,18 +282,19 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
           wl[k] = e4m3x4(x0 - a01.x, x1 - a01.y, x2 - a23.x, x3 - a23.y);
         }
         const int off = D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-        *reinterpret_cast<uint4*>(hi_t + off) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
-        *reinterpret_cast<uint4*>(lo_t + off) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
+        sts_u4(hi_t + off, make_uint4(wh[0], wh[1], wh[2], wh[3]));
+        sts_u4(hi_t + C::kQT + off, make_uint4(wl[0], wl[1], wl[2], wl[3]));
       }
     }
     ptx::fence_proxy_async_smem();
-    ptx::mbar_arrive(BAR(kCbQ));
+    warp_arrive(BAR(kCbQ));
 
-    // keys this row attends to (rows past the last: none)
+    // keys this row attends to (rows past the last: none), from the first
+    // key of local tile 0
     const int tq = t0 + tok;
-    const int hi_r = live ? (a.causal ? min(len, tq + 1) : len) : 0;
-    const int lo_r = a.window > 0 ? max(0, tq - a.window + 1) : 0;
-    float m = -CUDART_INF_F, l = 0.f;
+    const int hi_r = (live ? (a.causal ? min(len, tq + 1) : len) : 0) - base;
+    const int lo_r = (a.window > 0 ? max(0, tq - a.window + 1) : 0) - base;
+    float m = kLowest, l = 0.f;
     int eref = -1000;
     const uint32_t t_o = tmem + C::kTO + q * D + lane_off;
     bool ok = true;
@@ -260,8 +302,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
       const int sb = NQ == 2 ? q : (j & 1);
       const uint32_t t_s = tmem + sb * 128 + lane_off;
       const uint32_t par = NQ == 2 ? (j & 1) : ((j >> 1) & 1);
-      // a slot of exponents is written again 8 tiles later, the TMA warp at
-      // most 5 ahead of the softmax (3 key stages, 2 score buffers)
+      // a slot of scales is written again 8 tiles later, the TMA warp at most
+      // 5 ahead of the softmax (3 key stages, 2 score buffers)
       ok = page_wait(BAR(kCbMeta + (j & (kMetaSlots - 1))), (j / kMetaSlots) & 1, lim, abort, a.status) &&
            page_wait(BAR(kCbS + sb), par, lim, abort, a.status);
       if (!__all_sync(0xffffffffu, ok)) {
@@ -269,110 +311,105 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
         break;
       }
       ptx::tc_fence_after();
-      const int* mt = meta + (j & (kMetaSlots - 1)) * 8;
-      const int e_in = eref;
-      bool blocks = true;
+      const uint32_t mt = sm + C::kMeta + (j & (kMetaSlots - 1)) * kMetaBytes;
+      const uint2 ref = lds_u2(mt + kMetaRef);
+      const int at0 = j * kTileKeys;
+      const bool whole = __all_sync(0xffffffffu, ref.y == 255u && lo_r <= at0 && hi_r >= at0 + kTileKeys);
+      // what O has to be multiplied by: the page scale it is held against and
+      // the base may both rise
+      float fo = eref == (int)ref.x ? 1.f : eref > -1000 ? pow2f(max(eref - (int)ref.x, -126)) : 0.f;
+      eref = (int)ref.x;
+      auto rescale_o = [&]() {
+        const uint64_t f2 = ptx::f2_pack(fo, fo);
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t v[16];
+          ptx::tmem_ld16(t_o + 16 * c, v);
 #pragma unroll
-      for (int k = 0; k < 8; k += 4) {
-        const int4 x = *reinterpret_cast<const int4*>(mt + k);
-        const int w4[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          blocks &= meta_ok(w4[i]);
-          eref = meta_ok(w4[i]) ? max(eref, meta_ev(w4[i])) : eref;
-        }
-      }
-      const int key0 = base + j * kTileKeys;
-      const int lo_t = lo_r - key0, hi_t = hi_r - key0;
-      const bool whole = __all_sync(0xffffffffu, blocks && lo_t <= 0 && hi_t >= kTileKeys);
-      const float m_in = m;
-      float sum_l = 0.f;
-      auto pass = [&](auto tag) {
-        constexpr bool MASKED = decltype(tag)::value;
-#pragma unroll 2
-        for (int c = 0; c < 4; ++c) {
-          uint32_t cur[32], pk[16];
-          ptx::tmem_ld32(t_s + 32 * c, cur);
-          const int2 w2 = *reinterpret_cast<const int2*>(mt + 2 * c);
-          const int wa = w2.x, wb = w2.y;
-          const float ca = cq * pow2f(meta_ek(wa)), cb = cq * pow2f(meta_ek(wb));
-          const int sa = min(max(meta_ev(wa) - eref, -60), 0), sb2 = min(max(meta_ev(wb) - eref, -60), 0);
-          // the row's columns of each block of 16
-          const int loa = meta_ok(wa) ? lo_t - 32 * c : 16, hia = hi_t - 32 * c;
-          const int lob = meta_ok(wb) ? lo_t - 32 * c - 16 : 16, hib = hi_t - 32 * c - 16;
-          float ha, hb;
-          exp_block<MASKED>(cur, ca, (float)sa - m, loa, hia, pk, ha);
-          exp_block<MASKED>(cur + 16, cb, (float)sb2 - m, lob, hib, pk + 8, hb);
-          // past FP16 (or the first weights of all, against the base -inf):
-          // a new base, and what the tile has so far follows it
-          if (__any_sync(0xffffffffu, !(ha + hb <= 32768.0f))) {
-            float top = -CUDART_INF_F;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const bool in_a = !MASKED || (k >= loa && k < hia), in_b = !MASKED || (k >= lob && k < hib);
-              top = in_a ? fmaxf(top, fmaf(__uint_as_float(cur[k]), ca, (float)sa)) : top;
-              top = in_b ? fmaxf(top, fmaf(__uint_as_float(cur[16 + k]), cb, (float)sb2)) : top;
-            }
-            const float m_new = fmaxf(m, top - 9.f);
-            const float f = m > -CUDART_INF_F ? exp2f(m - m_new) : 0.f;
-            sum_l *= f;
-            if (c > 0) {
-              ptx::tmem_st_wait();
-              for (int cc = 0; cc < c; ++cc) {
-                uint32_t v[16];
-                ptx::tmem_ld16(t_s + 16 * cc, v);
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                  const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&v[k]));
-                  v[k] = ptx::f16x2_rn(z.x * f, z.y * f);
-                }
-                ptx::tmem_st16(t_s + 16 * cc, v);
-              }
-            }
-            m = m_new;
-            exp_block<MASKED>(cur, ca, (float)sa - m, loa, hia, pk, ha);
-            exp_block<MASKED>(cur + 16, cb, (float)sb2 - m, lob, hib, pk + 8, hb);
+          for (int k = 0; k < 16; k += 2) {
+            float x, y;
+            ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), f2), x, y);
+            v[k] = __float_as_uint(x);
+            v[k + 1] = __float_as_uint(y);
           }
-          sum_l = fmaf(ha, pow2f(-sa), sum_l);
-          sum_l = fmaf(hb, pow2f(-sb2), sum_l);
-          ptx::tmem_st16(t_s + 16 * c, pk);
+          ptx::tmem_st16(t_o + 16 * c, v);
         }
       };
-      if (whole) pass(std::false_type{}); else pass(std::true_type{});
-      if (NQ == 1 && j > 0) {
-        // this tile's QK ran before the previous tile's PV: O waits for it
-        ok = page_wait(BAR(kCbOStep), (j - 1) & 1, lim, abort, a.status);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-        ptx::tc_fence_after();
-      }
-      if (__any_sync(0xffffffffu, m != m_in || eref != e_in)) {
-        const float f = m_in > -CUDART_INF_F ? exp2f(m_in - m) : (m > -CUDART_INF_F ? 0.f : 1.f);
-        l *= f;
-        if (j > 0) {
-          const float fo = e_in > -1000 ? f * pow2f(max(e_in - eref, -126)) : 0.f;
-          const uint64_t f2 = ptx::f2_pack(fo, fo);
+      // ---- weights, 64 keys at a time.  Those of keys 0-63 are handed over
+      // as soon as they are there, so that their product runs beside the
+      // rest.  The loop stays a loop: a body that fits the instruction
+      // buffers, its scores in the registers they were loaded to ----
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        const uint32_t t_h = t_s + 64 * half, mh = mt + 16 * half;
+        uint32_t pk[2][16];
+        float hat, sum;
+        auto scores = [&](uint32_t (&cur)[64]) {
+          ptx::tmem_ld64(t_h, cur);
+          if (!whole) {
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t v[32];
-            ptx::tmem_ld32(t_o + 32 * c, v);
-#pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              float x, y;
-              ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), f2), x, y);
-              v[k] = __float_as_uint(x);
-              v[k + 1] = __float_as_uint(y);
+            for (int k = 0; k < 4; ++k) {
+              const int at = at0 + 64 * half + 16 * k;
+              mask_block(cur + 16 * k, (ref.y >> (4 * half + k)) & 1u ? lo_r - at : 16, hi_r - at);
             }
-            ptx::tmem_st32(t_o + 32 * c, v);
           }
+        };
+        auto weights = [&](const uint32_t (&cur)[64]) {
+          hat = sum = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            // (a scale that underflows must not meet the -inf of a masked score)
+            const float ck = fmaxf(cq * lds_f(mh + 4 * k), 1.2e-38f);
+            float b;
+            exp_block(cur + 16 * k, ck, lds_f(mh + kMetaShift + 4 * k) - m, pk[k >> 1] + 8 * (k & 1), b);
+            hat += b;
+            sum = fmaf(b, lds_f(mh + kMetaInv + 4 * k), sum);
+          }
+        };
+        {
+          uint32_t cur[64];
+          scores(cur);
+          weights(cur);
         }
+        // past FP16 (or the first weights of all, against the lowest base): a
+        // new base, and what there is so far follows it
+        if (__builtin_expect(__any_sync(0xffffffffu, hat > 32768.0f), 0)) {
+          uint32_t cur[64];
+          scores(cur);
+          float top = kLowest;
+#pragma unroll
+          for (int k = 0; k < 64; ++k)
+            top = fmaxf(top, fmaf(__uint_as_float(cur[k]), fmaxf(cq * lds_f(mh + 4 * (k >> 4)), 1.2e-38f),
+                                  lds_f(mh + kMetaShift + 4 * (k >> 4))));
+          const float m_new = fmaxf(m, top - 9.f), f = exp2f(m - m_new);
+          m = m_new;
+          l *= f;
+          fo *= f;
+          weights(cur);
+        }
+        l += sum;
+        // over the first 32 of the 64 score columns just read
+        ptx::tmem_st16(t_h, pk[0]);
+        ptx::tmem_st16(t_h + 16, pk[1]);
+        if (NQ == 1 && half == 0 && j > 0) {
+          // this tile's QK ran before the previous tile's PV: O waits for it
+          ok = __all_sync(0xffffffffu, page_wait(BAR(kCbOStep), (j - 1) & 1, lim, abort, a.status));
+          ptx::tc_fence_after();
+        }
+        if (__any_sync(0xffffffffu, fo != 1.f)) {
+          if (half == 1) {
+            // O holds the first half's product already: once that is done
+            ok = __all_sync(0xffffffffu, ok && page_wait(BAR(kCbHalf + q), j & 1, lim, abort, a.status));
+            ptx::tc_fence_after();
+          }
+          if (j > 0 || half == 1) rescale_o();
+          fo = 1.f;
+        }
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        warp_arrive(BAR((half == 0 ? kCbP : kCbPb) + q));
       }
-      l += sum_l;
-      ptx::tmem_st_wait();
-      ptx::tc_fence_before();
-      ptx::mbar_arrive(BAR(kCbP + q));
+      if (!ok) break;
     }
 
     // ---- result ----
@@ -432,18 +469,19 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
       const uint32_t par = (j >> 1) & 1;
       if (!page_wait(BAR(kCbFullVr + s), par, lim, abort, a.status)) break;
       const int key = base + j * kTileKeys + r;
-      const bool use = key >= first && key < len && meta_ok(meta[(j & (kMetaSlots - 1)) * 8 + (r >> 4)]);
+      const uint32_t there = lds_u2(sm + C::kMeta + (j & (kMetaSlots - 1)) * kMetaBytes + kMetaRef).y;
+      const bool use = key >= first && key < len && ((there >> (r >> 4)) & 1u);
       uint4 raw[D / 16];
-      const uint8_t* src = smem + C::kVr + s * C::kKT;
+      const uint32_t src = sm + C::kVr + s * C::kKT;
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
         const int off = D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-        raw[c] = *reinterpret_cast<const uint4*>(src + off);
+        raw[c] = lds_u4(src + off);
         if (!use) raw[c] = make_uint4(0u, 0u, 0u, 0u);
       }
-      ptx::mbar_arrive(BAR(kCbEmptyVr + s));
+      warp_arrive(BAR(kCbEmptyVr + s));
       if (j >= 2 && !page_wait(BAR(kCbEmptyV + s), par ^ 1u, lim, abort, a.status)) break;
-      uint8_t* dst = smem + C::kV + s * C::kVT;
+      const uint32_t dst = sm + C::kV + s * C::kVT;
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
         const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
@@ -455,19 +493,20 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
           o.y = f16x2_of_e4m3x2((uint16_t)(w[2 * i] >> 16));
           o.z = f16x2_of_e4m3x2((uint16_t)w[2 * i + 1]);
           o.w = f16x2_of_e4m3x2((uint16_t)(w[2 * i + 1] >> 16));
-          *reinterpret_cast<uint4*>(dst + (ch >> 3) * 16384 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = o;
+          sts_u4(dst + (ch >> 3) * 16384 + r * 128 + (((ch & 7) ^ (r & 7)) << 4), o);
         }
       }
       ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(BAR(kCbFullV + s));
+      warp_arrive(BAR(kCbFullV + s));
     }
-  } else if (warp == C::kMmaWarp) {
+  } else {
+    if (warp == C::kMmaWarp) {
     // ============================= MMA =============================
     if (lane == 0) {
       constexpr uint32_t kIdS = ptx::idesc_f8kind(128, kTileKeys);
       constexpr uint32_t kIdO = ptx::idesc_f16kind(128, D, true, false);
       constexpr uint32_t kLay = D == 128 ? ptx::kLayoutSw128 : ptx::kLayoutSw64;
-      const uint32_t s_base = ptx::smem_u32(smem);
+      const uint32_t s_base = sm;
       const uint64_t d8 = ptx::smem_desc(s_base, 16, 8 * D, kLay);       // E4M3 rows of D bytes
       const uint64_t dv = ptx::smem_desc(s_base, 16384, 1024, ptx::kLayoutSw128);
       auto plus = [](uint64_t d, uint32_t off) { return d + (uint64_t)(off >> 4); };
@@ -482,12 +521,15 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
             ptx::mma_f8(dst, da + (uint64_t)(2 * k), db + (uint64_t)(2 * k), kIdS, (part > 0 || k > 0) ? 1u : 0u);
         }
       };
-      auto pv = [&](int j, int q, uint32_t p_tmem) {
+      auto pv = [&](int j, int q, int half, uint32_t p_tmem) {
         const uint64_t db = plus(dv, C::kV + (j & 1) * C::kVT);
 #pragma unroll
-        for (int k = 0; k < kTileKeys / 16; ++k)
-          ptx::mma_f16_ts(tmem + C::kTO + q * D, p_tmem + 8 * k, db + (uint64_t)((k * 2048) >> 4), kIdO,
-                          (j > 0 || k > 0) ? 1u : 0u);
+        for (int k = 0; k < kTileKeys / 32; ++k) {
+          // weights of 64 keys: 32 columns, 64 apart
+          const int kk = 4 * half + k;
+          ptx::mma_f16_ts(tmem + C::kTO + q * D, p_tmem + 64 * half + 8 * k,
+                          db + (uint64_t)((kk * 2048) >> 4), kIdO, (j > 0 || kk > 0) ? 1u : 0u);
+        }
       };
       int ks = 0;
       uint32_t kph = 0;
@@ -524,8 +566,13 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
           for (int q = 0; q < NQ && ok; ++q) {
             if (!(ok = page_wait(BAR(kCbP + q), j & 1, lim, abort, a.status))) break;
             if (q == 0 && !(ok = page_wait(BAR(kCbFullV + (j & 1)), (j >> 1) & 1, lim, abort, a.status))) break;
+            const uint32_t t_p = tmem + (NQ == 2 ? q : (j & 1)) * 128;
             ptx::tc_fence_after();
-            pv(j, q, tmem + (NQ == 2 ? q : (j & 1)) * 128);
+            pv(j, q, 0, t_p);
+            ptx::mma_commit(BAR(kCbHalf + q));
+            if (!(ok = page_wait(BAR(kCbPb + q), j & 1, lim, abort, a.status))) break;
+            ptx::tc_fence_after();
+            pv(j, q, 1, t_p);
             if (q == NQ - 1) ptx::mma_commit(BAR(kCbEmptyV + (j & 1)));
             if (NQ == 1) ptx::mma_commit(BAR(kCbOStep));
             if (NQ == 2 && more) {
@@ -542,36 +589,49 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
       page_drain(BAR(kCbODone), 0, lim);
     }
     __syncwarp();
-  } else {
+    } else if (warp == C::kMmaWarp + 1) {
     // ============================== TMA ==============================
-    const uint32_t s_base = ptx::smem_u32(smem);
+    const uint32_t s_base = sm;
     // lane k < 8: the page of keys [16 k, 16 k + 16) of a tile
-    auto look = [&](int j) -> BlockMeta {
-      BlockMeta o{-1, 0};
+    auto look = [&](int j) -> BlockPage {
+      BlockPage o{-1, -1000, -1000};
       const int key = base + j * kTileKeys + 16 * lane;
       // (a page wholly before every row's window may be gone already)
       if (j < n_t && lane < 8 && key < key_hi && ((long long)((key >> a.p.shift) + 1) << a.p.shift) > key_lo) {
         o.id = seq_page(a.s, b, key >> a.p.shift, a.p.n_pages, a.status);
         if (o.id >= 0) {
           const long long blk = (long long)o.id * heads + h;
-          o.word = (scale_exp(__ldg(a.p.scale[0] + blk)) + 64) | ((scale_exp(__ldg(a.p.scale[1] + blk)) + 64) << 8) |
-                   (1 << 16);
+          o.ek = scale_exp(__ldg(a.p.scale[0] + blk));
+          o.ev = scale_exp(__ldg(a.p.scale[1] + blk));
         }
       }
       return o;
     };
-    BlockMeta cur = look(0);
+    BlockPage cur = look(0);
+    int eref = -1000;   // largest V exponent so far
     int ks = 0, last_k = -1, last_v = -1;
     uint32_t kph = 0;
     bool ok = true;
     for (int j = 0; j < n_t; ++j) {
-      const BlockMeta nxt = look(j + 1);
+      const BlockPage nxt = look(j + 1);
       const bool box = cur.id >= 0 && ((16 * lane) & (a.p.page - 1)) == 0;
       const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, box));
       const uint32_t bytes = boxes * (uint32_t)(a.p.page * D);
       if (j >= kKStages) ok = page_wait(BAR(kCbEmptyK + ks), kph ^ 1u, lim, abort, a.status);
       if (!__all_sync(0xffffffffu, ok)) break;
-      if (lane < 8) const_cast<int*>(meta)[(j & (kMetaSlots - 1)) * 8 + lane] = cur.word;
+      {
+        const uint32_t mt = sm + C::kMeta + (j & (kMetaSlots - 1)) * kMetaBytes;
+        eref = max(eref, (int)__reduce_max_sync(0xffffffffu, cur.ev));
+        const uint32_t there = __ballot_sync(0xffffffffu, cur.id >= 0) & 255u;
+        // far smaller V scales stop at 2^-60, where FP16 drops every weight
+        const int sh = cur.id >= 0 ? max(cur.ev - eref, -60) : 0;
+        if (lane < 8) {
+          sts_f(mt + 4 * lane, cur.id >= 0 ? pow2f(cur.ek) : 1.f);
+          sts_f(mt + kMetaShift + 4 * lane, (float)sh);
+          sts_f(mt + kMetaInv + 4 * lane, pow2f(-sh));
+        }
+        if (lane == 0) sts_u2(mt + kMetaRef, (uint32_t)eref, there);
+      }
       __syncwarp();
       if (lane == 0) {
         ptx::mbar_arrive(BAR(kCbMeta + (j & (kMetaSlots - 1))));
@@ -603,6 +663,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
     for (int j = max(0, last_v - kVStages + 1); j <= last_v; ++j)
       page_drain(BAR(kCbFullVr + (j & 1)), (j >> 1) & 1, lim);
     __syncwarp();
+    }
   }
 
   ptx::tc_fence_before();
