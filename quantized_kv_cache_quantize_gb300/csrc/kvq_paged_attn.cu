@@ -15,7 +15,11 @@ namespace kvq {
 namespace {
 
 // ---- few rows: the decoding form ----
-constexpr int kDecRows = 16;
+// Rows of a cache head up to which the decoding form is taken: it reads the
+// keys once for every 16 rows, the tensor-core form works on 128 rows however
+// few there are.
+constexpr int kDecRows = 32;
+int rows_of_item(long long cap) { return cap <= 8 ? 8 : 16; }
 
 std::atomic<uint64_t> g_decode_smem[2][2], g_item_smem[2][2];
 
@@ -51,6 +55,7 @@ DecodeWs decode_ws(int sms, int batch, int rows_cap, int d) {
 
 // A CTA per (sequence, cache head): the most units an item can have are few,
 // and the items no more than two waves of CTAs.
+// (items: of all sequences and cache heads)
 bool decode_by_item(int sms, long long items, long long keys) {
   return keys <= (long long)kItemUnits * kUnit && items <= 2LL * sms;
 }
@@ -59,8 +64,9 @@ template <int D, int NT>
 kvq_status launch_decode(const PagedAttnArgs& a, cudaStream_t stream) {
   const int sms = sm_count_current();
   if (sms <= 0) return KVQ_ERR_CUDA;
-  const int rows_cap = a.max_q * a.group;
-  const long long items = (long long)a.s.batch * a.p.heads;
+  const int cap = a.max_q * a.group, rows_cap = std::min(cap, 8 * NT);
+  const int groups_cap = (cap + 8 * NT - 1) / (8 * NT);
+  const long long items = (long long)a.s.batch * a.p.heads * groups_cap;
   CUtensorMap mk, mv;
   const long long blocks = (long long)a.p.n_pages * a.p.heads;
   const int box = a.p.page < kUnit ? a.p.page : kUnit;
@@ -71,6 +77,7 @@ kvq_status launch_decode(const PagedAttnArgs& a, cudaStream_t stream) {
   DecodeArgs d{};
   d.a = a;
   d.rows_cap = rows_cap;
+  d.groups_cap = groups_cap;
   if (decode_by_item(sms, items, (long long)a.s.width * a.p.page)) {
     if (ensure_smem_limit(decode_item_kernel<D, NT>, smem, g_item_smem[D == 128][NT - 1]) != cudaSuccess ||
         launch_dependent(decode_item_kernel<D, NT>, (unsigned)items, kDecWarps * 32, smem, stream, d, mk, mv) !=
@@ -81,7 +88,7 @@ kvq_status launch_decode(const PagedAttnArgs& a, cudaStream_t stream) {
   const DecodeWs ws = decode_ws(sms, a.s.batch, rows_cap, D);
   if (a.ws_bytes < ws.bytes) return KVQ_ERR_INVALID_ARG;
   // the units there can be, from the table's width, bound the grid
-  const double most = (double)a.s.batch * a.p.heads * ((double)a.s.width * a.p.page / kUnit + 1.0);
+  const double most = (double)items * ((double)a.s.width * a.p.page / kUnit + 1.0);
   int grid = sms;
   if (most < (double)sms * kDecWarps * kMinUnits) {
     grid = (int)(most / kMinUnits) + 1;
@@ -97,7 +104,8 @@ kvq_status launch_decode(const PagedAttnArgs& a, cudaStream_t stream) {
   if (launch_dependent(decode_kernel<D, NT>, (unsigned)grid, kDecWarps * 32, smem, stream, d, mk, mv) !=
       cudaSuccess)
     return KVQ_ERR_CUDA;
-  if (launch_dependent(join_kernel<D>, (unsigned)items, kJoinWarps * 32, 0, stream, d) != cudaSuccess)
+  const long long rows = (long long)a.s.batch * a.p.heads * cap;
+  if (launch_dependent(join_kernel<D, 8 * NT>, (unsigned)rows, kJoinWarps * 32, 0, stream, d) != cudaSuccess)
     return KVQ_ERR_CUDA;
   return KVQ_OK;
 }
@@ -164,18 +172,23 @@ size_t paged_attention_workspace(int kv_heads, int q_heads, int d, int batch, lo
   if (max_q > rows) max_q = rows;
   const long long cap = (long long)max_q * (q_heads / kv_heads);
   const int sms = std::max(sm_count_current(), 1);
-  if (cap <= kDecRows)
-    return decode_by_item(sms, (long long)batch * kv_heads, keys) ? 16 : decode_ws(sms, batch, (int)cap, d).bytes;
+  if (cap <= kDecRows) {
+    const int r = rows_of_item(cap);
+    return decode_by_item(sms, (long long)batch * kv_heads * ((cap + r - 1) / r), keys)
+               ? 16
+               : decode_ws(sms, batch, (int)std::min<long long>(cap, r), d).bytes;
+  }
   int q_tiles = 0;
   return chunk_ws(split_limit(sms, chunk_tiles(batch, kv_heads, cap, &q_tiles)), rows, q_heads, d);
 }
 
 kvq_status launch_paged_attention(const PagedAttnArgs& a, cudaStream_t stream) {
   const long long cap = (long long)a.max_q * a.group;
-  if (cap > 0x3fffffffLL || (long long)a.s.batch * a.p.heads > 0x7fffffffLL) return KVQ_ERR_TOO_LARGE;
+  if (cap > 0x3fffffffLL || (long long)a.s.batch * a.p.heads > 0x7fffffffLL / (cap <= kDecRows ? kDecRows : 1))
+    return KVQ_ERR_TOO_LARGE;
   if (cap <= kDecRows) {
-    if (a.p.d == 64) return cap > 8 ? launch_decode<64, 2>(a, stream) : launch_decode<64, 1>(a, stream);
-    return cap > 8 ? launch_decode<128, 2>(a, stream) : launch_decode<128, 1>(a, stream);
+    if (a.p.d == 64) return rows_of_item(cap) > 8 ? launch_decode<64, 2>(a, stream) : launch_decode<64, 1>(a, stream);
+    return rows_of_item(cap) > 8 ? launch_decode<128, 2>(a, stream) : launch_decode<128, 1>(a, stream);
   }
   if (a.p.d == 64) return cap > 128 ? launch_chunk<64, 2>(a, stream) : launch_chunk<64, 1>(a, stream);
   return cap > 128 ? launch_chunk<128, 2>(a, stream) : launch_chunk<128, 1>(a, stream);

@@ -1,6 +1,7 @@
-// Attention over the paged cache for few query rows per sequence (up to 16
-// rows of a cache head: its group of query heads times the sequence's query
-// tokens), the form of a decoding step.
+// Attention over the paged cache for few query rows per sequence (the rows of a
+// cache head: its group of query heads times the sequence's query tokens), the
+// form of a decoding step.  Up to 8 or 16 rows are an item; more rows are items
+// of their own, which find the keys in L2.
 //
 // Per (sequence, cache head): s_j = c q . k_j, one pass over the keys with the
 // running maximum and sum of the softmax.  The keys are read once for all
@@ -64,16 +65,19 @@ struct DecodeArgs {
   long long* pre;      // [batch + 1] first unit of each sequence (written by CTA 0)
   float* part_o;       // [2 warps][rows_cap][D]
   float* part_ml;      // [2 warps][rows_cap][2]
-  int rows_cap;        // max_q * group
+  int rows_cap;        // rows of an item at most: min(max_q * group, 8 NT)
+  int groups_cap;      // items per cache head at most
   int warps;           // of the grid
 };
 
-// What sequence b has to do: rows, keys [lo, hi) that any row attends to
-// (lo rounded down to a unit), units of one head.
+// What sequence b has to do: its rows, keys [lo, len) that any row attends to
+// (lo rounded down to a unit), units of an item, items of a cache head.
 struct SeqWork {
-  int r0, n, len, lo, units;
+  int r0, n, len, lo, units, groups;
   int seen;   // first key some row attends to; lo is this rounded down
 };
+// R: rows of an item
+template <int R>
 __device__ __forceinline__ SeqWork seq_work(const PagedAttnArgs& a, int b) {
   SeqWork w;
   seq_rows(a.s, b, w.r0, w.n, a.status);
@@ -87,6 +91,7 @@ __device__ __forceinline__ SeqWork seq_work(const PagedAttnArgs& a, int b) {
   w.lo = w.seen & ~(kUnit - 1);
   // a sequence with rows has one unit at least: it writes their empty result
   w.units = w.n > 0 ? max(1, (w.len - w.lo + kUnit - 1) / kUnit) : 0;
+  w.groups = (w.n * a.group + R - 1) / R;
   return w;
 }
 
@@ -126,13 +131,13 @@ struct Ring {
   uint32_t phase;
 };
 
-// One segment: units [i0, i0 + seg) of (b, h), by one warp.  o, m, l: for the
-// rows nt * 8 + 2 t + c (c = 0, 1) the channels CH g .. of sum p v (channel
+// One segment: units [i0, i0 + seg) of rows rb .. of (b, h), by one warp.  o, m,
+// l: for the rows rb + nt * 8 + 2 t + c (c = 0, 1) the channels CH g .. of sum p v (channel
 // 2 k + i in o[nt][k][c + 2 i]), the base in units of log 2 and sum p.  False
 // when a wait ran out.
 template <int D, int NT>
 __device__ __forceinline__ bool decode_segment(const PagedAttnArgs& a, const CUtensorMap& map_k,
-                                               const CUtensorMap& map_v, Ring& rg, int b, int h,
+                                               const CUtensorMap& map_v, Ring& rg, int b, int h, int rb,
                                                const SeqWork& w, int i0, int seg,
                                                float (&o)[NT][D / 16][4], float (&m)[NT][2],
                                                float (&l)[NT][2]) {
@@ -210,7 +215,7 @@ __device__ __forceinline__ bool decode_segment(const PagedAttnArgs& a, const CUt
   int lo_r[NT][2], hi_r[NT][2];   // keys each column's row attends to
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int r = nt * 8 + g;
+    const int r = rb + nt * 8 + g;
     uint2 raw[KC * 4];
 #pragma unroll
     for (int k = 0; k < KC * 4; ++k) raw[k] = make_uint2(0u, 0u);
@@ -251,7 +256,7 @@ __device__ __forceinline__ bool decode_segment(const PagedAttnArgs& a, const CUt
       // column 2t + c is the row whose lanes have g = 2t + c
       const int ec = __shfl_sync(0xffffffffu, e, (2 * t + c) * 4);
       cq[nt][c] = scale_log2 * pow2f(ec / 2) * pow2f(ec - ec / 2);
-      const int rc = nt * 8 + 2 * t + c;
+      const int rc = rb + nt * 8 + 2 * t + c;
       const int tq = t0 + rc / a.group;
       hi_r[nt][c] = rc < rows ? (a.causal ? min(w.len, tq + 1) : w.len) : 0;
       lo_r[nt][c] = a.window > 0 ? max(0, tq - a.window + 1) : 0;
@@ -516,7 +521,10 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
   auto scan = [&](int c0, long long carry) -> long long {
     const int b = c0 + (int)threadIdx.x;
     long long v = 0;
-    if (b < a.s.batch) v = (long long)seq_work(a, b).units * heads;
+    if (b < a.s.batch) {
+      const SeqWork x = seq_work<8 * NT>(a, b);
+      v = (long long)x.units * x.groups * heads;
+    }
     long long incl = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -572,18 +580,19 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
 
   Ring rg{ring, bars, 0, 0u};
   SeqWork w{};
-  if (u0 < u1) w = seq_work(a, b);
-  int h = 0, i0 = 0;
+  if (u0 < u1) w = seq_work<8 * NT>(a, b);
+  int item = 0, i0 = 0;   // the sequence's items: (head, row group)
   if (u0 < u1) {
-    h = (int)((u0 - at) / w.units);
+    item = (int)((u0 - at) / w.units);
     i0 = (int)((u0 - at) % w.units);
   }
   for (long long u = u0; u < u1;) {
     const int seg = (int)min((long long)(w.units - i0), u1 - u);
     float o[NT][D / 16][4], m[NT][2], l[NT][2];
-    if (!decode_segment<D, NT>(a, map_k, map_v, rg, b, h, w, i0, seg, o, m, l)) break;
+    const int h = item / w.groups, rb = item % w.groups * (8 * NT);
+    if (!decode_segment<D, NT>(a, map_k, map_v, rg, b, h, rb, w, i0, seg, o, m, l)) break;
     // ---- its result: the item's, or a part of it ----
-    const int rows = w.n * a.group;
+    const int rows = min(w.n * a.group - rb, 8 * NT);
     const bool complete = seg == w.units;
     const long long slot = 2LL * gw + (u == u0 ? 0 : 1);
 #pragma unroll
@@ -593,7 +602,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
         const int r = nt * 8 + 2 * t + c;
         if (r >= rows) continue;
         if (complete) {
-          store_row<D, NT>(a, w, h, r, o, nt, c, m[nt][c], l[nt][c]);
+          store_row<D, NT>(a, w, h, rb + r, o, nt, c, m[nt][c], l[nt][c]);
         } else {
           float4* dst = reinterpret_cast<float4*>(p.part_o + (slot * p.rows_cap + r) * D + CH * g);
 #pragma unroll
@@ -606,11 +615,11 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
     // ---- the next segment ----
     u += seg;
     i0 = 0;
-    if (u < u1 && ++h == heads) {
-      h = 0;
+    if (u < u1 && ++item == heads * w.groups) {
+      item = 0;
       do {
         ++b;
-        w = seq_work(a, b);
+        w = seq_work<8 * NT>(a, b);
       } while (w.units == 0 && b + 1 < a.s.batch);
       if (w.units == 0) break;   // not with lengths that hold still during the call
     }
@@ -640,14 +649,17 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
   }
   __syncwarp();
   ptx::grid_dependency_wait();
-  const int b = (int)(blockIdx.x / (unsigned)a.p.heads), h = (int)(blockIdx.x % (unsigned)a.p.heads);
-  const SeqWork w = seq_work(a, b);
-  if (w.units == 0) return;
+  const int rb = (int)(blockIdx.x % (unsigned)p.groups_cap) * (8 * NT);
+  const unsigned bh = blockIdx.x / (unsigned)p.groups_cap;
+  const int b = (int)(bh / (unsigned)a.p.heads), h = (int)(bh % (unsigned)a.p.heads);
+  const SeqWork w = seq_work<8 * NT>(a, b);
+  const int rows = min(w.n * a.group - rb, 8 * NT);
+  if (w.units == 0 || rows <= 0) return;
   const int i0 = w.units * wid / kDecWarps, i1 = w.units * (wid + 1) / kDecWarps;
   float o[NT][D / 16][4], m[NT][2], l[NT][2];
   bool ok = true;
   if (i1 > i0) {
-    ok = decode_segment<D, NT>(a, map_k, map_v, rg, b, h, w, i0, i1 - i0, o, m, l);
+    ok = decode_segment<D, NT>(a, map_k, map_v, rg, b, h, rb, w, i0, i1 - i0, o, m, l);
   } else {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -666,7 +678,6 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
       if (g == 0) ml_s[wid][nt * 8 + 2 * t + c] = make_float2(m[nt][c], l[nt][c]);
   // no copy of any warp is in flight once all are here: the rings are free
   if (__syncthreads_or(!ok)) return;
-  const int rows = w.n * a.group;
   float* part = reinterpret_cast<float*>(smem);   // [warp][row][D]
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -698,7 +709,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) v[c] = fmaf(part[(k * NT * 8 + r) * D + (D / 32) * lane + c], f, v[c]);
     }
-    const long long row = (long long)(w.r0 + r / a.group) * a.q_heads + h * a.group + r % a.group;
+    const int rr = rb + r;
+    const long long row = (long long)(w.r0 + rr / a.group) * a.q_heads + h * a.group + rr % a.group;
     if (!KVQ_IN_BOUNDS(row, (long long)a.s.rows * a.q_heads, a.status, a.bounds_site)) continue;
     const float f = ls > 0.f ? 1.f / ls : 0.f;
 #pragma unroll
@@ -711,72 +723,73 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
   }
 }
 
-// Joins the parts of items that several warps covered: one block per
-// (sequence, cache head), per row the largest maximum, then sums weighted by
-// 2^(m - M), the parts in order.  32 lanes hold the row's channels, the
-// block's warps take every eighth part.
-constexpr int kJoinWarps = 8;
-template <int D>
+// Joins the parts of items that several warps covered: one block per row of a
+// (sequence, cache head), the largest maximum, then sums weighted by
+// 2^(m - M), the parts in order.  The block's warps take every fourth part, 32
+// lanes hold the channels.
+constexpr int kJoinWarps = 4;
+template <int D, int R>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ DecodeArgs p) {
   constexpr int C = D / 32;
   __shared__ float sum_o[kJoinWarps][D];
   __shared__ float sum_l[kJoinWarps], top_m[kJoinWarps];
   ptx::grid_dependency_wait();
   const PagedAttnArgs& a = p.a;
-  const int heads = a.p.heads, b = blockIdx.x / heads, h = blockIdx.x % heads;
-  const long long s0 = p.pre[b], units = (p.pre[b + 1] - s0) / heads, total = p.pre[a.s.batch];
-  if (units == 0) return;
-  const long long per = max((total + p.warps - 1) / p.warps, (long long)kMinUnits);
-  const long long first = s0 + h * units;
-  const long long wa = first / per, wb = (first + units - 1) / per;
-  if (wa == wb) return;
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int heads = a.p.heads, cap = a.max_q * a.group;
+  const int r = (int)(blockIdx.x % (unsigned)cap);
+  const unsigned bh = blockIdx.x / (unsigned)cap;
+  const int b = (int)(bh / (unsigned)heads), h = (int)(bh % (unsigned)heads);
   int r0, n;
   seq_rows(a.s, b, r0, n, a.status);
   n = min(n, a.max_q);
-  for (int r = 0; r < n * a.group; ++r) {
-    auto slot = [&](long long w) { return (2 * w + (w == wa && first > wa * per ? 1 : 0)) * p.rows_cap + r; };
-    float top = -CUDART_INF_F;
-    for (long long w = wa + threadIdx.x; w <= wb; w += kJoinWarps * 32) top = fmaxf(top, p.part_ml[slot(w) * 2]);
+  const int groups = (n * a.group + R - 1) / R;
+  if (r >= n * a.group) return;
+  const long long s0 = p.pre[b], units = (p.pre[b + 1] - s0) / (heads * groups), total = p.pre[a.s.batch];
+  const long long per = max((total + p.warps - 1) / p.warps, (long long)kMinUnits);
+  const long long first = s0 + (h * groups + r / R) * units;
+  const long long wa = first / per, wb = (first + units - 1) / per;
+  if (wa == wb) return;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  auto slot = [&](long long w) { return (2 * w + (w == wa && first > wa * per ? 1 : 0)) * p.rows_cap + r % R; };
+  float top = -CUDART_INF_F;
+  for (long long w = wa + threadIdx.x; w <= wb; w += kJoinWarps * 32) top = fmaxf(top, p.part_ml[slot(w) * 2]);
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    if (lane == 0) top_m[wid] = top;
-    __syncthreads();
+  for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+  if (lane == 0) top_m[wid] = top;
+  __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kJoinWarps; ++k) top = fmaxf(top, top_m[k]);
-    const float base = top > -CUDART_INF_F ? top : 0.f;
-    float o[C], ls = 0.f;
+  for (int k = 0; k < kJoinWarps; ++k) top = fmaxf(top, top_m[k]);
+  const float base = top > -CUDART_INF_F ? top : 0.f;
+  float o[C], ls = 0.f;
 #pragma unroll
-    for (int c = 0; c < C; ++c) o[c] = 0.f;
-    for (long long w = wa + wid; w <= wb; w += kJoinWarps) {
-      const long long at = slot(w);
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
-      const float f = ptx::ex2_approx(ml.x - base);
-      ls = fmaf(ml.y, f, ls);
+  for (int c = 0; c < C; ++c) o[c] = 0.f;
+#pragma unroll 4
+  for (long long w = wa + wid; w <= wb; w += kJoinWarps) {
+    const long long at = slot(w);
+    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
+    const float f = ptx::ex2_approx(ml.x - base);
+    ls = fmaf(ml.y, f, ls);
 #pragma unroll
-      for (int c = 0; c < C; ++c) o[c] = fmaf(p.part_o[at * D + lane + 32 * c], f, o[c]);
-    }
-#pragma unroll
-    for (int c = 0; c < C; ++c) sum_o[wid][lane + 32 * c] = o[c];
-    if (lane == 0) sum_l[wid] = ls;
-    __syncthreads();
-    ls = 0.f;
-#pragma unroll
-    for (int k = 0; k < kJoinWarps; ++k) ls += sum_l[k];
-    const long long row = (long long)(r0 + r / a.group) * a.q_heads + h * a.group + r % a.group;
-    if (KVQ_IN_BOUNDS(row, (long long)a.s.rows * a.q_heads, a.status, a.bounds_site)) {
-      for (int c = threadIdx.x; c < D; c += kJoinWarps * 32) {
-        float v = 0.f;
-#pragma unroll
-        for (int k = 0; k < kJoinWarps; ++k) v += sum_o[k][c];
-        const __nv_bfloat16 z = __float2bfloat16_rn(ls > 0.f ? v / ls : 0.f);
-        a.out[row * D + c] = *reinterpret_cast<const uint16_t*>(&z);
-      }
-      if (threadIdx.x == 0 && a.lse != nullptr)
-        a.lse[row] = ls > 0.f ? 0.6931471805599453f * (top + log2f(ls)) : -CUDART_INF_F;
-    }
-    __syncthreads();
+    for (int c = 0; c < C; ++c) o[c] = fmaf(p.part_o[at * D + lane + 32 * c], f, o[c]);
   }
+#pragma unroll
+  for (int c = 0; c < C; ++c) sum_o[wid][lane + 32 * c] = o[c];
+  if (lane == 0) sum_l[wid] = ls;
+  __syncthreads();
+  ls = 0.f;
+#pragma unroll
+  for (int k = 0; k < kJoinWarps; ++k) ls += sum_l[k];
+  const long long row = (long long)(r0 + r / a.group) * a.q_heads + h * a.group + r % a.group;
+  if (!KVQ_IN_BOUNDS(row, (long long)a.s.rows * a.q_heads, a.status, a.bounds_site)) return;
+  for (int c = threadIdx.x; c < D; c += kJoinWarps * 32) {
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < kJoinWarps; ++k) v += sum_o[k][c];
+    const __nv_bfloat16 z = __float2bfloat16_rn(ls > 0.f ? v / ls : 0.f);
+    a.out[row * D + c] = *reinterpret_cast<const uint16_t*>(&z);
+  }
+  if (threadIdx.x == 0 && a.lse != nullptr)
+    a.lse[row] = ls > 0.f ? 0.6931471805599453f * (top + log2f(ls)) : -CUDART_INF_F;
 }
 
 }  // namespace
