@@ -21,7 +21,18 @@ namespace {
 constexpr int kDecRows = 32;
 int rows_of_item(long long cap) { return cap <= 8 ? 8 : 16; }
 
-std::atomic<uint64_t> g_decode_smem[2][2], g_item_smem[2][2];
+std::atomic<uint64_t> g_decode_smem[2][2], g_decode12_smem[2], g_item_smem[2][2];
+
+// Warps of the decoding form, per CTA.  Twelve hide more of the latency of
+// products and votes than eight where every warp has a long run of keys
+// (103 against 119 us: 32 sequences of 16384 keys, 8 heads of 64 channels);
+// with short runs the larger CTA's start costs more (19.6 against 17.1 us: 16
+// of 4096, 4 heads).  Two column tiles have no registers for twelve.
+constexpr int kDecWarps = 8, kDecWarpsLong = 12, kLongUnits = 16;
+int decode_warps(int sms, int row_tiles, double units) {
+  return row_tiles == 1 && units >= (double)kLongUnits * kDecWarps * sms ? kDecWarpsLong : kDecWarps;
+}
+double decode_units(long long items, long long keys) { return (double)items * ((double)keys / kUnit + 1.0); }
 
 template <typename... Args>
 cudaError_t launch_dependent(void (*kern)(Args...), unsigned grid, int threads, int smem,
@@ -43,9 +54,9 @@ cudaError_t launch_dependent(void (*kern)(Args...), unsigned grid, int threads, 
 struct DecodeWs {
   size_t pre, ml, o, bytes;
 };
-DecodeWs decode_ws(int sms, int batch, int rows_cap, int d) {
+DecodeWs decode_ws(int warps, int batch, int rows_cap, int d) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  const size_t slots = 2 * (size_t)sms * kDecWarps * rows_cap;
+  const size_t slots = 2 * (size_t)warps * rows_cap;
   DecodeWs w{};
   w.ml = up(((size_t)batch + 1) * 8);
   w.o = w.ml + up(slots * 8);
@@ -73,37 +84,45 @@ kvq_status launch_decode(const PagedAttnArgs& a, cudaStream_t stream) {
   if (!make_pages_map(&mk, a.p.codes[0], D, a.p.page, blocks, box) ||
       !make_pages_map(&mv, a.p.codes[1], D, a.p.page, blocks, box))
     return KVQ_ERR_CUDA;
-  const int smem = DecCfg<D>::kAlloc;
+  const int smem = DecCfg<D, kDecWarps>::kAlloc;
   DecodeArgs d{};
   d.a = a;
   d.rows_cap = rows_cap;
   d.groups_cap = groups_cap;
   if (decode_by_item(sms, items, (long long)a.s.width * a.p.page)) {
-    if (ensure_smem_limit(decode_item_kernel<D, NT>, smem, g_item_smem[D == 128][NT - 1]) != cudaSuccess ||
-        launch_dependent(decode_item_kernel<D, NT>, (unsigned)items, kDecWarps * 32, smem, stream, d, mk, mv) !=
-            cudaSuccess)
+    const auto kern = decode_item_kernel<D, NT, kDecWarps>;
+    if (ensure_smem_limit(kern, smem, g_item_smem[D == 128][NT - 1]) != cudaSuccess ||
+        launch_dependent(kern, (unsigned)items, kDecWarps * 32, smem, stream, d, mk, mv) != cudaSuccess)
       return KVQ_ERR_CUDA;
     return KVQ_OK;
   }
-  const DecodeWs ws = decode_ws(sms, a.s.batch, rows_cap, D);
-  if (a.ws_bytes < ws.bytes) return KVQ_ERR_INVALID_ARG;
   // the units there can be, from the table's width, bound the grid
-  const double most = (double)items * ((double)a.s.width * a.p.page / kUnit + 1.0);
+  const double most = decode_units(items, (long long)a.s.width * a.p.page);
+  const int warps = decode_warps(sms, NT, most);
+  const DecodeWs ws = decode_ws(sms * warps, a.s.batch, rows_cap, D);
+  if (a.ws_bytes < ws.bytes) return KVQ_ERR_INVALID_ARG;
   int grid = sms;
-  if (most < (double)sms * kDecWarps * kMinUnits) {
-    grid = (int)(most / kMinUnits) + 1;
-    if (grid > sms) grid = sms;
-  }
+  if (most < (double)sms * warps * kMinUnits) grid = std::min((int)(most / kMinUnits) + 1, sms);
   uint8_t* base = static_cast<uint8_t*>(a.ws);
   d.pre = reinterpret_cast<long long*>(base + ws.pre);
   d.part_ml = reinterpret_cast<float*>(base + ws.ml);
   d.part_o = reinterpret_cast<float*>(base + ws.o);
-  d.warps = grid * kDecWarps;
-  if (ensure_smem_limit(decode_kernel<D, NT>, smem, g_decode_smem[D == 128][NT - 1]) != cudaSuccess)
-    return KVQ_ERR_CUDA;
-  if (launch_dependent(decode_kernel<D, NT>, (unsigned)grid, kDecWarps * 32, smem, stream, d, mk, mv) !=
-      cudaSuccess)
-    return KVQ_ERR_CUDA;
+  d.warps = grid * warps;
+  if constexpr (NT == 1) {
+    if (warps == kDecWarpsLong) {
+      const auto kern = decode_kernel<D, NT, kDecWarpsLong>;
+      const int bytes = DecCfg<D, kDecWarpsLong>::kAlloc;
+      if (ensure_smem_limit(kern, bytes, g_decode12_smem[D == 128]) != cudaSuccess ||
+          launch_dependent(kern, (unsigned)grid, kDecWarpsLong * 32, bytes, stream, d, mk, mv) != cudaSuccess)
+        return KVQ_ERR_CUDA;
+    }
+  }
+  if (warps == kDecWarps) {
+    const auto kern = decode_kernel<D, NT, kDecWarps>;
+    if (ensure_smem_limit(kern, smem, g_decode_smem[D == 128][NT - 1]) != cudaSuccess ||
+        launch_dependent(kern, (unsigned)grid, kDecWarps * 32, smem, stream, d, mk, mv) != cudaSuccess)
+      return KVQ_ERR_CUDA;
+  }
   const long long rows = (long long)a.s.batch * a.p.heads * cap;
   if (launch_dependent(join_kernel<D, 8 * NT>, (unsigned)rows, kJoinWarps * 32, 0, stream, d) != cudaSuccess)
     return KVQ_ERR_CUDA;
@@ -174,9 +193,10 @@ size_t paged_attention_workspace(int kv_heads, int q_heads, int d, int batch, lo
   const int sms = std::max(sm_count_current(), 1);
   if (cap <= kDecRows) {
     const int r = rows_of_item(cap);
-    return decode_by_item(sms, (long long)batch * kv_heads * ((cap + r - 1) / r), keys)
-               ? 16
-               : decode_ws(sms, batch, (int)std::min<long long>(cap, r), d).bytes;
+    const long long items = (long long)batch * kv_heads * ((cap + r - 1) / r);
+    if (decode_by_item(sms, items, keys)) return 16;
+    return decode_ws(sms * decode_warps(sms, r / 8, decode_units(items, keys)), batch,
+                     (int)std::min<long long>(cap, r), d).bytes;
   }
   int q_tiles = 0;
   return chunk_ws(split_limit(sms, chunk_tiles(batch, kv_heads, cap, &q_tiles)), rows, q_heads, d);

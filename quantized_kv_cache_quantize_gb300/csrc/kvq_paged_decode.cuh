@@ -26,7 +26,9 @@
 // fragment of four k-steps (the query fragment permuted alike), and two rows'
 // bytes interleaved by one byte permute are the V^T fragment.  A tcgen05
 // product would need the codes converted and stored to shared memory again
-// for a tile that has 16 of 128 rows filled.
+// for a tile that has 16 of 128 rows filled.  E4M3 products (m16n8k32, the
+// query in high and low parts) would spare the conversion of K, but measured
+// slower: 249 against 188 us for 16 rows, 32 sequences of 16384 keys, 8 heads.
 //
 // Numbers.  E4M3 codes are exact in FP16.  A query row is scaled by a power of
 // two to a largest magnitude in [2^14, 2^15), exact in FP16 down to 2^-39 of
@@ -44,19 +46,19 @@
 namespace kvq {
 namespace {
 
-constexpr int kDecWarps = 8;       // per CTA, one CTA per SM
 constexpr int kUnit = 32;          // keys per unit
 constexpr int kMinUnits = 2;       // per warp, when the work is small
 constexpr int kItemUnits = 32;     // of an item at most, for a CTA of its own
-constexpr int kScan = kDecWarps * 32;
 
-template <int D>
+// W warps per CTA, one CTA per SM
+template <int D, int W>
 struct DecCfg {
+  static constexpr int kWarps = W;
   static constexpr int kHalf = kUnit * D;                 // K (or V) rows of a unit
   static constexpr int kStage = 2 * kHalf;
-  static constexpr int kStages = 24576 / kStage;          // per warp: 24 KB of copies in flight
-  static constexpr int kBar = kDecWarps * kStages * kStage;
-  static constexpr int kBytes = kBar + kDecWarps * kStages * 8;
+  static constexpr int kStages = 196608 / (kWarps * kStage);   // per warp; 192 KB in all
+  static constexpr int kBar = kWarps * kStages * kStage;
+  static constexpr int kBytes = kBar + kWarps * kStages * 8;
   static constexpr int kAlloc = kBytes + 1024;
 };
 
@@ -97,7 +99,7 @@ __device__ __forceinline__ SeqWork seq_work(const PagedAttnArgs& a, int b) {
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -135,13 +137,13 @@ struct Ring {
 // l: for the rows rb + nt * 8 + 2 t + c (c = 0, 1) the channels CH g .. of sum p v (channel
 // 2 k + i in o[nt][k][c + 2 i]), the base in units of log 2 and sum p.  False
 // when a wait ran out.
-template <int D, int NT>
+template <int D, int NT, int W>
 __device__ __forceinline__ bool decode_segment(const PagedAttnArgs& a, const CUtensorMap& map_k,
                                                const CUtensorMap& map_v, Ring& rg, int b, int h, int rb,
                                                const SeqWork& w, int i0, int seg,
                                                float (&o)[NT][D / 16][4], float (&m)[NT][2],
                                                float (&l)[NT][2]) {
-  using C = DecCfg<D>;
+  using C = DecCfg<D, W>;
   constexpr int KC = D / 64;       // 16-byte chunks of a key row per lane
   constexpr int MT = D / 16;       // channel tiles of the output
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, heads = a.p.heads;
@@ -153,6 +155,27 @@ __device__ __forceinline__ bool decode_segment(const PagedAttnArgs& a, const CUt
   const int key_first = w.lo + i0 * kUnit;
   const int key_end = min(w.len, w.lo + (i0 + seg) * kUnit);
   const int t0 = w.len - w.n;
+  // ---- the query rows' loads, first: their latency runs beside the table's ----
+  uint2 raw[NT][KC * 4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = rb + nt * 8 + g;
+#pragma unroll
+    for (int k = 0; k < KC * 4; ++k) raw[nt][k] = make_uint2(0u, 0u);
+    if (r < rows) {
+      const int i = r / a.group, hq = h * a.group + r % a.group;
+      const uint16_t* qp = a.q + (long long)(w.r0 + i) * a.q_row_stride + (long long)hq * a.q_head_stride;
+#pragma unroll
+      for (int k = 0; k < KC; ++k) {
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const uint4 x = __ldg(reinterpret_cast<const uint4*>(qp + 16 * (t + 4 * k)) + v);
+          raw[nt][4 * k + 2 * v] = make_uint2(x.x, x.y);
+          raw[nt][4 * k + 2 * v + 1] = make_uint2(x.z, x.w);
+        }
+      }
+    }
+  }
   // pages, 32 at a time, one per lane: id (-1: none), exponents of K and V
   const int shift = a.p.shift;
   const int page_end = (max(key_end, key_first) + a.p.page - 1) >> shift;
@@ -215,28 +238,11 @@ __device__ __forceinline__ bool decode_segment(const PagedAttnArgs& a, const CUt
   int lo_r[NT][2], hi_r[NT][2];   // keys each column's row attends to
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int r = rb + nt * 8 + g;
-    uint2 raw[KC * 4];
-#pragma unroll
-    for (int k = 0; k < KC * 4; ++k) raw[k] = make_uint2(0u, 0u);
-    if (r < rows) {
-      const int i = r / a.group, hq = h * a.group + r % a.group;
-      const uint16_t* qp = a.q + (long long)(w.r0 + i) * a.q_row_stride + (long long)hq * a.q_head_stride;
-#pragma unroll
-      for (int k = 0; k < KC; ++k) {
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const uint4 x = __ldg(reinterpret_cast<const uint4*>(qp + 16 * (t + 4 * k)) + v);
-          raw[4 * k + 2 * v] = make_uint2(x.x, x.y);
-          raw[4 * k + 2 * v + 1] = make_uint2(x.z, x.w);
-        }
-      }
-    }
     uint32_t mx = 0;   // largest magnitude, as its bits
 #pragma unroll
     for (int k = 0; k < KC * 4; ++k) {
-      mx = max(mx, max(max((raw[k].x & 0x7fffu), (raw[k].x >> 16) & 0x7fffu),
-                       max((raw[k].y & 0x7fffu), (raw[k].y >> 16) & 0x7fffu)));
+      mx = max(mx, max(max((raw[nt][k].x & 0x7fffu), (raw[nt][k].x >> 16) & 0x7fffu),
+                       max((raw[nt][k].y & 0x7fffu), (raw[nt][k].y >> 16) & 0x7fffu)));
     }
     mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
@@ -246,10 +252,8 @@ __device__ __forceinline__ bool decode_segment(const PagedAttnArgs& a, const CUt
     const float f0 = pow2f(-(e / 2)), f1 = pow2f(-(e - e / 2));
 #pragma unroll
     for (int k = 0; k < KC * 4; ++k) {
-      qf[nt][k][0] = ptx::f16x2_rn(__uint_as_float(raw[k].x << 16) * f0 * f1,
-                                   __uint_as_float(raw[k].x & 0xffff0000u) * f0 * f1);
-      qf[nt][k][1] = ptx::f16x2_rn(__uint_as_float(raw[k].y << 16) * f0 * f1,
-                                   __uint_as_float(raw[k].y & 0xffff0000u) * f0 * f1);
+      qf[nt][k][0] = ptx::f16x2_rn(__uint_as_float(raw[nt][k].x << 16) * f0 * f1, __uint_as_float(raw[nt][k].x & 0xffff0000u) * f0 * f1);
+      qf[nt][k][1] = ptx::f16x2_rn(__uint_as_float(raw[nt][k].y << 16) * f0 * f1, __uint_as_float(raw[nt][k].y & 0xffff0000u) * f0 * f1);
     }
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
@@ -493,14 +497,15 @@ __device__ __forceinline__ void store_row(const PagedAttnArgs& a, const SeqWork&
   if (g == 0 && a.lse != nullptr) a.lse[row] = l > 0.f ? 0.6931471805599453f * (m + log2f(l)) : -CUDART_INF_F;
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kDecWarps * 32, 1)
+template <int D, int NT, int W>
+__global__ void __launch_bounds__(W * 32, 1)
     decode_kernel(const __grid_constant__ DecodeArgs p, const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v) {
-  using C = DecCfg<D>;
+  using C = DecCfg<D, W>;
   constexpr int CH = D / 8;        // output channels per lane
   extern __shared__ uint8_t smem_raw[];
-  __shared__ long long scan_warp[kDecWarps];
+  __shared__ long long scan_warp[C::kWarps];
+  constexpr int kScan = C::kWarps * 32;
   __shared__ long long pre_s[kScan + 1];
   const PagedAttnArgs& a = p.a;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
@@ -536,7 +541,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
     __syncthreads();
     long long before = carry, all = carry;
 #pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) {
+    for (int w = 0; w < C::kWarps; ++w) {
       if (w < wid) before += scan_warp[w];
       all += scan_warp[w];
     }
@@ -590,7 +595,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
     const int seg = (int)min((long long)(w.units - i0), u1 - u);
     float o[NT][D / 16][4], m[NT][2], l[NT][2];
     const int h = item / w.groups, rb = item % w.groups * (8 * NT);
-    if (!decode_segment<D, NT>(a, map_k, map_v, rg, b, h, rb, w, i0, seg, o, m, l)) break;
+    if (!decode_segment<D, NT, W>(a, map_k, map_v, rg, b, h, rb, w, i0, seg, o, m, l)) break;
     // ---- its result: the item's, or a part of it ----
     const int rows = min(w.n * a.group - rb, 8 * NT);
     const bool complete = seg == w.units;
@@ -629,14 +634,14 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
 // Short sequences: a CTA per item, the item's units divided among its warps and
 // joined in shared memory.  No scan of the batch, no workspace, one launch:
 // what counts there is the latency of one pass.
-template <int D, int NT>
-__global__ void __launch_bounds__(kDecWarps * 32, 1)
+template <int D, int NT, int W>
+__global__ void __launch_bounds__(W * 32, 1)
     decode_item_kernel(const __grid_constant__ DecodeArgs p, const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v) {
-  using C = DecCfg<D>;
+  using C = DecCfg<D, W>;
   constexpr int CH = D / 8;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ float2 ml_s[kDecWarps][NT * 8];
+  __shared__ float2 ml_s[C::kWarps][NT * 8];
   const PagedAttnArgs& a = p.a;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -655,11 +660,11 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
   const SeqWork w = seq_work<8 * NT>(a, b);
   const int rows = min(w.n * a.group - rb, 8 * NT);
   if (w.units == 0 || rows <= 0) return;
-  const int i0 = w.units * wid / kDecWarps, i1 = w.units * (wid + 1) / kDecWarps;
+  const int i0 = w.units * wid / C::kWarps, i1 = w.units * (wid + 1) / C::kWarps;
   float o[NT][D / 16][4], m[NT][2], l[NT][2];
   bool ok = true;
   if (i1 > i0) {
-    ok = decode_segment<D, NT>(a, map_k, map_v, rg, b, h, rb, w, i0, i1 - i0, o, m, l);
+    ok = decode_segment<D, NT, W>(a, map_k, map_v, rg, b, h, rb, w, i0, i1 - i0, o, m, l);
   } else {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -692,17 +697,17 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
     }
   __syncthreads();
   // a warp per row, the parts in order
-  for (int r = wid; r < rows; r += kDecWarps) {
+  for (int r = wid; r < rows; r += C::kWarps) {
     float top = -CUDART_INF_F;
 #pragma unroll
-    for (int k = 0; k < kDecWarps; ++k) top = fmaxf(top, ml_s[k][r].x);
+    for (int k = 0; k < C::kWarps; ++k) top = fmaxf(top, ml_s[k][r].x);
     const float base = top > -CUDART_INF_F ? top : 0.f;
     float ls = 0.f, v[D / 32];
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) v[c] = 0.f;
 #pragma unroll
-    for (int k = 0; k < kDecWarps; ++k) {
-      if (w.units * (k + 1) / kDecWarps <= w.units * k / kDecWarps) continue;   // a warp without units
+    for (int k = 0; k < C::kWarps; ++k) {
+      if (w.units * (k + 1) / C::kWarps <= w.units * k / C::kWarps) continue;   // a warp without units
       const float2 ml = ml_s[k][r];
       const float f = ptx::ex2_approx(ml.x - base);
       ls = fmaf(ml.y, f, ls);

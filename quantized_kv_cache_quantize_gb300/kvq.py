@@ -596,8 +596,10 @@ def paged_attention(cache: PagedCache, q: torch.Tensor, block_table: torch.Tenso
     if q_heads < 1 or q_heads % cache.kv_heads:
         raise ValueError(f"q has {q_heads} heads, not a multiple of the cache's {cache.kv_heads}")
     s = _sequences(cache, rows, block_table, kv_lens, offsets)
-    if max_q is None:
-        max_q = 1 if offsets is None else rows
+    if offsets is None:
+        max_q = 1
+    elif max_q is None:
+        max_q = rows
     dev = cache.device
     handle = _handle(stream, dev)
     if out is not None:
