@@ -61,6 +61,7 @@ struct ChunkCfg {
   static constexpr int kSoftmaxWarps = 4 * NQ;
   static constexpr int kMmaWarp = kSoftmaxWarps + 4;
   static constexpr int kThreads = (kSoftmaxWarps + 6) * 32;
+  static constexpr bool kHalves = NQ == 2;         // weights handed over by halves
   static constexpr int kTO = 256;                  // O tiles behind two score buffers
   static constexpr int kTCols = 512;
   static_assert(kTO + NQ * D <= kTCols, "tensor memory");
@@ -243,10 +244,14 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
     const int q = warp >> 2;
     const int r = (warp & 3) * 32 + lane;        // TMEM lane, row of the query tile
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const int row = row0 + q * 128 + r;          // of the head's rows
-    const bool live = row < rows;
-    const int tok = live ? row / a.group : 0;
-    const int hq = h * a.group + (live ? row % a.group : 0);
+    // row of the head's rows; one past the last repeats it and is not stored
+    const bool live = row0 + q * 128 + r < rows;
+    const int row = min(row0 + q * 128 + r, rows - 1);
+    const int tok = row / a.group;
+    const int hq = h * a.group + row % a.group;
+    // a warp without a row of its own only keeps the barriers going: its
+    // lanes of the products go nowhere
+    const bool idle = row0 + q * 128 + (warp & 3) * 32 >= rows;
     // ---- the query row: scale, split, store (K-major, swizzled) ----
     float cq;
     {
@@ -254,7 +259,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
       const uint4* qp = reinterpret_cast<const uint4*>(a.q + (long long)(r0 + tok) * a.q_row_stride +
                                                        (long long)hq * a.q_head_stride);
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) raw[c] = live ? __ldg(qp + c) : make_uint4(0u, 0u, 0u, 0u);
+      for (int c = 0; c < D / 8; ++c) raw[c] = __ldg(qp + c);
       uint32_t mx = 0;
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) {
@@ -289,10 +294,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
     ptx::fence_proxy_async_smem();
     warp_arrive(BAR(kCbQ));
 
-    // keys this row attends to (rows past the last: none), from the first
-    // key of local tile 0
+    // keys this row attends to, from the first key of local tile 0
     const int tq = t0 + tok;
-    const int hi_r = (live ? (a.causal ? min(len, tq + 1) : len) : 0) - base;
+    const int hi_r = (a.causal ? min(len, tq + 1) : len) - base;
     const int lo_r = (a.window > 0 ? max(0, tq - a.window + 1) : 0) - base;
     float m = kLowest, l = 0.f;
     int eref = -1000;
@@ -311,6 +315,14 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
         break;
       }
       ptx::tc_fence_after();
+      if (idle) {
+        if (NQ == 1 && j > 0)
+          ok = __all_sync(0xffffffffu, page_wait(BAR(kCbOStep), (j - 1) & 1, lim, abort, a.status));
+        if (C::kHalves) warp_arrive(BAR(kCbP + q));
+        warp_arrive(BAR(kCbPb + q));
+        if (!ok) break;
+        continue;
+      }
       const uint32_t mt = sm + C::kMeta + (j & (kMetaSlots - 1)) * kMetaBytes;
       const uint2 ref = lds_u2(mt + kMetaRef);
       const int at0 = j * kTileKeys;
@@ -386,28 +398,47 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
           l *= f;
           fo *= f;
           weights(cur);
+          if (!C::kHalves && half == 1) {   // the first half's, still here
+            ptx::tmem_st_wait();
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+              uint32_t v[16];
+              ptx::tmem_ld16(t_s + 16 * c, v);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&v[k]));
+                v[k] = ptx::f16x2_rn(z.x * f, z.y * f);
+              }
+              ptx::tmem_st16(t_s + 16 * c, v);
+            }
+          }
         }
         l += sum;
         // over the first 32 of the 64 score columns just read
         ptx::tmem_st16(t_h, pk[0]);
         ptx::tmem_st16(t_h + 16, pk[1]);
-        if (NQ == 1 && half == 0 && j > 0) {
-          // this tile's QK ran before the previous tile's PV: O waits for it
-          ok = __all_sync(0xffffffffu, page_wait(BAR(kCbOStep), (j - 1) & 1, lim, abort, a.status));
-          ptx::tc_fence_after();
-        }
         if (__any_sync(0xffffffffu, fo != 1.f)) {
-          if (half == 1) {
-            // O holds the first half's product already: once that is done
+          // O is held by products still to be waited for: with NQ = 1 the
+          // previous tile's (this tile's QK ran before it), with halves
+          // handed over the first half's
+          if (NQ == 1 && j > 0) {
+            ok = __all_sync(0xffffffffu, ok && page_wait(BAR(kCbOStep), (j - 1) & 1, lim, abort, a.status));
+          } else if (C::kHalves && half == 1) {
             ok = __all_sync(0xffffffffu, ok && page_wait(BAR(kCbHalf + q), j & 1, lim, abort, a.status));
-            ptx::tc_fence_after();
           }
-          if (j > 0 || half == 1) rescale_o();
+          ptx::tc_fence_after();
+          if (j > 0 || (C::kHalves && half == 1)) rescale_o();
           fo = 1.f;
         }
-        ptx::tmem_st_wait();
-        ptx::tc_fence_before();
-        warp_arrive(BAR((half == 0 ? kCbP : kCbPb) + q));
+        if (C::kHalves || half == 1) {
+          // NQ = 1: the previous tile's weights are consumed before these
+          // are announced (the barrier must not run two phases ahead)
+          if (NQ == 1 && j > 0)
+            ok = __all_sync(0xffffffffu, ok && page_wait(BAR(kCbOStep), (j - 1) & 1, lim, abort, a.status));
+          ptx::tmem_st_wait();
+          ptx::tc_fence_before();
+          warp_arrive(BAR((C::kHalves && half == 0 ? kCbP : kCbPb) + q));
+        }
       }
       if (!ok) break;
     }
@@ -549,6 +580,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
         ptx::tc_fence_after();
         ok = next_k();
         if (ok) {
+#pragma unroll
           for (int q = 0; q < NQ; ++q) {
             qk(ks, q, tmem + q * 128);
             ptx::mma_commit(BAR(kCbS + q));
@@ -563,15 +595,20 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
             ptx::mma_commit(BAR(kCbS + ((j + 1) & 1)));
             step_k();
           }
-          for (int q = 0; q < NQ && ok; ++q) {
-            if (!(ok = page_wait(BAR(kCbP + q), j & 1, lim, abort, a.status))) break;
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) {
+            if (!ok) break;
+            if (C::kHalves && !(ok = page_wait(BAR(kCbP + q), j & 1, lim, abort, a.status))) break;
             if (q == 0 && !(ok = page_wait(BAR(kCbFullV + (j & 1)), (j >> 1) & 1, lim, abort, a.status))) break;
             const uint32_t t_p = tmem + (NQ == 2 ? q : (j & 1)) * 128;
-            ptx::tc_fence_after();
-            pv(j, q, 0, t_p);
-            ptx::mma_commit(BAR(kCbHalf + q));
+            if (C::kHalves) {
+              ptx::tc_fence_after();
+              pv(j, q, 0, t_p);
+              ptx::mma_commit(BAR(kCbHalf + q));
+            }
             if (!(ok = page_wait(BAR(kCbPb + q), j & 1, lim, abort, a.status))) break;
             ptx::tc_fence_after();
+            if (!C::kHalves) pv(j, q, 0, t_p);
             pv(j, q, 1, t_p);
             if (q == NQ - 1) ptx::mma_commit(BAR(kCbEmptyV + (j & 1)));
             if (NQ == 1) ptx::mma_commit(BAR(kCbOStep));
@@ -579,7 +616,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
               if (q == 0 && !(ok = next_k())) break;
               qk(ks, q, tmem + q * 128);
               ptx::mma_commit(BAR(kCbS + q));
-              if (q == 1) step_k();
+              if (q == NQ - 1) step_k();
             }
           }
         }
@@ -592,12 +629,14 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
     } else if (warp == C::kMmaWarp + 1) {
     // ============================== TMA ==============================
     const uint32_t s_base = sm;
-    // lane k < 8: the page of keys [16 k, 16 k + 16) of a tile
+    // pages of four tiles at a time, lane 8 i + k that of keys [16 k, 16 k +
+    // 16) of tile j + i: two dependent loads, issued four tiles ahead of
+    // their use (one tile at a time they bound the whole kernel)
     auto look = [&](int j) -> BlockPage {
       BlockPage o{-1, -1000, -1000};
       const int key = base + j * kTileKeys + 16 * lane;
       // (a page wholly before every row's window may be gone already)
-      if (j < n_t && lane < 8 && key < key_hi && ((long long)((key >> a.p.shift) + 1) << a.p.shift) > key_lo) {
+      if (j + (lane >> 3) < n_t && key < key_hi && ((long long)((key >> a.p.shift) + 1) << a.p.shift) > key_lo) {
         o.id = seq_page(a.s, b, key >> a.p.shift, a.p.n_pages, a.status);
         if (o.id >= 0) {
           const long long blk = (long long)o.id * heads + h;
@@ -607,13 +646,22 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
       }
       return o;
     };
-    BlockPage cur = look(0);
+    BlockPage four = look(0), next_four = look(4);
     int eref = -1000;   // largest V exponent so far
     int ks = 0, last_k = -1, last_v = -1;
     uint32_t kph = 0;
     bool ok = true;
     for (int j = 0; j < n_t; ++j) {
-      const BlockPage nxt = look(j + 1);
+      if (j > 0 && (j & 3) == 0) {
+        four = next_four;
+        next_four = look(j + 4);
+      }
+      const int from = 8 * (j & 3) + (lane & 7);
+      BlockPage cur;
+      cur.id = __shfl_sync(0xffffffffu, four.id, from);
+      cur.ek = __shfl_sync(0xffffffffu, four.ek, from);
+      cur.ev = __shfl_sync(0xffffffffu, four.ev, from);
+      if (lane >= 8) cur.id = -1;
       const bool box = cur.id >= 0 && ((16 * lane) & (a.p.page - 1)) == 0;
       const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, box));
       const uint32_t bytes = boxes * (uint32_t)(a.p.page * D);
@@ -622,7 +670,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
       {
         const uint32_t mt = sm + C::kMeta + (j & (kMetaSlots - 1)) * kMetaBytes;
         eref = max(eref, (int)__reduce_max_sync(0xffffffffu, cur.ev));
-        const uint32_t there = __ballot_sync(0xffffffffu, cur.id >= 0) & 255u;
+        const uint32_t there = __ballot_sync(0xffffffffu, cur.id >= 0);
         // far smaller V scales stop at 2^-60, where FP16 drops every weight
         const int sh = cur.id >= 0 ? max(cur.ev - eref, -60) : 0;
         if (lane < 8) {
@@ -655,7 +703,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
         ks = 0;
         kph ^= 1u;
       }
-      cur = nxt;
     }
     // no copy is in flight when the CTA exits, however the others ended
     for (int j = max(0, last_k - kKStages + 1); j <= last_k; ++j)
