@@ -34,23 +34,6 @@ int decode_warps(int sms, int row_tiles, double units) {
 }
 double decode_units(long long items, long long keys) { return (double)items * ((double)keys / kUnit + 1.0); }
 
-template <typename... Args>
-cudaError_t launch_dependent(void (*kern)(Args...), unsigned grid, int threads, int smem,
-                             cudaStream_t stream, Args... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  note_launch();
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 struct DecodeWs {
   size_t pre, ml, o, bytes;
 };

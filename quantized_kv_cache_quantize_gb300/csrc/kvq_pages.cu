@@ -17,12 +17,7 @@ __device__ __forceinline__ bool append_item(const AppendArgs& a, int item, int& 
                                             int& first, int& end) {
   const PageSeqs& s = a.s;
   int n;
-  if (s.offsets == nullptr) {
-    b = item;
-    r0 = b;
-    n = 1;
-    p = 0;
-  } else {
+  {
     int lo = 0, hi = s.batch - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -43,69 +38,176 @@ __device__ __forceinline__ bool append_item(const AppendArgs& a, int item, int& 
   return (p << a.p.shift) < end;
 }
 
-// one warp per page, head and K or V
+// Earlier codes [row][D] of rows [0, lo) under a scale grown by 2^-shift
+// (shift < 0), by the threads of the block.
 template <int D>
-__global__ void __launch_bounds__(64) append_kernel(const AppendArgs a) {
-  constexpr int C = D / 32;
-  const int lane = threadIdx.x & 31, kv = threadIdx.x >> 5;
-  const int head = blockIdx.x % a.p.heads;
+__device__ __forceinline__ void rescale_codes(uint8_t* codes, int lo, int shift, int tid, int threads) {
+  const float f = pow2f(shift);
+  uint2* c = reinterpret_cast<uint2*>(codes);
+  for (int i = tid; i < lo * (D / 8); i += threads) {
+    uint2 w = c[i];
+    uint32_t* v = &w.x;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t a = f16x2_of_e4m3x2((uint16_t)v[k]), b = f16x2_of_e4m3x2((uint16_t)(v[k] >> 16));
+      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a));
+      const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&b));
+      v[k] = e4m3x4(x.x * f, x.y * f, y.x * f, y.y * f);
+    }
+    c[i] = w;
+  }
+}
+
+// largest magnitude of 8 BF16 values, as its bits (they order like the values;
+// an infinity or a NaN comes out above every finite number)
+__device__ __forceinline__ uint32_t max_bits(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) m = max(m, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+  return m;
+}
+__device__ __forceinline__ uint2 codes_of(const uint4& v, float f) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t o[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    o[k] = e4m3x4(__uint_as_float(w[2 * k] << 16) * f, __uint_as_float(w[2 * k] & 0xffff0000u) * f,
+                  __uint_as_float(w[2 * k + 1] << 16) * f, __uint_as_float(w[2 * k + 1] & 0xffff0000u) * f);
+  return make_uint2(o[0], o[1]);
+}
+// the largest value of the block that the scale rule sees: beyond the code
+// range (or not finite) it is recorded and the codes saturate
+__device__ __forceinline__ int scale_of(uint32_t bits, int* status) {
+  const float m = __uint_as_float(bits << 16);
+  if (!in_code_range(m)) {
+    atomicCAS(status, 0, (int)KVQ_ERR_RANGE);
+    return kPageExpMax;
+  }
+  return exp_for_max(m);
+}
+
+// Many new tokens.  One block per page, head and K or V, 32 values a thread in
+// flight: 3 bytes of traffic per value and next to no work, bound by HBM
+// (each value read once, its codes written once; the page's maximum has to be
+// known before the first code, so the values wait in registers for it).
+template <int D>
+__global__ void __launch_bounds__(512) append_kernel(const __grid_constant__ AppendArgs a) {
+  constexpr int C = D / 8;             // 16-byte chunks of a row
+  __shared__ uint32_t part[16];
+  const int tid = threadIdx.x, lane = tid & 31;
+  ptx::grid_dependency_wait();
+  const int kv = blockIdx.x & 1, hi_ = blockIdx.x >> 1;
+  const int head = hi_ % a.p.heads;
   int b, p, r0, first, end;
-  if (!append_item(a, blockIdx.x / a.p.heads, b, p, r0, first, end)) return;
+  if (!append_item(a, hi_ / a.p.heads, b, p, r0, first, end)) return;
   const int id = seq_page(a.s, b, p, a.p.n_pages, a.status);
   if (id < 0) return;
   const int t0 = p << a.p.shift;
   const int lo = max(first - t0, 0), hi = min(end - t0, a.p.page);
   const long long blk = (long long)id * a.p.heads + head;
-  uint8_t* codes = a.p.codes[kv] + blk * a.p.page * D + C * lane;
-  const uint16_t* x = a.x[kv] + (r0 + (t0 - first)) * a.row_stride[kv] + head * a.head_stride[kv] + C * lane;
-  float m = 0.f;
-  bool fine = true;
-  for (int t = lo; t < hi; ++t)
-    for (int c = 0; c < C; ++c) {
-      const float v = fabsf(__uint_as_float((uint32_t)__ldg(x + t * a.row_stride[kv] + c) << 16));
-      m = fmaxf(m, v);
-      fine &= in_code_range(v);
-    }
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (!fine) atomicCAS(a.status, 0, (int)KVQ_ERR_RANGE);
-  int e = exp_for_max(m);
-  if (lo > 0) {
-    const int old = scale_exp(a.p.scale[kv][blk]);
-    if (e > old) {
-      const float f = pow2f(old - e);
-      for (int t = 0; t < lo; ++t)
-        for (int c = 0; c < C; c += 2) {
-          const uint32_t h = f16x2_of_e4m3x2(*reinterpret_cast<uint16_t*>(codes + t * D + c));
-          const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
-          *reinterpret_cast<uint16_t*>(codes + t * D + c) = (uint16_t)e4m3x4(v.x * f, v.y * f, 0.f, 0.f);
-        }
-    }
-    e = max(e, old);
+  if (!KVQ_IN_BOUNDS(blk, (long long)a.p.n_pages * a.p.heads, a.status, a.bounds_site)) return;
+  uint8_t* codes = a.p.codes[kv] + blk * a.p.page * D;
+  const int c = tid % C, step = blockDim.x / C;      // page / 4 rows at a time
+  const uint16_t* x = a.x[kv] + (long long)(r0 + (t0 - first)) * a.row_stride[kv] + head * a.head_stride[kv] + 8 * c;
+  uint4 v[4];
+  uint32_t m = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int t = tid / C + k * step;
+    v[k] = t >= lo && t < hi ? __ldg(reinterpret_cast<const uint4*>(x + t * a.row_stride[kv])) : make_uint4(0u, 0u, 0u, 0u);
   }
-  __syncwarp();
-  if (lane == 0) a.p.scale[kv][blk] = scale_bits(e);
+  const int old = lo > 0 ? scale_exp(a.p.scale[kv][blk]) : kPageExpMin;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) m = max(m, max_bits(v[k]));
+  m = __reduce_max_sync(0xffffffffu, m);
+  if (blockDim.x > 32) {
+    if (lane == 0) part[tid >> 5] = m;
+    __syncthreads();
+    m = __reduce_max_sync(0xffffffffu, lane < (int)(blockDim.x >> 5) ? part[lane] : 0u);
+  }
+  const int e = max(scale_of(m, a.status), old);
+  if (lo > 0 && e > old) rescale_codes<D>(codes, lo, old - e, tid, blockDim.x);
+  if (tid == 0) a.p.scale[kv][blk] = scale_bits(e);
   const float f = pow2f(-e);
-  for (int t = lo; t < hi; ++t)
-    for (int c = 0; c < C; c += 2) {
-      const float v0 = __uint_as_float((uint32_t)__ldg(x + t * a.row_stride[kv] + c) << 16);
-      const float v1 = __uint_as_float((uint32_t)__ldg(x + t * a.row_stride[kv] + c + 1) << 16);
-      *reinterpret_cast<uint16_t*>(codes + t * D + c) = (uint16_t)e4m3x4(v0 * f, v1 * f, 0.f, 0.f);
-    }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int t = tid / C + k * step;
+    if (t >= lo && t < hi) *reinterpret_cast<uint2*>(codes + t * D + 8 * c) = codes_of(v[k], f);
+  }
+}
+
+// One token of every sequence: a warp per sequence, head and K or V, D / 8
+// lanes of it with values.  What counts is the chain of dependent loads:
+// length, table entry, then scale and row together.
+template <int D>
+__global__ void __launch_bounds__(128) append_one_kernel(const __grid_constant__ AppendArgs a) {
+  const int lane = threadIdx.x & 31;
+  ptx::grid_dependency_wait();
+  const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int kv = (int)(w & 1), head = (int)((w >> 1) % a.p.heads);
+  const long long item = (w >> 1) / a.p.heads;
+  if (item >= a.s.batch) return;
+  const int b = (int)item;
+  const bool has = lane < D / 8;
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  if (has) v = __ldg(reinterpret_cast<const uint4*>(a.x[kv] + b * a.row_stride[kv] + head * a.head_stride[kv] + 8 * lane));
+  const int len = seq_len(a.s, b, a.p.shift, a.status);
+  if (len < 1) {
+    page_error(a.status);     // a new token, but no place for it
+    return;
+  }
+  const int p = (len - 1) >> a.p.shift, t = (len - 1) & (a.p.page - 1);
+  const int id = seq_page(a.s, b, p, a.p.n_pages, a.status);
+  if (id < 0) return;
+  const long long blk = (long long)id * a.p.heads + head;
+  if (!KVQ_IN_BOUNDS(blk, (long long)a.p.n_pages * a.p.heads, a.status, a.bounds_site)) return;
+  uint8_t* codes = a.p.codes[kv] + blk * a.p.page * D;
+  const int old = t > 0 ? scale_exp(a.p.scale[kv][blk]) : kPageExpMin;
+  const uint32_t m = __reduce_max_sync(0xffffffffu, max_bits(v));
+  const int e = max(scale_of(m, a.status), old);
+  if (t > 0 && e > old) rescale_codes<D>(codes, t, old - e, lane, 32);
+  if (lane == 0 && (t == 0 || e > old)) a.p.scale[kv][blk] = scale_bits(e);
+  if (has) *reinterpret_cast<uint2*>(codes + t * D + 8 * lane) = codes_of(v, pow2f(-e));
 }
 
 // ---- copies ---------------------------------------------------------------
 
-// one page of one layer, by all threads of the block
-__device__ __forceinline__ void copy_page(const PagePool& p, int layer, int src, int dst) {
-  const long long from = (long long)layer * p.n_pages + src, to = (long long)layer * p.n_pages + dst;
+// Copies, bound by HBM (each byte read and written once).  The unit of work is
+// 16 KB of one page's K or V in one layer, four 16-byte loads a thread in
+// flight before the first store, so that the blocks of one resident wave
+// finish together whatever the number of pages (whole pages a block left a
+// fifth of the wave idle at 495 pages x 8 layers: 176 us).
+constexpr int kCopyThreads = 256, kCopyUnit = kCopyThreads * 4;   // in 16-byte vectors
+__host__ __device__ __forceinline__ long long copy_units(const PagePool& p, long long pages) {
+  const long long segs = (p.page_bytes / 16 + kCopyUnit - 1) / kCopyUnit;
+  return pages * p.layers * 2 * segs;
+}
+// unit u of `n` pages: pages in the order pair(k, &src, &dst)
+template <typename Pair>
+__device__ __forceinline__ void copy_unit(const PagePool& p, long long u, int n, Pair pair) {
+  const int segs = (int)((p.page_bytes / 16 + kCopyUnit - 1) / kCopyUnit);
+  const int seg = (int)(u % segs);
+  u /= segs;
+  const int kv = (int)(u & 1);
+  u >>= 1;
+  int src, dst;
+  pair((int)(u % n), &src, &dst);
+  const long long layer = u / n;
+  const long long from = layer * p.n_pages + src, to = layer * p.n_pages + dst;
+  const uint4* s = reinterpret_cast<const uint4*>(p.codes[kv] + from * p.page_bytes);
+  uint4* d = reinterpret_cast<uint4*>(p.codes[kv] + to * p.page_bytes);
+  const int end = (int)(p.page_bytes / 16), at = seg * kCopyUnit + threadIdx.x;
+  uint4 v[4];
 #pragma unroll
-  for (int kv = 0; kv < 2; ++kv) {
-    const uint4* s = reinterpret_cast<const uint4*>(p.codes[kv] + from * p.page_bytes);
-    uint4* d = reinterpret_cast<uint4*>(p.codes[kv] + to * p.page_bytes);
-    for (long long i = threadIdx.x; i < p.page_bytes / 16; i += blockDim.x) d[i] = s[i];
-    for (int h = threadIdx.x; h < p.heads; h += blockDim.x)
+  for (int k = 0; k < 4; ++k)
+    if (at + k * kCopyThreads < end) v[k] = s[at + k * kCopyThreads];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (at + k * kCopyThreads < end) d[at + k * kCopyThreads] = v[k];
+  if (seg == 0)
+    for (int h = threadIdx.x; h < p.heads; h += kCopyThreads)
       p.scale[kv][to * p.heads + h] = p.scale[kv][from * p.heads + h];
-  }
 }
 
 // (src, dst) pairs as kernel parameters: no upload, and nothing that must
@@ -117,20 +219,25 @@ struct CopyArgs {
   int32_t src[kCopyPairs], dst[kCopyPairs];
 };
 
-__global__ void __launch_bounds__(256) copy_kernel(const __grid_constant__ CopyArgs a) {
-  for (long long i = blockIdx.x; i < (long long)a.n * a.pool.layers; i += gridDim.x) {
-    const int pair = (int)(i % a.n);
-    copy_page(a.pool, (int)(i / a.n), a.src[pair], a.dst[pair]);
-  }
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyArgs a) {
+  ptx::grid_dependency_wait();
+  const long long total = copy_units(a.pool, a.n);
+  for (long long u = blockIdx.x; u < total; u += gridDim.x)
+    copy_unit(a.pool, u, a.n, [&](int k, int* src, int* dst) {
+      *src = a.src[k];
+      *dst = a.dst[k];
+    });
 }
 
 // ---- compaction -------------------------------------------------------------
 // The plan, one block: a bitmap of the live pages in shared memory, the number
 // of live pages below each of its words, then holes and movers paired by rank.
 constexpr int kPlanThreads = 1024;
-__global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const CompactArgs a) {
+__global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const __grid_constant__ CompactArgs a) {
   extern __shared__ uint32_t bits[];
   __shared__ int warp_sum[kPlanThreads / 32];
+  ptx::grid_dependency_wait();
+  ptx::launch_dependents();
   const int n_pages = a.pool.n_pages, words = (n_pages + 31) / 32;
   const int tid = threadIdx.x, lane = tid & 31;
   for (int i = tid; i < words; i += kPlanThreads) bits[i] = 0u;
@@ -204,7 +311,8 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const Compac
   }
 }
 
-__global__ void __launch_bounds__(256) compact_apply_kernel(const CompactArgs a) {
+__global__ void __launch_bounds__(kCopyThreads) compact_apply_kernel(const __grid_constant__ CompactArgs a) {
+  ptx::grid_dependency_wait();
   const int n_pages = a.pool.n_pages;
   const int moves = a.ws[0], n_live = *a.n_live;
   const int32_t* src = a.ws + 4;
@@ -217,10 +325,12 @@ __global__ void __launch_bounds__(256) compact_apply_kernel(const CompactArgs a)
     const int id = a.table[row * a.stride + col];
     a.table_out[row * a.out_stride + col] = id >= n_live && id < n_pages ? to[id] : id;
   }
-  for (long long i = blockIdx.x; i < (long long)moves * a.pool.layers; i += gridDim.x) {
-    const int k = (int)(i % moves);
-    copy_page(a.pool, (int)(i / moves), src[k], dst[k]);
-  }
+  const long long units = copy_units(a.pool, moves);
+  for (long long u = blockIdx.x; u < units; u += gridDim.x)
+    copy_unit(a.pool, u, moves, [&](int k, int* from, int* into) {
+      *from = src[k];
+      *into = dst[k];
+    });
 }
 
 std::atomic<uint64_t> g_plan_smem{0};
@@ -235,13 +345,18 @@ int sm_count_current() {
 }
 
 cudaError_t launch_pages_append(const AppendArgs& a, cudaStream_t stream) {
-  const long long items = a.s.offsets == nullptr ? a.s.batch : (a.s.rows >> a.p.shift) + 2LL * a.s.batch;
-  const long long grid = items * a.p.heads;
-  if (grid == 0) return cudaSuccess;
-  if (a.p.d == 64) append_kernel<64><<<(unsigned)grid, 64, 0, stream>>>(a);
-  else append_kernel<128><<<(unsigned)grid, 64, 0, stream>>>(a);
-  note_launch();
-  return cudaGetLastError();
+  const bool one = a.s.offsets == nullptr;
+  const long long items = one ? a.s.batch : (a.s.rows >> a.p.shift) + 2LL * a.s.batch;
+  const long long units = items * a.p.heads * 2;
+  if (units == 0) return cudaSuccess;
+  if (one) {
+    const unsigned grid = (unsigned)((units + 3) / 4);
+    return a.p.d == 64 ? launch_dependent(append_one_kernel<64>, grid, 128, 0, stream, a)
+                       : launch_dependent(append_one_kernel<128>, grid, 128, 0, stream, a);
+  }
+  const int threads = a.p.page * a.p.d / 32;
+  return a.p.d == 64 ? launch_dependent(append_kernel<64>, (unsigned)units, threads, 0, stream, a)
+                     : launch_dependent(append_kernel<128>, (unsigned)units, threads, 0, stream, a);
 }
 
 cudaError_t launch_pages_copy(const PagePool& p, const int32_t* src, const int32_t* dst, int n,
@@ -256,11 +371,8 @@ cudaError_t launch_pages_copy(const PagePool& p, const int32_t* src, const int32
       a.src[i] = src[at + i];
       a.dst[i] = dst[at + i];
     }
-    long long grid = (long long)a.n * p.layers;
-    if (grid > 8LL * sms) grid = 8LL * sms;
-    copy_kernel<<<(unsigned)grid, 256, 0, stream>>>(a);
-    note_launch();
-    const cudaError_t e = cudaGetLastError();
+    const long long units = copy_units(p, a.n), most = 8LL * sms;
+    const cudaError_t e = launch_dependent(copy_kernel, (unsigned)(units < most ? units : most), kCopyThreads, 0, stream, a);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -272,13 +384,9 @@ cudaError_t launch_pages_compact(const CompactArgs& a, cudaStream_t stream) {
   const int smem = (a.pool.n_pages + 31) / 32 * 4;
   cudaError_t e = ensure_smem_limit(compact_plan_kernel, kCompactMaxPages / 8, g_plan_smem);
   if (e != cudaSuccess) return e;
-  compact_plan_kernel<<<1, kPlanThreads, smem, stream>>>(a);
-  note_launch();
-  e = cudaGetLastError();
+  e = launch_dependent(compact_plan_kernel, 1u, kPlanThreads, smem, stream, a);
   if (e != cudaSuccess) return e;
-  compact_apply_kernel<<<(unsigned)(8 * sms), 256, 0, stream>>>(a);
-  note_launch();
-  return cudaGetLastError();
+  return launch_dependent(compact_apply_kernel, (unsigned)(8 * sms), kCopyThreads, 0, stream, a);
 }
 
 }  // namespace kvq

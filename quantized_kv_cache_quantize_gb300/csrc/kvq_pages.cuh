@@ -13,6 +13,25 @@
 namespace kvq {
 namespace {
 
+// Launch that may start while the stream's previous kernel finishes (the
+// kernel waits for it before its first global access).
+template <typename... Args>
+cudaError_t launch_dependent(void (*kern)(Args...), unsigned grid, int threads, int smem,
+                             cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  note_launch();
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Bounded wait on an mbarrier phase: false when the limit ran out (recorded)
 // or `abort` (may be null) was raised by another role.
 __device__ __noinline__ bool page_wait_slow(uint32_t bar, uint32_t parity, unsigned long long limit_ns,

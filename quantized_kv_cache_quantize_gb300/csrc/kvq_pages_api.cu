@@ -114,7 +114,7 @@ kvq_status kvq_pages_append(const kvq_pages* pages, int32_t layer, const uint16_
   kvq::AppendArgs a{};
   a.p = layer_of(pages, layer);
   a.s = seqs_of(seqs);
-  if (((long long)(seqs->rows >> a.p.shift) + 2LL * seqs->batch) * pages->kv_heads >= (1LL << 31))
+  if (((long long)(seqs->rows >> a.p.shift) + 2LL * seqs->batch) * pages->kv_heads >= (1LL << 30))
     return KVQ_ERR_TOO_LARGE;
   a.x[0] = k_new;
   a.x[1] = v_new;

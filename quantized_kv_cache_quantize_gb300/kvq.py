@@ -497,12 +497,15 @@ class PagedCache:
             return int(lib().kvq_paged_workspace_bytes(self._at, q_heads, batch, width, rows, max_q))
 
 
-def _switch(device):
-    """_on_device, without the cost of a switch where none is needed: the
-    paged calls are short."""
-    if device.type != "cuda" or device.index == torch.cuda.current_device():
+def _switch(device, stream=None):
+    """_on_device and _alloc_on together, without their cost where neither is
+    needed: the paged calls are short."""
+    if device.type != "cuda" or (stream is None and device.index == torch.cuda.current_device()):
         return _NO_SWITCH
-    return torch.cuda.device(device)
+    both = contextlib.ExitStack()
+    both.enter_context(torch.cuda.device(device))
+    both.enter_context(_alloc_on(stream, device))
+    return both
 
 
 def _handle(stream, device) -> int:
@@ -607,7 +610,7 @@ def paged_attention(cache: PagedCache, q: torch.Tensor, block_table: torch.Tenso
             raise ValueError(f"out is on {out.device}, q on {dev}")
         _check_out(q, out)
     lse = None
-    with _switch(dev), _alloc_on(stream, dev):
+    with _switch(dev, stream):
         if out is None:
             out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
         if with_lse:
@@ -678,7 +681,7 @@ def pages_compact(cache: PagedCache, block_table: torch.Tensor, out=None, worksp
         if out.shape != shape:
             raise ValueError(f"out must have the shape of block_table {list(shape)}, got "
                              f"{list(out.shape)}")
-    with _switch(dev), _alloc_on(stream, dev):
+    with _switch(dev, stream):
         if out is None:
             out = torch.empty(shape, dtype=torch.int32, device=dev)
         n_live = torch.empty(1, dtype=torch.int32, device=dev)
