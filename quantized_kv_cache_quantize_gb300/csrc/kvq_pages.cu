@@ -230,81 +230,83 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
 }
 
 // ---- compaction -------------------------------------------------------------
-// The plan, one block: a bitmap of the live pages in shared memory, the number
-// of live pages below each of its words, then holes and movers paired by rank.
-constexpr int kPlanThreads = 1024;
+// The plan, one block: a bitmap of the live pages in shared memory and the
+// number of live pages below every eighth of its words; with those any page's
+// rank is a few loads away, and holes and movers are paired by rank, a page a
+// thread.  What it takes is latency (a walk over the bits of a word by one
+// thread took 11.5 us for 2000 pages).
+constexpr int kPlanThreads = 1024, kRankWords = 8;
+__host__ __device__ __forceinline__ int plan_words(int n_pages) {
+  return ((n_pages + 31) / 32 + kRankWords - 1) / kRankWords * kRankWords;
+}
+__host__ __device__ __forceinline__ int plan_bytes(int n_pages) {
+  return plan_words(n_pages) * 4 + plan_words(n_pages) / kRankWords * 4;
+}
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const __grid_constant__ CompactArgs a) {
   extern __shared__ uint32_t bits[];
   __shared__ int warp_sum[kPlanThreads / 32];
   ptx::grid_dependency_wait();
   ptx::launch_dependents();
-  const int n_pages = a.pool.n_pages, words = (n_pages + 31) / 32;
+  const int n_pages = a.pool.n_pages, words = plan_words(n_pages), groups = words / kRankWords;
+  int* below = reinterpret_cast<int*>(bits + words);   // [groups] live pages before the group
   const int tid = threadIdx.x, lane = tid & 31;
   for (int i = tid; i < words; i += kPlanThreads) bits[i] = 0u;
   __syncthreads();
   const long long total = (long long)a.batch * a.width;
+#pragma unroll 4
   for (long long i = tid; i < total; i += kPlanThreads) {
     const int id = __ldg(a.table + (i / a.width) * a.stride + i % a.width);
     if (id >= n_pages) page_error(a.status);
     if (id >= 0 && id < n_pages) atomicOr(bits + (id >> 5), 1u << (id & 31));
   }
   __syncthreads();
-  // each thread's run of words, and the live pages before it
-  const int per = (words + kPlanThreads - 1) / kPlanThreads;
-  const int w0 = min(tid * per, words), w1 = min(w0 + per, words);
+  // each thread's run of groups, and the live pages before it
+  const int per = (groups + kPlanThreads - 1) / kPlanThreads;
+  const int g0 = min(tid * per, groups), g1 = min(g0 + per, groups);
   int mine = 0;
-  for (int w = w0; w < w1; ++w) mine += __popc(bits[w]);
+  for (int w = g0 * kRankWords; w < g1 * kRankWords; ++w) mine += __popc(bits[w]);
   int incl = mine;
+#pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
   }
   if (lane == 31) warp_sum[tid >> 5] = incl;
   __syncthreads();
-  int before = incl - mine, n_live = 0;
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
-    if (w < (tid >> 5)) before += warp_sum[w];
-    n_live += warp_sum[w];
+  int all = warp_sum[lane];                // every warp scans the warps' sums
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, all, o);
+    if (lane >= o) all += v;
   }
+  const int n_live = __shfl_sync(0xffffffffu, all, 31);
+  int before = __shfl_sync(0xffffffffu, all, (tid >> 5) - 1 & 31);
+  before = (tid < 32 ? 0 : before) + incl - mine;
+  for (int g = g0; g < g1; ++g) {
+    below[g] = before;
+    for (int w = g * kRankWords; w < (g + 1) * kRankWords; ++w) before += __popc(bits[w]);
+  }
+  __syncthreads();
+  auto rank = [&](int id) {                // live pages below id (id < 32 * words)
+    const int w = id >> 5;
+    int r = below[w / kRankWords] + __popc(bits[w] & ((1u << (id & 31)) - 1u));
+    for (int k = w & ~(kRankWords - 1); k < w; ++k) r += __popc(bits[k]);
+    return r;
+  };
+  auto live = [&](int id) { return ((bits[id >> 5] >> (id & 31)) & 1u) != 0u; };
   int32_t* src = a.ws + 4;
   int32_t* dst = src + n_pages;
   int32_t* to = dst + n_pages;
-  // holes below n_live, by rank (ids before it that are not live)
-  int live = before;
-  for (int w = w0; w < w1; ++w) {
-    const uint32_t v = bits[w];
-    for (uint32_t h = ~v; h != 0u; h &= h - 1u) {
-      const int bit = __ffs((int)h) - 1, id = 32 * w + bit;
-      if (id < n_live) dst[id - (live + __popc(v & ((1u << bit) - 1u)))] = id;
-    }
-    live += __popc(v);
-  }
-  // live pages below n_live, and so the rank of the first mover
-  __shared__ int kept;
-  if (tid == 0) kept = 0;
+  const int kept = n_live < n_pages ? rank(n_live) : n_live;
+  for (int id = tid; id < n_live; id += kPlanThreads)
+    if (!live(id)) dst[id - rank(id)] = id;
   __syncthreads();
-  int below = 0;
-  for (int w = w0; w < w1; ++w) {
-    const int id = 32 * w;
-    const uint32_t m = id + 32 <= n_live ? ~0u : id >= n_live ? 0u : (1u << (n_live - id)) - 1u;
-    below += __popc(bits[w] & m);
-  }
-  for (int o = 16; o > 0; o >>= 1) below += __shfl_xor_sync(0xffffffffu, below, o);
-  if (lane == 0 && below != 0) atomicAdd(&kept, below);
-  __syncthreads();
-  live = before;
-  for (int w = w0; w < w1; ++w) {
-    const uint32_t v = bits[w];
-    for (uint32_t h = v; h != 0u; h &= h - 1u) {
-      const int bit = __ffs((int)h) - 1, id = 32 * w + bit;
-      if (id >= n_live) {
-        const int rank = live + __popc(v & ((1u << bit) - 1u)) - kept;
-        src[rank] = id;
-        to[id] = dst[rank];
-      }
+  for (int id = n_live + tid; id < n_pages; id += kPlanThreads)
+    if (live(id)) {
+      const int r = rank(id) - kept, into = dst[r];
+      src[r] = id;
+      to[id] = into;
     }
-    live += __popc(v);
-  }
   if (tid == 0) {
     a.ws[0] = n_live - kept;
     *a.n_live = n_live;
@@ -381,8 +383,8 @@ cudaError_t launch_pages_copy(const PagePool& p, const int32_t* src, const int32
 cudaError_t launch_pages_compact(const CompactArgs& a, cudaStream_t stream) {
   const int sms = sm_count_current();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  const int smem = (a.pool.n_pages + 31) / 32 * 4;
-  cudaError_t e = ensure_smem_limit(compact_plan_kernel, kCompactMaxPages / 8, g_plan_smem);
+  const int smem = plan_bytes(a.pool.n_pages);
+  cudaError_t e = ensure_smem_limit(compact_plan_kernel, plan_bytes(kCompactMaxPages), g_plan_smem);
   if (e != cudaSuccess) return e;
   e = launch_dependent(compact_plan_kernel, 1u, kPlanThreads, smem, stream, a);
   if (e != cudaSuccess) return e;
