@@ -174,11 +174,11 @@ __global__ void __launch_bounds__(128) append_one_kernel(const __grid_constant__
 // ---- copies ---------------------------------------------------------------
 
 // Copies, bound by HBM (each byte read and written once).  The unit of work is
-// 16 KB of one page's K or V in one layer, four 16-byte loads a thread in
+// 32 KB of one page's K or V in one layer, eight 16-byte loads a thread in
 // flight before the first store, so that the blocks of one resident wave
 // finish together whatever the number of pages (whole pages a block left a
 // fifth of the wave idle at 495 pages x 8 layers: 176 us).
-constexpr int kCopyThreads = 256, kCopyUnit = kCopyThreads * 4;   // in 16-byte vectors
+constexpr int kCopyThreads = 256, kCopyVecs = 8, kCopyUnit = kCopyThreads * kCopyVecs;   // in 16-byte vectors
 __host__ __device__ __forceinline__ long long copy_units(const PagePool& p, long long pages) {
   const long long segs = (p.page_bytes / 16 + kCopyUnit - 1) / kCopyUnit;
   return pages * p.layers * 2 * segs;
@@ -198,12 +198,12 @@ __device__ __forceinline__ void copy_unit(const PagePool& p, long long u, int n,
   const uint4* s = reinterpret_cast<const uint4*>(p.codes[kv] + from * p.page_bytes);
   uint4* d = reinterpret_cast<uint4*>(p.codes[kv] + to * p.page_bytes);
   const int end = (int)(p.page_bytes / 16), at = seg * kCopyUnit + threadIdx.x;
-  uint4 v[4];
+  uint4 v[kCopyVecs];
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
+  for (int k = 0; k < kCopyVecs; ++k)
     if (at + k * kCopyThreads < end) v[k] = s[at + k * kCopyThreads];
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
+  for (int k = 0; k < kCopyVecs; ++k)
     if (at + k * kCopyThreads < end) d[at + k * kCopyThreads] = v[k];
   if (seg == 0)
     for (int h = threadIdx.x; h < p.heads; h += kCopyThreads)

@@ -1,6 +1,7 @@
 // extern "C" entry points of the paged 8-bit cache: argument checks on the
 // host, before anything is launched, and dispatch.
 #include <cuda_runtime.h>
+#include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
 #include <cmath>
@@ -9,6 +10,14 @@
 #include "kvq_pages.h"
 
 namespace {
+
+// An entry point's NVTX range (for Nsight timelines and ncu --nvtx filters).
+// The other entry points get theirs in the binding; these calls are short
+// enough for that to be a tenth of them.
+struct Range {
+  explicit Range(const char* name) { nvtxRangePushA(name); }
+  ~Range() { nvtxRangePop(); }
+};
 
 bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1u)) == 0; }
 
@@ -101,6 +110,7 @@ kvq_status kvq_pages_append(const kvq_pages* pages, int32_t layer, const uint16_
                             int64_t k_row_stride, int64_t k_head_stride, const uint16_t* v_new,
                             int64_t v_row_stride, int64_t v_head_stride, const kvq_sequences* seqs,
                             void* stream) {
+  const Range range("kvq_pages_append");
   kvq_status st = check_pool(pages);
   if (st != KVQ_OK) return st;
   if (layer < 0 || layer >= pages->layers) return KVQ_ERR_INVALID_ARG;
@@ -142,6 +152,7 @@ kvq_status kvq_paged_attention(const kvq_pages* pages, int32_t layer, const uint
                                const kvq_sequences* seqs, int32_t max_q, float scale,
                                int32_t causal, int32_t window, void* workspace,
                                size_t workspace_bytes, uint16_t* out, float* lse, void* stream) {
+  const Range range("kvq_paged_attention");
   kvq_status st = check_pool(pages);
   if (st != KVQ_OK) return st;
   if (layer < 0 || layer >= pages->layers) return KVQ_ERR_INVALID_ARG;
@@ -185,6 +196,7 @@ kvq_status kvq_paged_attention(const kvq_pages* pages, int32_t layer, const uint
 
 kvq_status kvq_pages_copy(const kvq_pages* pages, const int32_t* src, const int32_t* dst, int32_t n,
                           void* stream) {
+  const Range range("kvq_pages_copy");
   const kvq_status st = check_pool(pages);
   if (st != KVQ_OK) return st;
   if (n < 0) return KVQ_ERR_INVALID_ARG;
@@ -226,6 +238,7 @@ kvq_status kvq_pages_compact(const kvq_pages* pages, const int32_t* table, int32
                              int32_t width, int64_t table_stride, int32_t* table_out,
                              int64_t table_out_stride, int32_t* n_live, void* workspace,
                              size_t workspace_bytes, void* stream) {
+  const Range range("kvq_pages_compact");
   const kvq_status st = check_pool(pages);
   if (st != KVQ_OK) return st;
   if (pages->n_pages > kvq::kCompactMaxPages) return KVQ_ERR_TOO_LARGE;

@@ -10,6 +10,7 @@ import ctypes
 import functools
 import math
 import os
+import threading
 
 import numpy as np
 import torch
@@ -481,6 +482,8 @@ class PagedCache:
         self.device = k_codes.device
         self.layers, self.n_pages, self.kv_heads, self.page_tokens, self.head_dim = k_codes.shape
         self._at = ctypes.addressof(c)
+        self._need = {}         # workspace bytes by the call's sizes
+        self._workspaces = {}   # by thread and stream
 
     @classmethod
     def zeros(cls, layers: int, n_pages: int, kv_heads: int, page_tokens: int, head_dim: int,
@@ -493,8 +496,30 @@ class PagedCache:
 
     def workspace_bytes(self, q_heads: int, batch: int, width: int, rows: int, max_q: int) -> int:
         """kvq_paged_workspace_bytes (width: entries per row of the block table)."""
-        with _switch(self.device):
-            return int(lib().kvq_paged_workspace_bytes(self._at, q_heads, batch, width, rows, max_q))
+        key = (q_heads, batch, width, rows, max_q)
+        need = self._need.get(key)
+        if need is None:
+            with _switch(self.device):
+                need = int(lib().kvq_paged_workspace_bytes(self._at, q_heads, batch, width, rows, max_q))
+            if len(self._need) >= 4096:
+                self._need.clear()
+            self._need[key] = need
+        return need
+
+    def _workspace(self, need: int, stream) -> torch.Tensor:
+        """Scratch for a call that was given none.  Kept between the calls of a
+        thread on a stream (those run one after another; nothing in it has to
+        survive a call); a call that is being captured, or names its stream,
+        gets one of its own."""
+        if stream is not None or torch.cuda.is_current_stream_capturing():
+            return torch.empty(need, dtype=torch.uint8, device=self.device)
+        key = (threading.get_ident(), torch._C._cuda_getCurrentRawStream(self.device.index))
+        ws = self._workspaces.get(key)
+        if ws is None or ws.numel() < need:
+            if len(self._workspaces) >= 64:
+                self._workspaces.clear()
+            ws = self._workspaces[key] = torch.empty(need, dtype=torch.uint8, device=self.device)
+        return ws
 
 
 def _switch(device, stream=None):
@@ -564,7 +589,6 @@ def _sequences(cache: PagedCache, rows: int, block_table, kv_lens, offsets) -> S
                            kv_lens.data_ptr(), None if offsets is None else offsets.data_ptr(), rows)
 
 
-@_nvtx("kvq_pages_append")
 def pages_append(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor,
                  block_table: torch.Tensor, kv_lens: torch.Tensor, offsets=None, layer: int = 0,
                  stream=None):
@@ -584,7 +608,6 @@ def pages_append(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor,
             ctypes.addressof(s), _handle(stream, cache.device)), "kvq_pages_append")
 
 
-@_nvtx("kvq_paged_attention")
 def paged_attention(cache: PagedCache, q: torch.Tensor, block_table: torch.Tensor,
                     kv_lens: torch.Tensor, offsets=None, max_q: int | None = None,
                     scale: float | None = None, causal: bool = True, window: int = 0,
@@ -616,11 +639,9 @@ def paged_attention(cache: PagedCache, q: torch.Tensor, block_table: torch.Tenso
         if with_lse:
             lse = torch.empty((rows, q_heads), dtype=torch.float32, device=dev)
         if workspace is None:
-            ws, ws_bytes = None, lib().kvq_paged_workspace_bytes(cache._at, q_heads, s.batch, s.width,
-                                                                 rows, max_q)
+            ws, ws_bytes = None, cache.workspace_bytes(q_heads, s.batch, s.width, rows, max_q)
             if ws_bytes > 16:
-                workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-                ws = workspace.data_ptr()
+                ws = cache._workspace(ws_bytes, stream).data_ptr()
         else:
             ws_ptr, ws_bytes = _workspace_arg(workspace, dev)
             ws = ws_ptr.value
@@ -649,7 +670,6 @@ def _host_ids(ids, name: str) -> tuple:
     return own.buffer_info()[0], len(own), own
 
 
-@_nvtx("kvq_pages_copy")
 def pages_copy(cache: PagedCache, src, dst, stream=None):
     """kvq_pages_copy: pages src[i] -> dst[i] of every layer (lists or CPU
     integer tensors; the dst distinct, none of them a src)."""
@@ -665,7 +685,6 @@ def pages_copy(cache: PagedCache, src, dst, stream=None):
                "kvq_pages_copy")
 
 
-@_nvtx("kvq_pages_compact")
 def pages_compact(cache: PagedCache, block_table: torch.Tensor, out=None, workspace=None,
                   stream=None):
     """kvq_pages_compact: moves the live pages (entries >= 0 of block_table)
@@ -686,9 +705,8 @@ def pages_compact(cache: PagedCache, block_table: torch.Tensor, out=None, worksp
             out = torch.empty(shape, dtype=torch.int32, device=dev)
         n_live = torch.empty(1, dtype=torch.int32, device=dev)
         if workspace is None:
-            need = lib().kvq_pages_compact_workspace_bytes(cache._at)
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-            ws, ws_bytes = workspace.data_ptr(), need
+            ws_bytes = lib().kvq_pages_compact_workspace_bytes(cache._at)
+            ws = cache._workspace(max(ws_bytes, 16), stream).data_ptr()
         else:
             ws_ptr, ws_bytes = _workspace_arg(workspace, dev)
             ws = ws_ptr.value
