@@ -17,11 +17,26 @@ namespace {
 // ---- few rows: the decoding form ----
 // Rows of a cache head up to which the decoding form is taken: it reads the
 // keys once for every 16 rows, the tensor-core form works on 128 rows however
-// few there are.
+// few there are.  Decoding / tensor-core form in us, 64 channels, 16 sequences
+// of 4096 keys, 4 heads: 32 rows 31.7 / 33.8, 40 rows 40.6 / 33.8; 32 of 16384
+// keys, 8 heads: 280 / 409 and 411 / 409; 128 channels: 354 / 440, 518 / 440.
 constexpr int kDecRows = 32;
 int rows_of_item(long long cap) { return cap <= 8 ? 8 : 16; }
 
-std::atomic<uint64_t> g_decode_smem[2][2], g_decode12_smem[2], g_item_smem[2][2];
+std::atomic<uint64_t> g_decode_smem[2][2], g_decode12_smem[2], g_item_smem[2][2], g_item_wide[2][2];
+
+// clusters of more than 8 CTAs, allowed once per kernel and device
+template <typename Kernel>
+cudaError_t ensure_wide_clusters(Kernel kern, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? (uint64_t{1} << dev) : 0;
+  if (bit != 0 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && bit != 0) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // Warps of the decoding form, per CTA.  Twelve hide more of the latency of
 // products and votes than eight where every warp has a long run of keys
@@ -47,11 +62,58 @@ DecodeWs decode_ws(int warps, int batch, int rows_cap, int d) {
   return w;
 }
 
-// A CTA per (sequence, cache head): the most units an item can have are few,
-// and the items no more than two waves of CTAs.
-// (items: of all sequences and cache heads)
-bool decode_by_item(int sms, long long items, long long keys) {
-  return keys <= (long long)kItemUnits * kUnit && items <= 2LL * sms;
+// Clusters of c = 2^k CTAs of the item kernel that run at once on the current
+// device (its SMs come in groups that a cluster cannot straddle: of 152 SMs 76
+// clusters of 2, 36 of 4, 15 of 8, 7 of 16); asked once per device.
+int active_clusters(int k) {
+  static std::atomic<int> known[64][5];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  const int had = known[dev][k].load(std::memory_order_relaxed);
+  if (had != 0) return had - 1;
+  const auto kern = decode_item_kernel<128, 1, kDecWarps>;
+  const int smem = DecCfg<128, kDecWarps>::kAlloc;
+  int n = 0;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(64u << k);
+  cfg.blockDim = dim3(kDecWarps * 32);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 1u << k;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (ensure_smem_limit(kern, smem, g_item_smem[1][0]) != cudaSuccess ||
+      ensure_wide_clusters(kern, g_item_wide[1][0]) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+    (void)cudaGetLastError();   // no clusters, then
+    n = 0;
+  }
+  known[dev][k].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
+// CTAs per item (sequence, cache head, row group), or 0 for equal runs of the
+// line of all keys.  An item's CTAs start at once and join by themselves, but
+// the longest item decides; the line scans the batch, takes a second kernel,
+// which joins every item's pieces, and balances.  The times below, in us, are
+// fits to measured ones (sequences of one length; 128 channels, grouped by 4,
+// item / line): 32 items of 512 keys 6.5 / 9.7, of 8192 15.5 / 18.7; 64 of 8192
+// 26.9 / 34.9; 48 of 32768 83 / 76; 192 of 2048 25.7 / 23.0; 4 of 32768 17.3 /
+// 24.7.  Keys are known by the table's width only, so a CTA's share is limited
+// too, to 4096 keys: the longest of a ragged batch then costs 25 us at most.
+int decode_by_item(int sms, int d, long long items, long long keys) {
+  if (items > 2LL * sms) return 0;
+  int c = 1;
+  for (int k = 1; (1 << k) <= kMaxCluster && items <= active_clusters(k); ++k) c = 1 << k;
+  const double units = (double)keys / kUnit, share = (double)((items + sms - 1) / sms) * units / c;
+  if (share > 128.0) return 0;
+  const double unit = d == 128 ? 0.16 : 0.12;
+  const double t_item = (c > 1 || items > sms ? 5.5 : 3.8) + unit * share;
+  const double pieces = std::min(units, (double)sms * kDecWarps / (double)items);
+  const double t_line = 8.7 + 0.02 * pieces + 1.25 * unit * units * (double)items / sms;
+  return t_item < t_line ? c : 0;
 }
 
 template <int D, int NT>
@@ -72,10 +134,13 @@ kvq_status launch_decode(const PagedAttnArgs& a, cudaStream_t stream) {
   d.a = a;
   d.rows_cap = rows_cap;
   d.groups_cap = groups_cap;
-  if (decode_by_item(sms, items, (long long)a.s.width * a.p.page)) {
+  d.cluster = decode_by_item(sms, D, items, (long long)a.s.width * a.p.page);
+  if (d.cluster > 0) {
     const auto kern = decode_item_kernel<D, NT, kDecWarps>;
     if (ensure_smem_limit(kern, smem, g_item_smem[D == 128][NT - 1]) != cudaSuccess ||
-        launch_dependent(kern, (unsigned)items, kDecWarps * 32, smem, stream, d, mk, mv) != cudaSuccess)
+        (d.cluster > 8 && ensure_wide_clusters(kern, g_item_wide[D == 128][NT - 1]) != cudaSuccess) ||
+        launch_clusters(kern, (unsigned)(items * d.cluster), (unsigned)d.cluster, kDecWarps * 32, smem, stream, d, mk,
+                        mv) != cudaSuccess)
       return KVQ_ERR_CUDA;
     return KVQ_OK;
   }
@@ -121,8 +186,12 @@ int split_limit(int sms, long long ctas) {
   const long long s = ctas > 0 ? (2LL * sms + ctas - 1) / ctas : 1;
   return (int)(s > kMaxSplits ? kMaxSplits : s);
 }
+// Query tiles of 128 rows a CTA: one or two.  Two against one in us, 8
+// sequences of 4096 keys, 8 heads of 128 channels: 140 rows 46.1 / 50.3, 256
+// rows 53.4 / 49.3, 400 rows 71.2 / 94.9.
+int query_tiles(long long cap) { return cap <= 128 ? 1 : 2; }
 long long chunk_tiles(int batch, int heads, long long cap, int* q_tiles) {
-  const int per = cap <= 128 ? 128 : 256;
+  const int per = 128 * query_tiles(cap);
   *q_tiles = (int)((cap + per - 1) / per);
   return (long long)batch * heads * *q_tiles;
 }
@@ -177,7 +246,7 @@ size_t paged_attention_workspace(int kv_heads, int q_heads, int d, int batch, lo
   if (cap <= kDecRows) {
     const int r = rows_of_item(cap);
     const long long items = (long long)batch * kv_heads * ((cap + r - 1) / r);
-    if (decode_by_item(sms, items, keys)) return 16;
+    if (decode_by_item(sms, d, items, keys) > 0) return 16;
     return decode_ws(sms * decode_warps(sms, r / 8, decode_units(items, keys)), batch,
                      (int)std::min<long long>(cap, r), d).bytes;
   }
@@ -193,8 +262,8 @@ kvq_status launch_paged_attention(const PagedAttnArgs& a, cudaStream_t stream) {
     if (a.p.d == 64) return rows_of_item(cap) > 8 ? launch_decode<64, 2>(a, stream) : launch_decode<64, 1>(a, stream);
     return rows_of_item(cap) > 8 ? launch_decode<128, 2>(a, stream) : launch_decode<128, 1>(a, stream);
   }
-  if (a.p.d == 64) return cap > 128 ? launch_chunk<64, 2>(a, stream) : launch_chunk<64, 1>(a, stream);
-  return cap > 128 ? launch_chunk<128, 2>(a, stream) : launch_chunk<128, 1>(a, stream);
+  if (a.p.d == 64) return query_tiles(cap) == 2 ? launch_chunk<64, 2>(a, stream) : launch_chunk<64, 1>(a, stream);
+  return query_tiles(cap) == 2 ? launch_chunk<128, 2>(a, stream) : launch_chunk<128, 1>(a, stream);
 }
 
 }  // namespace kvq

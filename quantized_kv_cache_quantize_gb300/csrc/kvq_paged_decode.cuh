@@ -48,7 +48,7 @@ namespace {
 
 constexpr int kUnit = 32;          // keys per unit
 constexpr int kMinUnits = 2;       // per warp, when the work is small
-constexpr int kItemUnits = 32;     // of an item at most, for a CTA of its own
+constexpr int kMaxCluster = 16;
 
 // W warps per CTA, one CTA per SM
 template <int D, int W>
@@ -70,6 +70,7 @@ struct DecodeArgs {
   int rows_cap;        // rows of an item at most: min(max_q * group, 8 NT)
   int groups_cap;      // items per cache head at most
   int warps;           // of the grid
+  int cluster;         // CTAs per item (decode_item_kernel)
 };
 
 // What sequence b has to do: its rows, keys [lo, len) that any row attends to
@@ -631,17 +632,19 @@ __global__ void __launch_bounds__(W * 32, 1)
   }
 }
 
-// Short sequences: a CTA per item, the item's units divided among its warps and
-// joined in shared memory.  No scan of the batch, no workspace, one launch:
-// what counts there is the latency of one pass.
+// Few or short items: a CTA or a cluster of CTAs per item, the item's units
+// divided among all their warps, the parts joined in shared memory, then across
+// the cluster's.  No scan of the batch, no workspace, one launch: what counts
+// there is the latency of one pass.
 template <int D, int NT, int W>
 __global__ void __launch_bounds__(W * 32, 1)
     decode_item_kernel(const __grid_constant__ DecodeArgs p, const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v) {
   using C = DecCfg<D, W>;
-  constexpr int CH = D / 8;
+  constexpr int CH = D / 8, R = NT * 8;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ float2 ml_s[C::kWarps][NT * 8];
+  __shared__ float2 ml_s[W][R];
+  __shared__ float2 cta_ml[R];
   const PagedAttnArgs& a = p.a;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -654,69 +657,49 @@ __global__ void __launch_bounds__(W * 32, 1)
   }
   __syncwarp();
   ptx::grid_dependency_wait();
-  const int rb = (int)(blockIdx.x % (unsigned)p.groups_cap) * (8 * NT);
-  const unsigned bh = blockIdx.x / (unsigned)p.groups_cap;
+  // CTAs of a cluster are neighbours in the grid
+  const unsigned ctas = (unsigned)p.cluster, rank = blockIdx.x % ctas, item = blockIdx.x / ctas;
+  const int rb = (int)(item % (unsigned)p.groups_cap) * R;
+  const unsigned bh = item / (unsigned)p.groups_cap;
   const int b = (int)(bh / (unsigned)a.p.heads), h = (int)(bh % (unsigned)a.p.heads);
-  const SeqWork w = seq_work<8 * NT>(a, b);
-  const int rows = min(w.n * a.group - rb, 8 * NT);
-  if (w.units == 0 || rows <= 0) return;
-  const int i0 = w.units * wid / C::kWarps, i1 = w.units * (wid + 1) / C::kWarps;
+  const SeqWork w = seq_work<R>(a, b);
+  const int rows = w.units > 0 ? max(0, min(w.n * a.group - rb, R)) : 0;
+  const long long parts = (long long)ctas * W;
+  auto begin = [&](int warp) { return (int)((long long)w.units * ((int)rank * W + warp) / parts); };
+  const int i0 = begin(wid), i1 = rows > 0 ? begin(wid + 1) : i0;
   float o[NT][D / 16][4], m[NT][2], l[NT][2];
   bool ok = true;
-  if (i1 > i0) {
-    ok = decode_segment<D, NT, W>(a, map_k, map_v, rg, b, h, rb, w, i0, i1 - i0, o, m, l);
-  } else {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        m[nt][c] = -CUDART_INF_F;
-        l[nt][c] = 0.f;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) o[nt][k][c] = o[nt][k][c + 2] = 0.f;
-      }
-  }
+  if (i1 > i0) ok = decode_segment<D, NT, W>(a, map_k, map_v, rg, b, h, rb, w, i0, i1 - i0, o, m, l);
+  // a warp without units, or whose copies did not come, has no part (its
+  // weights are zero)
+  const bool part_of = i1 > i0 && ok;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int c = 0; c < 2; ++c)
-      if (g == 0) ml_s[wid][nt * 8 + 2 * t + c] = make_float2(m[nt][c], l[nt][c]);
-  // no copy of any warp is in flight once all are here: the rings are free
-  if (__syncthreads_or(!ok)) return;
-  float* part = reinterpret_cast<float*>(smem);   // [warp][row][D]
+      if (g == 0)
+        ml_s[wid][nt * 8 + 2 * t + c] = part_of ? make_float2(m[nt][c], l[nt][c]) : make_float2(-CUDART_INF_F, 0.f);
+  __syncthreads();   // no copy of any warp is in flight now: the rings are free
+  float* part = reinterpret_cast<float*>(smem);   // [warp][row][D], then [row][D] of the CTA
+  float* cta_o = part + W * R * D;
+  if (part_of) {
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int r = nt * 8 + 2 * t + c;
-      if (r >= rows || i1 <= i0) continue;
-      float4* dst = reinterpret_cast<float4*>(part + (wid * NT * 8 + r) * D + CH * g);
+      for (int c = 0; c < 2; ++c) {
+        const int r = nt * 8 + 2 * t + c;
+        if (r >= rows) continue;
+        float4* dst = reinterpret_cast<float4*>(part + (wid * R + r) * D + CH * g);
 #pragma unroll
-      for (int k = 0; k < CH / 4; ++k)
-        dst[k] = make_float4(o[nt][2 * k][c], o[nt][2 * k][c + 2], o[nt][2 * k + 1][c], o[nt][2 * k + 1][c + 2]);
-    }
+        for (int k = 0; k < CH / 4; ++k)
+          dst[k] = make_float4(o[nt][2 * k][c], o[nt][2 * k][c + 2], o[nt][2 * k + 1][c], o[nt][2 * k + 1][c + 2]);
+      }
+  }
   __syncthreads();
-  // a warp per row, the parts in order
-  for (int r = wid; r < rows; r += C::kWarps) {
-    float top = -CUDART_INF_F;
-#pragma unroll
-    for (int k = 0; k < C::kWarps; ++k) top = fmaxf(top, ml_s[k][r].x);
-    const float base = top > -CUDART_INF_F ? top : 0.f;
-    float ls = 0.f, v[D / 32];
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c) v[c] = 0.f;
-#pragma unroll
-    for (int k = 0; k < C::kWarps; ++k) {
-      if (w.units * (k + 1) / C::kWarps <= w.units * k / C::kWarps) continue;   // a warp without units
-      const float2 ml = ml_s[k][r];
-      const float f = ptx::ex2_approx(ml.x - base);
-      ls = fmaf(ml.y, f, ls);
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) v[c] = fmaf(part[(k * NT * 8 + r) * D + (D / 32) * lane + c], f, v[c]);
-    }
+  auto store = [&](int r, const float (&v)[D / 32], float top, float ls) {
     const int rr = rb + r;
     const long long row = (long long)(w.r0 + rr / a.group) * a.q_heads + h * a.group + rr % a.group;
-    if (!KVQ_IN_BOUNDS(row, (long long)a.s.rows * a.q_heads, a.status, a.bounds_site)) continue;
+    if (!KVQ_IN_BOUNDS(row, (long long)a.s.rows * a.q_heads, a.status, a.bounds_site)) return;
     const float f = ls > 0.f ? 1.f / ls : 0.f;
 #pragma unroll
     for (int c = 0; c < D / 32; c += 2) {
@@ -725,7 +708,55 @@ __global__ void __launch_bounds__(W * 32, 1)
     }
     if (lane == 0 && a.lse != nullptr)
       a.lse[row] = ls > 0.f ? 0.6931471805599453f * (top + log2f(ls)) : -CUDART_INF_F;
+  };
+  // a warp per row, the parts in order
+  for (int r = wid; r < rows; r += W) {
+    float top = -CUDART_INF_F;
+#pragma unroll
+    for (int k = 0; k < W; ++k) top = fmaxf(top, ml_s[k][r].x);
+    const float base = top > -CUDART_INF_F ? top : 0.f;
+    float ls = 0.f, v[D / 32];
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) v[c] = 0.f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      const float2 ml = ml_s[k][r];
+      if (ml.y == 0.f) continue;   // nothing there, not even numbers
+      const float f = ptx::ex2_approx(ml.x - base);
+      ls = fmaf(ml.y, f, ls);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) v[c] = fmaf(part[(k * R + r) * D + (D / 32) * lane + c], f, v[c]);
+    }
+    if (ctas == 1) {
+      store(r, v, top, ls);
+    } else {
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) cta_o[r * D + (D / 32) * lane + c] = v[c];
+      if (lane == 0) cta_ml[r] = make_float2(top, ls);
+    }
   }
+  if (ctas == 1) return;
+  ptx::cluster_sync();
+  // every CTA of the cluster is here, with or without units: a row is joined
+  // by one warp of one CTA, the CTAs' parts in order
+  for (int r = (int)rank + (int)ctas * wid; r < rows; r += (int)ctas * W) {
+    const uint32_t at_ml = ptx::smem_u32(&cta_ml[r]), at_o = ptx::smem_u32(cta_o + r * D + (D / 32) * lane);
+    float top = -CUDART_INF_F;
+    for (unsigned k = 0; k < ctas; ++k) top = fmaxf(top, ptx::ld_cluster_f32(ptx::mapa(at_ml, k)));
+    const float base = top > -CUDART_INF_F ? top : 0.f;
+    float ls = 0.f, v[D / 32];
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) v[c] = 0.f;
+    for (unsigned k = 0; k < ctas; ++k) {
+      const uint32_t ml = ptx::mapa(at_ml, k), from = ptx::mapa(at_o, k);
+      const float f = ptx::ex2_approx(ptx::ld_cluster_f32(ml) - base);
+      ls = fmaf(ptx::ld_cluster_f32(ml + 4), f, ls);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) v[c] = fmaf(ptx::ld_cluster_f32(from + 4 * c), f, v[c]);
+    }
+    store(r, v, top, ls);
+  }
+  ptx::cluster_sync();   // nobody leaves while its shared memory is read
 }
 
 // Joins the parts of items that several warps covered: one block per row of a

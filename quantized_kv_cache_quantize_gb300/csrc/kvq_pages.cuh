@@ -16,20 +16,28 @@ namespace {
 // Launch that may start while the stream's previous kernel finishes (the
 // kernel waits for it before its first global access).
 template <typename... Args>
-cudaError_t launch_dependent(void (*kern)(Args...), unsigned grid, int threads, int smem,
-                             cudaStream_t stream, Args... args) {
+cudaError_t launch_clusters(void (*kern)(Args...), unsigned grid, unsigned cluster, int threads, int smem,
+                            cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   note_launch();
   return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+template <typename... Args>
+cudaError_t launch_dependent(void (*kern)(Args...), unsigned grid, int threads, int smem,
+                             cudaStream_t stream, Args... args) {
+  return launch_clusters<Args...>(kern, grid, 1u, threads, smem, stream, args...);
 }
 
 // Bounded wait on an mbarrier phase: false when the limit ran out (recorded)
