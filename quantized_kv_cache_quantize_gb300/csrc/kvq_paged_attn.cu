@@ -15,13 +15,13 @@ namespace kvq {
 namespace {
 
 // ---- few rows: the decoding form ----
-// Rows of a cache head up to which the decoding form is taken: it reads the
-// keys once for every 16 rows, the tensor-core form works on 128 rows however
-// few there are.  Decoding / tensor-core form in us, 64 channels, 16 sequences
-// of 4096 keys, 4 heads: 32 rows 31.7 / 33.8, 40 rows 40.6 / 33.8; 32 of 16384
-// keys, 8 heads: 280 / 409 and 411 / 409; 128 channels: 354 / 440, 518 / 440.
-constexpr int kDecRows = 32;
-int rows_of_item(long long cap) { return cap <= 8 ? 8 : 16; }
+// Rows of a cache head up to which the decoding form is taken: two column
+// tiles are what a warp's registers hold.  Past them it would read the keys
+// again from L2, and the tensor-core form, which works on 128 rows however few
+// there are, is as good or better.  Decoding / tensor-core form in us, 32
+// sequences of 16384 keys, 8 heads of 128 channels: 16 rows 183 / 283, 24 rows
+// in two passes 343 / 283; 64 channels: 148 / 247, 278 / 247.
+constexpr int kDecRows = 16;
 
 std::atomic<uint64_t> g_decode_smem[2][2], g_decode12_smem[2], g_item_smem[2][2], g_item_wide[2][2];
 
@@ -116,13 +116,20 @@ int decode_by_item(int sms, int d, long long items, long long keys) {
   return t_item < t_line ? c : 0;
 }
 
+// Keys of a sequence that its rows attend to, at most: the table's width, or
+// the window's keys before its last max_q tokens.  (Fewer keys never need more
+// workspace: the size asked for is that of the width.)
+long long key_bound(const PagedAttnArgs& a) {
+  const long long keys = (long long)a.s.width * a.p.page;
+  return a.window > 0 ? std::min(keys, (long long)a.window + a.max_q) : keys;
+}
+
 template <int D, int NT>
 kvq_status launch_decode(const PagedAttnArgs& a, cudaStream_t stream) {
   const int sms = sm_count_current();
   if (sms <= 0) return KVQ_ERR_CUDA;
-  const int cap = a.max_q * a.group, rows_cap = std::min(cap, 8 * NT);
-  const int groups_cap = (cap + 8 * NT - 1) / (8 * NT);
-  const long long items = (long long)a.s.batch * a.p.heads * groups_cap;
+  const int cap = a.max_q * a.group;
+  const long long items = (long long)a.s.batch * a.p.heads;
   CUtensorMap mk, mv;
   const long long blocks = (long long)a.p.n_pages * a.p.heads;
   const int box = a.p.page < kUnit ? a.p.page : kUnit;
@@ -132,9 +139,8 @@ kvq_status launch_decode(const PagedAttnArgs& a, cudaStream_t stream) {
   const int smem = DecCfg<D, kDecWarps>::kAlloc;
   DecodeArgs d{};
   d.a = a;
-  d.rows_cap = rows_cap;
-  d.groups_cap = groups_cap;
-  d.cluster = decode_by_item(sms, D, items, (long long)a.s.width * a.p.page);
+  d.rows_cap = cap;
+  d.cluster = decode_by_item(sms, D, items, key_bound(a));
   if (d.cluster > 0) {
     const auto kern = decode_item_kernel<D, NT, kDecWarps>;
     if (ensure_smem_limit(kern, smem, g_item_smem[D == 128][NT - 1]) != cudaSuccess ||
@@ -144,10 +150,10 @@ kvq_status launch_decode(const PagedAttnArgs& a, cudaStream_t stream) {
       return KVQ_ERR_CUDA;
     return KVQ_OK;
   }
-  // the units there can be, from the table's width, bound the grid
-  const double most = decode_units(items, (long long)a.s.width * a.p.page);
+  // the units there can be bound the grid
+  const double most = decode_units(items, key_bound(a));
   const int warps = decode_warps(sms, NT, most);
-  const DecodeWs ws = decode_ws(sms * warps, a.s.batch, rows_cap, D);
+  const DecodeWs ws = decode_ws(sms * warps, a.s.batch, cap, D);
   if (a.ws_bytes < ws.bytes) return KVQ_ERR_INVALID_ARG;
   int grid = sms;
   if (most < (double)sms * warps * kMinUnits) grid = std::min((int)(most / kMinUnits) + 1, sms);
@@ -172,7 +178,7 @@ kvq_status launch_decode(const PagedAttnArgs& a, cudaStream_t stream) {
       return KVQ_ERR_CUDA;
   }
   const long long rows = (long long)a.s.batch * a.p.heads * cap;
-  if (launch_dependent(join_kernel<D, 8 * NT>, (unsigned)rows, kJoinWarps * 32, 0, stream, d) != cudaSuccess)
+  if (launch_dependent(join_kernel<D>, (unsigned)rows, kJoinWarps * 32, 0, stream, d) != cudaSuccess)
     return KVQ_ERR_CUDA;
   return KVQ_OK;
 }
@@ -186,9 +192,11 @@ int split_limit(int sms, long long ctas) {
   const long long s = ctas > 0 ? (2LL * sms + ctas - 1) / ctas : 1;
   return (int)(s > kMaxSplits ? kMaxSplits : s);
 }
-// Query tiles of 128 rows a CTA: one or two.  Two against one in us, 8
-// sequences of 4096 keys, 8 heads of 128 channels: 140 rows 46.1 / 50.3, 256
-// rows 53.4 / 49.3, 400 rows 71.2 / 94.9.
+// Query tiles of 128 rows a CTA: one or two.  Two against one in us, 32
+// sequences of 16384 keys, 8 heads of 128 channels: 128 rows 443 / 290, 144
+// rows 472 / 570, 256 rows 480 / 576; 16 of 4096: 64.5 / 46.4, 69.2 / 87.7,
+// 72.6 / 90.1.  (With few CTAs, 4 sequences of 2048 keys, one is the better at
+// 256 rows, 29.9 / 26.0, and past that.)
 int query_tiles(long long cap) { return cap <= 128 ? 1 : 2; }
 long long chunk_tiles(int batch, int heads, long long cap, int* q_tiles) {
   const int per = 128 * query_tiles(cap);
@@ -210,7 +218,7 @@ kvq_status launch_chunk(const PagedAttnArgs& a, cudaStream_t stream) {
   // ranges: the cost model of the window attention's key-range split
   int max_splits = split_limit(sms, ctas), per = 0;
   while (max_splits > 1 && chunk_ws(max_splits, a.s.rows, a.q_heads, D) > a.ws_bytes) --max_splits;
-  const long long keys = (long long)a.s.width * a.p.page;
+  const long long keys = key_bound(a);
   attention_split((long long)a.s.batch * a.p.heads, (int)cap, (int)((keys + 127) / 128), 0, D, 128 * NQ, sms,
                   max_splits, &c.splits, &per);
   if (a.ws_bytes < chunk_ws(c.splits, a.s.rows, a.q_heads, D)) return KVQ_ERR_INVALID_ARG;
@@ -244,11 +252,9 @@ size_t paged_attention_workspace(int kv_heads, int q_heads, int d, int batch, lo
   const long long cap = (long long)max_q * (q_heads / kv_heads);
   const int sms = std::max(sm_count_current(), 1);
   if (cap <= kDecRows) {
-    const int r = rows_of_item(cap);
-    const long long items = (long long)batch * kv_heads * ((cap + r - 1) / r);
+    const long long items = (long long)batch * kv_heads;
     if (decode_by_item(sms, d, items, keys) > 0) return 16;
-    return decode_ws(sms * decode_warps(sms, r / 8, decode_units(items, keys)), batch,
-                     (int)std::min<long long>(cap, r), d).bytes;
+    return decode_ws(sms * decode_warps(sms, cap <= 8 ? 1 : 2, decode_units(items, keys)), batch, (int)cap, d).bytes;
   }
   int q_tiles = 0;
   return chunk_ws(split_limit(sms, chunk_tiles(batch, kv_heads, cap, &q_tiles)), rows, q_heads, d);
@@ -259,8 +265,8 @@ kvq_status launch_paged_attention(const PagedAttnArgs& a, cudaStream_t stream) {
   if (cap > 0x3fffffffLL || (long long)a.s.batch * a.p.heads > 0x7fffffffLL / (cap <= kDecRows ? kDecRows : 1))
     return KVQ_ERR_TOO_LARGE;
   if (cap <= kDecRows) {
-    if (a.p.d == 64) return rows_of_item(cap) > 8 ? launch_decode<64, 2>(a, stream) : launch_decode<64, 1>(a, stream);
-    return rows_of_item(cap) > 8 ? launch_decode<128, 2>(a, stream) : launch_decode<128, 1>(a, stream);
+    if (a.p.d == 64) return cap > 8 ? launch_decode<64, 2>(a, stream) : launch_decode<64, 1>(a, stream);
+    return cap > 8 ? launch_decode<128, 2>(a, stream) : launch_decode<128, 1>(a, stream);
   }
   if (a.p.d == 64) return query_tiles(cap) == 2 ? launch_chunk<64, 2>(a, stream) : launch_chunk<64, 1>(a, stream);
   return query_tiles(cap) == 2 ? launch_chunk<128, 2>(a, stream) : launch_chunk<128, 1>(a, stream);

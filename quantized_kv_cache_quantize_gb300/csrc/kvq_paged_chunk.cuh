@@ -23,11 +23,13 @@
 // The base m is raised only when a weight would leave FP16 (64 keys' sum past
 // 2^15), to leave the largest at 2^9, so weights down to 2^-33 of it remain.
 //
-// Roles: 4 NQ warps softmax (one row per thread), 4 warps V conversion, one
-// MMA thread, one TMA warp.  With NQ = 2 the two query tiles alternate on the
-// tensor core (PV0 QK0' PV1 QK1'), each key tile is read and converted once
-// for 256 rows; NQ = 1 (at most 128 rows a head) holds two score buffers and
-// runs the next Q K^T ahead of the softmax instead.
+// Roles: two groups of 4 warps softmax (one row per thread), 4 warps V
+// conversion, one MMA thread, one TMA warp.  With NQ = 2 a group has a query
+// tile of its own; the two alternate on the tensor core (PV0 QK0' PV1 QK1'),
+// each key tile is read and converted once for 256 rows.  With NQ = 1 (at most
+// 128 rows a head) the groups take the key tiles of one query tile in turn,
+// each with its own base, sum and O, and join at the end: with one group alone
+// 64 rows of 32 sequences, 16384 keys and 8 heads took 440 us, not 286.
 #pragma once
 
 #include <math_constants.h>
@@ -58,13 +60,12 @@ struct ChunkCfg {
   static constexpr int kBar = kMeta + kMetaSlots * kMetaBytes;
   static constexpr int kBytes = kBar + 512;
   static constexpr int kAlloc = kBytes + 1024;
-  static constexpr int kSoftmaxWarps = 4 * NQ;
+  static constexpr int kSoftmaxWarps = 8;
   static constexpr int kMmaWarp = kSoftmaxWarps + 4;
   static constexpr int kThreads = (kSoftmaxWarps + 6) * 32;
-  static constexpr bool kHalves = NQ == 2;         // weights handed over by halves
   static constexpr int kTO = 256;                  // O tiles behind two score buffers
   static constexpr int kTCols = 512;
-  static_assert(kTO + NQ * D <= kTCols, "tensor memory");
+  static_assert(kTO + 2 * D <= kTCols, "tensor memory");
   static_assert(kAlloc <= 232448, "shared memory");
 };
 
@@ -76,16 +77,15 @@ enum : int {
   kCbEmptyVr = 9,   // [2] value codes read (4 arrivals)
   kCbFullV = 11,    // [2] FP16 values written (4 arrivals)
   kCbEmptyV = 13,   // [2] the tile's PV MMAs done
-  kCbS = 15,        // [2] scores ready
+  kCbS = 15,        // [2] scores of a group's tile ready
   kCbP = 17,        // [2] weights of keys 0-63 written, O rescaled (4 arrivals)
-  kCbOStep = 19,    // NQ = 1: a tile's PV done
-  kCbODone = 20,    // every MMA done
-  kCbMeta = 21,     // [8] a tile's page exponents written.  Not the key
+  kCbODone = 19,    // every MMA done
+  kCbMeta = 20,     // [8] a tile's page exponents written.  Not the key
                     // barrier: its stage can be refilled, and its phase
                     // passed twice, before a slow softmax warp looks at it
-  kCbPb = 29,       // [2] weights of keys 64-127 written (4 arrivals)
-  kCbHalf = 31,     // [2] PV of keys 0-63 done
-  kCbCount = 33
+  kCbPb = 28,       // [2] weights of keys 64-127 written (4 arrivals)
+  kCbHalf = 30,     // [2] PV of keys 0-63 done
+  kCbCount = 32
 };
 
 struct ChunkArgs {
@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
   const PagedAttnArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   ptx::grid_dependency_wait();
+  ptx::launch_dependents();
 
   // the longest row tiles (the last ones, under a causal mask) go first
   const int heads = a.p.heads;
@@ -223,7 +224,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
       ptx::mbar_init(BAR(kCbHalf + i), 1);
     }
     for (int i = 0; i < kMetaSlots; ++i) ptx::mbar_init(BAR(kCbMeta + i), 1);
-    ptx::mbar_init(BAR(kCbOStep), 1);
     ptx::mbar_init(BAR(kCbODone), 1);
     *abort = 0;
     ptx::fence_mbar_init();
@@ -245,13 +245,14 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
     const int r = (warp & 3) * 32 + lane;        // TMEM lane, row of the query tile
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     // row of the head's rows; one past the last repeats it and is not stored
-    const bool live = row0 + q * 128 + r < rows;
-    const int row = min(row0 + q * 128 + r, rows - 1);
+    const int qoff = row0 + (NQ == 2 ? q * 128 : 0);
+    const bool live = qoff + r < rows;
+    const int row = min(qoff + r, rows - 1);
     const int tok = row / a.group;
     const int hq = h * a.group + row % a.group;
     // a warp without a row of its own only keeps the barriers going: its
     // lanes of the products go nowhere
-    const bool idle = row0 + q * 128 + (warp & 3) * 32 >= rows;
+    const bool idle = qoff + (warp & 3) * 32 >= rows;
     // ---- the query row: scale, split, store (K-major, swizzled) ----
     float cq;
     {
@@ -268,31 +269,34 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
         for (int k = 0; k < 4; ++k) mx = max(mx, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
       }
       const int e = max((int)(mx >> 7), 1) - 127 - 7;      // largest magnitude to [2^7, 2^8)
-      const float f0 = pow2f(-(e / 2)), f1 = pow2f(-(e - e / 2));
+      // (an infinity or a NaN makes the whole row NaN)
+      const float f0 = mx < 0x7f80u ? pow2f(-(e / 2)) : CUDART_NAN_F, f1 = pow2f(-(e - e / 2));
       cq = a.scale * 1.4426950408889634f * pow2f(e / 2) * pow2f(e - e / 2);
-      const uint32_t hi_t = sm + C::kQ + q * 2 * C::kQT;
+      const uint32_t hi_t = sm + C::kQ + (NQ == 2 ? q : 0) * 2 * C::kQT;
+      if (NQ == 2 || q == 0) {
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        uint32_t wh[4], wl[4];
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t wh[4], wl[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint4& v = raw[2 * c + (k >> 1)];
-          const uint32_t w0 = (k & 1) ? v.z : v.x, w1 = (k & 1) ? v.w : v.y;
-          const float x0 = __uint_as_float(w0 << 16) * f0 * f1, x1 = __uint_as_float(w0 & 0xffff0000u) * f0 * f1;
-          const float x2 = __uint_as_float(w1 << 16) * f0 * f1, x3 = __uint_as_float(w1 & 0xffff0000u) * f0 * f1;
-          wh[k] = e4m3x4(x0, x1, x2, x3);
-          const uint32_t h01 = f16x2_of_e4m3x2((uint16_t)wh[k]), h23 = f16x2_of_e4m3x2((uint16_t)(wh[k] >> 16));
-          const float2 a01 = __half22float2(*reinterpret_cast<const __half2*>(&h01));
-          const float2 a23 = __half22float2(*reinterpret_cast<const __half2*>(&h23));
-          wl[k] = e4m3x4(x0 - a01.x, x1 - a01.y, x2 - a23.x, x3 - a23.y);
+          for (int k = 0; k < 4; ++k) {
+            const uint4& v = raw[2 * c + (k >> 1)];
+            const uint32_t w0 = (k & 1) ? v.z : v.x, w1 = (k & 1) ? v.w : v.y;
+            const float x0 = __uint_as_float(w0 << 16) * f0 * f1, x1 = __uint_as_float(w0 & 0xffff0000u) * f0 * f1;
+            const float x2 = __uint_as_float(w1 << 16) * f0 * f1, x3 = __uint_as_float(w1 & 0xffff0000u) * f0 * f1;
+            wh[k] = e4m3x4(x0, x1, x2, x3);
+            const uint32_t h01 = f16x2_of_e4m3x2((uint16_t)wh[k]), h23 = f16x2_of_e4m3x2((uint16_t)(wh[k] >> 16));
+            const float2 a01 = __half22float2(*reinterpret_cast<const __half2*>(&h01));
+            const float2 a23 = __half22float2(*reinterpret_cast<const __half2*>(&h23));
+            wl[k] = e4m3x4(x0 - a01.x, x1 - a01.y, x2 - a23.x, x3 - a23.y);
+          }
+          const int off = D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+          sts_u4(hi_t + off, make_uint4(wh[0], wh[1], wh[2], wh[3]));
+          sts_u4(hi_t + C::kQT + off, make_uint4(wl[0], wl[1], wl[2], wl[3]));
         }
-        const int off = D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-        sts_u4(hi_t + off, make_uint4(wh[0], wh[1], wh[2], wh[3]));
-        sts_u4(hi_t + C::kQT + off, make_uint4(wl[0], wl[1], wl[2], wl[3]));
+        ptx::fence_proxy_async_smem();
+        warp_arrive(BAR(kCbQ));
       }
     }
-    ptx::fence_proxy_async_smem();
-    warp_arrive(BAR(kCbQ));
 
     // keys this row attends to, from the first key of local tile 0
     const int tq = t0 + tok;
@@ -302,25 +306,22 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
     int eref = -1000;
     const uint32_t t_o = tmem + C::kTO + q * D + lane_off;
     bool ok = true;
-    for (int j = 0; j < n_t; ++j) {
-      const int sb = NQ == 2 ? q : (j & 1);
-      const uint32_t t_s = tmem + sb * 128 + lane_off;
+    const uint32_t t_s = tmem + q * 128 + lane_off;
+    for (int j = NQ == 2 ? 0 : q; j < n_t; j += NQ == 2 ? 1 : 2) {
       const uint32_t par = NQ == 2 ? (j & 1) : ((j >> 1) & 1);
+      const bool first = NQ == 2 ? j == 0 : j < 2;
       // a slot of scales is written again 8 tiles later, the TMA warp at most
       // 5 ahead of the softmax (3 key stages, 2 score buffers)
       ok = page_wait(BAR(kCbMeta + (j & (kMetaSlots - 1))), (j / kMetaSlots) & 1, lim, abort, a.status) &&
-           page_wait(BAR(kCbS + sb), par, lim, abort, a.status);
+           page_wait(BAR(kCbS + q), par, lim, abort, a.status);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
       }
       ptx::tc_fence_after();
       if (idle) {
-        if (NQ == 1 && j > 0)
-          ok = __all_sync(0xffffffffu, page_wait(BAR(kCbOStep), (j - 1) & 1, lim, abort, a.status));
-        if (C::kHalves) warp_arrive(BAR(kCbP + q));
+        warp_arrive(BAR(kCbP + q));
         warp_arrive(BAR(kCbPb + q));
-        if (!ok) break;
         continue;
       }
       const uint32_t mt = sm + C::kMeta + (j & (kMetaSlots - 1)) * kMetaBytes;
@@ -398,47 +399,22 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
           l *= f;
           fo *= f;
           weights(cur);
-          if (!C::kHalves && half == 1) {   // the first half's, still here
-            ptx::tmem_st_wait();
-#pragma unroll 1
-            for (int c = 0; c < 2; ++c) {
-              uint32_t v[16];
-              ptx::tmem_ld16(t_s + 16 * c, v);
-#pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&v[k]));
-                v[k] = ptx::f16x2_rn(z.x * f, z.y * f);
-              }
-              ptx::tmem_st16(t_s + 16 * c, v);
-            }
-          }
         }
         l += sum;
         // over the first 32 of the 64 score columns just read
         ptx::tmem_st16(t_h, pk[0]);
         ptx::tmem_st16(t_h + 16, pk[1]);
         if (__any_sync(0xffffffffu, fo != 1.f)) {
-          // O is held by products still to be waited for: with NQ = 1 the
-          // previous tile's (this tile's QK ran before it), with halves
-          // handed over the first half's
-          if (NQ == 1 && j > 0) {
-            ok = __all_sync(0xffffffffu, ok && page_wait(BAR(kCbOStep), (j - 1) & 1, lim, abort, a.status));
-          } else if (C::kHalves && half == 1) {
-            ok = __all_sync(0xffffffffu, ok && page_wait(BAR(kCbHalf + q), j & 1, lim, abort, a.status));
-          }
+          // (the product of the first half is still under way; the group's
+          // previous tile's was done before these scores were)
+          if (half == 1) ok = __all_sync(0xffffffffu, ok && page_wait(BAR(kCbHalf + q), par, lim, abort, a.status));
           ptx::tc_fence_after();
-          if (j > 0 || (C::kHalves && half == 1)) rescale_o();
+          if (!first || half == 1) rescale_o();
           fo = 1.f;
         }
-        if (C::kHalves || half == 1) {
-          // NQ = 1: the previous tile's weights are consumed before these
-          // are announced (the barrier must not run two phases ahead)
-          if (NQ == 1 && j > 0)
-            ok = __all_sync(0xffffffffu, ok && page_wait(BAR(kCbOStep), (j - 1) & 1, lim, abort, a.status));
-          ptx::tmem_st_wait();
-          ptx::tc_fence_before();
-          warp_arrive(BAR((C::kHalves && half == 0 ? kCbP : kCbPb) + q));
-        }
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        warp_arrive(BAR((half == 0 ? kCbP : kCbPb) + q));
       }
       if (!ok) break;
     }
@@ -446,30 +422,66 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
     // ---- result ----
     if (ok) ok = page_wait(BAR(kCbODone), 0, lim, abort, a.status);
     ok = __all_sync(0xffffffffu, ok && !*abort);
-    if (ok) {
-      ptx::tc_fence_after();
+    ptx::tc_fence_after();
+    const float fe = eref > -1000 ? pow2f(eref) : 0.f;
+    // NQ = 1: the second group's share goes through shared memory, whose tiles
+    // nobody reads any more
+    const bool mine = n_t > (NQ == 2 ? 0 : q);   // the group had tiles
+    float f0 = fe, f1 = 0.f;
+    const uint32_t part_at = sm + C::kV + 4 * r, ml_at = sm + C::kK + 8 * r;
+    if constexpr (NQ == 1) {
+      if (q == 1) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[32];
+          if (!(mine && ok)) break;
+          ptx::tmem_ld32(t_o + 32 * c, v);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) sts_f(part_at + (32 * c + k) * 512, __uint_as_float(v[k]) * fe);
+        }
+        sts_u2(ml_at, __float_as_uint(m), __float_as_uint(mine && ok ? l : 0.f));
+      }
+      asm volatile("bar.sync 1, 256;" ::: "memory");   // the eight softmax warps
+      if (q == 0) {
+        const uint2 ml = lds_u2(ml_at);
+        const float m1 = __uint_as_float(ml.x), l1 = __uint_as_float(ml.y), top = fmaxf(m, m1);
+        f0 = exp2f(m - top);
+        f1 = l1 == 0.f ? 0.f : exp2f(m1 - top);
+        l = l * f0 + l1 * f1;
+        f0 *= fe;
+        m = top;
+      }
+    }
+    if (ok && (NQ == 2 || q == 0)) {
       const long long orow = (long long)(r0 + tok) * a.q_heads + hq;
       const bool store = live && KVQ_IN_BOUNDS(orow, (long long)a.s.rows * a.q_heads, a.status, a.bounds_site);
-      const float fe = eref > -1000 ? pow2f(eref) : 0.f;
       const bool part = p.splits > 1;
-      const float f = part ? fe : (l > 0.f ? fe / l : 0.f);
+      const float f = part ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+      f0 *= f;
+      f1 *= f;
       const long long prow = (long long)split * a.s.rows * a.q_heads + orow;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t v[32];
-        if (n_t > 0) {
+        if (mine) {
           ptx::tmem_ld32(t_o + 32 * c, v);   // warp-collective: every lane
         } else {
 #pragma unroll
           for (int k = 0; k < 32; ++k) v[k] = 0u;
+        }
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          float x = __uint_as_float(v[k]) * f0;
+          if (NQ == 1 && f1 != 0.f) x = fmaf(lds_f(part_at + (32 * c + k) * 512), f1, x);
+          v[k] = __float_as_uint(x);
         }
         if (!store) continue;
         if (part) {
           float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + 32 * c);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            dst[k] = make_float4(__uint_as_float(v[4 * k]) * f, __uint_as_float(v[4 * k + 1]) * f,
-                                 __uint_as_float(v[4 * k + 2]) * f, __uint_as_float(v[4 * k + 3]) * f);
+            dst[k] = make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]),
+                                 __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3]));
         } else {
           uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + 32 * c);
 #pragma unroll
@@ -477,8 +489,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
             uint32_t z[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(v[8 * k + 2 * i]) * f,
-                                                             __uint_as_float(v[8 * k + 2 * i + 1]) * f);
+              const __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(v[8 * k + 2 * i]),
+                                                             __uint_as_float(v[8 * k + 2 * i + 1]));
               z[i] = *reinterpret_cast<const uint32_t*>(&y);
             }
             dst[k] = make_uint4(z[0], z[1], z[2], z[3]);
@@ -487,7 +499,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
       }
       if (store) {
         if (part) *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(m, l);
-        else if (a.lse != nullptr) a.lse[orow] = l > 0.f ? 0.6931471805599453f * (m + log2f(l)) : -CUDART_INF_F;
+        else if (a.lse != nullptr) a.lse[orow] = l == 0.f ? -CUDART_INF_F : 0.6931471805599453f * (m + log2f(l));
       }
     }
   } else if (warp < C::kMmaWarp) {
@@ -559,7 +571,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
           // weights of 64 keys: 32 columns, 64 apart
           const int kk = 4 * half + k;
           ptx::mma_f16_ts(tmem + C::kTO + q * D, p_tmem + 64 * half + 8 * k,
-                          db + (uint64_t)((kk * 2048) >> 4), kIdO, (j > 0 || kk > 0) ? 1u : 0u);
+                          db + (uint64_t)((kk * 2048) >> 4), kIdO, (j > 2 - NQ || kk > 0) ? 1u : 0u);
         }
       };
       int ks = 0;
@@ -598,20 +610,17 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
 #pragma unroll
           for (int q = 0; q < NQ; ++q) {
             if (!ok) break;
-            if (C::kHalves && !(ok = page_wait(BAR(kCbP + q), j & 1, lim, abort, a.status))) break;
+            const int grp = NQ == 2 ? q : (j & 1);
+            const uint32_t par = NQ == 2 ? (j & 1) : ((j >> 1) & 1), t_p = tmem + grp * 128;
+            if (!(ok = page_wait(BAR(kCbP + grp), par, lim, abort, a.status))) break;
             if (q == 0 && !(ok = page_wait(BAR(kCbFullV + (j & 1)), (j >> 1) & 1, lim, abort, a.status))) break;
-            const uint32_t t_p = tmem + (NQ == 2 ? q : (j & 1)) * 128;
-            if (C::kHalves) {
-              ptx::tc_fence_after();
-              pv(j, q, 0, t_p);
-              ptx::mma_commit(BAR(kCbHalf + q));
-            }
-            if (!(ok = page_wait(BAR(kCbPb + q), j & 1, lim, abort, a.status))) break;
             ptx::tc_fence_after();
-            if (!C::kHalves) pv(j, q, 0, t_p);
-            pv(j, q, 1, t_p);
+            pv(j, grp, 0, t_p);
+            ptx::mma_commit(BAR(kCbHalf + grp));
+            if (!(ok = page_wait(BAR(kCbPb + grp), par, lim, abort, a.status))) break;
+            ptx::tc_fence_after();
+            pv(j, grp, 1, t_p);
             if (q == NQ - 1) ptx::mma_commit(BAR(kCbEmptyV + (j & 1)));
-            if (NQ == 1) ptx::mma_commit(BAR(kCbOStep));
             if (NQ == 2 && more) {
               if (q == 0 && !(ok = next_k())) break;
               qk(ks, q, tmem + q * 128);
@@ -755,13 +764,13 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
 #pragma unroll
     for (int c = 0; c < C; ++c) o[c] = fmaf(p.part_o[(s * step + row) * D + C * lane + c], f, o[c]);
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
   for (int c = 0; c < C; c += 2) {
     const __nv_bfloat162 y = __floats2bfloat162_rn(o[c] * inv, o[c + 1] * inv);
     *reinterpret_cast<uint32_t*>(a.out + row * D + C * lane + c) = *reinterpret_cast<const uint32_t*>(&y);
   }
-  if (lane == 0 && a.lse != nullptr) a.lse[row] = l > 0.f ? 0.6931471805599453f * (top + log2f(l)) : -CUDART_INF_F;
+  if (lane == 0 && a.lse != nullptr) a.lse[row] = l == 0.f ? -CUDART_INF_F : 0.6931471805599453f * (top + log2f(l));
 }
 
 }  // namespace

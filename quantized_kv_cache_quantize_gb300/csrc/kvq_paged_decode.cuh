@@ -1,7 +1,6 @@
 // Attention over the paged cache for few query rows per sequence (the rows of a
 // cache head: its group of query heads times the sequence's query tokens), the
-// form of a decoding step.  Up to 8 or 16 rows are an item; more rows are items
-// of their own, which find the keys in L2.
+// form of a decoding step, up to 16 rows.
 //
 // Per (sequence, cache head): s_j = c q . k_j, one pass over the keys with the
 // running maximum and sum of the softmax.  The keys are read once for all
@@ -48,6 +47,11 @@ namespace {
 
 constexpr int kUnit = 32;          // keys per unit
 constexpr int kMinUnits = 2;       // per warp, when the work is small
+// What an item's start costs the warp that comes to it from another one, in
+// units: its table entries, scales, query rows and first copies one after
+// another (64 sequences of up to 8192 keys, 8 heads: none 95.9, one 88.1, two
+// 85.5, three 86.5 us).
+constexpr int kStartUnits = 2;
 constexpr int kMaxCluster = 16;
 
 // W warps per CTA, one CTA per SM
@@ -67,20 +71,17 @@ struct DecodeArgs {
   long long* pre;      // [batch + 1] first unit of each sequence (written by CTA 0)
   float* part_o;       // [2 warps][rows_cap][D]
   float* part_ml;      // [2 warps][rows_cap][2]
-  int rows_cap;        // rows of an item at most: min(max_q * group, 8 NT)
-  int groups_cap;      // items per cache head at most
+  int rows_cap;        // rows of an item at most: max_q * group, up to 8 NT
   int warps;           // of the grid
   int cluster;         // CTAs per item (decode_item_kernel)
 };
 
 // What sequence b has to do: its rows, keys [lo, len) that any row attends to
-// (lo rounded down to a unit), units of an item, items of a cache head.
+// (lo rounded down to a unit), units of a cache head.
 struct SeqWork {
-  int r0, n, len, lo, units, groups;
+  int r0, n, len, lo, units;
   int seen;   // first key some row attends to; lo is this rounded down
 };
-// R: rows of an item
-template <int R>
 __device__ __forceinline__ SeqWork seq_work(const PagedAttnArgs& a, int b) {
   SeqWork w;
   seq_rows(a.s, b, w.r0, w.n, a.status);
@@ -94,7 +95,6 @@ __device__ __forceinline__ SeqWork seq_work(const PagedAttnArgs& a, int b) {
   w.lo = w.seen & ~(kUnit - 1);
   // a sequence with rows has one unit at least: it writes their empty result
   w.units = w.n > 0 ? max(1, (w.len - w.lo + kUnit - 1) / kUnit) : 0;
-  w.groups = (w.n * a.group + R - 1) / R;
   return w;
 }
 
@@ -134,13 +134,13 @@ struct Ring {
   uint32_t phase;
 };
 
-// One segment: units [i0, i0 + seg) of rows rb .. of (b, h), by one warp.  o, m,
-// l: for the rows rb + nt * 8 + 2 t + c (c = 0, 1) the channels CH g .. of sum p v (channel
+// One segment: units [i0, i0 + seg) of (b, h), by one warp.  o, m, l: for the
+// rows nt * 8 + 2 t + c (c = 0, 1) the channels CH g .. of sum p v (channel
 // 2 k + i in o[nt][k][c + 2 i]), the base in units of log 2 and sum p.  False
 // when a wait ran out.
 template <int D, int NT, int W>
 __device__ __forceinline__ bool decode_segment(const PagedAttnArgs& a, const CUtensorMap& map_k,
-                                               const CUtensorMap& map_v, Ring& rg, int b, int h, int rb,
+                                               const CUtensorMap& map_v, Ring& rg, int b, int h,
                                                const SeqWork& w, int i0, int seg,
                                                float (&o)[NT][D / 16][4], float (&m)[NT][2],
                                                float (&l)[NT][2]) {
@@ -160,7 +160,7 @@ __device__ __forceinline__ bool decode_segment(const PagedAttnArgs& a, const CUt
   uint2 raw[NT][KC * 4];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int r = rb + nt * 8 + g;
+    const int r = nt * 8 + g;
 #pragma unroll
     for (int k = 0; k < KC * 4; ++k) raw[nt][k] = make_uint2(0u, 0u);
     if (r < rows) {
@@ -250,7 +250,8 @@ __device__ __forceinline__ bool decode_segment(const PagedAttnArgs& a, const CUt
     // the maximum's exponent becomes 14 (a subnormal maximum's at most)
     const int e = max((int)(mx >> 7), 1) - 127 - 14;
     // x * 2^-e in two steps, each factor a normal number
-    const float f0 = pow2f(-(e / 2)), f1 = pow2f(-(e - e / 2));
+    // (an infinity or a NaN makes the whole row NaN)
+    const float f0 = mx < 0x7f80u ? pow2f(-(e / 2)) : CUDART_NAN_F, f1 = pow2f(-(e - e / 2));
 #pragma unroll
     for (int k = 0; k < KC * 4; ++k) {
       qf[nt][k][0] = ptx::f16x2_rn(__uint_as_float(raw[nt][k].x << 16) * f0 * f1, __uint_as_float(raw[nt][k].x & 0xffff0000u) * f0 * f1);
@@ -261,7 +262,7 @@ __device__ __forceinline__ bool decode_segment(const PagedAttnArgs& a, const CUt
       // column 2t + c is the row whose lanes have g = 2t + c
       const int ec = __shfl_sync(0xffffffffu, e, (2 * t + c) * 4);
       cq[nt][c] = scale_log2 * pow2f(ec / 2) * pow2f(ec - ec / 2);
-      const int rc = rb + nt * 8 + 2 * t + c;
+      const int rc = nt * 8 + 2 * t + c;
       const int tq = t0 + rc / a.group;
       hi_r[nt][c] = rc < rows ? (a.causal ? min(w.len, tq + 1) : w.len) : 0;
       lo_r[nt][c] = a.window > 0 ? max(0, tq - a.window + 1) : 0;
@@ -485,7 +486,7 @@ __device__ __forceinline__ void store_row(const PagedAttnArgs& a, const SeqWork&
   const int g = (threadIdx.x & 31) >> 2;
   const long long row = (long long)(w.r0 + r / a.group) * a.q_heads + h * a.group + r % a.group;
   if (!KVQ_IN_BOUNDS(row, (long long)a.s.rows * a.q_heads, a.status, a.bounds_site)) return;
-  const float f = l > 0.f ? 1.f / l : 0.f;
+  const float f = l == 0.f ? 0.f : 1.f / l;
   uint32_t v[CH / 2];
 #pragma unroll
   for (int k = 0; k < CH / 2; ++k) {
@@ -495,7 +496,7 @@ __device__ __forceinline__ void store_row(const PagedAttnArgs& a, const SeqWork&
   uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + CH * g);
 #pragma unroll
   for (int k = 0; k < CH / 8; ++k) dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-  if (g == 0 && a.lse != nullptr) a.lse[row] = l > 0.f ? 0.6931471805599453f * (m + log2f(l)) : -CUDART_INF_F;
+  if (g == 0 && a.lse != nullptr) a.lse[row] = l == 0.f ? -CUDART_INF_F : 0.6931471805599453f * (m + log2f(l));
 }
 
 template <int D, int NT, int W>
@@ -528,8 +529,8 @@ __global__ void __launch_bounds__(W * 32, 1)
     const int b = c0 + (int)threadIdx.x;
     long long v = 0;
     if (b < a.s.batch) {
-      const SeqWork x = seq_work<8 * NT>(a, b);
-      v = (long long)x.units * x.groups * heads;
+      const SeqWork x = seq_work(a, b);
+      v = x.units > 0 ? (long long)(x.units + kStartUnits) * heads : 0;
     }
     long long incl = v;
 #pragma unroll
@@ -586,19 +587,23 @@ __global__ void __launch_bounds__(W * 32, 1)
 
   Ring rg{ring, bars, 0, 0u};
   SeqWork w{};
-  if (u0 < u1) w = seq_work<8 * NT>(a, b);
-  int item = 0, i0 = 0;   // the sequence's items: (head, row group)
+  if (u0 < u1) w = seq_work(a, b);
+  int h = 0, i0 = 0;
   if (u0 < u1) {
-    item = (int)((u0 - at) / w.units);
-    i0 = (int)((u0 - at) % w.units);
+    h = (int)((u0 - at) / (w.units + kStartUnits));
+    i0 = (int)((u0 - at) % (w.units + kStartUnits)) - kStartUnits;
   }
   for (long long u = u0; u < u1;) {
+    if (i0 < 0) {   // the item's start
+      u -= i0;
+      i0 = 0;
+      if (u >= u1) break;
+    }
     const int seg = (int)min((long long)(w.units - i0), u1 - u);
     float o[NT][D / 16][4], m[NT][2], l[NT][2];
-    const int h = item / w.groups, rb = item % w.groups * (8 * NT);
-    if (!decode_segment<D, NT, W>(a, map_k, map_v, rg, b, h, rb, w, i0, seg, o, m, l)) break;
+    if (!decode_segment<D, NT, W>(a, map_k, map_v, rg, b, h, w, i0, seg, o, m, l)) break;
     // ---- its result: the item's, or a part of it ----
-    const int rows = min(w.n * a.group - rb, 8 * NT);
+    const int rows = w.n * a.group;
     const bool complete = seg == w.units;
     const long long slot = 2LL * gw + (u == u0 ? 0 : 1);
 #pragma unroll
@@ -608,7 +613,7 @@ __global__ void __launch_bounds__(W * 32, 1)
         const int r = nt * 8 + 2 * t + c;
         if (r >= rows) continue;
         if (complete) {
-          store_row<D, NT>(a, w, h, rb + r, o, nt, c, m[nt][c], l[nt][c]);
+          store_row<D, NT>(a, w, h, r, o, nt, c, m[nt][c], l[nt][c]);
         } else {
           float4* dst = reinterpret_cast<float4*>(p.part_o + (slot * p.rows_cap + r) * D + CH * g);
 #pragma unroll
@@ -620,12 +625,12 @@ __global__ void __launch_bounds__(W * 32, 1)
       }
     // ---- the next segment ----
     u += seg;
-    i0 = 0;
-    if (u < u1 && ++item == heads * w.groups) {
-      item = 0;
+    i0 = -kStartUnits;
+    if (u < u1 && ++h == heads) {
+      h = 0;
       do {
         ++b;
-        w = seq_work<8 * NT>(a, b);
+        w = seq_work(a, b);
       } while (w.units == 0 && b + 1 < a.s.batch);
       if (w.units == 0) break;   // not with lengths that hold still during the call
     }
@@ -657,19 +662,18 @@ __global__ void __launch_bounds__(W * 32, 1)
   }
   __syncwarp();
   ptx::grid_dependency_wait();
+  ptx::launch_dependents();
   // CTAs of a cluster are neighbours in the grid
   const unsigned ctas = (unsigned)p.cluster, rank = blockIdx.x % ctas, item = blockIdx.x / ctas;
-  const int rb = (int)(item % (unsigned)p.groups_cap) * R;
-  const unsigned bh = item / (unsigned)p.groups_cap;
-  const int b = (int)(bh / (unsigned)a.p.heads), h = (int)(bh % (unsigned)a.p.heads);
-  const SeqWork w = seq_work<R>(a, b);
-  const int rows = w.units > 0 ? max(0, min(w.n * a.group - rb, R)) : 0;
+  const int b = (int)(item / (unsigned)a.p.heads), h = (int)(item % (unsigned)a.p.heads);
+  const SeqWork w = seq_work(a, b);
+  const int rows = w.n * a.group;
   const long long parts = (long long)ctas * W;
   auto begin = [&](int warp) { return (int)((long long)w.units * ((int)rank * W + warp) / parts); };
   const int i0 = begin(wid), i1 = rows > 0 ? begin(wid + 1) : i0;
   float o[NT][D / 16][4], m[NT][2], l[NT][2];
   bool ok = true;
-  if (i1 > i0) ok = decode_segment<D, NT, W>(a, map_k, map_v, rg, b, h, rb, w, i0, i1 - i0, o, m, l);
+  if (i1 > i0) ok = decode_segment<D, NT, W>(a, map_k, map_v, rg, b, h, w, i0, i1 - i0, o, m, l);
   // a warp without units, or whose copies did not come, has no part (its
   // weights are zero)
   const bool part_of = i1 > i0 && ok;
@@ -697,17 +701,16 @@ __global__ void __launch_bounds__(W * 32, 1)
   }
   __syncthreads();
   auto store = [&](int r, const float (&v)[D / 32], float top, float ls) {
-    const int rr = rb + r;
-    const long long row = (long long)(w.r0 + rr / a.group) * a.q_heads + h * a.group + rr % a.group;
+    const long long row = (long long)(w.r0 + r / a.group) * a.q_heads + h * a.group + r % a.group;
     if (!KVQ_IN_BOUNDS(row, (long long)a.s.rows * a.q_heads, a.status, a.bounds_site)) return;
-    const float f = ls > 0.f ? 1.f / ls : 0.f;
+    const float f = ls == 0.f ? 0.f : 1.f / ls;
 #pragma unroll
     for (int c = 0; c < D / 32; c += 2) {
       const __nv_bfloat162 z = __floats2bfloat162_rn(v[c] * f, v[c + 1] * f);
       *reinterpret_cast<uint32_t*>(a.out + row * D + (D / 32) * lane + c) = *reinterpret_cast<const uint32_t*>(&z);
     }
     if (lane == 0 && a.lse != nullptr)
-      a.lse[row] = ls > 0.f ? 0.6931471805599453f * (top + log2f(ls)) : -CUDART_INF_F;
+      a.lse[row] = ls == 0.f ? -CUDART_INF_F : 0.6931471805599453f * (top + log2f(ls));
   };
   // a warp per row, the parts in order
   for (int r = wid; r < rows; r += W) {
@@ -764,7 +767,7 @@ __global__ void __launch_bounds__(W * 32, 1)
 // 2^(m - M), the parts in order.  The block's warps take every fourth part, 32
 // lanes hold the channels.
 constexpr int kJoinWarps = 4;
-template <int D, int R>
+template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ DecodeArgs p) {
   constexpr int C = D / 32;
   __shared__ float sum_o[kJoinWarps][D];
@@ -778,15 +781,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
   int r0, n;
   seq_rows(a.s, b, r0, n, a.status);
   n = min(n, a.max_q);
-  const int groups = (n * a.group + R - 1) / R;
   if (r >= n * a.group) return;
-  const long long s0 = p.pre[b], units = (p.pre[b + 1] - s0) / (heads * groups), total = p.pre[a.s.batch];
+  const long long s0 = p.pre[b], span = (p.pre[b + 1] - s0) / heads, total = p.pre[a.s.batch];
   const long long per = max((total + p.warps - 1) / p.warps, (long long)kMinUnits);
-  const long long first = s0 + (h * groups + r / R) * units;
-  const long long wa = first / per, wb = (first + units - 1) / per;
+  const long long first = s0 + h * span + kStartUnits;
+  const long long wa = first / per, wb = (first + span - kStartUnits - 1) / per;
   if (wa == wb) return;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  auto slot = [&](long long w) { return (2 * w + (w == wa && first > wa * per ? 1 : 0)) * p.rows_cap + r % R; };
+  auto slot = [&](long long w) { return (2 * w + (w == wa && first > wa * per ? 1 : 0)) * p.rows_cap + r; };
   float top = -CUDART_INF_F;
   for (long long w = wa + threadIdx.x; w <= wb; w += kJoinWarps * 32) top = fmaxf(top, p.part_ml[slot(w) * 2]);
 #pragma unroll
@@ -821,11 +823,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     float v = 0.f;
 #pragma unroll
     for (int k = 0; k < kJoinWarps; ++k) v += sum_o[k][c];
-    const __nv_bfloat16 z = __float2bfloat16_rn(ls > 0.f ? v / ls : 0.f);
+    const __nv_bfloat16 z = __float2bfloat16_rn(ls == 0.f ? 0.f : v / ls);
     a.out[row * D + c] = *reinterpret_cast<const uint16_t*>(&z);
   }
   if (threadIdx.x == 0 && a.lse != nullptr)
-    a.lse[row] = ls > 0.f ? 0.6931471805599453f * (top + log2f(ls)) : -CUDART_INF_F;
+    a.lse[row] = ls == 0.f ? -CUDART_INF_F : 0.6931471805599453f * (top + log2f(ls));
 }
 
 }  // namespace

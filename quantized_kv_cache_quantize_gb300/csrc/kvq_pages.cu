@@ -35,7 +35,7 @@ __device__ __forceinline__ bool append_item(const AppendArgs& a, int item, int& 
   end = len;
   r0 += first - start;                      // row of token `first`
   p += first >> a.p.shift;
-  return (p << a.p.shift) < end;
+  return p <= (end - 1) >> a.p.shift;       // (end may be 0)
 }
 
 // Earlier codes [row][D] of rows [0, lo) under a scale grown by 2^-shift
@@ -144,6 +144,7 @@ template <int D>
 __global__ void __launch_bounds__(128) append_one_kernel(const __grid_constant__ AppendArgs a) {
   const int lane = threadIdx.x & 31;
   ptx::grid_dependency_wait();
+  ptx::launch_dependents();
   const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int kv = (int)(w & 1), head = (int)((w >> 1) % a.p.heads);
   const long long item = (w >> 1) / a.p.heads;
