@@ -426,12 +426,11 @@ typedef struct kvq_pages {
  *            those of pages wholly before every row's window.  width *
  *            page_tokens <= 2^30 (else KVQ_ERR_TOO_LARGE).
  *   kv_lens  int32 [batch]: tokens per sequence (0 is allowed).
- *   offsets  int32 [batch + 1], ascending from 0: rows [offsets[b],
- *            offsets[b + 1]) of the call's packed row tensor belong to
- *            sequence b (none is allowed).  NULL: one row per sequence
- *            (rows == batch).
- *   rows     rows of the packed tensor; rows at or behind offsets[batch] are
- *            neither read nor written.
+ *   offsets  int32 [batch + 1], ascending: rows [offsets[b], offsets[b + 1])
+ *            of the call's packed row tensor belong to sequence b (none is
+ *            allowed).  NULL: one row per sequence (rows == batch).
+ *   rows     rows of the packed tensor, <= 2^30; those before offsets[0] and
+ *            those at or behind offsets[batch] are neither read nor written.
  * A table entry outside [0, n_pages), a length outside [0, width *
  * page_tokens] or an offset outside [0, rows] makes the call skip what it
  * points at and record KVQ_ERR_PAGE in the device status word (see
@@ -474,8 +473,8 @@ kvq_status kvq_pages_append(const kvq_pages *pages, int32_t layer, const uint16_
 /*
  * Workspace bytes of kvq_paged_attention for this pool, q_heads, rows query
  * rows in batch sequences of at most max_q rows each, and a table of `width`
- * entries per sequence.  Depends on the current device's SM count.  0 on a
- * bad argument; 16 when the call needs none (workspace may be NULL then).
+ * entries per sequence (max_q = 1 for a call without offsets).  Depends on
+ * the current device.  0 on a bad argument; 16 when the call needs none (workspace may be NULL then).
  */
 size_t kvq_paged_workspace_bytes(const kvq_pages *pages, int32_t q_heads, int32_t batch,
                                  int32_t width, int32_t rows, int32_t max_q);
@@ -493,7 +492,8 @@ size_t kvq_paged_workspace_bytes(const kvq_pages *pages, int32_t q_heads, int32_
  *   lse = log sum_j exp(s_j).
  * A row that attends to nothing gets out = 0, lse = -infinity.  What masked
  * places hold (NaN codes among it) does not matter when no row of the
- * sequence's query heads attends there.
+ * sequence's query heads attends there.  A query row that holds a NaN or an
+ * infinity gives NaN.
  * out: BF16 [rows][q_heads][head_dim] device, contiguous; lse: fp32
  * [rows][q_heads] device or NULL.  max_q: at least the largest n_b (rows
  * beyond it are not computed and record KVQ_ERR_PAGE).  workspace: device,
@@ -522,8 +522,8 @@ kvq_status kvq_pages_copy(const kvq_pages *pages, const int32_t *src, const int3
  * (a page is freed by writing -1 over its entries; an entry < 0 is empty).
  * With n live pages, those with ids >= n move, in ascending order, into the
  * free ids below n, in ascending order, in every layer.  table_out (int32
- * [batch][width], rows table_out_stride apart; may be the input table with
- * its stride) gets the new ids, empty entries as they were; n_live (int32
+ * [batch][width], rows table_out_stride apart; the input table with its
+ * stride, or memory that does not overlap it) gets the new ids, empty entries as they were; n_live (int32
  * device, one element) gets n: pages [n, n_pages) are free afterwards.
  * Entries >= n_pages record KVQ_ERR_PAGE and stay as they are.  n_pages <=
  * 2^20 (else KVQ_ERR_TOO_LARGE).  workspace: device, 16-byte aligned, >=

@@ -46,7 +46,7 @@ kvq_status check_sequences(const kvq_sequences* s, int page_tokens) {
   if (s == nullptr || s->batch < 0 || s->width < 0 || s->rows < 0) return KVQ_ERR_INVALID_ARG;
   if (s->offsets == nullptr && s->rows != s->batch) return KVQ_ERR_INVALID_ARG;
   if (s->batch > (1 << 24)) return KVQ_ERR_INVALID_ARG;
-  if ((long long)s->width * page_tokens > (1LL << 30)) return KVQ_ERR_TOO_LARGE;
+  if ((long long)s->width * page_tokens > (1LL << 30) || s->rows > (1 << 30)) return KVQ_ERR_TOO_LARGE;
   if (s->rows == 0) return KVQ_OK;
   if (s->batch < 1 || s->kv_lens == nullptr) return KVQ_ERR_INVALID_ARG;
   if (s->width > 0 && s->table == nullptr) return KVQ_ERR_INVALID_ARG;
@@ -181,7 +181,7 @@ kvq_status kvq_paged_attention(const kvq_pages* pages, int32_t layer, const uint
   a.group = q_heads / pages->kv_heads;
   a.max_q = max_q;
   a.causal = causal != 0;
-  a.window = window;
+  a.window = std::min(window, 1 << 30);   // no sequence is longer; t - window stays in 32 bits
   a.scale = scale;
   a.out = out;
   a.lse = lse;

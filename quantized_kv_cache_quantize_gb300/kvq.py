@@ -589,6 +589,12 @@ def _sequences(cache: PagedCache, rows: int, block_table, kv_lens, offsets) -> S
                            kv_lens.data_ptr(), None if offsets is None else offsets.data_ptr(), rows)
 
 
+def _int32(name: str, value: int):
+    """ctypes would drop the upper bits of what does not fit."""
+    if not -0x80000000 <= value <= 0x7FFFFFFF:
+        raise ValueError(f"{name} is {value}, beyond 32 bits")
+
+
 def pages_append(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor,
                  block_table: torch.Tensor, kv_lens: torch.Tensor, offsets=None, layer: int = 0,
                  stream=None):
@@ -596,6 +602,7 @@ def pages_append(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor,
     of all sequences packed (rows offsets[b] .. offsets[b + 1] are sequence
     b's; None: one row each), appended so that sequence b then holds
     kv_lens[b] tokens."""
+    _int32("layer", layer)
     shape, ks = _paged_rows(cache, k_new, "k_new")
     shape_v, vs = _paged_rows(cache, v_new, "v_new")
     if shape != shape_v or shape[1] != cache.kv_heads:
@@ -617,6 +624,9 @@ def paged_attention(cache: PagedCache, q: torch.Tensor, block_table: torch.Tenso
     tokens).  max_q: the most rows a sequence has (default: all of them).
     Returns out [rows, q_heads, head_dim] (and lse [rows, q_heads] fp32 with
     with_lse)."""
+    _int32("layer", layer)
+    _int32("window", window)
+    _int32("max_q", max_q or 0)
     shape, qs = _paged_rows(cache, q, "q")
     rows, q_heads, d = shape
     if q_heads < 1 or q_heads % cache.kv_heads:

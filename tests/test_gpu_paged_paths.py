@@ -128,6 +128,21 @@ def test_row_that_is_not_finite(d, hq, n, batch, bad):
     check_some(cache, got, q, table, lens, counts, [at // n], 1 / np.sqrt(d), True, 0)
 
 
+@pytest.mark.parametrize("n,hq", [(8, 2), (40, 2)])
+def test_widest_window(n, hq):
+    """A window of 2^31 - 1 hides nothing, nor from rows before the first key."""
+    cache = kvq.PagedCache.zeros(1, 4, 1, 16, 64)
+    fill(cache, 6)
+    lens = [2, 30]
+    table = shuffled_table(lens, 16, 4, 7)
+    q = torch.randn(2 * n, hq, 64, device="cuda").bfloat16()
+    call = lambda w: kvq.paged_attention(cache, q, table, dev(lens), offsets_of([n, n]), max_q=n, causal=False, window=w,
+                                         with_lse=True)
+    a, b = call(0), call(0x7FFFFFFF)
+    clean()
+    assert torch.isfinite(a[1]).all() and torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 @pytest.mark.parametrize("n,hq", [(1, 4), (20, 2)])
 def test_rows_behind_the_last_sequence_stay(n, hq):
     cache = kvq.PagedCache.zeros(1, 20, 2, 16, 64)

@@ -260,3 +260,17 @@ def test_binding_refusals(lib):
             kvq.pages_copy(cache, src, dst)
     with pytest.raises(ValueError, match="not a CUDA device"):
         kvq.pages_copy(cache, [1], [2])
+
+
+def test_arguments_beyond_32_bits(lib):
+    """Refused, not cut: 2^32 + 5 would arrive as a window of 5."""
+    codes = torch.zeros(1, 2, 1, 16, 64, dtype=torch.uint8).view(torch.float8_e4m3fn)
+    cache = kvq.PagedCache(codes, codes.clone(), *[torch.ones(1, 2, 1, dtype=torch.bfloat16) for _ in range(2)])
+    x, table, lens = torch.zeros(1, 1, 64), torch.zeros(1, 1, dtype=torch.int32), torch.ones(1, dtype=torch.int32)
+    for kw in (dict(window=(1 << 32) + 5), dict(layer=1 << 32), dict(max_q=(1 << 33) + 1)):
+        with pytest.raises(ValueError, match="beyond 32 bits"):
+            kvq.paged_attention(cache, x, table, lens, **kw)
+    with pytest.raises(ValueError, match="beyond 32 bits"):
+        kvq.pages_append(cache, x, x, table, lens, layer=-(1 << 32))
+    assert _attend(lib, s=_seqs(rows=(1 << 30) + 1, offsets=PTR)) == kvq.KVQ_ERR_TOO_LARGE
+    assert _append(lib, s=_seqs(rows=(1 << 30) + 1, offsets=PTR)) == kvq.KVQ_ERR_TOO_LARGE
