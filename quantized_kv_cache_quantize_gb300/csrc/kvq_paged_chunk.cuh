@@ -5,7 +5,14 @@
 // token r / group, head r % group, and a CTA takes 128 NQ of them over all
 // their keys, 128 at a time: S = c Q K^T, O += P V with the running base and
 // sum of the softmax.  4 d flops per row and key against 2 d bytes per key and
-// CTA: bound by the tensor cores, then by the exponentials and what feeds them.
+// CTA: bound by the tensor cores.  Measured (24 heads of 128 channels, 4680 rows,
+// 23400 keys): 1.02 ms, 1320 TFLOP/s; 3720 cycles a tile of 128 keys and 256
+// rows, of which the products take 2048 at their nominal rates.  They do not
+// reach them: Q K^T reads both operands from shared memory, all of its 128
+// bytes a cycle, beside the conversion of V and the tiles that arrive.
+// (Leaving out the exponentials saves 2 %, the conversion nothing; scores in
+// halves of 64 keys, so that the next ones start earlier, read the query twice
+// as often: 1.34 ms.)
 //
 // Products on tcgen05, accumulators in tensor memory.
 // - Q K^T: the E4M3 key tile goes from the page by TMA straight to the tensor
