@@ -19,8 +19,8 @@ namespace {
 // tiles are what a warp's registers hold.  Past them it would read the keys
 // again from L2, and the tensor-core form, which works on 128 rows however few
 // there are, is as good or better.  Decoding / tensor-core form in us, 32
-// sequences of 16384 keys, 8 heads of 128 channels: 16 rows 183 / 283, 24 rows
-// in two passes 343 / 283; 64 channels: 148 / 247, 278 / 247.
+// sequences of 16384 keys, 8 heads of 128 channels: 16 rows 183 / 258, 24 rows
+// in two passes 343 / 258; 64 channels: 148 / 245, 278 / 245.
 constexpr int kDecRows = 16;
 
 std::atomic<uint64_t> g_decode_smem[2][2], g_decode12_smem[2], g_item_smem[2][2], g_item_wide[2][2];
@@ -193,10 +193,10 @@ int split_limit(int sms, long long ctas) {
   return (int)(s > kMaxSplits ? kMaxSplits : s);
 }
 // Query tiles of 128 rows a CTA: one or two.  Two against one in us, 32
-// sequences of 16384 keys, 8 heads of 128 channels: 128 rows 443 / 290, 144
-// rows 472 / 570, 256 rows 480 / 576; 16 of 4096: 64.5 / 46.4, 69.2 / 87.7,
-// 72.6 / 90.1.  (With few CTAs, 4 sequences of 2048 keys, one is the better at
-// 256 rows, 29.9 / 26.0, and past that.)
+// sequences of 16384 keys, 8 heads of 128 channels: 128 rows 444 / 266, 144
+// rows 459 / 521, 256 rows 467 / 531; 16 of 4096: 64.8 / 43.8, 67.7 / 81.7,
+// 70.4 / 84.4.  (With few CTAs, 4 sequences of 2048 keys, one is the better at
+// 256 rows, 28.0 / 25.2, and past that.)
 int query_tiles(long long cap) { return cap <= 128 ? 1 : 2; }
 long long chunk_tiles(int batch, int heads, long long cap, int* q_tiles) {
   const int per = 128 * query_tiles(cap);

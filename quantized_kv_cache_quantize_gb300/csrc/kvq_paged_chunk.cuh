@@ -6,13 +6,14 @@
 // their keys, 128 at a time: S = c Q K^T, O += P V with the running base and
 // sum of the softmax.  4 d flops per row and key against 2 d bytes per key and
 // CTA: bound by the tensor cores.  Measured (24 heads of 128 channels, 4680 rows,
-// 23400 keys): 1.02 ms, 1320 TFLOP/s; 3720 cycles a tile of 128 keys and 256
+// 23400 keys): 0.96 ms, 1400 TFLOP/s; 3500 cycles a tile of 128 keys and 256
 // rows, of which the products take 2048 at their nominal rates.  They do not
 // reach them: Q K^T reads both operands from shared memory, all of its 128
-// bytes a cycle, beside the conversion of V and the tiles that arrive.
-// (Leaving out the exponentials saves 2 %, the conversion nothing; scores in
-// halves of 64 keys, so that the next ones start earlier, read the query twice
-// as often: 1.34 ms.)
+// bytes a cycle, and every commit and every instruction of the issuing thread
+// shows (a commit less a tile 2 %, its loop unrolled by two tiles 2 %).
+// Leaving out the exponentials would save 2 %, the conversion of V nothing;
+// scores in halves of 64 keys, so that the next ones start earlier, read the
+// query twice as often: 1.34 ms.
 //
 // Products on tcgen05, accumulators in tensor memory.
 // - Q K^T: the E4M3 key tile goes from the page by TMA straight to the tensor
@@ -36,7 +37,7 @@
 // each key tile is read and converted once for 256 rows.  With NQ = 1 (at most
 // 128 rows a head) the groups take the key tiles of one query tile in turn,
 // each with its own base, sum and O, and join at the end: with one group alone
-// 64 rows of 32 sequences, 16384 keys and 8 heads took 440 us, not 286.
+// 64 rows of 32 sequences, 16384 keys and 8 heads took 440 us, not 261.
 #pragma once
 
 #include <math_constants.h>
@@ -48,7 +49,7 @@ namespace kvq {
 namespace {
 
 constexpr int kTileKeys = 128;
-constexpr int kKStages = 3, kVStages = 2, kMetaSlots = 8;
+constexpr int kVStages = 2, kMetaSlots = 8;
 // a slot of a tile's page scales, per block of 16 keys: 2^e of K [8], the V
 // exponent relative to eref [8] (as float) and 2^-that [8]; then eref and the
 // mask of blocks whose page is there
@@ -56,6 +57,7 @@ constexpr int kMetaBytes = 128, kMetaShift = 32, kMetaInv = 64, kMetaRef = 96;
 
 template <int D, int NQ>
 struct ChunkCfg {
+  static constexpr int kKStages = NQ == 2 ? 2 : 3;
   static constexpr int kQT = 128 * D;              // one E4M3 query tile
   static constexpr int kQ = 0;                     // [NQ][high, low]
   static constexpr int kK = NQ * 2 * kQT;          // key codes
@@ -76,23 +78,26 @@ struct ChunkCfg {
   static_assert(kAlloc <= 232448, "shared memory");
 };
 
+// A commit costs the tensor core some of its time (one less a tile: 2 %), so
+// nothing is signalled twice.  "Scores of a tile ready" also says that all
+// products issued before them are done, which frees a key stage and a value
+// stage; there are as many barriers for it as keep their phases apart.
 enum : int {
   kCbQ = 0,         // query tiles written (4 NQ arrivals, one per warp)
-  kCbFullK = 1,     // [3] key codes landed, page exponents written
-  kCbEmptyK = 4,    // [3] the tile's QK MMAs done
-  kCbFullVr = 7,    // [2] value codes landed
-  kCbEmptyVr = 9,   // [2] value codes read (4 arrivals)
-  kCbFullV = 11,    // [2] FP16 values written (4 arrivals)
-  kCbEmptyV = 13,   // [2] the tile's PV MMAs done
-  kCbS = 15,        // [2] scores of a group's tile ready
-  kCbP = 17,        // [2] weights of keys 0-63 written, O rescaled (4 arrivals)
-  kCbODone = 19,    // every MMA done
-  kCbMeta = 20,     // [8] a tile's page exponents written.  Not the key
+  kCbFullK = 1,     // [3] key codes landed
+  kCbFullVr = 4,    // [2] value codes landed
+  kCbEmptyVr = 6,   // [2] value codes read (4 arrivals)
+  kCbFullV = 8,     // [2] FP16 values written (4 arrivals)
+  kCbS = 10,        // [4] scores ready: tile j of query tile q at 2 q + j % 2
+                    // (NQ = 2), tile j at j % 4 (NQ = 1)
+  kCbP = 14,        // [2] weights of keys 0-63 written, O rescaled (4 arrivals)
+  kCbPb = 16,       // [2] weights of keys 64-127 written (4 arrivals)
+  kCbHalf = 18,     // [2] PV of keys 0-63 done
+  kCbODone = 20,    // every MMA done
+  kCbMeta = 21,     // [8] a tile's page exponents written.  Not the key
                     // barrier: its stage can be refilled, and its phase
                     // passed twice, before a slow softmax warp looks at it
-  kCbPb = 28,       // [2] weights of keys 64-127 written (4 arrivals)
-  kCbHalf = 30,     // [2] PV of keys 0-63 done
-  kCbCount = 32
+  kCbCount = 29
 };
 
 struct ChunkArgs {
@@ -216,16 +221,12 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
   auto BAR = [&](int i) { return bar0 + 8u * (uint32_t)i; };
   if (tid == 0) {
     ptx::mbar_init(BAR(kCbQ), 4 * NQ);
-    for (int i = 0; i < kKStages; ++i) {
-      ptx::mbar_init(BAR(kCbFullK + i), 1);
-      ptx::mbar_init(BAR(kCbEmptyK + i), 1);
-    }
+    for (int i = 0; i < C::kKStages; ++i) ptx::mbar_init(BAR(kCbFullK + i), 1);
+    for (int i = 0; i < 4; ++i) ptx::mbar_init(BAR(kCbS + i), 1);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(BAR(kCbFullVr + i), 1);
       ptx::mbar_init(BAR(kCbEmptyVr + i), 4);
       ptx::mbar_init(BAR(kCbFullV + i), 4);
-      ptx::mbar_init(BAR(kCbEmptyV + i), 1);
-      ptx::mbar_init(BAR(kCbS + i), 1);
       ptx::mbar_init(BAR(kCbP + i), 4);
       ptx::mbar_init(BAR(kCbPb + i), 4);
       ptx::mbar_init(BAR(kCbHalf + i), 1);
@@ -245,6 +246,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const unsigned long long lim = a.wait_limit_ns;
   const uint32_t sm = ptx::smem_u32(smem);
+  // barrier and phase of tile j's scores (query tile q)
+  auto s_bar = [](int q, int j) { return kCbS + (NQ == 2 ? 2 * q + (j & 1) : (j & 3)); };
+  auto s_par = [](int j) { return (uint32_t)(NQ == 2 ? j >> 1 : j >> 2) & 1u; };
 
   if (warp < C::kSoftmaxWarps) {
     // =========================== softmax ===========================
@@ -318,9 +322,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
       const uint32_t par = NQ == 2 ? (j & 1) : ((j >> 1) & 1);
       const bool first = NQ == 2 ? j == 0 : j < 2;
       // a slot of scales is written again 8 tiles later, the TMA warp at most
-      // 5 ahead of the softmax (3 key stages, 2 score buffers)
+      // 5 ahead of the softmax (key stages and score buffers)
       ok = page_wait(BAR(kCbMeta + (j & (kMetaSlots - 1))), (j / kMetaSlots) & 1, lim, abort, a.status) &&
-           page_wait(BAR(kCbS + q), par, lim, abort, a.status);
+           page_wait(BAR(s_bar(q, j)), s_par(j), lim, abort, a.status);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
@@ -530,7 +534,12 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
         if (!use) raw[c] = make_uint4(0u, 0u, 0u, 0u);
       }
       warp_arrive(BAR(kCbEmptyVr + s));
-      if (j >= 2 && !page_wait(BAR(kCbEmptyV + s), par ^ 1u, lim, abort, a.status)) break;
+      // PV of tile j - 2 is done with this stage: it was issued before the
+      // scores of tile j - 1 of the second query tile (NQ = 1: of tile j)
+      if (j >= 2) {
+        const int after = NQ == 2 ? j - 1 : j;
+        if (!page_wait(BAR(s_bar(1, after)), s_par(after), lim, abort, a.status)) break;
+      }
       const uint32_t dst = sm + C::kV + s * C::kVT;
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
@@ -571,8 +580,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
             ptx::mma_f8(dst, da + (uint64_t)(2 * k), db + (uint64_t)(2 * k), kIdS, (part > 0 || k > 0) ? 1u : 0u);
         }
       };
-      auto pv = [&](int j, int q, int half, uint32_t p_tmem) {
-        const uint64_t db = plus(dv, C::kV + (j & 1) * C::kVT);
+      auto pv = [&](int j, int vs, int q, int half, uint32_t p_tmem) {
+        const uint64_t db = plus(dv, C::kV + vs * C::kVT);
 #pragma unroll
         for (int k = 0; k < kTileKeys / 32; ++k) {
           // weights of 64 keys: 32 columns, 64 apart
@@ -589,8 +598,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
         return good;
       };
       auto step_k = [&]() {
-        ptx::mma_commit(BAR(kCbEmptyK + ks));
-        if (++ks == kKStages) {
+        if (++ks == C::kKStages) {
           ks = 0;
           kph ^= 1u;
         }
@@ -602,37 +610,47 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
 #pragma unroll
           for (int q = 0; q < NQ; ++q) {
             qk(ks, q, tmem + q * 128);
-            ptx::mma_commit(BAR(kCbS + q));
+            ptx::mma_commit(BAR(s_bar(q, 0)));
           }
           step_k();
         }
-        for (int j = 0; j < n_t && ok; ++j) {
-          const bool more = j + 1 < n_t;
-          if (NQ == 1 && more) {
-            if (!(ok = next_k())) break;
-            qk(ks, 0, tmem + ((j + 1) & 1) * 128);
-            ptx::mma_commit(BAR(kCbS + ((j + 1) & 1)));
-            step_k();
-          }
+        // two tiles a turn: stages and barriers that alternate are constants
+        // then (the issue of one group's products waits behind this thread)
+        for (int j0 = 0; j0 < n_t && ok; j0 += 2) {
+          const uint32_t ph = (uint32_t)(j0 >> 1) & 1u;   // of what alternates by tiles
 #pragma unroll
-          for (int q = 0; q < NQ; ++q) {
-            if (!ok) break;
-            const int grp = NQ == 2 ? q : (j & 1);
-            const uint32_t par = NQ == 2 ? (j & 1) : ((j >> 1) & 1), t_p = tmem + grp * 128;
-            if (!(ok = page_wait(BAR(kCbP + grp), par, lim, abort, a.status))) break;
-            if (q == 0 && !(ok = page_wait(BAR(kCbFullV + (j & 1)), (j >> 1) & 1, lim, abort, a.status))) break;
-            ptx::tc_fence_after();
-            pv(j, grp, 0, t_p);
-            ptx::mma_commit(BAR(kCbHalf + grp));
-            if (!(ok = page_wait(BAR(kCbPb + grp), par, lim, abort, a.status))) break;
-            ptx::tc_fence_after();
-            pv(j, grp, 1, t_p);
-            if (q == NQ - 1) ptx::mma_commit(BAR(kCbEmptyV + (j & 1)));
-            if (NQ == 2 && more) {
-              if (q == 0 && !(ok = next_k())) break;
-              qk(ks, q, tmem + q * 128);
-              ptx::mma_commit(BAR(kCbS + q));
-              if (q == NQ - 1) step_k();
+          for (int u = 0; u < 2; ++u) {
+            const int j = j0 + u;
+            if (!ok || j >= n_t) break;
+            const bool more = j + 1 < n_t;
+            if (NQ == 1 && more) {
+              if (!(ok = next_k())) break;
+              qk(ks, 0, tmem + ((u + 1) & 1) * 128);
+              ptx::mma_commit(BAR(s_bar(0, j + 1)));
+              step_k();
+            }
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+              if (!ok) break;
+              const int grp = NQ == 2 ? q : u;
+              const uint32_t par = NQ == 2 ? (uint32_t)u : ph, t_p = tmem + grp * 128;
+              if (!(ok = page_wait(BAR(kCbP + grp), par, lim, abort, a.status))) break;
+              if (q == 0 && !(ok = page_wait(BAR(kCbFullV + u), ph, lim, abort, a.status))) break;
+              ptx::tc_fence_after();
+              pv(j, u, grp, 0, t_p);
+              ptx::mma_commit(BAR(kCbHalf + grp));
+              if (!(ok = page_wait(BAR(kCbPb + grp), par, lim, abort, a.status))) break;
+              ptx::tc_fence_after();
+              pv(j, u, grp, 1, t_p);
+              if (NQ == 2 && more) {
+                const int kst = (u + 1) & 1;
+                if (q == 0) {
+                  if (!(ok = page_wait(BAR(kCbFullK + kst), ph ^ (uint32_t)u, lim, abort, a.status))) break;
+                  ptx::tc_fence_after();
+                }
+                qk(kst, q, tmem + q * 128);
+                ptx::mma_commit(BAR(kCbS + 2 * q + kst));
+              }
             }
           }
         }
@@ -665,7 +683,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
     BlockPage four = look(0), next_four = look(4);
     int eref = -1000;   // largest V exponent so far
     int ks = 0, last_k = -1, last_v = -1;
-    uint32_t kph = 0;
     bool ok = true;
     for (int j = 0; j < n_t; ++j) {
       if (j > 0 && (j & 3) == 0) {
@@ -681,7 +698,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
       const bool box = cur.id >= 0 && ((16 * lane) & (a.p.page - 1)) == 0;
       const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, box));
       const uint32_t bytes = boxes * (uint32_t)(a.p.page * D);
-      if (j >= kKStages) ok = page_wait(BAR(kCbEmptyK + ks), kph ^ 1u, lim, abort, a.status);
+      if (j >= C::kKStages) {   // the scores of the tile before in this stage are ready
+        const int before = j - C::kKStages;
+        ok = page_wait(BAR(s_bar(NQ - 1, before)), s_par(before), lim, abort, a.status);
+      }
       if (!__all_sync(0xffffffffu, ok)) break;
       {
         const uint32_t mt = sm + C::kMeta + (j & (kMetaSlots - 1)) * kMetaBytes;
@@ -715,14 +735,11 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
         ptx::tma_load_3d(s_base + C::kVr + (j & 1) * C::kKT + 16 * lane * D, &map_v, 0, 0, cur.id * heads + h,
                          BAR(kCbFullVr + (j & 1)));
       last_v = j;
-      if (++ks == kKStages) {
-        ks = 0;
-        kph ^= 1u;
-      }
+      if (++ks == C::kKStages) ks = 0;
     }
     // no copy is in flight when the CTA exits, however the others ended
-    for (int j = max(0, last_k - kKStages + 1); j <= last_k; ++j)
-      page_drain(BAR(kCbFullK + j % kKStages), (j / kKStages) & 1, lim);
+    for (int j = max(0, last_k - C::kKStages + 1); j <= last_k; ++j)
+      page_drain(BAR(kCbFullK + j % C::kKStages), (j / C::kKStages) & 1, lim);
     for (int j = max(0, last_v - kVStages + 1); j <= last_v; ++j)
       page_drain(BAR(kCbFullVr + (j & 1)), (j >> 1) & 1, lim);
     __syncwarp();
