@@ -194,8 +194,8 @@ int split_limit(int sms, long long ctas) {
 }
 // Query tiles of 128 rows a CTA: one or two.  Two against one in us, 32
 // sequences of 16384 keys, 8 heads of 128 channels: 128 rows 444 / 266, 144
-// rows 459 / 521, 256 rows 467 / 531; 16 of 4096: 64.8 / 43.8, 67.7 / 81.7,
-// 70.4 / 84.4.  (With few CTAs, 4 sequences of 2048 keys, one is the better at
+// rows 444 / 521, 256 rows 451 / 531; 16 of 4096: 64.8 / 43.8, 65.6 / 81.7,
+// 68.4 / 84.4.  (With few CTAs, 4 sequences of 2048 keys, one is the better at
 // 256 rows, 28.0 / 25.2, and past that.)
 int query_tiles(long long cap) { return cap <= 128 ? 1 : 2; }
 long long chunk_tiles(int batch, int heads, long long cap, int* q_tiles) {

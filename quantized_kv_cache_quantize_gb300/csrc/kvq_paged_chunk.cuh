@@ -6,11 +6,11 @@
 // their keys, 128 at a time: S = c Q K^T, O += P V with the running base and
 // sum of the softmax.  4 d flops per row and key against 2 d bytes per key and
 // CTA: bound by the tensor cores.  Measured (24 heads of 128 channels, 4680 rows,
-// 23400 keys): 0.96 ms, 1400 TFLOP/s; 3500 cycles a tile of 128 keys and 256
+// 23400 keys): 0.94 ms, 1430 TFLOP/s; 3400 cycles a tile of 128 keys and 256
 // rows, of which the products take 2048 at their nominal rates.  They do not
 // reach them: Q K^T reads both operands from shared memory, all of its 128
 // bytes a cycle, and every commit and every instruction of the issuing thread
-// shows (a commit less a tile 2 %, its loop unrolled by two tiles 2 %).
+// shows (four commits less a tile 6 %, its loop unrolled by two tiles 2 %).
 // Leaving out the exponentials would save 2 %, the conversion of V nothing;
 // scores in halves of 64 keys, so that the next ones start earlier, read the
 // query twice as often: 1.34 ms.
@@ -92,7 +92,7 @@ enum : int {
                     // (NQ = 2), tile j at j % 4 (NQ = 1)
   kCbP = 14,        // [2] weights of keys 0-63 written, O rescaled (4 arrivals)
   kCbPb = 16,       // [2] weights of keys 64-127 written (4 arrivals)
-  kCbHalf = 18,     // [2] PV of keys 0-63 done
+  kCbHalf = 18,     // [2] PV of keys 0-63 done, when a softmax warp asked
   kCbODone = 20,    // every MMA done
   kCbMeta = 21,     // [8] a tile's page exponents written.  Not the key
                     // barrier: its stage can be refilled, and its phase
@@ -166,6 +166,31 @@ __device__ __forceinline__ void mask_block(uint32_t* s, int lo, int hi) {
   for (int k = 0; k < 16; ++k) s[k] = k >= lo && k < hi ? s[k] : 0xff800000u;
 }
 
+// words that pass between a softmax warp and the MMA thread
+__device__ __forceinline__ void st_release(uint32_t at, uint32_t v) {
+  asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_acquire(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+// waits until the word is v, bounded
+__device__ __noinline__ bool wait_word(uint32_t at, uint32_t v, unsigned long long limit_ns, volatile int* abort,
+                                       int* status) {
+  const uint64_t t0 = ptx::globaltimer();
+  while (ld_acquire(at) != v) {
+    if (*abort) return false;
+    if (ptx::globaltimer() - t0 > limit_ns) {
+      *abort = 1;
+      atomicCAS(status, 0, (int)KVQ_ERR_TIMEOUT);
+      return false;
+    }
+    __nanosleep(100);
+  }
+  return true;
+}
+
 // one arrival for a warp whose lanes are all done (a barrier takes its
 // arrivals one after another: 128 of them cost some hundred cycles)
 __device__ __forceinline__ void warp_arrive(uint32_t bar) {
@@ -217,6 +242,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
 
   volatile int* abort = reinterpret_cast<volatile int*>(smem + C::kBar + kCbCount * 8);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBar + kCbCount * 8 + 4);
+  // per group: the tile (+ 1) whose first half's product a softmax warp waits
+  // for, and the last one it was told of.  It needs that only when its base
+  // rises within a tile, too rarely for a commit in every tile (3 %).
+  const uint32_t ask0 = ptx::smem_u32(smem + C::kBar + kCbCount * 8 + 8), told0 = ask0 + 8;
   const uint32_t bar0 = ptx::smem_u32(smem + C::kBar);
   auto BAR = [&](int i) { return bar0 + 8u * (uint32_t)i; };
   if (tid == 0) {
@@ -234,6 +263,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
     for (int i = 0; i < kMetaSlots; ++i) ptx::mbar_init(BAR(kCbMeta + i), 1);
     ptx::mbar_init(BAR(kCbODone), 1);
     *abort = 0;
+    for (int i = 0; i < 2; ++i) {
+      st_release(ask0 + 4 * i, 0u);
+      st_release(told0 + 4 * i, 0u);
+    }
     ptx::fence_mbar_init();
   }
   if (warp == 0) {
@@ -418,7 +451,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
         if (__any_sync(0xffffffffu, fo != 1.f)) {
           // (the product of the first half is still under way; the group's
           // previous tile's was done before these scores were)
-          if (half == 1) ok = __all_sync(0xffffffffu, ok && page_wait(BAR(kCbHalf + q), par, lim, abort, a.status));
+          if (half == 1) {
+            if (lane == 0) st_release(ask0 + 4 * q, (uint32_t)j + 1u);
+            ok = __all_sync(0xffffffffu, ok && wait_word(told0 + 4 * q, (uint32_t)j + 1u, lim, abort, a.status));
+          }
           ptx::tc_fence_after();
           if (!first || half == 1) rescale_o();
           fo = 1.f;
@@ -603,6 +639,28 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
           kph ^= 1u;
         }
       };
+      // weights of the second half, or before them the question for the
+      // first half's product
+      uint32_t half_ph = 0;   // phases of the two barriers
+      auto wait_second = [&](int grp, uint32_t par, uint32_t tile) {
+        const uint64_t t_0 = ptx::globaltimer();
+        while (!ptx::mbar_try_wait_sleep(BAR(kCbPb + grp), par, 1000u)) {
+          if (ld_acquire(ask0 + 4 * grp) == tile && ld_acquire(told0 + 4 * grp) != tile) {
+            ptx::mma_commit(BAR(kCbHalf + grp));
+            if (!page_wait(BAR(kCbHalf + grp), (half_ph >> grp) & 1u, lim, abort, a.status)) return false;
+            half_ph ^= 1u << grp;
+            ptx::tc_fence_before();
+            st_release(told0 + 4 * grp, tile);
+          }
+          if (*abort) return false;
+          if (ptx::globaltimer() - t_0 > lim) {
+            *abort = 1;
+            atomicCAS(a.status, 0, (int)KVQ_ERR_TIMEOUT);
+            return false;
+          }
+        }
+        return true;
+      };
       if (ok && n_t > 0) {
         ptx::tc_fence_after();
         ok = next_k();
@@ -638,8 +696,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
               if (q == 0 && !(ok = page_wait(BAR(kCbFullV + u), ph, lim, abort, a.status))) break;
               ptx::tc_fence_after();
               pv(j, u, grp, 0, t_p);
-              ptx::mma_commit(BAR(kCbHalf + grp));
-              if (!(ok = page_wait(BAR(kCbPb + grp), par, lim, abort, a.status))) break;
+              if (!ptx::mbar_try_wait_sleep(BAR(kCbPb + grp), par, 2000u) &&
+                  !(ok = wait_second(grp, par, (uint32_t)j + 1u)))
+                break;
               ptx::tc_fence_after();
               pv(j, u, grp, 1, t_p);
               if (NQ == 2 && more) {

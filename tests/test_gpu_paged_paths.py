@@ -143,6 +143,28 @@ def test_widest_window(n, hq):
     assert torch.isfinite(a[1]).all() and torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("d,hq,n", [(128, 2, 30), (64, 4, 40), (128, 4, 60), (128, 8, 70)])
+@pytest.mark.parametrize("step", [1, 40, 64, 100])
+def test_scores_that_keep_growing(d, hq, n, step):
+    """Keys whose scores climb by some binades every `step` keys, so that the
+    softmax's base rises again and again, at any place of a tile."""
+    page, length = 16, 1024
+    cache = kvq.PagedCache.zeros(1, length // page, 1, page, d)
+    fill(cache, 4)
+    k = cache.k_codes.view(torch.uint8)
+    k.zero_()
+    grow = torch.arange(length, device="cuda") // step * step / 8.0       # 0 .. 128
+    codes = (grow / 16).to(torch.float8_e4m3fn)                            # rounded as they are
+    k[0, :, 0, :, 0] = codes.view(torch.uint8).view(length // page, page)
+    cache.k_scale.fill_(1.0)
+    q = (torch.randn(n, hq, d, generator=torch.Generator("cuda").manual_seed(3), device="cuda") * 0.1).bfloat16()
+    q[:, :, 0] = 16.0
+    table = torch.arange(length // page, dtype=torch.int32, device="cuda")[None]
+    got = kvq.paged_attention(cache, q, table, dev([length]), offsets_of([n]), max_q=n, scale=1.0, with_lse=True)
+    clean()
+    check_some(cache, got, q, table, [length], [n], [0], 1.0, True, 0)
+
+
 @pytest.mark.parametrize("n,hq", [(1, 4), (20, 2)])
 def test_rows_behind_the_last_sequence_stay(n, hq):
     cache = kvq.PagedCache.zeros(1, 20, 2, 16, 64)
