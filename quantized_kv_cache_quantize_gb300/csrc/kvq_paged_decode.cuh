@@ -32,9 +32,16 @@
 // Numbers.  E4M3 codes are exact in FP16.  A query row is scaled by a power of
 // two to a largest magnitude in [2^14, 2^15), exact in FP16 down to 2^-39 of
 // that maximum.  The page scales are powers of two applied outside the
-// products: K's to the fp32 scores, V's to the weight before it is rounded to
-// FP16, relative to the largest V scale seen (the running reference), with
-// headroom 2^15: weights down to 2^-39 of the largest contribution remain.
+// products: K's to the fp32 scores, V's (2^ev) to the weight before it is
+// rounded to FP16.  Two running bases a row, over the keys that it attends to:
+// the largest score m for the sum of weights, which knows no V scale, and the
+// largest score plus ev, held as m + eo, for the output.  The largest product
+// of a weight and its scale stands at 2^15 in FP16, so products down to 2^-39
+// of it remain, whatever the scales of pages that carry less, or that other
+// rows see.  A second exponential a score keeps the sum exact at any distance
+// of the two bases; the special-function unit is idle enough, and the maxima
+// of the eight row groups meet only where a base rises (64 sequences of up to
+// 8192 keys: 83 us either way).
 #pragma once
 
 #include <math_constants.h>
@@ -53,6 +60,7 @@ constexpr int kMinUnits = 2;       // per warp, when the work is small
 // 85.5, three 86.5 us).
 constexpr int kStartUnits = 2;
 constexpr int kMaxCluster = 16;
+constexpr float kNoOutput = -1000.f;   // where a row's output has no base yet
 
 // W warps per CTA, one CTA per SM
 template <int D, int W>
@@ -281,7 +289,9 @@ __device__ __forceinline__ bool decode_segment(const PagedAttnArgs& a, const CUt
     m[nt][0] = m[nt][1] = -CUDART_INF_F;
     l[nt][0] = l[nt][1] = 0.f;
   }
-  int eref = -1000;   // exponent O is held against (the largest V scale so far)
+  float eo[NT][2];    // O is held against m + eo (see the head of this file)
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) eo[nt][0] = eo[nt][1] = kNoOutput;
   bool ok = true;
 
   for (int i = 0; i < seg; ++i) {
@@ -333,15 +343,16 @@ __device__ __forceinline__ bool decode_segment(const PagedAttnArgs& a, const CUt
       }
     }
     // ---- softmax ----
-    float mx[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) mx[nt][0] = mx[nt][1] = -CUDART_INF_F;
+    // the lane's largest score of a column among each tile's keys
+    float xm[2][NT][2];
+    const float ev[2] = {(float)evt[0], (float)evt[1]};
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
       const float fk = pow2f(ekt[mt]);
       const int ka = key0 + 16 * mt + key_row(g);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
+        xm[mt][nt][0] = xm[mt][nt][1] = -CUDART_INF_F;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           float v = s[mt][nt][c] * (cq[nt][c & 1] * fk);
@@ -351,33 +362,40 @@ __device__ __forceinline__ bool decode_segment(const PagedAttnArgs& a, const CUt
             v = see ? v : -CUDART_INF_F;
           }
           s[mt][nt][c] = v;
-          mx[nt][c & 1] = fmaxf(mx[nt][c & 1], v);
+          xm[mt][nt][c & 1] = fmaxf(xm[mt][nt][c & 1], v);
         }
+      }
     }
+    // (a score plus ev is looked at through its distance from m, which is
+    // exact near m however large the scores)
     bool grows = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) mx[nt][c] = fmaxf(mx[nt][c], __shfl_xor_sync(0xffffffffu, mx[nt][c], x));
-        grows |= mx[nt][c] > m[nt][c];
-      }
-    const int etop = max(idt[0] >= 0 ? evt[0] : -1000, idt[1] >= 0 ? evt[1] : -1000);
-    if (__any_sync(0xffffffffu, grows || etop > eref)) {
-      const int enew = max(eref, etop);
-      const float fe = eref > -1000 ? pow2f(max(eref - enew, -126)) : 0.f;
-      eref = enew;
+        for (int mt = 0; mt < 2; ++mt)
+          grows |= xm[mt][nt][c] > m[nt][c] || (xm[mt][nt][c] - m[nt][c]) + ev[mt] > eo[nt][c];
+    if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float f[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const float mn = fmaxf(m[nt][c], mx[nt][c]);
-          f[c] = mn > -CUDART_INF_F ? ptx::ex2_approx(m[nt][c] - mn) : 1.f;
+          float top = fmaxf(xm[0][nt][c], xm[1][nt][c]);
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+          const float mn = fmaxf(m[nt][c], top);
+          const bool any = mn > -CUDART_INF_F;     // the row attends to something so far
+          const float mb = any ? mn : 0.f, down = any ? m[nt][c] - mn : 0.f;
+          float en = fmaxf((xm[0][nt][c] - mb) + ev[0], (xm[1][nt][c] - mb) + ev[1]);
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) en = fmaxf(en, __shfl_xor_sync(0xffffffffu, en, x));
+          en = fmaxf(en, eo[nt][c] + down);
+          l[nt][c] *= ptx::ex2_approx(down);
+          f[c] = ptx::ex2_approx(down + (eo[nt][c] - en));
           m[nt][c] = mn;
-          l[nt][c] *= f[c];
-          f[c] *= fe;
+          eo[nt][c] = en;
         }
 #pragma unroll
         for (int k = 0; k < MT; ++k)
@@ -388,23 +406,22 @@ __device__ __forceinline__ bool decode_segment(const PagedAttnArgs& a, const CUt
     // ---- weights: P^T as B fragments ----
     uint32_t pf[2][NT][2];
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-      // 2^15 times the V scale relative to the reference; far smaller
-      // scales stop at 2^-45, where FP16 has dropped the weight already
-      const int sh = 15 + min(max(evt[mt] - eref, -60), 0);
-      const float fs = (float)sh, inv = pow2f(-sh);
+    for (int nt = 0; nt < NT; ++nt) {
+      const float m0 = m[nt][0] > -CUDART_INF_F ? m[nt][0] : 0.f, m1 = m[nt][1] > -CUDART_INF_F ? m[nt][1] : 0.f;
+      const uint64_t mb = ptx::f2_pack(m0, m1);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float e[4];
+      for (int mt = 0; mt < 2; ++mt) {
+        const uint64_t up = ptx::f2_pack((ev[mt] - eo[nt][0]) + 15.f, (ev[mt] - eo[nt][1]) + 15.f);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float mc = m[nt][c & 1];
-          e[c] = ptx::ex2_approx(s[mt][nt][c] - (mc > -CUDART_INF_F ? mc : 0.f) + fs);
+        for (int i = 0; i < 2; ++i) {
+          const uint64_t x = ptx::f2_sub(ptx::f2_pack(s[mt][nt][2 * i], s[mt][nt][2 * i + 1]), mb);
+          float x0, x1, w0, w1;
+          ptx::f2_unpack(x, x0, x1);
+          l[nt][0] += ptx::ex2_approx(x0);
+          l[nt][1] += ptx::ex2_approx(x1);
+          ptx::f2_unpack(ptx::f2_add(x, up), w0, w1);
+          pf[mt][nt][i] = transpose8x8(ptx::f16x2_rn(ptx::ex2_approx(w0), ptx::ex2_approx(w1)));
         }
-        l[nt][0] = fmaf(e[0] + e[2], inv, l[nt][0]);
-        l[nt][1] = fmaf(e[1] + e[3], inv, l[nt][1]);
-        pf[mt][nt][0] = transpose8x8(ptx::f16x2_rn(e[0], e[1]));
-        pf[mt][nt][1] = transpose8x8(ptx::f16x2_rn(e[2], e[3]));
       }
     }
     // ---- O^T += V^T P^T ----
@@ -461,11 +478,11 @@ __device__ __forceinline__ bool decode_segment(const PagedAttnArgs& a, const CUt
     return false;
   }
   // O in original units, the sums over the keys' lanes
-  const float fo = eref > -1000 ? pow2f(eref) * pow2f(-15) : 0.f;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
+      const float fo = eo[nt][c] > kNoOutput ? ptx::ex2_approx(eo[nt][c] - 15.f) : 0.f;
 #pragma unroll
       for (int x = 4; x < 32; x <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);
 #pragma unroll
@@ -712,7 +729,9 @@ __global__ void __launch_bounds__(W * 32, 1)
     if (lane == 0 && a.lse != nullptr)
       a.lse[row] = ls == 0.f ? -CUDART_INF_F : 0.6931471805599453f * (top + log2f(ls));
   };
-  // a warp per row, the parts in order
+  // a warp per row, the parts in order.  A part is weighed by 2^(m - M) in two
+  // equal factors: far below the others in weight, it may still lead the
+  // output by its V scales, up to 2^120, where one factor would be zero
   for (int r = wid; r < rows; r += W) {
     float top = -CUDART_INF_F;
 #pragma unroll
@@ -725,10 +744,10 @@ __global__ void __launch_bounds__(W * 32, 1)
     for (int k = 0; k < W; ++k) {
       const float2 ml = ml_s[k][r];
       if (ml.y == 0.f) continue;   // nothing there, not even numbers
-      const float f = ptx::ex2_approx(ml.x - base);
-      ls = fmaf(ml.y, f, ls);
+      const float f = ptx::ex2_approx(0.5f * (ml.x - base));
+      ls = fmaf(ml.y * f, f, ls);
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) v[c] = fmaf(part[(k * R + r) * D + (D / 32) * lane + c], f, v[c]);
+      for (int c = 0; c < D / 32; ++c) v[c] = fmaf(part[(k * R + r) * D + (D / 32) * lane + c] * f, f, v[c]);
     }
     if (ctas == 1) {
       store(r, v, top, ls);
@@ -752,10 +771,10 @@ __global__ void __launch_bounds__(W * 32, 1)
     for (int c = 0; c < D / 32; ++c) v[c] = 0.f;
     for (unsigned k = 0; k < ctas; ++k) {
       const uint32_t ml = ptx::mapa(at_ml, k), from = ptx::mapa(at_o, k);
-      const float f = ptx::ex2_approx(ptx::ld_cluster_f32(ml) - base);
-      ls = fmaf(ptx::ld_cluster_f32(ml + 4), f, ls);
+      const float f = ptx::ex2_approx(0.5f * (ptx::ld_cluster_f32(ml) - base));
+      ls = fmaf(ptx::ld_cluster_f32(ml + 4) * f, f, ls);
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) v[c] = fmaf(ptx::ld_cluster_f32(from + 4 * c), f, v[c]);
+      for (int c = 0; c < D / 32; ++c) v[c] = fmaf(ptx::ld_cluster_f32(from + 4 * c) * f, f, v[c]);
     }
     store(r, v, top, ls);
   }
@@ -764,7 +783,7 @@ __global__ void __launch_bounds__(W * 32, 1)
 
 // Joins the parts of items that several warps covered: one block per row of a
 // (sequence, cache head), the largest maximum, then sums weighted by
-// 2^(m - M), the parts in order.  The block's warps take every fourth part, 32
+// 2^(m - M) (as two factors), the parts in order.  The block's warps take every fourth part, 32
 // lanes hold the channels.
 constexpr int kJoinWarps = 4;
 template <int D>
@@ -805,10 +824,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
   for (long long w = wa + wid; w <= wb; w += kJoinWarps) {
     const long long at = slot(w);
     const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
-    const float f = ptx::ex2_approx(ml.x - base);
-    ls = fmaf(ml.y, f, ls);
+    const float f = ptx::ex2_approx(0.5f * (ml.x - base));
+    ls = fmaf(ml.y * f, f, ls);
 #pragma unroll
-    for (int c = 0; c < C; ++c) o[c] = fmaf(p.part_o[at * D + lane + 32 * c], f, o[c]);
+    for (int c = 0; c < C; ++c) o[c] = fmaf(p.part_o[at * D + lane + 32 * c] * f, f, o[c]);
   }
 #pragma unroll
   for (int c = 0; c < C; ++c) sum_o[wid][lane + 32 * c] = o[c];
