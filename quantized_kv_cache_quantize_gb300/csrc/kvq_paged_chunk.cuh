@@ -26,10 +26,14 @@
 //   four warps, as the transposed operand.  P in two E4M3 parts would spare
 //   that, but its range (2^-9 to 448) is too short for softmax weights.
 // Page scales are powers of two outside the products: K's on the scores, V's
-// on the weight before it is rounded, relative to the largest so far (eref);
-// the sum of weights is taken without them.
-// The base m is raised only when a weight would leave FP16 (64 keys' sum past
-// 2^15), to leave the largest at 2^9, so weights down to 2^-33 of it remain.
+// (2^ev) on the weight before it is rounded, as an addend to the exponent.  A
+// row's base m follows score plus ev over the keys that the row attends to: it
+// is raised only when a weight would leave FP16 (64 keys' sum past 2^15), to
+// leave the largest at 2^9, so products of a weight and its scale down to 2^-33
+// of the row's largest remain, whatever scales other pages have.
+// The sum l of weights has the same base but no V scale: each block of 16 keys
+// adds its weights' sum times 2^-ev.  The largest score is within 60 of m - 15
+// to m - 9 on either side, so l stays inside fp32.
 //
 // Roles: two groups of 4 warps softmax (one row per thread), 4 warps V
 // conversion, one MMA thread, one TMA warp.  With NQ = 2 a group has a query
@@ -50,10 +54,19 @@ namespace {
 
 constexpr int kTileKeys = 128;
 constexpr int kVStages = 2, kMetaSlots = 8;
-// a slot of a tile's page scales, per block of 16 keys: 2^e of K [8], the V
-// exponent relative to eref [8] (as float) and 2^-that [8]; then eref and the
-// mask of blocks whose page is there
-constexpr int kMetaBytes = 128, kMetaShift = 32, kMetaInv = 64, kMetaRef = 96;
+// a slot of a tile's page scales, per block of 16 keys: 2^e of K [8], V's e [8]
+// (as float) and 2^-that [8]; then the mask of blocks whose page is there, and
+// 0.0, or kWideMark where the sum of weights needs exponentials of its own
+constexpr int kMetaBytes = 128, kMetaShift = 32, kMetaInv = 64, kMetaThere = 96, kMetaWide = 100;
+// Weights with V's scale in them flush to zero 126 binades below m, 135 or more
+// below the row's largest product.  On a page whose V scale is D binades under
+// the largest one so far that leaves out of l what is 135 - D binades or more
+// below the largest weight: nothing that 2^30 keys could add up to 2^-15 of, up
+// to D = 90.  Past it a tile's sum is taken from the scores alone.  The mark is
+// a number beyond every bound, so that the test for a new base takes notice of
+// it by itself (a branch of its own cost 1 to 2 %).
+constexpr int kWideSpan = 90;
+constexpr uint32_t kWideMark = 0x70000000u;   // 1.6e29
 
 template <int D, int NQ>
 struct ChunkCfg {
@@ -125,6 +138,11 @@ __device__ __forceinline__ uint2 lds_u2(uint32_t at) {
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
   return v;
 }
+__device__ __forceinline__ uint32_t lds_u(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
 __device__ __forceinline__ float lds_f(uint32_t at) {
   float v;
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
@@ -142,6 +160,15 @@ __device__ __forceinline__ void sts_u2(uint32_t at, uint32_t x, uint32_t y) {
 
 // where the base of a row starts: every weight against it is infinite
 constexpr float kLowest = -1e30f;
+
+// log of a sum l of weights against base m (binades).  l can be far from 1, so
+// its exponent joins m before its logarithm does: both terms then have the
+// size of the result.
+__device__ __forceinline__ float lse_of(float m, float l) {
+  if (l == 0.f) return -CUDART_INF_F;
+  const int r = min(max((int)(__float_as_uint(l) >> 23) - 127, -126), 126);
+  return 0.6931471805599453f * ((m + (float)r) + log2f(l * pow2f(-r)));
+}
 
 // weights of 16 scores, 2^(score scale + shift), as FP16 pairs, and their sum
 __device__ __forceinline__ void exp_block(const uint32_t* s, float scale, float shift, uint32_t* pk, float& sum) {
@@ -164,6 +191,23 @@ __device__ __forceinline__ void exp_block(const uint32_t* s, float scale, float 
 __device__ __forceinline__ void mask_block(uint32_t* s, int lo, int hi) {
 #pragma unroll
   for (int k = 0; k < 16; ++k) s[k] = k >= lo && k < hi ? s[k] : 0xff800000u;
+}
+
+
+// the sum of 64 weights from their scores alone; out of line, so that it takes
+// no place among the instructions of ordinary tiles (2.6 %: 980 against 955 us)
+__device__ __noinline__ float wide_sum(uint32_t t_h, uint32_t mh, float cq, float m, int lo, int hi, uint32_t there) {
+  float sum = 0.f;
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k) {
+    const float ck = fmaxf(cq * lds_f(mh + 4 * k), 1.2e-38f);
+    uint32_t v[16];
+    ptx::tmem_ld16(t_h + 16 * k, v);
+    mask_block(v, (there >> k) & 1u ? lo - 16 * k : 16, hi - 16 * k);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum += ptx::ex2_approx(fmaf(__uint_as_float(v[i]), ck, -m));
+  }
+  return sum;
 }
 
 // words that pass between a softmax warp and the MMA thread
@@ -347,7 +391,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
     const int hi_r = (a.causal ? min(len, tq + 1) : len) - base;
     const int lo_r = (a.window > 0 ? max(0, tq - a.window + 1) : 0) - base;
     float m = kLowest, l = 0.f;
-    int eref = -1000;
     const uint32_t t_o = tmem + C::kTO + q * D + lane_off;
     bool ok = true;
     const uint32_t t_s = tmem + q * 128 + lane_off;
@@ -369,15 +412,11 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
         continue;
       }
       const uint32_t mt = sm + C::kMeta + (j & (kMetaSlots - 1)) * kMetaBytes;
-      const uint2 ref = lds_u2(mt + kMetaRef);
+      const uint32_t there = lds_u(mt + kMetaThere);
       const int at0 = j * kTileKeys;
-      const bool whole = __all_sync(0xffffffffu, ref.y == 255u && lo_r <= at0 && hi_r >= at0 + kTileKeys);
-      // what O has to be multiplied by: the page scale it is held against and
-      // the base may both rise
-      float fo = eref == (int)ref.x ? 1.f : eref > -1000 ? pow2f(max(eref - (int)ref.x, -126)) : 0.f;
-      eref = (int)ref.x;
-      auto rescale_o = [&]() {
-        const uint64_t f2 = ptx::f2_pack(fo, fo);
+      const bool whole = __all_sync(0xffffffffu, there == 255u && lo_r <= at0 && hi_r >= at0 + kTileKeys);
+      auto rescale_o = [&](float f) {
+        const uint64_t f2 = ptx::f2_pack(f, f);
 #pragma unroll 1
         for (int c = 0; c < D / 16; ++c) {
           uint32_t v[16];
@@ -401,18 +440,20 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
         const uint32_t t_h = t_s + 64 * half, mh = mt + 16 * half;
         uint32_t pk[2][16];
         float hat, sum;
+        const float wide = lds_f(mt + kMetaWide);
         auto scores = [&](uint32_t (&cur)[64]) {
           ptx::tmem_ld64(t_h, cur);
           if (!whole) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int at = at0 + 64 * half + 16 * k;
-              mask_block(cur + 16 * k, (ref.y >> (4 * half + k)) & 1u ? lo_r - at : 16, hi_r - at);
+              mask_block(cur + 16 * k, (there >> (4 * half + k)) & 1u ? lo_r - at : 16, hi_r - at);
             }
           }
         };
         auto weights = [&](const uint32_t (&cur)[64]) {
-          hat = sum = 0.f;
+          hat = wide;
+          sum = 0.f;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             // (a scale that underflows must not meet the -inf of a masked score)
@@ -435,30 +476,34 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
           scores(cur);
           float top = kLowest;
 #pragma unroll
-          for (int k = 0; k < 64; ++k)
-            top = fmaxf(top, fmaf(__uint_as_float(cur[k]), fmaxf(cq * lds_f(mh + 4 * (k >> 4)), 1.2e-38f),
-                                  lds_f(mh + kMetaShift + 4 * (k >> 4))));
-          const float m_new = fmaxf(m, top - 9.f), f = exp2f(m - m_new);
+          for (int k = 0; k < 4; ++k) {
+            float most = -CUDART_INF_F;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) most = fmaxf(most, __uint_as_float(cur[16 * k + i]));
+            top = fmaxf(top, fmaf(most, fmaxf(cq * lds_f(mh + 4 * k), 1.2e-38f), lds_f(mh + kMetaShift + 4 * k)));
+          }
+          // (by two factors: l may stand 75 binades above 2^m)
+          const float m_new = fmaxf(m, top - 9.f), f = exp2f(0.5f * (m - m_new));
           m = m_new;
-          l *= f;
-          fo *= f;
+          l = l * f * f;
           weights(cur);
+          if (wide != 0.f)
+            sum = wide_sum(t_h, mh, cq, m, lo_r - at0 - 64 * half, hi_r - at0 - 64 * half, there >> (4 * half));
+          if (__any_sync(0xffffffffu, f != 1.f)) {
+            // (the product of the first half is still under way; the group's
+            // previous tile's was done before these scores were)
+            if (half == 1) {
+              if (lane == 0) st_release(ask0 + 4 * q, (uint32_t)j + 1u);
+              ok = __all_sync(0xffffffffu, ok && wait_word(told0 + 4 * q, (uint32_t)j + 1u, lim, abort, a.status));
+            }
+            ptx::tc_fence_after();
+            if (!first || half == 1) rescale_o(f * f);
+          }
         }
         l += sum;
         // over the first 32 of the 64 score columns just read
         ptx::tmem_st16(t_h, pk[0]);
         ptx::tmem_st16(t_h + 16, pk[1]);
-        if (__any_sync(0xffffffffu, fo != 1.f)) {
-          // (the product of the first half is still under way; the group's
-          // previous tile's was done before these scores were)
-          if (half == 1) {
-            if (lane == 0) st_release(ask0 + 4 * q, (uint32_t)j + 1u);
-            ok = __all_sync(0xffffffffu, ok && wait_word(told0 + 4 * q, (uint32_t)j + 1u, lim, abort, a.status));
-          }
-          ptx::tc_fence_after();
-          if (!first || half == 1) rescale_o();
-          fo = 1.f;
-        }
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
         warp_arrive(BAR((half == 0 ? kCbP : kCbPb) + q));
@@ -470,11 +515,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
     if (ok) ok = page_wait(BAR(kCbODone), 0, lim, abort, a.status);
     ok = __all_sync(0xffffffffu, ok && !*abort);
     ptx::tc_fence_after();
-    const float fe = eref > -1000 ? pow2f(eref) : 0.f;
     // NQ = 1: the second group's share goes through shared memory, whose tiles
     // nobody reads any more
     const bool mine = n_t > (NQ == 2 ? 0 : q);   // the group had tiles
-    float f0 = fe, f1 = 0.f;
+    float f0 = 1.f, f1 = 0.f;
     const uint32_t part_at = sm + C::kV + 4 * r, ml_at = sm + C::kK + 8 * r;
     if constexpr (NQ == 1) {
       if (q == 1) {
@@ -484,7 +528,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
           if (!(mine && ok)) break;
           ptx::tmem_ld32(t_o + 32 * c, v);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) sts_f(part_at + (32 * c + k) * 512, __uint_as_float(v[k]) * fe);
+          for (int k = 0; k < 32; ++k) sts_f(part_at + (32 * c + k) * 512, __uint_as_float(v[k]));
         }
         sts_u2(ml_at, __float_as_uint(m), __float_as_uint(mine && ok ? l : 0.f));
       }
@@ -492,10 +536,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
       if (q == 0) {
         const uint2 ml = lds_u2(ml_at);
         const float m1 = __uint_as_float(ml.x), l1 = __uint_as_float(ml.y), top = fmaxf(m, m1);
-        f0 = exp2f(m - top);
-        f1 = l1 == 0.f ? 0.f : exp2f(m1 - top);
-        l = l * f0 + l1 * f1;
-        f0 *= fe;
+        const float h0 = exp2f(0.5f * (m - top)), h1 = l1 == 0.f ? 0.f : exp2f(0.5f * (m1 - top));
+        l = l * h0 * h0 + l1 * h1 * h1;   // (by two factors, as above)
+        f0 = h0 * h0;
+        f1 = h1 * h1;
         m = top;
       }
     }
@@ -546,7 +590,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
       }
       if (store) {
         if (part) *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(m, l);
-        else if (a.lse != nullptr) a.lse[orow] = l == 0.f ? -CUDART_INF_F : 0.6931471805599453f * (m + log2f(l));
+        else if (a.lse != nullptr) a.lse[orow] = lse_of(m, l);
       }
     }
   } else if (warp < C::kMmaWarp) {
@@ -559,7 +603,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
       const uint32_t par = (j >> 1) & 1;
       if (!page_wait(BAR(kCbFullVr + s), par, lim, abort, a.status)) break;
       const int key = base + j * kTileKeys + r;
-      const uint32_t there = lds_u2(sm + C::kMeta + (j & (kMetaSlots - 1)) * kMetaBytes + kMetaRef).y;
+      const uint32_t there = lds_u(sm + C::kMeta + (j & (kMetaSlots - 1)) * kMetaBytes + kMetaThere);
       const bool use = key >= first && key < len && ((there >> (r >> 4)) & 1u);
       uint4 raw[D / 16];
       const uint32_t src = sm + C::kVr + s * C::kKT;
@@ -740,7 +784,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
       return o;
     };
     BlockPage four = look(0), next_four = look(4);
-    int eref = -1000;   // largest V exponent so far
+    int ev_top = -1000;   // largest V exponent so far
     int ks = 0, last_k = -1, last_v = -1;
     bool ok = true;
     for (int j = 0; j < n_t; ++j) {
@@ -764,16 +808,16 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
       if (!__all_sync(0xffffffffu, ok)) break;
       {
         const uint32_t mt = sm + C::kMeta + (j & (kMetaSlots - 1)) * kMetaBytes;
-        eref = max(eref, (int)__reduce_max_sync(0xffffffffu, cur.ev));
+        ev_top = max(ev_top, (int)__reduce_max_sync(0xffffffffu, cur.id >= 0 ? cur.ev : -1000));
+        const int ev_low = (int)__reduce_min_sync(0xffffffffu, cur.id >= 0 ? cur.ev : 1000);
         const uint32_t there = __ballot_sync(0xffffffffu, cur.id >= 0);
-        // far smaller V scales stop at 2^-60, where FP16 drops every weight
-        const int sh = cur.id >= 0 ? max(cur.ev - eref, -60) : 0;
         if (lane < 8) {
+          const int ev = cur.id >= 0 ? cur.ev : 0;
           sts_f(mt + 4 * lane, cur.id >= 0 ? pow2f(cur.ek) : 1.f);
-          sts_f(mt + kMetaShift + 4 * lane, (float)sh);
-          sts_f(mt + kMetaInv + 4 * lane, pow2f(-sh));
+          sts_f(mt + kMetaShift + 4 * lane, (float)ev);
+          sts_f(mt + kMetaInv + 4 * lane, pow2f(-ev));
         }
-        if (lane == 0) sts_u2(mt + kMetaRef, (uint32_t)eref, there);
+        if (lane == 0) sts_u2(mt + kMetaThere, there, ev_top - ev_low > kWideSpan ? kWideMark : 0u);
       }
       __syncwarp();
       if (lane == 0) {
@@ -842,8 +886,9 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
   for (int c = 0; c < C; ++c) o[c] = 0.f;
   for (int s = 0; s < p.splits; ++s) {
     const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (s * step + row) * 2);
-    const float f = ptx::ex2_approx(ml.x - base);
-    l = fmaf(ml.y, f, l);
+    // (the sum by two factors: it may stand 75 binades above 2^m)
+    const float h = ptx::ex2_approx(0.5f * (ml.x - base)), f = h * h;
+    l = fmaf(ml.y * h, h, l);
 #pragma unroll
     for (int c = 0; c < C; ++c) o[c] = fmaf(p.part_o[(s * step + row) * D + C * lane + c], f, o[c]);
   }
@@ -853,7 +898,7 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
     const __nv_bfloat162 y = __floats2bfloat162_rn(o[c] * inv, o[c + 1] * inv);
     *reinterpret_cast<uint32_t*>(a.out + row * D + C * lane + c) = *reinterpret_cast<const uint32_t*>(&y);
   }
-  if (lane == 0 && a.lse != nullptr) a.lse[row] = l == 0.f ? -CUDART_INF_F : 0.6931471805599453f * (top + log2f(l));
+  if (lane == 0 && a.lse != nullptr) a.lse[row] = lse_of(top, l);
 }
 
 }  // namespace

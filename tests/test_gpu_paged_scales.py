@@ -1,6 +1,7 @@
 """Paged attention over pages whose value scales lie far apart: the answer is
 the formula's wherever the softmax puts its weight, on pages of large or small
-scale, whatever other rows see, over the whole range of exponents: the decoding forms."""
+scale, whatever other rows see, in every form and over the whole range of
+exponents."""
 from __future__ import annotations
 
 import math
@@ -109,7 +110,8 @@ def attend(cache, q, table, lens, counts, causal=True, window=0):
     return got
 
 
-ROWS = [(128, 1, 1, 1), (64, 3, 1, 1), (128, 3, 4, 1), (64, 4, 2, 2)]     # d, query rows, q heads, cache heads
+ROWS = [(128, 1, 1, 1), (64, 3, 1, 1), (128, 3, 4, 1), (64, 4, 2, 2), (64, 40, 1, 1), (128, 20, 2, 1), (128, 300, 1, 1),
+        (64, 150, 4, 2)]     # d, query rows, q heads, cache heads
 
 
 @pytest.mark.parametrize("d,n,hq,hkv", ROWS)
@@ -128,7 +130,8 @@ def test_weight_on_the_page_of_small_scale(d, n, hq, hkv, span):
             check(got, pool, q, table, [32], [n], causal=False)
 
 
-@pytest.mark.parametrize("d,n,hq,hkv", [(128, 2, 1, 1), (64, 4, 3, 1), (128, 12, 1, 1)])
+@pytest.mark.parametrize("d,n,hq,hkv", [(128, 2, 1, 1), (64, 4, 3, 1), (128, 12, 1, 1), (64, 40, 1, 1), (128, 20, 6, 1),
+                                        (64, 300, 1, 1), (128, 150, 4, 2)])
 @pytest.mark.parametrize("span", [20, 36, 61, 120])
 def test_large_page_that_a_row_does_not_see(d, n, hq, hkv, span):
     """The page of large scale lies behind the causal limit of the earlier
@@ -148,7 +151,8 @@ def test_large_page_that_a_row_does_not_see(d, n, hq, hkv, span):
     check(attend(cache, q, table, [length], [n], window=window), pool, q, table, [length], [n], window=window)
 
 
-@pytest.mark.parametrize("d,n,hq,hkv", [(128, 1, 2, 1), (64, 5, 3, 1)])
+@pytest.mark.parametrize("d,n,hq,hkv", [(128, 1, 2, 1), (64, 5, 3, 1), (64, 40, 1, 1), (128, 120, 1, 1), (128, 140, 2, 1),
+                                        (64, 300, 1, 1)])
 @pytest.mark.parametrize("span,low", [(19, -30), (23, -60), (30, -60), (36, -60), (61, -90), (120, -180)])
 def test_large_page_met_on_the_way(d, n, hq, hkv, span, low):
     """Ordinary pages, then one of a large scale and no weight in some later
@@ -164,7 +168,8 @@ def test_large_page_met_on_the_way(d, n, hq, hkv, span, low):
         check(attend(cache, q, table, [length], [n], causal=False), pool, q, table, [length], [n], causal=False)
 
 
-@pytest.mark.parametrize("d,n,hq,batch", [(64, 1, 2, 1), (128, 3, 4, 1), (64, 1, 8, 310), (128, 2, 8, 310)])
+@pytest.mark.parametrize("d,n,hq,batch", [(64, 1, 2, 1), (128, 3, 4, 1), (64, 24, 1, 1), (64, 1, 8, 310), (128, 2, 8, 310),
+                                          (64, 24, 1, 310), (128, 60, 2, 310), (64, 130, 1, 310), (128, 200, 2, 310)])
 @pytest.mark.parametrize("first", [True, False])
 def test_many_keys_that_count_only_in_the_sum(d, n, hq, batch, first):
     """One key of the largest scale against 1000 or 8000 of the smallest, 16
@@ -185,7 +190,8 @@ def test_many_keys_that_count_only_in_the_sum(d, n, hq, batch, first):
 @pytest.mark.parametrize("d,page,hq,hkv,batch,n", [
     (128, 32, 16, 8, 50, 1), (64, 16, 16, 8, 60, 2), (128, 64, 32, 8, 40, 4),    # equal runs of the line
     (64, 32, 8, 4, 40, 1),                                                       # a CTA an item
-    (128, 32, 2, 1, 3, 1), (64, 16, 4, 2, 2, 3)])                                # clusters
+    (128, 32, 2, 1, 3, 1), (64, 16, 4, 2, 2, 3),                                 # clusters
+    (64, 32, 4, 1, 1, 9), (128, 64, 4, 2, 2, 40)])                               # tensor cores, keys in ranges
 def test_scales_of_every_page_their_own(d, page, hq, hkv, batch, n):
     """Exponents all over the range, scores too, the keys divided among warps,
     CTAs and ranges in every way there is."""
