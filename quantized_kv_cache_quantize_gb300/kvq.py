@@ -651,7 +651,10 @@ def paged_attention(cache: PagedCache, q: torch.Tensor, block_table: torch.Tenso
         if workspace is None:
             ws, ws_bytes = None, cache.workspace_bytes(q_heads, s.batch, s.width, rows, max_q)
             if ws_bytes > 16:
-                ws = cache._workspace(ws_bytes, stream).data_ptr()
+                # (held until the call returns: a call launches two kernels,
+                # and another thread's may come between them)
+                workspace = cache._workspace(ws_bytes, stream)
+                ws = workspace.data_ptr()
         else:
             ws_ptr, ws_bytes = _workspace_arg(workspace, dev)
             ws = ws_ptr.value
@@ -716,7 +719,8 @@ def pages_compact(cache: PagedCache, block_table: torch.Tensor, out=None, worksp
         n_live = torch.empty(1, dtype=torch.int32, device=dev)
         if workspace is None:
             ws_bytes = lib().kvq_pages_compact_workspace_bytes(cache._at)
-            ws = cache._workspace(max(ws_bytes, 16), stream).data_ptr()
+            workspace = cache._workspace(max(ws_bytes, 16), stream)   # held, as above
+            ws = workspace.data_ptr()
         else:
             ws_ptr, ws_bytes = _workspace_arg(workspace, dev)
             ws = ws_ptr.value
