@@ -50,7 +50,7 @@ int decode_warps(int sms, int row_tiles, double units) {
 double decode_units(long long items, long long keys) { return (double)items * ((double)keys / kUnit + 1.0); }
 
 struct DecodeWs {
-  size_t pre, ml, o, bytes;
+  size_t ml, o, bytes;   // the first units come first
 };
 DecodeWs decode_ws(int warps, int batch, int rows_cap, int d) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
@@ -158,7 +158,7 @@ kvq_status launch_decode(const PagedAttnArgs& a, cudaStream_t stream) {
   int grid = sms;
   if (most < (double)sms * warps * kMinUnits) grid = std::min((int)(most / kMinUnits) + 1, sms);
   uint8_t* base = static_cast<uint8_t*>(a.ws);
-  d.pre = reinterpret_cast<long long*>(base + ws.pre);
+  d.pre = reinterpret_cast<long long*>(base);
   d.part_ml = reinterpret_cast<float*>(base + ws.ml);
   d.part_o = reinterpret_cast<float*>(base + ws.o);
   d.warps = grid * warps;

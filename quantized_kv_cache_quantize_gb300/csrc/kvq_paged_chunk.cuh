@@ -395,7 +395,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
     bool ok = true;
     const uint32_t t_s = tmem + q * 128 + lane_off;
     for (int j = NQ == 2 ? 0 : q; j < n_t; j += NQ == 2 ? 1 : 2) {
-      const uint32_t par = NQ == 2 ? (j & 1) : ((j >> 1) & 1);
       const bool first = NQ == 2 ? j == 0 : j < 2;
       // a slot of scales is written again 8 tiles later, the TMA warp at most
       // 5 ahead of the softmax (key stages and score buffers)
