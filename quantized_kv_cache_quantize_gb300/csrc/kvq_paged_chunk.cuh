@@ -194,19 +194,37 @@ __device__ __forceinline__ void mask_block(uint32_t* s, int lo, int hi) {
 }
 
 
-// the sum of 64 weights from their scores alone; out of line, so that it takes
-// no place among the instructions of ordinary tiles (2.6 %: 980 against 955 us)
-__device__ __noinline__ float wide_sum(uint32_t t_h, uint32_t mh, float cq, float m, int lo, int hi, uint32_t there) {
+// A score with its V exponent, each step rounded by itself: its distance from a
+// base taken from such a sum is what it says, however large the scores.  (A
+// fused product's distance holds what the base's rounding left out, 2^16 binades
+// at a score of 2^40: the weights of the largest keys would be zero or infinite.)
+__device__ __forceinline__ float with_ev(float s, float ck, float ev) { return __fadd_rn(__fmul_rn(s, ck), ev); }
+constexpr float kFarBase = 1048576.f;   // a base that large, 2^20 binades, takes with_ev's distances
+// 64 weights by with_ev's distances, written over the scores, and their sum from
+// exponents without V's.  Out of line, so that it takes no place among the
+// instructions of ordinary tiles (in line 2 to 4 %).
+__device__ __noinline__ float weights_apart(uint32_t t_h, uint32_t mh, float cq, float m, int lo, int hi,
+                                            uint32_t there) {
   float sum = 0.f;
 #pragma unroll 1
-  for (int k = 0; k < 4; ++k) {
-    const float ck = fmaxf(cq * lds_f(mh + 4 * k), 1.2e-38f);
-    uint32_t v[16];
-    ptx::tmem_ld16(t_h + 16 * k, v);
-    mask_block(v, (there >> k) & 1u ? lo - 16 * k : 16, hi - 16 * k);
+  for (int k = 0; k < 4; k += 2) {
+    uint32_t v[32], w[16];
+    ptx::tmem_ld32(t_h + 16 * k, v);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) sum += ptx::ex2_approx(fmaf(__uint_as_float(v[i]), ck, -m));
+    for (int i = 0; i < 2; ++i) {
+      const float ck = fmaxf(cq * lds_f(mh + 4 * (k + i)), 1.2e-38f), ev = lds_f(mh + kMetaShift + 4 * (k + i));
+      mask_block(v + 16 * i, (there >> (k + i)) & 1u ? lo - 16 * (k + i) : 16, hi - 16 * (k + i));
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float x0 = with_ev(__uint_as_float(v[16 * i + 2 * c]), ck, ev) - m;
+        const float x1 = with_ev(__uint_as_float(v[16 * i + 2 * c + 1]), ck, ev) - m;
+        w[8 * i + c] = ptx::f16x2_rn(ptx::ex2_approx(x0), ptx::ex2_approx(x1));
+        sum += ptx::ex2_approx(x0 - ev) + ptx::ex2_approx(x1 - ev);
+      }
+    }
+    ptx::tmem_st16(t_h + 8 * k, w);   // (columns that the loads are past)
   }
+  ptx::tmem_st_wait();
   return sum;
 }
 
@@ -479,15 +497,18 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
             float most = -CUDART_INF_F;
 #pragma unroll
             for (int i = 0; i < 16; ++i) most = fmaxf(most, __uint_as_float(cur[16 * k + i]));
-            top = fmaxf(top, fmaf(most, fmaxf(cq * lds_f(mh + 4 * k), 1.2e-38f), lds_f(mh + kMetaShift + 4 * k)));
+            top = fmaxf(top, with_ev(most, fmaxf(cq * lds_f(mh + 4 * k), 1.2e-38f), lds_f(mh + kMetaShift + 4 * k)));
           }
           // (by two factors: l may stand 75 binades above 2^m)
-          const float m_new = fmaxf(m, top - 9.f), f = exp2f(0.5f * (m - m_new));
+          const float m_new = fmaxf(m, __fadd_ru(top, -9.f)), f = exp2f(0.5f * (m - m_new));
           m = m_new;
           l = l * f * f;
           weights(cur);
-          if (wide != 0.f)
-            sum = wide_sum(t_h, mh, cq, m, lo_r - at0 - 64 * half, hi_r - at0 - 64 * half, there >> (4 * half));
+          if (__any_sync(0xffffffffu, wide != 0.f || (fabsf(m) > kFarBase && m > kLowest))) {
+            sum = weights_apart(t_h, mh, cq, m, lo_r - at0 - 64 * half, hi_r - at0 - 64 * half, there >> (4 * half));
+            ptx::tmem_ld16(t_h, pk[0]);
+            ptx::tmem_ld16(t_h + 16, pk[1]);
+          }
           if (__any_sync(0xffffffffu, f != 1.f)) {
             // (the product of the first half is still under way; the group's
             // previous tile's was done before these scores were)

@@ -210,3 +210,44 @@ def test_scales_of_every_page_their_own(d, page, hq, hkv, batch, n):
         check(got, pool, q[rows], table[b:b + 1], lens[b:b + 1], [n], rows=rows)
     again = attend(cache, q, table, lens, counts)
     assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+@pytest.mark.parametrize("d,n,hq,hkv", ROWS)
+@pytest.mark.parametrize("e", [0, 18, 22, 40, 60])
+@pytest.mark.parametrize("span", [0, 30, 120])
+def test_keys_of_any_scale(d, n, hq, hkv, e, span):
+    """Key scales up to the largest, scores up to 2^69 binades: one key takes
+    everything, by half of the scores' size or more, and the output is its
+    value (in 16 bits); the logarithm is its score."""
+    page, length = 16, 400
+    rng = np.random.default_rng(e + n)
+    n_pages = length // page
+    codes, exps = random_pool(e + d, 1, n_pages, hkv, page, d)
+    k0 = rng.uniform(-200, 200, (n_pages, hkv, page))
+    best, worst = rng.permutation(length)[:2]
+    k0[best // page, :, best % page], k0[worst // page, :, worst % page] = 448.0, -448.0
+    k = np.zeros((n_pages, hkv, page, d))
+    k[..., 0] = k0
+    codes[0][0] = torch.from_numpy(P.e4m3_code(P.e4m3_round(k)))
+    exps[0][:] = e
+    exps[1][:] = rng.integers(-(span // 2), span // 2 + 1, exps[1].shape)
+    cache = cache_of(codes, exps)
+    q = query(9, n, hq, d, [1, -1, 1])
+    table = np.arange(n_pages, dtype=np.int32)[None]
+    scale = 0.3                                  # times log2 e: not a power of two
+    got = kvq.paged_attention(cache, q.cuda(), dev(table), dev([length]), offsets_of([n]), max_q=n, scale=scale,
+                              causal=False, with_lse=True)
+    torch.cuda.synchronize()
+    assert kvq.last_device_status() == kvq.KVQ_OK
+    values = P.Pool([c[0].numpy() for c in codes], [x[0] for x in exps]).rows(1, table[0], length)
+    gap = scale * 248 * 2.0 ** e                 # from the winner's score to any other's, in nats, or more
+    for h in range(hq):
+        for i in range(n):
+            v = values[h // (hq // hkv)]
+            want = v[best if q[i, h, 0] > 0 else worst]
+            # all others together: 400 e^-gap of at most 448 2^(span / 2)
+            rest = 400 * math.exp(-min(gap, 700.0)) * 448 * 2.0 ** (span // 2)
+            o = got[0][i, h].double().cpu().numpy()
+            assert (np.abs(o - want) <= 2.0 ** -8 * np.abs(want) + rest).all(), (h, i)
+            z, s = float(got[1][i, h]), scale * 448.0 * 2.0 ** e
+            assert abs(z - s) <= s * 2.0 ** -20, (h, i, z, s)
