@@ -463,7 +463,9 @@ kvq_status kvq_pages_bytes(const kvq_pages *pages, size_t *codes_bytes, size_t *
  * become e4m3(c * 2^(e_old - e)).  New codes are e4m3(x * 2^-e), to nearest,
  * ties to even, saturating.  Tokens of the page behind the last new one keep
  * their bytes.  No page may be written for two sequences in one call.  A
- * value that is not finite or beyond 448 * 2^60 records KVQ_ERR_RANGE.
+ * value that is not finite or beyond 448 * 2^60 records KVQ_ERR_RANGE; the
+ * scale of its page and head is 2^60 then, and earlier codes follow it (most of
+ * them to zero).
  */
 kvq_status kvq_pages_append(const kvq_pages *pages, int32_t layer, const uint16_t *k_new,
                             int64_t k_row_stride, int64_t k_head_stride, const uint16_t *v_new,
@@ -490,13 +492,24 @@ size_t kvq_paged_workspace_bytes(const kvq_pages *pages, int32_t q_heads, int32_
  * (window counts back from t, with or without causal):
  *   s_j = scale * q . k_j,  out = sum_j softmax(s)_j v_j,
  *   lse = log sum_j exp(s_j).
+ * for any page scales, as far as scores stay within fp32.
  * A row that attends to nothing gets out = 0, lse = -infinity.  What masked
  * places hold (NaN codes among it) does not matter when no row of the
  * sequence's query heads attends there.  A query row that holds a NaN or an
  * infinity gives NaN.
+ * Precision.  Codes and scales enter exactly; scores, sums and outputs are
+ * held in fp32.  A weight times its V scale is rounded to FP16: 2^-11 of it,
+ * and the products below 2^-33 of the row's largest (2^-39 up to 16 rows a
+ * head) go.  The query depends on the rows a cache head has, max_q * q_heads /
+ * kv_heads: up to 16, FP16 after scaling by a power of two, exact down to
+ * 2^-31 of the row's largest element, off by 2^-39 of it at most below; more
+ * than 16, two E4M3 parts, exact down to 2^-9 and off by 2^-17 at most.
  * out: BF16 [rows][q_heads][head_dim] device, contiguous; lse: fp32
  * [rows][q_heads] device or NULL.  max_q: at least the largest n_b (rows
- * beyond it are not computed and record KVQ_ERR_PAGE).  workspace: device,
+ * beyond it are not computed and record KVQ_ERR_PAGE); it chooses the kernel
+ * and sizes the grid and the workspace, so the largest n_b itself is the best
+ * value: 64 sequences of one token each with max_q = 64 run as 64 prompts,
+ * most of their tiles empty.  workspace: device,
  * 16-byte aligned, >= kvq_paged_workspace_bytes; its contents need not be
  * kept, and calls that overlap on the GPU need workspaces of their own.
  * rows == 0 is a no-op.

@@ -19,8 +19,9 @@ namespace {
 // tiles are what a warp's registers hold.  Past them it would read the keys
 // again from L2, and the tensor-core form, which works on 128 rows however few
 // there are, is as good or better.  Decoding / tensor-core form in us, 32
-// sequences of 16384 keys, 8 heads of 128 channels: 16 rows 183 / 258, 24 rows
-// in two passes 343 / 258; 64 channels: 148 / 245, 278 / 245.
+// sequences of 16384 keys, 8 heads of 128 channels: 16 rows 186 / 258, 24 rows
+// (in two passes, measured before the present form) 343 / 258; 64 channels:
+// 145 / 222, 278 / 222.
 constexpr int kDecRows = 16;
 
 std::atomic<uint64_t> g_decode_smem[2][2], g_decode12_smem[2], g_item_smem[2][2], g_item_wide[2][2];
@@ -40,9 +41,9 @@ cudaError_t ensure_wide_clusters(Kernel kern, std::atomic<uint64_t>& done) {
 
 // Warps of the decoding form, per CTA.  Twelve hide more of the latency of
 // products and votes than eight where every warp has a long run of keys
-// (103 against 119 us: 32 sequences of 16384 keys, 8 heads of 64 channels);
-// with short runs the larger CTA's start costs more (19.6 against 17.1 us: 16
-// of 4096, 4 heads).  Two column tiles have no registers for twelve.
+// (94 against 110 us: 32 sequences of 16384 keys, 8 heads of 64 channels);
+// with short runs the larger CTA's start costs more (20.5 against 17.8 us: 16
+// of 4096, 4 heads of 128).  Two column tiles have no registers for twelve.
 constexpr int kDecWarps = 8, kDecWarpsLong = 12, kLongUnits = 16;
 int decode_warps(int sms, int row_tiles, double units) {
   return row_tiles == 1 && units >= (double)kLongUnits * kDecWarps * sms ? kDecWarpsLong : kDecWarps;
@@ -99,9 +100,9 @@ int active_clusters(int k) {
 // the longest item decides; the line scans the batch, takes a second kernel,
 // which joins every item's pieces, and balances.  The times below, in us, are
 // fits to measured ones (sequences of one length; 128 channels, grouped by 4,
-// item / line): 32 items of 512 keys 6.5 / 9.7, of 8192 15.5 / 18.7; 64 of 8192
-// 26.9 / 34.9; 48 of 32768 83 / 76; 192 of 2048 25.7 / 23.0; 4 of 32768 17.3 /
-// 24.7.  Keys are known by the table's width only, so a CTA's share is limited
+// item / line): 32 items of 512 keys 6.7 / 10.0, of 8192 15.8 / 18.7; 64 of
+// 8192 26.7 / 33.3; 48 of 32768 78.8 / 75.9; 192 of 2048 27.5 / 24.3; 4 of 32768
+// 16.6 / 23.1.  Keys are known by the table's width only, so a CTA's share is limited
 // too, to 4096 keys: the longest of a ragged batch then costs 25 us at most.
 int decode_by_item(int sms, int d, long long items, long long keys) {
   if (items > 2LL * sms) return 0;
@@ -193,10 +194,10 @@ int split_limit(int sms, long long ctas) {
   return (int)(s > kMaxSplits ? kMaxSplits : s);
 }
 // Query tiles of 128 rows a CTA: one or two.  Two against one in us, 32
-// sequences of 16384 keys, 8 heads of 128 channels: 128 rows 444 / 266, 144
-// rows 444 / 521, 256 rows 451 / 531; 16 of 4096: 64.8 / 43.8, 65.6 / 81.7,
-// 68.4 / 84.4.  (With few CTAs, 4 sequences of 2048 keys, one is the better at
-// 256 rows, 28.0 / 25.2, and past that.)
+// sequences of 16384 keys, 8 heads of 128 channels: 128 rows 418 / 267, 144
+// rows 438 / 518, 256 rows 447 / 530; 16 of 4096: 61.6 / 43.6, 64.9 / 81.3,
+// 67.8 / 83.9.  (With few CTAs, 4 sequences of 2048 keys, one is the better at
+// 256 rows, 28.0 / 24.8, and past that.)
 int query_tiles(long long cap) { return cap <= 128 ? 1 : 2; }
 long long chunk_tiles(int batch, int heads, long long cap, int* q_tiles) {
   const int per = 128 * query_tiles(cap);

@@ -5,12 +5,16 @@
 // token r / group, head r % group, and a CTA takes 128 NQ of them over all
 // their keys, 128 at a time: S = c Q K^T, O += P V with the running base and
 // sum of the softmax.  4 d flops per row and key against 2 d bytes per key and
-// CTA: bound by the tensor cores.  Measured (24 heads of 128 channels, 4680 rows,
-// 23400 keys): 0.94 ms, 1430 TFLOP/s; 3400 cycles a tile of 128 keys and 256
-// rows, of which the products take 2048 at their nominal rates.  They do not
-// reach them: Q K^T reads both operands from shared memory, all of its 128
-// bytes a cycle, and every commit and every instruction of the issuing thread
-// shows (four commits less a tile 6 %, its loop unrolled by two tiles 2 %).
+// CTA: at 128 channels bound by the tensor cores.  Measured (24 heads of 128
+// channels, 4680 rows, 23400 keys): 0.98 ms, 1380 TFLOP/s, with other inputs in
+// each call, 0.945 ms on the same ones again and again: 3400 cycles a tile of
+// 128 keys and 256 rows, of which the products take 2048 at their nominal rates.
+// They do not reach them: Q K^T reads both operands from shared memory, all of
+// its 128 bytes a cycle, and every commit and every instruction of the issuing
+// thread shows (four commits less a tile 6 %, its loop unrolled by two tiles
+// 2 %).  At 64 channels the products are half as long and the softmax is not:
+// the tensor pipe is active 34 % of the time, not 56 (1536 rows of 24 heads,
+// 8192 keys), 256 rows of 32 sequences of 16384 keys and 8 heads take 375 us.
 // Leaving out the exponentials would save 2 %, the conversion of V nothing;
 // scores in halves of 64 keys, so that the next ones start earlier, read the
 // query twice as often: 1.34 ms.

@@ -30,8 +30,8 @@
 // slower: 249 against 188 us for 16 rows, 32 sequences of 16384 keys, 8 heads.
 //
 // Numbers.  E4M3 codes are exact in FP16.  A query row is scaled by a power of
-// two to a largest magnitude in [2^14, 2^15), exact in FP16 down to 2^-39 of
-// that maximum.  The page scales are powers of two applied outside the
+// two to a largest magnitude in [2^14, 2^15): exact in FP16 down to 2^-31 of
+// that maximum, off by 2^-39 of it at most below.  The page scales are powers of two applied outside the
 // products: K's to the fp32 scores, V's (2^ev) to the weight before it is
 // rounded to FP16.  Two running bases a row, over the keys that it attends to:
 // the largest score m for the sum of weights, which knows no V scale, and the
@@ -56,8 +56,8 @@ constexpr int kUnit = 32;          // keys per unit
 constexpr int kMinUnits = 2;       // per warp, when the work is small
 // What an item's start costs the warp that comes to it from another one, in
 // units: its table entries, scales, query rows and first copies one after
-// another (64 sequences of up to 8192 keys, 8 heads: none 95.9, one 88.1, two
-// 85.5, three 86.5 us).
+// another (64 sequences of up to 8192 keys, 8 heads: none 96.7, one 87.9, two
+// 85.1, three 85.1 us).
 constexpr int kStartUnits = 2;
 constexpr int kMaxCluster = 16;
 constexpr float kNoOutput = -1000.f;   // where a row's output has no base yet

@@ -621,7 +621,9 @@ def paged_attention(cache: PagedCache, q: torch.Tensor, block_table: torch.Tenso
                     layer: int = 0, out=None, with_lse: bool = False, workspace=None, stream=None):
     """kvq_paged_attention: q [rows, q_heads, head_dim] bf16, packed like
     pages_append's rows (which come first: kv_lens counts the queries' own
-    tokens).  max_q: the most rows a sequence has (default: all of them).
+    tokens).  max_q: the most rows a sequence has.  It chooses the kernel and
+    sizes the workspace; with offsets, name it: the default is all rows of the
+    batch, so that single tokens of many sequences would run as prompts.
     Returns out [rows, q_heads, head_dim] (and lse [rows, q_heads] fp32 with
     with_lse)."""
     _int32("layer", layer)
