@@ -492,7 +492,8 @@ size_t kvq_paged_workspace_bytes(const kvq_pages *pages, int32_t q_heads, int32_
  * (window counts back from t, with or without causal):
  *   s_j = scale * q . k_j,  out = sum_j softmax(s)_j v_j,
  *   lse = log sum_j exp(s_j).
- * for any page scales, as far as scores stay within fp32.
+ * for any page scales, as far as scale * max |q| * 448 * 2^e of a K page stays
+ * within fp32.
  * A row that attends to nothing gets out = 0, lse = -infinity.  What masked
  * places hold (NaN codes among it) does not matter when no row of the
  * sequence's query heads attends there.  A query row that holds a NaN or an
