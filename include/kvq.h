@@ -53,8 +53,9 @@ typedef enum {
   KVQ_ERR_TOO_LARGE = 7,    /* needs more than the built-in scratch holds   */
   KVQ_ERR_RANGE = 8,        /* an operand left the FP16 range (see below)   */
   KVQ_ERR_BOUNDS = 9,       /* checked build only: an index left its buffer */
-  KVQ_ERR_PAGE = 10         /* paged cache: a table entry, length or offset
+  KVQ_ERR_PAGE = 10,        /* paged cache: a table entry, length or offset
                                points outside the cache (see kvq_pages)     */
+  KVQ_ERR_POSITION = 11     /* rotary positions: one outside the table      */
 } kvq_status;
 
 /* Correction applied to cached-key scores before the softmax. */
@@ -520,6 +521,85 @@ kvq_status kvq_paged_attention(const kvq_pages *pages, int32_t layer, const uint
                                const kvq_sequences *seqs, int32_t max_q, float scale,
                                int32_t causal, int32_t window, void *workspace,
                                size_t workspace_bytes, uint16_t *out, float *lse, void *stream);
+
+/* ---- Rotary positions ---------------------------------------------------------
+ *
+ * Rotation of queries and keys by their positions, for the layers that the
+ * paged cache and the chunk window serve; no counterpart in the paper (its
+ * Hadamard rotation, kvq_rotate, is another one and comes after this).
+ *
+ * A row has `axes` positions (1 for text, 3 for the time, height and width of
+ * video, up to 4).  Pair p of its channels, (p, pairs + p) or when interleaved
+ * (2 p, 2 p + 1), belongs to axis axis[p] and turns by the angle whose cosine
+ * and sine stand in cos_sin[position of that axis][p]:
+ *   y0 = x0 cos - x1 sin,   y1 = x1 cos + x0 sin
+ * (inverse != 0: with -sin, which undoes it and is its gradient), each product
+ * and each sum rounded to fp32 by itself, the result once to BF16.  Channels
+ * from 2 pairs on stay as they are.
+ *   cos_sin  fp32 [n_positions][pairs][2] device, 16-byte aligned
+ *   pairs    a multiple of 8, 2 pairs <= head_dim; n_positions >= 1
+ * A position outside [0, n_positions) records KVQ_ERR_POSITION in the device
+ * status word; the row is rotated by the nearest position of the table.
+ */
+#define KVQ_ROPE_MAX_PAIRS 64
+#define KVQ_ROPE_MAX_AXES 4
+typedef struct kvq_rope_table {
+  float *cos_sin;
+  int32_t n_positions, pairs, axes, interleaved;
+  uint8_t axis[KVQ_ROPE_MAX_PAIRS];
+} kvq_rope_table;
+
+/*
+ * Fills cos_sin: factor * cos and factor * sin of position * frequency[p], the
+ * angle, its cosine and sine in 64 bits, rounded once.  frequency: HOST array
+ * of `pairs` finite numbers, read before the call returns.
+ */
+kvq_status kvq_rope_fill(const kvq_rope_table *table, const double *frequency, double factor,
+                         void *stream);
+
+/* One tensor of a kvq_rope call: row i of batch entry b and head h at b *
+ * batch_stride + i * row_stride + h * head_stride elements (multiples of 8;
+ * head_dim contiguous), 16-byte aligned.  y == x with the same strides (in
+ * place) or memory that does not overlap it. */
+typedef struct kvq_rope_tensor {
+  const uint16_t *x;
+  uint16_t *y;
+  int64_t x_batch_stride, x_row_stride, x_head_stride;
+  int64_t y_batch_stride, y_row_stride, y_head_stride;
+  int32_t heads;
+} kvq_rope_tensor;
+
+/*
+ * Rotates n_tensors (1 or 2: queries and keys) tensors of batch x rows rows,
+ * BF16, head_dim 64 or 128.  positions: int32 device, that of batch entry b,
+ * row i and axis k at b * pos_batch_stride + i * pos_row_stride + k *
+ * pos_axis_stride elements.  batch * rows == 0 is a no-op.  batch * rows <=
+ * 2^31 - 1, times the tensors' heads <= 2^35 (else KVQ_ERR_TOO_LARGE).
+ */
+kvq_status kvq_rope(const kvq_rope_table *table, const int32_t *positions, int64_t pos_batch_stride,
+                    int64_t pos_row_stride, int64_t pos_axis_stride, int32_t batch, int32_t rows,
+                    int32_t head_dim, int32_t inverse, const kvq_rope_tensor *tensors,
+                    int32_t n_tensors, void *stream);
+
+/*
+ * kvq_pages_append of keys that are rotated on the way (values are not), and
+ * the queries beside them: the rotated key goes to its E4M3 code and into the
+ * page's maximum from fp32, rounded once.  positions: int32 [rows][axes]
+ * device (rows pos_row_stride elements apart, axes next to each other), or
+ * NULL where axes == 1: the tokens' places in their sequences, kv_lens[b] -
+ * n_b + i.  q: BF16 as in kvq_paged_attention, rotated into q_out (in place or
+ * apart, strides of its own); NULL with q_heads = 0 for none.  Rows before
+ * offsets[0] and at or behind offsets[batch] are neither read nor written.
+ * rows * q_heads <= 2^32 (else KVQ_ERR_TOO_LARGE).  Everything else as
+ * kvq_pages_append says.
+ */
+kvq_status kvq_pages_append_rope(const kvq_pages *pages, int32_t layer, const kvq_rope_table *table,
+                                 const int32_t *positions, int64_t pos_row_stride,
+                                 const uint16_t *k_new, int64_t k_row_stride, int64_t k_head_stride,
+                                 const uint16_t *v_new, int64_t v_row_stride, int64_t v_head_stride,
+                                 const uint16_t *q, int64_t q_row_stride, int64_t q_head_stride,
+                                 int32_t q_heads, uint16_t *q_out, int64_t q_out_row_stride,
+                                 int64_t q_out_head_stride, const kvq_sequences *seqs, void *stream);
 
 /*
  * Copy pages src[i] -> dst[i], i < n, of every layer: K, V and scales (the

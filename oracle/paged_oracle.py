@@ -139,3 +139,34 @@ def compact(table, n_pages: int):
     moves = list(zip([x for x in live if x >= n], holes))
     to = dict(moves)
     return np.vectorize(lambda x: to.get(int(x), int(x)))(t) if t.size else t, n, moves
+
+
+def rope(x, positions, frequency, axis, interleaved: bool, inverse: bool = False):
+    """Rows x [rows, heads, d] turned by their positions [rows, axes]: pair p, of
+    the axis axis[p], by the angle position * frequency[p]."""
+    x = np.array(x, np.float64)
+    n = len(frequency)
+    angle = np.asarray(positions, np.float64)[:, np.asarray(axis)] * np.asarray(frequency, np.float64)
+    turn = np.exp((-1j if inverse else 1j) * angle)[:, None]
+    first, second = (x[..., 0:2 * n:2], x[..., 1:2 * n:2]) if interleaved else (x[..., :n], x[..., n:2 * n])
+    z = (first + 1j * second) * turn
+    y = x.copy()
+    if interleaved:
+        y[..., 0:2 * n:2], y[..., 1:2 * n:2] = z.real, z.imag
+    else:
+        y[..., :n], y[..., n:2 * n] = z.real, z.imag
+    return y
+
+
+def rope_steps(x, cos_sin, positions, axis, interleaved: bool, inverse: bool = False):
+    """The same with a table [positions, pairs, 2], each product and each sum
+    rounded to fp32 by itself: the values that the append quantizes."""
+    x, cos_sin = np.array(x, np.float32), np.asarray(cos_sin, np.float32)
+    n = cos_sin.shape[1]
+    cs = cos_sin[np.asarray(positions)[:, np.asarray(axis)], np.arange(n)][:, None]
+    c, s = cs[..., 0], -cs[..., 1] if inverse else cs[..., 1]
+    a, b = (slice(0, 2 * n, 2), slice(1, 2 * n, 2)) if interleaved else (slice(0, n), slice(n, 2 * n))
+    first, second, y = x[..., a], x[..., b], x.copy()
+    y[..., a] = first * c - second * s
+    y[..., b] = second * c + first * s
+    return y

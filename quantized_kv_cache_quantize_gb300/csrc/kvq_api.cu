@@ -319,6 +319,8 @@ const char* kvq_status_string(kvq_status s) {
       return "checked build: an index left its buffer (see kvq_debug_bounds_site)";
     case KVQ_ERR_PAGE:
       return "paged cache: a table entry, length or offset points outside the cache";
+    case KVQ_ERR_POSITION:
+      return "rotary positions: a position outside the table";
   }
   return "unknown status";
 }

@@ -34,6 +34,38 @@ struct AppendArgs {
   int* bounds_site;
 };
 
+// A table of rotations: (cos, sin) of pair p at a position, and the pair's axis.
+struct RopeTab {
+  const float2* cs;   // [n][pairs]
+  int n, pairs, axes, interleaved;
+  uint8_t axis[KVQ_ROPE_MAX_PAIRS];
+};
+
+// One tensor that is rotated, [batch][row][head][d] at strides in elements.
+struct RopeTensor {
+  const uint16_t* x;
+  uint16_t* y;
+  long long xb, xr, xh, yb, yr, yh;
+  int heads;
+};
+
+struct RopeArgs {
+  RopeTab t;
+  const int32_t* pos;
+  long long pb, pr, pa;   // strides of batch entries, rows, axes
+  RopeTensor x[2];
+  int batch, rows, d, inverse;
+  int* status;
+};
+
+struct AppendRopeArgs {
+  AppendArgs a;
+  RopeTab t;
+  const int32_t* pos;     // null: a token's place in its sequence
+  long long pr;
+  RopeTensor q;           // heads = 0: none
+};
+
 struct PagedAttnArgs {
   PageLayer p;
   PageSeqs s;
@@ -71,6 +103,10 @@ struct CompactArgs {
 };
 
 cudaError_t launch_pages_append(const AppendArgs& a, cudaStream_t stream);
+cudaError_t launch_rope_fill(float* cos_sin, int n, int pairs, const double* frequency, double factor,
+                             cudaStream_t stream);
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream);
+cudaError_t launch_pages_append_rope(const AppendRopeArgs& a, cudaStream_t stream);
 kvq_status launch_paged_attention(const PagedAttnArgs& a, cudaStream_t stream);
 // bytes, 16 where none are needed
 size_t paged_attention_workspace(int kv_heads, int q_heads, int d, int batch, long long keys, int rows, int max_q);

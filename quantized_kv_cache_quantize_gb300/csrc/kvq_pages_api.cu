@@ -93,6 +93,61 @@ kvq::PagePool pool_of(const kvq_pages* p) {
 // rows of 16-byte vectors at these strides
 bool bad_stride(int64_t s) { return s < 0 || (s & 7) != 0; }
 
+kvq_status check_rope(const kvq_rope_table* t, int head_dim) {
+  if (t == nullptr || t->cos_sin == nullptr || t->n_positions < 1) return KVQ_ERR_INVALID_ARG;
+  if (t->pairs < 8 || t->pairs % 8 != 0 || t->pairs > KVQ_ROPE_MAX_PAIRS || 2 * t->pairs > head_dim) return KVQ_ERR_INVALID_ARG;
+  if (t->axes < 1 || t->axes > KVQ_ROPE_MAX_AXES) return KVQ_ERR_INVALID_ARG;
+  for (int p = 0; p < t->pairs; ++p)
+    if (t->axis[p] >= t->axes) return KVQ_ERR_INVALID_ARG;
+  if (!aligned(t->cos_sin, 16)) return KVQ_ERR_ALIGNMENT;
+  return KVQ_OK;
+}
+
+kvq::RopeTab rope_of(const kvq_rope_table* t) {
+  kvq::RopeTab o{};
+  o.cs = reinterpret_cast<const float2*>(t->cos_sin);
+  o.n = t->n_positions;
+  o.pairs = t->pairs;
+  o.axes = t->axes;
+  o.interleaved = t->interleaved != 0;
+  std::copy(t->axis, t->axis + KVQ_ROPE_MAX_PAIRS, o.axis);
+  return o;
+}
+
+// The checks and arguments that the appends share; *done where there is
+// nothing to append.
+kvq_status append_args(const kvq_pages* pages, int32_t layer, const uint16_t* k_new, int64_t k_row_stride,
+                       int64_t k_head_stride, const uint16_t* v_new, int64_t v_row_stride, int64_t v_head_stride,
+                       const kvq_sequences* seqs, kvq::AppendArgs* out, bool* done) {
+  *done = false;
+  kvq_status st = check_pool(pages);
+  if (st != KVQ_OK) return st;
+  if (layer < 0 || layer >= pages->layers) return KVQ_ERR_INVALID_ARG;
+  st = check_sequences(seqs, pages->page_tokens);
+  if (st != KVQ_OK) return st;
+  if (seqs->rows == 0) {
+    *done = true;
+    return KVQ_OK;
+  }
+  if (k_new == nullptr || v_new == nullptr) return KVQ_ERR_INVALID_ARG;
+  if (bad_stride(k_row_stride) || bad_stride(k_head_stride) || bad_stride(v_row_stride) ||
+      bad_stride(v_head_stride) || !aligned(k_new, 16) || !aligned(v_new, 16))
+    return KVQ_ERR_ALIGNMENT;
+  kvq::AppendArgs a{};
+  a.p = layer_of(pages, layer);
+  a.s = seqs_of(seqs);
+  if (((long long)(seqs->rows >> a.p.shift) + 2LL * seqs->batch) * pages->kv_heads >= (1LL << 30))
+    return KVQ_ERR_TOO_LARGE;
+  a.x[0] = k_new;
+  a.x[1] = v_new;
+  a.row_stride[0] = k_row_stride;
+  a.row_stride[1] = v_row_stride;
+  a.head_stride[0] = k_head_stride;
+  a.head_stride[1] = v_head_stride;
+  *out = a;
+  return KVQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -111,32 +166,109 @@ kvq_status kvq_pages_append(const kvq_pages* pages, int32_t layer, const uint16_
                             int64_t v_row_stride, int64_t v_head_stride, const kvq_sequences* seqs,
                             void* stream) {
   const Range range("kvq_pages_append");
-  kvq_status st = check_pool(pages);
-  if (st != KVQ_OK) return st;
-  if (layer < 0 || layer >= pages->layers) return KVQ_ERR_INVALID_ARG;
-  st = check_sequences(seqs, pages->page_tokens);
-  if (st != KVQ_OK) return st;
-  if (seqs->rows == 0) return KVQ_OK;
-  if (k_new == nullptr || v_new == nullptr) return KVQ_ERR_INVALID_ARG;
-  if (bad_stride(k_row_stride) || bad_stride(k_head_stride) || bad_stride(v_row_stride) ||
-      bad_stride(v_head_stride) || !aligned(k_new, 16) || !aligned(v_new, 16))
-    return KVQ_ERR_ALIGNMENT;
-  kvq::AppendArgs a{};
-  a.p = layer_of(pages, layer);
-  a.s = seqs_of(seqs);
-  if (((long long)(seqs->rows >> a.p.shift) + 2LL * seqs->batch) * pages->kv_heads >= (1LL << 30))
-    return KVQ_ERR_TOO_LARGE;
-  a.x[0] = k_new;
-  a.x[1] = v_new;
-  a.row_stride[0] = k_row_stride;
-  a.row_stride[1] = v_row_stride;
-  a.head_stride[0] = k_head_stride;
-  a.head_stride[1] = v_head_stride;
+  kvq::AppendArgs a;
+  bool done;
+  const kvq_status st = append_args(pages, layer, k_new, k_row_stride, k_head_stride, v_new, v_row_stride, v_head_stride,
+                                    seqs, &a, &done);
+  if (st != KVQ_OK || done) return st;
   a.status = kvq::status_ptr();
   a.bounds_site = kvq::bounds_site_ptr();
   if (a.status == nullptr) return KVQ_ERR_CUDA;
   return kvq::launch_pages_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK
                                                                                       : KVQ_ERR_CUDA;
+}
+
+kvq_status kvq_rope_fill(const kvq_rope_table* table, const double* frequency, double factor, void* stream) {
+  const Range range("kvq_rope_fill");
+  const kvq_status st = check_rope(table, 2 * KVQ_ROPE_MAX_PAIRS);
+  if (st != KVQ_OK) return st;
+  if (frequency == nullptr || !std::isfinite(factor)) return KVQ_ERR_INVALID_ARG;
+  for (int p = 0; p < table->pairs; ++p)
+    if (!std::isfinite(frequency[p])) return KVQ_ERR_INVALID_ARG;
+  return kvq::launch_rope_fill(table->cos_sin, table->n_positions, table->pairs, frequency, factor,
+                               static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? KVQ_OK
+             : KVQ_ERR_CUDA;
+}
+
+kvq_status kvq_rope(const kvq_rope_table* table, const int32_t* positions, int64_t pos_batch_stride,
+                    int64_t pos_row_stride, int64_t pos_axis_stride, int32_t batch, int32_t rows, int32_t head_dim,
+                    int32_t inverse, const kvq_rope_tensor* tensors, int32_t n_tensors, void* stream) {
+  const Range range("kvq_rope");
+  if (head_dim != 64 && head_dim != 128) return KVQ_ERR_UNSUPPORTED;
+  const kvq_status st = check_rope(table, head_dim);
+  if (st != KVQ_OK) return st;
+  if (batch < 0 || rows < 0 || tensors == nullptr || n_tensors < 1 || n_tensors > 2) return KVQ_ERR_INVALID_ARG;
+  kvq::RopeArgs a{};
+  long long heads = 0;
+  for (int i = 0; i < n_tensors; ++i) {
+    const kvq_rope_tensor& t = tensors[i];
+    if (t.heads < 0) return KVQ_ERR_INVALID_ARG;
+    heads += t.heads;
+    a.x[i] = kvq::RopeTensor{t.x, t.y, t.x_batch_stride, t.x_row_stride, t.x_head_stride,
+                             t.y_batch_stride, t.y_row_stride, t.y_head_stride, t.heads};
+  }
+  const long long all = (long long)batch * rows;
+  if (all > 0x7fffffffLL || heads > 0x7fffffffLL || (all > 0 && heads > (1LL << 35) / all)) return KVQ_ERR_TOO_LARGE;
+  if (all == 0 || heads == 0) return KVQ_OK;
+  if (positions == nullptr) return KVQ_ERR_INVALID_ARG;
+  if (!aligned(positions, 4)) return KVQ_ERR_ALIGNMENT;
+  for (int i = 0; i < n_tensors; ++i) {
+    const kvq_rope_tensor& t = tensors[i];
+    if (t.heads == 0) continue;
+    if (t.x == nullptr || t.y == nullptr) return KVQ_ERR_INVALID_ARG;
+    if (!aligned(t.x, 16) || !aligned(t.y, 16) || bad_stride(t.x_batch_stride) || bad_stride(t.x_row_stride) ||
+        bad_stride(t.x_head_stride) || bad_stride(t.y_batch_stride) || bad_stride(t.y_row_stride) ||
+        bad_stride(t.y_head_stride))
+      return KVQ_ERR_ALIGNMENT;
+  }
+  a.t = rope_of(table);
+  a.pos = positions;
+  a.pb = pos_batch_stride;
+  a.pr = pos_row_stride;
+  a.pa = pos_axis_stride;
+  a.batch = batch;
+  a.rows = rows;
+  a.d = head_dim;
+  a.inverse = inverse != 0;
+  a.status = kvq::status_ptr();
+  if (a.status == nullptr) return KVQ_ERR_CUDA;
+  return kvq::launch_rope(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+kvq_status kvq_pages_append_rope(const kvq_pages* pages, int32_t layer, const kvq_rope_table* table,
+                                 const int32_t* positions, int64_t pos_row_stride, const uint16_t* k_new,
+                                 int64_t k_row_stride, int64_t k_head_stride, const uint16_t* v_new,
+                                 int64_t v_row_stride, int64_t v_head_stride, const uint16_t* q, int64_t q_row_stride,
+                                 int64_t q_head_stride, int32_t q_heads, uint16_t* q_out, int64_t q_out_row_stride,
+                                 int64_t q_out_head_stride, const kvq_sequences* seqs, void* stream) {
+  const Range range("kvq_pages_append_rope");
+  kvq::AppendRopeArgs p{};
+  bool done;
+  kvq_status st = check_pool(pages);
+  if (st != KVQ_OK) return st;
+  st = check_rope(table, pages->head_dim);
+  if (st != KVQ_OK) return st;
+  if (q_heads < 0 || (q == nullptr) != (q_heads == 0) || (q_out == nullptr) != (q_heads == 0)) return KVQ_ERR_INVALID_ARG;
+  if (positions == nullptr && table->axes != 1) return KVQ_ERR_INVALID_ARG;
+  if (!aligned(positions, 4) || !aligned(q, 16) || !aligned(q_out, 16) || bad_stride(q_row_stride) ||
+      bad_stride(q_head_stride) || bad_stride(q_out_row_stride) || bad_stride(q_out_head_stride))
+    return KVQ_ERR_ALIGNMENT;
+  st = append_args(pages, layer, k_new, k_row_stride, k_head_stride, v_new, v_row_stride, v_head_stride, seqs, &p.a, &done);
+  if (st != KVQ_OK || done) return st;
+  // blocks of the launch: two per page and head, and those of the queries
+  if ((long long)seqs->rows * q_heads > (1LL << 32) ||
+      (((long long)(seqs->rows >> p.a.p.shift) + 2LL * seqs->batch) * pages->kv_heads * 2 +
+       (long long)seqs->rows * q_heads * (pages->head_dim / 16) / 32 + 1) > 0x7fffffffLL)
+    return KVQ_ERR_TOO_LARGE;
+  p.a.status = kvq::status_ptr();
+  p.a.bounds_site = kvq::bounds_site_ptr();
+  if (p.a.status == nullptr) return KVQ_ERR_CUDA;
+  p.t = rope_of(table);
+  p.pos = positions;
+  p.pr = pos_row_stride;
+  p.q = kvq::RopeTensor{q, q_out, 0, q_row_stride, q_head_stride, 0, q_out_row_stride, q_out_head_stride, q_heads};
+  return kvq::launch_pages_append_rope(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
 size_t kvq_paged_workspace_bytes(const kvq_pages* pages, int32_t q_heads, int32_t batch,

@@ -31,6 +31,7 @@ KVQ_ERR_TOO_LARGE = 7
 KVQ_ERR_RANGE = 8
 KVQ_ERR_BOUNDS = 9
 KVQ_ERR_PAGE = 10
+KVQ_ERR_POSITION = 11
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 KEYS_PER_TOKEN = 0
@@ -85,6 +86,29 @@ class SequencesStruct(ctypes.Structure):
     ]
 
 
+ROPE_MAX_PAIRS = 64
+ROPE_MAX_AXES = 4
+
+
+class RopeTableStruct(ctypes.Structure):
+    """Mirror of ``kvq_rope_table`` in include/kvq.h."""
+    _fields_ = [
+        ("cos_sin", ctypes.c_void_p), ("n_positions", ctypes.c_int32), ("pairs", ctypes.c_int32),
+        ("axes", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("axis", ctypes.c_uint8 * ROPE_MAX_PAIRS),
+    ]
+
+
+class RopeTensorStruct(ctypes.Structure):
+    """Mirror of ``kvq_rope_tensor`` in include/kvq.h."""
+    _fields_ = [
+        ("x", ctypes.c_void_p), ("y", ctypes.c_void_p),
+        ("x_batch_stride", ctypes.c_int64), ("x_row_stride", ctypes.c_int64), ("x_head_stride", ctypes.c_int64),
+        ("y_batch_stride", ctypes.c_int64), ("y_row_stride", ctypes.c_int64), ("y_head_stride", ctypes.c_int64),
+        ("heads", ctypes.c_int32),
+    ]
+
+
+_RopeTensors = RopeTensorStruct * 2
 _P = ctypes.c_void_p
 _SIGNATURES = {
     "kvq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -116,6 +140,11 @@ _SIGNATURES = {
                                        ctypes.POINTER(ctypes.c_size_t)]),
     "kvq_pages_append": (ctypes.c_int, [_P, ctypes.c_int32, _P, ctypes.c_int64, ctypes.c_int64,
                                         _P, ctypes.c_int64, ctypes.c_int64, _P, _P]),
+    "kvq_rope_fill": (ctypes.c_int, [_P, _P, ctypes.c_double, _P]),
+    "kvq_rope": (ctypes.c_int, [_P, _P] + [ctypes.c_int64] * 3 + [ctypes.c_int32] * 4 + [_P, ctypes.c_int32, _P]),
+    "kvq_pages_append_rope": (ctypes.c_int, [_P, ctypes.c_int32, _P, _P, ctypes.c_int64] +
+                              [_P, ctypes.c_int64, ctypes.c_int64] * 3 +
+                              [ctypes.c_int32, _P, ctypes.c_int64, ctypes.c_int64, _P, _P]),
     "kvq_paged_workspace_bytes": (ctypes.c_size_t, [_P] + [ctypes.c_int32] * 5),
     "kvq_paged_attention": (ctypes.c_int, [_P, ctypes.c_int32, _P, ctypes.c_int64, ctypes.c_int64,
                                            ctypes.c_int32, _P, ctypes.c_int32, ctypes.c_float,
@@ -613,6 +642,192 @@ def pages_append(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor,
         _check(lib().kvq_pages_append(
             cache._at, layer, k_new.data_ptr(), ks[0], ks[1], v_new.data_ptr(), vs[0], vs[1],
             ctypes.addressof(s), _handle(stream, cache.device)), "kvq_pages_append")
+
+
+def rope_frequencies(pairs: int, base: float = 10000.0, sections=None) -> list[float]:
+    """base^(-i / n) of pair i of n: one ladder over all pairs, or with
+    ``sections`` (pairs of each axis) a ladder of its own for each axis."""
+    sections = [pairs] if sections is None else list(sections)
+    if sum(sections) != pairs:
+        raise ValueError(f"sections {sections} do not add up to {pairs} pairs")
+    return [float(base) ** (-i / n) for n in sections for i in range(n)]
+
+
+class RopeTable:
+    """Cosines and sines of rotary positions (``kvq_rope_table``): cos_sin fp32
+    [n_positions, pairs, 2], made once and kept by the caller;
+    ``RopeTable.build`` computes one.  ``sections``: how many pairs each axis
+    of a position has, in order (None: one axis), or ``axis``: the axis of
+    each pair.  ``interleaved``: pairs of neighbouring channels, otherwise
+    channels p and pairs + p."""
+
+    def __init__(self, cos_sin: torch.Tensor, sections=None, interleaved: bool = False, axis=None):
+        if (cos_sin.dim() != 3 or cos_sin.shape[2] != 2 or cos_sin.dtype != torch.float32
+                or not cos_sin.is_contiguous()):
+            raise ValueError("cos_sin must be a contiguous float32 tensor [n_positions, pairs, 2], got "
+                             f"{cos_sin.dtype} {list(cos_sin.shape)}")
+        n_positions, pairs = int(cos_sin.shape[0]), int(cos_sin.shape[1])
+        if pairs < 8 or pairs % 8 or pairs > ROPE_MAX_PAIRS:
+            raise ValueError(f"the pairs must be a multiple of 8 up to {ROPE_MAX_PAIRS}, got {pairs}")
+        if not 1 <= n_positions <= 0x7FFFFFFF:
+            raise ValueError(f"a table of {n_positions} positions")
+        if axis is None:
+            sections = [pairs] if sections is None else [int(n) for n in sections]
+            if sum(sections) != pairs or min(sections) < 0 or len(sections) > ROPE_MAX_AXES:
+                raise ValueError(f"sections must be up to {ROPE_MAX_AXES} numbers that add up to {pairs} pairs, got {sections}")
+            axis, axes = [a for a, n in enumerate(sections) for _ in range(n)], len(sections)
+        else:
+            if sections is not None:
+                raise ValueError("either sections or axis")
+            axis = [int(a) for a in axis]
+            if len(axis) != pairs or min(axis) < 0 or max(axis) >= ROPE_MAX_AXES:
+                raise ValueError(f"axis must name one of up to {ROPE_MAX_AXES} axes for each of {pairs} pairs, got {axis}")
+            axes = max(axis) + 1
+        c = RopeTableStruct()
+        c.cos_sin, c.n_positions, c.pairs = cos_sin.data_ptr(), n_positions, pairs
+        c.axes, c.interleaved = axes, 1 if interleaved else 0
+        for p, a in enumerate(axis):
+            c.axis[p] = a
+        self.cos_sin, self.struct, self.device = cos_sin, c, cos_sin.device
+        self.n_positions, self.pairs, self.axes, self.interleaved = n_positions, pairs, axes, bool(interleaved)
+        self._at = ctypes.addressof(c)
+
+    @classmethod
+    def build(cls, n_positions: int, frequencies, sections=None, interleaved: bool = False, axis=None,
+              factor: float = 1.0, device="cuda", stream=None) -> "RopeTable":
+        """kvq_rope_fill: the table of position * frequencies[p] (rope_frequencies
+        or any others), cosines and sines times ``factor``."""
+        f = array.array("d", frequencies)
+        dev = torch.device(device)
+        if dev.type != "cuda":
+            raise ValueError(f"the table is computed on a CUDA device, not on {dev}")
+        if dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        with _switch(dev, stream):
+            t = cls(torch.empty((n_positions, len(f), 2), dtype=torch.float32, device=dev), sections, interleaved, axis)
+            _check(lib().kvq_rope_fill(t._at, f.buffer_info()[0], float(factor), _handle(stream, dev)), "kvq_rope_fill")
+        return t
+
+
+def _rope_view(t: torch.Tensor, name: str, like: torch.Tensor | None = None) -> tuple:
+    """(batch, rows, heads, d) and the strides of (batch, row, head) of [rows,
+    heads, d] or [batch, heads, rows, d]; BF16, the channels contiguous."""
+    shape, st = t.shape, t.stride()
+    if len(shape) not in (3, 4):
+        raise ValueError(f"{name} must have shape [rows, heads, d] or [batch, heads, rows, d], got {list(shape)}")
+    if t.dtype is not torch.bfloat16 or not t.is_cuda or (st[-1] != 1 and t.numel() > 0):
+        raise ValueError(f"{name} must be a CUDA bfloat16 tensor with contiguous channels")
+    if like is not None and (shape != like.shape or t.device != like.device):
+        raise ValueError(f"{name} must be a tensor {list(like.shape)} on {like.device}, got {list(shape)} on {t.device}")
+    if like is not None and any(n > 1 and s == 0 for n, s in zip(shape, st)):
+        raise ValueError(f"{name} must not repeat memory (strides {list(st)})")
+    if len(shape) == 3:
+        return (1, shape[0], shape[1], shape[2]), (0, st[0], st[1])
+    return (shape[0], shape[2], shape[1], shape[3]), (st[0], st[2], st[1])
+
+
+def rope(table: RopeTable, q: torch.Tensor, positions: torch.Tensor, k: torch.Tensor | None = None, q_out=None,
+         k_out=None, inverse: bool = False, stream=None):
+    """kvq_rope: q (and k) bf16 [rows, heads, d], as the paged calls take them,
+    or [batch, heads, rows, d], as the chunk window's do.  positions int32:
+    [rows, axes] ([rows] with one axis), for four dimensions shared by the
+    batch, or [batch, rows, axes].  q_out, k_out: where to write (q itself for
+    in place).  Returns the rotated q, with k the pair."""
+    shape, qs = _rope_view(q, "q")
+    batch, rows, heads, d = shape
+    dev = q.device
+    if table.device != dev:
+        raise ValueError(f"the table is on {table.device}, q on {dev}")
+    kshape = ks = None
+    if k is not None:
+        kshape, ks = _rope_view(k, "k")
+        if k.dim() != q.dim() or kshape[:2] != shape[:2] or kshape[3] != d or k.device != dev:
+            raise ValueError(f"k must be like q {list(q.shape)} but for its heads, got {list(k.shape)} on {k.device}")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    if positions.dtype is not torch.int32 or positions.device != dev:
+        raise ValueError(f"positions must be an int32 tensor on {dev}, got {positions.dtype} on {positions.device}")
+    pshape, ps = positions.shape, positions.stride()
+    if table.axes == 1 and pshape == (rows,):
+        pos = (0, ps[0], 0)
+    elif pshape == (rows, table.axes):
+        pos = (0, ps[0], ps[1])
+    elif q.dim() == 4 and pshape == (batch, rows, table.axes):
+        pos = ps
+    else:
+        raise ValueError(f"positions must have shape [{rows}, {table.axes}]"
+                         + (f" or [{batch}, {rows}, {table.axes}]" if q.dim() == 4 else "") + f", got {list(pshape)}")
+    handle = _handle(stream, dev)
+    with _switch(dev, stream):
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        else:
+            _rope_view(q_out, "q_out", q)
+        _, qo = _rope_view(q_out, "q_out")
+        t = _RopeTensors()
+        t[0] = RopeTensorStruct(q.data_ptr(), q_out.data_ptr(), *qs, *qo, heads)
+        if k is not None:
+            if k_out is None:
+                k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
+            else:
+                _rope_view(k_out, "k_out", k)
+            _, ko = _rope_view(k_out, "k_out")
+            t[1] = RopeTensorStruct(k.data_ptr(), k_out.data_ptr(), *ks, *ko, kshape[2])
+        _check(lib().kvq_rope(table._at, positions.data_ptr(), *pos, batch, rows, d, 1 if inverse else 0,
+                              ctypes.addressof(t), 1 if k is None else 2, handle), "kvq_rope")
+    return q_out if k is None else (q_out, k_out)
+
+
+def pages_append_rope(cache: PagedCache, table: RopeTable, k_new: torch.Tensor, v_new: torch.Tensor,
+                      block_table: torch.Tensor, kv_lens: torch.Tensor, offsets=None, positions=None, q=None,
+                      q_out=None, layer: int = 0, stream=None):
+    """kvq_pages_append_rope: pages_append with the keys rotated on the way, and
+    the queries q [rows, q_heads, head_dim] beside them.  positions int32
+    [rows, axes] ([rows] with one axis); None, for one axis: the tokens' places
+    in their sequences.  Returns the rotated queries (q_out, q itself for in
+    place; rows outside the offsets are left as they are), None without q."""
+    _int32("layer", layer)
+    shape, ks = _paged_rows(cache, k_new, "k_new")
+    shape_v, vs = _paged_rows(cache, v_new, "v_new")
+    if shape != shape_v or shape[1] != cache.kv_heads:
+        raise ValueError(f"k_new and v_new must have shape [rows, {cache.kv_heads}, "
+                         f"{cache.head_dim}], got {list(shape)} and {list(shape_v)}")
+    dev, rows = cache.device, shape[0]
+    if table.device != dev:
+        raise ValueError(f"the table is on {table.device}, the cache on {dev}")
+    s = _sequences(cache, rows, block_table, kv_lens, offsets)
+    pos_at, pos_stride = None, 0
+    if positions is not None:
+        pshape = positions.shape
+        if (positions.dtype is not torch.int32 or positions.device != dev
+                or not (pshape == (rows, table.axes) or (table.axes == 1 and pshape == (rows,)))):
+            raise ValueError(f"positions must be an int32 tensor [{rows}, {table.axes}] on {dev}, got "
+                             f"{positions.dtype} {list(pshape)} on {positions.device}")
+        if table.axes > 1 and positions.stride(1) != 1 and rows > 0:
+            raise ValueError("positions must be contiguous in their last dimension")
+        pos_at, pos_stride = positions.data_ptr(), positions.stride(0)
+    elif table.axes != 1:
+        raise ValueError(f"positions of {table.axes} axes must be given")
+    handle = _handle(stream, dev)
+    with _switch(dev, stream):
+        query = (None, 0, 0, 0, None, 0, 0)
+        if q is not None:
+            qshape, qs = _paged_rows(cache, q, "q")
+            if qshape[0] != rows or qshape[1] < 1:
+                raise ValueError(f"q must have {rows} rows and heads, got {list(qshape)}")
+            if q_out is None:
+                q_out = torch.empty(qshape, dtype=torch.bfloat16, device=dev)
+            else:
+                _rope_view(q_out, "q_out", q)
+            qo = q_out.stride()
+            if rows > 0:   # (an empty tensor has no address)
+                query = (q.data_ptr(), qs[0], qs[1], qshape[1], q_out.data_ptr(), qo[0], qo[1])
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        _check(lib().kvq_pages_append_rope(
+            cache._at, layer, table._at, pos_at, pos_stride, k_new.data_ptr(), ks[0], ks[1], v_new.data_ptr(),
+            vs[0], vs[1], *query, ctypes.addressof(s), handle), "kvq_pages_append_rope")
+    return q_out
 
 
 def paged_attention(cache: PagedCache, q: torch.Tensor, block_table: torch.Tensor,
