@@ -541,12 +541,10 @@ kvq_status kvq_paged_attention(const kvq_pages *pages, int32_t layer, const uint
  * A position outside [0, n_positions) records KVQ_ERR_POSITION in the device
  * status word; the row is rotated by the nearest position of the table.
  */
-#define KVQ_ROPE_MAX_PAIRS 64
-#define KVQ_ROPE_MAX_AXES 4
 typedef struct kvq_rope_table {
   float *cos_sin;
   int32_t n_positions, pairs, axes, interleaved;
-  uint8_t axis[KVQ_ROPE_MAX_PAIRS];
+  uint8_t axis[64];
 } kvq_rope_table;
 
 /*

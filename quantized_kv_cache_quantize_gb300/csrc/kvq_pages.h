@@ -6,6 +6,7 @@
 namespace kvq {
 
 constexpr int kPageExpMin = -60, kPageExpMax = 60;   // scale exponents
+constexpr int kRopeMaxPairs = 64, kRopeMaxAxes = 4;
 constexpr int kCompactMaxPages = 1 << 20;            // the plan's bitmap fits shared memory
 
 // One layer of a pool.
@@ -38,7 +39,7 @@ struct AppendArgs {
 struct RopeTab {
   const float2* cs;   // [n][pairs]
   int n, pairs, axes, interleaved;
-  uint8_t axis[KVQ_ROPE_MAX_PAIRS];
+  uint8_t axis[kRopeMaxPairs];
 };
 
 // One tensor that is rotated, [batch][row][head][d] at strides in elements.

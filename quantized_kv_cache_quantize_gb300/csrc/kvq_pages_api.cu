@@ -95,8 +95,8 @@ bool bad_stride(int64_t s) { return s < 0 || (s & 7) != 0; }
 
 kvq_status check_rope(const kvq_rope_table* t, int head_dim) {
   if (t == nullptr || t->cos_sin == nullptr || t->n_positions < 1) return KVQ_ERR_INVALID_ARG;
-  if (t->pairs < 8 || t->pairs % 8 != 0 || t->pairs > KVQ_ROPE_MAX_PAIRS || 2 * t->pairs > head_dim) return KVQ_ERR_INVALID_ARG;
-  if (t->axes < 1 || t->axes > KVQ_ROPE_MAX_AXES) return KVQ_ERR_INVALID_ARG;
+  if (t->pairs < 8 || t->pairs % 8 != 0 || t->pairs > kvq::kRopeMaxPairs || 2 * t->pairs > head_dim) return KVQ_ERR_INVALID_ARG;
+  if (t->axes < 1 || t->axes > kvq::kRopeMaxAxes) return KVQ_ERR_INVALID_ARG;
   for (int p = 0; p < t->pairs; ++p)
     if (t->axis[p] >= t->axes) return KVQ_ERR_INVALID_ARG;
   if (!aligned(t->cos_sin, 16)) return KVQ_ERR_ALIGNMENT;
@@ -110,7 +110,7 @@ kvq::RopeTab rope_of(const kvq_rope_table* t) {
   o.pairs = t->pairs;
   o.axes = t->axes;
   o.interleaved = t->interleaved != 0;
-  std::copy(t->axis, t->axis + KVQ_ROPE_MAX_PAIRS, o.axis);
+  std::copy(t->axis, t->axis + kvq::kRopeMaxPairs, o.axis);
   return o;
 }
 
@@ -180,7 +180,7 @@ kvq_status kvq_pages_append(const kvq_pages* pages, int32_t layer, const uint16_
 
 kvq_status kvq_rope_fill(const kvq_rope_table* table, const double* frequency, double factor, void* stream) {
   const Range range("kvq_rope_fill");
-  const kvq_status st = check_rope(table, 2 * KVQ_ROPE_MAX_PAIRS);
+  const kvq_status st = check_rope(table, 2 * kvq::kRopeMaxPairs);
   if (st != KVQ_OK) return st;
   if (frequency == nullptr || !std::isfinite(factor)) return KVQ_ERR_INVALID_ARG;
   for (int p = 0; p < table->pairs; ++p)

@@ -15,7 +15,7 @@ struct FillArgs {
   float2* cs;
   int n, pairs;
   double factor;
-  double f[KVQ_ROPE_MAX_PAIRS];
+  double f[kRopeMaxPairs];
 };
 // Angles, cosines and sines in 64 bits, once for the life of a table.
 __global__ void __launch_bounds__(256) rope_fill_kernel(const __grid_constant__ FillArgs a) {

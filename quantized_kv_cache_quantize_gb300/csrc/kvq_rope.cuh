@@ -10,7 +10,7 @@ namespace {
 // The positions of a row, each held inside the table (a position outside it is
 // recorded).
 struct RopeAt {
-  int p[KVQ_ROPE_MAX_AXES];
+  int p[kRopeMaxAxes];
 };
 __device__ __forceinline__ int rope_position(const RopeTab& t, int p, int* status) {
   if ((unsigned)p >= (unsigned)t.n) {
@@ -22,14 +22,14 @@ __device__ __forceinline__ int rope_position(const RopeTab& t, int p, int* statu
 __device__ __forceinline__ RopeAt rope_at(const RopeTab& t, const int32_t* pos, long long axis_stride, int* status) {
   RopeAt at;
 #pragma unroll
-  for (int k = 0; k < KVQ_ROPE_MAX_AXES; ++k) at.p[k] = k < t.axes ? rope_position(t, __ldg(pos + k * axis_stride), status) : 0;
+  for (int k = 0; k < kRopeMaxAxes; ++k) at.p[k] = k < t.axes ? rope_position(t, __ldg(pos + k * axis_stride), status) : 0;
   return at;
 }
 __device__ __forceinline__ RopeAt rope_at(const RopeTab& t, int pos, int* status) {
   RopeAt at;
   at.p[0] = rope_position(t, pos, status);
 #pragma unroll
-  for (int k = 1; k < KVQ_ROPE_MAX_AXES; ++k) at.p[k] = at.p[0];
+  for (int k = 1; k < kRopeMaxAxes; ++k) at.p[k] = at.p[0];
   return at;
 }
 
