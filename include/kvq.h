@@ -600,6 +600,44 @@ kvq_status kvq_pages_append_rope(const kvq_pages *pages, int32_t layer, const kv
                                  int64_t q_out_head_stride, const kvq_sequences *seqs, void *stream);
 
 /*
+ * Shapes of attention scores and masks beyond causal and window, for
+ * kvq_paged_attention_scored.  Any of them may be left out (0 or NULL).
+ *   softcap  > 0: s = softcap * tanh(s / softcap) of the scaled score; from
+ *            2^-20 to 2^20
+ *   slopes   fp32 [q_heads] device, finite: s - slopes[h] * |t - j| for the row
+ *            at position t and the key at j, after the cap
+ *   prefix   int32 [batch] device: with causal, a row also attends to the keys
+ *            j < prefix[b] (a prompt whose front sees itself whole)
+ *   ranges   int32 [rows][2] device, 8-byte aligned: row r attends only to the
+ *            keys ranges[r][0] <= j < ranges[r][1] (documents packed into one
+ *            sequence; a row with an empty range attends to nothing)
+ * Row i of sequence b at position t = kv_lens[b] - n_b + i then attends to
+ *   0 <= j < kv_lens[b];  causal: j <= t or j < prefix[b];  window > 0: j > t
+ *   - window;  ranges[r][0] <= j < ranges[r][1].
+ * Any int32 is a valid prefix or bound.  What slopes, prefix and ranges hold is
+ * read on the device when the call runs.
+ */
+typedef struct kvq_scores {
+  float softcap;
+  const float *slopes;
+  const int32_t *prefix;
+  const int32_t *ranges;
+} kvq_scores;
+
+/*
+ * kvq_paged_attention with such scores (NULL: plain ones); the same arguments
+ * otherwise, the same workspace, and what it says of rows that attend to
+ * nothing, of what masked places hold, of NaN and of precision holds here.
+ * lse = log sum_j exp(s_j) of the shaped scores.
+ */
+kvq_status kvq_paged_attention_scored(const kvq_pages *pages, int32_t layer, const uint16_t *q,
+                                      int64_t q_row_stride, int64_t q_head_stride, int32_t q_heads,
+                                      const kvq_sequences *seqs, int32_t max_q, float scale,
+                                      int32_t causal, int32_t window, const kvq_scores *scores,
+                                      void *workspace, size_t workspace_bytes, uint16_t *out,
+                                      float *lse, void *stream);
+
+/*
  * Copy pages src[i] -> dst[i], i < n, of every layer: K, V and scales (the
  * last, partly filled page of a sequence that forks; full pages are shared
  * through the tables).  src, dst: HOST arrays, read before the call returns.

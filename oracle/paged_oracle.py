@@ -170,3 +170,47 @@ def rope_steps(x, cos_sin, positions, axis, interleaved: bool, inverse: bool = F
     y[..., a] = first * c - second * s
     y[..., b] = second * c + first * s
     return y
+
+
+def attention_scored(pool: Pool, q, table, lens, counts, scale: float, causal: bool, window: int, softcap: float = 0.0,
+                     slopes=None, prefix=None, ranges=None):
+    """attention with shaped scores and further masks: what it returns, and
+    last shape_err [rows, q_heads], max_j of |s_j| + |bias_j|, by which the
+    rounding of the shaping itself is measured."""
+    q = np.asarray(q, np.float64)
+    rows, hq, d = q.shape
+    out, lse = np.zeros((rows, hq, d)), np.full((rows, hq), -math.inf)
+    bound, serr, qerr, herr = np.zeros((rows, hq, d)), np.zeros((rows, hq)), np.zeros((rows, hq)), np.zeros((rows, hq))
+    at = 0
+    for b, (length, n) in enumerate(zip(lens, counts)):
+        k, v = pool.rows(0, table[b], length), pool.rows(1, table[b], length)
+        j = np.arange(length)
+        for i in range(n):
+            t = length - n + i
+            see = np.ones(length, bool)
+            if causal:
+                see &= (j <= t) | (j < (0 if prefix is None else int(prefix[b])))
+            if window > 0:
+                see &= j > t - window
+            if ranges is not None:
+                see &= (j >= int(ranges[at + i][0])) & (j < int(ranges[at + i][1]))
+            if not see.any():
+                continue
+            for h in range(hq):
+                g = h // (hq // k.shape[0])
+                s = scale * (k[g][see] @ q[at + i, h])
+                if softcap > 0:
+                    s = softcap * np.tanh(s / softcap)
+                bias = 0 * s if slopes is None else -float(slopes[h]) * np.abs(t - j[see])
+                herr[at + i, h] = (np.abs(s) + np.abs(bias)).max()
+                s = s + bias
+                m = s.max()
+                p = np.exp(s - m)
+                lse[at + i, h] = m + math.log(p.sum())
+                p /= p.sum()
+                out[at + i, h] = p @ v[g][see]
+                bound[at + i, h] = p @ np.abs(v[g][see])
+                serr[at + i, h] = scale * (np.abs(k[g][see]) @ np.abs(q[at + i, h])).max()
+                qerr[at + i, h] = scale * np.abs(q[at + i, h]).max() * np.abs(k[g][see]).sum(1).max()
+        at += n
+    return out, lse, bound, serr, qerr, herr

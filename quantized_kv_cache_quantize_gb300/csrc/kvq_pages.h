@@ -67,6 +67,14 @@ struct AppendRopeArgs {
   RopeTensor q;           // heads = 0: none
 };
 
+// Shapes of scores and masks beyond causal and window (kvq_scores).
+struct ScoreShape {
+  float cap;              // 0: none
+  const float* slopes;    // null: none
+  const int32_t* prefix;
+  const int32_t* ranges;
+};
+
 struct PagedAttnArgs {
   PageLayer p;
   PageSeqs s;
@@ -82,6 +90,7 @@ struct PagedAttnArgs {
   int* status;
   int* bounds_site;
   unsigned long long wait_limit_ns;
+  ScoreShape shape;      // of the scored call
 };
 
 // Pages of all layers, for copies.
@@ -109,6 +118,7 @@ cudaError_t launch_rope_fill(float* cos_sin, int n, int pairs, const double* fre
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream);
 cudaError_t launch_pages_append_rope(const AppendRopeArgs& a, cudaStream_t stream);
 kvq_status launch_paged_attention(const PagedAttnArgs& a, cudaStream_t stream);
+kvq_status launch_paged_attention_scored(const PagedAttnArgs& a, cudaStream_t stream);
 // bytes, 16 where none are needed
 size_t paged_attention_workspace(int kv_heads, int q_heads, int d, int batch, long long keys, int rows, int max_q);
 cudaError_t launch_pages_copy(const PagePool& p, const int32_t* src, const int32_t* dst, int n,

@@ -148,6 +148,58 @@ kvq_status append_args(const kvq_pages* pages, int32_t layer, const uint16_t* k_
   return KVQ_OK;
 }
 
+// The checks and arguments that the attention calls share; *done where there
+// are no rows.
+kvq_status attention_args(const kvq_pages* pages, int32_t layer, const uint16_t* q, int64_t q_row_stride,
+                          int64_t q_head_stride, int32_t q_heads, const kvq_sequences* seqs, int32_t max_q, float scale,
+                          int32_t causal, int32_t window, void* workspace, size_t workspace_bytes, uint16_t* out,
+                          float* lse, kvq::PagedAttnArgs* out_args, bool* done) {
+  *done = false;
+  kvq_status st = check_pool(pages);
+  if (st != KVQ_OK) return st;
+  if (layer < 0 || layer >= pages->layers) return KVQ_ERR_INVALID_ARG;
+  if (q_heads < 1 || q_heads % pages->kv_heads != 0) return KVQ_ERR_INVALID_ARG;
+  st = check_sequences(seqs, pages->page_tokens);
+  if (st != KVQ_OK) return st;
+  if (!std::isfinite(scale) || scale <= 0.f || window < 0 || max_q < 0) return KVQ_ERR_INVALID_ARG;
+  if (seqs->rows == 0) {
+    *done = true;
+    return KVQ_OK;
+  }
+  if (max_q < 1 || q == nullptr || out == nullptr) return KVQ_ERR_INVALID_ARG;
+  if (bad_stride(q_row_stride) || bad_stride(q_head_stride) || !aligned(q, 16) || !aligned(out, 16) ||
+      !aligned(lse, 4) || !aligned(workspace, 16))
+    return KVQ_ERR_ALIGNMENT;
+  if (max_q > seqs->rows) max_q = seqs->rows;
+  if (seqs->offsets == nullptr) max_q = 1;
+  const size_t need = kvq::paged_attention_workspace(
+      pages->kv_heads, q_heads, pages->head_dim, seqs->batch,
+      (long long)seqs->width * pages->page_tokens, seqs->rows, max_q);
+  if (need > 16 && (workspace == nullptr || workspace_bytes < need)) return KVQ_ERR_INVALID_ARG;
+  kvq::PagedAttnArgs a{};
+  a.p = layer_of(pages, layer);
+  a.s = seqs_of(seqs);
+  a.q = q;
+  a.q_row_stride = q_row_stride;
+  a.q_head_stride = q_head_stride;
+  a.q_heads = q_heads;
+  a.group = q_heads / pages->kv_heads;
+  a.max_q = max_q;
+  a.causal = causal != 0;
+  a.window = std::min(window, 1 << 30);   // no sequence is longer; t - window stays in 32 bits
+  a.scale = scale;
+  a.out = out;
+  a.lse = lse;
+  a.ws = workspace;
+  a.ws_bytes = workspace_bytes;
+  a.status = kvq::status_ptr();
+  a.bounds_site = kvq::bounds_site_ptr();
+  a.wait_limit_ns = kvq::wait_limit_ns();
+  if (a.status == nullptr) return KVQ_ERR_CUDA;
+  *out_args = a;
+  return KVQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -285,45 +337,33 @@ kvq_status kvq_paged_attention(const kvq_pages* pages, int32_t layer, const uint
                                int32_t causal, int32_t window, void* workspace,
                                size_t workspace_bytes, uint16_t* out, float* lse, void* stream) {
   const Range range("kvq_paged_attention");
-  kvq_status st = check_pool(pages);
-  if (st != KVQ_OK) return st;
-  if (layer < 0 || layer >= pages->layers) return KVQ_ERR_INVALID_ARG;
-  if (q_heads < 1 || q_heads % pages->kv_heads != 0) return KVQ_ERR_INVALID_ARG;
-  st = check_sequences(seqs, pages->page_tokens);
-  if (st != KVQ_OK) return st;
-  if (!std::isfinite(scale) || scale <= 0.f || window < 0 || max_q < 0) return KVQ_ERR_INVALID_ARG;
-  if (seqs->rows == 0) return KVQ_OK;
-  if (max_q < 1 || q == nullptr || out == nullptr) return KVQ_ERR_INVALID_ARG;
-  if (bad_stride(q_row_stride) || bad_stride(q_head_stride) || !aligned(q, 16) || !aligned(out, 16) ||
-      !aligned(lse, 4) || !aligned(workspace, 16))
-    return KVQ_ERR_ALIGNMENT;
-  if (max_q > seqs->rows) max_q = seqs->rows;
-  if (seqs->offsets == nullptr) max_q = 1;
-  const size_t need = kvq::paged_attention_workspace(
-      pages->kv_heads, q_heads, pages->head_dim, seqs->batch,
-      (long long)seqs->width * pages->page_tokens, seqs->rows, max_q);
-  if (need > 16 && (workspace == nullptr || workspace_bytes < need)) return KVQ_ERR_INVALID_ARG;
-  kvq::PagedAttnArgs a{};
-  a.p = layer_of(pages, layer);
-  a.s = seqs_of(seqs);
-  a.q = q;
-  a.q_row_stride = q_row_stride;
-  a.q_head_stride = q_head_stride;
-  a.q_heads = q_heads;
-  a.group = q_heads / pages->kv_heads;
-  a.max_q = max_q;
-  a.causal = causal != 0;
-  a.window = std::min(window, 1 << 30);   // no sequence is longer; t - window stays in 32 bits
-  a.scale = scale;
-  a.out = out;
-  a.lse = lse;
-  a.ws = workspace;
-  a.ws_bytes = workspace_bytes;
-  a.status = kvq::status_ptr();
-  a.bounds_site = kvq::bounds_site_ptr();
-  a.wait_limit_ns = kvq::wait_limit_ns();
-  if (a.status == nullptr) return KVQ_ERR_CUDA;
+  kvq::PagedAttnArgs a;
+  bool done;
+  const kvq_status st = attention_args(pages, layer, q, q_row_stride, q_head_stride, q_heads, seqs, max_q, scale, causal,
+                                       window, workspace, workspace_bytes, out, lse, &a, &done);
+  if (st != KVQ_OK || done) return st;
   return kvq::launch_paged_attention(a, static_cast<cudaStream_t>(stream));
+}
+
+kvq_status kvq_paged_attention_scored(const kvq_pages* pages, int32_t layer, const uint16_t* q,
+                                      int64_t q_row_stride, int64_t q_head_stride, int32_t q_heads,
+                                      const kvq_sequences* seqs, int32_t max_q, float scale,
+                                      int32_t causal, int32_t window, const kvq_scores* scores, void* workspace,
+                                      size_t workspace_bytes, uint16_t* out, float* lse, void* stream) {
+  const Range range("kvq_paged_attention_scored");
+  const bool capped = scores != nullptr && scores->softcap != 0.f;
+  if (capped && !(scores->softcap >= 9.5367431640625e-07f && scores->softcap <= 1048576.f)) return KVQ_ERR_INVALID_ARG;
+  if (scores != nullptr && (!aligned(scores->slopes, 4) || !aligned(scores->prefix, 4) || !aligned(scores->ranges, 8)))
+    return KVQ_ERR_ALIGNMENT;
+  kvq::PagedAttnArgs a;
+  bool done;
+  const kvq_status st = attention_args(pages, layer, q, q_row_stride, q_head_stride, q_heads, seqs, max_q, scale, causal,
+                                       window, workspace, workspace_bytes, out, lse, &a, &done);
+  if (st != KVQ_OK || done) return st;
+  if (!capped && (scores == nullptr || (!scores->slopes && !scores->prefix && !scores->ranges)))
+    return kvq::launch_paged_attention(a, static_cast<cudaStream_t>(stream));
+  a.shape = kvq::ScoreShape{scores->softcap, scores->slopes, scores->prefix, scores->ranges};
+  return kvq::launch_paged_attention_scored(a, static_cast<cudaStream_t>(stream));
 }
 
 kvq_status kvq_pages_copy(const kvq_pages* pages, const int32_t* src, const int32_t* dst, int32_t n,

@@ -108,6 +108,14 @@ class RopeTensorStruct(ctypes.Structure):
     ]
 
 
+class ScoresStruct(ctypes.Structure):
+    """Mirror of ``kvq_scores`` in include/kvq.h."""
+    _fields_ = [
+        ("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("prefix", ctypes.c_void_p),
+        ("ranges", ctypes.c_void_p),
+    ]
+
+
 _RopeTensors = RopeTensorStruct * 2
 _P = ctypes.c_void_p
 _SIGNATURES = {
@@ -150,6 +158,10 @@ _SIGNATURES = {
                                            ctypes.c_int32, _P, ctypes.c_int32, ctypes.c_float,
                                            ctypes.c_int32, ctypes.c_int32, _P, ctypes.c_size_t, _P,
                                            _P, _P]),
+    "kvq_paged_attention_scored": (ctypes.c_int, [_P, ctypes.c_int32, _P, ctypes.c_int64, ctypes.c_int64,
+                                                  ctypes.c_int32, _P, ctypes.c_int32, ctypes.c_float,
+                                                  ctypes.c_int32, ctypes.c_int32, _P, _P, ctypes.c_size_t, _P,
+                                                  _P, _P]),
     "kvq_pages_copy": (ctypes.c_int, [_P, _P, _P, ctypes.c_int32, _P]),
     "kvq_pages_compact_workspace_bytes": (ctypes.c_size_t, [_P]),
     "kvq_pages_compact": (ctypes.c_int, [_P, _P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int64,
@@ -830,15 +842,34 @@ def pages_append_rope(cache: PagedCache, table: RopeTable, k_new: torch.Tensor, 
     return q_out
 
 
+def _scores(cache: PagedCache, q_heads: int, batch: int, rows: int, softcap, slopes, prefix, ranges):
+    """A call's kvq_scores, None for plain scores."""
+    if slopes is None and prefix is None and ranges is None and softcap == 0.0:
+        return None
+    for name, t, dtype, shape in (("slopes", slopes, torch.float32, (q_heads,)), ("prefix", prefix, torch.int32, (batch,)),
+                                  ("ranges", ranges, torch.int32, (rows, 2))):
+        if t is not None and (t.dtype is not dtype or t.shape != shape or t.device != cache.device
+                              or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {cache.device}, got "
+                             f"{t.dtype} {list(t.shape)} on {t.device}")
+    return ScoresStruct(softcap, *[None if t is None else t.data_ptr() for t in (slopes, prefix, ranges)])
+
+
 def paged_attention(cache: PagedCache, q: torch.Tensor, block_table: torch.Tensor,
                     kv_lens: torch.Tensor, offsets=None, max_q: int | None = None,
                     scale: float | None = None, causal: bool = True, window: int = 0,
-                    layer: int = 0, out=None, with_lse: bool = False, workspace=None, stream=None):
+                    layer: int = 0, out=None, with_lse: bool = False, workspace=None, stream=None,
+                    softcap: float = 0.0, slopes=None, prefix=None, ranges=None):
     """kvq_paged_attention: q [rows, q_heads, head_dim] bf16, packed like
     pages_append's rows (which come first: kv_lens counts the queries' own
     tokens).  max_q: the most rows a sequence has.  It chooses the kernel and
     sizes the workspace; with offsets, name it: the default is all rows of the
     batch, so that single tokens of many sequences would run as prompts.
+    Shaped scores and further masks (kvq_paged_attention_scored): softcap, the
+    scores' cap (0: none); slopes, fp32 [q_heads], a bias that falls with the
+    distance of row and key; prefix, int32 [batch], the tokens at the front of
+    each sequence that all its rows see; ranges, int32 [rows, 2], first and
+    end of the keys that a row may see.
     Returns out [rows, q_heads, head_dim] (and lse [rows, q_heads] fp32 with
     with_lse)."""
     _int32("layer", layer)
@@ -849,6 +880,7 @@ def paged_attention(cache: PagedCache, q: torch.Tensor, block_table: torch.Tenso
     if q_heads < 1 or q_heads % cache.kv_heads:
         raise ValueError(f"q has {q_heads} heads, not a multiple of the cache's {cache.kv_heads}")
     s = _sequences(cache, rows, block_table, kv_lens, offsets)
+    shaped = _scores(cache, q_heads, s.batch, rows, softcap, slopes, prefix, ranges)
     if offsets is None:
         max_q = 1
     elif max_q is None:
@@ -875,10 +907,17 @@ def paged_attention(cache: PagedCache, q: torch.Tensor, block_table: torch.Tenso
         else:
             ws_ptr, ws_bytes = _workspace_arg(workspace, dev)
             ws = ws_ptr.value
-        _check(lib().kvq_paged_attention(
-            cache._at, layer, q.data_ptr(), qs[0], qs[1], q_heads, ctypes.addressof(s), max_q,
-            1.0 / math.sqrt(d) if scale is None else scale, 1 if causal else 0, window, ws, ws_bytes,
-            out.data_ptr(), None if lse is None else lse.data_ptr(), handle), "kvq_paged_attention")
+        scale = 1.0 / math.sqrt(d) if scale is None else scale
+        lse_at = None if lse is None else lse.data_ptr()
+        if shaped is None:
+            _check(lib().kvq_paged_attention(
+                cache._at, layer, q.data_ptr(), qs[0], qs[1], q_heads, ctypes.addressof(s), max_q, scale,
+                1 if causal else 0, window, ws, ws_bytes, out.data_ptr(), lse_at, handle), "kvq_paged_attention")
+        else:
+            _check(lib().kvq_paged_attention_scored(
+                cache._at, layer, q.data_ptr(), qs[0], qs[1], q_heads, ctypes.addressof(s), max_q, scale,
+                1 if causal else 0, window, ctypes.addressof(shaped), ws, ws_bytes, out.data_ptr(), lse_at,
+                handle), "kvq_paged_attention_scored")
     return (out, lse) if with_lse else out
 
 
