@@ -176,14 +176,17 @@ def attention_scored(pool: Pool, q, table, lens, counts, scale: float, causal: b
                      slopes=None, prefix=None, ranges=None):
     """attention with shaped scores and further masks: what it returns, and
     last shape_err [rows, q_heads], max_j of |s_j| + |bias_j|, by which the
-    rounding of the shaping itself is measured."""
+    rounding of the shaping itself is measured, and top [rows, q_heads], the
+    largest product of a weight and its V scale."""
     q = np.asarray(q, np.float64)
     rows, hq, d = q.shape
     out, lse = np.zeros((rows, hq, d)), np.full((rows, hq), -math.inf)
     bound, serr, qerr, herr = np.zeros((rows, hq, d)), np.zeros((rows, hq)), np.zeros((rows, hq)), np.zeros((rows, hq))
+    tops = np.zeros((rows, hq))
     at = 0
     for b, (length, n) in enumerate(zip(lens, counts)):
         k, v = pool.rows(0, table[b], length), pool.rows(1, table[b], length)
+        ev = 2.0 ** np.repeat(pool.exp[1][np.asarray(table[b][:-(-length // pool.page)], np.int64)], pool.page, axis=0)[:length]
         j = np.arange(length)
         for i in range(n):
             t = length - n + i
@@ -210,7 +213,8 @@ def attention_scored(pool: Pool, q, table, lens, counts, scale: float, causal: b
                 p /= p.sum()
                 out[at + i, h] = p @ v[g][see]
                 bound[at + i, h] = p @ np.abs(v[g][see])
+                tops[at + i, h] = (p * ev[see, g]).max()
                 serr[at + i, h] = scale * (np.abs(k[g][see]) @ np.abs(q[at + i, h])).max()
                 qerr[at + i, h] = scale * np.abs(q[at + i, h]).max() * np.abs(k[g][see]).sum(1).max()
         at += n
-    return out, lse, bound, serr, qerr, herr
+    return out, lse, bound, serr, qerr, herr, tops

@@ -21,7 +21,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkvq.so")
 SOURCES = ["kvq_api.cu", "kvq_quant.cu", "kvq_quant_mma.cu", "kvq_attn.cu", "kvq_attn_exact.cu", "kvq_attn_kch.cu",
            "kvq_attn_pair.cu", "kvq_pages_api.cu", "kvq_pages.cu", "kvq_rope.cu",
-           "kvq_paged_attn.cu", "kvq_paged_scored.cu"]
+           "kvq_paged_attn.cu", "kvq_paged_biased.cu", "kvq_paged_capped.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

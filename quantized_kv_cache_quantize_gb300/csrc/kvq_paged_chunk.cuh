@@ -52,6 +52,7 @@
 
 #include "kvq_checks.cuh"
 #include "kvq_pages.cuh"
+#include "kvq_scores.cuh"
 
 namespace kvq {
 namespace {
@@ -232,6 +233,35 @@ __device__ __noinline__ float weights_apart(uint32_t t_h, uint32_t mh, float cq,
   return sum;
 }
 
+// the same for shaped scores
+template <int MODE>
+__device__ __noinline__ float shaped_weights_apart(uint32_t t_h, uint32_t mh, float cq, float m, int lo, int hi,
+                                                   uint32_t there, RowShape shape, int dist, bool left) {
+  float sum = 0.f;
+#pragma unroll 1
+  for (int k = 0; k < 4; k += 2) {
+    uint32_t v[32], w[16];
+    ptx::tmem_ld32(t_h + 16 * k, v);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float raw = cq * lds_f(mh + 4 * (k + i)), ev = lds_f(mh + kMetaShift + 4 * (k + i));
+      shape_block<MODE>(v + 16 * i, raw, shape, dist - 16 * (k + i), left);
+      const float ck = fmaxf(shape_factor<MODE>(shape, raw), 1.2e-38f);
+      mask_block(v + 16 * i, (there >> (k + i)) & 1u ? lo - 16 * (k + i) : 16, hi - 16 * (k + i));
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float x0 = with_ev(__uint_as_float(v[16 * i + 2 * c]), ck, ev) - m;
+        const float x1 = with_ev(__uint_as_float(v[16 * i + 2 * c + 1]), ck, ev) - m;
+        w[8 * i + c] = ptx::f16x2_rn(ptx::ex2_approx(x0), ptx::ex2_approx(x1));
+        sum += ptx::ex2_approx(x0 - ev) + ptx::ex2_approx(x1 - ev);
+      }
+    }
+    ptx::tmem_st16(t_h + 8 * k, w);   // (columns that the loads are past)
+  }
+  ptx::tmem_st_wait();
+  return sum;
+}
+
 // words that pass between a softmax warp and the MMA thread
 __device__ __forceinline__ void st_release(uint32_t at, uint32_t v) {
   asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
@@ -264,7 +294,7 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(bar);
 }
 
-template <int D, int NQ>
+template <int D, int NQ, int MODE>
 __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
     chunk_kernel(const __grid_constant__ ChunkArgs p, const __grid_constant__ CUtensorMap map_k,
                  const __grid_constant__ CUtensorMap map_v) {
@@ -298,13 +328,35 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
   const int t0 = len - n;                       // position of row 0
   // keys that some row of the tile attends to, and their 128-key tiles
   const int i_first = row0 / a.group, i_last = (min(rows, row0 + 128 * NQ) - 1) / a.group;
-  const int key_hi = a.causal ? max(min(len, t0 + i_last + 1), 0) : len;
-  const int key_lo = a.window > 0 ? max(0, t0 + i_first - a.window + 1) : 0;
+  int key_hi = a.causal ? max(min(len, t0 + i_last + 1), 0) : len;
+  int key_lo = a.window > 0 ? max(0, t0 + i_first - a.window + 1) : 0;
+  __shared__ int2 spans[MODE == kPlain ? 1 : 128 * NQ];   // [first, end) of each token's keys
+  __shared__ int hull[2];
+  if (MODE != kPlain) {
+    if (tid < 2) hull[tid] = tid == 0 ? 0x7fffffff : 0;
+    __syncthreads();
+    for (int i = i_first + tid; i <= i_last; i += C::kThreads) {
+      const RowView v = row_view(a, b, r0 + i, t0 + i, len);
+      spans[i - i_first] = make_int2(v.lo, v.hi);
+      if (v.lo < v.hi) {
+        atomicMin(&hull[0], v.lo);
+        atomicMax(&hull[1], v.hi);
+      }
+    }
+    __syncthreads();
+    key_hi = hull[1];
+    key_lo = min(hull[0], key_hi);
+  }
   const int tile_lo = key_lo / kTileKeys;
   const int tiles = key_hi > key_lo ? (key_hi + kTileKeys - 1) / kTileKeys - tile_lo : 0;
   const int j0 = (int)((long long)tiles * split / p.splits), j1 = (int)((long long)tiles * (split + 1) / p.splits);
   const int n_t = j1 - j0;
-  const int base = (tile_lo + j0) * kTileKeys;  // first key of local tile 0
+  const int base = (tile_lo + j0) * kTileKeys;  // first key of the range
+  // Tiles in ascending order; under a distance bias from the last one down: the
+  // largest scores come first then, and the base, set by them, need not rise
+  // again and again.
+  const bool down = MODE != kPlain && a.shape.slopes != nullptr;
+  auto tile_at = [&](int j) { return MODE != kPlain && down ? n_t - 1 - j : j; };
 
   volatile int* abort = reinterpret_cast<volatile int*>(smem + C::kBar + kCbCount * 8);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBar + kCbCount * 8 + 4);
@@ -381,7 +433,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
       const int e = max((int)(mx >> 7), 1) - 127 - 7;      // largest magnitude to [2^7, 2^8)
       // (an infinity or a NaN makes the whole row NaN)
       const float f0 = mx < 0x7f80u ? pow2f(-(e / 2)) : CUDART_NAN_F, f1 = pow2f(-(e - e / 2));
-      cq = a.scale * 1.4426950408889634f * pow2f(e / 2) * pow2f(e - e / 2);
+      cq = raw_factor<MODE>(a) * pow2f(e / 2) * pow2f(e - e / 2);
       const uint32_t hi_t = sm + C::kQ + (NQ == 2 ? q : 0) * 2 * C::kQT;
       if (NQ == 2 || q == 0) {
 #pragma unroll
@@ -410,8 +462,14 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
 
     // keys this row attends to, from the first key of local tile 0
     const int tq = t0 + tok;
-    const int hi_r = (a.causal ? min(len, tq + 1) : len) - base;
-    const int lo_r = (a.window > 0 ? max(0, tq - a.window + 1) : 0) - base;
+    RowView view{};
+    RowShape shape{};
+    if (MODE != kPlain) {
+      view = row_view(a, b, r0 + tok, tq, len);
+      shape = row_shape<MODE>(a, hq);
+    }
+    const int hi_r = (MODE != kPlain ? view.hi : a.causal ? min(len, tq + 1) : len) - base;
+    const int lo_r = (MODE != kPlain ? view.lo : a.window > 0 ? max(0, tq - a.window + 1) : 0) - base;
     float m = kLowest, l = 0.f;
     const uint32_t t_o = tmem + C::kTO + q * D + lane_off;
     bool ok = true;
@@ -434,7 +492,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
       }
       const uint32_t mt = sm + C::kMeta + (j & (kMetaSlots - 1)) * kMetaBytes;
       const uint32_t there = lds_u(mt + kMetaThere);
-      const int at0 = j * kTileKeys;
+      const int at0 = tile_at(j) * kTileKeys;
+      const bool left = MODE != kPlain && __all_sync(0xffffffffu, base + at0 + kTileKeys <= view.ref + 1);
       const bool whole = __all_sync(0xffffffffu, there == 255u && lo_r <= at0 && hi_r >= at0 + kTileKeys);
       auto rescale_o = [&](float f) {
         const uint64_t f2 = ptx::f2_pack(f, f);
@@ -462,8 +521,17 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
         uint32_t pk[2][16];
         float hat, sum;
         const float wide = lds_f(mt + kMetaWide);
+        // (a scale that underflows must not meet the -inf of a masked score)
+        auto factor = [&](uint32_t ek_at) {
+          return MODE != kPlain ? fmaxf(shape_factor<MODE>(shape, cq * lds_f(ek_at)), 1.2e-38f) : fmaxf(cq * lds_f(ek_at), 1.2e-38f);
+        };
         auto scores = [&](uint32_t (&cur)[64]) {
           ptx::tmem_ld64(t_h, cur);
+          if (MODE != kPlain) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              shape_block<MODE>(cur + 16 * k, cq * lds_f(mh + 4 * k), shape, view.ref - (base + at0 + 64 * half + 16 * k), left);
+          }
           if (!whole) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -477,8 +545,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
           sum = 0.f;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            // (a scale that underflows must not meet the -inf of a masked score)
-            const float ck = fmaxf(cq * lds_f(mh + 4 * k), 1.2e-38f);
+            const float ck = factor(mh + 4 * k);
             float b;
             exp_block(cur + 16 * k, ck, lds_f(mh + kMetaShift + 4 * k) - m, pk[k >> 1] + 8 * (k & 1), b);
             hat += b;
@@ -501,7 +568,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
             float most = -CUDART_INF_F;
 #pragma unroll
             for (int i = 0; i < 16; ++i) most = fmaxf(most, __uint_as_float(cur[16 * k + i]));
-            top = fmaxf(top, with_ev(most, fmaxf(cq * lds_f(mh + 4 * k), 1.2e-38f), lds_f(mh + kMetaShift + 4 * k)));
+            top = fmaxf(top, with_ev(most, factor(mh + 4 * k), lds_f(mh + kMetaShift + 4 * k)));
           }
           // (by two factors: l may stand 75 binades above 2^m)
           const float m_new = fmaxf(m, __fadd_ru(top, -9.f)), f = exp2f(0.5f * (m - m_new));
@@ -509,7 +576,11 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
           l = l * f * f;
           weights(cur);
           if (__any_sync(0xffffffffu, wide != 0.f || (fabsf(m) > kFarBase && m > kLowest))) {
-            sum = weights_apart(t_h, mh, cq, m, lo_r - at0 - 64 * half, hi_r - at0 - 64 * half, there >> (4 * half));
+            if constexpr (MODE == kPlain)
+              sum = weights_apart(t_h, mh, cq, m, lo_r - at0 - 64 * half, hi_r - at0 - 64 * half, there >> (4 * half));
+            else
+              sum = shaped_weights_apart<MODE>(t_h, mh, cq, m, lo_r - at0 - 64 * half, hi_r - at0 - 64 * half,
+                                               there >> (4 * half), shape, view.ref - (base + at0 + 64 * half), left);
             ptx::tmem_ld16(t_h, pk[0]);
             ptx::tmem_ld16(t_h + 16, pk[1]);
           }
@@ -614,7 +685,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
       }
       if (store) {
         if (part) *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(m, l);
-        else if (a.lse != nullptr) a.lse[orow] = lse_of(m, l);
+        else if (a.lse != nullptr) a.lse[orow] = lse_of(m, l) + (MODE != kPlain ? ref_bias(a, view, hq) : 0.f);
       }
     }
   } else if (warp < C::kMmaWarp) {
@@ -625,10 +696,25 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
     for (int j = 0; j < n_t; ++j) {
       const int s = j & 1;
       const uint32_t par = (j >> 1) & 1;
-      if (!page_wait(BAR(kCbFullVr + s), par, lim, abort, a.status)) break;
-      const int key = base + j * kTileKeys + r;
+      const bool landed = page_wait(BAR(kCbFullVr + s), par, lim, abort, a.status);
+      if (MODE != kPlain ? !__all_sync(0xffffffffu, landed) : !landed) break;
+      const int key = base + tile_at(j) * kTileKeys + r;
       const uint32_t there = lds_u(sm + C::kMeta + (j & (kMetaSlots - 1)) * kMetaBytes + kMetaThere);
-      const bool use = key >= first && key < len && ((there >> (r >> 4)) & 1u);
+      bool use = key >= first && key < len && ((there >> (r >> 4)) & 1u);
+      if (MODE != kPlain) {
+        use = use && key >= key_lo && key < key_hi;
+        // between ranges there may be keys that no row attends to: the keys of
+        // this warp that some row does, a token's run of them a lane
+        if (a.shape.ranges != nullptr) {
+          uint32_t some = 0;
+          for (int i = lane; i <= i_last - i_first; i += 32) {
+            const int from = max(spans[i].x - (key - lane), 0), to = min(spans[i].y - (key - lane), 32);
+            if (from < to) some |= (0xffffffffu << from) & (0xffffffffu >> (32 - to));
+          }
+          some = __reduce_or_sync(0xffffffffu, some);   // (every lane, whatever its own key)
+          use = use && ((some >> lane) & 1u);
+        }
+      }
       uint4 raw[D / 16];
       const uint32_t src = sm + C::kVr + s * C::kKT;
 #pragma unroll
@@ -642,7 +728,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
       // scores of tile j - 1 of the second query tile (NQ = 1: of tile j)
       if (j >= 2) {
         const int after = NQ == 2 ? j - 1 : j;
-        if (!page_wait(BAR(s_bar(1, after)), s_par(after), lim, abort, a.status)) break;
+        const bool free = page_wait(BAR(s_bar(1, after)), s_par(after), lim, abort, a.status);
+        if (MODE != kPlain ? !__all_sync(0xffffffffu, free) : !free) break;
       }
       const uint32_t dst = sm + C::kV + s * C::kVT;
 #pragma unroll
@@ -795,7 +882,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
     // their use (one tile at a time they bound the whole kernel)
     auto look = [&](int j) -> BlockPage {
       BlockPage o{-1, -1000, -1000};
-      const int key = base + j * kTileKeys + 16 * lane;
+      const int key = MODE != kPlain ? base + tile_at(j + (lane >> 3)) * kTileKeys + 16 * (lane & 7)
+                                     : base + j * kTileKeys + 16 * lane;
       // (a page wholly before every row's window may be gone already)
       if (j + (lane >> 3) < n_t && key < key_hi && ((long long)((key >> a.p.shift) + 1) << a.p.shift) > key_lo) {
         o.id = seq_page(a.s, b, key >> a.p.shift, a.p.n_pages, a.status);
@@ -883,7 +971,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
 
 // Joins the key ranges of split row tiles: one warp per query row and head,
 // the ranges in order.
-template <int D>
+template <int D, int MODE>
 __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkArgs p) {
   constexpr int C = D / 32;
   ptx::grid_dependency_wait();
@@ -922,7 +1010,14 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
     const __nv_bfloat162 y = __floats2bfloat162_rn(o[c] * inv, o[c + 1] * inv);
     *reinterpret_cast<uint32_t*>(a.out + row * D + C * lane + c) = *reinterpret_cast<const uint32_t*>(&y);
   }
-  if (lane == 0 && a.lse != nullptr) a.lse[row] = lse_of(top, l);
+  if (lane == 0 && a.lse != nullptr) {
+    float z = lse_of(top, l);
+    if (MODE != kPlain) {
+      const int len = seq_len(a.s, (int)b, a.p.shift, a.status);
+      z += ref_bias(a, row_view(a, (int)b, r0 + i, len - min(n, a.max_q) + i, len), hq);
+    }
+    a.lse[row] = z;
+  }
 }
 
 }  // namespace

@@ -48,6 +48,7 @@
 
 #include "kvq_checks.cuh"
 #include "kvq_pages.cuh"
+#include "kvq_scores.cuh"
 
 namespace kvq {
 namespace {
@@ -89,7 +90,9 @@ struct DecodeArgs {
 struct SeqWork {
   int r0, n, len, lo, units;
   int seen;   // first key some row attends to; lo is this rounded down
+  int end;    // no row attends to a key from here on
 };
+template <int MODE>
 __device__ __forceinline__ SeqWork seq_work(const PagedAttnArgs& a, int b) {
   SeqWork w;
   seq_rows(a.s, b, w.r0, w.n, a.status);
@@ -100,9 +103,22 @@ __device__ __forceinline__ SeqWork seq_work(const PagedAttnArgs& a, int b) {
   w.len = seq_len(a.s, b, a.p.shift, a.status);
   const int t0 = w.len - w.n;
   w.seen = a.window > 0 ? max(0, t0 - a.window + 1) : 0;
+  w.end = w.len;
+  if (MODE != kPlain) {
+    int lo = w.len, hi = 0;
+    for (int i = 0; i < w.n; ++i) {
+      const RowView v = row_view(a, b, w.r0 + i, t0 + i, w.len);
+      if (v.lo < v.hi) {
+        lo = min(lo, v.lo);
+        hi = max(hi, v.hi);
+      }
+    }
+    w.seen = min(lo, hi);
+    w.end = hi;
+  }
   w.lo = w.seen & ~(kUnit - 1);
   // a sequence with rows has one unit at least: it writes their empty result
-  w.units = w.n > 0 ? max(1, (w.len - w.lo + kUnit - 1) / kUnit) : 0;
+  w.units = w.n > 0 ? max(1, (w.end - w.lo + kUnit - 1) / kUnit) : 0;
   return w;
 }
 
@@ -142,11 +158,34 @@ struct Ring {
   uint32_t phase;
 };
 
+// Raw scores of 16 keys capped, in units of the cap.
+template <int NT>
+__device__ __forceinline__ void cap_scores(float (&s)[NT][4], const float (&cq)[NT][2], float fk) {
+  float top = 0.f;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      s[nt][c] *= cq[nt][c & 1] * fk;
+      top = fmaxf(top, fabsf(s[nt][c]));
+    }
+  const bool far = __any_sync(0xffffffffu, top > 1.f);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 4; c += 2) {
+      float x, y;
+      ptx::f2_unpack(tanh_small(ptx::f2_pack(s[nt][c], s[nt][c + 1])), x, y);
+      s[nt][c] = far ? tanh_any(s[nt][c], x) : x;
+      s[nt][c + 1] = far ? tanh_any(s[nt][c + 1], y) : y;
+    }
+}
+
 // One segment: units [i0, i0 + seg) of (b, h), by one warp.  o, m, l: for the
 // rows nt * 8 + 2 t + c (c = 0, 1) the channels CH g .. of sum p v (channel
 // 2 k + i in o[nt][k][c + 2 i]), the base in units of log 2 and sum p.  False
 // when a wait ran out.
-template <int D, int NT, int W>
+template <int D, int NT, int W, int MODE>
 __device__ __forceinline__ bool decode_segment(const PagedAttnArgs& a, const CUtensorMap& map_k,
                                                const CUtensorMap& map_v, Ring& rg, int b, int h,
                                                const SeqWork& w, int i0, int seg,
@@ -156,13 +195,13 @@ __device__ __forceinline__ bool decode_segment(const PagedAttnArgs& a, const CUt
   constexpr int KC = D / 64;       // 16-byte chunks of a key row per lane
   constexpr int MT = D / 16;       // channel tiles of the output
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, heads = a.p.heads;
-  const float scale_log2 = a.scale * 1.4426950408889634f;
+  const float scale_log2 = raw_factor<MODE>(a);   // (of the cap, in a capped mode)
   const uint32_t ring = rg.data, bars = rg.bars;
   int& stage = rg.stage;
   uint32_t& phase = rg.phase;
   const int rows = w.n * a.group;
   const int key_first = w.lo + i0 * kUnit;
-  const int key_end = min(w.len, w.lo + (i0 + seg) * kUnit);
+  const int key_end = min(w.end, w.lo + (i0 + seg) * kUnit);
   const int t0 = w.len - w.n;
   // ---- the query rows' loads, first: their latency runs beside the table's ----
   uint2 raw[NT][KC * 4];
@@ -245,6 +284,9 @@ __device__ __forceinline__ bool decode_segment(const PagedAttnArgs& a, const CUt
   uint32_t qf[NT][KC * 4][2];
   float cq[NT][2];
   int lo_r[NT][2], hi_r[NT][2];   // keys each column's row attends to
+  int ref[NT][2];                 // where its distances are counted from
+  RowShape shape[NT][2];
+  int every_lo = 0, every_hi = 0x7fffffff;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     uint32_t mx = 0;   // largest magnitude, as its bits
@@ -272,13 +314,34 @@ __device__ __forceinline__ bool decode_segment(const PagedAttnArgs& a, const CUt
       cq[nt][c] = scale_log2 * pow2f(ec / 2) * pow2f(ec - ec / 2);
       const int rc = nt * 8 + 2 * t + c;
       const int tq = t0 + rc / a.group;
-      hi_r[nt][c] = rc < rows ? (a.causal ? min(w.len, tq + 1) : w.len) : 0;
-      lo_r[nt][c] = a.window > 0 ? max(0, tq - a.window + 1) : 0;
+      if (MODE == kPlain) {
+        hi_r[nt][c] = rc < rows ? (a.causal ? min(w.len, tq + 1) : w.len) : 0;
+        lo_r[nt][c] = a.window > 0 ? max(0, tq - a.window + 1) : 0;
+      } else {
+        hi_r[nt][c] = lo_r[nt][c] = ref[nt][c] = 0;
+        shape[nt][c] = RowShape{};
+        if (rc < rows) {
+          const RowView v = row_view(a, b, w.r0 + rc / a.group, tq, w.len);
+          hi_r[nt][c] = v.hi;
+          lo_r[nt][c] = v.lo;
+          ref[nt][c] = v.ref;
+          shape[nt][c] = row_shape<MODE>(a, h * a.group + rc % a.group);
+          every_lo = max(every_lo, v.lo);
+          every_hi = min(every_hi, v.hi);
+        }
+      }
+    }
+  }
+  if (MODE != kPlain) {
+#pragma unroll
+    for (int x = 1; x < 4; x <<= 1) {
+      every_lo = max(every_lo, __shfl_xor_sync(0xffffffffu, every_lo, x));
+      every_hi = min(every_hi, __shfl_xor_sync(0xffffffffu, every_hi, x));
     }
   }
   // keys every row attends to
-  const int all_lo = a.window > 0 ? max(0, w.len - a.window) : 0;
-  const int all_hi = a.causal ? min(w.len, t0 + 1) : w.len;
+  const int all_lo = MODE != kPlain ? every_lo : a.window > 0 ? max(0, w.len - a.window) : 0;
+  const int all_hi = MODE != kPlain ? every_hi : a.causal ? min(w.len, t0 + 1) : w.len;
 
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -345,25 +408,35 @@ __device__ __forceinline__ bool decode_segment(const PagedAttnArgs& a, const CUt
     // ---- softmax ----
     // the lane's largest score of a column among each tile's keys
     float xm[2][NT][2];
+    uint32_t some[2][2];   // lanes whose key (of tile, of its half) a row of theirs attends to
     const float ev[2] = {(float)evt[0], (float)evt[1]};
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
       const float fk = pow2f(ekt[mt]);
       const int ka = key0 + 16 * mt + key_row(g);
+      bool mine[2] = {false, false};
+      if (MODE == kCapped) cap_scores<NT>(s[mt], cq, fk);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         xm[mt][nt][0] = xm[mt][nt][1] = -CUDART_INF_F;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          float v = s[mt][nt][c] * (cq[nt][c & 1] * fk);
+          float v = MODE == kCapped ? s[mt][nt][c] * shape[0][0].cap2 : s[mt][nt][c] * (cq[nt][c & 1] * fk);
+          if (MODE != kPlain && shape[0][0].biased)
+            v = fmaf(-shape[nt][c & 1].slope2, (float)abs(ref[nt][c & 1] - (ka + 8 * (c >> 1))), v);
           if (!whole) {
             const int key = ka + 8 * (c >> 1);
             const bool see = key >= lo_r[nt][c & 1] && key < hi_r[nt][c & 1] && idt[mt] >= 0;
             v = see ? v : -CUDART_INF_F;
+            mine[c >> 1] |= see;
           }
           s[mt][nt][c] = v;
           xm[mt][nt][c & 1] = fmaxf(xm[mt][nt][c & 1], v);
         }
+      }
+      if (MODE != kPlain && !whole) {
+        some[mt][0] = __ballot_sync(0xffffffffu, mine[0]);
+        some[mt][1] = __ballot_sync(0xffffffffu, mine[1]);
       }
     }
     // (a score plus ev is looked at through its distance from m, which is
@@ -439,7 +512,10 @@ __device__ __forceinline__ bool decode_segment(const PagedAttnArgs& a, const CUt
           // what no row of the sequence may see must not reach the product
           // (a zero weight times a NaN)
           const int key = key0 + r;
-          const bool use = key >= w.seen && key < w.len && idt[mt] >= 0;
+          bool use = key >= w.seen && key < w.len && idt[mt] >= 0;
+          // (between ranges there may be keys that no row attends to: key_row(g)
+          // is the key of lanes 4 g .. 4 g + 3, which hold all rows)
+          if (MODE != kPlain) use = use && ((some[mt][j >> 1] >> (4 * (2 * t + (j & 1)))) & 15u) != 0u;
 #pragma unroll
           for (int v = 0; v < D / 32; ++v) x[j][v] = use ? x[j][v] : 0u;
         }
@@ -494,10 +570,18 @@ __device__ __forceinline__ bool decode_segment(const PagedAttnArgs& a, const CUt
   return true;
 }
 
+// what a row's distance from its own keys adds to lse
+template <int MODE>
+__device__ __forceinline__ float row_bias(const PagedAttnArgs& a, const SeqWork& w, int b, int h, int r) {
+  if (MODE == kPlain) return 0.f;
+  const int i = r / a.group;
+  return ref_bias(a, row_view(a, b, w.r0 + i, w.len - w.n + i, w.len), h * a.group + r % a.group);
+}
+
 // Row r of the head's rows, from the lane's share (lanes g hold channels
 // CH g .., n = nt, c the row's place): BF16 out and lse.
-template <int D, int NT>
-__device__ __forceinline__ void store_row(const PagedAttnArgs& a, const SeqWork& w, int h, int r,
+template <int D, int NT, int MODE>
+__device__ __forceinline__ void store_row(const PagedAttnArgs& a, const SeqWork& w, int b, int h, int r,
                                           const float (&o)[NT][D / 16][4], int nt, int c, float m, float l) {
   constexpr int CH = D / 8;
   const int g = (threadIdx.x & 31) >> 2;
@@ -513,10 +597,11 @@ __device__ __forceinline__ void store_row(const PagedAttnArgs& a, const SeqWork&
   uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + CH * g);
 #pragma unroll
   for (int k = 0; k < CH / 8; ++k) dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-  if (g == 0 && a.lse != nullptr) a.lse[row] = l == 0.f ? -CUDART_INF_F : 0.6931471805599453f * (m + log2f(l));
+  if (g == 0 && a.lse != nullptr)
+    a.lse[row] = (l == 0.f ? -CUDART_INF_F : 0.6931471805599453f * (m + log2f(l))) + row_bias<MODE>(a, w, b, h, r);
 }
 
-template <int D, int NT, int W>
+template <int D, int NT, int W, int MODE>
 __global__ void __launch_bounds__(W * 32, 1)
     decode_kernel(const __grid_constant__ DecodeArgs p, const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v) {
@@ -546,7 +631,7 @@ __global__ void __launch_bounds__(W * 32, 1)
     const int b = c0 + (int)threadIdx.x;
     long long v = 0;
     if (b < a.s.batch) {
-      const SeqWork x = seq_work(a, b);
+      const SeqWork x = seq_work<MODE>(a, b);
       v = x.units > 0 ? (long long)(x.units + kStartUnits) * heads : 0;
     }
     long long incl = v;
@@ -604,7 +689,7 @@ __global__ void __launch_bounds__(W * 32, 1)
 
   Ring rg{ring, bars, 0, 0u};
   SeqWork w{};
-  if (u0 < u1) w = seq_work(a, b);
+  if (u0 < u1) w = seq_work<MODE>(a, b);
   int h = 0, i0 = 0;
   if (u0 < u1) {
     h = (int)((u0 - at) / (w.units + kStartUnits));
@@ -618,7 +703,7 @@ __global__ void __launch_bounds__(W * 32, 1)
     }
     const int seg = (int)min((long long)(w.units - i0), u1 - u);
     float o[NT][D / 16][4], m[NT][2], l[NT][2];
-    if (!decode_segment<D, NT, W>(a, map_k, map_v, rg, b, h, w, i0, seg, o, m, l)) break;
+    if (!decode_segment<D, NT, W, MODE>(a, map_k, map_v, rg, b, h, w, i0, seg, o, m, l)) break;
     // ---- its result: the item's, or a part of it ----
     const int rows = w.n * a.group;
     const bool complete = seg == w.units;
@@ -630,7 +715,7 @@ __global__ void __launch_bounds__(W * 32, 1)
         const int r = nt * 8 + 2 * t + c;
         if (r >= rows) continue;
         if (complete) {
-          store_row<D, NT>(a, w, h, r, o, nt, c, m[nt][c], l[nt][c]);
+          store_row<D, NT, MODE>(a, w, b, h, r, o, nt, c, m[nt][c], l[nt][c]);
         } else {
           float4* dst = reinterpret_cast<float4*>(p.part_o + (slot * p.rows_cap + r) * D + CH * g);
 #pragma unroll
@@ -647,7 +732,7 @@ __global__ void __launch_bounds__(W * 32, 1)
       h = 0;
       do {
         ++b;
-        w = seq_work(a, b);
+        w = seq_work<MODE>(a, b);
       } while (w.units == 0 && b + 1 < a.s.batch);
       if (w.units == 0) break;   // not with lengths that hold still during the call
     }
@@ -658,7 +743,7 @@ __global__ void __launch_bounds__(W * 32, 1)
 // divided among all their warps, the parts joined in shared memory, then across
 // the cluster's.  No scan of the batch, no workspace, one launch: what counts
 // there is the latency of one pass.
-template <int D, int NT, int W>
+template <int D, int NT, int W, int MODE>
 __global__ void __launch_bounds__(W * 32, 1)
     decode_item_kernel(const __grid_constant__ DecodeArgs p, const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v) {
@@ -683,14 +768,14 @@ __global__ void __launch_bounds__(W * 32, 1)
   // CTAs of a cluster are neighbours in the grid
   const unsigned ctas = (unsigned)p.cluster, rank = blockIdx.x % ctas, item = blockIdx.x / ctas;
   const int b = (int)(item / (unsigned)a.p.heads), h = (int)(item % (unsigned)a.p.heads);
-  const SeqWork w = seq_work(a, b);
+  const SeqWork w = seq_work<MODE>(a, b);
   const int rows = w.n * a.group;
   const long long parts = (long long)ctas * W;
   auto begin = [&](int warp) { return (int)((long long)w.units * ((int)rank * W + warp) / parts); };
   const int i0 = begin(wid), i1 = rows > 0 ? begin(wid + 1) : i0;
   float o[NT][D / 16][4], m[NT][2], l[NT][2];
   bool ok = true;
-  if (i1 > i0) ok = decode_segment<D, NT, W>(a, map_k, map_v, rg, b, h, w, i0, i1 - i0, o, m, l);
+  if (i1 > i0) ok = decode_segment<D, NT, W, MODE>(a, map_k, map_v, rg, b, h, w, i0, i1 - i0, o, m, l);
   // a warp without units, or whose copies did not come, has no part (its
   // weights are zero)
   const bool part_of = i1 > i0 && ok;
@@ -727,7 +812,7 @@ __global__ void __launch_bounds__(W * 32, 1)
       *reinterpret_cast<uint32_t*>(a.out + row * D + (D / 32) * lane + c) = *reinterpret_cast<const uint32_t*>(&z);
     }
     if (lane == 0 && a.lse != nullptr)
-      a.lse[row] = ls == 0.f ? -CUDART_INF_F : 0.6931471805599453f * (top + log2f(ls));
+      a.lse[row] = (ls == 0.f ? -CUDART_INF_F : 0.6931471805599453f * (top + log2f(ls))) + row_bias<MODE>(a, w, b, h, r);
   };
   // a warp per row, the parts in order.  A part is weighed by 2^(m - M) in two
   // equal factors: far below the others in weight, it may still lead the
@@ -786,7 +871,7 @@ __global__ void __launch_bounds__(W * 32, 1)
 // 2^(m - M) (as two factors), the parts in order.  The block's warps take every fourth part, 32
 // lanes hold the channels.
 constexpr int kJoinWarps = 4;
-template <int D>
+template <int D, int MODE>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ DecodeArgs p) {
   constexpr int C = D / 32;
   __shared__ float sum_o[kJoinWarps][D];
@@ -845,8 +930,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     const __nv_bfloat16 z = __float2bfloat16_rn(ls == 0.f ? 0.f : v / ls);
     a.out[row * D + c] = *reinterpret_cast<const uint16_t*>(&z);
   }
-  if (threadIdx.x == 0 && a.lse != nullptr)
-    a.lse[row] = ls == 0.f ? -CUDART_INF_F : 0.6931471805599453f * (top + log2f(ls));
+  if (threadIdx.x == 0 && a.lse != nullptr) {
+    SeqWork w{};
+    w.r0 = r0;
+    w.n = n;
+    if (MODE != kPlain) w.len = seq_len(a.s, b, a.p.shift, a.status);
+    a.lse[row] = (ls == 0.f ? -CUDART_INF_F : 0.6931471805599453f * (top + log2f(ls))) + row_bias<MODE>(a, w, b, h, r);
+  }
 }
 
 }  // namespace

@@ -119,6 +119,10 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream);
 cudaError_t launch_pages_append_rope(const AppendRopeArgs& a, cudaStream_t stream);
 kvq_status launch_paged_attention(const PagedAttnArgs& a, cudaStream_t stream);
 kvq_status launch_paged_attention_scored(const PagedAttnArgs& a, cudaStream_t stream);
+kvq_status launch_paged_biased(const PagedAttnArgs& a, cudaStream_t stream);
+kvq_status launch_paged_capped(const PagedAttnArgs& a, cudaStream_t stream);
+// CTAs per item of the decoding form, 0 for the line of all keys
+int decode_by_item(int sms, int d, long long items, long long keys);
 // bytes, 16 where none are needed
 size_t paged_attention_workspace(int kv_heads, int q_heads, int d, int batch, long long keys, int rows, int max_q);
 cudaError_t launch_pages_copy(const PagePool& p, const int32_t* src, const int32_t* dst, int n,

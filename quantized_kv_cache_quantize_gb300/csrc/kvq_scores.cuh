@@ -1,5 +1,15 @@
-// Device helpers of attention with shaped scores: what a row attends to.
+// Device helpers of attention with shaped scores: what a row attends to, and the
+// shaping itself.
+//
+// Numbers.  A capped score is cap * tanh(x), x the score over the cap.  For |x| <=
+// 1, where scores that a cap is meant for lie, tanh is x times a polynomial in x^2
+// (tanh_fit.py; 2^-22 of it at most with its roundings): eight fused or plain
+// products on pairs, none of them on the special-function unit, which the softmax's
+// exponentials need.  Beyond, 1 - 2 / (1 + 2^(2 x log2 e)): two special functions a
+// score, off by 2^-22.  A distance is a whole number, exact in fp32 up to 2^24.
 #pragma once
+
+#include <math_constants.h>
 
 #include "kvq_pages.cuh"
 
@@ -33,6 +43,108 @@ __device__ __forceinline__ RowView row_view(const PagedAttnArgs& a, int b, int r
 // what the distance |t - ref| takes from lse
 __device__ __forceinline__ float ref_bias(const PagedAttnArgs& a, const RowView& v, int hq) {
   return a.shape.slopes == nullptr || v.t == v.ref ? 0.f : -__ldg(a.shape.slopes + hq) * (float)abs(v.t - v.ref);
+}
+
+constexpr int kPlain = 0, kBiased = 1, kCapped = 2;   // kernels' modes; a capped one may be biased too
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// tanh of a pair, |x| <= 1
+__device__ __forceinline__ uint64_t tanh_small(uint64_t x) {
+  auto both = [](float c) { return ptx::f2_pack(c, c); };
+  const uint64_t z = ptx::f2_mul(x, x);
+  uint64_t p = ptx::f2_fma(z, both(1.038025133e-03f), both(-6.194324698e-03f));
+  p = ptx::f2_fma(p, z, both(2.027970739e-02f));
+  p = ptx::f2_fma(p, z, both(-5.345164612e-02f));
+  p = ptx::f2_fma(p, z, both(1.332507581e-01f));
+  p = ptx::f2_fma(p, z, both(-3.333282769e-01f));
+  p = ptx::f2_fma(p, z, both(9.999999404e-01f));
+  return ptx::f2_mul(p, x);
+}
+// tanh of any number, given tanh_small of it
+__device__ __forceinline__ float tanh_any(float x, float small) {
+  const float far = fmaf(-2.f, rcp_approx(1.f + ptx::ex2_approx(2.885390082f * x)), 1.f);
+  return fabsf(x) <= 1.f ? small : far;
+}
+
+// What shapes the scores of one row, in units of log 2.
+struct RowShape {
+  float cap2;      // cap log2 e
+  float slope2;    // slope log2 e
+  bool biased;     // of the call
+};
+template <int MODE>
+__device__ __forceinline__ RowShape row_shape(const PagedAttnArgs& a, int hq) {
+  RowShape r;
+  r.cap2 = MODE == kCapped ? a.shape.cap * 1.4426950408889634f : 0.f;
+  r.biased = a.shape.slopes != nullptr;
+  r.slope2 = r.biased ? __ldg(a.shape.slopes + hq) * 1.4426950408889634f : 0.f;
+  return r;
+}
+// the factor of a raw score: to units of log 2, or of the cap
+template <int MODE>
+__device__ __forceinline__ float raw_factor(const PagedAttnArgs& a) {
+  return MODE == kCapped ? a.scale / a.shape.cap : a.scale * 1.4426950408889634f;
+}
+
+// 16 raw scores of neighbouring keys, key 0 `dist` before the row's reference
+// place, shaped in place: what is left is a factor (shape_factor) to units of
+// log 2.  ck: raw_factor with the scales of row and page.  `left`: no key of any
+// lane's lies behind its row's reference place.
+template <int MODE>
+__device__ __forceinline__ float shape_factor(const RowShape& r, float ck) {
+  return r.biased ? 1.f : MODE == kCapped ? r.cap2 : ck;
+}
+template <int MODE>
+__device__ __forceinline__ void shape_block(uint32_t* s, float ck, const RowShape& r, int dist, bool left) {
+  if (MODE != kCapped && !r.biased) return;
+  if (MODE == kCapped) {
+    const uint64_t c2 = ptx::f2_pack(ck, ck);
+    float top = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float x, y;
+      ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), c2), x, y);
+      s[2 * k] = __float_as_uint(x);
+      s[2 * k + 1] = __float_as_uint(y);
+      top = ptx::max3(top, fabsf(x), fabsf(y));
+    }
+    const bool far = __any_sync(0xffffffffu, top > 1.f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float x0 = __uint_as_float(s[2 * k]), y0 = __uint_as_float(s[2 * k + 1]);
+      float x, y;
+      ptx::f2_unpack(tanh_small(ptx::f2_pack(x0, y0)), x, y);
+      if (far) {
+        x = tanh_any(x0, x);
+        y = tanh_any(y0, y);
+      }
+      s[2 * k] = __float_as_uint(x);
+      s[2 * k + 1] = __float_as_uint(y);
+    }
+  }
+  if (!r.biased) return;
+  const float f = MODE == kCapped ? r.cap2 : ck, d0 = (float)dist;
+  if (left) {
+    const uint64_t f2 = ptx::f2_pack(f, f), slope2 = ptx::f2_pack(r.slope2, r.slope2);
+    const float b = -r.slope2 * d0;
+    const uint64_t b2 = ptx::f2_pack(b, b);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float x, y;
+      const uint64_t bias = ptx::f2_fma(ptx::f2_pack((float)(2 * k), (float)(2 * k + 1)), slope2, b2);
+      ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), f2, bias), x, y);
+      s[2 * k] = __float_as_uint(x);
+      s[2 * k + 1] = __float_as_uint(y);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      s[k] = __float_as_uint(fmaf(-r.slope2, fabsf(d0 - (float)k), __uint_as_float(s[k]) * f));
+  }
 }
 
 }  // namespace
