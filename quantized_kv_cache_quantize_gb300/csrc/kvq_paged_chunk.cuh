@@ -233,6 +233,21 @@ __device__ __noinline__ float weights_apart(uint32_t t_h, uint32_t mh, float cq,
   return sum;
 }
 
+// 64 raw scores capped, `most` their largest magnitude.  One vote for all of them,
+// so that the pairs' chains run side by side.
+__device__ __forceinline__ void cap_scores64(uint32_t (&s)[64], uint32_t mh, float cq, float most) {
+  float ck[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) ck[k] = cq * lds_f(mh + 4 * k);
+  if (__any_sync(0xffffffffu, most * fmaxf(fmaxf(ck[0], ck[1]), fmaxf(ck[2], ck[3])) > 1.f)) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) cap_block(s + 16 * k, ck[k], true);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) cap_block(s + 16 * k, ck[k], false);
+  }
+}
+
 // the same for shaped scores
 template <int MODE>
 __device__ __noinline__ float shaped_weights_apart(uint32_t t_h, uint32_t mh, float cq, float m, int lo, int hi,
@@ -245,7 +260,9 @@ __device__ __noinline__ float shaped_weights_apart(uint32_t t_h, uint32_t mh, fl
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float raw = cq * lds_f(mh + 4 * (k + i)), ev = lds_f(mh + kMetaShift + 4 * (k + i));
-      shape_block<MODE>(v + 16 * i, raw, shape, dist - 16 * (k + i), left);
+      if (MODE == kCapped) cap_block(v + 16 * i, raw, true);
+      if (shape.biased)
+        bias_block(v + 16 * i, MODE == kCapped ? shape.cap2 : raw, shape, dist - 16 * (k + i), left);
       const float ck = fmaxf(shape_factor<MODE>(shape, raw), 1.2e-38f);
       mask_block(v + 16 * i, (there >> (k + i)) & 1u ? lo - 16 * (k + i) : 16, hi - 16 * (k + i));
 #pragma unroll
@@ -526,11 +543,18 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
           return MODE != kPlain ? fmaxf(shape_factor<MODE>(shape, cq * lds_f(ek_at)), 1.2e-38f) : fmaxf(cq * lds_f(ek_at), 1.2e-38f);
         };
         auto scores = [&](uint32_t (&cur)[64]) {
-          ptx::tmem_ld64(t_h, cur);
-          if (MODE != kPlain) {
+          if constexpr (MODE == kCapped) {
+            float most;
+            ptx::tmem_ld64_max(t_h, cur, most);
+            cap_scores64(cur, mh, cq, most);
+          } else {
+            ptx::tmem_ld64(t_h, cur);
+          }
+          if (MODE != kPlain && shape.biased) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              shape_block<MODE>(cur + 16 * k, cq * lds_f(mh + 4 * k), shape, view.ref - (base + at0 + 64 * half + 16 * k), left);
+              bias_block(cur + 16 * k, MODE == kCapped ? shape.cap2 : cq * lds_f(mh + 4 * k), shape,
+                         view.ref - (base + at0 + 64 * half + 16 * k), left);
           }
           if (!whole) {
 #pragma unroll

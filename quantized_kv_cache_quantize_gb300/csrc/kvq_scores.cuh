@@ -90,44 +90,34 @@ __device__ __forceinline__ float raw_factor(const PagedAttnArgs& a) {
   return MODE == kCapped ? a.scale / a.shape.cap : a.scale * 1.4426950408889634f;
 }
 
-// 16 raw scores of neighbouring keys, key 0 `dist` before the row's reference
-// place, shaped in place: what is left is a factor (shape_factor) to units of
-// log 2.  ck: raw_factor with the scales of row and page.  `left`: no key of any
-// lane's lies behind its row's reference place.
+// What is left to do to a shaped score: a factor to units of log 2.
 template <int MODE>
 __device__ __forceinline__ float shape_factor(const RowShape& r, float ck) {
   return r.biased ? 1.f : MODE == kCapped ? r.cap2 : ck;
 }
-template <int MODE>
-__device__ __forceinline__ void shape_block(uint32_t* s, float ck, const RowShape& r, int dist, bool left) {
-  if (MODE != kCapped && !r.biased) return;
-  if (MODE == kCapped) {
-    const uint64_t c2 = ptx::f2_pack(ck, ck);
-    float top = 0.f;
+// tanh of 16 raw scores times ck, in place; `far`: some may lie beyond 1
+__device__ __forceinline__ void cap_block(uint32_t* s, float ck, bool far) {
+  const uint64_t c2 = ptx::f2_pack(ck, ck);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      float x, y;
-      ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), c2), x, y);
-      s[2 * k] = __float_as_uint(x);
-      s[2 * k + 1] = __float_as_uint(y);
-      top = ptx::max3(top, fabsf(x), fabsf(y));
+  for (int k = 0; k < 8; ++k) {
+    const uint64_t x2 = ptx::f2_mul(ptx::f2_pack(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), c2);
+    float x, y;
+    ptx::f2_unpack(tanh_small(x2), x, y);
+    if (far) {
+      float x0, y0;
+      ptx::f2_unpack(x2, x0, y0);
+      x = tanh_any(x0, x);
+      y = tanh_any(y0, y);
     }
-    const bool far = __any_sync(0xffffffffu, top > 1.f);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float x0 = __uint_as_float(s[2 * k]), y0 = __uint_as_float(s[2 * k + 1]);
-      float x, y;
-      ptx::f2_unpack(tanh_small(ptx::f2_pack(x0, y0)), x, y);
-      if (far) {
-        x = tanh_any(x0, x);
-        y = tanh_any(y0, y);
-      }
-      s[2 * k] = __float_as_uint(x);
-      s[2 * k + 1] = __float_as_uint(y);
-    }
+    s[2 * k] = __float_as_uint(x);
+    s[2 * k + 1] = __float_as_uint(y);
   }
-  if (!r.biased) return;
-  const float f = MODE == kCapped ? r.cap2 : ck, d0 = (float)dist;
+}
+// The bias of 16 neighbouring keys, key 0 `dist` before the row's reference
+// place, added to their scores times f.  `left`: no key of any lane's lies
+// behind its row's reference place.
+__device__ __forceinline__ void bias_block(uint32_t* s, float f, const RowShape& r, int dist, bool left) {
+  const float d0 = (float)dist;
   if (left) {
     const uint64_t f2 = ptx::f2_pack(f, f), slope2 = ptx::f2_pack(r.slope2, r.slope2);
     const float b = -r.slope2 * d0;
