@@ -192,6 +192,22 @@ __device__ __forceinline__ void exp_block(const uint32_t* s, float scale, float 
   ptx::f2_unpack(acc, x, y);
   sum = x + y;
 }
+// the same of 16 raw scores that stay below 0.4 of their cap
+__device__ __forceinline__ void exp_low_block(const uint32_t* s, const LowCap& c, float shift, uint32_t* pk, float& sum) {
+  const uint64_t b2 = ptx::f2_pack(shift, shift);
+  uint64_t acc = ptx::f2_pack(0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    float x0, x1;
+    ptx::f2_unpack(low_scores(ptx::f2_pack(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), c, b2), x0, x1);
+    const float e0 = ptx::ex2_approx(x0), e1 = ptx::ex2_approx(x1);
+    acc = ptx::f2_add(acc, ptx::f2_pack(e0, e1));
+    pk[k] = ptx::f16x2_rn(e0, e1);
+  }
+  float x, y;
+  ptx::f2_unpack(acc, x, y);
+  sum = x + y;
+}
 // scores of columns outside [lo, hi) become -inf
 __device__ __forceinline__ void mask_block(uint32_t* s, int lo, int hi) {
 #pragma unroll
@@ -233,22 +249,27 @@ __device__ __noinline__ float weights_apart(uint32_t t_h, uint32_t mh, float cq,
   return sum;
 }
 
-// 64 raw scores capped, `most` their largest magnitude.  One vote for all of them,
-// so that the pairs' chains run side by side.
-__device__ __forceinline__ void cap_scores64(uint32_t (&s)[64], uint32_t mh, float cq, float most) {
-  float ck[4];
+// The largest of 64 shaped scores with their V exponents.
+template <int MODE>
+__device__ __noinline__ float shaped_top(uint32_t t_h, uint32_t mh, float cq, int lo, int hi, uint32_t there, RowShape shape,
+                                         int dist, bool left) {
+  float top = kLowest;
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k) {
+    uint32_t v[16];
+    ptx::tmem_ld16(t_h + 16 * k, v);
+    const float raw = cq * lds_f(mh + 4 * k), ev = lds_f(mh + kMetaShift + 4 * k);
+    if (MODE == kCapped) cap_block(v, raw, true);
+    if (shape.biased) bias_block(v, MODE == kCapped ? shape.cap2 : raw, shape, dist - 16 * k, left);
+    mask_block(v, (there >> k) & 1u ? lo - 16 * k : 16, hi - 16 * k);
+    float most = -CUDART_INF_F;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) ck[k] = cq * lds_f(mh + 4 * k);
-  if (__any_sync(0xffffffffu, most * fmaxf(fmaxf(ck[0], ck[1]), fmaxf(ck[2], ck[3])) > 1.f)) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) cap_block(s + 16 * k, ck[k], true);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) cap_block(s + 16 * k, ck[k], false);
+    for (int i = 0; i < 16; ++i) most = fmaxf(most, __uint_as_float(v[i]));
+    top = fmaxf(top, with_ev(most, fmaxf(shape_factor<MODE>(shape, raw), 1.2e-38f), ev));
   }
+  return top;
 }
-
-// the same for shaped scores
+// weights_apart for shaped scores, whatever their base
 template <int MODE>
 __device__ __noinline__ float shaped_weights_apart(uint32_t t_h, uint32_t mh, float cq, float m, int lo, int hi,
                                                    uint32_t there, RowShape shape, int dist, bool left) {
@@ -542,26 +563,20 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
         auto factor = [&](uint32_t ek_at) {
           return MODE != kPlain ? fmaxf(shape_factor<MODE>(shape, cq * lds_f(ek_at)), 1.2e-38f) : fmaxf(cq * lds_f(ek_at), 1.2e-38f);
         };
+        const int at_h = at0 + 64 * half;
+        // (a block whose page is not there begins behind its end)
+        auto from = [&](int k) { return (there >> (4 * half + k)) & 1u ? lo_r - (at_h + 16 * k) : 16; };
         auto scores = [&](uint32_t (&cur)[64]) {
-          if constexpr (MODE == kCapped) {
-            float most;
-            ptx::tmem_ld64_max(t_h, cur, most);
-            cap_scores64(cur, mh, cq, most);
-          } else {
-            ptx::tmem_ld64(t_h, cur);
-          }
+          if (MODE != kCapped) ptx::tmem_ld64(t_h, cur);
           if (MODE != kPlain && shape.biased) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               bias_block(cur + 16 * k, MODE == kCapped ? shape.cap2 : cq * lds_f(mh + 4 * k), shape,
-                         view.ref - (base + at0 + 64 * half + 16 * k), left);
+                         view.ref - (base + at_h + 16 * k), left);
           }
           if (!whole) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int at = at0 + 64 * half + 16 * k;
-              mask_block(cur + 16 * k, (there >> (4 * half + k)) & 1u ? lo_r - at : 16, hi_r - at);
-            }
+            for (int k = 0; k < 4; ++k) mask_block(cur + 16 * k, from(k), hi_r - (at_h + 16 * k));
           }
         };
         auto weights = [&](const uint32_t (&cur)[64]) {
@@ -576,7 +591,37 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
             sum = fmaf(b, lds_f(mh + kMetaInv + 4 * k), sum);
           }
         };
-        {
+        if constexpr (MODE == kCapped) {
+          uint32_t cur[64];
+          float most, ck[4];
+          ptx::tmem_ld64_max(t_h, cur, most);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) ck[k] = cq * lds_f(mh + 4 * k);
+          const float ck_most = fmaxf(fmaxf(ck[0], ck[1]), fmaxf(ck[2], ck[3])), x_most = most * ck_most;
+          const bool low = x_most <= kLowX && ck_most <= kLowMost && ck[0] == ck[1] && ck[0] == ck[2] && ck[0] == ck[3];
+          if (__all_sync(0xffffffffu, low) && whole && !shape.biased) {
+            hat = wide;
+            sum = 0.f;
+            const LowCap lc = low_cap(ck[0], shape.cap2);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float b;
+              exp_low_block(cur + 16 * k, lc, lds_f(mh + kMetaShift + 4 * k) - m, pk[k >> 1] + 8 * (k & 1), b);
+              hat += b;
+              sum = fmaf(b, lds_f(mh + kMetaInv + 4 * k), sum);
+            }
+          } else {
+            if (__any_sync(0xffffffffu, x_most > 1.f)) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) cap_block(cur + 16 * k, ck[k], true);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) cap_block(cur + 16 * k, ck[k], false);
+            }
+            scores(cur);
+            weights(cur);
+          }
+        } else {
           uint32_t cur[64];
           scores(cur);
           weights(cur);
@@ -584,27 +629,35 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
         // past FP16 (or the first weights of all, against the lowest base): a
         // new base, and what there is so far follows it
         if (__builtin_expect(__any_sync(0xffffffffu, hat > 32768.0f), 0)) {
-          uint32_t cur[64];
-          scores(cur);
-          float top = kLowest;
+          float top = kLowest, f;
+          auto rise = [&]() {   // (by two factors: l may stand 75 binades above 2^m)
+            const float m_new = fmaxf(m, __fadd_ru(top, -9.f));
+            f = exp2f(0.5f * (m - m_new));
+            m = m_new;
+            l = l * f * f;
+          };
+          if constexpr (MODE == kPlain) {
+            uint32_t cur[64];
+            scores(cur);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float most = -CUDART_INF_F;
+            for (int k = 0; k < 4; ++k) {
+              float most = -CUDART_INF_F;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) most = fmaxf(most, __uint_as_float(cur[16 * k + i]));
-            top = fmaxf(top, with_ev(most, factor(mh + 4 * k), lds_f(mh + kMetaShift + 4 * k)));
-          }
-          // (by two factors: l may stand 75 binades above 2^m)
-          const float m_new = fmaxf(m, __fadd_ru(top, -9.f)), f = exp2f(0.5f * (m - m_new));
-          m = m_new;
-          l = l * f * f;
-          weights(cur);
-          if (__any_sync(0xffffffffu, wide != 0.f || (fabsf(m) > kFarBase && m > kLowest))) {
-            if constexpr (MODE == kPlain)
-              sum = weights_apart(t_h, mh, cq, m, lo_r - at0 - 64 * half, hi_r - at0 - 64 * half, there >> (4 * half));
-            else
-              sum = shaped_weights_apart<MODE>(t_h, mh, cq, m, lo_r - at0 - 64 * half, hi_r - at0 - 64 * half,
-                                               there >> (4 * half), shape, view.ref - (base + at0 + 64 * half), left);
+              for (int i = 0; i < 16; ++i) most = fmaxf(most, __uint_as_float(cur[16 * k + i]));
+              top = fmaxf(top, with_ev(most, factor(mh + 4 * k), lds_f(mh + kMetaShift + 4 * k)));
+            }
+            rise();
+            weights(cur);
+            if (__any_sync(0xffffffffu, wide != 0.f || (fabsf(m) > kFarBase && m > kLowest))) {
+              sum = weights_apart(t_h, mh, cq, m, lo_r - at_h, hi_r - at_h, there >> (4 * half));
+              ptx::tmem_ld16(t_h, pk[0]);
+              ptx::tmem_ld16(t_h + 16, pk[1]);
+            }
+          } else {
+            const int lo_h = lo_r - at_h, hi_h = hi_r - at_h, dist = view.ref - (base + at_h);
+            top = shaped_top<MODE>(t_h, mh, cq, lo_h, hi_h, there >> (4 * half), shape, dist, left);
+            rise();
+            sum = shaped_weights_apart<MODE>(t_h, mh, cq, m, lo_h, hi_h, there >> (4 * half), shape, dist, left);
             ptx::tmem_ld16(t_h, pk[0]);
             ptx::tmem_ld16(t_h + 16, pk[1]);
           }

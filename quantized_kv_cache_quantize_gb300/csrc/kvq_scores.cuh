@@ -3,10 +3,10 @@
 //
 // Numbers.  A capped score is cap * tanh(x), x the score over the cap.  For |x| <=
 // 1, where scores that a cap is meant for lie, tanh is x times a polynomial in x^2
-// (tanh_fit.py; 2^-22 of it at most with its roundings): eight fused or plain
-// products on pairs, none of them on the special-function unit, which the softmax's
-// exponentials need.  Beyond, 1 - 2 / (1 + 2^(2 x log2 e)): two special functions a
-// score, off by 2^-22.  A distance is a whole number, exact in fp32 up to 2^24.
+// (tanh_fit.py), 2^-22 of it at most with its roundings: products on pairs, none of
+// them on the special-function unit, which the softmax's exponentials need.  Beyond,
+// 1 - 2 / (1 + 2^(2 x log2 e)): two special functions a score, off by 2^-22.  A
+// distance is a whole number, exact in fp32 up to 2^24.
 #pragma once
 
 #include <math_constants.h>
@@ -88,6 +88,29 @@ __device__ __forceinline__ RowShape row_shape(const PagedAttnArgs& a, int hq) {
 template <int MODE>
 __device__ __forceinline__ float raw_factor(const PagedAttnArgs& a) {
   return MODE == kCapped ? a.scale / a.shape.cap : a.scale * 1.4426950408889634f;
+}
+
+// Up to 0.4 of the cap four terms do, and fold: with the row's and page's factor
+// ck in the coefficients, the shaped score in units of log 2 is s (c0 + c1 s^2 +
+// c2 s^4 + c3 s^6) of the raw score s, its last product the one that also adds
+// what stands in the exponent beside it.  Three products on pairs more than a
+// plain score (4680 rows, 24 heads, 23400 keys).  ck is held below kLowMost so
+// that ck^7 stays in fp32; larger ones take the way of larger scores.
+constexpr float kLowX = 0.4f, kLowMost = 16384.f;
+struct LowCap {
+  float c0, c1, c2, c3;
+};
+__device__ __forceinline__ LowCap low_cap(float ck, float cap2) {
+  const float k2 = ck * ck, k0 = cap2 * ck, k4 = k0 * k2, k6 = k4 * k2;
+  return LowCap{9.999998808e-01f * k0, -3.333135545e-01f * k4, 1.327087432e-01f * k6, -4.754934832e-02f * (k6 * k2)};
+}
+__device__ __forceinline__ uint64_t low_scores(uint64_t s, const LowCap& c, uint64_t beside) {
+  auto both = [](float x) { return ptx::f2_pack(x, x); };
+  const uint64_t z = ptx::f2_mul(s, s);
+  uint64_t p = ptx::f2_fma(both(c.c3), z, both(c.c2));
+  p = ptx::f2_fma(p, z, both(c.c1));
+  p = ptx::f2_fma(p, z, both(c.c0));
+  return ptx::f2_fma(p, s, beside);
 }
 
 // What is left to do to a shaped score: a factor to units of log 2.
