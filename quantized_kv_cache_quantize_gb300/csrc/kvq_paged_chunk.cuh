@@ -208,6 +208,48 @@ __device__ __forceinline__ void exp_low_block(const uint32_t* s, const LowCap& c
   ptx::f2_unpack(acc, x, y);
   sum = x + y;
 }
+// the same of any 16 raw scores under a short cap; ck: their factor; masked: those
+// outside [lo, hi) left out
+template <bool MASKED>
+__device__ __forceinline__ void exp_far_block(const uint32_t* s, float ck, float cap2, float shift, int lo, int hi,
+                                              uint32_t* pk, float& sum) {
+  const float ct = 2.885390082f * ck;
+  const uint64_t f2 = ptx::f2_pack(-2.f * cap2, -2.f * cap2), b2 = ptx::f2_pack(cap2 + shift, cap2 + shift);
+  uint64_t acc = ptx::f2_pack(0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    float x0, x1;
+    ptx::f2_unpack(far_scores(ptx::f2_pack(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), ct, f2, b2), x0, x1);
+    if (MASKED) {
+      x0 = 2 * k >= lo && 2 * k < hi ? x0 : -CUDART_INF_F;
+      x1 = 2 * k + 1 >= lo && 2 * k + 1 < hi ? x1 : -CUDART_INF_F;
+    }
+    const float e0 = ptx::ex2_approx(x0), e1 = ptx::ex2_approx(x1);
+    acc = ptx::f2_add(acc, ptx::f2_pack(e0, e1));
+    pk[k] = ptx::f16x2_rn(e0, e1);
+  }
+  float x, y;
+  ptx::f2_unpack(acc, x, y);
+  sum = x + y;
+}
+// the same of 16 raw scores with a bias that runs straight along them: `beside` at
+// key 0, `step` more with each key
+__device__ __forceinline__ void exp_bias_block(const uint32_t* s, float ck, float beside, float step, uint32_t* pk, float& sum) {
+  const uint64_t c2 = ptx::f2_pack(ck, ck), b2 = ptx::f2_pack(beside, beside), d2 = ptx::f2_pack(step, step);
+  uint64_t acc = ptx::f2_pack(0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    float x0, x1;
+    const uint64_t b = ptx::f2_fma(ptx::f2_pack((float)(2 * k), (float)(2 * k + 1)), d2, b2);
+    ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), c2, b), x0, x1);
+    const float e0 = ptx::ex2_approx(x0), e1 = ptx::ex2_approx(x1);
+    acc = ptx::f2_add(acc, ptx::f2_pack(e0, e1));
+    pk[k] = ptx::f16x2_rn(e0, e1);
+  }
+  float x, y;
+  ptx::f2_unpack(acc, x, y);
+  sum = x + y;
+}
 // scores of columns outside [lo, hi) become -inf
 __device__ __forceinline__ void mask_block(uint32_t* s, int lo, int hi) {
 #pragma unroll
@@ -249,52 +291,93 @@ __device__ __noinline__ float weights_apart(uint32_t t_h, uint32_t mh, float cq,
   return sum;
 }
 
-// The largest of 64 shaped scores with their V exponents.
+// Shaped scores, 64 of a row, by loops over blocks of 16 in tensor memory: the way
+// of every half tile that is not plain work, out of line and short, so that it
+// takes little room among the instructions of those that are.
+struct HalfRow {
+  uint32_t t_h, mh, there;   // scores, scales, blocks whose page is there
+  int lo, hi, dist;          // keys seen, place of the reference, from key 0
+  float cq;
+  RowShape shape;
+};
 template <int MODE>
-__device__ __noinline__ float shaped_top(uint32_t t_h, uint32_t mh, float cq, int lo, int hi, uint32_t there, RowShape shape,
-                                         int dist, bool left) {
+__device__ __forceinline__ void shape_block(uint32_t* v, float raw, const HalfRow& h, int k) {
+  if (MODE == kCapped) cap_block(v, raw, true);
+  if (h.shape.biased) bias_block(v, MODE == kCapped ? h.shape.cap2 : raw, h.shape, h.dist - 16 * k, false);
+}
+// The largest of them with their V exponents.  A cap alone keeps the order of raw
+// scores: the largest of a block is shaped, no other.
+template <int MODE, bool MASKED>
+__device__ __noinline__ float shaped_top(HalfRow h) {
   float top = kLowest;
 #pragma unroll 1
   for (int k = 0; k < 4; ++k) {
-    uint32_t v[16];
-    ptx::tmem_ld16(t_h + 16 * k, v);
-    const float raw = cq * lds_f(mh + 4 * k), ev = lds_f(mh + kMetaShift + 4 * k);
-    if (MODE == kCapped) cap_block(v, raw, true);
-    if (shape.biased) bias_block(v, MODE == kCapped ? shape.cap2 : raw, shape, dist - 16 * k, left);
-    mask_block(v, (there >> k) & 1u ? lo - 16 * k : 16, hi - 16 * k);
+    const float raw = h.cq * lds_f(h.mh + 4 * k), ev = lds_f(h.mh + kMetaShift + 4 * k);
     float most = -CUDART_INF_F;
+    if (!MASKED && !h.shape.biased) {
+      most = ptx::tmem_max16(h.t_h + 16 * k);
+    } else {
+      uint32_t v[16];
+      ptx::tmem_ld16(h.t_h + 16 * k, v);
+      if (h.shape.biased) shape_block<MODE>(v, raw, h, k);
+      if (MASKED) mask_block(v, (h.there >> k) & 1u ? h.lo - 16 * k : 16, h.hi - 16 * k);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) most = fmaxf(most, __uint_as_float(v[i]));
-    top = fmaxf(top, with_ev(most, fmaxf(shape_factor<MODE>(shape, raw), 1.2e-38f), ev));
+      for (int i = 0; i < 16; i += 2) most = ptx::max3(most, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+    }
+    if (MODE == kCapped && !h.shape.biased && most > -CUDART_INF_F) {
+      const float x = raw * most;
+      float s0, s1;
+      ptx::f2_unpack(tanh_small(ptx::f2_pack(x, x)), s0, s1);
+      most = tanh_any(x, s0);
+    }
+    top = fmaxf(top, with_ev(most, fmaxf(shape_factor<MODE>(h.shape, raw), 1.2e-38f), ev));
   }
   return top;
 }
-// weights_apart for shaped scores, whatever their base
-template <int MODE>
-__device__ __noinline__ float shaped_weights_apart(uint32_t t_h, uint32_t mh, float cq, float m, int lo, int hi,
-                                                   uint32_t there, RowShape shape, int dist, bool left) {
+// Their weights against base m, in FP16 over the scores, and the sum.
+template <int MODE, bool MASKED>
+__device__ __noinline__ float shaped_weights(HalfRow h, float m) {
+  const bool far = MODE == kCapped && !h.shape.biased && h.shape.cap2 <= kShortCap * 1.4426950408889634f;
   float sum = 0.f;
 #pragma unroll 1
-  for (int k = 0; k < 4; k += 2) {
-    uint32_t v[32], w[16];
-    ptx::tmem_ld32(t_h + 16 * k, v);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float raw = cq * lds_f(mh + 4 * (k + i)), ev = lds_f(mh + kMetaShift + 4 * (k + i));
-      if (MODE == kCapped) cap_block(v + 16 * i, raw, true);
-      if (shape.biased)
-        bias_block(v + 16 * i, MODE == kCapped ? shape.cap2 : raw, shape, dist - 16 * (k + i), left);
-      const float ck = fmaxf(shape_factor<MODE>(shape, raw), 1.2e-38f);
-      mask_block(v + 16 * i, (there >> (k + i)) & 1u ? lo - 16 * (k + i) : 16, hi - 16 * (k + i));
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const float x0 = with_ev(__uint_as_float(v[16 * i + 2 * c]), ck, ev) - m;
-        const float x1 = with_ev(__uint_as_float(v[16 * i + 2 * c + 1]), ck, ev) - m;
-        w[8 * i + c] = ptx::f16x2_rn(ptx::ex2_approx(x0), ptx::ex2_approx(x1));
-        sum += ptx::ex2_approx(x0 - ev) + ptx::ex2_approx(x1 - ev);
-      }
+  for (int k = 0; k < 4; ++k) {
+    uint32_t v[16], w[8];
+    ptx::tmem_ld16(h.t_h + 16 * k, v);
+    const float raw = h.cq * lds_f(h.mh + 4 * k), shift = lds_f(h.mh + kMetaShift + 4 * k) - m;
+    const int lo = (h.there >> k) & 1u ? h.lo - 16 * k : 16, hi = h.hi - 16 * k;
+    float b;
+    if (far) {
+      exp_far_block<MASKED>(v, raw, h.shape.cap2, shift, lo, hi, w, b);
+    } else {
+      shape_block<MODE>(v, raw, h, k);
+      if (MASKED) mask_block(v, lo, hi);
+      exp_block(v, fmaxf(shape_factor<MODE>(h.shape, raw), 1.2e-38f), shift, w, b);
     }
-    ptx::tmem_st16(t_h + 8 * k, w);   // (columns that the loads are past)
+    sum = fmaf(b, lds_f(h.mh + kMetaInv + 4 * k), sum);
+    ptx::tmem_st8(h.t_h + 8 * k, w);   // (columns that the loads are past)
+  }
+  ptx::tmem_st_wait();
+  return sum;
+}
+// The same by with_ev's distances, the sum from exponents without V's.
+template <int MODE>
+__device__ __noinline__ float shaped_weights_apart(HalfRow h, float m) {
+  float sum = 0.f;
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k) {
+    uint32_t v[16], w[8];
+    ptx::tmem_ld16(h.t_h + 16 * k, v);
+    const float raw = h.cq * lds_f(h.mh + 4 * k), ev = lds_f(h.mh + kMetaShift + 4 * k);
+    shape_block<MODE>(v, raw, h, k);
+    const float ck = fmaxf(shape_factor<MODE>(h.shape, raw), 1.2e-38f);
+    mask_block(v, (h.there >> k) & 1u ? h.lo - 16 * k : 16, h.hi - 16 * k);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const float x0 = with_ev(__uint_as_float(v[2 * c]), ck, ev) - m, x1 = with_ev(__uint_as_float(v[2 * c + 1]), ck, ev) - m;
+      w[c] = ptx::f16x2_rn(ptx::ex2_approx(x0), ptx::ex2_approx(x1));
+      sum += ptx::ex2_approx(x0 - ev) + ptx::ex2_approx(x1 - ev);
+    }
+    ptx::tmem_st8(h.t_h + 8 * k, w);
   }
   ptx::tmem_st_wait();
   return sum;
@@ -532,6 +615,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
       const uint32_t there = lds_u(mt + kMetaThere);
       const int at0 = tile_at(j) * kTileKeys;
       const bool left = MODE != kPlain && __all_sync(0xffffffffu, base + at0 + kTileKeys <= view.ref + 1);
+      const bool right = MODE != kPlain && __all_sync(0xffffffffu, base + at0 >= view.ref);
       const bool whole = __all_sync(0xffffffffu, there == 255u && lo_r <= at0 && hi_r >= at0 + kTileKeys);
       auto rescale_o = [&](float f) {
         const uint64_t f2 = ptx::f2_pack(f, f);
@@ -549,6 +633,25 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
           ptx::tmem_st16(t_o + 16 * c, v);
         }
       };
+      // a new base under the largest score and V exponent; what there is so far
+      // follows it
+      auto rise = [&](float top) {   // (by two factors: l may stand 75 binades above 2^m)
+        const float m_new = fmaxf(m, __fadd_ru(top, -9.f)), f = exp2f(0.5f * (m - m_new));
+        m = m_new;
+        l = l * f * f;
+        return f;
+      };
+      auto follow = [&](int half, float f) {
+        if (!__any_sync(0xffffffffu, f != 1.f)) return;
+        // (the product of the first half is still under way; the group's
+        // previous tile's was done before these scores were)
+        if (half == 1) {
+          if (lane == 0) st_release(ask0 + 4 * q, (uint32_t)j + 1u);
+          ok = __all_sync(0xffffffffu, ok && wait_word(told0 + 4 * q, (uint32_t)j + 1u, lim, abort, a.status));
+        }
+        ptx::tc_fence_after();
+        if (!first || half == 1) rescale_o(f * f);
+      };
       // ---- weights, 64 keys at a time.  Those of keys 0-63 are handed over
       // as soon as they are there, so that their product runs beside the
       // rest.  The loop stays a loop: a body that fits the instruction
@@ -559,86 +662,42 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
         uint32_t pk[2][16];
         float hat, sum;
         const float wide = lds_f(mt + kMetaWide);
-        // (a scale that underflows must not meet the -inf of a masked score)
-        auto factor = [&](uint32_t ek_at) {
-          return MODE != kPlain ? fmaxf(shape_factor<MODE>(shape, cq * lds_f(ek_at)), 1.2e-38f) : fmaxf(cq * lds_f(ek_at), 1.2e-38f);
-        };
-        const int at_h = at0 + 64 * half;
-        // (a block whose page is not there begins behind its end)
-        auto from = [&](int k) { return (there >> (4 * half + k)) & 1u ? lo_r - (at_h + 16 * k) : 16; };
-        auto scores = [&](uint32_t (&cur)[64]) {
-          if (MODE != kCapped) ptx::tmem_ld64(t_h, cur);
-          if (MODE != kPlain && shape.biased) {
+        if constexpr (MODE == kPlain) {
+          // (a scale that underflows must not meet the -inf of a masked score)
+          auto factor = [&](uint32_t ek_at) { return fmaxf(cq * lds_f(ek_at), 1.2e-38f); };
+          auto scores = [&](uint32_t (&cur)[64]) {
+            ptx::tmem_ld64(t_h, cur);
+            if (!whole) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              bias_block(cur + 16 * k, MODE == kCapped ? shape.cap2 : cq * lds_f(mh + 4 * k), shape,
-                         view.ref - (base + at_h + 16 * k), left);
-          }
-          if (!whole) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mask_block(cur + 16 * k, from(k), hi_r - (at_h + 16 * k));
-          }
-        };
-        auto weights = [&](const uint32_t (&cur)[64]) {
-          hat = wide;
-          sum = 0.f;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float ck = factor(mh + 4 * k);
-            float b;
-            exp_block(cur + 16 * k, ck, lds_f(mh + kMetaShift + 4 * k) - m, pk[k >> 1] + 8 * (k & 1), b);
-            hat += b;
-            sum = fmaf(b, lds_f(mh + kMetaInv + 4 * k), sum);
-          }
-        };
-        if constexpr (MODE == kCapped) {
-          uint32_t cur[64];
-          float most, ck[4];
-          ptx::tmem_ld64_max(t_h, cur, most);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) ck[k] = cq * lds_f(mh + 4 * k);
-          const float ck_most = fmaxf(fmaxf(ck[0], ck[1]), fmaxf(ck[2], ck[3])), x_most = most * ck_most;
-          const bool low = x_most <= kLowX && ck_most <= kLowMost && ck[0] == ck[1] && ck[0] == ck[2] && ck[0] == ck[3];
-          if (__all_sync(0xffffffffu, low) && whole && !shape.biased) {
+              for (int k = 0; k < 4; ++k) {
+                const int at = at0 + 64 * half + 16 * k;
+                mask_block(cur + 16 * k, (there >> (4 * half + k)) & 1u ? lo_r - at : 16, hi_r - at);
+              }
+            }
+          };
+          auto weights = [&](const uint32_t (&cur)[64]) {
             hat = wide;
             sum = 0.f;
-            const LowCap lc = low_cap(ck[0], shape.cap2);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
+              const float ck = factor(mh + 4 * k);
               float b;
-              exp_low_block(cur + 16 * k, lc, lds_f(mh + kMetaShift + 4 * k) - m, pk[k >> 1] + 8 * (k & 1), b);
+              exp_block(cur + 16 * k, ck, lds_f(mh + kMetaShift + 4 * k) - m, pk[k >> 1] + 8 * (k & 1), b);
               hat += b;
               sum = fmaf(b, lds_f(mh + kMetaInv + 4 * k), sum);
             }
-          } else {
-            if (__any_sync(0xffffffffu, x_most > 1.f)) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) cap_block(cur + 16 * k, ck[k], true);
-            } else {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) cap_block(cur + 16 * k, ck[k], false);
-            }
+          };
+          {
+            uint32_t cur[64];
             scores(cur);
             weights(cur);
           }
-        } else {
-          uint32_t cur[64];
-          scores(cur);
-          weights(cur);
-        }
-        // past FP16 (or the first weights of all, against the lowest base): a
-        // new base, and what there is so far follows it
-        if (__builtin_expect(__any_sync(0xffffffffu, hat > 32768.0f), 0)) {
-          float top = kLowest, f;
-          auto rise = [&]() {   // (by two factors: l may stand 75 binades above 2^m)
-            const float m_new = fmaxf(m, __fadd_ru(top, -9.f));
-            f = exp2f(0.5f * (m - m_new));
-            m = m_new;
-            l = l * f * f;
-          };
-          if constexpr (MODE == kPlain) {
+          // past FP16 (or the first weights of all, against the lowest base): a
+          // new base, and what there is so far follows it
+          if (__builtin_expect(__any_sync(0xffffffffu, hat > 32768.0f), 0)) {
             uint32_t cur[64];
             scores(cur);
+            float top = kLowest;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               float most = -CUDART_INF_F;
@@ -646,37 +705,80 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
               for (int i = 0; i < 16; ++i) most = fmaxf(most, __uint_as_float(cur[16 * k + i]));
               top = fmaxf(top, with_ev(most, factor(mh + 4 * k), lds_f(mh + kMetaShift + 4 * k)));
             }
-            rise();
+            const float f = rise(top);
             weights(cur);
             if (__any_sync(0xffffffffu, wide != 0.f || (fabsf(m) > kFarBase && m > kLowest))) {
-              sum = weights_apart(t_h, mh, cq, m, lo_r - at_h, hi_r - at_h, there >> (4 * half));
+              sum = weights_apart(t_h, mh, cq, m, lo_r - at0 - 64 * half, hi_r - at0 - 64 * half, there >> (4 * half));
               ptx::tmem_ld16(t_h, pk[0]);
               ptx::tmem_ld16(t_h + 16, pk[1]);
             }
-          } else {
-            const int lo_h = lo_r - at_h, hi_h = hi_r - at_h, dist = view.ref - (base + at_h);
-            top = shaped_top<MODE>(t_h, mh, cq, lo_h, hi_h, there >> (4 * half), shape, dist, left);
-            rise();
-            sum = shaped_weights_apart<MODE>(t_h, mh, cq, m, lo_h, hi_h, there >> (4 * half), shape, dist, left);
-            ptx::tmem_ld16(t_h, pk[0]);
-            ptx::tmem_ld16(t_h + 16, pk[1]);
+            follow(half, f);
           }
-          if (__any_sync(0xffffffffu, f != 1.f)) {
-            // (the product of the first half is still under way; the group's
-            // previous tile's was done before these scores were)
-            if (half == 1) {
-              if (lane == 0) st_release(ask0 + 4 * q, (uint32_t)j + 1u);
-              ok = __all_sync(0xffffffffu, ok && wait_word(told0 + 4 * q, (uint32_t)j + 1u, lim, abort, a.status));
+        } else {
+          bool low = whole && (MODE == kBiased || !shape.biased);
+          hat = wide;
+          sum = 0.f;
+          if (MODE == kBiased) {
+            // (left of every row's reference place, or right of them all)
+            const float step = !shape.biased ? 0.f : left ? shape.slope2 : -shape.slope2;
+            low = low && (!shape.biased || left || right);
+            if (low) {
+              const float d0 = (float)(view.ref - (base + at0 + 64 * half));
+              uint32_t cur[64];
+              ptx::tmem_ld64(t_h, cur);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                float b;
+                const float beside = fmaf(-step, d0 - (float)(16 * k), lds_f(mh + kMetaShift + 4 * k) - m);
+                exp_bias_block(cur + 16 * k, cq * lds_f(mh + 4 * k), beside, step, pk[k >> 1] + 8 * (k & 1), b);
+                hat += b;
+                sum = fmaf(b, lds_f(mh + kMetaInv + 4 * k), sum);
+              }
             }
-            ptx::tc_fence_after();
-            if (!first || half == 1) rescale_o(f * f);
+          } else if (low) {
+            uint32_t cur[64];
+            float most;
+            ptx::tmem_ld64_max(t_h, cur, most);
+            const float s0 = lds_f(mh), ck = cq * s0;
+            low = __all_sync(0xffffffffu, most * ck <= kLowX && ck <= kLowMost && lds_f(mh + 4) == s0 && lds_f(mh + 8) == s0 &&
+                                              lds_f(mh + 12) == s0);
+            if (low) {
+              const LowCap lc = low_cap(ck, shape.cap2);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                float b;
+                exp_low_block(cur + 16 * k, lc, lds_f(mh + kMetaShift + 4 * k) - m, pk[k >> 1] + 8 * (k & 1), b);
+                hat += b;
+                sum = fmaf(b, lds_f(mh + kMetaInv + 4 * k), sum);
+              }
+            }
+          }
+          if (low && !__any_sync(0xffffffffu, hat > 32768.0f)) {
+            ptx::tmem_st16(t_h, pk[0]);
+            ptx::tmem_st16(t_h + 16, pk[1]);
+            ptx::tmem_st_wait();
+          } else {
+            const int at_h = at0 + 64 * half;
+            const HalfRow hr{t_h, mh, there >> (4 * half), lo_r - at_h, hi_r - at_h, view.ref - (base + at_h), cq, shape};
+            // a single weight up to 2^15 still fits FP16; but a sum that was too
+            // large for the short way above must not be so again and again
+            const float top = whole ? shaped_top<MODE, false>(hr) : shaped_top<MODE, true>(hr);
+            float f = 1.f;
+            if (__any_sync(0xffffffffu, top > m + (low ? 9.f : 15.f))) f = rise(top);
+            if (__any_sync(0xffffffffu, wide != 0.f || (fabsf(m) > kFarBase && m > kLowest)))
+              sum = shaped_weights_apart<MODE>(hr, m);
+            else
+              sum = whole ? shaped_weights<MODE, false>(hr, m) : shaped_weights<MODE, true>(hr, m);
+            follow(half, f);
           }
         }
         l += sum;
-        // over the first 32 of the 64 score columns just read
-        ptx::tmem_st16(t_h, pk[0]);
-        ptx::tmem_st16(t_h + 16, pk[1]);
-        ptx::tmem_st_wait();
+        if constexpr (MODE == kPlain) {
+          // over the first 32 of the 64 score columns just read
+          ptx::tmem_st16(t_h, pk[0]);
+          ptx::tmem_st16(t_h + 16, pk[1]);
+          ptx::tmem_st_wait();
+        }
         ptx::tc_fence_before();
         warp_arrive(BAR((half == 0 ? kCbP : kCbPb) + q));
       }

@@ -113,6 +113,18 @@ __device__ __forceinline__ uint64_t low_scores(uint64_t s, const LowCap& c, uint
   return ptx::f2_fma(p, s, beside);
 }
 
+// The same for any score, by cap2 (1 - 2 / (1 + t)), t = 2^(2 x log2 e), alone: off
+// by 2^-22 of the cap, whatever the score.  Half the instructions of the choice
+// between two ways, and nothing that a weight in FP16 shows while the cap is below
+// kShortCap: 2^-14 there, an eighth of its rounding.  ct: 2 ck log2 e.
+constexpr float kShortCap = 256.f;
+__device__ __forceinline__ uint64_t far_scores(uint64_t s, float ct, uint64_t minus2cap, uint64_t cap_beside) {
+  float x0, x1;
+  ptx::f2_unpack(ptx::f2_mul(s, ptx::f2_pack(ct, ct)), x0, x1);
+  ptx::f2_unpack(ptx::f2_add(ptx::f2_pack(ptx::ex2_approx(x0), ptx::ex2_approx(x1)), ptx::f2_pack(1.f, 1.f)), x0, x1);
+  return ptx::f2_fma(ptx::f2_pack(rcp_approx(x0), rcp_approx(x1)), minus2cap, cap_beside);
+}
+
 // What is left to do to a shaped score: a factor to units of log 2.
 template <int MODE>
 __device__ __forceinline__ float shape_factor(const RowShape& r, float ck) {

@@ -314,6 +314,19 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr)
       : "memory");
 }
+// The largest of 16 consecutive columns as fp32 (NaN aside), found by the load.
+__device__ __forceinline__ float tmem_max16(uint32_t taddr) {
+  float most;
+  asm volatile(
+      "{\n\t.reg .b32 r<16>;\n\t"
+      "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 "
+      "{r0, r1, r2, r3, r4, r5, r6, r7, r8, r9, r10, r11, r12, r13, r14, r15}, %0, [%1];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n\t}"
+      : "=f"(most)
+      : "r"(taddr)
+      : "memory");
+  return most;
+}
 // 64 consecutive 32-bit columns of this thread's TMEM lane, waited for.
 __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
   asm volatile(
