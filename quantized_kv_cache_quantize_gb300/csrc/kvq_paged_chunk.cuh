@@ -309,28 +309,31 @@ __device__ __forceinline__ void shape_block(uint32_t* v, float raw, const HalfRo
 // scores: the largest of a block is shaped, no other.
 template <int MODE, bool MASKED>
 __device__ __noinline__ float shaped_top(HalfRow h) {
-  float top = kLowest;
-#pragma unroll 1
-  for (int k = 0; k < 4; ++k) {
-    const float raw = h.cq * lds_f(h.mh + 4 * k), ev = lds_f(h.mh + kMetaShift + 4 * k);
-    float most = -CUDART_INF_F;
-    if (!MASKED && !h.shape.biased) {
-      most = ptx::tmem_max16(h.t_h + 16 * k);
-    } else {
+  float top = kLowest, most[4];
+  if (!MASKED && !h.shape.biased) {
+    ptx::tmem_max16x4(h.t_h, most);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
       uint32_t v[16];
       ptx::tmem_ld16(h.t_h + 16 * k, v);
-      if (h.shape.biased) shape_block<MODE>(v, raw, h, k);
+      if (h.shape.biased) shape_block<MODE>(v, h.cq * lds_f(h.mh + 4 * k), h, k);
       if (MASKED) mask_block(v, (h.there >> k) & 1u ? h.lo - 16 * k : 16, h.hi - 16 * k);
+      most[k] = -CUDART_INF_F;
 #pragma unroll
-      for (int i = 0; i < 16; i += 2) most = ptx::max3(most, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+      for (int i = 0; i < 16; i += 2) most[k] = ptx::max3(most[k], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
     }
-    if (MODE == kCapped && !h.shape.biased && most > -CUDART_INF_F) {
-      const float x = raw * most;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float raw = h.cq * lds_f(h.mh + 4 * k), ev = lds_f(h.mh + kMetaShift + 4 * k);
+    if (MODE == kCapped && !h.shape.biased && most[k] > -CUDART_INF_F) {
+      const float x = raw * most[k];
       float s0, s1;
       ptx::f2_unpack(tanh_small(ptx::f2_pack(x, x)), s0, s1);
-      most = tanh_any(x, s0);
+      most[k] = tanh_any(x, s0);
     }
-    top = fmaxf(top, with_ev(most, fmaxf(shape_factor<MODE>(h.shape, raw), 1.2e-38f), ev));
+    top = fmaxf(top, with_ev(most[k], fmaxf(shape_factor<MODE>(h.shape, raw), 1.2e-38f), ev));
   }
   return top;
 }
@@ -340,21 +343,24 @@ __device__ __noinline__ float shaped_weights(HalfRow h, float m) {
   const bool far = MODE == kCapped && !h.shape.biased && h.shape.cap2 <= kShortCap * 1.4426950408889634f;
   float sum = 0.f;
 #pragma unroll 1
-  for (int k = 0; k < 4; ++k) {
-    uint32_t v[16], w[8];
-    ptx::tmem_ld16(h.t_h + 16 * k, v);
-    const float raw = h.cq * lds_f(h.mh + 4 * k), shift = lds_f(h.mh + kMetaShift + 4 * k) - m;
-    const int lo = (h.there >> k) & 1u ? h.lo - 16 * k : 16, hi = h.hi - 16 * k;
-    float b;
-    if (far) {
-      exp_far_block<MASKED>(v, raw, h.shape.cap2, shift, lo, hi, w, b);
-    } else {
-      shape_block<MODE>(v, raw, h, k);
-      if (MASKED) mask_block(v, lo, hi);
-      exp_block(v, fmaxf(shape_factor<MODE>(h.shape, raw), 1.2e-38f), shift, w, b);
+  for (int k = 0; k < 4; k += 2) {
+    uint32_t v[32], w[16];
+    ptx::tmem_ld32(h.t_h + 16 * k, v);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float raw = h.cq * lds_f(h.mh + 4 * (k + i)), shift = lds_f(h.mh + kMetaShift + 4 * (k + i)) - m;
+      const int lo = (h.there >> (k + i)) & 1u ? h.lo - 16 * (k + i) : 16, hi = h.hi - 16 * (k + i);
+      float b;
+      if (far) {
+        exp_far_block<MASKED>(v + 16 * i, raw, h.shape.cap2, shift, lo, hi, w + 8 * i, b);
+      } else {
+        shape_block<MODE>(v + 16 * i, raw, h, k + i);
+        if (MASKED) mask_block(v + 16 * i, lo, hi);
+        exp_block(v + 16 * i, fmaxf(shape_factor<MODE>(h.shape, raw), 1.2e-38f), shift, w + 8 * i, b);
+      }
+      sum = fmaf(b, lds_f(h.mh + kMetaInv + 4 * (k + i)), sum);
     }
-    sum = fmaf(b, lds_f(h.mh + kMetaInv + 4 * k), sum);
-    ptx::tmem_st8(h.t_h + 8 * k, w);   // (columns that the loads are past)
+    ptx::tmem_st16(h.t_h + 8 * k, w);   // (columns that the loads are past)
   }
   ptx::tmem_st_wait();
   return sum;

@@ -314,18 +314,23 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr)
       : "memory");
 }
-// The largest of 16 consecutive columns as fp32 (NaN aside), found by the load.
-__device__ __forceinline__ float tmem_max16(uint32_t taddr) {
-  float most;
+// The largest of each 16 of 64 consecutive columns as fp32 (NaN aside), found by
+// the loads.
+__device__ __forceinline__ void tmem_max16x4(uint32_t taddr, float (&most)[4]) {
   asm volatile(
-      "{\n\t.reg .b32 r<16>;\n\t"
-      "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 "
-      "{r0, r1, r2, r3, r4, r5, r6, r7, r8, r9, r10, r11, r12, r13, r14, r15}, %0, [%1];\n\t"
+      "{\n\t.reg .b32 r<64>;\n\t"
+      "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {r0, r1, r2, r3, r4, r5, r6, r7, "
+      "r8, r9, r10, r11, r12, r13, r14, r15}, %0, [%4];\n\t"
+      "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {r16, r17, r18, r19, r20, r21, r22, r23, "
+      "r24, r25, r26, r27, r28, r29, r30, r31}, %1, [%5];\n\t"
+      "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {r32, r33, r34, r35, r36, r37, r38, r39, "
+      "r40, r41, r42, r43, r44, r45, r46, r47}, %2, [%6];\n\t"
+      "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {r48, r49, r50, r51, r52, r53, r54, r55, "
+      "r56, r57, r58, r59, r60, r61, r62, r63}, %3, [%7];\n\t"
       "tcgen05.wait::ld.sync.aligned;\n\t}"
-      : "=f"(most)
-      : "r"(taddr)
+      : "=f"(most[0]), "=f"(most[1]), "=f"(most[2]), "=f"(most[3])
+      : "r"(taddr), "r"(taddr + 16), "r"(taddr + 32), "r"(taddr + 48)
       : "memory");
-  return most;
 }
 // 64 consecutive 32-bit columns of this thread's TMEM lane, waited for.
 __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
