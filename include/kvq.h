@@ -572,7 +572,8 @@ typedef struct kvq_rope_tensor {
  * BF16, head_dim 64 or 128.  positions: int32 device, that of batch entry b,
  * row i and axis k at b * pos_batch_stride + i * pos_row_stride + k *
  * pos_axis_stride elements.  batch * rows == 0 is a no-op.  batch * rows <=
- * 2^31 - 1, times the tensors' heads <= 2^35 (else KVQ_ERR_TOO_LARGE).
+ * 2^31 - 1, times the tensors' heads <= 2^35, and batch * ceil(rows / 16) * the
+ * sum of ceil(heads / 8) < 2^31 (else KVQ_ERR_TOO_LARGE).
  */
 kvq_status kvq_rope(const kvq_rope_table *table, const int32_t *positions, int64_t pos_batch_stride,
                     int64_t pos_row_stride, int64_t pos_axis_stride, int32_t batch, int32_t rows,

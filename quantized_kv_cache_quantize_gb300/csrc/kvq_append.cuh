@@ -2,6 +2,7 @@
 // the scale rule over a page's new values, codes under a scale that grew.
 #pragma once
 
+#include "kvq_checks.cuh"
 #include "kvq_pages.cuh"
 
 namespace kvq {
@@ -83,6 +84,51 @@ __device__ __forceinline__ int scale_of(float m, int* status) {
   return exp_for_max(m);
 }
 __device__ __forceinline__ int scale_of(uint32_t bits, int* status) { return scale_of(__uint_as_float(bits << 16), status); }
+
+// One page of work item `item`, of one head, K or V, by a block of page * D / 32
+// threads, 32 values each: they wait in registers for the page's maximum.
+template <int D>
+__device__ __forceinline__ void append_page(const AppendArgs& a, int kv, int head, int item) {
+  constexpr int C = D / 8;             // 16-byte chunks of a row
+  __shared__ uint32_t part[16];
+  const int tid = threadIdx.x, lane = tid & 31;
+  int b, p, r0, first, end;
+  if (!append_item(a, item, b, p, r0, first, end)) return;
+  const int id = seq_page(a.s, b, p, a.p.n_pages, a.status);
+  if (id < 0) return;
+  const int t0 = p << a.p.shift;
+  const int lo = max(first - t0, 0), hi = min(end - t0, a.p.page);
+  const long long blk = (long long)id * a.p.heads + head;
+  if (!KVQ_IN_BOUNDS(blk, (long long)a.p.n_pages * a.p.heads, a.status, a.bounds_site)) return;
+  uint8_t* codes = a.p.codes[kv] + blk * a.p.page * D;
+  const int c = tid % C, step = blockDim.x / C;      // page / 4 rows at a time
+  const uint16_t* x = a.x[kv] + (long long)(r0 + (t0 - first)) * a.row_stride[kv] + head * a.head_stride[kv] + 8 * c;
+  uint4 v[4];
+  uint32_t m = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int t = tid / C + k * step;
+    v[k] = t >= lo && t < hi ? __ldg(reinterpret_cast<const uint4*>(x + t * a.row_stride[kv])) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  const int old = lo > 0 ? scale_exp(a.p.scale[kv][blk]) : kPageExpMin;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) m = __vmaxu2(m, max_pair(v[k]));
+  m = __reduce_max_sync(0xffffffffu, max_bits(m));
+  if (blockDim.x > 32) {
+    if (lane == 0) part[tid >> 5] = m;
+    __syncthreads();
+    m = __reduce_max_sync(0xffffffffu, lane < (int)(blockDim.x >> 5) ? part[lane] : 0u);
+  }
+  const int e = max(scale_of(m, a.status), old);
+  if (lo > 0 && e > old) rescale_codes<D>(codes, lo, old - e, tid, blockDim.x);
+  if (tid == 0) a.p.scale[kv][blk] = scale_bits(e);
+  const float f = pow2f(-e);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int t = tid / C + k * step;
+    if (t >= lo && t < hi) *reinterpret_cast<uint2*>(codes + t * D + 8 * c) = codes_of(v[k], f);
+  }
+}
 
 }  // namespace
 }  // namespace kvq

@@ -18,48 +18,9 @@ namespace {
 // 40 heads from 74.1 to 70.3 us, 6.3 TB/s; 4680 of 24 take 15.7 us, 5.5 TB/s).
 template <int D>
 __global__ void __launch_bounds__(512) append_kernel(const __grid_constant__ AppendArgs a) {
-  constexpr int C = D / 8;             // 16-byte chunks of a row
-  __shared__ uint32_t part[16];
-  const int tid = threadIdx.x, lane = tid & 31;
   ptx::grid_dependency_wait();
   const int kv = blockIdx.x & 1, hi_ = blockIdx.x >> 1;
-  const int head = hi_ % a.p.heads;
-  int b, p, r0, first, end;
-  if (!append_item(a, hi_ / a.p.heads, b, p, r0, first, end)) return;
-  const int id = seq_page(a.s, b, p, a.p.n_pages, a.status);
-  if (id < 0) return;
-  const int t0 = p << a.p.shift;
-  const int lo = max(first - t0, 0), hi = min(end - t0, a.p.page);
-  const long long blk = (long long)id * a.p.heads + head;
-  if (!KVQ_IN_BOUNDS(blk, (long long)a.p.n_pages * a.p.heads, a.status, a.bounds_site)) return;
-  uint8_t* codes = a.p.codes[kv] + blk * a.p.page * D;
-  const int c = tid % C, step = blockDim.x / C;      // page / 4 rows at a time
-  const uint16_t* x = a.x[kv] + (long long)(r0 + (t0 - first)) * a.row_stride[kv] + head * a.head_stride[kv] + 8 * c;
-  uint4 v[4];
-  uint32_t m = 0;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int t = tid / C + k * step;
-    v[k] = t >= lo && t < hi ? __ldg(reinterpret_cast<const uint4*>(x + t * a.row_stride[kv])) : make_uint4(0u, 0u, 0u, 0u);
-  }
-  const int old = lo > 0 ? scale_exp(a.p.scale[kv][blk]) : kPageExpMin;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) m = __vmaxu2(m, max_pair(v[k]));
-  m = __reduce_max_sync(0xffffffffu, max_bits(m));
-  if (blockDim.x > 32) {
-    if (lane == 0) part[tid >> 5] = m;
-    __syncthreads();
-    m = __reduce_max_sync(0xffffffffu, lane < (int)(blockDim.x >> 5) ? part[lane] : 0u);
-  }
-  const int e = max(scale_of(m, a.status), old);
-  if (lo > 0 && e > old) rescale_codes<D>(codes, lo, old - e, tid, blockDim.x);
-  if (tid == 0) a.p.scale[kv][blk] = scale_bits(e);
-  const float f = pow2f(-e);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int t = tid / C + k * step;
-    if (t >= lo && t < hi) *reinterpret_cast<uint2*>(codes + t * D + 8 * c) = codes_of(v[k], f);
-  }
+  append_page<D>(a, kv, hi_ % a.p.heads, hi_ / a.p.heads);
 }
 
 // One token of every sequence: a warp per sequence, head and K or V, D / 8

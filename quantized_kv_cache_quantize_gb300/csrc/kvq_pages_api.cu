@@ -252,16 +252,19 @@ kvq_status kvq_rope(const kvq_rope_table* table, const int32_t* positions, int64
   if (st != KVQ_OK) return st;
   if (batch < 0 || rows < 0 || tensors == nullptr || n_tensors < 1 || n_tensors > 2) return KVQ_ERR_INVALID_ARG;
   kvq::RopeArgs a{};
-  long long heads = 0;
+  long long heads = 0, groups = 0;
   for (int i = 0; i < n_tensors; ++i) {
     const kvq_rope_tensor& t = tensors[i];
     if (t.heads < 0) return KVQ_ERR_INVALID_ARG;
     heads += t.heads;
+    groups += ((long long)t.heads + 7) / 8;
     a.x[i] = kvq::RopeTensor{t.x, t.y, t.x_batch_stride, t.x_row_stride, t.x_head_stride,
                              t.y_batch_stride, t.y_row_stride, t.y_head_stride, t.heads};
   }
   const long long all = (long long)batch * rows;
   if (all > 0x7fffffffLL || heads > 0x7fffffffLL || (all > 0 && heads > (1LL << 35) / all)) return KVQ_ERR_TOO_LARGE;
+  const long long tiles = (long long)batch * (((long long)rows + 15) / 16);   // of 16 rows; a block each, and eight heads
+  if (tiles > 0 && groups > 0x7fffffffLL / tiles) return KVQ_ERR_TOO_LARGE;
   if (all == 0 || heads == 0) return KVQ_OK;
   if (positions == nullptr) return KVQ_ERR_INVALID_ARG;
   if (!aligned(positions, 4)) return KVQ_ERR_ALIGNMENT;

@@ -2,6 +2,8 @@
 // to the paged cache that rotates its keys on the way (sm_103a).
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "kvq_append.cuh"
 #include "kvq_checks.cuh"
 #include "kvq_pages.cuh"
@@ -30,36 +32,30 @@ __global__ void __launch_bounds__(256) rope_fill_kernel(const __grid_constant__ 
 }
 
 // ---- rotation ---------------------------------------------------------------
-// A thread rotates 16 channels of one row and head.
+// A block per R rows and eight heads of one tensor.  Each value is read and
+// written once and HBM bounds the large sizes; the turns, 4 bytes a channel, would
+// double the reads if every head fetched its own.  R = 4 spreads a small call over
+// the SMs, 16 leaves eight loads a thread in flight.
+template <int D, int R>
 __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeArgs a) {
+  __shared__ __align__(16) float2 turns[R * kRopeRow];
   ptx::grid_dependency_wait();
   ptx::launch_dependents();
-  const unsigned units = (unsigned)a.d / 16u;
-  const int heads = a.x[0].heads + a.x[1].heads;
-  unsigned long long i = (unsigned long long)blockIdx.x * blockDim.x + threadIdx.x;
-  const int u = (int)(i % units);
-  i /= units;
-  const int row = (int)(i % (unsigned)a.rows);
-  i /= (unsigned)a.rows;
-  int h = (int)(i % (unsigned)heads);
-  const unsigned long long b = i / (unsigned)heads;
-  if (b >= (unsigned long long)a.batch) return;
-  const bool second = h >= a.x[0].heads;
-  if (second) h -= a.x[0].heads;
+  const unsigned tiles = ((unsigned)a.rows + R - 1) / R;
+  const unsigned q_groups = (unsigned)(a.x[0].heads + kRopeHeads - 1) / kRopeHeads,
+                 groups = q_groups + (unsigned)(a.x[1].heads + kRopeHeads - 1) / kRopeHeads;
+  unsigned g = blockIdx.x % groups;
+  const unsigned rest = blockIdx.x / groups;
+  const int row0 = (int)(rest % tiles) * R;
+  const long long b = rest / tiles;
+  const bool second = g >= q_groups;
+  if (second) g -= q_groups;
   const RopeTensor& x = a.x[second ? 1 : 0];
-  int c0, c1;
-  rope_chunks(a.t, u, c0, c1);
-  const uint16_t* from = x.x + (long long)b * x.xb + (long long)row * x.xr + (long long)h * x.xh;
-  uint16_t* to = x.y + (long long)b * x.yb + (long long)row * x.yr + (long long)h * x.yh;
-  uint4 v = *reinterpret_cast<const uint4*>(from + c0), w = *reinterpret_cast<const uint4*>(from + c1);
-  if (u < (a.t.pairs >> 3)) {
-    const RopeAt at = rope_at(a.t, a.pos + (long long)b * a.pb + (long long)row * a.pr, a.pa, a.status);
-    float2 cs[8];
-    rope_turn<8>(a.t, at, 8 * u, a.inverse != 0, cs);
-    rope_apply(a.t, cs, v, w);
-  }
-  *reinterpret_cast<uint4*>(to + c0) = v;
-  *reinterpret_cast<uint4*>(to + c1) = w;
+  const int h0 = (int)g * kRopeHeads;
+  const int32_t* pos = a.pos + b * a.pb + row0 * a.pr;
+  rope_tile<D, R>(a.t, a.inverse != 0, turns, min(R, a.rows - row0), min(kRopeHeads, x.heads - h0),
+                  x.x + b * x.xb + row0 * x.xr + h0 * x.xh, x.xr, x.xh, x.y + b * x.yb + row0 * x.yr + h0 * x.yh, x.yr,
+                  x.yh, a.status, [&](int r, int axis) { return __ldg(pos + r * a.pr + axis * a.pa); });
 }
 
 // ---- append -----------------------------------------------------------------
@@ -73,78 +69,29 @@ __device__ __forceinline__ int seq_of_row(const PageSeqs& s, int r) {
   return lo;
 }
 
-// Queries beside the append: 16 channels of one row and head a thread.
-template <int D>
-__device__ __forceinline__ void append_query(const AppendRopeArgs& p, unsigned long long i) {
+// Queries beside the append, R rows and eight heads: block `at` of theirs.
+template <int D, int R>
+__device__ __forceinline__ void append_queries(const AppendRopeArgs& p, unsigned at, float2* turns) {
   const PageSeqs& s = p.a.s;
-  constexpr unsigned kUnits = D / 16;
-  const int u = (int)(i % kUnits);
-  i /= kUnits;
-  const int h = (int)(i % (unsigned)p.q.heads);
-  const unsigned long long row = i / (unsigned)p.q.heads;
-  if (row >= (unsigned long long)s.rows) return;
-  const int r = (int)row;
-  if (s.offsets != nullptr && (r < __ldg(s.offsets) || r >= __ldg(s.offsets + s.batch))) return;
-  int c0, c1;
-  rope_chunks(p.t, u, c0, c1);
-  const uint16_t* from = p.q.x + (long long)r * p.q.xr + (long long)h * p.q.xh;
-  uint16_t* to = p.q.y + (long long)r * p.q.yr + (long long)h * p.q.yh;
-  uint4 v = *reinterpret_cast<const uint4*>(from + c0), w = *reinterpret_cast<const uint4*>(from + c1);
-  if (u < (p.t.pairs >> 3)) {
-    RopeAt at;
-    if (p.pos != nullptr) {
-      at = rope_at(p.t, p.pos + (long long)r * p.pr, 1, p.a.status);
-    } else {
-      int b = r, end = r + 1;
-      if (s.offsets != nullptr) {
-        b = seq_of_row(s, r);
-        end = __ldg(s.offsets + b + 1);
-      }
-      at = rope_at(p.t, seq_len(s, b, p.a.p.shift, p.a.status) - (end - r), p.a.status);
+  const unsigned groups = (unsigned)(p.q.heads + kRopeHeads - 1) / kRopeHeads;
+  const int h0 = (int)(at % groups) * kRopeHeads;
+  int row0 = (int)(at / groups) * R, end = min(row0 + R, s.rows);
+  if (s.offsets != nullptr) {   // rows that no sequence has are left alone
+    row0 = max(row0, __ldg(s.offsets));
+    end = min(end, __ldg(s.offsets + s.batch));
+  }
+  if (row0 >= end) return;
+  auto place = [&](int r, int axis) {
+    if (p.pos != nullptr) return __ldg(p.pos + (row0 + r) * p.pr + axis);
+    int b = row0 + r, next = b + 1;
+    if (s.offsets != nullptr) {
+      b = seq_of_row(s, b);
+      next = __ldg(s.offsets + b + 1);
     }
-    float2 cs[8];
-    rope_turn<8>(p.t, at, 8 * u, false, cs);
-    rope_apply(p.t, cs, v, w);
-  }
-  *reinterpret_cast<uint4*>(to + c0) = v;
-  *reinterpret_cast<uint4*>(to + c1) = w;
-}
-
-// Chunk c (8 channels) of a key row, rotated, in fp32.  The lanes of a row's
-// D / 8 chunks are neighbours; every lane of the warp calls.
-template <int D>
-__device__ __forceinline__ void rotate_chunk(const RopeTab& t, const RopeAt& at, int c, bool live, const uint4& v,
-                                             float (&f)[8]) {
-  floats_of(v, f);
-  const int p8 = t.pairs >> 3;
-  if (t.interleaved) {
-    if (c < 2 * p8 && live) {
-      float2 cs[4];
-      rope_turn<4>(t, at, 4 * c, false, cs);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float x0 = f[2 * k], x1 = f[2 * k + 1];
-        f[2 * k] = turn_first(x0, x1, cs[k]);
-        f[2 * k + 1] = turn_second(x0, x1, cs[k]);
-      }
-    }
-    return;
-  }
-  const int other = c < p8 ? c + p8 : c < 2 * p8 ? c - p8 : c;
-  const int lane = (int)(threadIdx.x & 31), from = lane - c % (D / 8) + other;
-  uint4 o;
-  o.x = __shfl_sync(0xffffffffu, v.x, from);
-  o.y = __shfl_sync(0xffffffffu, v.y, from);
-  o.z = __shfl_sync(0xffffffffu, v.z, from);
-  o.w = __shfl_sync(0xffffffffu, v.w, from);
-  if (c < 2 * p8 && live) {
-    float g[8];
-    floats_of(o, g);
-    float2 cs[8];
-    rope_turn<8>(t, at, 8 * (c < p8 ? c : c - p8), false, cs);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = c < p8 ? turn_first(f[k], g[k], cs[k]) : turn_second(g[k], f[k], cs[k]);
-  }
+    return seq_len(s, b, p.a.p.shift, p.a.status) - (next - (row0 + r));
+  };
+  rope_tile<D, R>(p.t, false, turns, end - row0, min(kRopeHeads, p.q.heads - h0), p.q.x + row0 * p.q.xr + h0 * p.q.xh,
+                  p.q.xr, p.q.xh, p.q.y + row0 * p.q.yr + h0 * p.q.yh, p.q.yr, p.q.yh, p.a.status, place);
 }
 
 __device__ __forceinline__ uint32_t max_abs_bits(const float (&f)[8]) {
@@ -157,80 +104,127 @@ __device__ __forceinline__ uint2 codes_of(const float (&v)[8], float f) {
   return make_uint2(e4m3x4(v[0] * f, v[1] * f, v[2] * f, v[3] * f), e4m3x4(v[4] * f, v[5] * f, v[6] * f, v[7] * f));
 }
 
-// Many new tokens: a block per page, head and K or V; behind them blocks of
-// query rows.
+// One page of keys, heads [h0, h1), by a block of page * D / 32 threads: two units
+// of 16 channels a thread and head.  The page's turns go to shared memory once
+// for all heads; the next head's values are on their way while this one's page
+// maximum is found.
 template <int D>
-__global__ void __launch_bounds__(512) append_rope_kernel(const __grid_constant__ AppendRopeArgs p, unsigned kv_blocks) {
-  constexpr int C = D / 8;             // 16-byte chunks of a row
-  __shared__ uint32_t part[16];
+__device__ __forceinline__ void append_keys(const AppendRopeArgs& p, int item, int h0, int h1, float2* turns) {
+  constexpr int U = D / 16;
+  __shared__ uint32_t part[2][16];
   const AppendArgs& a = p.a;
-  const int tid = threadIdx.x, lane = tid & 31;
-  ptx::grid_dependency_wait();
-  if (blockIdx.x >= kv_blocks) {
-    append_query<D>(p, (unsigned long long)(blockIdx.x - kv_blocks) * blockDim.x + tid);
-    return;
-  }
-  const int kv = blockIdx.x & 1, hi_ = blockIdx.x >> 1;
-  const int head = hi_ % a.p.heads;
+  const int tid = threadIdx.x, lane = tid & 31, step = blockDim.x / U;   // half a page of rows
   int b, pg, r0, first, end;
-  if (!append_item(a, hi_ / a.p.heads, b, pg, r0, first, end)) return;
+  if (!append_item(a, item, b, pg, r0, first, end)) return;
   const int id = seq_page(a.s, b, pg, a.p.n_pages, a.status);
   if (id < 0) return;
   const int t0 = pg << a.p.shift;
   const int lo = max(first - t0, 0), hi = min(end - t0, a.p.page);
-  const long long blk = (long long)id * a.p.heads + head;
-  if (!KVQ_IN_BOUNDS(blk, (long long)a.p.n_pages * a.p.heads, a.status, a.bounds_site)) return;
-  uint8_t* codes = a.p.codes[kv] + blk * a.p.page * D;
-  const int c = tid % C, step = blockDim.x / C;      // page / 4 rows at a time
-  const int row = r0 + (t0 - first);                 // packed row of the page's token 0
-  const uint16_t* x = a.x[kv] + (long long)row * a.row_stride[kv] + head * a.head_stride[kv] + 8 * c;
-  float f[4][8];
-  uint32_t m = 0;
+  if (!KVQ_IN_BOUNDS((long long)id * a.p.heads + h1 - 1, (long long)a.p.n_pages * a.p.heads, a.status, a.bounds_site)) return;
+  const long long row = r0 + (t0 - first);           // packed row of the page's token 0
+  const int u = tid % U;
+  int c0, c1;
+  rope_chunks(p.t, u, c0, c1);
+  const uint16_t* x = a.x[0] + row * a.row_stride[0];
+  uint4 v[2], w[2];
+  auto load = [&](int h) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int t = tid / C + k * step;
-    const bool live = t >= lo && t < hi;
-    const uint4 v = live ? __ldg(reinterpret_cast<const uint4*>(x + t * a.row_stride[kv])) : make_uint4(0u, 0u, 0u, 0u);
-    if (kv == 0) {
-      RopeAt at{};
-      if (live)
-        at = p.pos != nullptr ? rope_at(p.t, p.pos + (long long)(row + t) * p.pr, 1, a.status)
-                              : rope_at(p.t, t0 + t, a.status);
-      rotate_chunk<D>(p.t, at, c, live, v, f[k]);
-    } else {
-      floats_of(v, f[k]);
+    for (int k = 0; k < 2; ++k) {
+      const int t = tid / U + k * step;
+      const uint16_t* from = x + t * a.row_stride[0] + h * a.head_stride[0];
+      const bool live = t >= lo && t < hi;
+      v[k] = live ? __ldg(reinterpret_cast<const uint4*>(from + c0)) : make_uint4(0u, 0u, 0u, 0u);
+      w[k] = live ? __ldg(reinterpret_cast<const uint4*>(from + c1)) : make_uint4(0u, 0u, 0u, 0u);
     }
-  }
-  const int old = lo > 0 ? scale_exp(a.p.scale[kv][blk]) : kPageExpMin;
+  };
+  load(h0);
+  rope_stage(p.t, turns, hi - lo, false, a.status, [&](int r, int axis) {
+    return p.pos != nullptr ? __ldg(p.pos + (row + lo + r) * p.pr + axis) : t0 + lo + r;
+  });
+  __syncthreads();
+  for (int h = h0; h < h1; ++h) {
+    const long long blk = (long long)id * a.p.heads + h;
+    uint8_t* codes = a.p.codes[0] + blk * a.p.page * D;
+    const int old = lo > 0 ? scale_exp(a.p.scale[0][blk]) : kPageExpMin;
+    float f[2][8], g[2][8];
+    uint32_t m = 0;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) m = max(m, max_abs_bits(f[k]));
-  m = __reduce_max_sync(0xffffffffu, m);
-  if (blockDim.x > 32) {
-    if (lane == 0) part[tid >> 5] = m;
-    __syncthreads();
-    m = __reduce_max_sync(0xffffffffu, lane < (int)(blockDim.x >> 5) ? part[lane] : 0u);
-  }
-  const int e = max(scale_of(__uint_as_float(m), a.status), old);
-  if (lo > 0 && e > old) rescale_codes<D>(codes, lo, old - e, tid, blockDim.x);
-  if (tid == 0) a.p.scale[kv][blk] = scale_bits(e);
-  const float s = pow2f(-e);
+    for (int k = 0; k < 2; ++k) {
+      const int t = tid / U + k * step;
+      if (u < (p.t.pairs >> 3) && t >= lo && t < hi) {
+        float2 cs[8];
+        rope_turns(turns + (t - lo) * kRopeRow, u, cs);
+        rope_apply(p.t, cs, v[k], w[k], f[k], g[k]);
+      } else {
+        floats_of(v[k], f[k]);
+        floats_of(w[k], g[k]);
+      }
+      m = max(m, max(max_abs_bits(f[k]), max_abs_bits(g[k])));
+    }
+    if (h + 1 < h1) load(h + 1);
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (blockDim.x > 32) {   // (two buffers: a head's is read while the next one's is written)
+      uint32_t* mine = part[(h - h0) & 1];
+      if (lane == 0) mine[tid >> 5] = m;
+      __syncthreads();
+      m = __reduce_max_sync(0xffffffffu, lane < (int)(blockDim.x >> 5) ? mine[lane] : 0u);
+    }
+    const int e = max(scale_of(__uint_as_float(m), a.status), old);
+    if (lo > 0 && e > old) rescale_codes<D>(codes, lo, old - e, tid, blockDim.x);
+    if (tid == 0) a.p.scale[0][blk] = scale_bits(e);
+    const float s = pow2f(-e);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int t = tid / C + k * step;
-    if (t >= lo && t < hi) *reinterpret_cast<uint2*>(codes + t * D + 8 * c) = codes_of(f[k], s);
+    for (int k = 0; k < 2; ++k) {
+      const int t = tid / U + k * step;
+      if (t >= lo && t < hi) {
+        *reinterpret_cast<uint2*>(codes + t * D + c0) = codes_of(f[k], s);
+        *reinterpret_cast<uint2*>(codes + t * D + c1) = codes_of(g[k], s);
+      }
+    }
   }
 }
 
-// One token of every sequence: a warp per sequence, head and K or V, as in the
-// plain append; behind them warps of query rows.
+// Many new tokens: blocks of keys (a page and `heads` heads), of values (a page
+// and head), of query rows.
+struct AppendGrid {
+  unsigned k_blocks, v_blocks;
+  int heads;   // per block of keys
+};
+constexpr int kQueryRows = 16;
+template <int D>
+__global__ void __launch_bounds__(512) append_rope_kernel(const __grid_constant__ AppendRopeArgs p, const AppendGrid g) {
+  extern __shared__ __align__(16) float2 turns[];
+  ptx::grid_dependency_wait();
+  unsigned at = blockIdx.x;
+  if (at < g.k_blocks) {
+    const unsigned groups = (unsigned)(p.a.p.heads + g.heads - 1) / (unsigned)g.heads;
+    const int h0 = (int)(at % groups) * g.heads;
+    append_keys<D>(p, (int)(at / groups), h0, min(h0 + g.heads, p.a.p.heads), turns);
+    return;
+  }
+  at -= g.k_blocks;
+  if (at < g.v_blocks) {
+    append_page<D>(p.a, 1, (int)(at % (unsigned)p.a.p.heads), (int)(at / (unsigned)p.a.p.heads));
+    return;
+  }
+  append_queries<D, kQueryRows>(p, at - g.v_blocks, turns);
+}
+
+// One token of every sequence: a warp per sequence, head and K or V, half the lanes
+// a unit of 16 channels each; behind them blocks of query rows.  What counts is
+// the chain of dependent loads: length, position, then turns beside table entry
+// and scale.
+constexpr int kOneRows = 4;
 template <int D>
 __global__ void __launch_bounds__(128) append_one_rope_kernel(const __grid_constant__ AppendRopeArgs p, unsigned kv_blocks) {
+  constexpr int U = D / 16;
+  __shared__ __align__(16) float2 turns[kOneRows * kRopeRow];
   const AppendArgs& a = p.a;
   const int lane = threadIdx.x & 31;
   ptx::grid_dependency_wait();
   ptx::launch_dependents();
   if (blockIdx.x >= kv_blocks) {
-    append_query<D>(p, (unsigned long long)(blockIdx.x - kv_blocks) * blockDim.x + threadIdx.x);
+    append_queries<D, kOneRows>(p, blockIdx.x - kv_blocks, turns);
     return;
   }
   const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
@@ -238,35 +232,51 @@ __global__ void __launch_bounds__(128) append_one_rope_kernel(const __grid_const
   const long long item = (w >> 1) / a.p.heads;
   if (item >= a.s.batch) return;
   const int b = (int)item;
-  const bool has = lane < D / 8;
-  uint4 v = make_uint4(0u, 0u, 0u, 0u);
-  if (has) v = __ldg(reinterpret_cast<const uint4*>(a.x[kv] + b * a.row_stride[kv] + head * a.head_stride[kv] + 8 * lane));
+  const bool has = lane < U;
+  int c0, c1;
+  rope_chunks(p.t, lane % U, c0, c1);
+  uint4 v = make_uint4(0u, 0u, 0u, 0u), y = v;
+  if (has) {
+    const uint16_t* from = a.x[kv] + b * a.row_stride[kv] + head * a.head_stride[kv];
+    v = __ldg(reinterpret_cast<const uint4*>(from + c0));
+    y = __ldg(reinterpret_cast<const uint4*>(from + c1));
+  }
   const int len = seq_len(a.s, b, a.p.shift, a.status);
   if (len < 1) {
     page_error(a.status);     // a new token, but no place for it
     return;
   }
   const int pg = (len - 1) >> a.p.shift, t = (len - 1) & (a.p.page - 1);
+  float f[8], g[8];
+  floats_of(v, f);
+  floats_of(y, g);
+  if (kv == 0 && lane < (p.t.pairs >> 3)) {
+    float2 cs[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int pair = 8 * lane + k;
+      const int pos = p.pos != nullptr ? __ldg(p.pos + b * p.pr + p.t.axis[pair]) : len - 1;
+      cs[k] = __ldg(p.t.cs + (long long)rope_position(p.t, pos, a.status) * p.t.pairs + pair);
+    }
+    rope_apply(p.t, cs, v, y, f, g);
+  }
   const int id = seq_page(a.s, b, pg, a.p.n_pages, a.status);
   if (id < 0) return;
   const long long blk = (long long)id * a.p.heads + head;
   if (!KVQ_IN_BOUNDS(blk, (long long)a.p.n_pages * a.p.heads, a.status, a.bounds_site)) return;
   uint8_t* codes = a.p.codes[kv] + blk * a.p.page * D;
   const int old = t > 0 ? scale_exp(a.p.scale[kv][blk]) : kPageExpMin;
-  float f[8];
-  if (kv == 0) {
-    const RopeAt at = p.pos != nullptr ? rope_at(p.t, p.pos + (long long)b * p.pr, 1, a.status)
-                                       : rope_at(p.t, len - 1, a.status);
-    rotate_chunk<D>(p.t, at, lane % (D / 8), has, v, f);
-  } else {
-    floats_of(v, f);
-  }
-  const uint32_t m = __reduce_max_sync(0xffffffffu, max_abs_bits(f));
+  const uint32_t m = __reduce_max_sync(0xffffffffu, max(max_abs_bits(f), max_abs_bits(g)));
   const int e = max(scale_of(__uint_as_float(m), a.status), old);
   if (t > 0 && e > old) rescale_codes<D>(codes, t, old - e, lane, 32);
   if (lane == 0 && (t == 0 || e > old)) a.p.scale[kv][blk] = scale_bits(e);
-  if (has) *reinterpret_cast<uint2*>(codes + t * D + 8 * lane) = codes_of(f, pow2f(-e));
+  if (has) {
+    *reinterpret_cast<uint2*>(codes + t * D + c0) = codes_of(f, pow2f(-e));
+    *reinterpret_cast<uint2*>(codes + t * D + c1) = codes_of(g, pow2f(-e));
+  }
 }
+
+std::atomic<uint64_t> g_append_smem[2];
 
 }  // namespace
 
@@ -285,22 +295,40 @@ cudaError_t launch_rope_fill(float* cos_sin, int n, int pairs, const double* fre
 }
 
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream) {
-  const long long threads = (long long)a.batch * a.rows * (a.x[0].heads + a.x[1].heads) * (a.d / 16);
-  return launch_dependent(rope_kernel, (unsigned)((threads + 255) / 256), 256, 0, stream, a);
+  const int sms = sm_count_current();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  const long long groups = (a.x[0].heads + kRopeHeads - 1) / kRopeHeads + (a.x[1].heads + kRopeHeads - 1) / kRopeHeads;
+  auto blocks = [&](int rows) { return (long long)a.batch * ((a.rows + rows - 1) / rows) * groups; };
+  // few rows: four a block, as long as those do not fill the GPU twice
+  const bool few = blocks(4) <= 16LL * sms;
+  const auto kern = few ? (a.d == 64 ? rope_kernel<64, 4> : rope_kernel<128, 4>)
+                        : (a.d == 64 ? rope_kernel<64, 16> : rope_kernel<128, 16>);
+  return launch_dependent(kern, (unsigned)blocks(few ? 4 : 16), 256, 0, stream, a);
 }
 
 cudaError_t launch_pages_append_rope(const AppendRopeArgs& p, cudaStream_t stream) {
   const AppendArgs& a = p.a;
-  const bool one = a.s.offsets == nullptr;
-  const long long items = one ? a.s.batch : (a.s.rows >> a.p.shift) + 2LL * a.s.batch;
-  const long long units = items * a.p.heads * 2;
-  const int threads = one ? 128 : a.p.page * a.p.d / 32;
-  const long long kv_blocks = one ? (units + 3) / 4 : units;
-  const long long q_blocks = ((long long)a.s.rows * p.q.heads * (a.p.d / 16) + threads - 1) / threads;
-  if (kv_blocks + q_blocks == 0) return cudaSuccess;
-  const auto kern = one ? (a.p.d == 64 ? append_one_rope_kernel<64> : append_one_rope_kernel<128>)
-                        : (a.p.d == 64 ? append_rope_kernel<64> : append_rope_kernel<128>);
-  return launch_dependent(kern, (unsigned)(kv_blocks + q_blocks), threads, 0, stream, p, (unsigned)kv_blocks);
+  const int sms = sm_count_current();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  const long long q_groups = (p.q.heads + kRopeHeads - 1) / kRopeHeads;
+  if (a.s.offsets == nullptr) {
+    const long long kv_blocks = ((long long)a.s.batch * a.p.heads * 2 + 3) / 4;
+    const long long q_blocks = (a.s.rows + kOneRows - 1) / kOneRows * q_groups;
+    const auto kern = a.p.d == 64 ? append_one_rope_kernel<64> : append_one_rope_kernel<128>;
+    return launch_dependent(kern, (unsigned)(kv_blocks + q_blocks), 128, 0, stream, p, (unsigned)kv_blocks);
+  }
+  const long long items = (a.s.rows >> a.p.shift) + 2LL * a.s.batch;
+  AppendGrid g{};
+  g.heads = 4;
+  while (g.heads > 1 && items * ((a.p.heads + g.heads - 1) / g.heads) < 3LL * sms) g.heads /= 2;
+  g.k_blocks = (unsigned)(items * ((a.p.heads + g.heads - 1) / g.heads));
+  g.v_blocks = (unsigned)(items * a.p.heads);
+  const long long q_blocks = (a.s.rows + kQueryRows - 1) / kQueryRows * q_groups;
+  const int smem = std::max(a.p.page, kQueryRows) * kRopeRow * (int)sizeof(float2);
+  const auto kern = a.p.d == 64 ? append_rope_kernel<64> : append_rope_kernel<128>;
+  const cudaError_t e = ensure_smem_limit(kern, 128 * kRopeRow * (int)sizeof(float2), g_append_smem[a.p.d == 128]);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kern, (unsigned)(g.k_blocks + g.v_blocks + q_blocks), a.p.page * a.p.d / 32, smem, stream, p, g);
 }
 
 }  // namespace kvq

@@ -7,11 +7,7 @@
 namespace kvq {
 namespace {
 
-// The positions of a row, each held inside the table (a position outside it is
-// recorded).
-struct RopeAt {
-  int p[kRopeMaxAxes];
-};
+// a row's position, held inside the table (one outside it is recorded)
 __device__ __forceinline__ int rope_position(const RopeTab& t, int p, int* status) {
   if ((unsigned)p >= (unsigned)t.n) {
     atomicCAS(status, 0, (int)KVQ_ERR_POSITION);
@@ -19,29 +15,32 @@ __device__ __forceinline__ int rope_position(const RopeTab& t, int p, int* statu
   }
   return p;
 }
-__device__ __forceinline__ RopeAt rope_at(const RopeTab& t, const int32_t* pos, long long axis_stride, int* status) {
-  RopeAt at;
-#pragma unroll
-  for (int k = 0; k < kRopeMaxAxes; ++k) at.p[k] = k < t.axes ? rope_position(t, __ldg(pos + k * axis_stride), status) : 0;
-  return at;
-}
-__device__ __forceinline__ RopeAt rope_at(const RopeTab& t, int pos, int* status) {
-  RopeAt at;
-  at.p[0] = rope_position(t, pos, status);
-#pragma unroll
-  for (int k = 1; k < kRopeMaxAxes; ++k) at.p[k] = at.p[0];
-  return at;
-}
 
-// (cos, sin) of pairs [p0, p0 + N)
-template <int N>
-__device__ __forceinline__ void rope_turn(const RopeTab& t, const RopeAt& at, int p0, bool inverse, float2 (&cs)[N]) {
+// Turns of rows in shared memory, kRopeRow numbers (cos, sin) a row: pair p stands
+// where the threads of a row's units (of 8 pairs) read 16 bytes each that are
+// neighbours, so that they meet different banks.
+constexpr int kRopeRow = kRopeMaxPairs;
+__device__ __forceinline__ int rope_slot(int p) { return ((p & 7) >> 1) * 16 + (p >> 3) * 2 + (p & 1); }
+// Fills those of `rows` rows, a pair a thread: neighbouring pairs of an axis are
+// neighbours in the table too.  pos(row, axis): a row's position.
+template <typename Pos>
+__device__ __forceinline__ void rope_stage(const RopeTab& t, float2* turns, int rows, bool inverse, int* status, Pos pos) {
+  for (int i = threadIdx.x; i < rows * kRopeRow; i += blockDim.x) {
+    const int r = i / kRopeRow, p = i % kRopeRow;
+    if (p >= t.pairs) continue;
+    const int at = rope_position(t, pos(r, (int)t.axis[p]), status);
+    float2 cs = __ldg(t.cs + (long long)at * t.pairs + p);
+    if (inverse) cs.y = -cs.y;
+    turns[r * kRopeRow + rope_slot(p)] = cs;
+  }
+}
+// the turns of unit u of a row
+__device__ __forceinline__ void rope_turns(const float2* row, int u, float2 (&cs)[8]) {
 #pragma unroll
-  for (int k = 0; k < N; ++k) {
-    const int axis = t.axis[p0 + k];
-    const int pos = axis == 0 ? at.p[0] : axis == 1 ? at.p[1] : axis == 2 ? at.p[2] : at.p[3];
-    cs[k] = __ldg(t.cs + (long long)pos * t.pairs + p0 + k);
-    if (inverse) cs[k].y = -cs[k].y;
+  for (int j = 0; j < 4; ++j) {
+    const float4 v = *reinterpret_cast<const float4*>(row + j * 16 + u * 2);
+    cs[2 * j] = make_float2(v.x, v.y);
+    cs[2 * j + 1] = make_float2(v.z, v.w);
   }
 }
 
@@ -80,8 +79,9 @@ __device__ __forceinline__ void rope_chunks(const RopeTab& t, int u, int& c0, in
   c0 = halves ? 8 * u : 16 * u;
   c1 = halves ? c0 + t.pairs : c0 + 8;
 }
-__device__ __forceinline__ void rope_apply(const RopeTab& t, const float2 (&cs)[8], uint4& a, uint4& b) {
-  float x[8], y[8], u[8], v[8];
+__device__ __forceinline__ void rope_apply(const RopeTab& t, const float2 (&cs)[8], const uint4& a, const uint4& b,
+                                           float (&u)[8], float (&v)[8]) {
+  float x[8], y[8];
   floats_of(a, x);
   floats_of(b, y);
   if (t.interleaved) {
@@ -99,8 +99,57 @@ __device__ __forceinline__ void rope_apply(const RopeTab& t, const float2 (&cs)[
       v[k] = turn_second(x[k], y[k], cs[k]);
     }
   }
-  a = bf16_of(u);
-  b = bf16_of(v);
+}
+
+// R rows of up to kRopeHeads heads of one tensor by a block: the values are asked
+// for first, then the rows' turns go through shared memory (R * kRopeRow), read
+// once for all heads.  x, y: row 0, head 0.
+constexpr int kRopeHeads = 8;
+template <int D, int R, typename Pos>
+__device__ __forceinline__ void rope_tile(const RopeTab& t, bool inverse, float2* turns, int rows, int heads,
+                                          const uint16_t* x, long long xr, long long xh, uint16_t* y, long long yr,
+                                          long long yh, int* status, Pos pos) {
+  constexpr int U = D / 16, kAll = R * kRopeHeads * U, N = R >= 16 ? 4 : 1;
+  const int step = (int)blockDim.x;
+  bool staged = false;
+  for (int i0 = threadIdx.x; i0 < kAll || !staged; i0 += N * step) {
+    uint4 v[N], w[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int i = i0 + k * step, u = i % U, r = i / U % R, h = i / (U * R);
+      if (i < kAll && r < rows && h < heads) {
+        int c0, c1;
+        rope_chunks(t, u, c0, c1);
+        const uint16_t* from = x + r * xr + h * xh;
+        v[k] = *reinterpret_cast<const uint4*>(from + c0);
+        w[k] = *reinterpret_cast<const uint4*>(from + c1);
+      }
+    }
+    if (!staged) {
+      rope_stage(t, turns, rows, inverse, status, pos);
+      __syncthreads();
+      staged = true;
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int i = i0 + k * step, u = i % U, r = i / U % R, h = i / (U * R);
+      if (i < kAll && r < rows && h < heads) {
+        int c0, c1;
+        rope_chunks(t, u, c0, c1);
+        if (u < (t.pairs >> 3)) {
+          float2 cs[8];
+          float f[8], g[8];
+          rope_turns(turns + r * kRopeRow, u, cs);
+          rope_apply(t, cs, v[k], w[k], f, g);
+          v[k] = bf16_of(f);
+          w[k] = bf16_of(g);
+        }
+        uint16_t* to = y + r * yr + h * yh;
+        *reinterpret_cast<uint4*>(to + c0) = v[k];
+        *reinterpret_cast<uint4*>(to + c1) = w[k];
+      }
+    }
+  }
 }
 
 }  // namespace

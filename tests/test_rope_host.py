@@ -138,6 +138,7 @@ def test_rope_refusals(lib):
     assert _rope(lib, rows=0) == 0 and _rope(lib, batch=0) == 0 and _rope(lib, heads=0, x=None, y=None) == 0
     assert _rope(lib, batch=1 << 16, rows=1 << 16) == kvq.KVQ_ERR_TOO_LARGE
     assert _rope(lib, rows=1 << 30, heads=64) == kvq.KVQ_ERR_TOO_LARGE
+    assert _rope(lib, rows=1, batch=1 << 30, heads=32) == kvq.KVQ_ERR_TOO_LARGE
     assert lib.kvq_rope(ctypes.byref(_table()), PTR, 0, 1, 0, 1, 1, 128, 0, None, 1, None) == 1
 
 
