@@ -37,8 +37,8 @@ __global__ void __launch_bounds__(256) rope_fill_kernel(const __grid_constant__ 
 // double the reads if every head fetched its own.  R = 4 spreads a small call over
 // the SMs, 16 leaves eight loads a thread in flight.
 template <int D, int R>
-__global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeArgs a) {
-  __shared__ __align__(16) float2 turns[R * kRopeRow];
+__global__ void __launch_bounds__(256, 4) rope_kernel(const __grid_constant__ RopeArgs a) {
+  __shared__ float4 turns[R * kRopeRow];
   ptx::grid_dependency_wait();
   ptx::launch_dependents();
   const unsigned tiles = ((unsigned)a.rows + R - 1) / R;
@@ -71,7 +71,7 @@ __device__ __forceinline__ int seq_of_row(const PageSeqs& s, int r) {
 
 // Queries beside the append, R rows and eight heads: block `at` of theirs.
 template <int D, int R>
-__device__ __forceinline__ void append_queries(const AppendRopeArgs& p, unsigned at, float2* turns) {
+__device__ __forceinline__ void append_queries(const AppendRopeArgs& p, unsigned at, float4* turns) {
   const PageSeqs& s = p.a.s;
   const unsigned groups = (unsigned)(p.q.heads + kRopeHeads - 1) / kRopeHeads;
   const int h0 = (int)(at % groups) * kRopeHeads;
@@ -109,7 +109,7 @@ __device__ __forceinline__ uint2 codes_of(const float (&v)[8], float f) {
 // for all heads; the next head's values are on their way while this one's page
 // maximum is found.
 template <int D>
-__device__ __forceinline__ void append_keys(const AppendRopeArgs& p, int item, int h0, int h1, float2* turns) {
+__device__ __forceinline__ void append_keys(const AppendRopeArgs& p, int item, int h0, int h1, float4* turns) {
   constexpr int U = D / 16;
   __shared__ uint32_t part[2][16];
   const AppendArgs& a = p.a;
@@ -152,9 +152,7 @@ __device__ __forceinline__ void append_keys(const AppendRopeArgs& p, int item, i
     for (int k = 0; k < 2; ++k) {
       const int t = tid / U + k * step;
       if (u < (p.t.pairs >> 3) && t >= lo && t < hi) {
-        float2 cs[8];
-        rope_turns(turns + (t - lo) * kRopeRow, u, cs);
-        rope_apply(p.t, cs, v[k], w[k], f[k], g[k]);
+        rope_apply(p.t, turns + (t - lo) * kRopeRow, u, v[k], w[k], f[k], g[k]);
       } else {
         floats_of(v[k], f[k]);
         floats_of(w[k], g[k]);
@@ -192,8 +190,8 @@ struct AppendGrid {
 };
 constexpr int kQueryRows = 16;
 template <int D>
-__global__ void __launch_bounds__(512) append_rope_kernel(const __grid_constant__ AppendRopeArgs p, const AppendGrid g) {
-  extern __shared__ __align__(16) float2 turns[];
+__global__ void __launch_bounds__(512, 2) append_rope_kernel(const __grid_constant__ AppendRopeArgs p, const AppendGrid g) {
+  extern __shared__ float4 turns[];
   ptx::grid_dependency_wait();
   unsigned at = blockIdx.x;
   if (at < g.k_blocks) {
@@ -218,7 +216,7 @@ constexpr int kOneRows = 4;
 template <int D>
 __global__ void __launch_bounds__(128) append_one_rope_kernel(const __grid_constant__ AppendRopeArgs p, unsigned kv_blocks) {
   constexpr int U = D / 16;
-  __shared__ __align__(16) float2 turns[kOneRows * kRopeRow];
+  __shared__ float4 turns[kOneRows * kRopeRow];   // of the block's four warps, or its query rows
   const AppendArgs& a = p.a;
   const int lane = threadIdx.x & 31;
   ptx::grid_dependency_wait();
@@ -250,15 +248,11 @@ __global__ void __launch_bounds__(128) append_one_rope_kernel(const __grid_const
   float f[8], g[8];
   floats_of(v, f);
   floats_of(y, g);
-  if (kv == 0 && lane < (p.t.pairs >> 3)) {
-    float2 cs[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int pair = 8 * lane + k;
-      const int pos = p.pos != nullptr ? __ldg(p.pos + b * p.pr + p.t.axis[pair]) : len - 1;
-      cs[k] = __ldg(p.t.cs + (long long)rope_position(p.t, pos, a.status) * p.t.pairs + pair);
-    }
-    rope_apply(p.t, cs, v, y, f, g);
+  if (kv == 0) {   // the warp's own row of turns
+    float4* row = turns + (threadIdx.x >> 5) * kRopeRow;
+    rope_stage_one(p.t, row, a.status, [&](int axis) { return p.pos != nullptr ? __ldg(p.pos + b * p.pr + axis) : len - 1; });
+    __syncwarp();
+    if (lane < (p.t.pairs >> 3)) rope_apply(p.t, row, lane, v, y, f, g);
   }
   const int id = seq_page(a.s, b, pg, a.p.n_pages, a.status);
   if (id < 0) return;
@@ -324,9 +318,9 @@ cudaError_t launch_pages_append_rope(const AppendRopeArgs& p, cudaStream_t strea
   g.k_blocks = (unsigned)(items * ((a.p.heads + g.heads - 1) / g.heads));
   g.v_blocks = (unsigned)(items * a.p.heads);
   const long long q_blocks = (a.s.rows + kQueryRows - 1) / kQueryRows * q_groups;
-  const int smem = std::max(a.p.page, kQueryRows) * kRopeRow * (int)sizeof(float2);
+  const int smem = std::max(a.p.page, kQueryRows) * kRopeRow * (int)sizeof(float4);
   const auto kern = a.p.d == 64 ? append_rope_kernel<64> : append_rope_kernel<128>;
-  const cudaError_t e = ensure_smem_limit(kern, 128 * kRopeRow * (int)sizeof(float2), g_append_smem[a.p.d == 128]);
+  const cudaError_t e = ensure_smem_limit(kern, 128 * kRopeRow * (int)sizeof(float4), g_append_smem[a.p.d == 128]);
   if (e != cudaSuccess) return e;
   return launch_dependent(kern, (unsigned)(g.k_blocks + g.v_blocks + q_blocks), a.p.page * a.p.d / 32, smem, stream, p, g);
 }
