@@ -39,7 +39,8 @@ struct AppendArgs {
 struct RopeTab {
   const float2* cs;   // [n][pairs]
   int n, pairs, axes, interleaved;
-  uint8_t axis[kRopeMaxPairs];
+  float none;         // -0
+  uint32_t axis[4];   // of each pair, two bits
 };
 
 // One tensor that is rotated, [batch][row][head][d] at strides in elements.

@@ -110,7 +110,8 @@ kvq::RopeTab rope_of(const kvq_rope_table* t) {
   o.pairs = t->pairs;
   o.axes = t->axes;
   o.interleaved = t->interleaved != 0;
-  std::copy(t->axis, t->axis + kvq::kRopeMaxPairs, o.axis);
+  o.none = -0.f;
+  for (int k = 0; k < t->pairs; ++k) o.axis[k >> 4] |= (uint32_t)t->axis[k] << (2 * (k & 15));
   return o;
 }
 

@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "kvq_append.cuh"
 #include "kvq_checks.cuh"
@@ -36,8 +37,8 @@ __global__ void __launch_bounds__(256) rope_fill_kernel(const __grid_constant__ 
 // written once and HBM bounds the large sizes; the turns, 4 bytes a channel, would
 // double the reads if every head fetched its own.  R = 4 spreads a small call over
 // the SMs, 16 leaves eight loads a thread in flight.
-template <int D, int R>
-__global__ void __launch_bounds__(256, 4) rope_kernel(const __grid_constant__ RopeArgs a) {
+template <int D, int R, bool INTER>
+__global__ void __launch_bounds__(256, 3) rope_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ float4 turns[R * kRopeRow];
   ptx::grid_dependency_wait();
   ptx::launch_dependents();
@@ -50,10 +51,11 @@ __global__ void __launch_bounds__(256, 4) rope_kernel(const __grid_constant__ Ro
   const long long b = rest / tiles;
   const bool second = g >= q_groups;
   if (second) g -= q_groups;
-  const RopeTensor& x = a.x[second ? 1 : 0];
+  RopeTensor x = a.x[0];
+  if (second) x = a.x[1];
   const int h0 = (int)g * kRopeHeads;
   const int32_t* pos = a.pos + b * a.pb + row0 * a.pr;
-  rope_tile<D, R>(a.t, a.inverse != 0, turns, min(R, a.rows - row0), min(kRopeHeads, x.heads - h0),
+  rope_tile<D, R, R / 4, INTER>(a.t, a.inverse != 0, turns, min(R, a.rows - row0), min(kRopeHeads, x.heads - h0),
                   x.x + b * x.xb + row0 * x.xr + h0 * x.xh, x.xr, x.xh, x.y + b * x.yb + row0 * x.yr + h0 * x.yh, x.yr,
                   x.yh, a.status, [&](int r, int axis) { return __ldg(pos + r * a.pr + axis * a.pa); });
 }
@@ -70,7 +72,7 @@ __device__ __forceinline__ int seq_of_row(const PageSeqs& s, int r) {
 }
 
 // Queries beside the append, R rows and eight heads: block `at` of theirs.
-template <int D, int R>
+template <int D, int R, int N, bool INTER>
 __device__ __forceinline__ void append_queries(const AppendRopeArgs& p, unsigned at, float4* turns) {
   const PageSeqs& s = p.a.s;
   const unsigned groups = (unsigned)(p.q.heads + kRopeHeads - 1) / kRopeHeads;
@@ -90,25 +92,29 @@ __device__ __forceinline__ void append_queries(const AppendRopeArgs& p, unsigned
     }
     return seq_len(s, b, p.a.p.shift, p.a.status) - (next - (row0 + r));
   };
-  rope_tile<D, R>(p.t, false, turns, end - row0, min(kRopeHeads, p.q.heads - h0), p.q.x + row0 * p.q.xr + h0 * p.q.xh,
+  rope_tile<D, R, N, INTER>(p.t, false, turns, end - row0, min(kRopeHeads, p.q.heads - h0), p.q.x + row0 * p.q.xr + h0 * p.q.xh,
                   p.q.xr, p.q.xh, p.q.y + row0 * p.q.yr + h0 * p.q.yh, p.q.yr, p.q.yh, p.a.status, place);
 }
 
-__device__ __forceinline__ uint32_t max_abs_bits(const float (&f)[8]) {
-  uint32_t m = 0;
+// largest magnitude of m and 16 values, a NaN before all
+__device__ __forceinline__ float most_of(float m, const float (&f)[8], const float (&g)[8]) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(f[k]) & 0x7fffffffu);
+  for (int k = 0; k < 8; ++k) asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(f[k]), "f"(g[k]));
   return m;
 }
 __device__ __forceinline__ uint2 codes_of(const float (&v)[8], float f) {
-  return make_uint2(e4m3x4(v[0] * f, v[1] * f, v[2] * f, v[3] * f), e4m3x4(v[4] * f, v[5] * f, v[6] * f, v[7] * f));
+  const uint64_t f2 = ptx::f2_pack(f, f);
+  float x[8];
+#pragma unroll
+  for (int k = 0; k < 8; k += 2) ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(v[k], v[k + 1]), f2), x[k], x[k + 1]);
+  return make_uint2(e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7]));
 }
 
 // One page of keys, heads [h0, h1), by a block of page * D / 32 threads: two units
 // of 16 channels a thread and head.  The page's turns go to shared memory once
 // for all heads; the next head's values are on their way while this one's page
 // maximum is found.
-template <int D>
+template <int D, bool INTER>
 __device__ __forceinline__ void append_keys(const AppendRopeArgs& p, int item, int h0, int h1, float4* turns) {
   constexpr int U = D / 16;
   __shared__ uint32_t part[2][16];
@@ -147,20 +153,22 @@ __device__ __forceinline__ void append_keys(const AppendRopeArgs& p, int item, i
     uint8_t* codes = a.p.codes[0] + blk * a.p.page * D;
     const int old = lo > 0 ? scale_exp(a.p.scale[0][blk]) : kPageExpMin;
     float f[2][8], g[2][8];
-    uint32_t m = 0;
+    float most = 0.f;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int t = tid / U + k * step;
       if (u < (p.t.pairs >> 3) && t >= lo && t < hi) {
-        rope_apply(p.t, turns + (t - lo) * kRopeRow, u, v[k], w[k], f[k], g[k]);
+        float4 cs[4];
+        rope_entries(turns + (t - lo) * kRopeRow, u, cs);
+        rope_apply<INTER>(p.t, cs, v[k], w[k], f[k], g[k]);
       } else {
         floats_of(v[k], f[k]);
         floats_of(w[k], g[k]);
       }
-      m = max(m, max(max_abs_bits(f[k]), max_abs_bits(g[k])));
+      most = most_of(most, f[k], g[k]);
     }
     if (h + 1 < h1) load(h + 1);
-    m = __reduce_max_sync(0xffffffffu, m);
+    uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
     if (blockDim.x > 32) {   // (two buffers: a head's is read while the next one's is written)
       uint32_t* mine = part[(h - h0) & 1];
       if (lane == 0) mine[tid >> 5] = m;
@@ -186,10 +194,10 @@ __device__ __forceinline__ void append_keys(const AppendRopeArgs& p, int item, i
 // and head), of query rows.
 struct AppendGrid {
   unsigned k_blocks, v_blocks;
-  int heads;   // per block of keys
+  int heads;    // per block of keys
+  int q_rows;   // per block of query rows
 };
-constexpr int kQueryRows = 16;
-template <int D>
+template <int D, bool INTER>
 __global__ void __launch_bounds__(512, 2) append_rope_kernel(const __grid_constant__ AppendRopeArgs p, const AppendGrid g) {
   extern __shared__ float4 turns[];
   ptx::grid_dependency_wait();
@@ -197,7 +205,7 @@ __global__ void __launch_bounds__(512, 2) append_rope_kernel(const __grid_consta
   if (at < g.k_blocks) {
     const unsigned groups = (unsigned)(p.a.p.heads + g.heads - 1) / (unsigned)g.heads;
     const int h0 = (int)(at % groups) * g.heads;
-    append_keys<D>(p, (int)(at / groups), h0, min(h0 + g.heads, p.a.p.heads), turns);
+    append_keys<D, INTER>(p, (int)(at / groups), h0, min(h0 + g.heads, p.a.p.heads), turns);
     return;
   }
   at -= g.k_blocks;
@@ -205,7 +213,9 @@ __global__ void __launch_bounds__(512, 2) append_rope_kernel(const __grid_consta
     append_page<D>(p.a, 1, (int)(at % (unsigned)p.a.p.heads), (int)(at / (unsigned)p.a.p.heads));
     return;
   }
-  append_queries<D, kQueryRows>(p, at - g.v_blocks, turns);
+  // (a page of 16 tokens has too few threads for 16 rows)
+  if (g.q_rows == 16) append_queries<D, 16, 2, INTER>(p, at - g.v_blocks, turns);
+  else append_queries<D, 4, 2, INTER>(p, at - g.v_blocks, turns);
 }
 
 // One token of every sequence: a warp per sequence, head and K or V, half the lanes
@@ -213,7 +223,7 @@ __global__ void __launch_bounds__(512, 2) append_rope_kernel(const __grid_consta
 // the chain of dependent loads: length, position, then turns beside table entry
 // and scale.
 constexpr int kOneRows = 4;
-template <int D>
+template <int D, bool INTER>
 __global__ void __launch_bounds__(128) append_one_rope_kernel(const __grid_constant__ AppendRopeArgs p, unsigned kv_blocks) {
   constexpr int U = D / 16;
   __shared__ float4 turns[kOneRows * kRopeRow];   // of the block's four warps, or its query rows
@@ -222,7 +232,7 @@ __global__ void __launch_bounds__(128) append_one_rope_kernel(const __grid_const
   ptx::grid_dependency_wait();
   ptx::launch_dependents();
   if (blockIdx.x >= kv_blocks) {
-    append_queries<D, kOneRows>(p, blockIdx.x - kv_blocks, turns);
+    append_queries<D, kOneRows, 2, INTER>(p, blockIdx.x - kv_blocks, turns);
     return;
   }
   const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
@@ -252,7 +262,11 @@ __global__ void __launch_bounds__(128) append_one_rope_kernel(const __grid_const
     float4* row = turns + (threadIdx.x >> 5) * kRopeRow;
     rope_stage_one(p.t, row, a.status, [&](int axis) { return p.pos != nullptr ? __ldg(p.pos + b * p.pr + axis) : len - 1; });
     __syncwarp();
-    if (lane < (p.t.pairs >> 3)) rope_apply(p.t, row, lane, v, y, f, g);
+    if (lane < (p.t.pairs >> 3)) {
+      float4 cs[4];
+      rope_entries(row, lane, cs);
+      rope_apply<INTER>(p.t, cs, v, y, f, g);
+    }
   }
   const int id = seq_page(a.s, b, pg, a.p.n_pages, a.status);
   if (id < 0) return;
@@ -260,7 +274,7 @@ __global__ void __launch_bounds__(128) append_one_rope_kernel(const __grid_const
   if (!KVQ_IN_BOUNDS(blk, (long long)a.p.n_pages * a.p.heads, a.status, a.bounds_site)) return;
   uint8_t* codes = a.p.codes[kv] + blk * a.p.page * D;
   const int old = t > 0 ? scale_exp(a.p.scale[kv][blk]) : kPageExpMin;
-  const uint32_t m = __reduce_max_sync(0xffffffffu, max(max_abs_bits(f), max_abs_bits(g)));
+  const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(most_of(0.f, f, g)));
   const int e = max(scale_of(__uint_as_float(m), a.status), old);
   if (t > 0 && e > old) rescale_codes<D>(codes, t, old - e, lane, 32);
   if (lane == 0 && (t == 0 || e > old)) a.p.scale[kv][blk] = scale_bits(e);
@@ -270,7 +284,7 @@ __global__ void __launch_bounds__(128) append_one_rope_kernel(const __grid_const
   }
 }
 
-std::atomic<uint64_t> g_append_smem[2];
+std::atomic<uint64_t> g_append_smem[2][2];
 
 }  // namespace
 
@@ -295,8 +309,12 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream) {
   auto blocks = [&](int rows) { return (long long)a.batch * ((a.rows + rows - 1) / rows) * groups; };
   // few rows: four a block, as long as those do not fill the GPU twice
   const bool few = blocks(4) <= 16LL * sms;
-  const auto kern = few ? (a.d == 64 ? rope_kernel<64, 4> : rope_kernel<128, 4>)
-                        : (a.d == 64 ? rope_kernel<64, 16> : rope_kernel<128, 16>);
+  auto pick = [&](auto inter) {
+    constexpr bool I = decltype(inter)::value;
+    return few ? (a.d == 64 ? rope_kernel<64, 4, I> : rope_kernel<128, 4, I>)
+               : (a.d == 64 ? rope_kernel<64, 16, I> : rope_kernel<128, 16, I>);
+  };
+  const auto kern = a.t.interleaved ? pick(std::true_type{}) : pick(std::false_type{});
   return launch_dependent(kern, (unsigned)blocks(few ? 4 : 16), 256, 0, stream, a);
 }
 
@@ -308,7 +326,11 @@ cudaError_t launch_pages_append_rope(const AppendRopeArgs& p, cudaStream_t strea
   if (a.s.offsets == nullptr) {
     const long long kv_blocks = ((long long)a.s.batch * a.p.heads * 2 + 3) / 4;
     const long long q_blocks = (a.s.rows + kOneRows - 1) / kOneRows * q_groups;
-    const auto kern = a.p.d == 64 ? append_one_rope_kernel<64> : append_one_rope_kernel<128>;
+    auto pick = [&](auto inter) {
+      constexpr bool I = decltype(inter)::value;
+      return a.p.d == 64 ? append_one_rope_kernel<64, I> : append_one_rope_kernel<128, I>;
+    };
+    const auto kern = p.t.interleaved ? pick(std::true_type{}) : pick(std::false_type{});
     return launch_dependent(kern, (unsigned)(kv_blocks + q_blocks), 128, 0, stream, p, (unsigned)kv_blocks);
   }
   const long long items = (a.s.rows >> a.p.shift) + 2LL * a.s.batch;
@@ -317,10 +339,15 @@ cudaError_t launch_pages_append_rope(const AppendRopeArgs& p, cudaStream_t strea
   while (g.heads > 1 && items * ((a.p.heads + g.heads - 1) / g.heads) < 3LL * sms) g.heads /= 2;
   g.k_blocks = (unsigned)(items * ((a.p.heads + g.heads - 1) / g.heads));
   g.v_blocks = (unsigned)(items * a.p.heads);
-  const long long q_blocks = (a.s.rows + kQueryRows - 1) / kQueryRows * q_groups;
-  const int smem = std::max(a.p.page, kQueryRows) * kRopeRow * (int)sizeof(float4);
-  const auto kern = a.p.d == 64 ? append_rope_kernel<64> : append_rope_kernel<128>;
-  const cudaError_t e = ensure_smem_limit(kern, 128 * kRopeRow * (int)sizeof(float4), g_append_smem[a.p.d == 128]);
+  g.q_rows = a.p.page == 16 ? 4 : 16;
+  const long long q_blocks = (a.s.rows + g.q_rows - 1) / g.q_rows * q_groups;
+  const int smem = a.p.page * kRopeRow * (int)sizeof(float4);
+  auto pick = [&](auto inter) {
+    constexpr bool I = decltype(inter)::value;
+    return a.p.d == 64 ? append_rope_kernel<64, I> : append_rope_kernel<128, I>;
+  };
+  const auto kern = p.t.interleaved ? pick(std::true_type{}) : pick(std::false_type{});
+  const cudaError_t e = ensure_smem_limit(kern, 128 * kRopeRow * (int)sizeof(float4), g_append_smem[a.p.d == 128][p.t.interleaved]);
   if (e != cudaSuccess) return e;
   return launch_dependent(kern, (unsigned)(g.k_blocks + g.v_blocks + q_blocks), a.p.page * a.p.d / 32, smem, stream, p, g);
 }

@@ -7,6 +7,12 @@
 namespace kvq {
 namespace {
 
+// the axis of pair p.  (By selection: an address among the kernel's parameters that
+// each lane computes for itself is a slow load.)
+__device__ __forceinline__ int rope_axis(const RopeTab& t, int p) {
+  const uint32_t w = p < 32 ? (p < 16 ? t.axis[0] : t.axis[1]) : (p < 48 ? t.axis[2] : t.axis[3]);
+  return (int)((w >> (2 * (p & 15))) & 3u);
+}
 // a row's position, held inside the table (one outside it is recorded)
 __device__ __forceinline__ int rope_position(const RopeTab& t, int p, int* status) {
   if ((unsigned)p >= (unsigned)t.n) {
@@ -27,7 +33,7 @@ template <typename Pos>
 __device__ __forceinline__ void rope_stage_one(const RopeTab& t, float4* row, int* status, Pos pos, bool inverse = false) {
   const int e = threadIdx.x & 31, p = 2 * e;
   if (p >= t.pairs) return;
-  const int axis0 = t.axis[p], axis1 = t.axis[p + 1];
+  const int axis0 = rope_axis(t, p), axis1 = rope_axis(t, p + 1);
   const float2* from = t.cs + (long long)rope_position(t, pos(axis0), status) * t.pairs + p;
   float4 v;   // cos, sin, cos, sin
   if (axis0 == axis1) {
@@ -63,18 +69,15 @@ __device__ __forceinline__ uint4 bf16_of(const float (&f)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Two pairs: x0, x1 their first and second channels.  Each product and sum is
+// Two pairs: a, b their first and second channels.  Each product and sum is
 // rounded by itself: the bits are those of the formula evaluated step by step in
-// fp32, whatever else a kernel does around it.  (Products on pairs would be fused
-// with the sums behind them, and rounded once.)
-__device__ __forceinline__ void turn_pairs(float (&x0)[2], float (&x1)[2], const float4& cs) {
-  const float c[2] = {cs.x, cs.y}, s[2] = {cs.z, cs.w};
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float a = x0[i], b = x1[i];
-    x0[i] = __fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(b, s[i]));
-    x1[i] = __fadd_rn(__fmul_rn(b, c[i]), __fmul_rn(a, s[i]));
-  }
+// fp32, whatever else a kernel does around it.  The products are fused with a -0
+// that the compiler does not know (`none` of the call's table): it would make a
+// plain product on pairs and the sum behind it one operation, rounded once.
+__device__ __forceinline__ void turn_pairs(uint64_t a, uint64_t b, const float4& cs, uint64_t none, uint64_t& y0, uint64_t& y1) {
+  const uint64_t c = ptx::f2_pack(cs.x, cs.y), s = ptx::f2_pack(cs.z, cs.w);
+  y0 = ptx::f2_sub(ptx::f2_fma(a, c, none), ptx::f2_fma(b, s, none));
+  y1 = ptx::f2_add(ptx::f2_fma(b, c, none), ptx::f2_fma(a, s, none));
 }
 
 // 16 channels of a row, unit u of d / 16: where u < pairs / 8, the channels of
@@ -85,50 +88,65 @@ __device__ __forceinline__ void rope_chunks(const RopeTab& t, int u, int& c0, in
   c0 = halves ? 8 * u : 16 * u;
   c1 = halves ? c0 + t.pairs : c0 + 8;
 }
-// The unit's chunks a, b as fp32 f, g, rotated by the row's turns.
-__device__ __forceinline__ void rope_apply(const RopeTab& t, const float4* row, int u, const uint4& a, const uint4& b,
+// The unit's chunks a, b as fp32 f, g, rotated by its entries of the row's turns.
+// Interleaved pairs are the words of the chunks, the others a word of each.
+template <bool INTER>
+__device__ __forceinline__ void rope_apply(const RopeTab& t, const float4 (&cs)[4], const uint4& a, const uint4& b,
                                            float (&f)[8], float (&g)[8]) {
-  floats_of(a, f);
-  floats_of(b, g);
-  if (t.interleaved) {
+  const uint64_t none = ptx::f2_pack(t.none, t.none);
+  const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
+  auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
+  auto hi = [](uint32_t w) { return __uint_as_float(w & 0xffff0000u); };
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float(&z)[8] = j < 2 ? f : g;
-      const int k = 4 * (j & 1);
-      float x0[2] = {z[k], z[k + 2]}, x1[2] = {z[k + 1], z[k + 3]};
-      turn_pairs(x0, x1, row[rope_slot(u, j)]);
-      z[k] = x0[0], z[k + 2] = x0[1], z[k + 1] = x1[0], z[k + 3] = x1[1];
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float x0[2] = {f[2 * j], f[2 * j + 1]}, x1[2] = {g[2 * j], g[2 * j + 1]};
-      turn_pairs(x0, x1, row[rope_slot(u, j)]);
-      f[2 * j] = x0[0], f[2 * j + 1] = x0[1], g[2 * j] = x1[0], g[2 * j + 1] = x1[1];
+  for (int j = 0; j < 4; ++j) {
+    uint64_t y0, y1;
+    if (INTER) {
+      const uint32_t w0 = j < 2 ? wa[2 * j] : wb[2 * j - 4], w1 = j < 2 ? wa[2 * j + 1] : wb[2 * j - 3];
+      turn_pairs(ptx::f2_pack(lo(w0), lo(w1)), ptx::f2_pack(hi(w0), hi(w1)), cs[j], none, y0, y1);
+      if (j < 2) {
+        ptx::f2_unpack(y0, f[4 * j], f[4 * j + 2]);
+        ptx::f2_unpack(y1, f[4 * j + 1], f[4 * j + 3]);
+      } else {
+        ptx::f2_unpack(y0, g[4 * j - 8], g[4 * j - 6]);
+        ptx::f2_unpack(y1, g[4 * j - 7], g[4 * j - 5]);
+      }
+    } else {
+      turn_pairs(ptx::f2_pack(lo(wa[j]), hi(wa[j])), ptx::f2_pack(lo(wb[j]), hi(wb[j])), cs[j], none, y0, y1);
+      ptx::f2_unpack(y0, f[2 * j], f[2 * j + 1]);
+      ptx::f2_unpack(y1, g[2 * j], g[2 * j + 1]);
     }
   }
 }
+__device__ __forceinline__ void rope_entries(const float4* row, int u, float4 (&cs)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) cs[j] = row[rope_slot(u, j)];
+}
 
-// R rows of up to kRopeHeads heads of one tensor by a block: the values are asked
-// for first, then the rows' turns go through shared memory (R * kRopeRow), read
-// once for all heads.  x, y: row 0, head 0.
+// R rows of up to kRopeHeads heads of one tensor by a block, whose threads are a
+// multiple of R * D / 16: a thread has one unit of one row, of N heads at a time.
+// The values are asked for first, then the rows' turns go through shared memory
+// (R * kRopeRow), read once for all heads.  x, y: row 0, head 0.
 constexpr int kRopeHeads = 8;
-template <int D, int R, typename Pos>
+template <int D, int R, int N, bool INTER, typename Pos>
 __device__ __forceinline__ void rope_tile(const RopeTab& t, bool inverse, float4* turns, int rows, int heads,
                                           const uint16_t* x, long long xr, long long xh, uint16_t* y, long long yr,
                                           long long yh, int* status, Pos pos) {
-  constexpr int U = D / 16, kAll = R * kRopeHeads * U, N = R >= 16 ? 4 : 1;
-  const int step = (int)blockDim.x;
+  constexpr int U = D / 16;
+  const int u = threadIdx.x % U, r = threadIdx.x / U % R, step = blockDim.x / (R * U);
+  const bool live = r < rows, turned = u < (t.pairs >> 3);
+  int c0, c1;
+  rope_chunks(t, u, c0, c1);
+  x += r * xr;
+  y += r * yr;
+  float4 cs[4];
   bool staged = false;
-  for (int i0 = threadIdx.x; i0 < kAll || !staged; i0 += N * step) {
+  for (int h0 = threadIdx.x / (R * U); h0 < heads || !staged; h0 += N * step) {
     uint4 v[N], w[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      const int i = i0 + k * step, u = i % U, r = i / U % R, h = i / (U * R);
-      if (i < kAll && r < rows && h < heads) {
-        int c0, c1;
-        rope_chunks(t, u, c0, c1);
-        const uint16_t* from = x + r * xr + h * xh;
+      const int h = h0 + k * step;
+      if (live && h < heads) {
+        const uint16_t* from = x + h * xh;
         v[k] = *reinterpret_cast<const uint4*>(from + c0);
         w[k] = *reinterpret_cast<const uint4*>(from + c1);
       }
@@ -137,20 +155,19 @@ __device__ __forceinline__ void rope_tile(const RopeTab& t, bool inverse, float4
       rope_stage(t, turns, rows, inverse, status, pos);
       __syncthreads();
       staged = true;
+      if (live && turned) rope_entries(turns + r * kRopeRow, u, cs);
     }
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      const int i = i0 + k * step, u = i % U, r = i / U % R, h = i / (U * R);
-      if (i < kAll && r < rows && h < heads) {
-        int c0, c1;
-        rope_chunks(t, u, c0, c1);
-        if (u < (t.pairs >> 3)) {
+      const int h = h0 + k * step;
+      if (live && h < heads) {
+        if (turned) {
           float f[8], g[8];
-          rope_apply(t, turns + r * kRopeRow, u, v[k], w[k], f, g);
+          rope_apply<INTER>(t, cs, v[k], w[k], f, g);
           v[k] = bf16_of(f);
           w[k] = bf16_of(g);
         }
-        uint16_t* to = y + r * yr + h * yh;
+        uint16_t* to = y + h * yh;
         *reinterpret_cast<uint4*>(to + c0) = v[k];
         *reinterpret_cast<uint4*>(to + c1) = w[k];
       }
