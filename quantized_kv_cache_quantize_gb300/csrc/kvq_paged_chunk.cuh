@@ -50,6 +50,8 @@
 
 #include <math_constants.h>
 
+#include <type_traits>
+
 #include "kvq_checks.cuh"
 #include "kvq_pages.cuh"
 #include "kvq_scores.cuh"
@@ -745,18 +747,26 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
             uint32_t cur[64];
             float most;
             ptx::tmem_ld64_max(t_h, cur, most);
-            const float s0 = lds_f(mh), ck = cq * s0;
-            low = __all_sync(0xffffffffu, most * ck <= kLowX && ck <= kLowMost && lds_f(mh + 4) == s0 && lds_f(mh + 8) == s0 &&
-                                              lds_f(mh + 12) == s0);
-            if (low) {
-              const LowCap lc = low_cap(ck, shape.cap2);
+            float ck[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                float b;
-                exp_low_block(cur + 16 * k, lc, lds_f(mh + kMetaShift + 4 * k) - m, pk[k >> 1] + 8 * (k & 1), b);
-                hat += b;
-                sum = fmaf(b, lds_f(mh + kMetaInv + 4 * k), sum);
-              }
+            for (int k = 0; k < 4; ++k) ck[k] = cq * lds_f(mh + 4 * k);
+            const float ck_most = fmaxf(fmaxf(ck[0], ck[1]), fmaxf(ck[2], ck[3]));
+            low = __all_sync(0xffffffffu, most * ck_most <= kLowX && ck_most <= kLowMost);
+            if (low) {
+              auto all_four = [&](auto one_scale) {
+                LowCap lc = low_cap(ck[0], shape.cap2);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  if (!decltype(one_scale)::value && k > 0) lc = low_cap(ck[k], shape.cap2);
+                  float b;
+                  exp_low_block(cur + 16 * k, lc, lds_f(mh + kMetaShift + 4 * k) - m, pk[k >> 1] + 8 * (k & 1), b);
+                  hat += b;
+                  sum = fmaf(b, lds_f(mh + kMetaInv + 4 * k), sum);
+                }
+              };
+              // (pages of 64 tokens and more have one scale for all)
+              if (ck[1] == ck[0] && ck[2] == ck[0] && ck[3] == ck[0]) all_four(std::true_type{});
+              else all_four(std::false_type{});
             }
           }
           if (low && !__any_sync(0xffffffffu, hat > 32768.0f)) {

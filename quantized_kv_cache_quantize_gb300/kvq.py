@@ -10,6 +10,7 @@ import ctypes
 import functools
 import math
 import os
+import struct
 import threading
 
 import numpy as np
@@ -116,7 +117,10 @@ class ScoresStruct(ctypes.Structure):
     ]
 
 
-_RopeTensors = RopeTensorStruct * 2
+# one and two kvq_rope_tensor, packed (a call is short enough for the structure
+# to show); the layouts are RopeTensorStruct's
+_rope_tensor = struct.Struct("@PPqqqqqqi4x").pack
+_rope_tensors = struct.Struct("@" + "PPqqqqqqi4x" * 2).pack
 _P = ctypes.c_void_p
 _SIGNATURES = {
     "kvq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -700,7 +704,7 @@ class RopeTable:
         c.axes, c.interleaved = axes, 1 if interleaved else 0
         for p, a in enumerate(axis):
             c.axis[p] = a
-        self.cos_sin, self.struct, self.device = cos_sin, c, cos_sin.device
+        self.cos_sin, self.struct, self.device, self.index = cos_sin, c, cos_sin.device, cos_sin.get_device()
         self.n_positions, self.pairs, self.axes, self.interleaved = n_positions, pairs, axes, bool(interleaved)
         self._at = ctypes.addressof(c)
 
@@ -721,21 +725,34 @@ class RopeTable:
         return t
 
 
-def _rope_view(t: torch.Tensor, name: str, like: torch.Tensor | None = None) -> tuple:
-    """(batch, rows, heads, d) and the strides of (batch, row, head) of [rows,
-    heads, d] or [batch, heads, rows, d]; BF16, the channels contiguous."""
+def _rope_view(t: torch.Tensor, name: str, index: int) -> tuple:
+    """(batch, rows, heads, d, strides of batch, row and head) of [rows, heads, d]
+    or [batch, heads, rows, d]: BF16, the channels contiguous, on device
+    ``index``."""
     shape, st = t.shape, t.stride()
-    if len(shape) not in (3, 4):
-        raise ValueError(f"{name} must have shape [rows, heads, d] or [batch, heads, rows, d], got {list(shape)}")
-    if t.dtype is not torch.bfloat16 or not t.is_cuda or (st[-1] != 1 and t.numel() > 0):
-        raise ValueError(f"{name} must be a CUDA bfloat16 tensor with contiguous channels")
-    if like is not None and (shape != like.shape or t.device != like.device):
-        raise ValueError(f"{name} must be a tensor {list(like.shape)} on {like.device}, got {list(shape)} on {t.device}")
-    if like is not None and any(n > 1 and s == 0 for n, s in zip(shape, st)):
-        raise ValueError(f"{name} must not repeat memory (strides {list(st)})")
     if len(shape) == 3:
-        return (1, shape[0], shape[1], shape[2]), (0, st[0], st[1])
-    return (shape[0], shape[2], shape[1], shape[3]), (st[0], st[2], st[1])
+        rows, heads, d = shape
+        view = (1, rows, heads, d, 0, st[0], st[1])
+    elif len(shape) == 4:
+        batch, heads, rows, d = shape
+        view = (batch, rows, heads, d, st[0], st[2], st[1])
+    else:
+        raise ValueError(f"{name} must have shape [rows, heads, d] or [batch, heads, rows, d], got {list(shape)}")
+    if t.dtype is not torch.bfloat16 or (st[-1] != 1 and t.numel() > 0) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA bfloat16 tensor with contiguous channels")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the table on cuda:{index}")
+    return view
+
+
+def _rope_out(t: torch.Tensor, name: str, like: torch.Tensor, index: int) -> tuple:
+    """Strides of batch, row and head of a given output."""
+    view = _rope_view(t, name, index)
+    if t.shape != like.shape:
+        raise ValueError(f"{name} must have shape {list(like.shape)}, got {list(t.shape)}")
+    if any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
+        raise ValueError(f"{name} must not repeat memory (strides {list(t.stride())})")
+    return view[4:]
 
 
 def rope(table: RopeTable, q: torch.Tensor, positions: torch.Tensor, k: torch.Tensor | None = None, q_out=None,
@@ -745,48 +762,47 @@ def rope(table: RopeTable, q: torch.Tensor, positions: torch.Tensor, k: torch.Te
     [rows, axes] ([rows] with one axis), for four dimensions shared by the
     batch, or [batch, rows, axes].  q_out, k_out: where to write (q itself for
     in place).  Returns the rotated q, with k the pair."""
-    shape, qs = _rope_view(q, "q")
-    batch, rows, heads, d = shape
-    dev = q.device
-    if table.device != dev:
-        raise ValueError(f"the table is on {table.device}, q on {dev}")
-    kshape = ks = None
+    index, axes = table.index, table.axes
+    batch, rows, heads, d, qb, qr, qh = _rope_view(q, "q", index)
+    four = q.dim() == 4
     if k is not None:
-        kshape, ks = _rope_view(k, "k")
-        if k.dim() != q.dim() or kshape[:2] != shape[:2] or kshape[3] != d or k.device != dev:
-            raise ValueError(f"k must be like q {list(q.shape)} but for its heads, got {list(k.shape)} on {k.device}")
+        k_batch, k_rows, k_heads, k_d, kb, kr, kh = _rope_view(k, "k", index)
+        if (k_batch, k_rows, k_d) != (batch, rows, d) or (k.dim() == 4) != four:
+            raise ValueError(f"k must be like q {list(q.shape)} but for its heads, got {list(k.shape)}")
     elif k_out is not None:
         raise ValueError("k_out without k")
-    if positions.dtype is not torch.int32 or positions.device != dev:
-        raise ValueError(f"positions must be an int32 tensor on {dev}, got {positions.dtype} on {positions.device}")
-    pshape, ps = positions.shape, positions.stride()
-    if table.axes == 1 and pshape == (rows,):
-        pos = (0, ps[0], 0)
-    elif pshape == (rows, table.axes):
-        pos = (0, ps[0], ps[1])
-    elif q.dim() == 4 and pshape == (batch, rows, table.axes):
-        pos = ps
+    shape, st = positions.shape, positions.stride()
+    if positions.dtype is not torch.int32 or positions.get_device() != index:
+        raise ValueError(f"positions must be an int32 tensor on cuda:{index}, got {positions.dtype} on {positions.device}")
+    if shape == (rows, axes):
+        pb, pr, pa = 0, st[0], st[1]
+    elif axes == 1 and shape == (rows,):
+        pb, pr, pa = 0, st[0], 0
+    elif four and shape == (batch, rows, axes):
+        pb, pr, pa = st
     else:
-        raise ValueError(f"positions must have shape [{rows}, {table.axes}]"
-                         + (f" or [{batch}, {rows}, {table.axes}]" if q.dim() == 4 else "") + f", got {list(pshape)}")
+        raise ValueError(f"positions must have shape [{rows}, {axes}]"
+                         + (f" or [{batch}, {rows}, {axes}]" if four else "") + f", got {list(shape)}")
+    dev = table.device
     handle = _handle(stream, dev)
     with _switch(dev, stream):
         if q_out is None:
             q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+            ob, orow, oh = (heads * rows * d, d, rows * d) if four else (0, heads * d, d)
         else:
-            _rope_view(q_out, "q_out", q)
-        _, qo = _rope_view(q_out, "q_out")
-        t = _RopeTensors()
-        t[0] = RopeTensorStruct(q.data_ptr(), q_out.data_ptr(), *qs, *qo, heads)
-        if k is not None:
+            ob, orow, oh = _rope_out(q_out, "q_out", q, index)
+        at = (q.data_ptr(), q_out.data_ptr(), qb, qr, qh, ob, orow, oh, heads)
+        if k is None:
+            tensors, n = _rope_tensor(*at), 1
+        else:
             if k_out is None:
                 k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
+                ob, orow, oh = (k_heads * rows * d, d, rows * d) if four else (0, k_heads * d, d)
             else:
-                _rope_view(k_out, "k_out", k)
-            _, ko = _rope_view(k_out, "k_out")
-            t[1] = RopeTensorStruct(k.data_ptr(), k_out.data_ptr(), *ks, *ko, kshape[2])
-        _check(lib().kvq_rope(table._at, positions.data_ptr(), *pos, batch, rows, d, 1 if inverse else 0,
-                              ctypes.addressof(t), 1 if k is None else 2, handle), "kvq_rope")
+                ob, orow, oh = _rope_out(k_out, "k_out", k, index)
+            tensors, n = _rope_tensors(*at, k.data_ptr(), k_out.data_ptr(), kb, kr, kh, ob, orow, oh, k_heads), 2
+        _check(lib().kvq_rope(table._at, positions.data_ptr(), pb, pr, pa, batch, rows, d, 1 if inverse else 0,
+                              tensors, n, handle), "kvq_rope")
     return q_out if k is None else (q_out, k_out)
 
 
@@ -804,36 +820,37 @@ def pages_append_rope(cache: PagedCache, table: RopeTable, k_new: torch.Tensor, 
     if shape != shape_v or shape[1] != cache.kv_heads:
         raise ValueError(f"k_new and v_new must have shape [rows, {cache.kv_heads}, "
                          f"{cache.head_dim}], got {list(shape)} and {list(shape_v)}")
-    dev, rows = cache.device, shape[0]
+    dev, rows, axes = cache.device, shape[0], table.axes
     if table.device != dev:
         raise ValueError(f"the table is on {table.device}, the cache on {dev}")
     s = _sequences(cache, rows, block_table, kv_lens, offsets)
     pos_at, pos_stride = None, 0
     if positions is not None:
-        pshape = positions.shape
+        at = positions.shape
         if (positions.dtype is not torch.int32 or positions.device != dev
-                or not (pshape == (rows, table.axes) or (table.axes == 1 and pshape == (rows,)))):
-            raise ValueError(f"positions must be an int32 tensor [{rows}, {table.axes}] on {dev}, got "
-                             f"{positions.dtype} {list(pshape)} on {positions.device}")
-        if table.axes > 1 and positions.stride(1) != 1 and rows > 0:
+                or not (at == (rows, axes) or (axes == 1 and at == (rows,)))):
+            raise ValueError(f"positions must be an int32 tensor [{rows}, {axes}] on {dev}, got "
+                             f"{positions.dtype} {list(at)} on {positions.device}")
+        if axes > 1 and positions.stride(1) != 1 and rows > 0:
             raise ValueError("positions must be contiguous in their last dimension")
         pos_at, pos_stride = positions.data_ptr(), positions.stride(0)
-    elif table.axes != 1:
-        raise ValueError(f"positions of {table.axes} axes must be given")
+    elif axes != 1:
+        raise ValueError(f"positions of {axes} axes must be given")
     handle = _handle(stream, dev)
     with _switch(dev, stream):
         query = (None, 0, 0, 0, None, 0, 0)
         if q is not None:
-            qshape, qs = _paged_rows(cache, q, "q")
-            if qshape[0] != rows or qshape[1] < 1:
-                raise ValueError(f"q must have {rows} rows and heads, got {list(qshape)}")
+            at, qs = _paged_rows(cache, q, "q")
+            heads = at[1]
+            if at[0] != rows or heads < 1:
+                raise ValueError(f"q must have {rows} rows and heads, got {list(at)}")
             if q_out is None:
-                q_out = torch.empty(qshape, dtype=torch.bfloat16, device=dev)
+                q_out = torch.empty(at, dtype=torch.bfloat16, device=dev)
+                out_row, out_head = heads * at[2], at[2]
             else:
-                _rope_view(q_out, "q_out", q)
-            qo = q_out.stride()
+                _, out_row, out_head = _rope_out(q_out, "q_out", q, table.index)
             if rows > 0:   # (an empty tensor has no address)
-                query = (q.data_ptr(), qs[0], qs[1], qshape[1], q_out.data_ptr(), qo[0], qo[1])
+                query = (q.data_ptr(), qs[0], qs[1], heads, q_out.data_ptr(), out_row, out_head)
         elif q_out is not None:
             raise ValueError("q_out without q")
         _check(lib().kvq_pages_append_rope(

@@ -202,3 +202,11 @@ def test_binding_refuses_host_tensors(lib):
         kvq.pages_append_rope(cache, t, x, x, table, lens)
     with pytest.raises(ValueError, match="beyond 32 bits"):
         kvq.pages_append_rope(cache, t, x, x, table, lens, layer=1 << 32)
+
+
+def test_packed_tensors_are_the_structure():
+    """The binding packs kvq_rope_tensor by hand; ctypes' copy of it, which is
+    checked against the header above, has the same bytes."""
+    a, b = tuple(range(1, 10)), tuple(range(11, 20))
+    both = (kvq.RopeTensorStruct * 2)(kvq.RopeTensorStruct(*a), kvq.RopeTensorStruct(*b))
+    assert kvq._rope_tensors(*a, *b) == bytes(both) and kvq._rope_tensor(*a) == bytes(both)[:ctypes.sizeof(kvq.RopeTensorStruct)]
