@@ -453,6 +453,23 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
   const int rows = n * a.group;                 // of this head
   const int row0 = qt * (128 * NQ);
   if (row0 >= rows) return;
+  // A softmax thread's query row.  (One past the last repeats it and is not
+  // stored.)  Shaped scores need more of a CTA before its first tile, and their
+  // masks leave many a CTA few tiles: the row is asked for before anything else
+  // (200 documents in 8000 tokens, with the output as whole rows below: 171 to
+  // 159 us).  Plain scores gain nothing by either, long runs of tiles lose 3 %.
+  const int qoff = row0 + (NQ == 2 ? ((warp >> 2) & 1) * 128 : 0);
+  const int row = min(qoff + (warp & 3) * 32 + lane, rows - 1);
+  const int tok = row / a.group;
+  const int hq = h * a.group + row % a.group;
+  uint4 raw[D / 8];
+  auto load_row = [&]() {
+    const uint4* qp = reinterpret_cast<const uint4*>(a.q + (long long)(r0 + tok) * a.q_row_stride +
+                                                     (long long)hq * a.q_head_stride);
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) raw[c] = __ldg(qp + c);
+  };
+  if (MODE != kPlain && warp < C::kSoftmaxWarps) load_row();
   const int len = seq_len(a.s, b, a.p.shift, a.status);
   const int t0 = len - n;                       // position of row 0
   // keys that some row of the tile attends to, and their 128-key tiles
@@ -535,23 +552,15 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
     const int q = warp >> 2;
     const int r = (warp & 3) * 32 + lane;        // TMEM lane, row of the query tile
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    // row of the head's rows; one past the last repeats it and is not stored
-    const int qoff = row0 + (NQ == 2 ? q * 128 : 0);
     const bool live = qoff + r < rows;
-    const int row = min(qoff + r, rows - 1);
-    const int tok = row / a.group;
-    const int hq = h * a.group + row % a.group;
     // a warp without a row of its own only keeps the barriers going: its
     // lanes of the products go nowhere
     const bool idle = qoff + (warp & 3) * 32 >= rows;
     // ---- the query row: scale, split, store (K-major, swizzled) ----
+    // (the second group of one query tile needs the row's scale too)
     float cq;
     {
-      uint4 raw[D / 8];
-      const uint4* qp = reinterpret_cast<const uint4*>(a.q + (long long)(r0 + tok) * a.q_row_stride +
-                                                       (long long)hq * a.q_head_stride);
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c) raw[c] = __ldg(qp + c);
+      if (MODE == kPlain) load_row();
       uint32_t mx = 0;
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) {
@@ -572,8 +581,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
           for (int k = 0; k < 4; ++k) {
             const uint4& v = raw[2 * c + (k >> 1)];
             const uint32_t w0 = (k & 1) ? v.z : v.x, w1 = (k & 1) ? v.w : v.y;
-            const float x0 = __uint_as_float(w0 << 16) * f0 * f1, x1 = __uint_as_float(w0 & 0xffff0000u) * f0 * f1;
-            const float x2 = __uint_as_float(w1 << 16) * f0 * f1, x3 = __uint_as_float(w1 & 0xffff0000u) * f0 * f1;
+            const uint64_t p0 = ptx::f2_pack(f0, f0), p1 = ptx::f2_pack(f1, f1);
+            float x0, x1, x2, x3;
+            ptx::f2_unpack(ptx::f2_mul(ptx::f2_mul(ptx::f2_pack(__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xffff0000u)), p0), p1), x0, x1);
+            ptx::f2_unpack(ptx::f2_mul(ptx::f2_mul(ptx::f2_pack(__uint_as_float(w1 << 16), __uint_as_float(w1 & 0xffff0000u)), p0), p1), x2, x3);
             wh[k] = e4m3x4(x0, x1, x2, x3);
             const uint32_t h01 = f16x2_of_e4m3x2((uint16_t)wh[k]), h23 = f16x2_of_e4m3x2((uint16_t)(wh[k] >> 16));
             const float2 a01 = __half22float2(*reinterpret_cast<const __half2*>(&h01));
@@ -723,7 +734,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
             follow(half, f);
           }
         } else {
-          bool low = whole && (MODE == kBiased || !shape.biased);
+          // (the first weights of all have no base yet)
+          bool low = whole && (MODE == kBiased || !shape.biased) && !(first && half == 0);
           hat = wide;
           sum = 0.f;
           if (MODE == kBiased) {
@@ -841,6 +853,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
       f0 *= f;
       f1 *= f;
       const long long prow = (long long)split * a.s.rows * a.q_heads + orow;
+      // the warp's rows of the output, in the query tiles' place: rows a lane leave
+      // it as whole rows
+      const uint32_t room = sm + C::kQ + (uint32_t)warp * (32 * 2 * D);
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t v[32];
@@ -856,15 +871,14 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
           if (NQ == 1 && f1 != 0.f) x = fmaf(lds_f(part_at + (32 * c + k) * 512), f1, x);
           v[k] = __float_as_uint(x);
         }
-        if (!store) continue;
         if (part) {
+          if (!store) continue;
           float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + 32 * c);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             dst[k] = make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]),
                                  __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3]));
         } else {
-          uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + 32 * c);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             uint32_t z[4];
@@ -874,8 +888,22 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
                                                              __uint_as_float(v[8 * k + 2 * i + 1]));
               z[i] = *reinterpret_cast<const uint32_t*>(&y);
             }
-            dst[k] = make_uint4(z[0], z[1], z[2], z[3]);
+            if (MODE != kPlain)
+              sts_u4(room + lane * (2 * D) + (((4 * c + k) ^ (lane & 7)) << 4), make_uint4(z[0], z[1], z[2], z[3]));
+            else if (store)
+              reinterpret_cast<uint4*>(a.out + orow * D + 32 * c)[k] = make_uint4(z[0], z[1], z[2], z[3]);
           }
+        }
+      }
+      if (MODE != kPlain && !part) {
+        constexpr int kChunks = D / 8, kRows = 32 / kChunks;   // 16-byte chunks of a row, rows at a time
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 32 / kRows; ++k) {
+          const int from = k * kRows + lane / kChunks, ch = lane % kChunks;
+          const long long to = __shfl_sync(0xffffffffu, store ? orow : -1LL, from);
+          const uint4 z = lds_u4(room + from * (2 * D) + ((ch ^ (from & 7)) << 4));
+          if (to >= 0) *reinterpret_cast<uint4*>(a.out + to * D + 8 * ch) = z;
         }
       }
       if (store) {
