@@ -210,21 +210,23 @@ __device__ __forceinline__ void exp_low_block(const uint32_t* s, const LowCap& c
   ptx::f2_unpack(acc, x, y);
   sum = x + y;
 }
-// the same of any 16 raw scores under a short cap; ck: their factor; masked: those
-// outside [lo, hi) left out
+// the same of any 16 raw scores under a short cap; ck: their factor; masked: only
+// of those whose bit is set
 template <bool MASKED>
-__device__ __forceinline__ void exp_far_block(const uint32_t* s, float ck, float cap2, float shift, int lo, int hi,
+__device__ __forceinline__ void exp_far_block(const uint32_t* s, float ck, float cap2, float shift, uint32_t seen,
                                               uint32_t* pk, float& sum) {
   const float ct = 2.885390082f * ck;
   const uint64_t f2 = ptx::f2_pack(-2.f * cap2, -2.f * cap2), b2 = ptx::f2_pack(cap2 + shift, cap2 + shift);
   uint64_t acc = ptx::f2_pack(0.f, 0.f);
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
+    // (what a masked key holds must not reach its neighbour)
+    const uint32_t s0 = !MASKED || seen & (1u << (2 * k)) ? s[2 * k] : 0u, s1 = !MASKED || seen & (2u << (2 * k)) ? s[2 * k + 1] : 0u;
     float x0, x1;
-    ptx::f2_unpack(far_scores(ptx::f2_pack(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), ct, f2, b2), x0, x1);
+    ptx::f2_unpack(far_scores(ptx::f2_pack(__uint_as_float(s0), __uint_as_float(s1)), ct, f2, b2), x0, x1);
     if (MASKED) {
-      x0 = 2 * k >= lo && 2 * k < hi ? x0 : -CUDART_INF_F;
-      x1 = 2 * k + 1 >= lo && 2 * k + 1 < hi ? x1 : -CUDART_INF_F;
+      x0 = seen & (1u << (2 * k)) ? x0 : -CUDART_INF_F;
+      x1 = seen & (2u << (2 * k)) ? x1 : -CUDART_INF_F;
     }
     const float e0 = ptx::ex2_approx(x0), e1 = ptx::ex2_approx(x1);
     acc = ptx::f2_add(acc, ptx::f2_pack(e0, e1));
@@ -251,6 +253,16 @@ __device__ __forceinline__ void exp_bias_block(const uint32_t* s, float ck, floa
   float x, y;
   ptx::f2_unpack(acc, x, y);
   sum = x + y;
+}
+// columns of 16 within [lo, hi), a bit each
+__device__ __forceinline__ uint32_t bits_within(int lo, int hi) {
+  const int a = min(max(lo, 0), 16), b = min(max(hi, 0), 16);
+  return (0xffffu << a) & ((1u << b) - 1u);
+}
+// scores of columns whose bit is not set become -inf
+__device__ __forceinline__ void keep_bits(uint32_t* s, uint32_t bits) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k) s[k] = bits & (1u << k) ? s[k] : 0xff800000u;
 }
 // scores of columns outside [lo, hi) become -inf
 __device__ __forceinline__ void mask_block(uint32_t* s, int lo, int hi) {
@@ -320,7 +332,7 @@ __device__ __noinline__ float shaped_top(HalfRow h) {
       uint32_t v[16];
       ptx::tmem_ld16(h.t_h + 16 * k, v);
       if (h.shape.biased) shape_block<MODE>(v, h.cq * lds_f(h.mh + 4 * k), h, k);
-      if (MASKED) mask_block(v, (h.there >> k) & 1u ? h.lo - 16 * k : 16, h.hi - 16 * k);
+      if (MASKED) keep_bits(v, bits_within((h.there >> k) & 1u ? h.lo - 16 * k : 16, h.hi - 16 * k));
       most[k] = -CUDART_INF_F;
 #pragma unroll
       for (int i = 0; i < 16; i += 2) most[k] = ptx::max3(most[k], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
@@ -351,13 +363,13 @@ __device__ __noinline__ float shaped_weights(HalfRow h, float m) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float raw = h.cq * lds_f(h.mh + 4 * (k + i)), shift = lds_f(h.mh + kMetaShift + 4 * (k + i)) - m;
-      const int lo = (h.there >> (k + i)) & 1u ? h.lo - 16 * (k + i) : 16, hi = h.hi - 16 * (k + i);
+      const uint32_t seen = MASKED ? bits_within((h.there >> (k + i)) & 1u ? h.lo - 16 * (k + i) : 16, h.hi - 16 * (k + i)) : 0u;
       float b;
       if (far) {
-        exp_far_block<MASKED>(v + 16 * i, raw, h.shape.cap2, shift, lo, hi, w + 8 * i, b);
+        exp_far_block<MASKED>(v + 16 * i, raw, h.shape.cap2, shift, seen, w + 8 * i, b);
       } else {
         shape_block<MODE>(v + 16 * i, raw, h, k + i);
-        if (MASKED) mask_block(v + 16 * i, lo, hi);
+        if (MASKED) keep_bits(v + 16 * i, seen);
         exp_block(v + 16 * i, fmaxf(shape_factor<MODE>(h.shape, raw), 1.2e-38f), shift, w + 8 * i, b);
       }
       sum = fmaf(b, lds_f(h.mh + kMetaInv + 4 * (k + i)), sum);
@@ -498,11 +510,16 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
   const int j0 = (int)((long long)tiles * split / p.splits), j1 = (int)((long long)tiles * (split + 1) / p.splits);
   const int n_t = j1 - j0;
   const int base = (tile_lo + j0) * kTileKeys;  // first key of the range
-  // Tiles in ascending order; under a distance bias from the last one down: the
-  // largest scores come first then, and the base, set by them, need not rise
-  // again and again.
-  const bool down = MODE != kPlain && a.shape.slopes != nullptr;
-  auto tile_at = [&](int j) { return MODE != kPlain && down ? n_t - 1 - j : j; };
+  // Tiles in ascending order; under a distance bias from the rows' own tile down
+  // and then from there up: the largest scores come first, and the base, set by
+  // them, need not rise again and again (4096 rows and keys both ways around them,
+  // in ascending order 2 times as long).
+  int own = -1;
+  if (MODE != kPlain && a.shape.slopes != nullptr && n_t > 0) {
+    const int t_mid = min(max(t0 + (i_first + i_last) / 2, key_lo), key_hi - 1);
+    own = a.causal ? n_t - 1 : min(max(t_mid / kTileKeys - tile_lo - j0, 0), n_t - 1);
+  }
+  auto tile_at = [&](int j) { return MODE != kPlain && j <= own ? own - j : j; };
 
   volatile int* abort = reinterpret_cast<volatile int*>(smem + C::kBar + kCbCount * 8);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBar + kCbCount * 8 + 4);
@@ -743,16 +760,26 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
             const float step = !shape.biased ? 0.f : left ? shape.slope2 : -shape.slope2;
             low = low && (!shape.biased || left || right);
             if (low) {
-              const float d0 = (float)(view.ref - (base + at0 + 64 * half));
               uint32_t cur[64];
               ptx::tmem_ld64(t_h, cur);
+              if (shape.biased) {
+                const float d0 = (float)(view.ref - (base + at0 + 64 * half));
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                float b;
-                const float beside = fmaf(-step, d0 - (float)(16 * k), lds_f(mh + kMetaShift + 4 * k) - m);
-                exp_bias_block(cur + 16 * k, cq * lds_f(mh + 4 * k), beside, step, pk[k >> 1] + 8 * (k & 1), b);
-                hat += b;
-                sum = fmaf(b, lds_f(mh + kMetaInv + 4 * k), sum);
+                for (int k = 0; k < 4; ++k) {
+                  float b;
+                  const float beside = fmaf(-step, d0 - (float)(16 * k), lds_f(mh + kMetaShift + 4 * k) - m);
+                  exp_bias_block(cur + 16 * k, cq * lds_f(mh + 4 * k), beside, step, pk[k >> 1] + 8 * (k & 1), b);
+                  hat += b;
+                  sum = fmaf(b, lds_f(mh + kMetaInv + 4 * k), sum);
+                }
+              } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  float b;
+                  exp_block(cur + 16 * k, cq * lds_f(mh + 4 * k), lds_f(mh + kMetaShift + 4 * k) - m, pk[k >> 1] + 8 * (k & 1), b);
+                  hat += b;
+                  sum = fmaf(b, lds_f(mh + kMetaInv + 4 * k), sum);
+                }
               }
             }
           } else if (low) {

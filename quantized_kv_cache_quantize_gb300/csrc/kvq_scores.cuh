@@ -52,6 +52,12 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// the smaller, or NaN where one is
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 // tanh of a pair, |x| <= 1
 __device__ __forceinline__ uint64_t tanh_small(uint64_t x) {
   auto both = [](float c) { return ptx::f2_pack(c, c); };
@@ -114,15 +120,19 @@ __device__ __forceinline__ uint64_t low_scores(uint64_t s, const LowCap& c, uint
 }
 
 // The same for any score, by cap2 (1 - 2 / (1 + t)), t = 2^(2 x log2 e), alone: off
-// by 2^-22 of the cap, whatever the score.  Half the instructions of the choice
+// by 2^-21 of the cap, whatever the score.  Half the instructions of the choice
 // between two ways, and nothing that a weight in FP16 shows while the cap is below
-// kShortCap: 2^-14 there, an eighth of its rounding.  ct: 2 ck log2 e.
+// kShortCap: 2^-13 there, a quarter of its rounding.  ct: 2 ck log2 e.
 constexpr float kShortCap = 256.f;
 __device__ __forceinline__ uint64_t far_scores(uint64_t s, float ct, uint64_t minus2cap, uint64_t cap_beside) {
   float x0, x1;
   ptx::f2_unpack(ptx::f2_mul(s, ptx::f2_pack(ct, ct)), x0, x1);
-  ptx::f2_unpack(ptx::f2_add(ptx::f2_pack(ptx::ex2_approx(x0), ptx::ex2_approx(x1)), ptx::f2_pack(1.f, 1.f)), x0, x1);
-  return ptx::f2_fma(ptx::f2_pack(rcp_approx(x0), rcp_approx(x1)), minus2cap, cap_beside);
+  // (1 / a, 1 / b) = (b, a) / (a b): one reciprocal for two.  Past 2^60 1 / a is
+  // nothing beside 1, and a b stays in fp32.  (A NaN takes its neighbour with it.)
+  const float e0 = ptx::ex2_approx(min_nan(x0, 60.f)), e1 = ptx::ex2_approx(min_nan(x1, 60.f));
+  ptx::f2_unpack(ptx::f2_add(ptx::f2_pack(e0, e1), ptx::f2_pack(1.f, 1.f)), x0, x1);
+  const float r = rcp_approx(x0 * x1);
+  return ptx::f2_fma(ptx::f2_mul(ptx::f2_pack(x1, x0), ptx::f2_pack(r, r)), minus2cap, cap_beside);
 }
 
 // What is left to do to a shaped score: a factor to units of log 2.

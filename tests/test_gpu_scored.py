@@ -262,6 +262,35 @@ def test_not_finite_rows_and_seen_keys(rows):
     assert torch.equal(nan.all(-1), want) and torch.equal(nan.any(-1), want) and torch.equal(torch.isnan(lse).cpu(), want)
 
 
+@pytest.mark.parametrize("rows", [1, 5, 70, 300])
+@pytest.mark.parametrize("heat", [1.0, 20.0])
+def test_masked_neighbours_of_seen_keys(rows, heat):
+    """NaN in every key that a row's range leaves out, right beside those that it
+    sees, at odd and even places; scores below the cap and far beyond it."""
+    d, page, lens = 64, 32, [500]
+    rng, codes, exps, table = pool_case(12, lens, page, 2, d, e_lo=-9, e_hi=-6)
+    q = rows_of(rng, rows, 2, d, heat=heat)
+    ranges = np.tile([[101, 130]], (rows, 1))
+    ranges[rows // 2:] = [[102, 131]]
+    if rows == 1:
+        ranges[0] = [101, 131]
+    pool = P.Pool([c[0].numpy() for c in codes], [e[0] for e in exps])
+    codes = [c.clone() for c in codes]
+    for j in list(range(101)) + list(range(131, 500)):
+        for c in codes:
+            c[0, table[0][j // page], :, j % page] = 0x7F
+    codes[0][0, table[0][101 // page], :, 101 % page] = 0x7F                   # K alone: V is weighed by zero there
+    for sl in (slice(0, rows // 2), slice(rows // 2, rows)):
+        if rows == 1 or sl.start == 0:
+            continue
+        ref = P.attention_scored(pool, q.double().numpy(), table, lens, [rows], 0.2, False, 0, 6.0, ranges=ranges)
+        got = kvq.paged_attention(cache_of(codes, exps), q.cuda(), dev(table), dev(lens), offsets_of([rows]), scale=0.2,
+                                  causal=False, with_lse=True, max_q=rows, softcap=6.0, ranges=dev(ranges))
+        clean()
+        check([g[sl] for g in got], [x[sl] for x in ref], d, 30, 6.0, str(sl))
+        assert torch.isnan(got[1][:rows // 2]).all()                            # these see key 101
+
+
 @pytest.mark.parametrize("hq,counts", [(4, [1, 1]), (4, [3, 2]), (4, [70, 5]), (2, [200, 90])])
 def test_without_shapes_it_is_the_plain_call(hq, counts):
     """Shapes that change nothing: a prefix of no token, ranges over everything;
