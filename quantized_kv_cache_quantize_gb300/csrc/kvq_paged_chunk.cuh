@@ -784,9 +784,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
             }
           } else if (low) {
             uint32_t cur[64];
-            float most;
+            float most, ck[4];
             ptx::tmem_ld64_max(t_h, cur, most);
-            float ck[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) ck[k] = cq * lds_f(mh + 4 * k);
             const float ck_most = fmaxf(fmaxf(ck[0], ck[1]), fmaxf(ck[2], ck[3]));
@@ -817,8 +816,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
             const HalfRow hr{t_h, mh, there >> (4 * half), lo_r - at_h, hi_r - at_h, view.ref - (base + at_h), cq, shape};
             // a single weight up to 2^15 still fits FP16; but a sum that was too
             // large for the short way above must not be so again and again
-            const float top = whole ? shaped_top<MODE, false>(hr) : shaped_top<MODE, true>(hr);
             float f = 1.f;
+            const float top = whole ? shaped_top<MODE, false>(hr) : shaped_top<MODE, true>(hr);
             if (__any_sync(0xffffffffu, top > m + (low ? 9.f : 15.f))) f = rise(top);
             if (__any_sync(0xffffffffu, wide != 0.f || (fabsf(m) > kFarBase && m > kLowest)))
               sum = shaped_weights_apart<MODE>(hr, m);

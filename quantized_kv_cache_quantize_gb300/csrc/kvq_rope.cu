@@ -35,10 +35,12 @@ __global__ void __launch_bounds__(256) rope_fill_kernel(const __grid_constant__ 
 // ---- rotation ---------------------------------------------------------------
 // A block per R rows and eight heads of one tensor.  Each value is read and
 // written once and HBM bounds the large sizes; the turns, 4 bytes a channel, would
-// double the reads if every head fetched its own.  R = 4 spreads a small call over
-// the SMs, 16 leaves eight loads a thread in flight.
+// double the reads if every head fetched its own.  Queries and keys of 4680 tokens,
+// 24 heads, in the window's layout: 22.4 us, 5.1 TB/s (four heads a thread in
+// flight and three blocks an SM 25.2 us, five blocks 27.7).  R = 4 spreads a small
+// call over the SMs: 64 rows of 40 heads take 4.1 us, all of it latency.
 template <int D, int R, bool INTER>
-__global__ void __launch_bounds__(256, 3) rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(256, 4) rope_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ float4 turns[R * kRopeRow];
   ptx::grid_dependency_wait();
   ptx::launch_dependents();
@@ -55,7 +57,7 @@ __global__ void __launch_bounds__(256, 3) rope_kernel(const __grid_constant__ Ro
   if (second) x = a.x[1];
   const int h0 = (int)g * kRopeHeads;
   const int32_t* pos = a.pos + b * a.pb + row0 * a.pr;
-  rope_tile<D, R, R / 4, INTER>(a.t, a.inverse != 0, turns, min(R, a.rows - row0), min(kRopeHeads, x.heads - h0),
+  rope_tile<D, R, (R + 7) / 8, INTER>(a.t, a.inverse != 0, turns, min(R, a.rows - row0), min(kRopeHeads, x.heads - h0),
                   x.x + b * x.xb + row0 * x.xr + h0 * x.xh, x.xr, x.xh, x.y + b * x.yb + row0 * x.yr + h0 * x.yh, x.yr,
                   x.yh, a.status, [&](int r, int axis) { return __ldg(pos + r * a.pr + axis * a.pa); });
 }
@@ -190,10 +192,14 @@ __device__ __forceinline__ void append_keys(const AppendRopeArgs& p, int item, i
   }
 }
 
-// Many new tokens: blocks of keys (a page and `heads` heads), of values (a page
-// and head), of query rows.
+// Many new tokens: blocks of keys (a page and `heads` heads), of query rows, of
+// values (a page and head), the longest first.  Bound by HBM, 5 bytes of K and V a
+// channel and 4 of the queries, with the ALU pipe behind it (every product and sum
+// of the rotation by itself).  4680 tokens of 24 heads and their queries: 5.0 TB/s;
+// two heads a block of keys 37.4 us, four 33.4, eight 30.5, queries behind the
+// values 3 us more; without the load of the next head ahead 0.5 us more.
 struct AppendGrid {
-  unsigned k_blocks, v_blocks;
+  unsigned k_blocks, q_blocks;
   int heads;    // per block of keys
   int q_rows;   // per block of query rows
 };
@@ -209,13 +215,14 @@ __global__ void __launch_bounds__(512, 2) append_rope_kernel(const __grid_consta
     return;
   }
   at -= g.k_blocks;
-  if (at < g.v_blocks) {
-    append_page<D>(p.a, 1, (int)(at % (unsigned)p.a.p.heads), (int)(at / (unsigned)p.a.p.heads));
+  if (at < g.q_blocks) {
+    // (a page of 16 tokens has too few threads for 16 rows)
+    if (g.q_rows == 16) append_queries<D, 16, 2, INTER>(p, at, turns);
+    else append_queries<D, 4, 2, INTER>(p, at, turns);
     return;
   }
-  // (a page of 16 tokens has too few threads for 16 rows)
-  if (g.q_rows == 16) append_queries<D, 16, 2, INTER>(p, at - g.v_blocks, turns);
-  else append_queries<D, 4, 2, INTER>(p, at - g.v_blocks, turns);
+  at -= g.q_blocks;
+  append_page<D>(p.a, 1, (int)(at % (unsigned)p.a.p.heads), (int)(at / (unsigned)p.a.p.heads));
 }
 
 // One token of every sequence: a warp per sequence, head and K or V, half the lanes
@@ -335,12 +342,12 @@ cudaError_t launch_pages_append_rope(const AppendRopeArgs& p, cudaStream_t strea
   }
   const long long items = (a.s.rows >> a.p.shift) + 2LL * a.s.batch;
   AppendGrid g{};
-  g.heads = 4;
-  while (g.heads > 1 && items * ((a.p.heads + g.heads - 1) / g.heads) < 3LL * sms) g.heads /= 2;
+  g.heads = 8;   // a block of keys, as long as there is one for every SM
+  while (g.heads > 1 && items * ((a.p.heads + g.heads - 1) / g.heads) < sms) g.heads /= 2;
   g.k_blocks = (unsigned)(items * ((a.p.heads + g.heads - 1) / g.heads));
-  g.v_blocks = (unsigned)(items * a.p.heads);
   g.q_rows = a.p.page == 16 ? 4 : 16;
-  const long long q_blocks = (a.s.rows + g.q_rows - 1) / g.q_rows * q_groups;
+  g.q_blocks = (unsigned)((a.s.rows + g.q_rows - 1) / g.q_rows * q_groups);
+  const unsigned v_blocks = (unsigned)(items * a.p.heads);
   const int smem = a.p.page * kRopeRow * (int)sizeof(float4);
   auto pick = [&](auto inter) {
     constexpr bool I = decltype(inter)::value;
@@ -349,7 +356,7 @@ cudaError_t launch_pages_append_rope(const AppendRopeArgs& p, cudaStream_t strea
   const auto kern = p.t.interleaved ? pick(std::true_type{}) : pick(std::false_type{});
   const cudaError_t e = ensure_smem_limit(kern, 128 * kRopeRow * (int)sizeof(float4), g_append_smem[a.p.d == 128][p.t.interleaved]);
   if (e != cudaSuccess) return e;
-  return launch_dependent(kern, (unsigned)(g.k_blocks + g.v_blocks + q_blocks), a.p.page * a.p.d / 32, smem, stream, p, g);
+  return launch_dependent(kern, g.k_blocks + g.q_blocks + v_blocks, a.p.page * a.p.d / 32, smem, stream, p, g);
 }
 
 }  // namespace kvq
