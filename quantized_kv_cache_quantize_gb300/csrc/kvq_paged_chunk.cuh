@@ -751,8 +751,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
             follow(half, f);
           }
         } else {
-          // (the first weights of all have no base yet)
-          bool low = whole && (MODE == kBiased || !shape.biased) && !(first && half == 0);
+          // (the first weights have no base yet, and distances from one that is far
+          // out are with_ev's)
+          bool low = __all_sync(0xffffffffu, fabsf(m) <= kFarBase) && whole && (MODE == kBiased || !shape.biased);
           hat = wide;
           sum = 0.f;
           if (MODE == kBiased) {

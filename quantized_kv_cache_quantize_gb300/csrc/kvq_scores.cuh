@@ -120,9 +120,11 @@ __device__ __forceinline__ uint64_t low_scores(uint64_t s, const LowCap& c, uint
 }
 
 // The same for any score, by cap2 (1 - 2 / (1 + t)), t = 2^(2 x log2 e), alone: off
-// by 2^-21 of the cap, whatever the score.  Half the instructions of the choice
-// between two ways, and nothing that a weight in FP16 shows while the cap is below
-// kShortCap: 2^-13 there, a quarter of its rounding.  ct: 2 ck log2 e.
+// by 2^-20 of the cap at most, whatever the score (2 r, r = 1 / (1 + t) <= 1, with
+// five roundings of 2^-24 or 2^-23, t off by 2^-21 where it counts).  Half the
+// instructions of the choice between two ways (cap_block), and little that a weight
+// in FP16 shows while the cap is below kShortCap: 2^-12 there, half its rounding.
+// ct: 2 ck log2 e.
 constexpr float kShortCap = 256.f;
 __device__ __forceinline__ uint64_t far_scores(uint64_t s, float ct, uint64_t minus2cap, uint64_t cap_beside) {
   float x0, x1;

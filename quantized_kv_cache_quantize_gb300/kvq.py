@@ -861,8 +861,12 @@ def pages_append_rope(cache: PagedCache, table: RopeTable, k_new: torch.Tensor, 
 
 def _scores(cache: PagedCache, q_heads: int, batch: int, rows: int, softcap, slopes, prefix, ranges):
     """A call's kvq_scores, None for plain scores."""
-    if slopes is None and prefix is None and ranges is None and softcap == 0.0:
-        return None
+    if not softcap:
+        if slopes is None and prefix is None and ranges is None:
+            return None
+        softcap = 0.0
+    elif not 2.0 ** -20 <= softcap <= 2.0 ** 20:   # (a tiny one would be none as fp32)
+        raise KVQError(KVQ_ERR_INVALID_ARG, f"softcap {softcap}")
     for name, t, dtype, shape in (("slopes", slopes, torch.float32, (q_heads,)), ("prefix", prefix, torch.int32, (batch,)),
                                   ("ranges", ranges, torch.int32, (rows, 2))):
         if t is not None and (t.dtype is not dtype or t.shape != shape or t.device != cache.device

@@ -32,10 +32,13 @@ def pool_case(seed, lens, page, heads, d, **kw):
 
 def check(got, ref, d, n_keys, softcap, what=""):
     """check_attention's bounds with two more terms.
-    - The shaping's own rounding, as a score's error: a capped score is off by
-      2^-22 of the cap at most (the exponential 2^-22 of itself, two roundings, a
-      reciprocal of 2^-23), a biased one by three roundings, 2^-22 of |score| +
-      |bias|, in all; log2 units and back, the same again.  It enters serr, which
+    - The shaping's own rounding, as a score's error.  cap (1 - 2 r), r = 1 / (1 +
+      t) by one reciprocal of a pair's product: r is off by 2^-23 (the reciprocal)
+      and 3 2^-24 (1 + t, the product, its share), 5 2^-23 of the cap as 2 r; t by
+      2^-21 (the exponential 2^-22, its argument as much where the derivative
+      counts), 2 2^-23 of the cap as 2 t / (1 + t)^2 is 1/2 at most; the sum
+      2^-24: 2^-20 of the cap in all.  A bias: three roundings, 2^-22 of |score| +
+      |bias|; log2 units and back, the same again.  It enters serr, which
       tolerances() takes times (d + 4) 2^-23.
     - Weights times V scales in FP16 are off by half a subnormal step, 2^-25,
       where the largest of the row stands at 2^9 or above: 2^-34 of that largest
@@ -45,7 +48,7 @@ def check(got, ref, d, n_keys, softcap, what=""):
       d = 128 and 333 and 90 keys, row 30 of head 3 has 1.1e-19 in channel 82, all
       of it from weights below 2^-60 of the largest; FP16 leaves 0.)"""
     out, lse, bound, serr, qerr, herr, top = ref
-    extra = 2.0 ** -22 * softcap + 2.0 ** -21 * herr
+    extra = 2.0 ** -20 * softcap + 2.0 ** -21 * herr
     tol_o, tol_l = tolerances(out, lse, bound, serr + extra / ((d + 4) * 2.0 ** -23), qerr, d, n_keys)
     tol_o = tol_o + (n_keys * 448 * 2.0 ** -34 * top)[..., None]
     o, z = got[0].double().cpu().numpy(), got[1].double().cpu().numpy()
@@ -263,6 +266,32 @@ def test_not_finite_rows_and_seen_keys(rows):
 
 
 @pytest.mark.parametrize("rows", [1, 5, 70, 300])
+@pytest.mark.parametrize("power", [12, 30])
+def test_scores_beyond_every_bias(rows, power):
+    """Scores of 2^12 and 2^30 beside a bias: two equal keys, tiles apart, share
+    the row, whatever the rounding of a base that large; the others weigh nothing."""
+    d, page, n = 64, 64, 900
+    lens = [n]
+    rng, codes, exps, table = pool_case(14, lens, page, 1, d, e_lo=0, e_hi=0)
+    k = np.zeros((exps[0].shape[1], 1, page, d))
+    k[..., 0] = rng.integers(1, 8, k.shape[:-1]) / 8.0
+    best = (65, 700)
+    for j in best:
+        k[table[0][j // page], 0, j % page, 0] = 2.0
+    codes[0][0] = torch.from_numpy(P.e4m3_code(P.e4m3_round(k)))
+    q = torch.zeros(rows, 2, d, dtype=torch.bfloat16)
+    q[..., 0] = 2.0 ** power
+    pool = P.Pool([c[0].numpy() for c in codes], [e[0] for e in exps])
+    s = np.array([0.0, 2.0 ** -30], np.float32)
+    ref = P.attention_scored(pool, q.double().numpy(), table, lens, [rows], 0.5, False, 0, slopes=s)
+    got = kvq.paged_attention(cache_of(codes, exps), q.cuda(), dev(table), dev(lens), offsets_of([rows]), scale=0.5,
+                              causal=False, with_lse=True, max_q=rows, slopes=dev(s, torch.float32))
+    clean()
+    assert np.abs(ref[0][:, 0] - (pool.rows(1, table[0], n)[0][list(best)]).mean(0)).max() < 1e-12
+    check(got, ref, d, n, 0.0)
+
+
+@pytest.mark.parametrize("rows", [1, 5, 70, 300])
 @pytest.mark.parametrize("heat", [1.0, 20.0])
 def test_masked_neighbours_of_seen_keys(rows, heat):
     """NaN in every key that a row's range leaves out, right beside those that it
@@ -318,7 +347,7 @@ def test_refusals_on_the_device():
                       ("ranges", dev([0, 1, 0, 1])), ("ranges", dev([[0, 0], [1, 1]]).T)):
         with pytest.raises(ValueError, match=name):
             kvq.paged_attention(cache, q, table, lens, **{name: bad})
-    for cap in (-1.0, float("nan"), float("inf"), 2.0 ** -21, 2.0 ** 21):
+    for cap in (-1.0, float("nan"), float("inf"), 2.0 ** -21, 2.0 ** 21, 1e-60):
         with pytest.raises(kvq.KVQError) as e:
             kvq.paged_attention(cache, q, table, lens, softcap=cap)
         assert e.value.status == kvq.KVQ_ERR_INVALID_ARG

@@ -95,6 +95,10 @@ def test_binding_refusals(lib):
     cache = kvq.PagedCache(codes, codes.clone(), *[torch.ones(1, 4, 2, dtype=torch.bfloat16) for _ in range(2)])
     ok = dict(softcap=0.0, slopes=None, prefix=None, ranges=None)
     assert kvq._scores(cache, 4, 2, 3, **ok) is None
+    assert kvq._scores(cache, 4, 2, 3, **(ok | dict(softcap=None))) is None
+    for cap in (-1.0, 1e-60, math.nan, math.inf, 2.0 ** 21):
+        with pytest.raises(kvq.KVQError, match="softcap"):
+            kvq._scores(cache, 4, 2, 3, **(ok | dict(softcap=cap)))
     assert kvq._scores(cache, 4, 2, 3, **(ok | dict(softcap=3.0))).softcap == 3.0
     good = dict(slopes=torch.ones(4), prefix=torch.ones(2, dtype=torch.int32), ranges=torch.zeros(3, 2, dtype=torch.int32))
     s = kvq._scores(cache, 4, 2, 3, 0.0, **good)
@@ -104,3 +108,30 @@ def test_binding_refusals(lib):
                       ("ranges", torch.zeros(2, 3, dtype=torch.int32).T), ("ranges", torch.zeros(6, dtype=torch.int32))):
         with pytest.raises(ValueError, match=name):
             kvq._scores(cache, 4, 2, 3, **(ok | {name: bad}))
+
+
+# ---- the polynomials of tanh ----
+
+def _horner(c, x):
+    """x times the polynomial in x^2, every step rounded to fp32 as the kernels do."""
+    x = x.astype(np.float32)
+    z = (x * x).astype(np.float32)
+    p = np.full_like(z, c[-1])
+    for k in c[-2::-1]:
+        p = (p.astype(np.float64) * z + np.float64(k)).astype(np.float32)      # fused
+    return p * x
+
+
+@pytest.mark.parametrize("which,x_max,bound", [(0, 1.0, 2.0 ** -22), (1, 0.4, 2.0 ** -21.8)])
+def test_tanh_polynomials(which, x_max, bound):
+    """The constants in the kernels are the fit's, and near tanh to the bound that
+    is stated beside them."""
+    import re
+    from quantized_kv_cache_quantize_gb300.csrc import tanh_fit
+    fit = (tanh_fit.fit_coefficients(), tanh_fit.fit_coefficients(tanh_fit.LOW_TERMS, tanh_fit.LOW_X))[which].astype(np.float32)
+    assert tanh_fit.LOW_X == 0.4
+    src = open(os.path.join(os.path.dirname(tanh_fit.__file__), "kvq_scores.cuh")).read()
+    have = {np.float32(v) for v in re.findall(r"-?\d\.\d+e[-+]\d+(?=f)", src)}
+    assert {np.float32(c) for c in fit} <= have
+    x = np.linspace(1e-4, x_max, 200001)
+    assert np.abs(_horner(fit, x) / np.tanh(x.astype(np.float32).astype(np.float64)) - 1).max() <= bound
