@@ -135,6 +135,23 @@ def test_scored(d, page, hq, hkv, lens, counts, causal, window, softcap, slopes,
     run_case(d, page, hq, hkv, lens, counts, causal, window, softcap, slopes, prefix, docs)
 
 
+@pytest.mark.parametrize("d,hq,hkv,rows", [(128, 4, 4, 1), (64, 6, 3, 2), (128, 12, 4, 3)])
+@pytest.mark.parametrize("softcap,slopes,prefix,docs", [(5.0, True, True, 4), (0.0, False, False, 3), (8.0, False, False, 0)])
+def test_many_short_sequences(d, hq, hkv, rows, softcap, slopes, prefix, docs):
+    """More (sequence, head) pairs than two for every SM: the line of all keys."""
+    rng = np.random.default_rng(5)
+    lens = [int(n) for n in rng.integers(0, 150, 110)]
+    lens[3], lens[50] = 700, 0
+    run_case(d, 32, hq, hkv, lens, [min(rows, max(1, n)) for n in lens], True, 60 if docs else 0, softcap, slopes, prefix, docs, seed=1)
+
+
+@pytest.mark.parametrize("d,page,rows", [(128, 128, 1), (64, 16, 2)])
+@pytest.mark.parametrize("softcap,slopes,prefix,docs", [(5.0, True, False, 0), (0.0, True, False, 5)])
+def test_one_long_sequence(d, page, rows, softcap, slopes, prefix, docs):
+    """Few pairs: clusters of CTAs share the keys of one."""
+    run_case(d, page, 4, 2, [9000], [rows], True, 0, softcap, slopes, prefix, docs, seed=2)
+
+
 @pytest.mark.parametrize("softcap", [2.0 ** -20, 1e-3, 0.7, 50.0, 1000.0, 2.0 ** 20])
 @pytest.mark.parametrize("hq,counts", [(2, [1, 3]), (8, [2, 2]), (4, [70, 9]), (2, [200, 90])])
 def test_caps_of_every_size(softcap, hq, counts):
@@ -457,3 +474,38 @@ def test_a_layer_as_it_is_used():
         qt = torch.from_numpy(P.rope_steps(q.float().numpy(), cs, pos, [0] * 64, False)).bfloat16()
         ref = P.attention_scored(pool, qt.double().numpy(), table, lens, counts, d ** -0.5, True, 0, 15.0, ranges=ranges)
         check(got, ref, d, max(lens), 15.0, what=str(step))
+
+
+@pytest.mark.parametrize("hq,rows", [(4, 1), (2, 70)])
+def test_calls_at_once(hq, rows):
+    """Two calls under way on two streams, and two captured graphs replayed on
+    two streams: nothing they share."""
+    d, page, lens = 64, 32, [9000, 8000, 8500] if rows == 1 else [4000, 3000, 3500]
+    rng, codes, exps, table = pool_case(16, lens, page, 2, d, e_lo=-9, e_hi=-6)
+    cache, t, n, off = cache_of(codes, exps), dev(table), dev(lens), offsets_of([rows] * 3)
+    qs = [rows_of(rng, 3 * rows, hq, d).cuda() for _ in range(2)]
+    kws = [dict(softcap=4.0, ranges=dev(docs_of(rng, lens, [rows] * 3, 4))), dict(slopes=torch.full((hq,), 0.01, device="cuda"), prefix=dev([9, 8, 7]))]
+
+    def call(i, **kw):
+        return kvq.paged_attention(cache, qs[i], t, n, off, max_q=rows, with_lse=True, **kws[i], **kw)
+
+    want = [call(i) for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = [call(i, stream=s) for i, s in enumerate(streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for g, w in zip(got, want) for x, y in zip(g, w))
+    graphs, outs = [], []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(call(i))
+        graphs.append(g)
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for g, w in zip(outs, want) for x, y in zip(g, w))
+    clean()
