@@ -121,6 +121,7 @@ class ScoresStruct(ctypes.Structure):
 # to show); the layouts are RopeTensorStruct's
 _rope_tensor = struct.Struct("@PPqqqqqqi4x").pack
 _rope_tensors = struct.Struct("@" + "PPqqqqqqi4x" * 2).pack
+_packed_sequences = struct.Struct("@iiqPPPi4x").pack   # SequencesStruct's
 _P = ctypes.c_void_p
 _SIGNATURES = {
     "kvq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -524,7 +525,7 @@ class PagedCache:
         c.k_scale, c.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
         _check(lib().kvq_pages_bytes(ctypes.byref(c), None, None), "kvq_pages_bytes")
         self.struct = c
-        self.device = k_codes.device
+        self.device, self.index = k_codes.device, k_codes.get_device()
         self.layers, self.n_pages, self.kv_heads, self.page_tokens, self.head_dim = k_codes.shape
         self._at = ctypes.addressof(c)
         self._need = {}         # workspace bytes by the call's sizes
@@ -586,6 +587,9 @@ def _handle(stream, device) -> int:
 
 
 def _int32_dev(cache: PagedCache, t: torch.Tensor, name: str, dim: int):
+    if (t.dtype is torch.int32 and t.dim() == dim and t.get_device() == cache.index and t.is_cuda
+            and t.stride(-1) == 1):
+        return   # the usual case, before the questions that name what is wrong
     if t.dtype is not torch.int32 or t.dim() != dim or not t.is_cuda:
         raise ValueError(f"{name} must be a {dim}-dimensional CUDA int32 tensor, got {t.dtype} "
                          f"{list(t.shape)} on {t.device}")
@@ -615,7 +619,8 @@ def _paged_rows(cache: PagedCache, t: torch.Tensor, name: str) -> tuple:
     return shape, strides
 
 
-def _sequences(cache: PagedCache, rows: int, block_table, kv_lens, offsets) -> SequencesStruct:
+def _sequences(cache: PagedCache, rows: int, block_table, kv_lens, offsets) -> tuple:
+    """(a call's kvq_sequences, packed, its batch and width)"""
     _int32_dev(cache, block_table, "block_table", 2)
     _int32_dev(cache, kv_lens, "kv_lens", 1)
     batch, width = block_table.shape
@@ -630,8 +635,8 @@ def _sequences(cache: PagedCache, rows: int, block_table, kv_lens, offsets) -> S
         _int32_dev(cache, offsets, "offsets", 1)
         if offsets.shape[0] != batch + 1:
             raise ValueError(f"offsets must have {batch + 1} entries, got {offsets.shape[0]}")
-    return SequencesStruct(batch, width, _row_stride(block_table), block_table.data_ptr(),
-                           kv_lens.data_ptr(), None if offsets is None else offsets.data_ptr(), rows)
+    return _packed_sequences(batch, width, _row_stride(block_table), block_table.data_ptr(), kv_lens.data_ptr(),
+                             0 if offsets is None else offsets.data_ptr(), rows), batch, width
 
 
 def _int32(name: str, value: int):
@@ -653,11 +658,11 @@ def pages_append(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor,
     if shape != shape_v or shape[1] != cache.kv_heads:
         raise ValueError(f"k_new and v_new must have shape [rows, {cache.kv_heads}, "
                          f"{cache.head_dim}], got {list(shape)} and {list(shape_v)}")
-    s = _sequences(cache, shape[0], block_table, kv_lens, offsets)
+    s, _, _ = _sequences(cache, shape[0], block_table, kv_lens, offsets)
     with _switch(cache.device):
         _check(lib().kvq_pages_append(
             cache._at, layer, k_new.data_ptr(), ks[0], ks[1], v_new.data_ptr(), vs[0], vs[1],
-            ctypes.addressof(s), _handle(stream, cache.device)), "kvq_pages_append")
+            s, _handle(stream, cache.device)), "kvq_pages_append")
 
 
 def rope_frequencies(pairs: int, base: float = 10000.0, sections=None) -> list[float]:
@@ -823,7 +828,7 @@ def pages_append_rope(cache: PagedCache, table: RopeTable, k_new: torch.Tensor, 
     dev, rows, axes = cache.device, shape[0], table.axes
     if table.device != dev:
         raise ValueError(f"the table is on {table.device}, the cache on {dev}")
-    s = _sequences(cache, rows, block_table, kv_lens, offsets)
+    s, _, _ = _sequences(cache, rows, block_table, kv_lens, offsets)
     pos_at, pos_stride = None, 0
     if positions is not None:
         at = positions.shape
@@ -855,7 +860,7 @@ def pages_append_rope(cache: PagedCache, table: RopeTable, k_new: torch.Tensor, 
             raise ValueError("q_out without q")
         _check(lib().kvq_pages_append_rope(
             cache._at, layer, table._at, pos_at, pos_stride, k_new.data_ptr(), ks[0], ks[1], v_new.data_ptr(),
-            vs[0], vs[1], *query, ctypes.addressof(s), handle), "kvq_pages_append_rope")
+            vs[0], vs[1], *query, s, handle), "kvq_pages_append_rope")
     return q_out
 
 
@@ -900,8 +905,8 @@ def paged_attention(cache: PagedCache, q: torch.Tensor, block_table: torch.Tenso
     rows, q_heads, d = shape
     if q_heads < 1 or q_heads % cache.kv_heads:
         raise ValueError(f"q has {q_heads} heads, not a multiple of the cache's {cache.kv_heads}")
-    s = _sequences(cache, rows, block_table, kv_lens, offsets)
-    shaped = _scores(cache, q_heads, s.batch, rows, softcap, slopes, prefix, ranges)
+    s, batch, width = _sequences(cache, rows, block_table, kv_lens, offsets)
+    shaped = _scores(cache, q_heads, batch, rows, softcap, slopes, prefix, ranges)
     if offsets is None:
         max_q = 1
     elif max_q is None:
@@ -919,7 +924,7 @@ def paged_attention(cache: PagedCache, q: torch.Tensor, block_table: torch.Tenso
         if with_lse:
             lse = torch.empty((rows, q_heads), dtype=torch.float32, device=dev)
         if workspace is None:
-            ws, ws_bytes = None, cache.workspace_bytes(q_heads, s.batch, s.width, rows, max_q)
+            ws, ws_bytes = None, cache.workspace_bytes(q_heads, batch, width, rows, max_q)
             if ws_bytes > 16:
                 # (held until the call returns: a call launches two kernels,
                 # and another thread's may come between them)
@@ -932,11 +937,11 @@ def paged_attention(cache: PagedCache, q: torch.Tensor, block_table: torch.Tenso
         lse_at = None if lse is None else lse.data_ptr()
         if shaped is None:
             _check(lib().kvq_paged_attention(
-                cache._at, layer, q.data_ptr(), qs[0], qs[1], q_heads, ctypes.addressof(s), max_q, scale,
+                cache._at, layer, q.data_ptr(), qs[0], qs[1], q_heads, s, max_q, scale,
                 1 if causal else 0, window, ws, ws_bytes, out.data_ptr(), lse_at, handle), "kvq_paged_attention")
         else:
             _check(lib().kvq_paged_attention_scored(
-                cache._at, layer, q.data_ptr(), qs[0], qs[1], q_heads, ctypes.addressof(s), max_q, scale,
+                cache._at, layer, q.data_ptr(), qs[0], qs[1], q_heads, s, max_q, scale,
                 1 if causal else 0, window, ctypes.addressof(shaped), ws, ws_bytes, out.data_ptr(), lse_at,
                 handle), "kvq_paged_attention_scored")
     return (out, lse) if with_lse else out

@@ -205,8 +205,9 @@ def test_binding_refuses_host_tensors(lib):
 
 
 def test_packed_tensors_are_the_structure():
-    """The binding packs kvq_rope_tensor by hand; ctypes' copy of it, which is
-    checked against the header above, has the same bytes."""
+    """The binding packs kvq_rope_tensor and kvq_sequences by hand; ctypes' copies
+    of them, which are checked against the header, have the same bytes."""
     a, b = tuple(range(1, 10)), tuple(range(11, 20))
     both = (kvq.RopeTensorStruct * 2)(kvq.RopeTensorStruct(*a), kvq.RopeTensorStruct(*b))
+    assert kvq._packed_sequences(1, 2, 3, 4, 5, 6, 7) == bytes(kvq.SequencesStruct(1, 2, 3, 4, 5, 6, 7))
     assert kvq._rope_tensors(*a, *b) == bytes(both) and kvq._rope_tensor(*a) == bytes(both)[:ctypes.sizeof(kvq.RopeTensorStruct)]
