@@ -57,7 +57,7 @@
 // tensor memory, tcgen05.ld.red).  The other one, for masks, hot scores, new bases
 // and distances from far bases, is a pair of functions out of line that loop over
 // the scores in tensor memory, so short that they stay in the instruction buffers:
-// unrolled by another two they take a fifth longer.  8000 rows of 32 heads over 8
+// unrolled by another two they take a sixth longer.  8000 rows of 32 heads over 8
 // and as many keys, no mask, us: plain 809, biased 930, capped 1134 to 1190, capped
 // with scores up to 0.9 of the cap 2217.  24 heads of 4680 rows, 23400 keys, capped:
 // 1.29 to 1.37 ms, 0.98 to 1.05 PFLOP/s.
