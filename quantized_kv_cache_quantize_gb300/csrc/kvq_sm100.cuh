@@ -332,6 +332,18 @@ __device__ __forceinline__ void tmem_max16x4(uint32_t taddr, float (&most)[4]) {
       : "r"(taddr), "r"(taddr + 16), "r"(taddr + 32), "r"(taddr + 48)
       : "memory");
 }
+// 32 columns, and the largest magnitude of the 32 numbers (NaN aside), which the
+// load finds on its way.
+__device__ __forceinline__ void tmem_ld32_max(uint32_t taddr, uint32_t (&r)[32], float& most) {
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.abs.f32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, %32, [%33];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : KVQ_R8(0), KVQ_R8(8), KVQ_R8(16), KVQ_R8(24), "=f"(most)
+      : "r"(taddr)
+      : "memory");
+}
 // 64 consecutive 32-bit columns of this thread's TMEM lane, waited for.
 __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
   asm volatile(
@@ -342,20 +354,6 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
       "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : KVQ_R8(0), KVQ_R8(8), KVQ_R8(16), KVQ_R8(24), KVQ_R8(32), KVQ_R8(40), KVQ_R8(48), KVQ_R8(56)
-      : "r"(taddr)
-      : "memory");
-}
-// The same load, and the largest magnitude of the 64 numbers (NaN aside), which
-// the load finds on its way.
-__device__ __forceinline__ void tmem_ld64_max(uint32_t taddr, uint32_t (&r)[64], float& most) {
-  asm volatile(
-      "tcgen05.ld.red.sync.aligned.32x32b.x64.max.abs.f32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
-      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
-      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, %64, [%65];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : KVQ_R8(0), KVQ_R8(8), KVQ_R8(16), KVQ_R8(24), KVQ_R8(32), KVQ_R8(40), KVQ_R8(48), KVQ_R8(56), "=f"(most)
       : "r"(taddr)
       : "memory");
 }
