@@ -207,14 +207,21 @@ __device__ __forceinline__ void exp_block(const uint32_t* s, float scale, float 
   ptx::f2_unpack(acc, x, y);
   sum = x + y;
 }
-// the same of 16 raw scores that stay below 0.4 of their cap
-__device__ __forceinline__ void exp_low_block(const uint32_t* s, const LowCap& c, float shift, uint32_t* pk, float& sum) {
+// the same of 16 raw scores that stay below 0.4 of their cap; masked: only of
+// those whose bit is set
+template <bool MASKED>
+__device__ __forceinline__ void exp_low_block(const uint32_t* s, const LowCap& c, float shift, uint32_t seen, uint32_t* pk,
+                                              float& sum) {
   const uint64_t b2 = ptx::f2_pack(shift, shift);
   uint64_t acc = ptx::f2_pack(0.f, 0.f);
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     float x0, x1;
     ptx::f2_unpack(low_scores(ptx::f2_pack(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), c, b2), x0, x1);
+    if (MASKED) {
+      x0 = seen & (1u << (2 * k)) ? x0 : -CUDART_INF_F;
+      x1 = seen & (2u << (2 * k)) ? x1 : -CUDART_INF_F;
+    }
     const float e0 = ptx::ex2_approx(x0), e1 = ptx::ex2_approx(x1);
     acc = ptx::f2_add(acc, ptx::f2_pack(e0, e1));
     pk[k] = ptx::f16x2_rn(e0, e1);
@@ -367,18 +374,23 @@ __device__ __noinline__ float shaped_top(HalfRow h) {
 // Their weights against base m, in FP16 over the scores, and the sum.
 template <int MODE, bool MASKED>
 __device__ __noinline__ float shaped_weights(HalfRow h, float m) {
-  const bool far = MODE == kCapped && !h.shape.biased && h.shape.cap2 <= kShortCap * 1.4426950408889634f;
+  const bool cap = MODE == kCapped && !h.shape.biased, far = cap && h.shape.cap2 <= kShortCap * 1.4426950408889634f;
   float sum = 0.f;
 #pragma unroll 1
   for (int k = 0; k < 4; k += 2) {
     uint32_t v[32], w[16];
-    ptx::tmem_ld32(h.t_h + 16 * k, v);
+    float most;
+    ptx::tmem_ld32_max(h.t_h + 16 * k, v, most);
+    const float ck_most = h.cq * fmaxf(lds_f(h.mh + 4 * k), lds_f(h.mh + 4 * k + 4));
+    const bool low = __all_sync(0xffffffffu, most * ck_most <= kLowX && ck_most <= kLowMost) && cap;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float raw = h.cq * lds_f(h.mh + 4 * (k + i)), shift = lds_f(h.mh + kMetaShift + 4 * (k + i)) - m;
       const uint32_t seen = MASKED ? bits_within((h.there >> (k + i)) & 1u ? h.lo - 16 * (k + i) : 16, h.hi - 16 * (k + i)) : 0u;
       float b;
-      if (far) {
+      if (MASKED && low) {   // (an unmasked half that is low did not come here, or for its base alone)
+        exp_low_block<MASKED>(v + 16 * i, low_cap(raw, h.shape.cap2), shift, seen, w + 8 * i, b);
+      } else if (far) {
         exp_far_block<MASKED>(v + 16 * i, raw, h.shape.cap2, shift, seen, w + 8 * i, b);
       } else {
         shape_block<MODE>(v + 16 * i, raw, h, k + i);
@@ -632,14 +644,22 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
 
     // keys this row attends to, from the first key of local tile 0
     const int tq = t0 + tok;
-    RowView view{};
-    RowShape shape{};
+    int hi_r = (a.causal ? min(len, tq + 1) : len) - base;
+    int lo_r = (a.window > 0 ? max(0, tq - a.window + 1) : 0) - base;
+    int ref_r = 0;          // where the row's distances are counted from
+    float slope2 = 0.f;     // (what else shapes a score is the call's)
+    const bool biased = MODE != kPlain && a.shape.slopes != nullptr;
+    const float cap2 = MODE == kCapped ? a.shape.cap * 1.4426950408889634f : 0.f;
     if (MODE != kPlain) {
-      view = row_view(a, b, r0 + tok, tq, len);
-      shape = row_shape<MODE>(a, hq);
+      const RowView view = row_view(a, b, r0 + tok, tq, len);
+      hi_r = view.hi - base;
+      lo_r = view.lo - base;
+      ref_r = view.ref - base;
+      slope2 = row_shape<MODE>(a, hq).slope2;
     }
-    const int hi_r = (MODE != kPlain ? view.hi : a.causal ? min(len, tq + 1) : len) - base;
-    const int lo_r = (MODE != kPlain ? view.lo : a.window > 0 ? max(0, tq - a.window + 1) : 0) - base;
+    // a row that attends to nothing must not keep its warp from the straight way:
+    // whatever it gathers there is dropped at the end
+    const bool none = MODE != kPlain && lo_r >= hi_r;
     float m = kLowest, l = 0.f;
     const uint32_t t_o = tmem + C::kTO + q * D + lane_off;
     bool ok = true;
@@ -663,9 +683,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
       const uint32_t mt = sm + C::kMeta + (j & (kMetaSlots - 1)) * kMetaBytes;
       const uint32_t there = lds_u(mt + kMetaThere);
       const int at0 = tile_at(j) * kTileKeys;
-      const bool left = MODE == kBiased && __all_sync(0xffffffffu, base + at0 + kTileKeys <= view.ref + 1);
-      const bool right = MODE == kBiased && __all_sync(0xffffffffu, base + at0 >= view.ref);
-      const bool whole = __all_sync(0xffffffffu, there == 255u && lo_r <= at0 && hi_r >= at0 + kTileKeys);
+      const bool left = MODE == kBiased && __all_sync(0xffffffffu, at0 + kTileKeys <= ref_r + 1);
+      const bool right = MODE == kBiased && __all_sync(0xffffffffu, at0 >= ref_r);
+      const bool whole = __all_sync(0xffffffffu, there == 255u && ((lo_r <= at0 && hi_r >= at0 + kTileKeys) ||
+                                                                   (MODE != kPlain && none)));
       auto rescale_o = [&](float f) {
         const uint64_t f2 = ptx::f2_pack(f, f);
 #pragma unroll 1
@@ -766,18 +787,18 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
         } else {
           // (the first weights have no base yet, and distances from one that is far
           // out are with_ev's)
-          bool low = whole && (MODE == kBiased ? __all_sync(0xffffffffu, fabsf(m) <= kFarBase) != 0 : !shape.biased);
+          bool low = whole && (MODE == kBiased ? __all_sync(0xffffffffu, fabsf(m) <= kFarBase) != 0 : !biased);
           hat = wide;
           sum = 0.f;
           if (MODE == kBiased) {
             // (left of every row's reference place, or right of them all)
-            const float step = !shape.biased ? 0.f : left ? shape.slope2 : -shape.slope2;
-            low = low && (!shape.biased || left || right);
+            const float step = left ? slope2 : -slope2;
+            low = low && (!biased || left || right);
             if (low) {
               uint32_t cur[64];
               ptx::tmem_ld64(t_h, cur);
-              if (shape.biased) {
-                const float d0 = (float)(view.ref - (base + at0 + 64 * half));
+              if (biased) {
+                const float d0 = (float)(ref_r - (at0 + 64 * half));
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                   float b;
@@ -809,9 +830,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
               if (!low) break;
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
-                const LowCap lc = low_cap(k == 0 ? c0 : c1, shape.cap2);
+                const LowCap lc = low_cap(k == 0 ? c0 : c1, cap2);
                 float b;
-                exp_low_block(cur + 16 * k, lc, lds_f(mh + kMetaShift + 4 * (2 * i + k)) - m, pk[i] + 8 * k, b);
+                exp_low_block<false>(cur + 16 * k, lc, lds_f(mh + kMetaShift + 4 * (2 * i + k)) - m, 0u, pk[i] + 8 * k, b);
                 hat += b;
                 sum = fmaf(b, lds_f(mh + kMetaInv + 4 * (2 * i + k)), sum);
               }
@@ -823,7 +844,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
             ptx::tmem_st_wait();
           } else {
             const int at_h = at0 + 64 * half;
-            const HalfRow hr{t_h, mh, there >> (4 * half), lo_r - at_h, hi_r - at_h, view.ref - (base + at_h), cq, shape};
+            const HalfRow hr{t_h, mh, there >> (4 * half), lo_r - at_h, hi_r - at_h, ref_r - at_h, cq, RowShape{cap2, slope2, biased}};
             // a single weight up to 2^15 still fits FP16; but a sum that was too
             // large for the short way above must not be so again and again
             float f = 1.f;
@@ -853,6 +874,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
     if (ok) ok = page_wait(BAR(kCbODone), 0, lim, abort, a.status);
     ok = __all_sync(0xffffffffu, ok && !*abort);
     ptx::tc_fence_after();
+    if (none) {
+      m = kLowest;
+      l = 0.f;
+    }
     // NQ = 1: the second group's share goes through shared memory, whose tiles
     // nobody reads any more
     const bool mine = n_t > (NQ == 2 ? 0 : q);   // the group had tiles
@@ -903,8 +928,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
         }
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
-          float x = __uint_as_float(v[k]) * f0;
-          if (NQ == 1 && f1 != 0.f) x = fmaf(lds_f(part_at + (32 * c + k) * 512), f1, x);
+          float x = none ? 0.f : __uint_as_float(v[k]) * f0;
+          if (NQ == 1 && f1 != 0.f && !none) x = fmaf(lds_f(part_at + (32 * c + k) * 512), f1, x);
           v[k] = __float_as_uint(x);
         }
         if (part) {
@@ -944,7 +969,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
       }
       if (store) {
         if (part) *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(m, l);
-        else if (a.lse != nullptr) a.lse[orow] = lse_of(m, l) + (MODE != kPlain ? ref_bias(a, view, hq) : 0.f);
+        else if (a.lse != nullptr) a.lse[orow] = lse_of(m, l) + (MODE != kPlain ? ref_bias(a, row_view(a, b, r0 + tok, t0 + tok, len), hq) : 0.f);
       }
     }
   } else if (warp < C::kMmaWarp) {

@@ -599,6 +599,7 @@ __device__ __forceinline__ void store_row(const PagedAttnArgs& a, const SeqWork&
   for (int k = 0; k < CH / 2; ++k) {
     const __nv_bfloat162 z = __floats2bfloat162_rn(o[nt][k][c] * f, o[nt][k][c + 2] * f);
     v[k] = *reinterpret_cast<const uint32_t*>(&z);
+    if (MODE != kPlain && l == 0.f) v[k] = 0u;   // (zero weights times a NaN that other rows attend to)
   }
   uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + CH * g);
 #pragma unroll

@@ -282,6 +282,47 @@ def test_not_finite_rows_and_seen_keys(rows):
     assert torch.equal(nan.all(-1), want) and torch.equal(nan.any(-1), want) and torch.equal(torch.isnan(lse).cpu(), want)
 
 
+@pytest.mark.parametrize("rows", [2, 70, 300])
+@pytest.mark.parametrize("softcap,slope", [(0.0, 0.0), (5.0, 0.0), (0.0, 0.01), (5.0, 0.01)])
+@pytest.mark.parametrize("nan", [False, True])
+def test_rows_that_see_nothing_beside_rows_that_see_all(rows, softcap, slope, nan):
+    """Padding rows in the middle of others, whole tiles around them: zero and
+    -infinity, also where a value that the others attend to is a NaN."""
+    d, page, lens = 128, 64, [640]
+    rng, codes, exps, table = pool_case(17, lens, page, 2, d, e_lo=-9, e_hi=-6)
+    q = rows_of(rng, rows, 2, d)
+    ranges = np.tile([[0, 640]], (rows, 1))
+    ranges[1::3] = [[0, 0]]
+    if nan:
+        codes = [c.clone() for c in codes]
+        codes[1][0, table[0][2], :, 5, 7] = 0x7F
+    s = dev(np.full(2, slope), torch.float32)
+    out, lse = kvq.paged_attention(cache_of(codes, exps), q.cuda(), dev(table), dev(lens), offsets_of([rows]), scale=0.1,
+                                   causal=False, with_lse=True, max_q=rows, softcap=softcap, slopes=s, ranges=dev(ranges))
+    clean()
+    assert (out[1::3] == 0).all() and (lse[1::3] == -np.inf).all()
+    assert torch.isnan(out[0::3, :, 7]).all() if nan else torch.isfinite(out[0::3]).all()
+    if not nan:
+        pool = P.Pool([c[0].numpy() for c in codes], [e[0] for e in exps])
+        ref = P.attention_scored(pool, q.double().numpy(), table, lens, [rows], 0.1, False, 0, softcap, np.full(2, slope), ranges=ranges)
+        check((out, lse), ref, d, 640, softcap)
+
+
+def test_rows_that_see_nothing_in_many_sequences():
+    """The same in the line of all keys, single tokens and pairs of 160 sequences."""
+    d, page, batch = 64, 32, 160
+    lens = [64] * batch
+    rng, codes, exps, table = pool_case(18, lens, page, 2, d, e_lo=-9, e_hi=-6)
+    q = rows_of(rng, 2 * batch, 2, d)
+    ranges = np.tile([[0, 64], [7, 7]], (batch, 1))
+    codes = [c.clone() for c in codes]
+    codes[1][0, table[:, 0], :, 5, 7] = 0x7F
+    out, lse = kvq.paged_attention(cache_of(codes, exps), q.cuda(), dev(table), dev(lens), offsets_of([2] * batch), scale=0.1,
+                                   causal=False, with_lse=True, max_q=2, softcap=5.0, ranges=dev(ranges))
+    clean()
+    assert (out[1::2] == 0).all() and (lse[1::2] == -np.inf).all() and torch.isnan(out[0::2, :, 7]).all()
+
+
 @pytest.mark.parametrize("rows", [1, 5, 70, 300])
 @pytest.mark.parametrize("power", [12, 30])
 def test_scores_beyond_every_bias(rows, power):
