@@ -50,17 +50,18 @@
 // Shaped scores (MODE): the mathematics is in kvq_scores.cuh; what differs here is
 // the softmax.  The products are the same, the instructions per score are not, and
 // they decide: two warps a scheduler, whose largest stall is the wait for their own
-// results, tensor pipe 39 % active with a cap and 56 without.  A half tile takes
+// results, tensor pipe 40 % active with a cap and 56 without.  A half tile takes
 // one of two ways.  The straight one, 64 scores in registers, is for keys that all
 // rows of the warp see: plain scores, a bias that falls or rises along the tile, a
 // cap and scores up to 0.4 of it (their largest magnitude comes with the load from
 // tensor memory, tcgen05.ld.red).  The other one, for masks, hot scores, new bases
 // and distances from far bases, is a pair of functions out of line that loop over
 // the scores in tensor memory, so short that they stay in the instruction buffers:
-// unrolled by another two they take a sixth longer.  8000 rows of 32 heads over 8
-// and as many keys, no mask, us: plain 809, biased 930, capped 1134 to 1190, capped
-// with scores up to 0.9 of the cap 2217.  24 heads of 4680 rows, 23400 keys, capped:
-// 1.29 to 1.37 ms, 0.98 to 1.05 PFLOP/s.
+// unrolled by another two they take a sixth longer, and with more registers they
+// have the straight way's spilled (10 % of that).  8000 rows of 32 heads over 8 and
+// as many keys, no mask, us: plain 808, biased 940, capped 1165, capped with scores
+// up to 0.9 of the cap 2190.  24 heads of 4680 rows, 23400 keys, capped: 1.35 ms,
+// 1.0 PFLOP/s.
 #pragma once
 
 #include <math_constants.h>
@@ -818,8 +819,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
               }
             }
           } else if (low) {
-            // 32 at a time, a vote each, without a look at whether two pages have
-            // one scale: 1.35 ms, not 1.38 (the 4680 rows above)
+            // (32 at a time, a vote each, without a look at whether two pages have
+            // one scale: 1.35 ms, not 1.38, of the 4680 rows above)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               uint32_t cur[32];
