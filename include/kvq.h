@@ -558,7 +558,8 @@ kvq_status kvq_rope_fill(const kvq_rope_table *table, const double *frequency, d
 /* One tensor of a kvq_rope call: row i of batch entry b and head h at b *
  * batch_stride + i * row_stride + h * head_stride elements (multiples of 8;
  * head_dim contiguous), 16-byte aligned.  y == x with the same strides (in
- * place) or memory that does not overlap it. */
+ * place; with others the call is refused) or memory that overlaps no tensor of
+ * the call. */
 typedef struct kvq_rope_tensor {
   const uint16_t *x;
   uint16_t *y;
@@ -586,8 +587,8 @@ kvq_status kvq_rope(const kvq_rope_table *table, const int32_t *positions, int64
  * page's maximum from fp32, rounded once.  positions: int32 [rows][axes]
  * device (rows pos_row_stride elements apart, axes next to each other), or
  * NULL where axes == 1: the tokens' places in their sequences, kv_lens[b] -
- * n_b + i.  q: BF16 as in kvq_paged_attention, rotated into q_out (in place or
- * apart, strides of its own); NULL with q_heads = 0 for none.  Rows before
+ * n_b + i.  q: BF16 as in kvq_paged_attention, rotated into q_out: q itself with
+ * its strides, or memory that overlaps no input; NULL with q_heads = 0 for none.  Rows before
  * offsets[0] and at or behind offsets[batch] are neither read nor written.
  * rows * q_heads <= 2^32 (else KVQ_ERR_TOO_LARGE).  Everything else as
  * kvq_pages_append says.

@@ -277,7 +277,16 @@ kvq_status kvq_rope(const kvq_rope_table* table, const int32_t* positions, int64
         bad_stride(t.x_head_stride) || bad_stride(t.y_batch_stride) || bad_stride(t.y_row_stride) ||
         bad_stride(t.y_head_stride))
       return KVQ_ERR_ALIGNMENT;
+    // in place means place by place
+    if (t.x == t.y && ((batch > 1 && t.x_batch_stride != t.y_batch_stride) ||
+                       (rows > 1 && t.x_row_stride != t.y_row_stride) ||
+                       (t.heads > 1 && t.x_head_stride != t.y_head_stride)))
+      return KVQ_ERR_INVALID_ARG;
   }
+  // nothing is written that the other tensor reads or writes
+  if (n_tensors == 2 && tensors[0].heads != 0 && tensors[1].heads != 0 &&
+      (tensors[0].y == tensors[1].x || tensors[0].y == tensors[1].y || tensors[1].y == tensors[0].x))
+    return KVQ_ERR_INVALID_ARG;
   a.t = rope_of(table);
   a.pos = positions;
   a.pb = pos_batch_stride;
@@ -317,6 +326,11 @@ kvq_status kvq_pages_append_rope(const kvq_pages* pages, int32_t layer, const kv
       (((long long)(seqs->rows >> p.a.p.shift) + 2LL * seqs->batch) * pages->kv_heads * 2 +
        (long long)seqs->rows * q_heads * (pages->head_dim / 16) / 32 + 1) > 0x7fffffffLL)
     return KVQ_ERR_TOO_LARGE;
+  // queries in place are so place by place, and no key or value is written
+  if (q != nullptr && ((q == q_out && ((seqs->rows > 1 && q_row_stride != q_out_row_stride) ||
+                                       (q_heads > 1 && q_head_stride != q_out_head_stride))) ||
+                       q_out == k_new || q_out == v_new))
+    return KVQ_ERR_INVALID_ARG;
   p.a.status = kvq::status_ptr();
   p.a.bounds_site = kvq::bounds_site_ptr();
   if (p.a.status == nullptr) return KVQ_ERR_CUDA;

@@ -202,6 +202,14 @@ def test_refusals_on_the_device():
             kvq.rope(t, x, pos, q_out=bad)
     with pytest.raises(ValueError, match="repeat"):
         kvq.rope(t, x, pos, q_out=x[:1].expand(5, 2, 64))
+    y = x.clone()
+    shared = [dict(q_out=x.as_strided((5, 2, 64), (64, 320, 1))), dict(k=y, q_out=x, k_out=x), dict(k=y, q_out=y),
+              dict(k=y, k_out=x)]
+    for kw in shared:                                             # in place, but other places; the other tensor's memory
+        with pytest.raises(kvq.KVQError) as e:
+            kvq.rope(t, x, pos, **kw)
+        assert e.value.status == kvq.KVQ_ERR_INVALID_ARG
+    assert torch.equal(kvq.rope(t, y[:1], pos[:1], q_out=y.as_strided((1, 2, 64), (4096, 64, 1))), kvq.rope(t, x[:1], pos[:1]))
     with pytest.raises(ValueError, match="contiguous channels"):
         kvq.rope(t, x.transpose(1, 2), pos)
     with pytest.raises(ValueError, match="without k"):

@@ -135,6 +135,9 @@ def test_rope_refusals(lib):
     assert _rope(lib, x=PTR + 8) == 6 and _rope(lib, y=PTR + 2) == 6
     for field in ("x_batch_stride", "x_row_stride", "x_head_stride", "y_batch_stride", "y_row_stride", "y_head_stride"):
         assert _rope(lib, **{field: 12}) == 6 and _rope(lib, **{field: -8}) == 6
+    assert _rope(lib, y_batch_stride=4096, batch=2) == 1         # in place, but other places
+    assert _rope(lib, y_row_stride=4096) == 1 and _rope(lib, y_head_stride=4096) == 1
+    assert _rope(lib, n=2) == 1                                  # one writes what the other writes
     assert _rope(lib, rows=0) == 0 and _rope(lib, batch=0) == 0 and _rope(lib, heads=0, x=None, y=None) == 0
     assert _rope(lib, batch=1 << 16, rows=1 << 16) == kvq.KVQ_ERR_TOO_LARGE
     assert _rope(lib, rows=1 << 30, heads=64) == kvq.KVQ_ERR_TOO_LARGE
@@ -150,6 +153,9 @@ def test_append_refusals(lib):
     assert _append(lib, q=PTR + 8) == 6 and _append(lib, out=PTR + 8) == 6 and _append(lib, pos=PTR + 2) == 6
     assert _append(lib, qs=(12, 128)) == 6 and _append(lib, outs=(1024, -128)) == 6
     assert _append(lib, _table(axes=3)) == 1                     # several axes need positions
+    apart = dict(k=PTR + (1 << 20), v=PTR + (1 << 21))
+    assert _append(lib, outs=(2048, 128), **apart) == 1 and _append(lib, outs=(1024, 256), **apart) == 1
+    assert _append(lib, k=PTR + (1 << 20)) == 1 and _append(lib, v=PTR + (1 << 21)) == 1   # queries over the values, the keys
     assert _append(lib, s=_seqs(rows=0, batch=0)) == 0
     assert _append(lib, s=_seqs(rows=1 << 30, batch=2, offsets=PTR), heads=64, qs=(8192, 128), outs=(8192, 128)) == kvq.KVQ_ERR_TOO_LARGE
     for fields, status in ((dict(batch=-1), 1), (dict(table=None), 1), (dict(table_stride=4), 1), (dict(kv_lens=PTR + 1), 6)):
