@@ -633,9 +633,11 @@ typedef struct kvq_scores {
  * a place holds matters to nobody when no row of the sequence's query heads
  * attends there, also between ranges, and pages before and behind all of them
  * are not looked up.  A capped score is off by 2^-20 of the cap at most, for
- * caps above 256 by 2^-21 of itself; a bias and its sum with the score have the
- * rounding of fp32, the distance counted from the nearest key that the row
- * attends to.  lse = log sum_j exp(s_j) of the shaped scores.
+ * caps above 256 by 2^-21 of itself; a bias and its sum with the score are off by
+ * a few 2^-24 of their largest over the row's keys and 64 beside them, the
+ * distance counted from the nearest key that the row attends to (1.5 * |slope| *
+ * 2^-16 of an exponent there; slope times distance must stay within fp32).  lse
+ * = log sum_j exp(s_j) of the shaped scores.
  */
 kvq_status kvq_paged_attention_scored(const kvq_pages *pages, int32_t layer, const uint16_t *q,
                                       int64_t q_row_stride, int64_t q_head_stride, int32_t q_heads,
