@@ -916,7 +916,11 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
       f1 *= f;
       const long long prow = (long long)split * a.s.rows * a.q_heads + orow;
       // the warp's rows of the output, in the query tiles' place: rows a lane leave
-      // it as whole rows
+      // it as whole rows.  It lies over query rows that other warps write and the
+      // tensor core reads.  kCbODone is behind both: its commit comes after every
+      // product, and the MMA thread's first act is to wait for kCbQ, on which each
+      // warp arrives when its query rows are written, whether the CTA has key
+      // tiles or not.
       const uint32_t room = sm + C::kQ + (uint32_t)warp * (32 * 2 * D);
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
@@ -1045,7 +1049,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
       const uint64_t d8 = ptx::smem_desc(s_base, 16, 8 * D, kLay);       // E4M3 rows of D bytes
       const uint64_t dv = ptx::smem_desc(s_base, 16384, 1024, ptx::kLayoutSw128);
       auto plus = [](uint64_t d, uint32_t off) { return d + (uint64_t)(off >> 4); };
-      bool ok = n_t == 0 || page_wait(BAR(kCbQ), 0, lim, abort, a.status);
+      // (a CTA without key tiles waits too: the softmax warps' output takes the
+      // query tiles' place once kCbODone has come)
+      bool ok = page_wait(BAR(kCbQ), 0, lim, abort, a.status);
       auto qk = [&](int ks, int q, uint32_t dst) {
         const uint64_t db = plus(d8, C::kK + ks * C::kKT);
 #pragma unroll
