@@ -208,17 +208,17 @@ __device__ __forceinline__ void exp_block(const uint32_t* s, float scale, float 
   ptx::f2_unpack(acc, x, y);
   sum = x + y;
 }
-// the same of 16 raw scores that stay below 0.4 of their cap; masked: only of
-// those whose bit is set
+// the same of 16 raw scores that stay below 0.4 of their cap; ck: their factor;
+// masked: only of those whose bit is set
 template <bool MASKED>
-__device__ __forceinline__ void exp_low_block(const uint32_t* s, const LowCap& c, float shift, uint32_t seen, uint32_t* pk,
-                                              float& sum) {
+__device__ __forceinline__ void exp_low_block(const uint32_t* s, float ck, const LowCap& c, float shift, uint32_t seen,
+                                              uint32_t* pk, float& sum) {
   const uint64_t b2 = ptx::f2_pack(shift, shift);
   uint64_t acc = ptx::f2_pack(0.f, 0.f);
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     float x0, x1;
-    ptx::f2_unpack(low_scores(ptx::f2_pack(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), c, b2), x0, x1);
+    ptx::f2_unpack(low_scores(ptx::f2_pack(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), ck, c, b2), x0, x1);
     if (MASKED) {
       x0 = seen & (1u << (2 * k)) ? x0 : -CUDART_INF_F;
       x1 = seen & (2u << (2 * k)) ? x1 : -CUDART_INF_F;
@@ -383,14 +383,14 @@ __device__ __noinline__ float shaped_weights(HalfRow h, float m) {
     float most;
     ptx::tmem_ld32_max(h.t_h + 16 * k, v, most);
     const float ck_most = h.cq * fmaxf(lds_f(h.mh + 4 * k), lds_f(h.mh + 4 * k + 4));
-    const bool low = __all_sync(0xffffffffu, most * ck_most <= kLowX && ck_most <= kLowMost) && cap;
+    const bool low = __all_sync(0xffffffffu, most * ck_most <= kLowX) && cap;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float raw = h.cq * lds_f(h.mh + 4 * (k + i)), shift = lds_f(h.mh + kMetaShift + 4 * (k + i)) - m;
       const uint32_t seen = MASKED ? bits_within((h.there >> (k + i)) & 1u ? h.lo - 16 * (k + i) : 16, h.hi - 16 * (k + i)) : 0u;
       float b;
       if (MASKED && low) {   // (an unmasked half that is low did not come here, or for its base alone)
-        exp_low_block<MASKED>(v + 16 * i, low_cap(raw, h.shape.cap2), shift, seen, w + 8 * i, b);
+        exp_low_block<MASKED>(v + 16 * i, raw, low_cap(h.shape.cap2), shift, seen, w + 8 * i, b);
       } else if (far) {
         exp_far_block<MASKED>(v + 16 * i, raw, h.shape.cap2, shift, seen, w + 8 * i, b);
       } else {
@@ -827,13 +827,12 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
               float most;
               ptx::tmem_ld32_max(t_h + 32 * i, cur, most);
               const float c0 = cq * lds_f(mh + 8 * i), c1 = cq * lds_f(mh + 8 * i + 4), ck_most = fmaxf(c0, c1);
-              low = __all_sync(0xffffffffu, most * ck_most <= kLowX && ck_most <= kLowMost && fabsf(m) <= kFarBase);
+              low = __all_sync(0xffffffffu, most * ck_most <= kLowX && fabsf(m) <= kFarBase);
               if (!low) break;
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
-                const LowCap lc = low_cap(k == 0 ? c0 : c1, cap2);
                 float b;
-                exp_low_block<false>(cur + 16 * k, lc, lds_f(mh + kMetaShift + 4 * (2 * i + k)) - m, 0u, pk[i] + 8 * k, b);
+                exp_low_block<false>(cur + 16 * k, k == 0 ? c0 : c1, low_cap(cap2), lds_f(mh + kMetaShift + 4 * (2 * i + k)) - m, 0u, pk[i] + 8 * k, b);
                 hat += b;
                 sum = fmaf(b, lds_f(mh + kMetaInv + 4 * (2 * i + k)), sum);
               }

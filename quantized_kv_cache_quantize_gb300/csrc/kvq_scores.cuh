@@ -96,28 +96,28 @@ __device__ __forceinline__ float raw_factor(const PagedAttnArgs& a) {
   return MODE == kCapped ? a.scale / a.shape.cap : a.scale * 1.4426950408889634f;
 }
 
-// Up to 0.4 of the cap four terms do, and fold: with the row's and page's factor
-// ck in the coefficients, the shaped score in units of log 2 is s (c0 + c1 s^2 +
-// c2 s^4 + c3 s^6) of the raw score s, its last product the one that also adds
-// what stands in the exponent beside it: four products on pairs more than a plain
-// score has, where the seven terms take nine (24 heads of 4680 rows, 23400 keys:
-// 1.35 against 1.67 ms).  ck is held below kLowMost so that ck^7 stays in fp32;
-// larger ones take the way of larger scores.
-constexpr float kLowX = 0.4f, kLowMost = 16384.f;
+// Up to 0.4 of the cap four terms do, and fold with what follows: with the cap in
+// the coefficients the shaped score in units of log 2 is x (c0 + c1 x^2 + c2 x^4 +
+// c3 x^6), x the score over the cap, its last product the one that also adds what
+// stands in the exponent beside it: five products on pairs more than a plain score
+// has, where the seven terms take nine.  (The row's and page's factor ck must stay
+// out of the coefficients: raw scores of codes reach 1.5e7, ck 3e-8 where x is still
+// 0.4, and a c3 that holds ck^7 is lost to fp32's range, 2^-14 of the cap.)
+constexpr float kLowX = 0.4f;
 struct LowCap {
   float c0, c1, c2, c3;
 };
-__device__ __forceinline__ LowCap low_cap(float ck, float cap2) {
-  const float k2 = ck * ck, k0 = cap2 * ck, k4 = k0 * k2, k6 = k4 * k2;
-  return LowCap{9.999998808e-01f * k0, -3.333135545e-01f * k4, 1.327087432e-01f * k6, -4.754934832e-02f * (k6 * k2)};
+__device__ __forceinline__ LowCap low_cap(float cap2) {
+  return LowCap{9.999998808e-01f * cap2, -3.333135545e-01f * cap2, 1.327087432e-01f * cap2, -4.754934832e-02f * cap2};
 }
-__device__ __forceinline__ uint64_t low_scores(uint64_t s, const LowCap& c, uint64_t beside) {
+// of raw scores s times ck
+__device__ __forceinline__ uint64_t low_scores(uint64_t s, float ck, const LowCap& c, uint64_t beside) {
   auto both = [](float x) { return ptx::f2_pack(x, x); };
-  const uint64_t z = ptx::f2_mul(s, s);
+  const uint64_t x = ptx::f2_mul(s, both(ck)), z = ptx::f2_mul(x, x);
   uint64_t p = ptx::f2_fma(both(c.c3), z, both(c.c2));
   p = ptx::f2_fma(p, z, both(c.c1));
   p = ptx::f2_fma(p, z, both(c.c0));
-  return ptx::f2_fma(p, s, beside);
+  return ptx::f2_fma(p, x, beside);
 }
 
 // The same for any score, by cap2 (1 - 2 / (1 + t)), t = 2^(2 x log2 e), alone: off
