@@ -232,7 +232,8 @@ __device__ __forceinline__ void exp_low_block(const uint32_t* s, float ck, const
   sum = x + y;
 }
 // the same of any 16 raw scores under a short cap; ck: their factor; masked: only
-// of those whose bit is set
+// of those whose bit is set (the others are zeros: what they held would reach
+// their neighbours)
 template <bool MASKED>
 __device__ __forceinline__ void exp_far_block(const uint32_t* s, float ck, float cap2, float shift, uint32_t seen,
                                               uint32_t* pk, float& sum) {
@@ -241,10 +242,8 @@ __device__ __forceinline__ void exp_far_block(const uint32_t* s, float ck, float
   uint64_t acc = ptx::f2_pack(0.f, 0.f);
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    // (what a masked key holds must not reach its neighbour)
-    const uint32_t s0 = !MASKED || seen & (1u << (2 * k)) ? s[2 * k] : 0u, s1 = !MASKED || seen & (2u << (2 * k)) ? s[2 * k + 1] : 0u;
     float x0, x1;
-    ptx::f2_unpack(far_scores(ptx::f2_pack(__uint_as_float(s0), __uint_as_float(s1)), ct, f2, b2), x0, x1);
+    ptx::f2_unpack(far_scores(ptx::f2_pack(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), ct, f2, b2), x0, x1);
     if (MASKED) {
       x0 = seen & (1u << (2 * k)) ? x0 : -CUDART_INF_F;
       x1 = seen & (2u << (2 * k)) ? x1 : -CUDART_INF_F;
@@ -380,14 +379,32 @@ __device__ __noinline__ float shaped_weights(HalfRow h, float m) {
 #pragma unroll 1
   for (int k = 0; k < 4; k += 2) {
     uint32_t v[32], w[16];
-    float most;
-    ptx::tmem_ld32_max(h.t_h + 16 * k, v, most);
-    const float ck_most = h.cq * fmaxf(lds_f(h.mh + 4 * k), lds_f(h.mh + 4 * k + 4));
-    const bool low = __all_sync(0xffffffffu, most * ck_most <= kLowX) && cap;
+    ptx::tmem_ld32(h.t_h + 16 * k, v);
+    auto seen_of = [&](int i) {
+      return MASKED ? bits_within((h.there >> (k + i)) & 1u ? h.lo - 16 * (k + i) : 16, h.hi - 16 * (k + i)) : 0u;
+    };
+    // (what a masked key holds, or its page's scale, decides nothing, the way among
+    // these least: zeros, and the largest of the others)
+    bool low = MASKED && cap;
+    if (low) {
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t seen = seen_of(i);
+        float most = 0.f;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          v[16 * i + c] = seen & (1u << c) ? v[16 * i + c] : 0u;
+          most = fmaxf(most, fabsf(__uint_as_float(v[16 * i + c])));
+        }
+        top = fmaxf(top, most * (h.cq * lds_f(h.mh + 4 * (k + i))));
+      }
+      low = __all_sync(0xffffffffu, top <= kLowX);
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float raw = h.cq * lds_f(h.mh + 4 * (k + i)), shift = lds_f(h.mh + kMetaShift + 4 * (k + i)) - m;
-      const uint32_t seen = MASKED ? bits_within((h.there >> (k + i)) & 1u ? h.lo - 16 * (k + i) : 16, h.hi - 16 * (k + i)) : 0u;
+      const uint32_t seen = seen_of(i);
       float b;
       if (MASKED && low) {   // (an unmasked half that is low did not come here, or for its base alone)
         exp_low_block<MASKED>(v + 16 * i, raw, low_cap(h.shape.cap2), shift, seen, w + 8 * i, b);
