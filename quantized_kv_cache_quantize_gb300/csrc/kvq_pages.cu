@@ -238,7 +238,7 @@ int sm_count_current() {
 
 cudaError_t launch_pages_append(const AppendArgs& a, cudaStream_t stream) {
   const bool one = a.s.offsets == nullptr;
-  const long long items = one ? a.s.batch : (a.s.rows >> a.p.shift) + 2LL * a.s.batch;
+  const long long items = one ? a.s.batch : append_items(a.s.rows, a.s.batch, a.p.shift);
   const long long units = items * a.p.heads * 2;
   if (units == 0) return cudaSuccess;
   if (one) {

@@ -7,6 +7,7 @@ namespace kvq {
 
 constexpr int kPageExpMin = -60, kPageExpMax = 60;   // scale exponents
 constexpr int kRopeMaxPairs = 64, kRopeMaxAxes = 4;
+constexpr int kRopeHeads = 8;                        // of one block of a rotation
 constexpr int kCompactMaxPages = 1 << 20;            // the plan's bitmap fits shared memory
 
 // One layer of a pool.
@@ -51,6 +52,12 @@ struct RopeTensor {
   int heads;
 };
 
+// Blocks of a rotation of rows x heads, `tile` rows and kRopeHeads heads each.  (In
+// 64 bits: a call may have 2^31 - 1 rows, or heads.)
+inline long long rope_blocks(long long rows, long long heads, int tile) {
+  return (rows + tile - 1) / tile * ((heads + kRopeHeads - 1) / kRopeHeads);
+}
+
 struct RopeArgs {
   RopeTab t;
   const int32_t* pos;
@@ -59,6 +66,16 @@ struct RopeArgs {
   int batch, rows, d, inverse;
   int* status;
 };
+
+// Pages that an append with offsets looks at (see append_item), and the rows of a
+// block of queries beside it (a page of 16 tokens has too few threads for 16).
+inline long long append_items(long long rows, long long batch, int shift) { return (rows >> shift) + 2 * batch; }
+inline int append_query_rows(bool one_token, int page) { return one_token || page == 16 ? 4 : 16; }
+// Blocks of an append that rotates, at most: keys and values a page and head, queries.
+inline long long append_rope_blocks(const PageSeqs& s, const PageLayer& p, long long q_heads) {
+  return append_items(s.rows, s.batch, p.shift) * p.heads * 2 +
+         rope_blocks(s.rows, q_heads, append_query_rows(s.offsets == nullptr, p.page));
+}
 
 struct AppendRopeArgs {
   AppendArgs a;

@@ -253,19 +253,18 @@ kvq_status kvq_rope(const kvq_rope_table* table, const int32_t* positions, int64
   if (st != KVQ_OK) return st;
   if (batch < 0 || rows < 0 || tensors == nullptr || n_tensors < 1 || n_tensors > 2) return KVQ_ERR_INVALID_ARG;
   kvq::RopeArgs a{};
-  long long heads = 0, groups = 0;
+  long long heads = 0, blocks = 0;
   for (int i = 0; i < n_tensors; ++i) {
     const kvq_rope_tensor& t = tensors[i];
     if (t.heads < 0) return KVQ_ERR_INVALID_ARG;
     heads += t.heads;
-    groups += ((long long)t.heads + 7) / 8;
     a.x[i] = kvq::RopeTensor{t.x, t.y, t.x_batch_stride, t.x_row_stride, t.x_head_stride,
                              t.y_batch_stride, t.y_row_stride, t.y_head_stride, t.heads};
   }
   const long long all = (long long)batch * rows;
   if (all > 0x7fffffffLL || heads > 0x7fffffffLL || (all > 0 && heads > (1LL << 35) / all)) return KVQ_ERR_TOO_LARGE;
-  const long long tiles = (long long)batch * (((long long)rows + 15) / 16);   // of 16 rows; a block each, and eight heads
-  if (tiles > 0 && groups > 0x7fffffffLL / tiles) return KVQ_ERR_TOO_LARGE;
+  for (int i = 0; i < n_tensors; ++i) blocks += batch * kvq::rope_blocks(rows, tensors[i].heads, 16);
+  if (blocks > 0x7fffffffLL) return KVQ_ERR_TOO_LARGE;
   if (all == 0 || heads == 0) return KVQ_OK;
   if (positions == nullptr) return KVQ_ERR_INVALID_ARG;
   if (!aligned(positions, 4)) return KVQ_ERR_ALIGNMENT;
@@ -321,10 +320,7 @@ kvq_status kvq_pages_append_rope(const kvq_pages* pages, int32_t layer, const kv
     return KVQ_ERR_ALIGNMENT;
   st = append_args(pages, layer, k_new, k_row_stride, k_head_stride, v_new, v_row_stride, v_head_stride, seqs, &p.a, &done);
   if (st != KVQ_OK || done) return st;
-  // blocks of the launch: two per page and head, and those of the queries
-  if ((long long)seqs->rows * q_heads > (1LL << 32) ||
-      (((long long)(seqs->rows >> p.a.p.shift) + 2LL * seqs->batch) * pages->kv_heads * 2 +
-       (long long)seqs->rows * q_heads * (pages->head_dim / 16) / 32 + 1) > 0x7fffffffLL)
+  if ((long long)seqs->rows * q_heads > (1LL << 32) || kvq::append_rope_blocks(p.a.s, p.a.p, q_heads) > 0x7fffffffLL)
     return KVQ_ERR_TOO_LARGE;
   // queries in place are so place by place, and no key or value is written
   if (q != nullptr && ((q == q_out && ((seqs->rows > 1 && q_row_stride != q_out_row_stride) ||

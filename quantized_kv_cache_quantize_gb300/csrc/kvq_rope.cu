@@ -45,8 +45,8 @@ __global__ void __launch_bounds__(256, 4) rope_kernel(const __grid_constant__ Ro
   ptx::grid_dependency_wait();
   ptx::launch_dependents();
   const unsigned tiles = ((unsigned)a.rows + R - 1) / R;
-  const unsigned q_groups = (unsigned)(a.x[0].heads + kRopeHeads - 1) / kRopeHeads,
-                 groups = q_groups + (unsigned)(a.x[1].heads + kRopeHeads - 1) / kRopeHeads;
+  const unsigned q_groups = ((unsigned)a.x[0].heads + kRopeHeads - 1) / kRopeHeads,
+                 groups = q_groups + ((unsigned)a.x[1].heads + kRopeHeads - 1) / kRopeHeads;
   unsigned g = blockIdx.x % groups;
   const unsigned rest = blockIdx.x / groups;
   const int row0 = (int)(rest % tiles) * R;
@@ -77,7 +77,7 @@ __device__ __forceinline__ int seq_of_row(const PageSeqs& s, int r) {
 template <int D, int R, int N, bool INTER>
 __device__ __forceinline__ void append_queries(const AppendRopeArgs& p, unsigned at, float4* turns) {
   const PageSeqs& s = p.a.s;
-  const unsigned groups = (unsigned)(p.q.heads + kRopeHeads - 1) / kRopeHeads;
+  const unsigned groups = ((unsigned)p.q.heads + kRopeHeads - 1) / kRopeHeads;
   const int h0 = (int)(at % groups) * kRopeHeads;
   int row0 = (int)(at / groups) * R, end = min(row0 + R, s.rows);
   if (s.offsets != nullptr) {   // rows that no sequence has are left alone
@@ -216,7 +216,6 @@ __global__ void __launch_bounds__(512, 2) append_rope_kernel(const __grid_consta
   }
   at -= g.k_blocks;
   if (at < g.q_blocks) {
-    // (a page of 16 tokens has too few threads for 16 rows)
     if (g.q_rows == 16) append_queries<D, 16, 2, INTER>(p, at, turns);
     else append_queries<D, 4, 2, INTER>(p, at, turns);
     return;
@@ -229,7 +228,7 @@ __global__ void __launch_bounds__(512, 2) append_rope_kernel(const __grid_consta
 // a unit of 16 channels each; behind them blocks of query rows.  What counts is
 // the chain of dependent loads: length, position, then turns beside table entry
 // and scale.
-constexpr int kOneRows = 4;
+constexpr int kOneRows = 4;   // append_query_rows
 template <int D, bool INTER>
 __global__ void __launch_bounds__(128) append_one_rope_kernel(const __grid_constant__ AppendRopeArgs p, unsigned kv_blocks) {
   constexpr int U = D / 16;
@@ -312,8 +311,9 @@ cudaError_t launch_rope_fill(float* cos_sin, int n, int pairs, const double* fre
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream) {
   const int sms = sm_count_current();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  const long long groups = (a.x[0].heads + kRopeHeads - 1) / kRopeHeads + (a.x[1].heads + kRopeHeads - 1) / kRopeHeads;
-  auto blocks = [&](int rows) { return (long long)a.batch * ((a.rows + rows - 1) / rows) * groups; };
+  auto blocks = [&](int tile) {
+    return a.batch * (rope_blocks(a.rows, a.x[0].heads, tile) + rope_blocks(a.rows, a.x[1].heads, tile));
+  };
   // few rows: four a block, as long as those do not fill the GPU twice
   const bool few = blocks(4) <= 16LL * sms;
   auto pick = [&](auto inter) {
@@ -329,10 +329,10 @@ cudaError_t launch_pages_append_rope(const AppendRopeArgs& p, cudaStream_t strea
   const AppendArgs& a = p.a;
   const int sms = sm_count_current();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  const long long q_groups = (p.q.heads + kRopeHeads - 1) / kRopeHeads;
+  const int q_rows = append_query_rows(a.s.offsets == nullptr, a.p.page);
+  const long long q_blocks = rope_blocks(a.s.rows, p.q.heads, q_rows);
   if (a.s.offsets == nullptr) {
     const long long kv_blocks = ((long long)a.s.batch * a.p.heads * 2 + 3) / 4;
-    const long long q_blocks = (a.s.rows + kOneRows - 1) / kOneRows * q_groups;
     auto pick = [&](auto inter) {
       constexpr bool I = decltype(inter)::value;
       return a.p.d == 64 ? append_one_rope_kernel<64, I> : append_one_rope_kernel<128, I>;
@@ -340,13 +340,13 @@ cudaError_t launch_pages_append_rope(const AppendRopeArgs& p, cudaStream_t strea
     const auto kern = p.t.interleaved ? pick(std::true_type{}) : pick(std::false_type{});
     return launch_dependent(kern, (unsigned)(kv_blocks + q_blocks), 128, 0, stream, p, (unsigned)kv_blocks);
   }
-  const long long items = (a.s.rows >> a.p.shift) + 2LL * a.s.batch;
+  const long long items = append_items(a.s.rows, a.s.batch, a.p.shift);
   AppendGrid g{};
   g.heads = 8;   // a block of keys, as long as there is one for every SM
   while (g.heads > 1 && items * ((a.p.heads + g.heads - 1) / g.heads) < sms) g.heads /= 2;
   g.k_blocks = (unsigned)(items * ((a.p.heads + g.heads - 1) / g.heads));
-  g.q_rows = a.p.page == 16 ? 4 : 16;
-  g.q_blocks = (unsigned)((a.s.rows + g.q_rows - 1) / g.q_rows * q_groups);
+  g.q_rows = q_rows;
+  g.q_blocks = (unsigned)q_blocks;
   const unsigned v_blocks = (unsigned)(items * a.p.heads);
   const int smem = a.p.page * kRopeRow * (int)sizeof(float4);
   auto pick = [&](auto inter) {

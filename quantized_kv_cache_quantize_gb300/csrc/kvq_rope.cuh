@@ -126,7 +126,6 @@ __device__ __forceinline__ void rope_entries(const float4* row, int u, float4 (&
 // multiple of R * D / 16: a thread has one unit of one row, of N heads at a time.
 // The values are asked for first, then the rows' turns go through shared memory
 // (R * kRopeRow), read once for all heads.  x, y: row 0, head 0.
-constexpr int kRopeHeads = 8;
 template <int D, int R, int N, bool INTER, typename Pos>
 __device__ __forceinline__ void rope_tile(const RopeTab& t, bool inverse, float4* turns, int rows, int heads,
                                           const uint16_t* x, long long xr, long long xh, uint16_t* y, long long yr,
