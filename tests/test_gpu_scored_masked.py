@@ -51,3 +51,28 @@ def test_masked_places_decide_no_bit(d, hq, rows, softcap, slope):
     for held, got in zip(HELD, results):
         for a, b in zip(got, results[0]):
             assert torch.equal(a, b), (held, int((a != b).sum()), float((a.float() - b.float()).abs().max()))
+
+
+@pytest.mark.parametrize("d,hq", [(64, 2), (128, 4)])
+@pytest.mark.parametrize("heat", [1.0, 20.0])
+@pytest.mark.parametrize("lo,hi", [(102, 131), (101, 130), (96, 128), (111, 112)])
+@pytest.mark.parametrize("softcap,slope", [(6.0, 0.0), (0.0, 0.01), (6.0, 0.01)])
+def test_one_row_beside_masked_neighbours(d, hq, heat, lo, hi, softcap, slope):
+    """A single row, the decoding form: NaN in every key and value beside those of
+    its range, which begins and ends at odd and even places."""
+    page, lens = 32, [500]
+    rng, codes, exps, table = pool_case(12, lens, page, 2, d, e_lo=-9, e_hi=-6)
+    q = rows_of(rng, 1, hq, d, heat=heat)
+    s = np.full(hq, slope, np.float32)
+    pool = P.Pool([c[0].numpy() for c in codes], [e[0] for e in exps])
+    ref = P.attention_scored(pool, q.double().numpy(), table, lens, [1], 0.2, False, 0, softcap, s, ranges=np.array([[lo, hi]]))
+    assert np.isfinite(ref[1]).all()
+    codes = [c.clone() for c in codes]
+    for j in list(range(lo)) + list(range(hi, 500)):
+        for c in codes:
+            c[0, table[0][j // page], :, j % page] = 0x7F
+    for off in (offsets_of([1]), None):
+        got = kvq.paged_attention(cache_of(codes, exps), q.cuda(), dev(table), dev(lens), off, scale=0.2, causal=False,
+                                  with_lse=True, max_q=1, softcap=softcap, slopes=dev(s, torch.float32), ranges=dev([[lo, hi]]))
+        clean()
+        check(got, ref, d, hi - lo, softcap, str(off))
