@@ -7,6 +7,7 @@
 #include <cmath>
 #include <vector>
 
+#include "kvq_overlap.h"
 #include "kvq_pages.h"
 
 namespace {
@@ -282,9 +283,18 @@ kvq_status kvq_rope(const kvq_rope_table* table, const int32_t* positions, int64
                        (t.heads > 1 && t.x_head_stride != t.y_head_stride)))
       return KVQ_ERR_INVALID_ARG;
   }
-  // nothing is written that the other tensor reads or writes
-  if (n_tensors == 2 && tensors[0].heads != 0 && tensors[1].heads != 0 &&
-      (tensors[0].y == tensors[1].x || tensors[0].y == tensors[1].y || tensors[1].y == tensors[0].x))
+  // nothing else is written that the call reads or writes
+  auto x_of = [&](int i) {
+    const kvq_rope_tensor& t = tensors[i];
+    return kvq::Strided{t.x, t.x_batch_stride, t.x_row_stride, t.x_head_stride, batch, rows, t.heads, head_dim};
+  };
+  auto y_of = [&](int i) {
+    const kvq_rope_tensor& t = tensors[i];
+    return kvq::Strided{t.y, t.y_batch_stride, t.y_row_stride, t.y_head_stride, batch, rows, t.heads, head_dim};
+  };
+  for (int i = 0; i < n_tensors; ++i)
+    if (tensors[i].x != tensors[i].y && kvq::overlap(x_of(i), y_of(i))) return KVQ_ERR_INVALID_ARG;
+  if (n_tensors == 2 && (kvq::overlap(y_of(0), x_of(1)) || kvq::overlap(y_of(0), y_of(1)) || kvq::overlap(y_of(1), x_of(0))))
     return KVQ_ERR_INVALID_ARG;
   a.t = rope_of(table);
   a.pos = positions;
@@ -322,11 +332,19 @@ kvq_status kvq_pages_append_rope(const kvq_pages* pages, int32_t layer, const kv
   if (st != KVQ_OK || done) return st;
   if ((long long)seqs->rows * q_heads > (1LL << 32) || kvq::append_rope_blocks(p.a.s, p.a.p, q_heads) > 0x7fffffffLL)
     return KVQ_ERR_TOO_LARGE;
-  // queries in place are so place by place, and no key or value is written
-  if (q != nullptr && ((q == q_out && ((seqs->rows > 1 && q_row_stride != q_out_row_stride) ||
-                                       (q_heads > 1 && q_head_stride != q_out_head_stride))) ||
-                       q_out == k_new || q_out == v_new))
-    return KVQ_ERR_INVALID_ARG;
+  // queries in place are so place by place, and nothing else that the call reads is written
+  if (q != nullptr) {
+    auto rows_of = [&](const uint16_t* x, int64_t row, int64_t head, int32_t heads) {
+      return kvq::Strided{x, 0, row, head, 1, seqs->rows, heads, pages->head_dim};
+    };
+    const kvq::Strided out = rows_of(q_out, q_out_row_stride, q_out_head_stride, q_heads);
+    if (q == q_out ? (seqs->rows > 1 && q_row_stride != q_out_row_stride) || (q_heads > 1 && q_head_stride != q_out_head_stride)
+                   : kvq::overlap(out, rows_of(q, q_row_stride, q_head_stride, q_heads)))
+      return KVQ_ERR_INVALID_ARG;
+    if (kvq::overlap(out, rows_of(k_new, k_row_stride, k_head_stride, pages->kv_heads)) ||
+        kvq::overlap(out, rows_of(v_new, v_row_stride, v_head_stride, pages->kv_heads)))
+      return KVQ_ERR_INVALID_ARG;
+  }
   p.a.status = kvq::status_ptr();
   p.a.bounds_site = kvq::bounds_site_ptr();
   if (p.a.status == nullptr) return KVQ_ERR_CUDA;
