@@ -65,6 +65,7 @@ struct RopeArgs {
   RopeTensor x[2];
   int batch, rows, d, inverse;
   int* status;
+  int* bounds_site;
 };
 
 // Pages that an append with offsets looks at (see append_item), and the rows of a

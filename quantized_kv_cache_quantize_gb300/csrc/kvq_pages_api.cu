@@ -306,6 +306,7 @@ kvq_status kvq_rope(const kvq_rope_table* table, const int32_t* positions, int64
   a.d = head_dim;
   a.inverse = inverse != 0;
   a.status = kvq::status_ptr();
+  a.bounds_site = kvq::bounds_site_ptr();
   if (a.status == nullptr) return KVQ_ERR_CUDA;
   return kvq::launch_rope(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }

@@ -55,11 +55,14 @@ __global__ void __launch_bounds__(256, 4) rope_kernel(const __grid_constant__ Ro
   if (second) g -= q_groups;
   RopeTensor x = a.x[0];
   if (second) x = a.x[1];
-  const int h0 = (int)g * kRopeHeads;
+  const int h0 = (int)g * kRopeHeads, rows = min(R, a.rows - row0), heads = min(kRopeHeads, x.heads - h0);
+  if (!KVQ_IN_BOUNDS(b * a.rows + row0 + rows - 1, (long long)a.batch * a.rows, a.status, a.bounds_site) ||
+      !KVQ_IN_BOUNDS(h0 + heads - 1, x.heads, a.status, a.bounds_site))
+    return;
   const int32_t* pos = a.pos + b * a.pb + row0 * a.pr;
-  rope_tile<D, R, (R + 7) / 8, INTER>(a.t, a.inverse != 0, turns, min(R, a.rows - row0), min(kRopeHeads, x.heads - h0),
+  rope_tile<D, R, (R + 7) / 8, INTER>(a.t, a.inverse != 0, turns, rows, heads,
                   x.x + b * x.xb + row0 * x.xr + h0 * x.xh, x.xr, x.xh, x.y + b * x.yb + row0 * x.yr + h0 * x.yh, x.yr,
-                  x.yh, a.status, [&](int r, int axis) { return __ldg(pos + r * a.pr + axis * a.pa); });
+                  x.yh, a.status, a.bounds_site, [&](int r, int axis) { return __ldg(pos + r * a.pr + axis * a.pa); });
 }
 
 // ---- append -----------------------------------------------------------------
@@ -85,6 +88,10 @@ __device__ __forceinline__ void append_queries(const AppendRopeArgs& p, unsigned
     end = min(end, __ldg(s.offsets + s.batch));
   }
   if (row0 >= end) return;
+  const int heads = min(kRopeHeads, p.q.heads - h0);
+  if (!KVQ_IN_BOUNDS(row0, end, p.a.status, p.a.bounds_site) || !KVQ_IN_BOUNDS(end - 1, s.rows, p.a.status, p.a.bounds_site) ||
+      !KVQ_IN_BOUNDS(h0 + heads - 1, p.q.heads, p.a.status, p.a.bounds_site))
+    return;
   auto place = [&](int r, int axis) {
     if (p.pos != nullptr) return __ldg(p.pos + (row0 + r) * p.pr + axis);
     int b = row0 + r, next = b + 1;
@@ -94,8 +101,8 @@ __device__ __forceinline__ void append_queries(const AppendRopeArgs& p, unsigned
     }
     return seq_len(s, b, p.a.p.shift, p.a.status) - (next - (row0 + r));
   };
-  rope_tile<D, R, N, INTER>(p.t, false, turns, end - row0, min(kRopeHeads, p.q.heads - h0), p.q.x + row0 * p.q.xr + h0 * p.q.xh,
-                  p.q.xr, p.q.xh, p.q.y + row0 * p.q.yr + h0 * p.q.yh, p.q.yr, p.q.yh, p.a.status, place);
+  rope_tile<D, R, N, INTER>(p.t, false, turns, end - row0, heads, p.q.x + row0 * p.q.xr + h0 * p.q.xh,
+                  p.q.xr, p.q.xh, p.q.y + row0 * p.q.yr + h0 * p.q.yh, p.q.yr, p.q.yh, p.a.status, p.a.bounds_site, place);
 }
 
 // largest magnitude of m and 16 values, a NaN before all
@@ -130,6 +137,9 @@ __device__ __forceinline__ void append_keys(const AppendRopeArgs& p, int item, i
   const int lo = max(first - t0, 0), hi = min(end - t0, a.p.page);
   if (!KVQ_IN_BOUNDS((long long)id * a.p.heads + h1 - 1, (long long)a.p.n_pages * a.p.heads, a.status, a.bounds_site)) return;
   const long long row = r0 + (t0 - first);           // packed row of the page's token 0
+  if (lo < hi && (!KVQ_IN_BOUNDS(row + lo, a.s.rows, a.status, a.bounds_site) ||
+                  !KVQ_IN_BOUNDS(row + hi - 1, a.s.rows, a.status, a.bounds_site)))
+    return;
   const int u = tid % U;
   int c0, c1;
   rope_chunks(p.t, u, c0, c1);
@@ -146,7 +156,7 @@ __device__ __forceinline__ void append_keys(const AppendRopeArgs& p, int item, i
     }
   };
   load(h0);
-  rope_stage(p.t, turns, hi - lo, false, a.status, [&](int r, int axis) {
+  rope_stage(p.t, turns, hi - lo, false, a.status, a.bounds_site, [&](int r, int axis) {
     return p.pos != nullptr ? __ldg(p.pos + (row + lo + r) * p.pr + axis) : t0 + lo + r;
   });
   __syncthreads();
@@ -266,7 +276,7 @@ __global__ void __launch_bounds__(128) append_one_rope_kernel(const __grid_const
   floats_of(y, g);
   if (kv == 0) {   // the warp's own row of turns
     float4* row = turns + (threadIdx.x >> 5) * kRopeRow;
-    rope_stage_one(p.t, row, a.status, [&](int axis) { return p.pos != nullptr ? __ldg(p.pos + b * p.pr + axis) : len - 1; });
+    rope_stage_one(p.t, row, a.status, a.bounds_site, [&](int axis) { return p.pos != nullptr ? __ldg(p.pos + b * p.pr + axis) : len - 1; });
     __syncwarp();
     if (lane < (p.t.pairs >> 3)) {
       float4 cs[4];

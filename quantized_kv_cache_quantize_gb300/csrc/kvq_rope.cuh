@@ -2,6 +2,7 @@
 // from the table, the rotation itself.
 #pragma once
 
+#include "kvq_checks.cuh"
 #include "kvq_pages.cuh"
 
 namespace kvq {
@@ -30,25 +31,30 @@ constexpr int kRopeRow = kRopeMaxPairs / 2;
 __device__ __forceinline__ int rope_slot(int unit, int j) { return 8 * j + (unit ^ (2 * j)); }
 // A row's, by a warp, a lane an entry.  pos(axis): the row's position.
 template <typename Pos>
-__device__ __forceinline__ void rope_stage_one(const RopeTab& t, float4* row, int* status, Pos pos, bool inverse = false) {
+__device__ __forceinline__ void rope_stage_one(const RopeTab& t, float4* row, int* status, int* site, Pos pos,
+                                               bool inverse = false) {
   const int e = threadIdx.x & 31, p = 2 * e;
   if (p >= t.pairs) return;
   const int axis0 = rope_axis(t, p), axis1 = rope_axis(t, p + 1);
   const float2* from = t.cs + (long long)rope_position(t, pos(axis0), status) * t.pairs + p;
+  if (!KVQ_IN_BOUNDS(from - t.cs, (long long)t.n * t.pairs - 1, status, site)) return;
   float4 v;   // cos, sin, cos, sin
   if (axis0 == axis1) {
     v = __ldg(reinterpret_cast<const float4*>(from));
   } else {
-    const float2 x = __ldg(from), y = __ldg(t.cs + (long long)rope_position(t, pos(axis1), status) * t.pairs + p + 1);
+    const float2* other = t.cs + (long long)rope_position(t, pos(axis1), status) * t.pairs + p + 1;
+    if (!KVQ_IN_BOUNDS(other - t.cs, (long long)t.n * t.pairs, status, site)) return;
+    const float2 x = __ldg(from), y = __ldg(other);
     v = make_float4(x.x, x.y, y.x, y.y);
   }
   row[rope_slot(e >> 2, e & 3)] = inverse ? make_float4(v.x, v.z, -v.y, -v.w) : make_float4(v.x, v.z, v.y, v.w);
 }
 // Those of `rows` rows by a block, a warp a row.  pos(row, axis): a row's position.
 template <typename Pos>
-__device__ __forceinline__ void rope_stage(const RopeTab& t, float4* turns, int rows, bool inverse, int* status, Pos pos) {
+__device__ __forceinline__ void rope_stage(const RopeTab& t, float4* turns, int rows, bool inverse, int* status, int* site,
+                                           Pos pos) {
   for (int r = threadIdx.x >> 5; r < rows; r += blockDim.x >> 5)
-    rope_stage_one(t, turns + r * kRopeRow, status, [&](int axis) { return pos(r, axis); }, inverse);
+    rope_stage_one(t, turns + r * kRopeRow, status, site, [&](int axis) { return pos(r, axis); }, inverse);
 }
 
 __device__ __forceinline__ void floats_of(const uint4& v, float (&f)[8]) {
@@ -129,7 +135,7 @@ __device__ __forceinline__ void rope_entries(const float4* row, int u, float4 (&
 template <int D, int R, int N, bool INTER, typename Pos>
 __device__ __forceinline__ void rope_tile(const RopeTab& t, bool inverse, float4* turns, int rows, int heads,
                                           const uint16_t* x, long long xr, long long xh, uint16_t* y, long long yr,
-                                          long long yh, int* status, Pos pos) {
+                                          long long yh, int* status, int* site, Pos pos) {
   constexpr int U = D / 16;
   const int u = threadIdx.x % U, r = threadIdx.x / U % R, step = blockDim.x / (R * U);
   const bool live = r < rows, turned = u < (t.pairs >> 3);
@@ -151,7 +157,7 @@ __device__ __forceinline__ void rope_tile(const RopeTab& t, bool inverse, float4
       }
     }
     if (!staged) {
-      rope_stage(t, turns, rows, inverse, status, pos);
+      rope_stage(t, turns, rows, inverse, status, site, pos);
       __syncthreads();
       staged = true;
       if (live && turned) rope_entries(turns + r * kRopeRow, u, cs);
