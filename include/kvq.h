@@ -559,8 +559,8 @@ kvq_status kvq_rope_fill(const kvq_rope_table *table, const double *frequency, d
  * batch_stride + i * row_stride + h * head_stride elements (multiples of 8;
  * head_dim contiguous), 16-byte aligned.  y == x with the same strides (in
  * place) or memory that overlaps no tensor of the call: a y that lies over
- * another place of an x or y is refused, place by place, so heads or rows
- * between those of another tensor are fine. */
+ * another place of an x or y, or over one of its own, is refused, place by place:
+ * heads or rows between those of another tensor are fine. */
 typedef struct kvq_rope_tensor {
   const uint16_t *x;
   uint16_t *y;
@@ -590,7 +590,7 @@ kvq_status kvq_rope(const kvq_rope_table *table, const int32_t *positions, int64
  * NULL where axes == 1: the tokens' places in their sequences, kv_lens[b] -
  * n_b + i.  q: BF16 as in kvq_paged_attention, rotated into q_out: q itself with
  * its strides, or memory that overlaps no input (refused as in kvq_rope where it
- * overlaps q, k_new or v_new); NULL with q_heads = 0 for none.  Rows before
+ * overlaps q, k_new, v_new or itself); NULL with q_heads = 0 for none.  Rows before
  * offsets[0] and at or behind offsets[batch] are neither read nor written.
  * rows * q_heads <= 2^32 (else KVQ_ERR_TOO_LARGE).  Everything else as
  * kvq_pages_append says.

@@ -77,4 +77,23 @@ class Overlap {
 };
 inline bool overlap(const Strided& a, const Strided& b) { return Overlap(a, b).found(); }
 
+// Whether two indices of one tensor are the same place: its first batch entry
+// against the others, the first row of that entry against its others, the first
+// head of that row against its others (two indices differ in one of these first,
+// and where their difference is a distance of nothing the first one's is too).
+inline bool repeats(Strided t) {
+  const int64_t stride[3] = {t.batch_stride, t.row_stride, t.head_stride};
+  int32_t Strided::*const size[3] = {&Strided::batch, &Strided::rows, &Strided::heads};
+  if (t.batch < 1 || t.rows < 1 || t.heads < 1) return false;
+  for (int k = 0; k < 3; ++k) {
+    Strided first = t, others = t;
+    first.*size[k] = 1;
+    others.*size[k] -= 1;
+    others.p = static_cast<const char*>(t.p) + 2 * stride[k];
+    if (overlap(first, others)) return true;
+    t = first;
+  }
+  return false;
+}
+
 }  // namespace kvq

@@ -293,7 +293,7 @@ kvq_status kvq_rope(const kvq_rope_table* table, const int32_t* positions, int64
     return kvq::Strided{t.y, t.y_batch_stride, t.y_row_stride, t.y_head_stride, batch, rows, t.heads, head_dim};
   };
   for (int i = 0; i < n_tensors; ++i)
-    if (tensors[i].x != tensors[i].y && kvq::overlap(x_of(i), y_of(i))) return KVQ_ERR_INVALID_ARG;
+    if ((tensors[i].x != tensors[i].y && kvq::overlap(x_of(i), y_of(i))) || kvq::repeats(y_of(i))) return KVQ_ERR_INVALID_ARG;
   if (n_tensors == 2 && (kvq::overlap(y_of(0), x_of(1)) || kvq::overlap(y_of(0), y_of(1)) || kvq::overlap(y_of(1), x_of(0))))
     return KVQ_ERR_INVALID_ARG;
   a.t = rope_of(table);
@@ -342,7 +342,7 @@ kvq_status kvq_pages_append_rope(const kvq_pages* pages, int32_t layer, const kv
     if (q == q_out ? (seqs->rows > 1 && q_row_stride != q_out_row_stride) || (q_heads > 1 && q_head_stride != q_out_head_stride)
                    : kvq::overlap(out, rows_of(q, q_row_stride, q_head_stride, q_heads)))
       return KVQ_ERR_INVALID_ARG;
-    if (kvq::overlap(out, rows_of(k_new, k_row_stride, k_head_stride, pages->kv_heads)) ||
+    if (kvq::repeats(out) || kvq::overlap(out, rows_of(k_new, k_row_stride, k_head_stride, pages->kv_heads)) ||
         kvq::overlap(out, rows_of(v_new, v_row_stride, v_head_stride, pages->kv_heads)))
       return KVQ_ERR_INVALID_ARG;
   }

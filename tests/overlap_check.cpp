@@ -47,6 +47,11 @@ int main() {
     bool want = false;
     for (long long p : x) want |= y.count(p) != 0;
     expect(t[0], t[1], want, "small");
+    for (int k = 0; k < 2; ++k) {
+      const long long all = (long long)t[k].batch * t[k].rows * t[k].heads * (t[k].d / 8);
+      ++checks;
+      if (kvq::repeats(t[k]) != ((long long)(k == 0 ? x : y).size() != all) && ++bad < 10) std::printf("repeats\n");
+    }
   }
   // slices of one projection [4680][48][128]: queries, keys, and a slice across both
   const long long row = 48 * 128;
@@ -63,6 +68,9 @@ int main() {
   expect(at(0, batch, 64, head, 4, 30000, 32, 64), at(32 * head, batch, 64, head, 4, 30000, 8, 64), false, "heads apart");
   expect(at(0, batch, 64, head, 4, 30000, 33, 64), at(32 * head, batch, 64, head, 4, 30000, 8, 64), true, "a head shared");
   expect(at(0, batch, 64, head, 4, 30000, 32, 64), at(0, batch, 40 * 64, 64, 4, 30000, 32, 64), true, "two layouts");
+  checks += 4;
+  bad += kvq::repeats(q) + kvq::repeats(at(0, batch, 64, head, 4, 30000, 40, 64)) +
+         !kvq::repeats(at(0, 0, row, 127 * 8, 1, 4680, 49, 128)) + !kvq::repeats(at(0, 0, 0, 128, 1, 2, 8, 128));
   // numbers beyond 64 bits
   const long long far = 0x7ffffffffffffff8LL;
   expect(at(0, far, far, far, 0x7fffffff, 0x7fffffff, 0x7fffffff, 128), at(64, far, far, far, 1, 1, 1, 128), true, "far");

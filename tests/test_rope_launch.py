@@ -70,6 +70,19 @@ def test_rotation_refuses_a_shifted_place(lib, shift):
         assert lib.kvq_rope(ctypes.byref(t), PTR + (1 << 40), 0, 1, 0, 1, 10, 128, 0, ctypes.byref(a), 1, None) == kvq.KVQ_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("row,head", [(0, 128), (1016, 128), (6144, 0), (6144, 64)])
+def test_outputs_that_repeat_memory(lib, row, head):
+    """Rows or heads of an output on top of one another, in place or not."""
+    t = kvq.RopeTableStruct()
+    t.cos_sin, t.n_positions, t.pairs, t.axes = PTR + (1 << 40), 100, 32, 1
+    for x in (1 << 30, 0):
+        a = _tensor(x, 1 << 30, 8, row, head)
+        assert lib.kvq_rope(ctypes.byref(t), PTR + (1 << 40), 0, 1, 0, 1, 10, 128, 0, ctypes.byref(a), 1, None) == kvq.KVQ_ERR_INVALID_ARG
+    args = [ctypes.byref(_pages()), 0, ctypes.byref(t), None, 0, PTR, 512, 128, PTR, 512, 128,
+            PTR + (1 << 31), 6144, 128, 8, PTR + (1 << 32), row, head, ctypes.byref(_seqs()), None]
+    assert lib.kvq_pages_append_rope(*args) == kvq.KVQ_ERR_INVALID_ARG
+
+
 @pytest.mark.parametrize("out", [128, 31 * 128, 32 * 128 + 7 * 128, 40 * 128 + 3 * 128, 6144 * 2, 6144 + 47 * 128])
 def test_append_refuses_overlaps(lib, out):
     """One projection of 48 heads a row: 32 of queries, 8 of keys, 8 of values."""
