@@ -51,11 +51,12 @@
 // the softmax.  The products are the same, the instructions per score are not, and
 // they decide: two warps a scheduler, whose largest stall is the wait for their own
 // results, tensor pipe 40 % active with a cap and 56 without.  A half tile takes
-// one of two ways.  The straight one, 64 scores in registers, is for keys that all
-// rows of the warp see: plain scores, a bias that falls or rises along the tile, a
-// cap and scores up to 0.4 of it (their largest magnitude comes with the load from
-// tensor memory, tcgen05.ld.red).  The other one, for masks, hot scores, new bases
-// and distances from far bases, is a pair of functions out of line that loop over
+// one of two ways.  The straight one, 64 scores in registers (with a cap twice 32),
+// is for keys that all rows of the warp see: plain scores, a bias that falls or
+// rises along the tile, a cap and scores up to 0.4 of it (their largest magnitude
+// comes with the load from tensor memory, tcgen05.ld.red).  The other one, for
+// masks, hot scores, a cap with a bias, new bases and distances from far bases, is
+// a pair of functions out of line that loop over
 // the scores in tensor memory, so short that they stay in the instruction buffers:
 // unrolled by another two they take a sixth longer, and with more registers they
 // have the straight way's spilled (10 % of that).  8000 rows of 32 heads over 8 and
@@ -336,8 +337,8 @@ struct HalfRow {
 };
 template <int MODE>
 __device__ __forceinline__ void shape_block(uint32_t* v, float raw, const HalfRow& h, int k) {
-  if (MODE == kCapped) cap_block(v, raw, true);
-  if (h.shape.biased) bias_block(v, MODE == kCapped ? h.shape.cap2 : raw, h.shape, h.dist - 16 * k, false);
+  if (MODE == kCapped) cap_block(v, raw);
+  if (h.shape.biased) bias_block(v, MODE == kCapped ? h.shape.cap2 : raw, h.shape, h.dist - 16 * k);
 }
 // The largest of them with their V exponents.  A cap alone keeps the order of raw
 // scores: the largest of a block is shaped, no other.

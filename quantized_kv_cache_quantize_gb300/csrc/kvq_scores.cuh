@@ -5,8 +5,9 @@
 // 1, where scores that a cap is meant for lie, tanh is x times a polynomial in x^2
 // (tanh_fit.py), 2^-22 of it at most with its roundings: products on pairs, none of
 // them on the special-function unit, which the softmax's exponentials need.  Beyond,
-// 1 - 2 / (1 + 2^(2 x log2 e)): two special functions a score, off by 2^-22.  A
-// distance is a whole number, exact in fp32 up to 2^24.
+// 1 - 2 / (1 + 2^(2 x log2 e)): two special functions a score, off by 2^-22; one and
+// a half in far_scores, which takes one reciprocal for two.  A distance is a whole
+// number, exact in fp32 up to 2^24.
 #pragma once
 
 #include <math_constants.h>
@@ -143,46 +144,26 @@ template <int MODE>
 __device__ __forceinline__ float shape_factor(const RowShape& r, float ck) {
   return r.biased ? 1.f : MODE == kCapped ? r.cap2 : ck;
 }
-// tanh of 16 raw scores times ck, in place; `far`: some may lie beyond 1
-__device__ __forceinline__ void cap_block(uint32_t* s, float ck, bool far) {
+// tanh of 16 raw scores times ck, in place
+__device__ __forceinline__ void cap_block(uint32_t* s, float ck) {
   const uint64_t c2 = ptx::f2_pack(ck, ck);
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const uint64_t x2 = ptx::f2_mul(ptx::f2_pack(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), c2);
-    float x, y;
+    float x0, y0, x, y;
+    ptx::f2_unpack(x2, x0, y0);
     ptx::f2_unpack(tanh_small(x2), x, y);
-    if (far) {
-      float x0, y0;
-      ptx::f2_unpack(x2, x0, y0);
-      x = tanh_any(x0, x);
-      y = tanh_any(y0, y);
-    }
-    s[2 * k] = __float_as_uint(x);
-    s[2 * k + 1] = __float_as_uint(y);
+    s[2 * k] = __float_as_uint(tanh_any(x0, x));
+    s[2 * k + 1] = __float_as_uint(tanh_any(y0, y));
   }
 }
 // The bias of 16 neighbouring keys, key 0 `dist` before the row's reference
-// place, added to their scores times f.  `left`: no key of any lane's lies
-// behind its row's reference place.
-__device__ __forceinline__ void bias_block(uint32_t* s, float f, const RowShape& r, int dist, bool left) {
+// place, added to their scores times f.
+__device__ __forceinline__ void bias_block(uint32_t* s, float f, const RowShape& r, int dist) {
   const float d0 = (float)dist;
-  if (left) {
-    const uint64_t f2 = ptx::f2_pack(f, f), slope2 = ptx::f2_pack(r.slope2, r.slope2);
-    const float b = -r.slope2 * d0;
-    const uint64_t b2 = ptx::f2_pack(b, b);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      float x, y;
-      const uint64_t bias = ptx::f2_fma(ptx::f2_pack((float)(2 * k), (float)(2 * k + 1)), slope2, b2);
-      ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), f2, bias), x, y);
-      s[2 * k] = __float_as_uint(x);
-      s[2 * k + 1] = __float_as_uint(y);
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-      s[k] = __float_as_uint(fmaf(-r.slope2, fabsf(d0 - (float)k), __uint_as_float(s[k]) * f));
-  }
+  for (int k = 0; k < 16; ++k)
+    s[k] = __float_as_uint(fmaf(-r.slope2, fabsf(d0 - (float)k), __uint_as_float(s[k]) * f));
 }
 
 }  // namespace

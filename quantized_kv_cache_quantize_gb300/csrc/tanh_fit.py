@@ -8,7 +8,7 @@ sqrt(p))^2 per coefficient, a factor of 11.8 for X = 1) and rewritten in powers
 of z.
 
 Run: python quantized_kv_cache_quantize_gb300/csrc/tanh_fit.py  (prints the
-constants of kvq_scores.cuh's tanh_small and kTanhLow).
+constants of kvq_scores.cuh's tanh_small, the highest power first there, and low_cap).
 """
 from __future__ import annotations
 
