@@ -60,9 +60,9 @@
 // the scores in tensor memory, so short that they stay in the instruction buffers:
 // unrolled by another two they take a sixth longer, and with more registers they
 // have the straight way's spilled (10 % of that).  8000 rows of 32 heads over 8 and
-// as many keys, no mask, us: plain 808, biased 940, capped 1165, capped with scores
-// up to 0.9 of the cap 2190.  24 heads of 4680 rows, 23400 keys, capped: 1.35 ms,
-// 1.0 PFLOP/s.
+// as many keys, no mask, us: plain 806, biased 950, capped 1158, capped with scores
+// up to 0.9 of the cap 2184, capped and biased 3930.  24 heads of 4680 rows, 23400
+// keys, capped, scores below 0.4 of the cap: 1.33 ms, 1.0 PFLOP/s.
 #pragma once
 
 #include <math_constants.h>
@@ -838,7 +838,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, NQ>::kThreads, 1)
             }
           } else if (low) {
             // (32 at a time, a vote each, without a look at whether two pages have
-            // one scale: 1.35 ms, not 1.38, of the 4680 rows above)
+            // one scale: 2 % less of the 4680 rows above)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               uint32_t cur[32];
