@@ -99,7 +99,9 @@ __device__ __forceinline__ void append_queries(const AppendRopeArgs& p, unsigned
       b = seq_of_row(s, b);
       next = __ldg(s.offsets + b + 1);
     }
-    return seq_len(s, b, p.a.p.shift, p.a.status) - (next - (row0 + r));
+    const int at = seq_len(s, b, p.a.p.shift, p.a.status) - (next - (row0 + r));
+    if (at < 0) page_error(p.a.status);   // a row before its sequence's first token
+    return max(at, 0);
   };
   rope_tile<D, R, N, INTER>(p.t, false, turns, end - row0, heads, p.q.x + row0 * p.q.xr + h0 * p.q.xh,
                   p.q.xr, p.q.xh, p.q.y + row0 * p.q.yr + h0 * p.q.yh, p.q.yr, p.q.yh, p.a.status, p.a.bounds_site, place);

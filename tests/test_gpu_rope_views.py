@@ -66,3 +66,21 @@ def test_append_writes_queries_beside_its_inputs(offsets):
         with pytest.raises(kvq.KVQError) as e:
             kvq.pages_append_rope(cache, t, k, v, table, lens, off, q=q, q_out=bad)
         assert e.value.status == kvq.KVQ_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("offsets,lens", [(None, [0, 3]), ([0, 5], [2]), ([0, 40, 41], [7, 1])])
+def test_more_rows_than_tokens_is_one_error(offsets, lens):
+    """Rows before their sequence's first token have no place: the length is what is
+    wrong, whichever of the keys' and the queries' blocks comes first."""
+    rng = np.random.default_rng(9)
+    rows = offsets[-1] if offsets else len(lens)
+    t = table_of(100, 64, None, False)
+    table = dev(np.arange(2 * len(lens)).reshape(len(lens), 2))
+    x = rows_of(rng, rows, 12, 128).cuda()
+    for _ in range(30):
+        cache = kvq.PagedCache.zeros(1, 8, 2, 16, 128)
+        y = kvq.pages_append_rope(cache, t, x[:, :2], x[:, 2:4], table, dev(lens), dev(offsets) if offsets else None, q=x[:, 4:])
+        torch.cuda.synchronize()
+        assert kvq.last_device_status() == kvq.KVQ_ERR_PAGE
+        first = 0 if offsets is None else offsets[1] - lens[0]     # the row of token 0, or of none
+        assert np.array_equal(bits(y[:first + 1]), bits(x[:first + 1, 4:]))     # as they are, at place 0
